@@ -130,6 +130,13 @@ def _load():
             getattr(lib, name).argtypes = [
                 ctypes.c_uint32, ctypes.c_uint32, c_int,
                 ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_uint32)]
+        u64p = ctypes.POINTER(ctypes.c_uint64)
+        lib.detor_rope_at.argtypes = [i64, i64, i64, i64, c_int, f32p, i64, i32p, u64p,
+                                      ctypes.c_float, c_int]
+        lib.detor_logprob.argtypes = [i64, i64, f32p, i64, i32p, i64, f32p, f32p, f32p, i32p,
+                                      f32p, c_int, c_int, c_int]
+        lib.detor_logprob_bwd.argtypes = [i64, i64, f32p, i64, i32p, f32p, f32p, f32p, f32p,
+                                          i64, c_int]
         if not lib.detor_fp_env_ok():
             raise RuntimeError("host FP environment flushes subnormals or "
                                "widens float evaluation; the oracle refuses")
@@ -427,3 +434,61 @@ def adamw(p, g, m, v, lr, beta1, beta2, eps, weight_decay, step,
                         np.float32(beta1), np.float32(beta2), np.float32(eps),
                         np.float32(weight_decay), int(step), _threads(nthreads))
     return p, m, v
+
+
+# ---------------------------------------------------------------- generation
+def _i32p(a):
+    return a.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
+
+
+def rope_at(x, positions, heads, head_dim, theta=10000.0, turns=None, rot=None, half=False,
+            inverse=False):
+    """Rotary embedding of the rows of x (rows x heads*head_dim) at positions
+    (negative: the row stays): a new array. turns: uint64 fixed-point turns a
+    position, or None for rope()'s angles."""
+    out = np.array(_f32(x), dtype=np.float32, order="C", copy=True)
+    pos = np.ascontiguousarray(positions, dtype=np.int32)
+    tp = None
+    if turns is not None:
+        turns = np.ascontiguousarray(turns).view(np.uint64)
+        tp = turns.ctypes.data_as(ctypes.POINTER(ctypes.c_uint64))
+    _load().detor_rope_at(out.shape[0], heads, head_dim, rot or head_dim, int(half), _fp(out),
+                          out.shape[1], _i32p(pos), tp, np.float32(theta), int(inverse))
+    return out
+
+
+def decode_attention(q, K, V, scale):
+    """One head of one request: q (d), K and V (n x d): the last row of causal
+    attention over the n tokens. n == 0 gives +0."""
+    n, d = K.shape
+    if n == 0:
+        return np.zeros(d, np.float32)
+    s = gemm(np.ascontiguousarray(q[None, :]), np.ascontiguousarray(K), transB=True)
+    p = softmax_causal(s, scale=scale, diag=n - 1)
+    return gemm(p, np.ascontiguousarray(V))[0]
+
+
+def logprob(logits, tokens, k=0, lanes=XENT_LANES, group=LANE_GROUP, nthreads=None):
+    """(logp, entropy, stats, top_ids, top_logp) of rows of logits."""
+    x = np.ascontiguousarray(_f32(logits))
+    y = np.ascontiguousarray(tokens, dtype=np.int32)
+    n, V = x.shape
+    logp, ent, stats = (np.empty(n, np.float32), np.empty(n, np.float32),
+                        np.empty((n, 4), np.float32))
+    ids, top = np.empty((n, k), np.int32), np.empty((n, k), np.float32)
+    _load().detor_logprob(n, V, _fp(x), V, _i32p(y), k, _fp(logp), _fp(ent), _fp(stats),
+                          _i32p(ids), _fp(top), lanes, group, _threads(nthreads))
+    return logp, ent, stats, ids, top
+
+
+def logprob_bwd(logits, tokens, stats, dlogp, dentropy=None, nthreads=None):
+    """The gradient with respect to the logits."""
+    x = np.ascontiguousarray(_f32(logits))
+    y = np.ascontiguousarray(tokens, dtype=np.int32)
+    st, g = np.ascontiguousarray(_f32(stats)), np.ascontiguousarray(_f32(dlogp))
+    gH = None if dentropy is None else np.ascontiguousarray(_f32(dentropy))
+    dx = np.empty_like(x)
+    _load().detor_logprob_bwd(x.shape[0], x.shape[1], _fp(x), x.shape[1], _i32p(y), _fp(st),
+                              _fp(g), None if gH is None else _fp(gH), _fp(dx), x.shape[1],
+                              _threads(nthreads))
+    return dx

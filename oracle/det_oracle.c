@@ -447,6 +447,65 @@ void detor_rope_bwd(int64_t rows, int64_t heads, int64_t head_dim, float *x, int
     parallel_for(rows, nthreads, rope_rows, &c);
 }
 
+/* Rotary embedding at positions of the caller's own. turns NULL: the angles of
+ * rope_rows with rot in the place of d. Else the phase is pos * turns[i] modulo
+ * 2^64 (one turn); the nearest quarter turn q (ties up), the signed rest in
+ * float, r = rest * (2^-62 pi / 2) with the constant in two floats, then
+ * sincos_v1's polynomials and quadrant. A negative position: no turn. */
+static const float TURN_HI = 0x1.921fb6p-62f, TURN_LO = -0x1.777a5cp-87f;
+
+static void sincos_turns(uint64_t u, float *sn, float *cs) {
+    const unsigned q = (unsigned)((u + ((uint64_t)1 << 61)) >> 62);
+    const int64_t rest = (int64_t)(u - ((uint64_t)q << 62));
+    const float f = (float)rest;
+    const float r = fmaf(f, TURN_HI, f * TURN_LO);
+    const float z = r * r;
+    float ps = S9F;
+    ps = fmaf(ps, z, S7F);
+    ps = fmaf(ps, z, S5F);
+    ps = fmaf(ps, z, S3F);
+    const float s = fmaf(r, z * ps, r);
+    float pc = C10F;
+    pc = fmaf(pc, z, C8F);
+    pc = fmaf(pc, z, C6F);
+    pc = fmaf(pc, z, C4F);
+    pc = fmaf(pc, z, C2F);
+    const float c = fmaf(pc, z, 1.0f);
+    *sn = q == 0 ? s : q == 1 ? c : q == 2 ? -s : -c;
+    *cs = q == 0 ? c : q == 1 ? -s : q == 2 ? -c : s;
+}
+
+void detor_rope_at(int64_t rows, int64_t heads, int64_t head_dim, int64_t rot, int half,
+                   float *x, int64_t ldx, const int32_t *positions, const uint64_t *turns,
+                   float theta, int inverse) {
+    const float L = detor_log(theta);
+    for (int64_t t = 0; t < rows; ++t) {
+        if (positions[t] < 0) continue;
+        for (int64_t i = 0; i < rot / 2; ++i) {
+            float sn, cs;
+            if (turns) {
+                sincos_turns((uint64_t)positions[t] * turns[i], &sn, &cs);
+            } else {
+                const float e = (float)(2 * i) / (float)rot;
+                const float w = detor_exp(-e * L);
+                sincos_v1((float)positions[t] * w, &sn, &cs);
+            }
+            for (int64_t h = 0; h < heads; ++h) {
+                float *p0 = x + t * ldx + h * head_dim + (half ? i : 2 * i);
+                float *p1 = half ? p0 + rot / 2 : p0 + 1;
+                const float x0 = *p0, x1 = *p1;
+                if (!inverse) {
+                    *p0 = x0 * cs - x1 * sn;
+                    *p1 = x0 * sn + x1 * cs;
+                } else {
+                    *p0 = x0 * cs + x1 * sn;
+                    *p1 = x1 * cs - x0 * sn;
+                }
+            }
+        }
+    }
+}
+
 /* Embedding backward (design notes R36): per id v and column j, the tokens'
  * gradients in ascending token order, the first as is, then left to right. */
 typedef struct {
@@ -801,6 +860,120 @@ static void xent_rows(int64_t lo, int64_t hi, int tix, void *c) {
         }
     }
     q->bad[tix] = bad;
+}
+
+/* ------------------------------------------------------------------------ */
+/* log probabilities of tokens                                               */
+/* ------------------------------------------------------------------------ */
+/* Per row: m, e_j and S as the cross-entropy; logp = (x_y - m) - log(S); T = the
+ * sum of e_j * (x_j - m) over 4096 chains (element j on chain j mod 4096, fmaf
+ * from +0 in ascending j, elements with e_j == 0 left out), folded in fours left
+ * to right, then by the butterfly within each 32 of the 1024 sums and over the
+ * 32 totals; entropy = log(S) - T / S; stats = (m, 1 / S, log S, entropy). The
+ * k alternatives: the largest logits, lowest id first among equals, NaN above
+ * all; each with (x - m) - log(S). Token -1: logp +0; others outside: NaN. */
+typedef struct {
+    int64_t V, ld, k;
+    const float *x;
+    const int32_t *tokens;
+    float *logp, *entropy, *stats, *top_logp;
+    int32_t *top_ids;
+    int lanes, group;
+} logprob_ctx;
+
+/* whether element (a, i) goes before (b, j) among the alternatives */
+static int goes_before(float a, int64_t i, float b, int64_t j) {
+    const int na = a != a, nb = b != b;
+    if (na != nb) return na;
+    if (!na && a != b) return a > b;
+    return i < j;
+}
+
+static void logprob_rows(int64_t lo, int64_t hi, int tix, void *c) {
+    (void)tix;
+    logprob_ctx *q = (logprob_ctx *)c;
+    float s[1024], T[4096], u[1024], tot[32];
+    for (int64_t r = lo; r < hi; ++r) {
+        const float *x = q->x + r * q->ld;
+        const int64_t y = q->tokens[r];
+        float m = x[0];
+        for (int64_t j = 1; j < q->V; ++j) if (x[j] > m || x[j] != x[j]) m = x[j];
+        for (int l = 0; l < q->lanes; ++l) s[l] = 0.0f;
+        for (int l = 0; l < 4096; ++l) T[l] = 0.0f;
+        for (int64_t j = 0; j < q->V; ++j) {
+            const float d = x[j] - m, e = detor_exp(d);
+            const int l = (int)((j / q->group) % q->lanes);
+            s[l] = s[l] + e;
+            if (e != 0.0f) T[j % 4096] = fmaf(e, d, T[j % 4096]);
+        }
+        const float S = butterfly(s, q->lanes);
+        for (int t = 0; t < 1024; ++t)
+            u[t] = ((T[4 * t] + T[4 * t + 1]) + T[4 * t + 2]) + T[4 * t + 3];
+        for (int w = 0; w < 32; ++w) tot[w] = butterfly(u + 32 * w, 32);
+        const float Tsum = butterfly(tot, 32);
+        const float logS = detor_log(S);
+        const float ent = logS - Tsum / S;
+        q->entropy[r] = ent;
+        q->logp[r] = y == -1 ? 0.0f : y < 0 || y >= q->V ? NAN : (x[y] - m) - logS;
+        if (q->stats) {
+            float *st = q->stats + 4 * r;
+            st[0] = m; st[1] = 1.0f / S; st[2] = logS; st[3] = ent;
+        }
+        /* the k first in order: each the best element after the one before */
+        for (int64_t k = 0; k < q->k; ++k) {
+            int64_t best = -1;
+            const int64_t prev = k ? q->top_ids[r * q->k + k - 1] : -1;
+            for (int64_t j = 0; j < q->V; ++j) {
+                if (prev >= 0 && !goes_before(x[prev], prev, x[j], j)) continue;
+                if (best < 0 || goes_before(x[j], j, x[best], best)) best = j;
+            }
+            q->top_ids[r * q->k + k] = (int32_t)best;
+            q->top_logp[r * q->k + k] = (x[best] - m) - logS;
+        }
+    }
+}
+
+void detor_logprob(int64_t rows, int64_t V, const float *x, int64_t ld, const int32_t *tokens,
+                   int64_t k, float *logp, float *entropy, float *stats, int32_t *top_ids,
+                   float *top_logp, int lanes, int group, int nthreads) {
+    logprob_ctx c = {V, ld, k, x, tokens, logp, entropy, stats, top_logp, top_ids, lanes, group};
+    parallel_for(rows, nthreads, logprob_rows, &c);
+}
+
+/* Its gradient: d = x_j - m, p = exp(d) * (1 / S), a = g * ([j == y] - p) (+0 for
+ * token -1), w = p * ((d - log S) + entropy) (+0 where p == 0); a - gH * w, or a
+ * without gH. A token outside [0, V) other than -1: a NaN row. */
+typedef struct {
+    int64_t V, ld, ldd;
+    const float *x, *stats, *g, *gH;
+    const int32_t *tokens;
+    float *dx;
+} logprob_bwd_ctx;
+
+static void logprob_bwd_rows(int64_t lo, int64_t hi, int tix, void *c) {
+    (void)tix;
+    logprob_bwd_ctx *q = (logprob_bwd_ctx *)c;
+    for (int64_t r = lo; r < hi; ++r) {
+        const float *x = q->x + r * q->ld, *st = q->stats + 4 * r;
+        const int64_t y = q->tokens[r];
+        for (int64_t j = 0; j < q->V; ++j) {
+            float *out = q->dx + r * q->ldd + j;
+            if (y < -1 || y >= q->V) { *out = NAN; continue; }
+            const float d = x[j] - st[0], p = detor_exp(d) * st[1];
+            const float hot = j == y ? 1.0f : 0.0f;
+            const float a = y == -1 ? 0.0f : q->g[r] * (hot - p);
+            if (!q->gH) { *out = a; continue; }
+            const float w = p == 0.0f ? 0.0f : p * ((d - st[2]) + st[3]);
+            *out = a - q->gH[r] * w;
+        }
+    }
+}
+
+void detor_logprob_bwd(int64_t rows, int64_t V, const float *x, int64_t ld,
+                       const int32_t *tokens, const float *stats, const float *g,
+                       const float *gH, float *dx, int64_t ldd, int nthreads) {
+    logprob_bwd_ctx c = {V, ld, ldd, x, stats, g, gH, tokens, dx};
+    parallel_for(rows, nthreads, logprob_bwd_rows, &c);
 }
 
 /* ------------------------------------------------------------------------ */

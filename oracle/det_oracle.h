@@ -132,6 +132,22 @@ int64_t detor_xent(int64_t rows, int64_t V, const float *logits, int64_t ld,
                    const int32_t *labels, float *loss, float *dlogits,
                    int64_t ldd, float dscale, int lanes, int group, int nthreads);
 
+/* Rotary embedding in place at positions[t] (negative: the row stays), the first
+ * rot elements of each head, pairs (2i, 2i+1) or (half) (i, i + rot / 2); turns
+ * NULL: detor_rope's angles; else 64-bit fixed-point turns a position. */
+void detor_rope_at(int64_t rows, int64_t heads, int64_t head_dim, int64_t rot, int half,
+                   float *x, int64_t ldx, const int32_t *positions, const uint64_t *turns,
+                   float theta, int inverse);
+
+/* Log probabilities of tokens with entropy, stats (rows x 4, may be NULL) and the
+ * k largest alternatives, and the gradient (gH may be NULL); see det_oracle.c. */
+void detor_logprob(int64_t rows, int64_t V, const float *x, int64_t ld, const int32_t *tokens,
+                   int64_t k, float *logp, float *entropy, float *stats, int32_t *top_ids,
+                   float *top_logp, int lanes, int group, int nthreads);
+void detor_logprob_bwd(int64_t rows, int64_t V, const float *x, int64_t ld,
+                       const int32_t *tokens, const float *stats, const float *g,
+                       const float *gH, float *dx, int64_t ldd, int nthreads);
+
 /* Mean of n floats: lanes-way chain sums (plain adds), xor butterfly, then a
  * division by (float)n. */
 float detor_mean(int64_t n, const float *x, int lanes, int group);
