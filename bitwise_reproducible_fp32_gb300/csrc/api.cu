@@ -1028,6 +1028,205 @@ DET_API det_status detlog_f32(const det_profile_v1 *prof, int64_t n, const float
     return exp_log(prof, n, x, y, stream, 1);
 }
 
+// ---------------------------------------------------------------- generation
+namespace {
+constexpr int64_t kTopMax = 32;
+constexpr int64_t kVocabMax = int64_t(1) << 30;   // sweeps past a row's end stay in int
+
+bool rotary_ok(const det_rotary &r, int64_t head_dim) {
+    return r.rot_dim >= 2 && r.rot_dim % 2 == 0 && r.rot_dim <= head_dim;
+}
+
+bool cache_ok(const det_kv_cache *c) {
+    return c && c->k && c->v && c->num_pages >= 1 && c->num_pages <= kDimMax &&
+           c->page_size >= 1 && c->page_size <= kDimMax && c->kv_heads >= 1 &&
+           c->kv_heads <= 65536 && c->head_dim >= 1 && c->head_dim <= 256 &&
+           c->page_stride >= c->head_dim && c->token_stride >= c->head_dim &&
+           c->head_stride >= c->head_dim;
+}
+
+bool pages_ok(int64_t batch, int64_t page_size, int64_t max_pages, int64_t ldt,
+              int64_t capacity) {
+    return batch >= 0 && batch <= 8192 && page_size >= 1 && page_size <= kDimMax &&
+           max_pages >= 1 && max_pages <= kDimMax && ldt >= max_pages && capacity >= 0 &&
+           capacity <= kDimMax;
+}
+
+bool decode_sizes_ok(int64_t batch, int64_t heads, int64_t kv_heads, int64_t head_dim) {
+    return batch >= 0 && batch <= 65535 && heads >= 1 && heads <= 65536 && kv_heads >= 1 &&
+           heads % kv_heads == 0 && head_dim >= 1 && head_dim <= 256;
+}
+}  // namespace
+
+DET_API det_status detrope_at_f32(const det_profile_v1 *prof, int64_t rows, int64_t heads,
+                                  int64_t head_dim, const float *x, int64_t ldx,
+                                  const int32_t *positions, const det_rotary *rotary,
+                                  int inverse, float *out, int64_t ldo, det_stream_t stream) {
+    det_status st = check_profile(prof);
+    if (st != DET_OK) return st;
+    if (rows < 0 || rows > kDimMax || heads < 1 || heads > 65536 || head_dim < 1 ||
+        head_dim > 65536 || !rotary || !rotary_ok(*rotary, head_dim) || ldx < heads * head_dim ||
+        ldo < heads * head_dim)
+        return DET_ERR_INVALID_ARG;
+    if (rows == 0) return DET_OK;
+    if (!x || !out || !positions || (x == out && ldx != ldo)) return DET_ERR_INVALID_ARG;
+    if ((st = check_device()) != DET_OK) return st;
+    const RotaryArgs ro = {rotary->turns, rotary->theta, int(rotary->rot_dim), rotary->half != 0};
+    return from_cuda(launch_rope_at(rows, int(heads), int(head_dim), x, ldx, positions, ro, inverse,
+                                    out, ldo, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+DET_API det_status detkv_append_f32(const det_profile_v1 *prof, int64_t rows, int64_t heads,
+                                    const float *qkv, int64_t ldqkv, const int64_t *slots,
+                                    const int32_t *positions, const det_rotary *rotary,
+                                    const det_kv_cache *cache, float *q_out, int64_t ldq,
+                                    int32_t *dev_status, det_stream_t stream) {
+    det_status st = check_profile(prof);
+    if (st != DET_OK) return st;
+    if (rows < 0 || rows > kDimMax || heads < 1 || heads > 65536 || !cache_ok(cache))
+        return DET_ERR_INVALID_ARG;
+    const int64_t d = cache->head_dim;
+    if (ldqkv < (heads + 2 * cache->kv_heads) * d || (rotary && !rotary_ok(*rotary, d)))
+        return DET_ERR_INVALID_ARG;
+    if (!rotary) q_out = nullptr;
+    if (q_out && ldq < heads * d) return DET_ERR_INVALID_ARG;
+    if (rows == 0) return DET_OK;
+    if (!qkv || !slots || (rotary && !positions) || (q_out == qkv && ldq != ldqkv))
+        return DET_ERR_INVALID_ARG;
+    if ((st = check_device()) != DET_OK) return st;
+    RotaryArgs ro = {nullptr, 1.0f, 0, 0};
+    if (rotary)
+        ro = {rotary->turns, rotary->theta, int(rotary->rot_dim), rotary->half != 0};
+    return from_cuda(launch_kv_append(rows, int(heads), qkv, ldqkv, slots,
+                                      rotary ? positions : nullptr, ro, *cache, q_out, ldq,
+                                      dev_status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+DET_API det_status detpages_extend(const det_profile_v1 *prof, int64_t batch, int64_t page_size,
+                                   const int32_t *lens, const int32_t *new_tokens,
+                                   int32_t *table, int64_t max_pages, int64_t ldt,
+                                   const int32_t *free_pages, int64_t capacity,
+                                   const int32_t *free_count, int64_t max_rows,
+                                   int32_t *lens_out, int32_t *free_count_out,
+                                   int32_t *row_start, int32_t *positions, int64_t *slots,
+                                   int32_t *dev_status, det_stream_t stream) {
+    det_status st = check_profile(prof);
+    if (st != DET_OK) return st;
+    if (!pages_ok(batch, page_size, max_pages, ldt, capacity) || max_rows < 0 ||
+        max_rows > kDimMax)
+        return DET_ERR_INVALID_ARG;
+    if (!free_count || !free_count_out || !row_start || free_count == free_count_out ||
+        (capacity > 0 && !free_pages) || (max_rows > 0 && (!positions || !slots)))
+        return DET_ERR_INVALID_ARG;
+    if (batch > 0 && (!lens || !new_tokens || !table || !lens_out || lens == lens_out))
+        return DET_ERR_INVALID_ARG;
+    if ((st = check_device()) != DET_OK) return st;
+    return from_cuda(launch_pages_extend(batch, page_size, lens, new_tokens, table, max_pages, ldt,
+                                         free_pages, capacity, free_count, max_rows, lens_out,
+                                         free_count_out, row_start, positions, slots, dev_status,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+DET_API det_status detpages_release(const det_profile_v1 *prof, int64_t batch, int64_t page_size,
+                                    const int32_t *lens, const int32_t *done,
+                                    const int32_t *table, int64_t max_pages, int64_t ldt,
+                                    int32_t *free_pages, int64_t capacity,
+                                    const int32_t *free_count, int32_t *lens_out,
+                                    int32_t *free_count_out, int32_t *dev_status,
+                                    det_stream_t stream) {
+    det_status st = check_profile(prof);
+    if (st != DET_OK) return st;
+    if (!pages_ok(batch, page_size, max_pages, ldt, capacity)) return DET_ERR_INVALID_ARG;
+    if (!free_count || !free_count_out || free_count == free_count_out ||
+        (capacity > 0 && !free_pages))
+        return DET_ERR_INVALID_ARG;
+    if (batch > 0 && (!lens || !done || !table || !lens_out || lens == lens_out))
+        return DET_ERR_INVALID_ARG;
+    if ((st = check_device()) != DET_OK) return st;
+    return from_cuda(launch_pages_release(batch, page_size, lens, done, table, max_pages, ldt,
+                                          free_pages, capacity, free_count, lens_out,
+                                          free_count_out, dev_status,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+DET_API det_status detdecode_attention_workspace_bytes(const det_profile_v1 *prof, int64_t batch,
+                                                       int64_t heads, int64_t kv_heads,
+                                                       int64_t head_dim, int64_t max_len,
+                                                       size_t *bytes) {
+    det_status st = check_profile(prof);
+    if (st != DET_OK) return st;
+    if (!bytes || !decode_sizes_ok(batch, heads, kv_heads, head_dim) || max_len < 1 ||
+        max_len > kDimMax)
+        return DET_ERR_INVALID_ARG;
+    *bytes = decode_workspace_bytes(batch, heads, kv_heads, head_dim, max_len);
+    return DET_OK;
+}
+
+DET_API det_status detdecode_attention_f32(const det_profile_v1 *prof, int64_t batch,
+                                           int64_t heads, const float *q, int64_t ldq,
+                                           const det_kv_cache *cache, const int32_t *table,
+                                           int64_t max_pages, int64_t ldt,
+                                           const int32_t *kv_lens, float scale, float *out,
+                                           int64_t ldo, void *workspace, size_t workspace_bytes,
+                                           int32_t *dev_status, det_stream_t stream) {
+    det_status st = check_profile(prof);
+    if (st != DET_OK) return st;
+    if (!cache_ok(cache) || !decode_sizes_ok(batch, heads, cache->kv_heads, cache->head_dim) ||
+        max_pages < 1 || max_pages > kDimMax || max_pages * cache->page_size > kDimMax ||
+        ldt < max_pages || ldq < heads * cache->head_dim || ldo < heads * cache->head_dim)
+        return DET_ERR_INVALID_ARG;
+    if (batch == 0) return DET_OK;
+    if (!q || !table || !kv_lens || !out) return DET_ERR_INVALID_ARG;
+    const size_t need = decode_workspace_bytes(batch, heads, cache->kv_heads, cache->head_dim,
+                                               max_pages * cache->page_size);
+    if (need > 0 && (!workspace || workspace_bytes < need ||
+                     reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
+        return DET_ERR_WORKSPACE;
+    if ((st = check_device()) != DET_OK) return st;
+    return from_cuda(launch_decode_attention(batch, int(heads), q, ldq, *cache, table, max_pages,
+                                             ldt, kv_lens, scale, out, ldo,
+                                             static_cast<float *>(workspace), dev_status,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+DET_API det_status detlogprob_f32(const det_profile_v1 *prof, int64_t rows, int64_t V,
+                                  const float *logits, int64_t ld, const int32_t *tokens,
+                                  int64_t top_k, float *logp, float *entropy, float *stats,
+                                  int32_t *top_ids, float *top_logp, int32_t *dev_status,
+                                  det_stream_t stream) {
+    det_status st = check_profile(prof);
+    if (st != DET_OK) return st;
+    if (rows < 0 || rows > kDimMax || V < 1 || V > kVocabMax || top_k < 0 || top_k > V ||
+        top_k > kTopMax || ld < V)
+        return DET_ERR_INVALID_ARG;
+    if (rows == 0) return DET_OK;
+    if (!logits || !tokens || !logp || !entropy || (top_k > 0 && (!top_ids || !top_logp)))
+        return DET_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(stats) % 16) return DET_ERR_ALIGNMENT;
+    if ((st = check_device()) != DET_OK) return st;
+    return from_cuda(launch_logprob(rows, V, logits, ld, tokens, int(top_k), logp, entropy, stats,
+                                    top_ids, top_logp, dev_status,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+DET_API det_status detlogprob_bwd_f32(const det_profile_v1 *prof, int64_t rows, int64_t V,
+                                      const float *logits, int64_t ld, const int32_t *tokens,
+                                      const float *stats, const float *dlogp,
+                                      const float *dentropy, float *dlogits, int64_t ldd,
+                                      det_stream_t stream) {
+    det_status st = check_profile(prof);
+    if (st != DET_OK) return st;
+    if (rows < 0 || rows > kDimMax || V < 1 || V > kVocabMax || ld < V || ldd < V)
+        return DET_ERR_INVALID_ARG;
+    if (rows == 0) return DET_OK;
+    if (!logits || !tokens || !stats || !dlogp || !dlogits || (dlogits == logits && ldd != ld))
+        return DET_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(stats) % 16) return DET_ERR_ALIGNMENT;
+    if ((st = check_device()) != DET_OK) return st;
+    return from_cuda(launch_logprob_bwd(rows, V, logits, ld, tokens, stats, dlogp, dentropy,
+                                        dlogits, ldd, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 DET_API det_status det_watchdog_status(int32_t *code, int clear) {
     if (!code) return DET_ERR_INVALID_ARG;
     unsigned int c = 0, c2 = 0;

@@ -183,6 +183,45 @@ cudaError_t launch_exp_map(int64_t n, const float *x, float *y, int is_log,
                            cudaStream_t s);
 cudaError_t launch_adamw(int64_t n, float *p, const float *g, float *m, float *v,
                          const det_adamw_hp &hp, cudaStream_t s);
+// The rotary embedding's angles and layout (det_rotary); rot 0: nothing turns.
+struct RotaryArgs {
+    const uint64_t *turns;
+    float theta;
+    int rot, half;
+};
+cudaError_t launch_rope_at(int64_t rows, int heads, int head_dim, const float *x, int64_t ldx,
+                           const int32_t *positions, const RotaryArgs &ro, int inverse,
+                           float *out, int64_t ldo, cudaStream_t s);
+cudaError_t launch_kv_append(int64_t rows, int heads, const float *qkv, int64_t ldqkv,
+                             const int64_t *slots, const int32_t *positions, const RotaryArgs &ro,
+                             const det_kv_cache &c, float *q_out, int64_t ldq,
+                             int32_t *dev_status, cudaStream_t s);
+cudaError_t launch_pages_extend(int64_t batch, int64_t page_size, const int32_t *lens,
+                                const int32_t *new_tokens, int32_t *table, int64_t max_pages,
+                                int64_t ldt, const int32_t *free_pages, int64_t capacity,
+                                const int32_t *free_count, int64_t max_rows, int32_t *lens_out,
+                                int32_t *free_count_out, int32_t *row_start, int32_t *positions,
+                                int64_t *slots, int32_t *dev_status, cudaStream_t s);
+cudaError_t launch_pages_release(int64_t batch, int64_t page_size, const int32_t *lens,
+                                 const int32_t *done, const int32_t *table, int64_t max_pages,
+                                 int64_t ldt, int32_t *free_pages, int64_t capacity,
+                                 const int32_t *free_count, int32_t *lens_out,
+                                 int32_t *free_count_out, int32_t *dev_status, cudaStream_t s);
+size_t decode_workspace_bytes(int64_t batch, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                              int64_t max_len);
+cudaError_t launch_decode_attention(int64_t batch, int heads, const float *q, int64_t ldq,
+                                    const det_kv_cache &c, const int32_t *table,
+                                    int64_t max_pages, int64_t ldt, const int32_t *kv_lens,
+                                    float scale, float *out, int64_t ldo, float *workspace,
+                                    int32_t *dev_status, cudaStream_t s);
+cudaError_t launch_logprob(int64_t rows, int64_t V, const float *logits, int64_t ld,
+                           const int32_t *tokens, int top_k, float *logp, float *entropy,
+                           float *stats, int32_t *top_ids, float *top_logp, int32_t *dev_status,
+                           cudaStream_t s);
+cudaError_t launch_logprob_bwd(int64_t rows, int64_t V, const float *logits, int64_t ld,
+                               const int32_t *tokens, const float *stats, const float *dlogp,
+                               const float *dentropy, float *dlogits, int64_t ldd,
+                               cudaStream_t s);
 // Host: bc = 1 - beta^t for both betas (beta^t by t-1 sequential products).
 void adamw_bias_correction(int64_t step, float beta1, float beta2, float *bc1, float *bc2);
 

@@ -221,4 +221,30 @@ __device__ __forceinline__ void det_sincos(float x, float &sn, float &cs) {
     cs = q == 0 ? c : q == 1 ? -s : q == 2 ? -c : s;
 }
 
+// sin and cos of a phase in 2^-64 turns: q = the nearest quarter turn (ties
+// up), the signed rest in float, r = rest * (2^-62 pi / 2) with the constant in
+// two floats, then det_sincos's polynomials and quadrant. The phase is exact,
+// so the angle's error does not grow with the position.
+constexpr float kTurnHi = 0x1.921fb6p-62f, kTurnLo = -0x1.777a5cp-87f;
+
+__device__ __forceinline__ void turns_sincos(uint64_t u, float &sn, float &cs) {
+    const unsigned q = unsigned((u + (uint64_t(1) << 61)) >> 62);
+    const float f = __ll2float_rn(static_cast<long long>(u - (uint64_t(q) << 62)));
+    const float r = __fmaf_rn(f, kTurnHi, __fmul_rn(f, kTurnLo));
+    const float z = __fmul_rn(r, r);
+    float ps = kS9;
+    ps = __fmaf_rn(ps, z, kS7);
+    ps = __fmaf_rn(ps, z, kS5);
+    ps = __fmaf_rn(ps, z, kS3);
+    const float s = __fmaf_rn(r, __fmul_rn(z, ps), r);
+    float pc = kCc10;
+    pc = __fmaf_rn(pc, z, kCc8);
+    pc = __fmaf_rn(pc, z, kCc6);
+    pc = __fmaf_rn(pc, z, kCc4);
+    pc = __fmaf_rn(pc, z, kCc2);
+    const float c = __fmaf_rn(pc, z, 1.0f);
+    sn = q == 0 ? s : q == 1 ? c : q == 2 ? -s : -c;
+    cs = q == 0 ? c : q == 1 ? -s : q == 2 ? -c : s;
+}
+
 }  // namespace det

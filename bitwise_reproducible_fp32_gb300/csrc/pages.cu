@@ -1,0 +1,291 @@
+// pages.cu -- block tables and slot maps of a paged key-value cache, built on the
+// GPU from request lengths, for sm_103a.
+//
+// Integers only; a step's arrays are kilobytes, so what bounds these is the
+// latency of one launch and of the two scans over the requests. Every CTA runs
+// the scans over the whole batch itself (a few loads a thread, all in L2) and
+// keeps their results in shared memory; then it takes its share of the rows and
+// pages, finding each one's request by binary search. So one launch serves, no
+// CTA waits for another, and nothing is read that the launch writes.
+#include <algorithm>
+
+#include "det_internal.cuh"
+
+namespace det {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kMaxBatch = 8192;
+constexpr int kPerThread = kMaxBatch / kThreads;
+
+// Exclusive prefix of v over the CTA's threads (all of them call); *total: the sum.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *warp_sums, int64_t *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t in = v;
+#pragma unroll
+    for (int off = 1; off < 32; off *= 2) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, in, off);
+        if (lane >= off) in += o;
+    }
+    if (lane == 31) warp_sums[warp] = in;
+    __syncthreads();
+    int64_t w = warp_sums[lane];
+#pragma unroll
+    for (int off = 1; off < 32; off *= 2) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, w, off);
+        if (lane >= off) w += o;
+    }
+    *total = __shfl_sync(0xffffffffu, w, 31);
+    const int64_t before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
+    __syncthreads();      // warp_sums is used again
+    return (warp ? before : 0) + in - v;
+}
+
+// The last index i < n with a[i] <= v (a ascending, a[0] <= v).
+__device__ __forceinline__ int last_at_most(const int *a, int n, int v) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= v) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+struct ExtendArgs {
+    int batch;
+    int64_t page_size;
+    const int32_t *lens, *new_tokens;
+    int32_t *table;
+    int64_t max_pages, ldt;
+    const int32_t *free_pages;
+    int64_t capacity;
+    const int32_t *free_count;
+    int max_rows;
+    int32_t *lens_out, *free_count_out, *row_start, *positions;
+    int64_t *slots;
+    int32_t *dev_status;
+};
+
+__global__ void __launch_bounds__(kThreads) pages_extend_kernel(ExtendArgs A) {
+    extern __shared__ int sm[];
+    int *s_row = sm;                        // first row of each request
+    int *s_page = sm + A.batch;             // pages taken before it
+    int *s_len = sm + 2 * A.batch;          // its length, or -1 - length when refused
+    __shared__ int64_t warp_sums[32];
+    __shared__ int s_taken;
+    const int tid = threadIdx.x, per = (A.batch + kThreads - 1) / kThreads;
+    const int b0 = tid * per;
+    const int64_t ps = A.page_size, room = min(A.max_pages * ps, int64_t(0x7fffffff));
+    int status = 0;
+    int64_t count = *A.free_count;
+    if (count < 0 || count > A.capacity) {
+        count = 0;
+        status |= 1;
+    }
+    if (tid == 0) s_taken = 0;
+    // 1. rows
+    int len[kPerThread], add[kPerThread];
+    int64_t sum = 0, total_rows, total_pages;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        len[k] = add[k] = 0;
+        if (k < per && b0 + k < A.batch) {
+            len[k] = A.lens[b0 + k];
+            add[k] = A.new_tokens[b0 + k];
+            if (len[k] < 0 || add[k] < 0 || int64_t(len[k]) + add[k] > room) {
+                status |= 1;
+                add[k] = -1;
+            }
+            sum += max(add[k], 0);
+        }
+    }
+    int64_t row = block_scan(sum, warp_sums, &total_rows);
+    // 2. pages, of the requests whose rows fit
+    int need[kPerThread];
+    sum = 0;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        need[k] = 0;
+        if (k < per && b0 + k < A.batch) {
+            s_row[b0 + k] = int(min(row, int64_t(A.max_rows)));
+            row += max(add[k], 0);
+            if (add[k] >= 0 && row > A.max_rows) {
+                status |= 4;
+                add[k] = -1;
+            }
+            if (add[k] >= 0)
+                need[k] = int((int64_t(len[k]) + add[k] + ps - 1) / ps - (len[k] + ps - 1) / ps);
+            sum += need[k];
+        }
+    }
+    int64_t page = block_scan(sum, warp_sums, &total_pages);
+    // 3. a request whose pages run out is refused; those granted are a prefix
+    // of the ones that need any
+    int taken = 0;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        if (k < per && b0 + k < A.batch) {
+            const int b = b0 + k;
+            s_page[b] = int(min(page, count));
+            page += need[k];
+            if (add[k] >= 0 && need[k] > 0) {
+                if (page > count) {
+                    status |= 2;
+                    add[k] = -1;
+                } else {
+                    taken = int(page);
+                }
+            }
+            s_len[b] = add[k] >= 0 ? len[k] : -1 - len[k];
+            if (blockIdx.x == 0) {
+                A.lens_out[b] = add[k] >= 0 ? len[k] + add[k] : len[k];
+                A.row_start[b] = s_row[b];
+            }
+        }
+    }
+    if (taken) atomicMax(&s_taken, taken);
+    status = (__syncthreads_or(status & 1) ? 1 : 0) | (__syncthreads_or(status & 2) ? 2 : 0) |
+             (__syncthreads_or(status & 4) ? 4 : 0);
+    taken = s_taken;
+    const int rows = int(min(total_rows, int64_t(A.max_rows)));
+    if (blockIdx.x == 0 && tid == 0) {
+        A.row_start[A.batch] = rows;
+        *A.free_count_out = int(count) - taken;
+        if (status && A.dev_status) atomicOr(reinterpret_cast<int *>(A.dev_status), status);
+    }
+    const int first = blockIdx.x * kThreads + tid, stride = gridDim.x * kThreads;
+    // 4. the table's new entries
+    for (int64_t p = first; p < taken; p += stride) {
+        const int b = last_at_most(s_page, A.batch, int(p));
+        const int64_t owned = (s_len[b] + ps - 1) / ps;
+        A.table[b * A.ldt + owned + (p - s_page[b])] = A.free_pages[count - 1 - p];
+    }
+    // 5. the rows
+    for (int64_t r = first; r < A.max_rows; r += stride) {
+        int pos = -1;
+        int64_t slot = -1;
+        if (r < rows) {
+            const int b = last_at_most(s_row, A.batch, int(r));
+            if (s_len[b] >= 0) {
+                pos = s_len[b] + int(r - s_row[b]);
+                const int64_t i = pos / ps, owned = (s_len[b] + ps - 1) / ps;
+                const int id = i < owned ? A.table[b * A.ldt + i]
+                                         : A.free_pages[count - 1 - (s_page[b] + i - owned)];
+                slot = id < 0 ? -1 : id * ps + pos % ps;
+            }
+        }
+        A.positions[r] = pos;
+        A.slots[r] = slot;
+    }
+}
+
+struct ReleaseArgs {
+    int batch;
+    int64_t page_size;
+    const int32_t *lens, *done, *table;
+    int64_t max_pages, ldt;
+    int32_t *free_pages;
+    int64_t capacity;
+    const int32_t *free_count;
+    int32_t *lens_out, *free_count_out, *dev_status;
+};
+
+__global__ void __launch_bounds__(kThreads) pages_release_kernel(ReleaseArgs A) {
+    extern __shared__ int sm[];
+    int *s_page = sm;                       // pages given back before each request
+    __shared__ int64_t warp_sums[32];
+    __shared__ int s_given;
+    const int tid = threadIdx.x, per = (A.batch + kThreads - 1) / kThreads;
+    const int b0 = tid * per;
+    const int64_t ps = A.page_size, room = A.max_pages * ps;
+    int status = 0;
+    int64_t count = *A.free_count;
+    const bool lost = count < 0 || count > A.capacity;
+    if (lost) {
+        count = 0;
+        status |= 1;
+    }
+    if (tid == 0) s_given = 0;
+    int len[kPerThread], pages[kPerThread];
+    int64_t sum = 0, total;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        len[k] = 0;
+        pages[k] = -1;
+        if (k < per && b0 + k < A.batch) {
+            len[k] = A.lens[b0 + k];
+            if (A.done[b0 + k]) {
+                if (len[k] < 0 || len[k] > room) status |= 1;
+                else pages[k] = int((len[k] + ps - 1) / ps);
+            }
+            sum += max(pages[k], 0);
+        }
+    }
+    int64_t page = block_scan(sum, warp_sums, &total);
+    int given = 0;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        if (k < per && b0 + k < A.batch) {
+            s_page[b0 + k] = int(min(page, A.capacity));
+            page += max(pages[k], 0);
+            if (pages[k] >= 0) {
+                if (count + page > A.capacity) {
+                    status |= 2;
+                    pages[k] = -1;
+                } else {
+                    given = int(page);
+                }
+            }
+            if (blockIdx.x == 0) A.lens_out[b0 + k] = pages[k] >= 0 ? 0 : len[k];
+        }
+    }
+    if (given) atomicMax(&s_given, given);
+    status = (__syncthreads_or(status & 1) ? 1 : 0) | (__syncthreads_or(status & 2) ? 2 : 0);
+    given = s_given;
+    if (blockIdx.x == 0 && tid == 0) {
+        *A.free_count_out = int(count) + given;
+        if (status && A.dev_status) atomicOr(reinterpret_cast<int *>(A.dev_status), status);
+    }
+    for (int64_t p = blockIdx.x * kThreads + tid; p < given; p += gridDim.x * kThreads) {
+        const int b = last_at_most(s_page, A.batch, int(p));
+        A.free_pages[count + p] = A.table[b * A.ldt + (p - s_page[b])];
+    }
+}
+
+unsigned grid_for(int64_t items) {
+    return unsigned(std::max<int64_t>(
+        1, std::min<int64_t>((items + kThreads - 1) / kThreads, sm_count_current_device())));
+}
+
+}  // namespace
+
+cudaError_t launch_pages_extend(int64_t batch, int64_t page_size, const int32_t *lens,
+                                const int32_t *new_tokens, int32_t *table, int64_t max_pages,
+                                int64_t ldt, const int32_t *free_pages, int64_t capacity,
+                                const int32_t *free_count, int64_t max_rows, int32_t *lens_out,
+                                int32_t *free_count_out, int32_t *row_start, int32_t *positions,
+                                int64_t *slots, int32_t *dev_status, cudaStream_t s) {
+    const ExtendArgs A = {int(batch), page_size, lens, new_tokens, table, max_pages, ldt,
+                          free_pages, capacity, free_count, int(max_rows), lens_out,
+                          free_count_out, row_start, positions, slots, dev_status};
+    const size_t smem = size_t(batch) * 3 * sizeof(int);
+    const cudaError_t e = cudaFuncSetAttribute(
+        pages_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * kMaxBatch * 4);
+    if (e != cudaSuccess) return e;
+    pages_extend_kernel<<<grid_for(max_rows), kThreads, smem, s>>>(A);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pages_release(int64_t batch, int64_t page_size, const int32_t *lens,
+                                 const int32_t *done, const int32_t *table, int64_t max_pages,
+                                 int64_t ldt, int32_t *free_pages, int64_t capacity,
+                                 const int32_t *free_count, int32_t *lens_out,
+                                 int32_t *free_count_out, int32_t *dev_status, cudaStream_t s) {
+    const ReleaseArgs A = {int(batch), page_size, lens, done, table, max_pages, ldt, free_pages,
+                           capacity, free_count, lens_out, free_count_out, dev_status};
+    pages_release_kernel<<<grid_for(std::min(batch * max_pages, capacity)), kThreads,
+                           size_t(batch) * sizeof(int), s>>>(A);
+    return cudaGetLastError();
+}
+
+}  // namespace det

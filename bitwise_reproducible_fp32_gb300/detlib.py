@@ -43,6 +43,21 @@ class GemmProblem(ctypes.Structure):
                 ("C", ctypes.c_void_p), ("ldc", ctypes.c_int64)]
 
 
+class Rotary(ctypes.Structure):
+    """det_rotary."""
+    _fields_ = [("rot_dim", ctypes.c_int64), ("half", ctypes.c_int),
+                ("theta", ctypes.c_float), ("turns", ctypes.c_void_p)]
+
+
+class KVCache(ctypes.Structure):
+    """det_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 class AdamWHP(ctypes.Structure):
     """det_adamw_hp."""
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float),
@@ -118,6 +133,23 @@ SIGNATURES = [
     ("detattention_bwd_saved_f32", _int, [_PROF, _i64, _i64, _i64, _i64, _vp, _i64, _vp,
                                           _i64, _f, _vp, ctypes.c_size_t, _vp, _i64, _vp,
                                           ctypes.c_size_t, _vp]),
+    ("detrope_at_f32", _int, [_PROF, _i64, _i64, _i64, _vp, _i64, _vp, ctypes.POINTER(Rotary),
+                              _int, _vp, _i64, _vp]),
+    ("detkv_append_f32", _int, [_PROF, _i64, _i64, _vp, _i64, _vp, _vp, ctypes.POINTER(Rotary),
+                                ctypes.POINTER(KVCache), _vp, _i64, _vp, _vp]),
+    ("detpages_extend", _int, [_PROF, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _i64,
+                               _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    ("detpages_release", _int, [_PROF, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp,
+                                _vp, _vp, _vp]),
+    ("detdecode_attention_f32", _int, [_PROF, _i64, _i64, _vp, _i64, ctypes.POINTER(KVCache), _vp,
+                                       _i64, _i64, _vp, _f, _vp, _i64, _vp, ctypes.c_size_t,
+                                       _vp, _vp]),
+    ("detdecode_attention_workspace_bytes", _int, [_PROF, _i64, _i64, _i64, _i64, _i64,
+                                                   ctypes.POINTER(ctypes.c_size_t)]),
+    ("detlogprob_f32", _int, [_PROF, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
+                              _vp, _vp]),
+    ("detlogprob_bwd_f32", _int, [_PROF, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64,
+                                  _vp]),
     ("det_watchdog_status", _int, [ctypes.POINTER(ctypes.c_int32), _int]),
 ]
 
@@ -791,6 +823,392 @@ def detadamw_f32(p, g, m, v, lr, beta1, beta2, eps, weight_decay, step,
                              ctypes.byref(hp), _stream(stream))
     _check("detadamw_f32", st)
     return p, m, v
+
+
+# ---------------------------------------------------------------- generation
+def _here(first, *rest):
+    """Every tensor lies on the current device, where the call runs."""
+    import torch
+    dev = torch.cuda.current_device()
+    if first.device.index != dev or any(t is not None and t.device.index != dev for t in rest):
+        raise ValueError(f"tensors must be on the current device, cuda:{dev}")
+
+
+def _empty(shape, like, stream, dtype=None):
+    """A tensor for this call's outputs, allocated for the stream it runs on."""
+    import torch
+    dtype = torch.float32 if dtype is None else dtype
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _cuda_int(t, name, dtype, n=None):
+    """A contiguous 1-D CUDA tensor of dtype (of n elements where given)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or t.dtype != dtype:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be 1-D and contiguous")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
+    return t
+
+
+def _cuda_rows(t, name, dtype, rows=None, cols=None):
+    """A 2-D CUDA tensor of dtype with contiguous rows (of the given shape)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or t.dtype != dtype:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.dim() != 2 or (t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be {rows} x {cols}, got {tuple(t.shape)}")
+    return t
+
+
+def _row_stride(t):
+    # a single row has no stride to speak of: report its length
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _status_word(t):
+    import torch
+    if t is not None:
+        _cuda_int(t, "dev_status", torch.int32, 1)
+    return t
+
+
+def rope_turns(rot_dim, theta=10000.0, factor=1.0, low=None, high=None, trained=None,
+               device="cuda"):
+    """Rotary frequencies as the 64-bit fixed-point turns a position that
+    detrope_at_f32 and detkv_append_f32 take (an int64 tensor of rot_dim / 2
+    values holding the 64 bits): w_i = theta^(-2i / rot_dim), formed in double.
+    factor > 1 stretches them for contexts longer than those trained on: all of
+    them by 1 / factor; or, with low, high and trained (the trained length), by
+    how many turns r = trained w_i / (2 pi) a pair makes over it: as they are for
+    r >= high, by 1 / factor for r <= low, and a blend of the two, linear in r,
+    between. All frequencies must lie in [0, pi]."""
+    import numpy as np
+    import torch
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and at least 2")
+    if not (factor >= 1.0 and theta > 0.0):
+        raise ValueError("factor must be at least 1 and theta positive")
+    w = np.float64(theta) ** (-np.arange(0, rot_dim, 2, dtype=np.float64) / rot_dim)
+    if trained is None:
+        if low is not None or high is not None:
+            raise ValueError("low and high go with trained")
+        w = w / factor
+    else:
+        if low is None or high is None or not 0.0 <= low < high:
+            raise ValueError("0 <= low < high go with trained")
+        keep = np.clip((trained * w / (2.0 * np.pi) - low) / (high - low), 0.0, 1.0)
+        w = w * (keep + (1.0 - keep) / factor)
+    if w.max() > np.pi:
+        raise ValueError("a frequency is above half a turn a position")
+    turns = np.rint(w / (2.0 * np.pi) * 2.0 ** 64).astype(np.uint64)
+    return torch.from_numpy(turns.view(np.int64)).to(device)
+
+
+def _rotary(head_dim, theta, turns, rot_dim, half):
+    import torch
+    if turns is not None:
+        _cuda_int(turns, "turns", torch.int64)
+        if rot_dim is None:
+            rot_dim = 2 * turns.numel()
+        if turns.numel() != rot_dim // 2:
+            raise ValueError(f"turns must hold {rot_dim // 2} values")
+    elif rot_dim is None:
+        rot_dim = head_dim
+    if rot_dim % 2 or not 2 <= rot_dim <= head_dim:
+        raise ValueError(f"rot_dim must be even, 2..{head_dim}")
+    return Rotary(rot_dim, int(bool(half)), theta, turns.data_ptr() if turns is not None else None)
+
+
+def detrope_at_f32(x, positions, heads, head_dim, theta=10000.0, turns=None, rot_dim=None,
+                   half=False, inverse=False, out=None, profile=None, stream=None):
+    """Rotary embedding of the rows of x (their first heads * head_dim columns) at
+    the int32 positions, into out (default: a new rows x heads * head_dim tensor;
+    out=x works in place). Negative positions pass through. turns: frequencies of
+    rope_turns (rot_dim defaults to all of them); None: theta, the bits of
+    detrope_f32. half: pairs (i, i + rot_dim / 2) instead of (2i, 2i+1). inverse:
+    the backward (dx from dy). Returns out."""
+    import torch
+    _cuda_rows(x, "x", torch.float32)
+    rows, width = x.shape[0], heads * head_dim
+    _cuda_int(positions, "positions", torch.int32, rows)
+    ro = _rotary(head_dim, theta, turns, rot_dim, half)
+    if x.shape[1] < width:
+        raise ValueError(f"x must have at least {width} columns")
+    if out is None:
+        out = _empty((rows, width), x, stream)
+    _cuda_rows(out, "out", torch.float32)
+    if out.shape[0] != rows or out.shape[1] < width:
+        raise ValueError(f"out must be {rows} rows of at least {width} columns")
+    _here(x, positions, turns, out)
+    _check("detrope_at_f32",
+           load().detrope_at_f32(_prof(profile), rows, heads, head_dim, x.data_ptr(),
+                                 _row_stride(x), positions.data_ptr(), ctypes.byref(ro),
+                                 int(bool(inverse)), out.data_ptr(), _row_stride(out),
+                                 _stream(stream)))
+    return out
+
+
+def _kv_cache(k_cache, v_cache):
+    import torch
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype != torch.float32:
+            raise TypeError(f"{name} must be float32 (the profile is FP32 only), got {t.dtype}")
+        if t.dim() != 4 or t.numel() == 0:
+            raise ValueError(f"{name} must be pages x page_size x kv_heads x head_dim")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must agree in shape and strides")
+    P, ps, G, d = k_cache.shape
+    sp, stok, sh, sd = k_cache.stride()
+    if d > 1 and sd != 1:
+        raise ValueError("the cache's last dimension must be contiguous")
+    # a dimension of one entry has no stride to speak of
+    sp, stok, sh = (s if n > 1 else (d + 3) // 4 * 4 for s, n in ((sp, P), (stok, ps), (sh, G)))
+    return KVCache(k_cache.data_ptr(), v_cache.data_ptr(), P, ps, G, d, sp, stok, sh)
+
+
+def detkv_append_f32(qkv, slots, k_cache, v_cache, heads, positions=None, theta=10000.0,
+                     turns=None, rot_dim=None, half=False, q_out=None, dev_status=None,
+                     profile=None, stream=None):
+    """Appends rows of packed [Q | K | V] to a paged cache (k_cache, v_cache: pages
+    x page_size x kv_heads x head_dim, any strides with contiguous head_dim): row
+    t's key and value go to slot slots[t] (int64; page * page_size + offset,
+    negative: padding, the row is skipped). positions (int32): Q and K are turned
+    there first as by detrope_at_f32 (a negative one is padding too) and Q goes to
+    q_out, by default the Q block of qkv itself; None: K is stored as it is and Q
+    stays. Rows that share a slot: the last one is kept. Returns q_out (None
+    without positions)."""
+    import torch
+    c = _kv_cache(k_cache, v_cache)
+    _cuda_rows(qkv, "qkv", torch.float32)
+    rows = qkv.shape[0]
+    if qkv.shape[1] < (heads + 2 * c.kv_heads) * c.head_dim:
+        raise ValueError(f"qkv must have {(heads + 2 * c.kv_heads) * c.head_dim} columns")
+    _cuda_int(slots, "slots", torch.int64, rows)
+    ro = None
+    if positions is not None:
+        _cuda_int(positions, "positions", torch.int32, rows)
+        ro = _rotary(c.head_dim, theta, turns, rot_dim, half)
+        width = heads * c.head_dim
+        if q_out is None:
+            q_out = qkv
+        _cuda_rows(q_out, "q_out", torch.float32)
+        if q_out.shape[0] != rows or q_out.shape[1] < width:
+            raise ValueError(f"q_out must be {rows} rows of at least {width} columns")
+    elif turns is not None or q_out is not None:
+        raise ValueError("turns and q_out need positions")
+    _status_word(dev_status)
+    _here(qkv, slots, k_cache, v_cache, positions, turns, q_out, dev_status)
+    _check("detkv_append_f32",
+           load().detkv_append_f32(_prof(profile), rows, heads, qkv.data_ptr(),
+                                   _row_stride(qkv), slots.data_ptr(), _ptr(positions),
+                                   ctypes.byref(ro) if ro is not None else None,
+                                   ctypes.byref(c), _ptr(q_out),
+                                   _row_stride(q_out) if q_out is not None else 0,
+                                   _ptr(dev_status), _stream(stream)))
+    return q_out[:, :heads * c.head_dim] if q_out is qkv else q_out
+
+
+def detpages_extend(lens, new_tokens, table, free_pages, free_count, page_size, max_rows,
+                    lens_out=None, free_count_out=None, row_start=None, positions=None,
+                    slots=None, dev_status=None, profile=None, stream=None):
+    """The block tables and slot maps of a step that gives request b new_tokens[b]
+    more tokens after lens[b] (int32 CUDA tensors of one length). table: requests
+    x max_pages int32, in place; free_pages: int32 page ids, the first
+    free_count[0] of them free, taken from the end. Returns (lens_out,
+    free_count_out, row_start, positions, slots): the lengths and the count after
+    the step, the rows of each request (one more value than requests), and of each
+    of the max_rows rows its position (int32) and slot (int64), -1 where there is
+    none. A request that cannot have all its tokens gets none (dev_status bits: 1
+    a length or count out of range, 2 out of pages, 4 past max_rows)."""
+    import torch
+    i32 = torch.int32
+    batch = lens.numel()
+    _cuda_int(lens, "lens", i32)
+    _cuda_int(new_tokens, "new_tokens", i32, batch)
+    _cuda_rows(table, "table", i32)
+    if table.shape[0] != batch:
+        raise ValueError(f"table must have {batch} rows")
+    _cuda_int(free_pages, "free_pages", i32)
+    _cuda_int(free_count, "free_count", i32, 1)
+    new = lambda t, name, n, dt: (_cuda_int(t, name, dt, n) if t is not None  # noqa: E731
+                                  else _empty((n,), lens, stream, dt))
+    lens_out = new(lens_out, "lens_out", batch, i32)
+    free_count_out = new(free_count_out, "free_count_out", 1, i32)
+    row_start = new(row_start, "row_start", batch + 1, i32)
+    positions = new(positions, "positions", max_rows, i32)
+    slots = new(slots, "slots", max_rows, torch.int64)
+    _status_word(dev_status)
+    _here(lens, new_tokens, table, free_pages, free_count, lens_out, free_count_out, row_start,
+          positions, slots, dev_status)
+    _check("detpages_extend",
+           load().detpages_extend(_prof(profile), batch, page_size, lens.data_ptr(),
+                                  new_tokens.data_ptr(), table.data_ptr(), table.shape[1],
+                                  _row_stride(table), free_pages.data_ptr(), free_pages.numel(),
+                                  free_count.data_ptr(), max_rows, lens_out.data_ptr(),
+                                  free_count_out.data_ptr(), row_start.data_ptr(),
+                                  positions.data_ptr(), slots.data_ptr(), _ptr(dev_status),
+                                  _stream(stream)))
+    return lens_out, free_count_out, row_start, positions, slots
+
+
+def detpages_release(lens, done, table, free_pages, free_count, page_size, lens_out=None,
+                     free_count_out=None, dev_status=None, profile=None, stream=None):
+    """Gives the pages of every request with done[b] != 0 (int32) back to
+    free_pages, from free_count[0] on. Returns (lens_out, free_count_out), the
+    lengths (0 for those) and the count after. dev_status bits: 1 a length out of
+    range, 2 the free list is full."""
+    import torch
+    i32 = torch.int32
+    batch = lens.numel()
+    _cuda_int(lens, "lens", i32)
+    _cuda_int(done, "done", i32, batch)
+    _cuda_rows(table, "table", i32)
+    if table.shape[0] != batch:
+        raise ValueError(f"table must have {batch} rows")
+    _cuda_int(free_pages, "free_pages", i32)
+    _cuda_int(free_count, "free_count", i32, 1)
+    lens_out = (_empty((batch,), lens, stream, i32) if lens_out is None
+                else _cuda_int(lens_out, "lens_out", i32, batch))
+    free_count_out = (_empty((1,), lens, stream, i32) if free_count_out is None
+                      else _cuda_int(free_count_out, "free_count_out", i32, 1))
+    _status_word(dev_status)
+    _here(lens, done, table, free_pages, free_count, lens_out, free_count_out, dev_status)
+    _check("detpages_release",
+           load().detpages_release(_prof(profile), batch, page_size, lens.data_ptr(),
+                                   done.data_ptr(), table.data_ptr(), table.shape[1],
+                                   _row_stride(table), free_pages.data_ptr(),
+                                   free_pages.numel(), free_count.data_ptr(),
+                                   lens_out.data_ptr(), free_count_out.data_ptr(),
+                                   _ptr(dev_status), _stream(stream)))
+    return lens_out, free_count_out
+
+
+def detdecode_attention_workspace_bytes(batch, heads, kv_heads, head_dim, max_len,
+                                        profile=None) -> int:
+    n = ctypes.c_size_t(0)
+    _check("detdecode_attention_workspace_bytes",
+           load().detdecode_attention_workspace_bytes(_prof(profile), batch, heads, kv_heads,
+                                                      head_dim, max_len, ctypes.byref(n)))
+    return n.value
+
+
+def detdecode_attention_f32(q, k_cache, v_cache, table, kv_lens, heads, scale=None, out=None,
+                            workspace=None, dev_status=None, profile=None, stream=None):
+    """Attention of one new token a request over a paged cache: row b of q (heads *
+    head_dim columns) against the kv_lens[b] (int32, the new token included)
+    tokens in the pages table[b] (int32, requests x max_pages). The heads are a
+    multiple of the cache's. Bit for bit the last row of detattention_f32 over
+    those tokens; a length of 0 gives 0. dev_status bits: 1 a length out of range,
+    2 a page out of range (the row is NaN). Returns out (requests x heads *
+    head_dim)."""
+    import torch
+    c = _kv_cache(k_cache, v_cache)
+    _cuda_rows(q, "q", torch.float32)
+    batch, width = q.shape[0], heads * c.head_dim
+    if q.shape[1] < width:
+        raise ValueError(f"q must have at least {width} columns")
+    _cuda_rows(table, "table", torch.int32)
+    if table.shape[0] != batch:
+        raise ValueError(f"table must have {batch} rows")
+    _cuda_int(kv_lens, "kv_lens", torch.int32, batch)
+    if out is None:
+        out = _empty((batch, width), q, stream)
+    _cuda_rows(out, "out", torch.float32)
+    if out.shape[0] != batch or out.shape[1] < width:
+        raise ValueError(f"out must be {batch} rows of at least {width} columns")
+    if scale is None:
+        scale = 1.0 / float(c.head_dim) ** 0.5
+    max_pages = table.shape[1]
+    if workspace is None:
+        need = detdecode_attention_workspace_bytes(batch, heads, c.kv_heads, c.head_dim,
+                                                   max_pages * c.page_size, profile)
+        if need:
+            workspace = _empty(((need + 3) // 4,), q, stream)
+    else:
+        _cuda_f32(workspace, "workspace", 1)
+    _status_word(dev_status)
+    _here(q, k_cache, v_cache, table, kv_lens, out, workspace, dev_status)
+    _check("detdecode_attention_f32",
+           load().detdecode_attention_f32(_prof(profile), batch, heads, q.data_ptr(),
+                                          _row_stride(q), ctypes.byref(c), table.data_ptr(),
+                                          max_pages, _row_stride(table), kv_lens.data_ptr(),
+                                          scale, out.data_ptr(), _row_stride(out),
+                                          _ptr(workspace),
+                                          workspace.numel() * 4 if workspace is not None else 0,
+                                          _ptr(dev_status), _stream(stream)))
+    return out
+
+
+def detlogprob_f32(logits, tokens, top_k=0, want_stats=True, logp=None, entropy=None, stats=None,
+                   top_ids=None, top_logp=None, dev_status=None, profile=None, stream=None):
+    """Log probabilities of the int32 tokens under rows of logits (-1: no token, 0;
+    outside the vocabulary: NaN and dev_status bit 1), the rows' entropies, and
+    their top_k (0..32) largest alternatives, the lowest id first among equals.
+    Returns (logp, entropy, top_ids, top_logp, stats): rows, rows, rows x top_k
+    int32 and float, and the rows x 4 floats that detlogprob_bwd_f32 reads (None
+    unless want_stats)."""
+    import torch
+    f32 = torch.float32
+    _cuda_rows(logits, "logits", f32)
+    rows, V = logits.shape
+    _cuda_int(tokens, "tokens", torch.int32, rows)
+    logp = _empty((rows,), logits, stream) if logp is None else _cuda_f32(logp, "logp", 1)
+    entropy = (_empty((rows,), logits, stream) if entropy is None
+               else _cuda_f32(entropy, "entropy", 1))
+    if stats is None and want_stats:
+        stats = _empty((rows, 4), logits, stream)
+    top_ids = (_empty((rows, top_k), logits, stream, torch.int32) if top_ids is None else top_ids)
+    top_logp = _empty((rows, top_k), logits, stream) if top_logp is None else top_logp
+    if logp.numel() != rows or entropy.numel() != rows:
+        raise ValueError(f"logp and entropy must hold {rows} values")
+    for t, name, dt, n in ((stats, "stats", f32, 4), (top_ids, "top_ids", torch.int32, top_k),
+                           (top_logp, "top_logp", f32, top_k)):
+        if t is not None and not _cuda_rows(t, name, dt, rows, n).is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    _status_word(dev_status)
+    _here(logits, tokens, logp, entropy, stats, top_ids, top_logp, dev_status)
+    _check("detlogprob_f32",
+           load().detlogprob_f32(_prof(profile), rows, V, logits.data_ptr(), _row_stride(logits),
+                                 tokens.data_ptr(), top_k, logp.data_ptr(), entropy.data_ptr(),
+                                 _ptr(stats), top_ids.data_ptr(), top_logp.data_ptr(),
+                                 _ptr(dev_status), _stream(stream)))
+    return logp, entropy, top_ids, top_logp, stats
+
+
+def detlogprob_bwd_f32(logits, tokens, stats, dlogp, dentropy=None, dlogits=None, profile=None,
+                       stream=None):
+    """The gradient of sum(dlogp * logp) + sum(dentropy * entropy) with respect to
+    the logits, from detlogprob_f32's stats. dlogits may be the logits (in place).
+    Returns dlogits."""
+    import torch
+    f32 = torch.float32
+    _cuda_rows(logits, "logits", f32)
+    rows, V = logits.shape
+    _cuda_int(tokens, "tokens", torch.int32, rows)
+    if not _cuda_rows(stats, "stats", f32, rows, 4).is_contiguous():
+        raise ValueError("stats must be contiguous")
+    for t, name in ((dlogp, "dlogp"), (dentropy, "dentropy")):
+        if t is not None and _cuda_f32(t, name, 1).numel() != rows:
+            raise ValueError(f"{name} must hold {rows} values")
+    dlogits = _empty((rows, V), logits, stream) if dlogits is None else dlogits
+    _cuda_rows(dlogits, "dlogits", f32, rows, V)
+    _here(logits, tokens, stats, dlogp, dentropy, dlogits)
+    _check("detlogprob_bwd_f32",
+           load().detlogprob_bwd_f32(_prof(profile), rows, V, logits.data_ptr(),
+                                     _row_stride(logits), tokens.data_ptr(), stats.data_ptr(),
+                                     dlogp.data_ptr(), _ptr(dentropy), dlogits.data_ptr(),
+                                     _row_stride(dlogits), _stream(stream)))
+    return dlogits
 
 
 # ---------------------------------------------------------------- exp / log

@@ -617,6 +617,205 @@ det_status detattention_bwd_saved_f32(const det_profile_v1 *prof, int64_t batch,
                                       void *workspace, size_t workspace_bytes,
                                       det_stream_t stream);
 
+/* ------------------------------------------------------------------ generation
+ * One step of generation with a trained model: block tables and slot maps of a
+ * paged key-value cache, the rotary embedding at positions of the caller's
+ * own, the append of new keys and values, attention of one new token over the
+ * cache, and the log probabilities of tokens with their gradient. The pages
+ * train and evaluate and print no generation path; these are profile v1's
+ * readings, chosen so that a generation step gives the bits of the training
+ * forward at that position (the GEMMs, RMSNorm and SwiGLU of a row do not
+ * depend on the other rows). */
+
+/* How positions turn into rotary angles, shared by the two rotary calls below.
+ * turns (device, rot_dim / 2 values) or NULL:
+ *   NULL   detrope_f32's angles with rot_dim in the place of head_dim:
+ *          a = (float)pos * w_i, w_i = exp(-((float)(2i) / (float)rot_dim) *
+ *          log(theta)), in float (so |a| > 2^20 gives NaN), and the profile's
+ *          sin and cos of it: the bits of detrope_f32;
+ *   else   frequencies of the caller's own, as 64-bit fixed-point turns a
+ *          position: turns[i] = w_i / (2 pi) in units of 2^-64. The phase pos *
+ *          turns[i] is exact modulo one turn at any position; q = the nearest
+ *          quarter turn (ties up), f = the signed rest (in [-2^61, 2^61)) rounded
+ *          to float, r = fmaf(f, HI, f * LO) with HI + LO = 2^-62 pi / 2 in two
+ *          floats, then the sin and cos polynomials in r and the quadrant q.
+ * rot_dim: the first rot_dim elements of each head turn (even, 2 .. head_dim);
+ * the rest pass through. half 0: pairs (2i, 2i+1); else pairs
+ * (i, i + rot_dim / 2). Each pair: y0 = x0 c - x1 s, y1 = x0 s + x1 c (products
+ * rounded, then the difference or sum). */
+typedef struct det_rotary {
+    int64_t rot_dim;
+    int half;
+    float theta;
+    const uint64_t *turns;
+} det_rotary;
+
+/* Rotary embedding of row t of x (heads x head_dim floats, row stride ldx) at
+ * position positions[t] (device int32) into out (row stride ldo). inverse != 0
+ * turns by the negative angle: the backward, dx from dy. A negative position
+ * marks padding: the row passes through unturned. out may equal x when
+ * ldo == ldx (in place) and must not otherwise overlap it; columns past
+ * heads * head_dim are not touched. rows may be 0.
+ * Errors: DET_ERR_INVALID_ARG for negative rows, heads or head_dim outside
+ * 1..65536, rot_dim odd or outside 2..head_dim, a stride below its row, null
+ * pointers, or out == x with another stride. */
+det_status detrope_at_f32(const det_profile_v1 *prof, int64_t rows, int64_t heads,
+                          int64_t head_dim, const float *x, int64_t ldx,
+                          const int32_t *positions, const det_rotary *rotary, int inverse,
+                          float *out, int64_t ldo, det_stream_t stream);
+
+/* A paged key-value cache (host struct, read during the call): the token in
+ * slot s (page s / page_size, offset s mod page_size) has its key of head g at
+ * k + page * page_stride + offset * token_stride + g * head_stride (in floats),
+ * head_dim contiguous floats; its value likewise from v. Any order of pages,
+ * tokens and heads can be described; two (page, offset, head) must not share
+ * floats. */
+typedef struct det_kv_cache {
+    float *k, *v;
+    int64_t num_pages, page_size, kv_heads, head_dim;
+    int64_t page_stride, token_stride, head_stride;
+} det_kv_cache;
+
+/* Appends rows of packed [Q | K | V] (heads, kv_heads and kv_heads heads of
+ * cache->head_dim floats, row stride ldqkv) to the cache: row t's V goes to slot
+ * slots[t] (device int64), its K too, turned at positions[t], and its Q, turned,
+ * to q_out (row stride ldq). rotary NULL (positions may be NULL then): K and V
+ * are stored as they are and q_out is not used. q_out NULL: Q is left out; q_out
+ * may be qkv itself with ldq == ldqkv (Q in place) and must not otherwise
+ * overlap qkv. The K and V blocks of qkv are not changed.
+ * A negative slot (or, with rotary, a negative position) marks padding: nothing
+ * is read or written for the row. A slot at or past num_pages * page_size ORs
+ * 1 into *dev_status (device int32, may be NULL) and is skipped likewise.
+ * Where several rows name the same slot, the cache holds the last such row.
+ * Errors: DET_ERR_INVALID_ARG for negative rows, heads outside 1..65536, a
+ * cache with null pointers, sizes below 1, head_dim above 256, kv_heads above
+ * 65536 or a stride below head_dim, and the rotary's and the strides' rules. */
+det_status detkv_append_f32(const det_profile_v1 *prof, int64_t rows, int64_t heads,
+                            const float *qkv, int64_t ldqkv, const int64_t *slots,
+                            const int32_t *positions, const det_rotary *rotary,
+                            const det_kv_cache *cache, float *q_out, int64_t ldq,
+                            int32_t *dev_status, det_stream_t stream);
+
+/* Block tables and slot maps of a step that gives request b new_tokens[b] more
+ * tokens after its lens[b] (device int32 arrays of `batch`). All arrays are
+ * device memory. table: batch x max_pages int32, row stride ldt; request b's
+ * first ceil(lens[b] / page_size) entries are its pages. free_pages: capacity
+ * page ids, of which the first *free_count are free; pages are taken from the
+ * end (free_pages[*free_count - 1] first) by ascending request, then ascending
+ * position, and written to the table's next entries; nothing else of the table
+ * and nothing of free_pages changes.
+ * Rows of new tokens are numbered through the requests in order: request b has
+ * rows row_start[b] .. row_start[b + 1] - 1 (row_start: batch + 1 values, each at
+ * most max_rows). positions (max_rows int32) and slots (max_rows int64) of each
+ * row: its position lens[b] + i and its slot; rows past the last hold -1.
+ * lens_out (batch) and free_count_out (1) are the lengths and the count after
+ * the step; they must not overlap lens and free_count.
+ * A request gets all of its tokens or none: one with a negative length or
+ * count, or more tokens than its table row holds, takes no rows and ORs 1 into
+ * *dev_status (may be NULL); one whose pages or those of the requests before
+ * it run out ORs 2, and one whose rows end past max_rows ORs 4: the rows of
+ * these hold -1 and their lengths stay. A *free_count outside 0..capacity
+ * counts as 0 and ORs 1.
+ * batch 0..8192; one launch. Errors: DET_ERR_INVALID_ARG for sizes outside
+ * their ranges (page_size >= 1, max_pages >= 1, ldt >= max_pages, 0 <= max_rows,
+ * 0 <= capacity, all < 2^31) or null pointers. */
+det_status detpages_extend(const det_profile_v1 *prof, int64_t batch, int64_t page_size,
+                           const int32_t *lens, const int32_t *new_tokens, int32_t *table,
+                           int64_t max_pages, int64_t ldt, const int32_t *free_pages,
+                           int64_t capacity, const int32_t *free_count, int64_t max_rows,
+                           int32_t *lens_out, int32_t *free_count_out, int32_t *row_start,
+                           int32_t *positions, int64_t *slots, int32_t *dev_status,
+                           det_stream_t stream);
+
+/* Gives the pages of every request b with done[b] != 0 back: its first
+ * ceil(lens[b] / page_size) table entries are written to free_pages from
+ * *free_count on, by ascending request, then position; lens_out[b] = 0. The
+ * other requests' lengths are copied to lens_out, and free_count_out is the
+ * count after. The table is not changed. A done request with a length outside
+ * its table row ORs 1 into *dev_status; one whose pages do not fit the
+ * free list's capacity ORs 2; both keep their length. Sizes and errors as
+ * detpages_extend. */
+det_status detpages_release(const det_profile_v1 *prof, int64_t batch, int64_t page_size,
+                            const int32_t *lens, const int32_t *done, const int32_t *table,
+                            int64_t max_pages, int64_t ldt, int32_t *free_pages,
+                            int64_t capacity, const int32_t *free_count, int32_t *lens_out,
+                            int32_t *free_count_out, int32_t *dev_status, det_stream_t stream);
+
+/* Attention of one new token a request over the paged cache: row b of q (heads
+ * x head_dim, row stride ldq) against the kv_lens[b] tokens (device int32, the
+ * new one included) in the pages table[b] (batch x max_pages int32, row stride
+ * ldt); query head h reads key-value head h / (heads / kv_heads). Per head, as
+ * the last row of detattention_f32 over those tokens (the same bits):
+ *   s_j = fmaf chain of q K_j from +0 over ascending d, x_j = s_j * scale;
+ *   m = max x_j (NaN-propagating), e_j = exp(x_j - m), S = the 256-chain sum of
+ *   the e_j folded by the butterfly, p_j = e_j * (1 / S);
+ *   o = fmaf chains of p_j V_j from +0 over each 256 tokens in ascending j, the
+ *   chunks added left to right.
+ * The bits do not depend on the page size, the table, the strides or the other
+ * requests. kv_lens[b] == 0 gives +0. A negative length or one past max_pages *
+ * page_size ORs 1 into *dev_status (may be NULL), a page outside
+ * 0..num_pages-1 among the request's ORs 2; the request's row is NaN then.
+ * Entries of the table past a request's pages are not read, nor are the slots
+ * past its length. out: row stride ldo, must not overlap q or the cache.
+ * workspace: at least detdecode_attention_workspace_bytes (16-byte aligned, no
+ * contents assumed); calls that share one must be ordered (one stream).
+ * Errors: DET_ERR_INVALID_ARG for batch outside 0..65535, heads not a multiple
+ * of kv_heads, the cache's rules (detkv_append_f32), max_pages < 1, max_pages *
+ * page_size >= 2^31, strides or null pointers; DET_ERR_WORKSPACE. */
+det_status detdecode_attention_f32(const det_profile_v1 *prof, int64_t batch, int64_t heads,
+                                   const float *q, int64_t ldq, const det_kv_cache *cache,
+                                   const int32_t *table, int64_t max_pages, int64_t ldt,
+                                   const int32_t *kv_lens, float scale, float *out, int64_t ldo,
+                                   void *workspace, size_t workspace_bytes,
+                                   int32_t *dev_status, det_stream_t stream);
+/* Workspace detdecode_attention_f32 needs for requests of up to max_len tokens
+ * (max_len = max_pages * page_size there), written to *bytes. */
+det_status detdecode_attention_workspace_bytes(const det_profile_v1 *prof, int64_t batch,
+                                               int64_t heads, int64_t kv_heads,
+                                               int64_t head_dim, int64_t max_len, size_t *bytes);
+
+/* Log probabilities of given tokens under rows of V logits, with the entropy
+ * and the top_k largest alternatives of each row:
+ *   m, e_j and S as detxent_f32 forms them; logp = (x_y - m) - log(S), so
+ *   logp = -loss of detxent_f32 bit for bit;
+ *   entropy = log(S) - T / S with T the sum of e_j * (x_j - m): 4096 chains, chain
+ *   j mod 4096 taking T = fmaf(e_j, x_j - m, T) from +0 in ascending j (elements
+ *   with e_j == 0 left out), folded as ((T_4t + T_4t+1) + T_4t+2) + T_4t+3, then
+ *   the butterfly 16..1 within each 32 consecutive t and the same butterfly over
+ *   the 32 totals;
+ *   the alternatives: the top_k largest logits, the lowest id first among equal
+ *   ones (+0 and -0 are equal; NaN counts as larger than +Inf), each with
+ *   (x - m) - log(S).
+ * A row whose maximum is NaN or infinite has NaN scores (its ids are still
+ * ordered); a -Inf logit elsewhere has probability 0.
+ * tokens: rows int32. -1 asks for no token: logp +0. Any other outside [0, V) gives
+ * logp NaN and ORs 1 into *dev_status (device int32, may be NULL); entropy and
+ * alternatives are formed either way.
+ * logp, entropy: rows floats. stats: rows x 4 floats (m, 1 / S, log S, entropy),
+ * what the gradient reads, 16-byte aligned, or NULL. top_ids (int32) and top_logp
+ * (floats): rows x top_k, dense; NULL when top_k is 0.
+ * V in 1..2^30, top_k in 0..min(V, 32), rows may be 0.
+ * Errors: DET_ERR_INVALID_ARG for sizes, strides or null pointers;
+ * DET_ERR_ALIGNMENT for a misaligned stats. */
+det_status detlogprob_f32(const det_profile_v1 *prof, int64_t rows, int64_t V,
+                          const float *logits, int64_t ld, const int32_t *tokens, int64_t top_k,
+                          float *logp, float *entropy, float *stats, int32_t *top_ids,
+                          float *top_logp, int32_t *dev_status, det_stream_t stream);
+
+/* The gradient of sum over rows of dlogp * logp + dentropy * entropy with respect
+ * to the logits, from the forward's stats. Per element, each operation rounded
+ * once: d = x_j - m, p = exp(d) * (1 / S), a = dlogp * ([j == y] - p),
+ *   w = p * ((d - log S) + entropy)   (+0 where p == 0),
+ *   dlogits_j = a - dentropy * w      (a when dentropy is NULL).
+ * A token of -1: a = +0. Any other outside [0, V): the row is NaN.
+ * dlogits: row stride ldd >= V; it may equal logits when ldd == ld (in place) and
+ * must not otherwise overlap it. dlogp, dentropy: rows floats. Errors as
+ * detlogprob_f32. */
+det_status detlogprob_bwd_f32(const det_profile_v1 *prof, int64_t rows, int64_t V,
+                              const float *logits, int64_t ld, const int32_t *tokens,
+                              const float *stats, const float *dlogp, const float *dentropy,
+                              float *dlogits, int64_t ldd, det_stream_t stream);
+
 /* Reads, and optionally clears, the current device's watchdog word.
  * *code == 0 means no bounded device wait has ever given up; otherwise bit k
  * identifies the kernel family that gave up (bit 0: GEMM operand staging,
