@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(LogprobArgs A) {
         __syncthreads();
         m = red[0];
         for (int w = 1; w < kThreads / 32; ++w) m = max_nan(m, red[w]);
+        m = __fadd_rn(m, 0.0f);          // a zero maximum is +0
         __syncthreads();
         // elements 4 (tid + 256 t) .. + 3 of sweep t lie on chains
         // 4 (tid + 256 (t mod 4)) .. + 3 of T

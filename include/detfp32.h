@@ -776,8 +776,8 @@ det_status detdecode_attention_workspace_bytes(const det_profile_v1 *prof, int64
 
 /* Log probabilities of given tokens under rows of V logits, with the entropy
  * and the top_k largest alternatives of each row:
- *   m, e_j and S as detxent_f32 forms them; logp = (x_y - m) - log(S), so
- *   logp = -loss of detxent_f32 bit for bit;
+ *   m (+0 for a zero of either sign), e_j and S as detxent_f32 forms them;
+ *   logp = (x_y - m) - log(S), so logp = -loss of detxent_f32 bit for bit;
  *   entropy = log(S) - T / S with T the sum of e_j * (x_j - m): 4096 chains, chain
  *   j mod 4096 taking T = fmaf(e_j, x_j - m, T) from +0 in ascending j (elements
  *   with e_j == 0 left out), folded as ((T_4t + T_4t+1) + T_4t+2) + T_4t+3, then

@@ -898,6 +898,7 @@ static void logprob_rows(int64_t lo, int64_t hi, int tix, void *c) {
         const int64_t y = q->tokens[r];
         float m = x[0];
         for (int64_t j = 1; j < q->V; ++j) if (x[j] > m || x[j] != x[j]) m = x[j];
+        m = m + 0.0f;          /* a zero maximum is +0 */
         for (int l = 0; l < q->lanes; ++l) s[l] = 0.0f;
         for (int l = 0; l < 4096; ++l) T[l] = 0.0f;
         for (int64_t j = 0; j < q->V; ++j) {

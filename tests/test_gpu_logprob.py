@@ -1,0 +1,184 @@
+"""GPU parity (0 ULP) of the token log probabilities, entropies, alternatives and
+their gradient against the oracle, and against 64 bits within derived bounds."""
+import numpy as np
+import pytest
+
+import oracle
+from bitcmp import assert_bitwise
+from bitwise_reproducible_fp32_gb300 import detlib
+from gen_util import F, U, logprob64
+from gpu_util import host, need_gpu, to_dev, torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    return need_gpu()
+
+
+def on_gpu(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def check(x, y, k, layout="dense", bwd=True, seed=0):
+    with np.errstate(all="ignore"):
+        want = oracle.logprob(x, y, k)
+    xd, yd = to_dev(x, layout), on_gpu(y.astype(np.int32))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    logp, ent, ids, top, stats = detlib.detlogprob_f32(xd, yd, top_k=k, dev_status=status)
+    for got, w, name in ((logp, want[0], "logp"), (ent, want[1], "entropy"),
+                         (stats, want[2], "stats"), (top, want[4], "top_logp")):
+        assert_bitwise(host(got), w, f"{name} V={x.shape[1]} {layout}")
+    assert np.array_equal(host(ids), want[3])
+    assert int(status) == int(((y < -1) | (y >= x.shape[1])).any())
+    if not bwd:
+        return want
+    rng = np.random.default_rng(seed)
+    g, gH = (rng.standard_normal(len(x)).astype(F) for _ in range(2))
+    for h in (None, gH):
+        w = oracle.logprob_bwd(x, y, want[2], g, h)
+        hd = None if h is None else on_gpu(h)
+        assert_bitwise(host(detlib.detlogprob_bwd_f32(xd, yd, stats, on_gpu(g), hd)), w, "grad")
+        out = to_dev(np.full(x.shape, 3.0, F), "offset")
+        detlib.detlogprob_bwd_f32(xd, yd, stats, on_gpu(g), hd, dlogits=out)
+        assert_bitwise(host(out), w, "grad, other alignment")
+    detlib.detlogprob_bwd_f32(xd, yd, stats, on_gpu(g), hd, dlogits=xd)
+    assert_bitwise(host(xd), w, "grad in place")
+    return want
+
+
+@pytest.mark.parametrize("V", [1, 2, 3, 5, 64, 255, 256, 1000, 1023, 1024, 1025, 4096, 4099, 10001,
+                               32000, 50257, 57590, 57601, 70001, 151936])
+@pytest.mark.parametrize("layout", ["dense", "padded", "offset"])
+def test_sizes(dev, V, layout):
+    rng = np.random.default_rng(V)
+    rows = 7 if V > 5000 else 400
+    x = (2 * rng.standard_normal((rows, V))).astype(F)
+    y = rng.integers(0, V, rows)
+    y[:3] = [-1, V, -2]
+    want = check(x, y, min(V, 20), layout)
+    logp, ent, b1, b2 = logprob64(x[3:], y[3:])
+    assert (np.abs(want[0][3:] - logp) <= b1).all() and (np.abs(want[1][3:] - ent) <= b2).all()
+
+
+@pytest.mark.parametrize("k", [0, 1, 2, 31, 32])
+@pytest.mark.parametrize("V", [32, 777, 50257, 80000])
+def test_alternatives_with_ties(dev, k, V):
+    # values of few distinct levels, constant rows, ascending and descending
+    # rows, the largest values side by side and far apart
+    rng = np.random.default_rng(k + V)
+    x = rng.integers(-3, 4, (12, V)).astype(F)
+    x[1] = 0.5
+    x[2] = np.arange(V) / V
+    x[3] = -np.arange(V) / V
+    x[4] = (2 * rng.standard_normal(V)).astype(F)
+    x[4, V // 2:V // 2 + 16] = 30.0
+    x[5] = np.where(np.arange(V) % 2, F(0.0), F(-0.0))
+    x[6] = rng.standard_normal(V)
+    x[6, [0, V - 1, V // 3]] = 9.0
+    x[7] = np.where(rng.random(V) < 0.001, 4.0, -4.0)
+    x[8, :] = -np.inf
+    x[8, V // 4] = 1.0
+    x[9] = np.repeat(rng.standard_normal(V // 8 + 1), 8)[:V]
+    check(x, np.full(12, V // 4), k, bwd=False)
+
+
+def test_infinities_and_nan(dev):
+    rng = np.random.default_rng(4)
+    for V in (40, 1000, 5003, 50257, 60011):
+        x = (2 * rng.standard_normal((9, V))).astype(F)
+        x[0, 3] = np.nan
+        x[1, [5, V - 1]] = np.nan
+        x[2, 7] = np.inf
+        x[3, :] = -np.inf
+        x[4, ::2] = -np.inf
+        x[5, :] = np.finfo(F).min
+        x[6, :] = np.finfo(F).min
+        x[6, V // 2] = 0.0
+        x[7, 1:] = -200.0
+        x[7, 0] = 0.0
+        x[8, 2] = np.finfo(F).max
+        check(x, np.array([3, 0, 7, 0, 1, 2, V // 2, 1, 2]), min(V, 32), "padded")
+
+
+def test_logp_is_the_cross_entropy(dev):
+    rng = np.random.default_rng(6)
+    x = (2 * rng.standard_normal((64, 50257))).astype(F)
+    y = on_gpu(rng.integers(0, 50257, 64).astype(np.int32))
+    xd = to_dev(x)
+    loss, _, dl = detlib.detxent_f32(xd, y, want_dlogits=True, dscale=1.0)
+    logp = detlib.detlogprob_f32(xd, y)[0]
+    assert_bitwise(host(logp), -host(loss))
+    # and its gradient with dlogp = -1: -(hot - p), the cross-entropy's p - hot
+    st = detlib.detlogprob_f32(xd, y)[4]
+    got = detlib.detlogprob_bwd_f32(xd, y, st, torch.full((64,), -1.0, device="cuda"))
+    assert_bitwise(host(got), host(dl))
+
+
+def test_gradient_formula_and_differences(dev):
+    rng = np.random.default_rng(9)
+    V, rows = 37, 5
+    x = rng.standard_normal((rows, V)).astype(F)
+    y = np.array([0, 36, 5, -1, 9])
+    g, gH = (rng.standard_normal(rows).astype(F) for _ in range(2))
+    st = detlib.detlogprob_f32(to_dev(x), on_gpu(y.astype(np.int32)))[4]
+    got = host(detlib.detlogprob_bwd_f32(to_dev(x), on_gpu(y.astype(np.int32)), st, on_gpu(g),
+                                         on_gpu(gH)))
+
+    def f(z):
+        d = z - z.max(1, keepdims=True)
+        lp = d - np.log(np.exp(d).sum(1, keepdims=True))
+        at = np.where(y < 0, 0.0, lp[np.arange(rows), np.maximum(y, 0)])
+        return g * at - gH * (np.exp(lp) * lp).sum(1)
+
+    x64 = x.astype(np.float64)
+    d = x64 - x64.max(1, keepdims=True)
+    lp = d - np.log(np.exp(d).sum(1, keepdims=True))
+    p, ent = np.exp(lp), -(np.exp(lp) * lp).sum(1, keepdims=True)
+    hot = (np.arange(V)[None] == y[:, None]).astype(float)
+    want = np.where(y[:, None] < 0, 0.0, g[:, None] * (hot - p)) - gH[:, None] * p * (lp + ent)
+    # p is off by at most |d| + 2 (exp) + 24 (S) + 3 roundings, w by 40 more
+    size = np.abs(g[:, None]) * (hot + p) + np.abs(gH[:, None]) * p * (np.abs(lp) + ent + 1)
+    assert (np.abs(got - want) <= size * (np.abs(d) + 70) * U).all()
+    h = 1e-5        # central differences: h^2 / 6 of third derivatives below 8, 1e-16 / h
+    for j in range(V):
+        step = np.zeros_like(x64)
+        step[:, j] = h
+        quot = (f(x64 + step) - f(x64 - step)) / (2 * h)
+        assert (np.abs(want[:, j] - quot) <= 1e-9 * 8).all()
+
+
+def test_rows_cycle_through_the_grid_on_a_stream_and_captured(dev):
+    rng = np.random.default_rng(10)
+    V = 2001
+    x = (2 * rng.standard_normal((1500, V))).astype(F)
+    y = rng.integers(0, V, 1500).astype(np.int32)
+    want = oracle.logprob(x, y, 4)
+    xd, yd = to_dev(x), on_gpu(y)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = detlib.detlogprob_f32(xd, yd, top_k=4, stream=s)
+    s.synchronize()
+    assert_bitwise(host(got[0]), want[0])
+    assert np.array_equal(host(got[2]), want[3])
+    outs = [torch.empty_like(t) for t in got]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        detlib.detlogprob_f32(xd, yd, top_k=4, logp=outs[0], entropy=outs[1], top_ids=outs[2],
+                              top_logp=outs[3], stats=outs[4])
+    xd.copy_(to_dev(x[::-1].copy()))
+    yd.copy_(on_gpu(y[::-1].copy()))
+    g.replay()
+    assert_bitwise(host(outs[0]), want[0][::-1])
+    assert_bitwise(host(outs[1]), want[1][::-1])
+    assert np.array_equal(host(outs[2]), want[3][::-1])
+    assert detlib.det_watchdog_status() == 0
+
+
+def test_no_rows(dev):
+    e = torch.empty((0, 10), device="cuda")
+    t = torch.empty(0, dtype=torch.int32, device="cuda")
+    out = detlib.detlogprob_f32(e, t, top_k=3)
+    assert [tuple(o.shape) for o in out] == [(0,), (0,), (0, 3), (0, 3), (0, 4)]
+    assert detlib.detlogprob_bwd_f32(e, t, out[4], out[0]).shape == (0, 10)
