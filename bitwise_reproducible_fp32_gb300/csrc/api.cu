@@ -1030,6 +1030,7 @@ DET_API det_status detlog_f32(const det_profile_v1 *prof, int64_t n, const float
 
 // ---------------------------------------------------------------- generation
 namespace {
+constexpr int64_t kLenMax = int64_t(1) << 30;     // tokens of a request
 constexpr int64_t kTopMax = 32;
 constexpr int64_t kVocabMax = int64_t(1) << 30;   // sweeps past a row's end stay in int
 
@@ -1156,7 +1157,7 @@ DET_API det_status detdecode_attention_workspace_bytes(const det_profile_v1 *pro
     det_status st = check_profile(prof);
     if (st != DET_OK) return st;
     if (!bytes || !decode_sizes_ok(batch, heads, kv_heads, head_dim) || max_len < 1 ||
-        max_len > kDimMax)
+        max_len > kLenMax)
         return DET_ERR_INVALID_ARG;
     *bytes = decode_workspace_bytes(batch, heads, kv_heads, head_dim, max_len);
     return DET_OK;
@@ -1172,7 +1173,7 @@ DET_API det_status detdecode_attention_f32(const det_profile_v1 *prof, int64_t b
     det_status st = check_profile(prof);
     if (st != DET_OK) return st;
     if (!cache_ok(cache) || !decode_sizes_ok(batch, heads, cache->kv_heads, cache->head_dim) ||
-        max_pages < 1 || max_pages > kDimMax || max_pages * cache->page_size > kDimMax ||
+        max_pages < 1 || max_pages > kLenMax || max_pages * cache->page_size > kLenMax ||
         ldt < max_pages || ldq < heads * cache->head_dim || ldo < heads * cache->head_dim)
         return DET_ERR_INVALID_ARG;
     if (batch == 0) return DET_OK;
@@ -1240,6 +1241,8 @@ DET_API det_status det_watchdog_status(int32_t *code, int clear) {
     if (e == cudaSuccess) e = rmsbwd_watchdog(&c3, clear);
     unsigned int c5 = 0;
     if (e == cudaSuccess) e = block_watchdog(&c5, clear);
-    *code = int32_t(c | c2 | c3 | c5);
+    unsigned int c6 = 0;
+    if (e == cudaSuccess) e = decode_watchdog(&c6, clear);
+    *code = int32_t(c | c2 | c3 | c5 | c6);
     return from_cuda(e);
 }

@@ -14,12 +14,14 @@
 // which keeps the scores in its shared memory between the two, so no second
 // launch, no atomics and, but for very long rows, no workspace are needed.
 //  - The row is cut at the profile's 256-token chunks; a CTA takes a run of them.
-//  - Every warp streams its own pieces of 32 tokens x 32 dimensions through a
-//    ring of kStages slots by 16-byte cp.async (4-byte where the strides want it),
-//    K pieces first, then V pieces: the ring already fills with V while the
-//    CTAs meet for m and S.
-//  - Scores: a lane a token, the chain over d from shared memory (rows padded to
-//    36 floats: 16-byte reads without bank conflicts), q broadcast.
+//  - Every warp streams its own pieces of 64 tokens x 32 dimensions through a
+//    ring of kStages slots, K pieces first, then V pieces: the ring already fills
+//    with V while the CTAs meet for m and S. A piece is one or a few TMA boxes (a
+//    box a page) where the page size is 8, 16, 32 or a multiple of 64 and every
+//    stride a multiple of 16 bytes; else 16- or 4-byte cp.async. Either way its
+//    rows are 128 bytes, the 16-byte units of row r swapped by r mod 8, so that
+//    reads along rows and along columns meet no bank conflict.
+//  - Scores: a lane two tokens, the chains over d from shared memory, q broadcast.
 //  - m and the 256 chains of S cross the cluster through distributed shared
 //    memory; a chain adds its groups in ascending order wherever they lie.
 //  - P V: a warp a (chunk, 32 dimensions), a lane a dimension, the chain over the
@@ -29,7 +31,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
-#include <cstdlib>
+#include <type_traits>
 
 #include "det_internal.cuh"
 #include "det_math.cuh"
@@ -37,23 +39,41 @@
 namespace cg = cooperative_groups;
 
 namespace det {
+
+// Set when a bounded wait for a piece gave up.
+__device__ unsigned int g_decode_watchdog;
+
 namespace {
 
-#ifndef DEC_W
-#define DEC_W 4
-#define DEC_ST 4
-#define DEC_CTAS 2
-#endif
-constexpr int kWarps = DEC_W;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = DEC_ST;
-constexpr int kRow = 36;                    // floats a piece's row takes
-constexpr int kPiece = 32 * kRow;
+constexpr int kTokens = 64;                 // of a piece, 32 dimensions each
+constexpr int kPieceBytes = kTokens * 128;
 constexpr int kMaxHeads = 8;
 constexpr int kMaxCluster = 16;
-constexpr int kPageCache = 1024;            // page ids of a CTA kept on chip
-constexpr int kCtasPerSm = DEC_CTAS;
+constexpr int kPageCache = 512;             // page ids of a CTA kept on chip
+enum Loader { kTma, kCopy16, kCopy4 };
+constexpr unsigned kWatchdogDecode = 32u;   // det_watchdog_status bit 5
+constexpr int kCtasPerSm = 2;
 constexpr int kSmemPerCta = (227 / kCtasPerSm - 1) * 1024;
+
+__device__ __forceinline__ float4 lds4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float lds1(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void sts1(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 
 struct DecodeArgs {
     int heads, kv_heads, head_dim;
@@ -73,7 +93,10 @@ struct DecodeArgs {
     float *workspace;
     int64_t max_len, ws_cta;  // ws_cta: floats of the workspace a CTA has
     int room;                 // floats of shared memory for scores and partials
+    int box;                  // tokens of a TMA box
     int unit_heads, batches;  // query heads a unit takes; units a key-value head
+    int stages;               // slots of a warp's ring
+    int64_t max_pages;
     int32_t *dev_status;
 };
 
@@ -103,33 +126,63 @@ __device__ __forceinline__ float butterfly32(float s) {
     return s;
 }
 
-struct Fixed {                          // the fixed part of a CTA's shared memory
-    float ring[kWarps][kStages][kPiece];
-    float q[kMaxHeads][256];
-    float chain[kMaxHeads][256];
-    float red[kMaxHeads][8];
-    float top[kMaxCluster][kMaxHeads];  // each CTA's maxima
+template <int NH>
+struct Fixed {                          // a CTA's shared memory after the rings
+    uint64_t full[kWarps][4];
+    float q[NH][256];
+    float chain[NH][256];
+    float red[NH][8];
+    float top[kMaxCluster][NH];         // each CTA's maxima
     int lost[kMaxCluster];
     int pages[kPageCache];
 };
-
-static_assert(sizeof(Fixed) % 16 == 0 && int(sizeof(Fixed)) + 4096 <= kSmemPerCta,
-              "room for scores beside the fixed part");
+// Beside it there is room for the scores and partials of short rows, or, for
+// longer ones, at least for the warps' copies of a piece's probabilities.
+constexpr int kRingBytes = kWarps * kPieceBytes;      // a stage of all warps
+// Stages where rows are long: units of many heads need the room for scores.
+constexpr int stages_of(int nh) { return nh <= 2 ? 3 : 2; }
+template <int NH>
+constexpr bool kFits = sizeof(Fixed<NH>) % 16 == 0 &&
+                       stages_of(NH) * kRingBytes + int(sizeof(Fixed<NH>)) +
+                               kWarps * NH * kTokens * 4 <= kSmemPerCta;
+static_assert(kFits<1> && kFits<2> && kFits<4> && kFits<kMaxHeads>, "shared memory");
 
 // NH: the heads of a unit the registers hold (nh <= NH of them live).
-template <int NH, bool VEC>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const DecodeArgs A) {
-    extern __shared__ float4 smem4[];
-    Fixed &F = *reinterpret_cast<Fixed *>(smem4);
-    float *room = reinterpret_cast<float *>(smem4) + sizeof(Fixed) / 4;
+template <int NH, Loader LOAD>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    decode_kernel(const DecodeArgs A, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const int stages = A.stages;                    // 2 or 3
+    Fixed<NH> &F = *reinterpret_cast<Fixed<NH> *>(smem_raw + stages * kRingBytes);
+    float *room = reinterpret_cast<float *>(&F + 1);
     cg::cluster_group cluster = cg::this_cluster();
     const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int unit = blockIdx.x / C, b = blockIdx.y;
+    const int unit = blockIdx.x / C;
+    const int b = blockIdx.y;
     const int g = unit / A.batches, d = A.head_dim;
     const int per_kv = A.heads / A.kv_heads, h_in = (unit - g * A.batches) * A.unit_heads;
     const int nh = min(A.unit_heads, per_kv - h_in), h0 = g * per_kv + h_in;
     float *o = A.out + b * A.ldo + int64_t(h0) * d;
+    const int32_t *pages = A.table + b * A.ldt;
+    if (LOAD == kTma && tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+        for (int i = 0; i < kWarps * 4; ++i) mbar_init(smem_u32(&F.full[0][i]), 1);
+        fence_mbar_init();
+    }
+    // the length, the query and, for a unit of one CTA, the first page ids are
+    // asked for together
+    int early[kPageCache / kThreads];
+    if (C == 1)
+#pragma unroll
+        for (int i = 0; i < kPageCache / kThreads; ++i)
+            early[i] = tid + i * kThreads < A.max_pages ? pages[tid + i * kThreads] : 0;
+    for (int i = tid; i < nh * d; i += kThreads) {
+        const int h = i / d;
+        F.q[h][i - h * d] = A.q[b * A.ldq + int64_t(h0) * d + i];
+    }
     const int n = A.kv_lens[b];
     if (n <= 0 || n > A.max_len) {      // the whole cluster
         const float fill = n == 0 ? 0.0f : __uint_as_float(0x7fc00000u);
@@ -138,15 +191,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
             atomicOr(reinterpret_cast<int *>(A.dev_status), 1);
         return;
     }
-    cluster.barrier_arrive();           // waited for before the first remote access
+    if (C > 1) cluster.barrier_arrive();    // waited for before the first remote access
+    auto meet = [&]() {                 // all threads of the unit
+        if (C > 1) cluster.sync(); else __syncthreads();
+    };
     // this CTA's run of chunks and tokens
     const int nch = (n + kKChunk - 1) / kKChunk, base = nch / C, rem = nch % C;
     auto first_chunk = [&](int r) { return r * base + min(r, rem); };
     const int c0 = first_chunk(rank), my = base + (rank < rem), most = base + (rem > 0);
     const int t0 = c0 * kKChunk, t1 = min(n, t0 + my * kKChunk);
     // scores [head][token], then partials [head][chunk][d], here or in L2
-    const int xs_ld = most * kKChunk, part_at = nh * xs_ld;
-    const bool on_chip = nh * most * (kKChunk + d) <= A.room;
+    const int64_t xs_ld = int64_t(most) * kKChunk, part_at = nh * xs_ld;
+    const bool on_chip = int64_t(nh) * most * (kKChunk + d) <= A.room;
     float *const ws = on_chip ? nullptr
                               : A.workspace + (int64_t(b) * (gridDim.x / C) + unit) * C * A.ws_cta;
     auto scores_of = [&](int r) {
@@ -154,7 +210,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
     };
     float *xs = on_chip ? room : ws + rank * A.ws_cta;
 
-    const int32_t *pages = A.table + b * A.ldt;
     const float *kb = A.k + g * A.head_stride, *vb = A.v + g * A.head_stride;
     auto page_of = [&](int t) {
         return A.page_shift >= 0 ? unsigned(t) >> A.page_shift : unsigned(t) / A.page_size;
@@ -162,141 +217,192 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
     const unsigned pg0 = page_of(t0), pgs = t1 > t0 ? page_of(t1 - 1) - pg0 + 1 : 0;
     const bool cached = pgs <= unsigned(kPageCache);
     int lost = 0;
-    for (unsigned i = tid; i < pgs; i += kThreads) {
-        int id = pages[pg0 + i];
+    auto check = [&](unsigned i, int id) {
         if (id < 0 || id >= A.num_pages) {
             lost = 1;
             id = 0;
         }
         if (cached) F.pages[i] = id;
+    };
+    if (C == 1 && cached) {
+#pragma unroll
+        for (int i = 0; i < kPageCache / kThreads; ++i)
+            if (unsigned(tid + i * kThreads) < pgs) check(tid + i * kThreads, early[i]);
+    } else {
+        for (unsigned i = tid; i < pgs; i += kThreads) check(i, pages[pg0 + i]);
     }
-    for (int i = tid; i < nh * d; i += kThreads) {
-        const int h = i / d;
-        F.q[h][i - h * d] = A.q[b * A.ldq + int64_t(h0) * d + i];
-    }
-    lost = __syncthreads_or(lost);
-    // a token's offset in the cache (a page out of range reads page 0 instead)
+    lost = __syncthreads_or(lost) ? 1 : 0;
+    // a token's page (one out of range reads page 0 instead)
+    auto id_of = [&](unsigned p) {
+        if (cached) return F.pages[p - pg0];
+        const int id = pages[p];
+        return id < 0 || id >= A.num_pages ? 0 : id;
+    };
     auto offset_of = [&](int t) {
         const unsigned p = page_of(t);
-        int id;
-        if (cached) {
-            id = F.pages[p - pg0];
-        } else {
-            id = pages[p];
-            if (id < 0 || id >= A.num_pages) id = 0;
-        }
-        return id * A.page_stride + int64_t(unsigned(t) - p * A.page_size) * A.token_stride;
+        return id_of(p) * A.page_stride + int64_t(unsigned(t) - p * A.page_size) * A.token_stride;
     };
 
-    // ---- the warp's pieces: K tiles warp, warp + kWarps, ... of 32 tokens, all
+    // ---- the warp's pieces: K tiles warp, warp + kWarps, ... of 64 tokens, all
     // their slices of 32 dimensions; then V jobs warp, warp + kWarps, ... (chunk,
-    // slice), 32 tokens at a time
-    const int nsl = (d + 31) / 32, tiles = (t1 - t0 + 31) / 32, jobs = my * nsl;
-    const uint32_t ring = smem_u32(&F.ring[warp][0][0]);
-    int kt = warp, ksl = 0, vj = warp, vt = 0, slot_in = 0;
-    int64_t off = 0;
-    auto issue = [&](const float *src, int t, int sl, int end) {
-        const uint32_t dst = ring + slot_in * (kPiece * 4);
-        const int live = min(32, end - t), width = min(32, d - 32 * sl);
-        src += 32 * sl;
-        if constexpr (VEC) {
+    // slice), 64 tokens at a time
+    const int nsl = (d + 31) / 32, tiles = (t1 - t0 + kTokens - 1) / kTokens, jobs = my * nsl;
+    const uint32_t ring = smem_u32(smem_raw) + warp * stages * kPieceBytes, bars = smem_u32(&F.full[warp][0]);
+    int kt = warp, ksl = 0, vj = warp, vt = 0, vsl = 0, vend = 0, slot_in = 0;
+    int64_t off[2] = {0, 0};
+    auto offsets = [&](int t, int end) {      // of the piece's tokens lane, lane + 32
+        if (LOAD == kTma) return;
+        if (t + lane < end) off[0] = offset_of(t + lane);
+        if (t + lane + 32 < end) off[1] = offset_of(t + lane + 32);
+    };
+    auto issue = [&](const float *src, const CUtensorMap *map, int t, int sl, int end) {
+        const uint32_t dst = ring + slot_in * kPieceBytes;
+        const int live = min(kTokens, end - t);
+        if constexpr (LOAD == kTma) {
+            const int boxes = (live + A.box - 1) / A.box;
+            if (lane == 0) mbar_arrive_expect_tx(bars + 8 * slot_in, boxes * A.box * 128);
+            __syncwarp();
+            if (lane < boxes) {
+                const int at = t + lane * A.box;
+                const unsigned p = page_of(at);
+                tma_load_4d(dst + lane * A.box * 128, map, 32 * sl, g,
+                            int(unsigned(at) - p * A.page_size), id_of(p), bars + 8 * slot_in);
+            }
+        } else if constexpr (LOAD == kCopy16) {
             const int col = lane & 7, r0 = lane >> 3;
-            const bool in = 4 * col < width;
+            const bool in = 4 * col < d - 32 * sl;
+            src += 32 * sl + 4 * col;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kTokens / 4; ++i) {
                 const int r = 4 * i + r0;
-                const int64_t at = __shfl_sync(0xffffffffu, off, r);
-                if (in && r < live) cp_async<16>(dst + (r * kRow + 4 * col) * 4, src + at + 4 * col);
+                const int64_t at = __shfl_sync(0xffffffffu, off[i >> 3], r & 31);
+                if (in && r < live) cp_async<16>(dst + r * 128 + ((col ^ (r & 7)) << 4), src + at);
             }
         } else {
+            const bool in = lane < d - 32 * sl;
+            src += 32 * sl + lane;
 #pragma unroll 8
-            for (int r = 0; r < 32; ++r) {
-                const int64_t at = __shfl_sync(0xffffffffu, off, r);
-                if (lane < width && r < live)
-                    cp_async<4>(dst + (r * kRow + lane) * 4, src + at + lane);
+            for (int r = 0; r < kTokens; ++r) {
+                const int64_t at = __shfl_sync(0xffffffffu, r < 32 ? off[0] : off[1], r & 31);
+                if (in && r < live)
+                    cp_async<4>(dst + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | (lane & 3) << 2),
+                                src + at);
             }
         }
     };
     auto issue_next = [&]() {
         if (kt < tiles) {
-            const int t = t0 + 32 * kt;
-            if (ksl == 0 && t + lane < t1) off = offset_of(t + lane);
-            issue(kb, t, ksl, t1);
+            const int t = t0 + kTokens * kt;
+            if (ksl == 0) offsets(t, t1);
+            issue(kb, &kmap, t, ksl, t1);
             if (++ksl == nsl) {
                 ksl = 0;
                 kt += kWarps;
             }
         } else if (vj < jobs) {
-            const int c = vj / nsl, sl = vj - c * nsl;
-            const int t = t0 + c * kKChunk + vt, end = min(t1, t0 + (c + 1) * kKChunk);
-            if (t + lane < end) off = offset_of(t + lane);
-            issue(vb, t, sl, end);
-            vt += 32;
-            if (t + 32 >= end) {
-                vt = 0;
-                vj += kWarps;
+            if (vt >= vend) {               // the next job: its slice and tokens
+                const int c = vj / nsl;
+                vsl = vj - c * nsl;
+                vt = t0 + c * kKChunk;
+                vend = min(t1, vt + kKChunk);
             }
+            offsets(vt, vend);
+            issue(vb, &vmap, vt, vsl, vend);
+            vt += kTokens;
+            if (vt >= vend) vj += kWarps;
         }
-        cp_commit();
-        slot_in = slot_in + 1 == kStages ? 0 : slot_in + 1;
+        if (LOAD != kTma) cp_commit();
+        slot_in = slot_in + 1 == stages ? 0 : slot_in + 1;
     };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue_next();
+    for (int i = 0; i < stages - 1; ++i) issue_next();
     int slot = 0;
+    uint32_t phase = 0;
+    bool stuck = false;           // a wait gave up: the rest wait no more
     auto next_piece = [&]() {
-        cp_wait<kStages - 2>();
+        if constexpr (LOAD == kTma) {
+            if (!stuck) stuck = __any_sync(0xffffffffu, !mbar_wait_bounded(bars + 8 * slot, phase));
+        } else {
+            if (stages == 3) cp_wait<1>(); else cp_wait<0>();
+        }
         __syncwarp();
-        issue_next();               // into the slot consumed before this one
-        const float *p = &F.ring[warp][slot][0];
-        slot = slot + 1 == kStages ? 0 : slot + 1;
+        if (!stuck) issue_next();   // into the slot consumed before this one
+        const uint32_t p = ring + slot * kPieceBytes;
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
+        }
         return p;
     };
+    // shared-memory offsets in a piece: 16-byte unit c of row `lane`, and column
+    // `lane` of rows r = 0..7 mod 8
+    uint32_t kat[8], vat[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        kat[i] = lane * 128 + ((i ^ (lane & 7)) << 4);
+        vat[i] = i * 128 + (((lane >> 2) ^ i) << 4) + ((lane & 3) << 2);
+    }
 
     // ---- scores
     float m[NH];
 #pragma unroll
     for (int h = 0; h < NH; ++h) m[h] = __uint_as_float(0xff800000u);
     for (int tl = warp; tl < tiles; tl += kWarps) {
-        float acc[NH];
+        float acc[2][NH];               // of tokens lane and lane + 32
 #pragma unroll
-        for (int h = 0; h < NH; ++h) acc[h] = 0.0f;
+        for (int h = 0; h < NH; ++h) acc[0][h] = acc[1][h] = 0.0f;
         for (int sl = 0; sl < nsl; ++sl) {
-            const float *row = next_piece() + lane * kRow;
+            const uint32_t piece = next_piece();
             const int width = min(32, d - 32 * sl);
             const float *q = &F.q[0][32 * sl];
-            auto four = [&](int c) {
-                const float4 kv = *reinterpret_cast<const float4 *>(row + c);
+            auto four = [&](int i) {
+                const float4 k0 = lds4(piece + kat[i]), k1 = lds4(piece + 4096 + kat[i]);
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
-                    const float4 qv = *reinterpret_cast<const float4 *>(q + h * 256 + c);
-                    acc[h] = __fmaf_rn(qv.x, kv.x, acc[h]);
-                    acc[h] = __fmaf_rn(qv.y, kv.y, acc[h]);
-                    acc[h] = __fmaf_rn(qv.z, kv.z, acc[h]);
-                    acc[h] = __fmaf_rn(qv.w, kv.w, acc[h]);
+                    const float4 qv = *reinterpret_cast<const float4 *>(q + h * 256 + 4 * i);
+                    acc[0][h] = __fmaf_rn(qv.x, k0.x, acc[0][h]);
+                    acc[1][h] = __fmaf_rn(qv.x, k1.x, acc[1][h]);
+                    acc[0][h] = __fmaf_rn(qv.y, k0.y, acc[0][h]);
+                    acc[1][h] = __fmaf_rn(qv.y, k1.y, acc[1][h]);
+                    acc[0][h] = __fmaf_rn(qv.z, k0.z, acc[0][h]);
+                    acc[1][h] = __fmaf_rn(qv.z, k1.z, acc[1][h]);
+                    acc[0][h] = __fmaf_rn(qv.w, k0.w, acc[0][h]);
+                    acc[1][h] = __fmaf_rn(qv.w, k1.w, acc[1][h]);
                 }
             };
             if (width == 32) {
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) four(c);
+                for (int i = 0; i < 8; ++i) four(i);
             } else {
-                int c = 0;
-                for (; c + 4 <= width; c += 4) four(c);
-                for (; c < width; ++c) {
-                    const float kv = row[c];
 #pragma unroll
-                    for (int h = 0; h < NH; ++h) acc[h] = __fmaf_rn(q[h * 256 + c], kv, acc[h]);
+                for (int i = 0; i < 8; ++i) {
+                    if (4 * i + 4 <= width) {
+                        four(i);
+                    } else if (4 * i < width) {
+                        for (int c = 4 * i; c < width; ++c) {
+                            const float k0 = lds1(piece + kat[i] + 4 * (c & 3));
+                            const float k1 = lds1(piece + 4096 + kat[i] + 4 * (c & 3));
+#pragma unroll
+                            for (int h = 0; h < NH; ++h) {
+                                acc[0][h] = __fmaf_rn(q[h * 256 + c], k0, acc[0][h]);
+                                acc[1][h] = __fmaf_rn(q[h * 256 + c], k1, acc[1][h]);
+                            }
+                        }
+                    }
                 }
             }
         }
-        const int t = t0 + 32 * tl + lane;
-        if (t < t1) {
 #pragma unroll
-            for (int h = 0; h < NH; ++h)
-                if (h < nh) {
-                    const float x = __fmul_rn(acc[h], A.scale);
-                    xs[h * xs_ld + (t - t0)] = x;
-                    m[h] = max_nan(m[h], x);
-                }
+        for (int k = 0; k < 2; ++k) {
+            const int t = t0 + kTokens * tl + 32 * k + lane;
+            if (t < t1) {
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+                    if (h < nh) {
+                        const float x = __fmul_rn(acc[k][h], A.scale);
+                        xs[h * xs_ld + (t - t0)] = x;
+                        m[h] = max_nan(m[h], x);
+                    }
+            }
         }
     }
     // ---- m over the cluster
@@ -308,15 +414,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
         if (lane == 0) F.red[h][warp] = m[h];
     }
     __syncthreads();
-    cluster.barrier_wait();
+    if (C > 1) cluster.barrier_wait();
     if (tid < NH) {
         float t = F.red[tid][0];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) t = max_nan(t, F.red[tid][w]);
-        for (int r = 0; r < C; ++r) cluster.map_shared_rank(&F.top[rank][tid], r)[0] = t;
+        for (int r = 0; r < C; ++r) *cluster.map_shared_rank(&F.top[rank][tid], r) = t;
     }
-    if (tid < C) cluster.map_shared_rank(&F.lost[rank], tid)[0] = lost;
-    cluster.sync();
+    if (tid < C) *cluster.map_shared_rank(&F.lost[rank], tid) = lost;
+    meet();
     for (int r = 0; r < C; ++r) lost |= F.lost[r];
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
@@ -340,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
             }
         }
     }
-    cluster.sync();
+    meet();
     // ---- chains of S: (head, chain) over the cluster's threads; the total goes
     // to every CTA
     for (int i = rank * kThreads + tid; i < nh * 256; i += C * kThreads) {
@@ -362,9 +468,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
             if (t + 2 < n) s = __fadd_rn(s, e.z);
             if (t + 3 < n) s = __fadd_rn(s, e.w);
         }
-        for (r = 0; r < C; ++r) cluster.map_shared_rank(&F.chain[h][l], r)[0] = s;
+        for (r = 0; r < C; ++r) *cluster.map_shared_rank(&F.chain[h][l], r) = s;
     }
-    cluster.sync();
+    meet();
     for (int i = warp; i < nh * 8; i += kWarps) {
         const float s = butterfly32(F.chain[i >> 3][(i & 7) * 32 + lane]);
         if (lane == 0) F.red[i >> 3][i & 7] = s;
@@ -387,76 +493,150 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
     }
     __syncthreads();
     // ---- P V: chunk partials (registers past the unit's heads repeat its last)
-    int head_at[NH];
+    uint32_t pat[NH];             // shared-memory addresses of the heads' rows
+    const uint32_t copies = smem_u32(room) + warp * (NH * kTokens * 4);
 #pragma unroll
-    for (int h = 0; h < NH; ++h) head_at[h] = min(h, nh - 1) * xs_ld;
+    for (int h = 0; h < NH; ++h)
+        pat[h] = on_chip ? smem_u32(room) + min(h, nh - 1) * int(xs_ld) * 4
+                         : copies + h * (kTokens * 4);
     for (int j = warp; j < jobs; j += kWarps) {
         const int c = j / nsl, sl = j - c * nsl;
         const int end = min(t1 - t0, (c + 1) * kKChunk);
         float acc[NH];
 #pragma unroll
         for (int h = 0; h < NH; ++h) acc[h] = 0.0f;
-        for (int t = c * kKChunk; t < end; t += 32) {
-            const float *p = next_piece() + lane;
-            const float *pr = xs + t;
+        for (int t = c * kKChunk; t < end; t += kTokens) {
+            float keep[2 * NH];
+            if (!on_chip)             // the piece's probabilities, from L2
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        keep[2 * h + k] = t + 32 * k + lane < end
+                                              ? xs[min(h, nh - 1) * xs_ld + t + 32 * k + lane]
+                                              : 0.0f;
+            const uint32_t piece = next_piece();
+            if (!on_chip) {
+#pragma unroll
+                for (int i = 0; i < 2 * NH; ++i)
+                    sts1(copies + (i * 32 + lane) * 4, keep[i]);
+                __syncwarp();
+            }
+            const uint32_t po = on_chip ? t * 4 : 0;
             auto four = [&](int r) {
-                const float v0 = p[r * kRow], v1 = p[(r + 1) * kRow], v2 = p[(r + 2) * kRow],
-                            v3 = p[(r + 3) * kRow];
+                const uint32_t up = piece + (r & ~7) * 128;
+                const float v0 = lds1(up + vat[r & 7]), v1 = lds1(up + vat[(r & 7) + 1]),
+                            v2 = lds1(up + vat[(r & 7) + 2]), v3 = lds1(up + vat[(r & 7) + 3]);
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
-                    const float4 w = *reinterpret_cast<const float4 *>(pr + head_at[h] + r);
+                    const float4 w = lds4(pat[h] + po + r * 4);
                     acc[h] = __fmaf_rn(w.x, v0, acc[h]);
                     acc[h] = __fmaf_rn(w.y, v1, acc[h]);
                     acc[h] = __fmaf_rn(w.z, v2, acc[h]);
                     acc[h] = __fmaf_rn(w.w, v3, acc[h]);
                 }
             };
-            if (end - t >= 32) {
+            const int live = end - t;
+            if (live >= kTokens) {
 #pragma unroll
-                for (int r = 0; r < 32; r += 4) four(r);
+                for (int r = 0; r < kTokens; r += 4) four(r);
             } else {
-                int r = 0;
-                for (; r + 4 <= end - t; r += 4) four(r);
-                for (; r < end - t; ++r) {
-                    const float v = p[r * kRow];
+#pragma unroll 2
+                for (int r8 = 0; r8 < kTokens; r8 += 8) {
 #pragma unroll
-                    for (int h = 0; h < NH; ++h)
-                        acc[h] = __fmaf_rn(pr[head_at[h] + r], v, acc[h]);
+                    for (int r = 0; r < 8; r += 4) {
+                        if (r8 + r + 4 <= live) {
+                            const uint32_t up = piece + r8 * 128;
+                            const float v0 = lds1(up + vat[r]), v1 = lds1(up + vat[r + 1]),
+                                        v2 = lds1(up + vat[r + 2]), v3 = lds1(up + vat[r + 3]);
+#pragma unroll
+                            for (int h = 0; h < NH; ++h) {
+                                const float4 w = lds4(pat[h] + po + (r8 + r) * 4);
+                                acc[h] = __fmaf_rn(w.x, v0, acc[h]);
+                                acc[h] = __fmaf_rn(w.y, v1, acc[h]);
+                                acc[h] = __fmaf_rn(w.z, v2, acc[h]);
+                                acc[h] = __fmaf_rn(w.w, v3, acc[h]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (r8 + r + k < live) {
+                                    const float v = lds1(piece + r8 * 128 + vat[r + k]);
+#pragma unroll
+                                    for (int h = 0; h < NH; ++h)
+                                        acc[h] = __fmaf_rn(lds1(pat[h] + po + (r8 + r + k) * 4), v,
+                                                           acc[h]);
+                                }
+                        }
+                    }
                 }
             }
         }
         if (32 * sl + lane < d)
 #pragma unroll
             for (int h = 0; h < NH; ++h)
-                if (h < nh) xs[part_at + (h * most + c) * d + 32 * sl + lane] = acc[h];
+                if (h < nh) xs[part_at + (int64_t(h) * most + c) * d + 32 * sl + lane] = acc[h];
     }
-    cp_wait<0>();
-    cluster.sync();
+    if (LOAD != kTma) cp_wait<0>();
+    if (LOAD == kTma && stuck) {        // let the copies in flight land, tell the cluster
+        for (int i = 0; i < stages; ++i) {
+            (void)mbar_wait_bounded(bars + 8 * slot, phase);
+            if (++slot == stages) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+        if (lane == 0) {
+            atomicOr(&g_decode_watchdog, kWatchdogDecode);
+            for (int r = 0; r < C; ++r) *cluster.map_shared_rank(&F.lost[rank], r) = 2;
+        }
+    }
+    meet();
+    for (int r = 0; r < C; ++r) lost |= F.lost[r];
     // ---- the chunks left to right
     for (int i = rank * kThreads + tid; i < nh * d; i += C * kThreads) {
         const int h = i / d;
         float t = 0.0f;
         for (int r = 0; r < C; ++r) {
-            const float *p = scores_of(r) + part_at + h * most * d + (i - h * d);
+            const float *p = scores_of(r) + part_at + int64_t(h) * most * d + (i - h * d);
             const int chunks = base + (r < rem);
             for (int c = 0; c < chunks; ++c) {
-                const float v = p[c * d];
+                const float v = p[int64_t(c) * d];
                 t = r == 0 && c == 0 ? v : __fadd_rn(t, v);
             }
         }
         o[i] = lost ? __uint_as_float(0x7fc00000u) : t;
     }
-    if (lost && rank == 0 && tid == 0 && A.dev_status)
+    if ((lost & 1) && rank == 0 && tid == 0 && A.dev_status)
         atomicOr(reinterpret_cast<int *>(A.dev_status), 2);
-    cluster.sync();               // the others still read this CTA's shared memory
+    if (C > 1) cluster.sync();    // the others still read this CTA's shared memory
+}
+
+int register_heads(int nh) { return nh <= 2 ? nh : nh <= 4 ? 4 : kMaxHeads; }
+
+// Shared memory of a CTA before the room.
+size_t fixed_bytes(int nh) {
+    switch (register_heads(nh)) {
+        case 1: return sizeof(Fixed<1>);
+        case 2: return sizeof(Fixed<2>);
+        case 4: return sizeof(Fixed<4>);
+        default: return sizeof(Fixed<kMaxHeads>);
+    }
 }
 
 struct DecodePlan {
-    int unit_heads, batches, cluster;
+    int unit_heads, batches, cluster, stages;
     int room;                     // floats of shared memory
     int64_t ws_cta, ws_bytes;
 };
 
+// The cluster: the largest power of two whose units all fit on the GPU at once
+// (and no more CTAs than the longest row has chunks). 12 heads of 64, us on one
+// GB300 with 1 / 2 / 4 / 8 / 16 CTAs: 64 requests of 700..2048 tokens 93 / 113 /
+// 134 / 238 / 238; 8 of 1024..2048: 30 / 24 / 24 / 36 / 36; one of 32768: 448 /
+// 233 / 116 / 71 / 51. Sizes between powers of two measured slower than the power
+// below. Two stages where a CTA's run is at most two chunks (three CTAs then fit
+// an SM: 256 requests of 100..512 tokens 112 -> 95), three else.
 DecodePlan decode_plan(int64_t batch, int64_t heads, int64_t kv_heads, int64_t head_dim,
                        int64_t max_len) {
     DecodePlan p;
@@ -466,13 +646,14 @@ DecodePlan decode_plan(int64_t batch, int64_t heads, int64_t kv_heads, int64_t h
     const int64_t units = std::max<int64_t>(1, batch * kv_heads * p.batches);
     const int64_t chunks = (max_len + kKChunk - 1) / kKChunk;
     const int64_t slots = int64_t(sm_count_current_device()) * kCtasPerSm;
-    int c = 1;
-    while (c < kMaxCluster && units * c < slots && 2 * c <= chunks) c *= 2;
-    const char *ev = getenv("DEC_C");
-    if (ev) { c = atoi(ev); while (c > 1 && c > chunks) c /= 2; }
-    p.cluster = c;
-    const int64_t need = int64_t(p.unit_heads) * ((chunks + c - 1) / c) * (kKChunk + head_dim);
-    const int64_t cap = (kSmemPerCta - int64_t(sizeof(Fixed))) / 4;
+    int64_t c = 1;
+    while (2 * c <= kMaxCluster && 2 * c * units <= slots && 2 * c <= chunks) c *= 2;
+    p.cluster = int(c);
+    const int64_t run = (chunks + c - 1) / c;         // a CTA's most chunks
+    p.stages = run <= 2 ? 2 : stages_of(p.unit_heads);
+    const int64_t need = int64_t(p.unit_heads) * run * (kKChunk + head_dim);
+    const int64_t cap =
+        (kSmemPerCta - p.stages * kRingBytes - int64_t(fixed_bytes(p.unit_heads))) / 4;
     p.room = int(std::min(need, cap));
     p.ws_cta = need > cap ? (need + 3) / 4 * 4 : 0;
     p.ws_bytes = p.ws_cta * 4 * units * c;
@@ -496,14 +677,28 @@ cudaError_t launch_decode_attention(int64_t batch, int heads, const float *q, in
     DecodeArgs A = {heads, int(c.kv_heads), int(c.head_dim), q, ldq, c.k, c.v, c.num_pages,
                     unsigned(c.page_size), -1, c.page_stride, c.token_stride, c.head_stride,
                     table, ldt, kv_lens, scale, out, ldo, workspace, max_len, p.ws_cta, p.room,
-                    p.unit_heads, p.batches, dev_status};
+                    0, p.unit_heads, p.batches, p.stages, max_pages, dev_status};
     for (int i = 0; i < 31; ++i)
         if (c.page_size == int64_t(1) << i) A.page_shift = i;
     auto al16 = [](const void *x) { return reinterpret_cast<uintptr_t>(x) % 16 == 0; };
-    const bool vec = al16(c.k) && al16(c.v) && c.head_dim % 4 == 0 && c.page_stride % 4 == 0 &&
+    const bool vec = al16(c.k) && al16(c.v) && c.page_stride % 4 == 0 &&
                      c.token_stride % 4 == 0 && c.head_stride % 4 == 0;
+    Loader load = vec && c.head_dim % 4 == 0 ? kCopy16 : kCopy4;
+    CUtensorMap kmap = {}, vmap = {};
+    const bool boxes = c.page_size == 8 || c.page_size == 16 || c.page_size == 32 ||
+                       c.page_size % kTokens == 0;
+    if (vec && boxes) {
+        A.box = int(std::min<int64_t>(c.page_size, kTokens));
+        const int64_t extent[4] = {c.head_dim, c.kv_heads, c.page_size, c.num_pages};
+        const int64_t stride[3] = {c.head_stride, c.token_stride, c.page_stride};
+        const uint32_t box[4] = {32, 1, uint32_t(A.box), 1};
+        if (make_tensor_map_4d(&kmap, c.k, extent, stride, box) &&
+            make_tensor_map_4d(&vmap, c.v, extent, stride, box))
+            load = kTma;
+    }
     auto run = [&](auto kern) {
-        const size_t smem = sizeof(Fixed) + size_t(p.room) * 4;
+        const size_t smem =
+            size_t(p.stages) * kRingBytes + fixed_bytes(p.unit_heads) + size_t(p.room) * 4;
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              int(smem));
         if (e == cudaSuccess && p.cluster > 8)
@@ -520,20 +715,31 @@ cudaError_t launch_decode_attention(int64_t batch, int heads, const float *q, in
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, kern, A);
+        e = cudaLaunchKernelEx(&cfg, kern, A, kmap, vmap);
         return e == cudaSuccess ? cudaGetLastError() : e;
     };
-    const int nh = p.unit_heads;
-    if (vec) {
-        if (nh == 1) return run(decode_kernel<1, true>);
-        if (nh == 2) return run(decode_kernel<2, true>);
-        if (nh <= 4) return run(decode_kernel<4, true>);
-        return run(decode_kernel<8, true>);
+    auto pick = [&](auto heads_in) {
+        constexpr int NH = decltype(heads_in)::value;
+        return load == kTma      ? run(decode_kernel<NH, kTma>)
+               : load == kCopy16 ? run(decode_kernel<NH, kCopy16>)
+                                 : run(decode_kernel<NH, kCopy4>);
+    };
+    switch (register_heads(p.unit_heads)) {
+        case 1: return pick(std::integral_constant<int, 1>());
+        case 2: return pick(std::integral_constant<int, 2>());
+        case 4: return pick(std::integral_constant<int, 4>());
+        default: return pick(std::integral_constant<int, kMaxHeads>());
     }
-    if (nh == 1) return run(decode_kernel<1, false>);
-    if (nh == 2) return run(decode_kernel<2, false>);
-    if (nh <= 4) return run(decode_kernel<4, false>);
-    return run(decode_kernel<8, false>);
+}
+
+cudaError_t decode_watchdog(unsigned int *code, int clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_decode_watchdog, sizeof(unsigned int));
+    if (e != cudaSuccess) return e;
+    if (clear && *code) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_decode_watchdog, &zero, sizeof(unsigned int));
+    }
+    return e;
 }
 
 }  // namespace det

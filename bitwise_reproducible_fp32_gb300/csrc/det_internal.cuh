@@ -26,7 +26,8 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr unsigned int kWatchdogGemm = 1u;   // GEMM operand staging
 // bit 1 (2u): cross-entropy row staging, defined in rowops.cu; bit 2 (4u):
 // RMSNorm-backward staging (rmsbwd.cu); bit 3 (8u): RMSNorm row staging
-// (rowops.cu); bit 4 (16u): causal-softmax row staging (block.cu)
+// (rowops.cu); bit 4 (16u): causal-softmax row staging (block.cu); bit 5 (32u):
+// decode attention's pieces (decode.cu)
 
 // ---------------------------------------------------------------- launchers
 // Each returns cudaSuccess or the launch error; arguments are validated by
@@ -127,11 +128,16 @@ cudaError_t launch_gemm_noalloc(const GemmArgs &a, bool *too_big, cudaStream_t s
 cudaError_t rowops_watchdog(unsigned int *code, int clear);
 cudaError_t rmsbwd_watchdog(unsigned int *code, int clear);
 cudaError_t block_watchdog(unsigned int *code, int clear);
+cudaError_t decode_watchdog(unsigned int *code, int clear);
 
 // 2-D fp32 TMA descriptor over a row-major matrix: inner = contiguous extent,
 // outer = rows, ld = row stride (elements); out-of-range boxes read zeros.
 bool make_tensor_map_2d(CUtensorMap *map, const float *base, int64_t inner, int64_t outer,
                         int64_t ld, uint32_t box_inner, uint32_t box_outer, bool swizzle128);
+// 4-D fp32 TMA descriptor with 128-byte swizzle: extents innermost first, the
+// strides (elements) of the outer three; false where it cannot be described.
+bool make_tensor_map_4d(CUtensorMap *map, const float *base, const int64_t (&extent)[4],
+                        const int64_t (&stride)[3], const uint32_t (&box_size)[4]);
 // Whether TMA can describe a matrix at base with row stride ld (16-byte rules).
 bool tma_operand_ok(const float *base, int64_t ld);
 // x = a + b (dense rows of D), then the RMSNorm of x into y, in one kernel
@@ -423,6 +429,15 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1,
+                                            int c2, int c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
         : "memory");
 }
 

@@ -1185,6 +1185,24 @@ bool make_tensor_map_2d(CUtensorMap *map, const float *base, int64_t inner, int6
     return r == CUDA_SUCCESS;
 }
 
+bool make_tensor_map_4d(CUtensorMap *map, const float *base, const int64_t (&extent)[4],
+                        const int64_t (&stride)[3], const uint32_t (&box_size)[4]) {
+    auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[4], strides[3];
+    cuuint32_t box[4], estr[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) {
+        dims[i] = cuuint64_t(extent[i]);
+        box[i] = box_size[i];
+        if (i < 3) strides[i] = cuuint64_t(stride[i]) * 4;
+    }
+    const CUresult r =
+        enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<float *>(base), dims, strides,
+            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool tma_operand_ok(const float *base, int64_t ld) {
     return (reinterpret_cast<uintptr_t>(base) % 16 == 0) && (ld % 4 == 0) &&
            (ld * 4 < (int64_t(1) << 40));

@@ -758,10 +758,12 @@ det_status detpages_release(const det_profile_v1 *prof, int64_t batch, int64_t p
  * Entries of the table past a request's pages are not read, nor are the slots
  * past its length. out: row stride ldo, must not overlap q or the cache.
  * workspace: at least detdecode_attention_workspace_bytes (16-byte aligned, no
- * contents assumed); calls that share one must be ordered (one stream).
+ * contents assumed); calls that share one must be ordered (one stream). A wait
+ * for a piece of the cache that gives up after 2 s sets bit 5 of
+ * det_watchdog_status(), and the request's row is NaN.
  * Errors: DET_ERR_INVALID_ARG for batch outside 0..65535, heads not a multiple
  * of kv_heads, the cache's rules (detkv_append_f32), max_pages < 1, max_pages *
- * page_size >= 2^31, strides or null pointers; DET_ERR_WORKSPACE. */
+ * page_size > 2^30, strides or null pointers; DET_ERR_WORKSPACE. */
 det_status detdecode_attention_f32(const det_profile_v1 *prof, int64_t batch, int64_t heads,
                                    const float *q, int64_t ldq, const det_kv_cache *cache,
                                    const int32_t *table, int64_t max_pages, int64_t ldt,
@@ -820,7 +822,8 @@ det_status detlogprob_bwd_f32(const det_profile_v1 *prof, int64_t rows, int64_t 
  * *code == 0 means no bounded device wait has ever given up; otherwise bit k
  * identifies the kernel family that gave up (bit 0: GEMM operand staging,
  * bit 1: cross-entropy row staging, bit 2: RMSNorm-backward tile staging,
- * bit 3: RMSNorm row staging, bit 4: causal-softmax row staging).
+ * bit 3: RMSNorm row staging, bit 4: causal-softmax row staging, bit 5:
+ * decode attention's pieces).
  * This call synchronises the device (it copies from device memory). */
 det_status det_watchdog_status(int32_t *code, int clear);
 
