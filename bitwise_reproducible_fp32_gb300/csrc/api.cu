@@ -1243,6 +1243,8 @@ DET_API det_status det_watchdog_status(int32_t *code, int clear) {
     if (e == cudaSuccess) e = block_watchdog(&c5, clear);
     unsigned int c6 = 0;
     if (e == cudaSuccess) e = decode_watchdog(&c6, clear);
-    *code = int32_t(c | c2 | c3 | c5 | c6);
+    unsigned int c7 = 0;
+    if (e == cudaSuccess) e = logprob_watchdog(&c7, clear);
+    *code = int32_t(c | c2 | c3 | c5 | c6 | c7);
     return from_cuda(e);
 }

@@ -27,7 +27,8 @@ constexpr unsigned int kWatchdogGemm = 1u;   // GEMM operand staging
 // bit 1 (2u): cross-entropy row staging, defined in rowops.cu; bit 2 (4u):
 // RMSNorm-backward staging (rmsbwd.cu); bit 3 (8u): RMSNorm row staging
 // (rowops.cu); bit 4 (16u): causal-softmax row staging (block.cu); bit 5 (32u):
-// decode attention's pieces (decode.cu)
+// decode attention's pieces (decode.cu); bit 6 (64u): log-probability row
+// staging (logprob.cu)
 
 // ---------------------------------------------------------------- launchers
 // Each returns cudaSuccess or the launch error; arguments are validated by
@@ -129,6 +130,7 @@ cudaError_t rowops_watchdog(unsigned int *code, int clear);
 cudaError_t rmsbwd_watchdog(unsigned int *code, int clear);
 cudaError_t block_watchdog(unsigned int *code, int clear);
 cudaError_t decode_watchdog(unsigned int *code, int clear);
+cudaError_t logprob_watchdog(unsigned int *code, int clear);
 
 // 2-D fp32 TMA descriptor over a row-major matrix: inner = contiguous extent,
 // outer = rows, ld = row stride (elements); out-of-range boxes read zeros.

@@ -20,16 +20,10 @@
 
 #include "det_internal.cuh"
 #include "det_math.cuh"
+#include "row_stage.cuh"
 
 namespace det {
 namespace {
-
-__device__ __forceinline__ float warp_butterfly_sum(float s) {
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1)
-        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
-    return s;
-}
 
 // ---------------------------------------------------------------- RMSNorm
 // One warp per row; lane l owns groups l, l + 32, ... Rows whose start, stride
@@ -124,14 +118,6 @@ __global__ void __launch_bounds__(kRmsWarps * 32)
 }
 
 // ---------------------------------------------------------------- cross-entropy
-// The profile's row max: NaN if any element is NaN, else the largest (ties
-// between +0 and -0 are bit-inert for the loss and dlogits).
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
 __device__ __forceinline__ uint64_t l2_policy_evict_last() {
     uint64_t pol;
     asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
@@ -185,20 +171,6 @@ __device__ __forceinline__ float dl_of(float e, float inv, float dscale) {
 }
 __device__ __forceinline__ float dl_of_label(float e, float inv, float dscale) {
     return __fmul_rn(__fsub_rn(__fmul_rn(e, inv), 1.0f), dscale);
-}
-
-// The profile's group g (elements 4g .. 4g+3) from granule g (cur) and
-// granule g + 1 (nxt): the last 4 - H elements of cur, then the first H of nxt.
-template <int H>
-__device__ __forceinline__ float4 group_of(float4 cur, float4 nxt) {
-    if (H == 0) return cur;
-    if (H == 1) return make_float4(cur.y, cur.z, cur.w, nxt.x);
-    if (H == 2) return make_float4(cur.z, cur.w, nxt.x, nxt.y);
-    return make_float4(cur.w, nxt.x, nxt.y, nxt.z);
-}
-
-__device__ __forceinline__ float comp(float4 v, int i) {
-    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 // Granule g+1 for lanes 0..30 comes from the next lane; lane 31 loaded it.
@@ -471,7 +443,6 @@ __global__ void __launch_bounds__(kXentThreads, 2)
 // The operations and their order are those of the register kernel below.
 constexpr int kXsThreads = 1024;
 constexpr int kXsMaxGranules = 14400;            // 230,400 bytes of row buffer
-constexpr int kXsPiece = 1024;                   // granules per bulk copy (16 KB)
 // Row parts, each with its mbarrier: a part is refilled with the next row as
 // soon as its dlogits are out. Two measured fastest (three: +1%, four: +3%,
 // eight: +8%; each part costs a CTA barrier a row).
@@ -484,78 +455,6 @@ constexpr unsigned kWatchdogXent = 2u;
 
 __device__ unsigned int g_rowops_watchdog;
 
-
-// Asks L2 to fetch granules [0, n) of the row whose aligned base is xa. Every
-// granule holds at least one element of the row, so no byte outside the
-// row's pages is touched.
-__device__ __forceinline__ void prefetch_granules_l2(const float *xa, int n) {
-    for (int q = 0; q < n; q += kXsPiece) {
-        const int c = min(kXsPiece, n - q);
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(xa + 4 * q),
-                     "r"(uint32_t(c) * 16u)
-                     : "memory");
-    }
-}
-
-// Thread 0: copies granules [q0, q1) of the row whose aligned base is xa into
-// the same granules of buf, completing on bar.
-__device__ __forceinline__ void load_granules(float4 *buf, const float *xa, int q0, int q1,
-                                              uint64_t *bar) {
-    const uint32_t b = smem_u32(bar);
-    mbar_arrive_expect_tx(b, uint32_t(q1 - q0) * 16u);
-    for (int q = q0; q < q1; q += kXsPiece) {
-        const int n = min(kXsPiece, q1 - q);
-        bulk_load(smem_u32(buf + q), xa + 4 * q, uint32_t(n) * 16u, b);
-    }
-}
-
-// Stage D for a row with misalignment H: chain l (< 256) adds the exps of its
-// groups g = l, l + 256, ... in ascending order. Group g is the last 4 - H
-// elements of granule g and the first H of granule g + 1; both granules are
-// read with 16-byte loads (consecutive chains, consecutive granules: no bank
-// conflicts), one sweep ahead of the adds.
-// 16-byte load from shared memory by shared-window address: the chain runs in
-// an out-of-line function, where a plain pointer would compile to a generic
-// load (slower, and tracked as a long-latency access).
-__device__ __forceinline__ float4 lds4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ float lds1(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-    return v;
-}
-
-template <int H>
-__device__ __noinline__ float xent_smem_chain(uint32_t buf, int V) {
-    const int l = threadIdx.x;
-    const int ngroups = (V + 3) >> 2, gfull = V >> 2;
-    float s = 0.0f;
-    int g = l;
-    if (g < gfull) {
-        float4 c0 = lds4(buf + 16u * g), c1 = H ? lds4(buf + 16u * (g + 1)) : c0;
-        for (; g < gfull; g += kXentLanes) {
-            const int gn = g + kXentLanes;
-            float4 n0 = c0, n1 = c1;
-            if (gn < gfull) {
-                n0 = lds4(buf + 16u * gn);
-                if (H) n1 = lds4(buf + 16u * (gn + 1));
-            }
-            const float4 v = group_of<H>(c0, c1);
-            s = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(s, v.x), v.y), v.z), v.w);
-            c0 = n0;
-            c1 = n1;
-        }
-    }
-    if (g < ngroups) {     // the last, partial group
-        for (int j = 4 * g; j < V; ++j) s = __fadd_rn(s, lds1(buf + 4u * (j + H)));
-    }
-    return s;
-}
 
 __global__ void __launch_bounds__(kXsThreads, 1)
     xent_smem_kernel(int64_t rows, int V, const float *logits, int64_t ld,

@@ -780,11 +780,12 @@ det_status detdecode_attention_workspace_bytes(const det_profile_v1 *prof, int64
  * and the top_k largest alternatives of each row:
  *   m (+0 for a zero of either sign), e_j and S as detxent_f32 forms them;
  *   logp = (x_y - m) - log(S), so logp = -loss of detxent_f32 bit for bit;
- *   entropy = log(S) - T / S with T the sum of e_j * (x_j - m): 4096 chains, chain
- *   j mod 4096 taking T = fmaf(e_j, x_j - m, T) from +0 in ascending j (elements
- *   with e_j == 0 left out), folded as ((T_4t + T_4t+1) + T_4t+2) + T_4t+3, then
- *   the butterfly 16..1 within each 32 consecutive t and the same butterfly over
- *   the 32 totals;
+ *   entropy = log(S) - T / S with T the sum of e_j * (x_j - m): the row is cut
+ *   into blocks of 16384 elements; in each, chain j mod 4096 takes
+ *   t = fmaf(e_j, x_j - m, t) from +0 in ascending j (elements with e_j == 0 left
+ *   out); the blocks' chains are added left to right from +0, then folded as
+ *   ((T_4i + T_4i+1) + T_4i+2) + T_4i+3, the butterfly 16..1 within each 32
+ *   consecutive i and the same butterfly over the 32 totals;
  *   the alternatives: the top_k largest logits, the lowest id first among equal
  *   ones (+0 and -0 are equal; NaN counts as larger than +Inf), each with
  *   (x - m) - log(S).
@@ -796,7 +797,9 @@ det_status detdecode_attention_workspace_bytes(const det_profile_v1 *prof, int64
  * logp, entropy: rows floats. stats: rows x 4 floats (m, 1 / S, log S, entropy),
  * what the gradient reads, 16-byte aligned, or NULL. top_ids (int32) and top_logp
  * (floats): rows x top_k, dense; NULL when top_k is 0.
- * V in 1..2^30, top_k in 0..min(V, 32), rows may be 0.
+ * V in 1..2^30, top_k in 0..min(V, 32), rows may be 0. A wait for a row's bulk
+ * copies that gives up after 2 s sets bit 6 of det_watchdog_status() and leaves
+ * the remaining rows unwritten.
  * Errors: DET_ERR_INVALID_ARG for sizes, strides or null pointers;
  * DET_ERR_ALIGNMENT for a misaligned stats. */
 det_status detlogprob_f32(const det_profile_v1 *prof, int64_t rows, int64_t V,
@@ -823,7 +826,7 @@ det_status detlogprob_bwd_f32(const det_profile_v1 *prof, int64_t rows, int64_t 
  * identifies the kernel family that gave up (bit 0: GEMM operand staging,
  * bit 1: cross-entropy row staging, bit 2: RMSNorm-backward tile staging,
  * bit 3: RMSNorm row staging, bit 4: causal-softmax row staging, bit 5:
- * decode attention's pieces).
+ * decode attention's pieces, bit 6: log-probability row staging).
  * This call synchronises the device (it copies from device memory). */
 det_status det_watchdog_status(int32_t *code, int clear);
 

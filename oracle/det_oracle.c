@@ -866,9 +866,9 @@ static void xent_rows(int64_t lo, int64_t hi, int tix, void *c) {
 /* log probabilities of tokens                                               */
 /* ------------------------------------------------------------------------ */
 /* Per row: m, e_j and S as the cross-entropy; logp = (x_y - m) - log(S); T = the
- * sum of e_j * (x_j - m) over 4096 chains (element j on chain j mod 4096, fmaf
- * from +0 in ascending j, elements with e_j == 0 left out), folded in fours left
- * to right, then by the butterfly within each 32 of the 1024 sums and over the
+ * sum of e_j * (x_j - m) over 4096 chains of each 16384 elements (element j on
+ * chain j mod 4096, fmaf from +0 in ascending j, elements with e_j == 0 left out),
+ * a chain's blocks added left to right from +0, then folded in fours left to right, then by the butterfly within each 32 of the 1024 sums and over the
  * 32 totals; entropy = log(S) - T / S; stats = (m, 1 / S, log S, entropy). The
  * k alternatives: the largest logits, lowest id first among equals, NaN above
  * all; each with (x - m) - log(S). Token -1: logp +0; others outside: NaN. */
@@ -892,7 +892,7 @@ static int goes_before(float a, int64_t i, float b, int64_t j) {
 static void logprob_rows(int64_t lo, int64_t hi, int tix, void *c) {
     (void)tix;
     logprob_ctx *q = (logprob_ctx *)c;
-    float s[1024], T[4096], u[1024], tot[32];
+    float s[1024], T[4096], B[4096], u[1024], tot[32];
     for (int64_t r = lo; r < hi; ++r) {
         const float *x = q->x + r * q->ld;
         const int64_t y = q->tokens[r];
@@ -900,12 +900,14 @@ static void logprob_rows(int64_t lo, int64_t hi, int tix, void *c) {
         for (int64_t j = 1; j < q->V; ++j) if (x[j] > m || x[j] != x[j]) m = x[j];
         m = m + 0.0f;          /* a zero maximum is +0 */
         for (int l = 0; l < q->lanes; ++l) s[l] = 0.0f;
-        for (int l = 0; l < 4096; ++l) T[l] = 0.0f;
+        for (int l = 0; l < 4096; ++l) T[l] = B[l] = 0.0f;
         for (int64_t j = 0; j < q->V; ++j) {
             const float d = x[j] - m, e = detor_exp(d);
             const int l = (int)((j / q->group) % q->lanes);
             s[l] = s[l] + e;
-            if (e != 0.0f) T[j % 4096] = fmaf(e, d, T[j % 4096]);
+            if (e != 0.0f) B[j % 4096] = fmaf(e, d, B[j % 4096]);
+            if (j % 16384 == 16383 || j + 1 == q->V)
+                for (int c2 = 0; c2 < 4096; ++c2) { T[c2] = T[c2] + B[c2]; B[c2] = 0.0f; }
         }
         const float S = butterfly(s, q->lanes);
         for (int t = 0; t < 1024; ++t)

@@ -108,8 +108,8 @@ def decode64(q, K, V, scale):
 def logprob64(x, y):
     """(logp, entropy, bounds of both) in 64 bits, rows with finite maxima. d = x - m
     rounds by U |d|, exp within a step (2U): e is off by U (|d| + 2) relative; S:
-    at most 4 ceil(V / 1024) + 8 adds; log within a step; T: a fmaf for each of
-    ceil(V / 4096) elements of a chain and 12 adds."""
+    at most 4 ceil(V / 1024) + 8 adds; log within a step; T: at most one fmaf for each
+    of ceil(V / 4096) elements of a chain, an add a block and 12 adds."""
     x = x.astype(np.float64)
     d = x - x.max(1, keepdims=True)
     e = np.exp(d)
@@ -125,5 +125,6 @@ def logprob64(x, y):
     b1 = U * (np.abs(dy) + 2 * np.abs(logS) + np.abs(logp) + wS) * 1.01 + 1e-37
     ent = logS - T
     b2 = U * (2 * np.abs(logS) + np.abs(ent) + wS + np.abs(T) * (wS + 2)
-              + (p * np.abs(dd) * (2 * np.abs(dd) + 2 + math.ceil(V / 4096) + 12)).sum(1)) * 1.01
+              + (p * np.abs(dd) * (2 * np.abs(dd) + 2 + math.ceil(V / 4096)
+                                         + math.ceil(V / 16384) + 12)).sum(1)) * 1.01
     return logp, ent, b1, b2 + 1e-37
