@@ -14,13 +14,13 @@
 // Forward, rows of more than 4096 logits: one persistent CTA an SM, its warps in
 // roles that follow one another down the rows, so that the max of one row, the
 // exps of the row before and its sums run at the same time:
-//   max    6 warps read a row straight from global memory (it stays in L2): its
-//          max and the maxima of 32 groups of threads, up to two rows ahead
-//   load   a lane brings the rows a second time, from L2, in segments of 1024
+//   max    8 warps read a row straight from global memory (it stays in L2): its
+//          max and the maxima of 32 groups of threads, up to three rows ahead
+//   load   a lane brings the rows a second time, from L2, in segments of 2048
 //          granules (row_stage.cuh) through a ring in shared memory
 //   exp    16 warps: e in place and T's chains (a chain belongs to the thread that
 //          owns its granules), and a list of the elements that may be alternatives
-//   chain  8 warps: the 256 chains of S, a segment behind where a group straddles
+//   chain  4 warps: the 256 chains of S, a segment behind where a group straddles
 //   final  a warp folds S and T, ranks the list and writes the row's results
 // They meet at mbarriers only, every wait bounded. Staging whole rows and going
 // through them phase by phase with all warps measured 2.6 times slower (874 us for
@@ -33,6 +33,7 @@
 // top_k maxima over the row instead. Neither way depends on the order of arrival.
 // Gradient: a thread four granules of a row; the exps again from the row's m.
 #include <algorithm>
+#include <cstddef>
 
 #include "det_internal.cuh"
 #include "det_math.cuh"
@@ -47,20 +48,23 @@ namespace {
 
 constexpr int kTChains = 4096;
 constexpr int kTBlock = 16384;          // elements
-constexpr int kSeg = kTChains / 4;      // granules of a segment: T's chains once
-constexpr int kRing = 8;                // segments in shared memory
-constexpr int kChainWarps = kXentLanes / 32, kExpWarps = 16, kMaxWarps = 6;
+constexpr int kSweep = kTChains / 4;    // granules that cover T's chains once
+constexpr int kSeg = 2 * kSweep;        // granules of a segment
+constexpr int kRing = 4;                // segments in shared memory
+constexpr int kChainWarps = 4, kExpWarps = 16, kMaxWarps = 8;
+constexpr int kChainThreads = kChainWarps * 32, kChains = kXentLanes / kChainThreads;
 constexpr int kExpThreads = kExpWarps * 32, kMaxThreads = kMaxWarps * 32;
 constexpr int kWarps = kChainWarps + kExpWarps + kMaxWarps + 2;
 constexpr int kStreamThreads = kWarps * 32;
-constexpr int kSets = kSeg / kExpThreads;    // granules a thread has in a segment
+constexpr int kSets = kSweep / kExpThreads;  // granules a thread has in a sweep
 constexpr int kMaxLoads = 8;            // granules a max thread reads at once
+constexpr int kAhead = 3;               // rows whose max may wait for its exps
 constexpr int kListed = 512;
 constexpr int kSmallVocab = kTChains;   // a warp a row up to here
 constexpr int kSmallWarps = 8, kSmallListed = 128;
 constexpr unsigned kWatchdogLogprob = 64u;   // det_watchdog_status bit 6
 constexpr float kInf = __builtin_inff();
-static_assert(kSeg % kXentLanes == 0 && kTBlock % kTChains == 0, "whole sweeps");
+static_assert(kSeg % kXentLanes == 0 && kTBlock % (4 * kSeg) == 0, "whole sweeps");
 
 // Order of the alternatives as a key: larger logits have larger keys, +0 and -0
 // the same, NaN the largest; the lower id wins among equal keys. A 64-bit rank
@@ -159,14 +163,23 @@ __device__ __forceinline__ float list_bound(float v, int top_k, int lane) {
     return __shfl_sync(0xffffffffu, v, __ffs(at) - 1);
 }
 
-// The ranks of a list of n <= 32 * N candidates in order: the k-th in lane k.
+// The ranks of a list of n candidates in order: the k-th in lane k.
 __device__ __forceinline__ uint64_t rank_list(const uint64_t *list, int n, int top_k,
                                               uint64_t *top, int lane) {
-    for (int c = lane; c < n; c += 32) {
-        const uint64_t r = list[c];
-        int better = 0;
-        for (int k = 0; k < n; ++k) better += list[k] > r;
-        if (better < top_k) top[better] = r;
+    for (int c0 = 0; c0 < n; c0 += 128) {
+        uint64_t r[4];
+        int better[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = c0 + 32 * i + lane < n ? list[c0 + 32 * i + lane] : 0;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const uint64_t o = list[k];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) better[i] += o > r[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (r[i] && better[i] < top_k) top[better[i]] = r[i];
     }
     __syncwarp();
     return lane < top_k ? top[lane] : 0;
@@ -220,44 +233,65 @@ __device__ __forceinline__ float4 exp_and_t(float4 v, f32x2 m2, float m, float4 
     return e;
 }
 
-struct RowState {                       // of the rows 0 and 1 mod 2 of a CTA
+struct alignas(16) RowState {           // of the rows 0 and 1 mod 2 of a CTA
     float T[kTChains];
     uint64_t list[kListed];
     uint64_t top[32];
-    float parts[kMaxWarps][32];         // the max threads' own maxima
-    float red[kChainWarps];
-    float m, bound;
+    float red[kXentLanes / 32];
     int listed;
+};
+struct RowMax {                         // of the rows 0 .. kAhead - 1 mod kAhead
+    float parts[kMaxWarps][32];         // the max threads' own maxima
+    float m, bound;
 };
 struct Stream {
     float4 ring[kRing][kSeg];
     RowState row[2];
+    RowMax max[kAhead];
     uint64_t loaded[kRing], exped[kRing], freed[kRing];
-    uint64_t parted[2], maxed[2], done[2], taken[2];
+    uint64_t parted[kAhead], maxed[kAhead], passed[kAhead], done[2], taken[2];
     int abort;
 };
+
+static_assert(sizeof(RowState) % 16 == 0 && offsetof(Stream, row) % 16 == 0 &&
+                  offsetof(Stream, max) % 16 == 0 && offsetof(Stream, loaded) % 8 == 0 &&
+                  offsetof(RowState, T) == 0 && sizeof(Stream) <= 227 * 1024,
+              "16-byte reads of T, 8-byte barriers");
 
 __device__ __forceinline__ void fence_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// The 4 groups of chain l in a staged segment (granules at `at`, `next` the
-// address of the granule after it): in ascending order.
+// The groups of chains l, l + kChainThreads, ... in a staged segment (granules at
+// `at`, `next` the address of the granule after it), in ascending order. inner:
+// every group is inside the row.
 template <int H>
-__device__ __forceinline__ float chain_segment(uint32_t at, uint32_t next, int l, int left, float s) {
+__device__ __forceinline__ void chain_segment(uint32_t at, uint32_t next, int l, int left,
+                                              bool inner, float (&s)[kChains]) {
+    if (inner) {
 #pragma unroll
-    for (int i = 0; i < kSeg / kXentLanes; ++i) {
-        const int g = l + kXentLanes * i;
-        if (4 * g + 3 < left) {
+        for (int i = 0; i < kSeg / kChainThreads; ++i) {
+            const int g = l + kChainThreads * i;
             const float4 c0 = lds4(at + 16u * g);
-            const float4 c1 = H ? lds4(g + 1 < kSeg ? at + 16u * (g + 1) : next) : c0;
+            const float4 c1 =
+                H ? lds4(i + 1 < kSeg / kChainThreads || g + 1 < kSeg ? at + 16u * (g + 1) : next)
+                  : c0;
             const float4 v = group_of<H>(c0, c1);
-            s = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(s, v.x), v.y), v.z), v.w);
-        } else {
-            for (int j = 4 * g; j < left; ++j) s = __fadd_rn(s, lds1(at + 4u * (j + H)));
+            float &c = s[i % kChains];
+            c = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(c, v.x), v.y), v.z), v.w);
         }
+        return;
     }
-    return s;
+#pragma unroll
+    for (int k = 0; k < kChains; ++k)
+        for (int i = k; i < kSeg / kChainThreads; i += kChains) {
+            const int g = l + kChainThreads * i;
+            for (int j = 4 * g; j < min(left, 4 * g + 4); ++j) {
+                const int at_j = j + H;      // past the segment: in the next one
+                s[k] = __fadd_rn(s[k], lds1(at_j < 4 * kSeg ? at + 4u * at_j
+                                                            : next + 4u * (at_j - 4 * kSeg)));
+            }
+        }
 }
 
 __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(LogprobArgs A) {
@@ -271,9 +305,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
             mbar_init(bar(sh.exped[i]), kExpWarps);
             mbar_init(bar(sh.freed[i]), kChainWarps);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kAhead; ++i) {
             mbar_init(bar(sh.parted[i]), kMaxWarps);
             mbar_init(bar(sh.maxed[i]), 1);
+            mbar_init(bar(sh.passed[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bar(sh.done[i]), kExpWarps + kChainWarps);
             mbar_init(bar(sh.taken[i]), 1);
             sh.row[i].listed = 0;
@@ -300,7 +337,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
         // ---- the chains of S
         for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, ++k) {
             const int h = shift_of(start_of(row)), ns = ((V + h + 3) / 4 + kSeg - 1) / kSeg;
-            float S = 0.0f;
+            float S[kChains];
+#pragma unroll
+            for (int c = 0; c < kChains; ++c) S[c] = 0.0f;
             bool ok = true;
             for (int s = 0; s < ns && ok; ++s, ++seg) {
                 ok = wait(sh.exped[seg % kRing], seg / kRing);
@@ -310,26 +349,31 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
                 const uint32_t at = smem_u32(sh.ring[seg % kRing]);
                 const uint32_t next = smem_u32(sh.ring[(seg + 1) % kRing]);
                 const int left = V - 4 * kSeg * s;
-                S = h == 0   ? chain_segment<0>(at, next, tid, left, S)
-                    : h == 1 ? chain_segment<1>(at, next, tid, left, S)
-                    : h == 2 ? chain_segment<2>(at, next, tid, left, S)
-                             : chain_segment<3>(at, next, tid, left, S);
+                const bool inner = left >= 4 * kSeg;
+                if (h == 0) chain_segment<0>(at, next, tid, left, inner, S);
+                else if (h == 1) chain_segment<1>(at, next, tid, left, inner, S);
+                else if (h == 2) chain_segment<2>(at, next, tid, left, inner, S);
+                else chain_segment<3>(at, next, tid, left, inner, S);
                 arrive(sh.freed[seg % kRing]);
             }
             if (!ok) break;
-            S = warp_butterfly_sum(S);
-            if (lane == 0) sh.row[k & 1].red[warp] = S;
+#pragma unroll
+            for (int c = 0; c < kChains; ++c) {
+                const float t = warp_butterfly_sum(S[c]);
+                if (lane == 0) sh.row[k & 1].red[c * kChainWarps + warp] = t;
+            }
             arrive(sh.done[k & 1]);
         }
     } else if (warp < kChainWarps + kExpWarps) {
         // ---- e in place, T, the list
-        const int et = tid - kXentLanes;
+        const int et = tid - kChainThreads;
         for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, ++k) {
             const int h = shift_of(start_of(row)), nch = (V + h + 3) / 4;
             const int ns = (nch + kSeg - 1) / kSeg;
             RowState &R = sh.row[k & 1];
-            if (!wait(sh.maxed[k & 1], k / 2)) break;
-            const float m = R.m, bound = R.bound;
+            if (!wait(sh.maxed[k % kAhead], k / kAhead)) break;
+            if (k >= 2 && !wait(sh.taken[k & 1], k / 2 - 1)) break;
+            const float m = sh.max[k % kAhead].m, bound = sh.max[k % kAhead].bound;
             const bool finite_m = fabsf(m) <= 0x1.fffffep127f;
             const f32x2 m2 = splat2(m);
             auto note = [&](float v, int j) {
@@ -351,37 +395,63 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
                 if (!ok) break;
                 float4 *b = sh.ring[seg % kRing];
                 // a block's first granule holds h elements of the block before
-                const bool turn = s > 0 && s % (kTBlock / kTChains) == 0;
+                const bool turn = s > 0 && s % (kTBlock / (4 * kSeg)) == 0;
+                if (turn)
 #pragma unroll
-                for (int u = 0; u < kSets; ++u) {
-                    const int q = et + u * kExpThreads, j0 = 4 * (s * kSeg + q) - h;
-                    if (s * kSeg + q >= nch) break;
-                    const float4 v = b[q];
-                    const int keep = turn && q == 0 ? h : 0;
-                    if (turn) flush(tt[u], tb[u], keep, 4);
-                    if (finite_m && j0 >= 0 && j0 + 3 < V) {
-                        b[q] = exp_and_t(v, m2, m, tb[u]);
-                        if (fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= bound) {
-                            if (v.x >= bound) note(v.x, j0);
-                            if (v.y >= bound) note(v.y, j0 + 1);
-                            if (v.z >= bound) note(v.z, j0 + 2);
-                            if (v.w >= bound) note(v.w, j0 + 3);
-                        }
-                    } else {
-                        float e[4], t[4] = {tb[u].x, tb[u].y, tb[u].z, tb[u].w};
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const float d = __fsub_rn(comp(v, c), m);
-                            e[c] = det_exp_call(d);
-                            if (j0 + c >= 0 && j0 + c < V) {
-                                if (e[c] != 0.0f) t[c] = __fmaf_rn(e[c], d, t[c]);
-                                if (comp(v, c) >= bound) note(comp(v, c), j0 + c);
-                            }
-                        }
-                        tb[u] = make_float4(t[0], t[1], t[2], t[3]);
-                        b[q] = make_float4(e[0], e[1], e[2], e[3]);
+                    for (int u = 0; u < kSets; ++u)
+                        flush(tt[u], tb[u], et + u * kExpThreads == 0 ? h : 0, 4);
+                const int keep = turn && et == 0 ? h : 0;
+                auto listing = [&](float4 v, int q) {
+                    if (fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= bound) {
+                        const int j0 = 4 * (s * kSeg + q) - h;
+                        if (v.x >= bound) note(v.x, j0);
+                        if (v.y >= bound) note(v.y, j0 + 1);
+                        if (v.z >= bound) note(v.z, j0 + 2);
+                        if (v.w >= bound) note(v.w, j0 + 3);
                     }
-                    if (keep) flush(tt[u], tb[u], 0, keep);
+                };
+                if (finite_m && s > 0 && 4 * kSeg * (s + 1) - h <= V) {
+                    // every element is inside the row
+#pragma unroll 1
+                    for (int q0 = et; q0 < kSeg; q0 += kSweep) {
+#pragma unroll
+                        for (int u = 0; u < kSets; ++u) {
+                            const int q = q0 + u * kExpThreads;
+                            const float4 v = b[q];
+                            b[q] = exp_and_t(v, m2, m, tb[u]);
+                            listing(v, q);
+                        }
+                        if (keep && q0 == et) flush(tt[0], tb[0], 0, keep);
+                    }
+                } else {
+                    // the row's ends, or a row without a finite max
+#pragma unroll 1
+                    for (int q0 = et; q0 < kSeg; q0 += kSweep) {
+#pragma unroll
+                        for (int u = 0; u < kSets; ++u) {
+                            const int q = q0 + u * kExpThreads, j0 = 4 * (s * kSeg + q) - h;
+                            if (s * kSeg + q >= nch) break;
+                            const float4 v = b[q];
+                            if (finite_m && j0 >= 0 && j0 + 3 < V) {
+                                b[q] = exp_and_t(v, m2, m, tb[u]);
+                                listing(v, q);
+                                continue;
+                            }
+                            float e[4], t[4] = {tb[u].x, tb[u].y, tb[u].z, tb[u].w};
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const float d = __fsub_rn(comp(v, c), m);
+                                e[c] = det_exp_call(d);
+                                if (j0 + c >= 0 && j0 + c < V) {
+                                    if (e[c] != 0.0f) t[c] = __fmaf_rn(e[c], d, t[c]);
+                                    if (comp(v, c) >= bound) note(comp(v, c), j0 + c);
+                                }
+                            }
+                            tb[u] = make_float4(t[0], t[1], t[2], t[3]);
+                            b[q] = make_float4(e[0], e[1], e[2], e[3]);
+                        }
+                        if (keep && q0 == et) flush(tt[0], tb[0], 0, keep);
+                    }
                 }
                 arrive(sh.exped[seg % kRing]);
             }
@@ -401,10 +471,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
         // ---- the max, and the 32 groups' (the lanes of the same number)
         const int mw = warp - kChainWarps - kExpWarps, mt = mw * 32 + lane;
         for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, ++k) {
-            RowState &R = sh.row[k & 1];
-            if (k >= 2 && !wait(sh.taken[k & 1], k / 2 - 1)) break;
+            RowMax &R = sh.max[k % kAhead];
+            if (k >= kAhead && !wait(sh.passed[k % kAhead], k / kAhead - 1)) break;
             const float *x = start_of(row);
             const int h = shift_of(x);
+            if (A.ahead && mt == 0 && row + gridDim.x < A.rows) {
+                const float *y = start_of(row + gridDim.x);
+                prefetch_granules_l2(y - shift_of(y), (V + shift_of(y) + 3) / 4);
+            }
             const int lo = h ? 1 : 0, hi = (V + h) / 4;      // granules inside the row
             const float4 *xa = reinterpret_cast<const float4 *>(x - h);
             float m = -kInf;
@@ -423,9 +497,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
             if (mt < head) m = max_nan(m, x[mt]);
             if (mt >= 32 && tail + mt - 32 < V) m = max_nan(m, x[tail + mt - 32]);
             R.parts[mw][lane] = m;
-            arrive(sh.parted[k & 1]);
+            arrive(sh.parted[k % kAhead]);
             if (mw == 0) {
-                if (!wait(sh.parted[k & 1], k / 2)) break;
+                if (!wait(sh.parted[k % kAhead], k / kAhead)) break;
                 float g = R.parts[0][lane];
 #pragma unroll
                 for (int w = 1; w < kMaxWarps; ++w) g = max_nan(g, R.parts[w][lane]);
@@ -440,7 +514,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
                     R.m = all;
                     R.bound = bound;
                 }
-                arrive(sh.maxed[k & 1]);
+                arrive(sh.maxed[k % kAhead]);
             }
         }
     } else if (warp == kWarps - 2) {
@@ -450,11 +524,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
             for (int64_t row = blockIdx.x; row < A.rows && ok; row += gridDim.x) {
                 const float *x = start_of(row);
                 const int h = shift_of(x), nch = (V + h + 3) / 4;
-                const int64_t then = row + 2 * int64_t(gridDim.x);
-                if (A.ahead && then < A.rows) {
-                    const float *y = start_of(then);
-                    prefetch_granules_l2(y - shift_of(y), (V + shift_of(y) + 3) / 4);
-                }
                 for (int q = 0; q < nch; q += kSeg, ++seg) {
                     const int at = seg % kRing;
                     if (seg >= kRing &&
@@ -486,7 +555,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
             const float S =
                 __fadd_rn(__fadd_rn(__fadd_rn(t[0], t[1]), __fadd_rn(t[2], t[3])),
                           __fadd_rn(__fadd_rn(t[4], t[5]), __fadd_rn(t[6], t[7])));
-            const float m = R.m;
+            const float m = sh.max[k % kAhead].m;
             uint64_t rank = 0;
             if (A.top_k > 0)
                 rank = R.listed > kListed || !(fabsf(m) <= 0x1.fffffep127f)
@@ -496,6 +565,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
             __syncwarp();
             if (lane == 0) R.listed = 0;
             arrive(sh.taken[k & 1]);
+            arrive(sh.passed[k % kAhead]);
         }
     }
     __syncthreads();
@@ -697,7 +767,7 @@ cudaError_t launch_logprob(int64_t rows, int64_t V, const float *logits, int64_t
         return cudaGetLastError();
     }
     const int64_t grid = std::min<int64_t>(rows, sms);
-    // three rows a CTA in L2 at once: prefetched where they fit with room to spare
+    // the rows between max and exps in L2, and the next one asked for where it fits
     A.ahead = 3 * grid * V * 4 <= int64_t(96) << 20;
     const cudaError_t e = cudaFuncSetAttribute(
         logprob_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Stream)));
