@@ -57,7 +57,7 @@ constexpr int kExpThreads = kExpWarps * 32, kMaxThreads = kMaxWarps * 32;
 constexpr int kWarps = kChainWarps + kExpWarps + kMaxWarps + 2;
 constexpr int kStreamThreads = kWarps * 32;
 constexpr int kSets = kSweep / kExpThreads;  // granules a thread has in a sweep
-constexpr int kMaxLoads = 8;            // granules a max thread reads at once
+constexpr int kMaxLoads = 6;            // granules a max thread reads at once
 constexpr int kAhead = 3;               // rows whose max may wait for its exps
 constexpr int kListed = 512;
 constexpr int kSmallVocab = kTChains;   // a warp a row up to here
@@ -88,6 +88,47 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t r) {
     return r;
 }
 
+// max / min of three (NaN-propagating where it forms the row's max).
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max4(float4 v) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(v.x), "f"(v.y), "f"(v.z));
+    return fmaxf(r, v.w);
+}
+__device__ __forceinline__ float min4(float a, float b, float c, float d) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return fminf(r, d);
+}
+__device__ __forceinline__ float more_max(float m, float4 v) {
+    return max3_nan(max3_nan(m, v.x, v.y), v.z, v.w);
+}
+
+// Eight butterflies 16..1 at once: in each level the two halves of the warp go
+// on with different values, so 9 shuffles serve instead of 40; the additions are
+// the butterfly's. Returns the total of v[row_of_lane(lane)].
+__device__ __forceinline__ float butterfly8(float (&v)[8], int lane) {
+#pragma unroll
+    for (int half = 4, off = 16; half >= 1; half >>= 1, off >>= 1) {
+        const bool up = lane & off;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float keep = up ? v[i + half] : v[i], send = up ? v[i] : v[i + half];
+            v[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, off));
+        }
+    }
+    float t = __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[0], 2));
+    return __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, 1));
+}
+// The lane that holds the total of v[w] then (among others).
+__device__ __forceinline__ int lane_of_row(int w) {
+    return (w & 4) << 2 | (w & 2) << 2 | (w & 1) << 2;
+}
+
 struct LogprobArgs {
     int64_t rows;
     int V;
@@ -103,26 +144,42 @@ struct LogprobArgs {
     int ahead;                  // 1: rows are prefetched into L2
 };
 
-// What a row's warp 0 lane writes of it, given S, T and the alternatives' ranks
-// (lane k < top_k holds the k-th).
-__device__ __forceinline__ void write_row(const LogprobArgs &A, int64_t row, const float *x, float m,
+// The logit whose rank this is (+0 for -0, which x - m does not tell apart).
+__device__ __forceinline__ float logit_of(uint64_t rank) {
+    const uint32_t k = uint32_t(rank >> 32);
+    if (k == 0xffffffffu) return __uint_as_float(0x7fc00000u);
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// A row's token and its logit, asked for before the sums are there.
+struct Asked {
+    int y;
+    float x;
+};
+__device__ __forceinline__ Asked ask(const LogprobArgs &A, int64_t row, const float *x) {
+    Asked a = {A.tokens[row], 0.0f};
+    if (a.y >= 0 && a.y < A.V) a.x = x[a.y];
+    return a;
+}
+
+// What a warp writes of a row, given S, T and the alternatives' ranks (lane
+// k < top_k holds the k-th).
+__device__ __forceinline__ void write_row(const LogprobArgs &A, int64_t row, Asked a, float m,
                                           float S, float T, uint64_t rank, int lane) {
     const float logS = det_log(S);
     const float ent = __fsub_rn(logS, __fdiv_rn(T, S));
     if (lane == 0) {
-        const int y = A.tokens[row];
-        const bool none = y == -1, wrong = !none && (y < 0 || y >= A.V);
+        const bool none = a.y == -1, wrong = !none && (a.y < 0 || a.y >= A.V);
         A.logp[row] = none    ? 0.0f
                       : wrong ? __uint_as_float(0x7fc00000u)
-                              : __fsub_rn(__fsub_rn(x[y], m), logS);
+                              : __fsub_rn(__fsub_rn(a.x, m), logS);
         A.entropy[row] = ent;
         if (A.stats) A.stats[row] = make_float4(m, __fdiv_rn(1.0f, S), logS, ent);
         if (wrong && A.dev_status) atomicOr(reinterpret_cast<int *>(A.dev_status), 1);
     }
     if (lane < A.top_k) {
-        const int j = id_of(rank);
-        A.top_ids[row * A.top_k + lane] = j;
-        A.top_logp[row * A.top_k + lane] = __fsub_rn(__fsub_rn(x[j], m), logS);
+        A.top_ids[row * A.top_k + lane] = id_of(rank);
+        A.top_logp[row * A.top_k + lane] = __fsub_rn(__fsub_rn(logit_of(rank), m), logS);
     }
 }
 
@@ -186,17 +243,17 @@ __device__ __forceinline__ uint64_t rank_list(const uint64_t *list, int n, int t
 }
 
 // e = exp(x - m) for the 4 elements of a granule and T's fmaf on their chains,
-// for a finite m: exp4's bits. n = rint(d log2 e) sits in the low bits of tm, so
-// p 2^n is p's bits plus tm's shifted up. Elements below the fast range (and
-// -inf) take the general exp; e == 0 leaves T alone.
-__device__ __forceinline__ float4 exp_and_t(float4 v, f32x2 m2, float m, float4 &t) {
+// for a finite m, without branches: exp4's bits where the returned value, the
+// least n = rint(d log2 e) plus kRoundMagic, is at least kFast; below (and at
+// -inf) both are formed again by exp_slow from the old t. n sits in the low bits
+// of tm, so p 2^n is p's bits plus tm's shifted up.
+constexpr float kFast = kRoundMagic - 125.0f;
+__device__ __forceinline__ float exp_and_t(float4 v, f32x2 m2, float4 &e, float4 &t) {
     const f32x2 d01 = sub2(pack2(v.x, v.y), m2), d23 = sub2(pack2(v.z, v.w), m2);
-    float d0, d1, d2, d3;
-    unpack2(d01, d0, d1);
-    unpack2(d23, d2, d3);
-    const f32x2 magic = splat2(kRoundMagic);
-    const f32x2 tm01 = add2(pack2(__fmul_rn(d0, kLog2e), __fmul_rn(d1, kLog2e)), magic);
-    const f32x2 tm23 = add2(pack2(__fmul_rn(d2, kLog2e), __fmul_rn(d3, kLog2e)), magic);
+    // d log2 e rounded on its own: a fused step with -0 (which changes no product),
+    // as a packed multiply that feeds a packed add rounds as if fused with it
+    const f32x2 magic = splat2(kRoundMagic), l2e = splat2(kLog2e), none = splat2(-0.0f);
+    const f32x2 tm01 = add2(fma2(d01, l2e, none), magic), tm23 = add2(fma2(d23, l2e, none), magic);
     const f32x2 n01 = sub2(tm01, magic), n23 = sub2(tm23, magic);
     const f32x2 hi = splat2(-kLn2Hi), lo = splat2(-kLn2Lo);
     const f32x2 r01 = fma2(n01, lo, fma2(n01, hi, d01)), r23 = fma2(n23, lo, fma2(n23, hi, d23));
@@ -215,26 +272,44 @@ __device__ __forceinline__ float4 exp_and_t(float4 v, f32x2 m2, float m, float4 
     auto scaled = [](float p, float tm) {
         return __int_as_float(__float_as_int(p) + int(__float_as_uint(tm) << 23));
     };
-    float4 e = make_float4(scaled(q0, a0), scaled(q1, a1), scaled(q2, a2), scaled(q3, a3));
-    constexpr float kFast = kRoundMagic - 125.0f;        // n >= -125
-    if (fminf(fminf(a0, a1), fminf(a2, a3)) >= kFast) {
-        unpack2(fma2(pack2(e.x, e.y), d01, pack2(t.x, t.y)), t.x, t.y);
-        unpack2(fma2(pack2(e.z, e.w), d23, pack2(t.z, t.w)), t.z, t.w);
-    } else {
-        if (!(a0 >= kFast)) e.x = det_exp_call(d0);
-        if (!(a1 >= kFast)) e.y = det_exp_call(d1);
-        if (!(a2 >= kFast)) e.z = det_exp_call(d2);
-        if (!(a3 >= kFast)) e.w = det_exp_call(d3);
-        if (e.x != 0.0f) t.x = __fmaf_rn(e.x, d0, t.x);
-        if (e.y != 0.0f) t.y = __fmaf_rn(e.y, d1, t.y);
-        if (e.z != 0.0f) t.z = __fmaf_rn(e.z, d2, t.z);
-        if (e.w != 0.0f) t.w = __fmaf_rn(e.w, d3, t.w);
+    e = make_float4(scaled(q0, a0), scaled(q1, a1), scaled(q2, a2), scaled(q3, a3));
+    unpack2(fma2(pack2(e.x, e.y), d01, pack2(t.x, t.y)), t.x, t.y);
+    unpack2(fma2(pack2(e.z, e.w), d23, pack2(t.z, t.w)), t.z, t.w);
+    return min4(a0, a1, a2, a3);
+}
+
+// The general form of it, for any m: elements with e == 0 leave T alone. e in
+// the first half, the new t in the second.
+struct ExpT { float4 e, t; };
+__device__ __noinline__ ExpT exp_slow(float4 v, float m, float4 t) {
+    float e[4], c[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const float d = __fsub_rn(comp(v, i), m);
+        const float x = det_exp(d);
+        const float y = x != 0.0f ? __fmaf_rn(x, d, i == 0 ? c[0] : i == 1 ? c[1] : i == 2 ? c[2] : c[3])
+                                  : (i == 0 ? c[0] : i == 1 ? c[1] : i == 2 ? c[2] : c[3]);
+        if (i == 0) { e[0] = x; c[0] = y; }
+        if (i == 1) { e[1] = x; c[1] = y; }
+        if (i == 2) { e[2] = x; c[2] = y; }
+        if (i == 3) { e[3] = x; c[3] = y; }
     }
-    return e;
+    return {make_float4(e[0], e[1], e[2], e[3]), make_float4(c[0], c[1], c[2], c[3])};
+}
+
+// Lists the elements of granule v (the first is element j0) at or above the bound.
+__device__ __noinline__ void list_granule(uint64_t *list, int *listed, float4 v, int j0,
+                                          float bound) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i)
+        if (comp(v, i) >= bound) {
+            const int at = atomicAdd(listed, 1);
+            if (at < kListed) list[at] = rank_of(comp(v, i), j0 + i);
+        }
 }
 
 struct alignas(16) RowState {           // of the rows 0 and 1 mod 2 of a CTA
-    float T[kTChains];
+    float4 T[kSweep];                   // by granule: chain c at float c + h mod 4096
     uint64_t list[kListed];
     uint64_t top[32];
     float red[kXentLanes / 32];
@@ -322,7 +397,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
     volatile int *abort = &sh.abort;
     // waits of a whole warp; false once any wait of the CTA has given up
     auto wait = [&](uint64_t &b, uint32_t phase) {
-        return __all_sync(0xffffffffu, mbar_wait_or_abort(bar(b), phase & 1u, abort)) != 0;
+        return __all_sync(0xffffffffu, mbar_wait_suspended_or_abort(bar(b), phase & 1u, abort)) != 0;
     };
     auto arrive = [&](uint64_t &b) {
         __syncwarp();
@@ -376,95 +451,97 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
             const float m = sh.max[k % kAhead].m, bound = sh.max[k % kAhead].bound;
             const bool finite_m = fabsf(m) <= 0x1.fffffep127f;
             const f32x2 m2 = splat2(m);
-            auto note = [&](float v, int j) {
-                const int at = atomicAdd(&R.listed, 1);
-                if (at < kListed) R.list[at] = rank_of(v, j);
+            // T of the current block; the blocks add up in R.T, from +0
+            float4 t[kSets];
+            auto flush = [&](int u, bool first, int from, int to) {
+                float4 &all = R.T[et + u * kExpThreads];
+                float4 a = all;
+                auto one = [&](float &x, float &y) {
+                    x = __fadd_rn(first ? 0.0f : x, y);
+                    y = 0.0f;
+                };
+                if (from <= 0 && 0 < to) one(a.x, t[u].x);
+                if (from <= 1 && 1 < to) one(a.y, t[u].y);
+                if (from <= 2 && 2 < to) one(a.z, t[u].z);
+                if (from <= 3 && 3 < to) one(a.w, t[u].w);
+                all = a;
             };
-            float4 tb[kSets], tt[kSets];     // T of the current block, and in all
 #pragma unroll
-            for (int u = 0; u < kSets; ++u) tb[u] = tt[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            auto flush = [](float4 &t, float4 &b, int from, int to) {
-                if (from <= 0 && 0 < to) { t.x = __fadd_rn(t.x, b.x); b.x = 0.0f; }
-                if (from <= 1 && 1 < to) { t.y = __fadd_rn(t.y, b.y); b.y = 0.0f; }
-                if (from <= 2 && 2 < to) { t.z = __fadd_rn(t.z, b.z); b.z = 0.0f; }
-                if (from <= 3 && 3 < to) { t.w = __fadd_rn(t.w, b.w); b.w = 0.0f; }
-            };
-            bool ok = true;
+            for (int u = 0; u < kSets; ++u) t[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            bool ok = true, fresh = true;        // fresh: R.T holds nothing of this row
             for (int s = 0; s < ns; ++s, ++seg) {
                 ok = wait(sh.loaded[seg % kRing], seg / kRing);
                 if (!ok) break;
                 float4 *b = sh.ring[seg % kRing];
-                // a block's first granule holds h elements of the block before
+                // a block's first granule holds h elements of the block before: the
+                // rest of the thread's chains are flushed before it, those after
                 const bool turn = s > 0 && s % (kTBlock / (4 * kSeg)) == 0;
-                if (turn)
-#pragma unroll
-                    for (int u = 0; u < kSets; ++u)
-                        flush(tt[u], tb[u], et + u * kExpThreads == 0 ? h : 0, 4);
                 const int keep = turn && et == 0 ? h : 0;
-                auto listing = [&](float4 v, int q) {
-                    if (fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= bound) {
-                        const int j0 = 4 * (s * kSeg + q) - h;
-                        if (v.x >= bound) note(v.x, j0);
-                        if (v.y >= bound) note(v.y, j0 + 1);
-                        if (v.z >= bound) note(v.z, j0 + 2);
-                        if (v.w >= bound) note(v.w, j0 + 3);
-                    }
-                };
-                if (finite_m && s > 0 && 4 * kSeg * (s + 1) - h <= V) {
-                    // every element is inside the row
-#pragma unroll 1
-                    for (int q0 = et; q0 < kSeg; q0 += kSweep) {
+                if (turn) {
 #pragma unroll
-                        for (int u = 0; u < kSets; ++u) {
-                            const int q = q0 + u * kExpThreads;
-                            const float4 v = b[q];
-                            b[q] = exp_and_t(v, m2, m, tb[u]);
-                            listing(v, q);
-                        }
-                        if (keep && q0 == et) flush(tt[0], tb[0], 0, keep);
-                    }
-                } else {
-                    // the row's ends, or a row without a finite max
-#pragma unroll 1
-                    for (int q0 = et; q0 < kSeg; q0 += kSweep) {
-#pragma unroll
-                        for (int u = 0; u < kSets; ++u) {
-                            const int q = q0 + u * kExpThreads, j0 = 4 * (s * kSeg + q) - h;
-                            if (s * kSeg + q >= nch) break;
-                            const float4 v = b[q];
-                            if (finite_m && j0 >= 0 && j0 + 3 < V) {
-                                b[q] = exp_and_t(v, m2, m, tb[u]);
-                                listing(v, q);
-                                continue;
-                            }
-                            float e[4], t[4] = {tb[u].x, tb[u].y, tb[u].z, tb[u].w};
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const float d = __fsub_rn(comp(v, c), m);
-                                e[c] = det_exp_call(d);
-                                if (j0 + c >= 0 && j0 + c < V) {
-                                    if (e[c] != 0.0f) t[c] = __fmaf_rn(e[c], d, t[c]);
-                                    if (comp(v, c) >= bound) note(comp(v, c), j0 + c);
-                                }
-                            }
-                            tb[u] = make_float4(t[0], t[1], t[2], t[3]);
-                            b[q] = make_float4(e[0], e[1], e[2], e[3]);
-                        }
-                        if (keep && q0 == et) flush(tt[0], tb[0], 0, keep);
-                    }
+                    for (int u = 0; u < kSets; ++u) flush(u, fresh, u == 0 ? keep : 0, 4);
                 }
+                const bool ends = s == 0 || s + 1 == ns;
+#pragma unroll 1
+                for (int q0 = et; q0 < kSeg; q0 += kSweep) {
+                    float4 v[kSets], e[kSets], old[kSets];
+                    float least = kInf, most = -kInf;
+#pragma unroll
+                    for (int u = 0; u < kSets; ++u) {
+                        old[u] = t[u];
+                        v[u] = b[q0 + u * kExpThreads];
+                        float top = 0.0f;
+                        if (ends) {
+                            // elements outside the row count as m: e = 1 and T as it was
+                            const int j0 = 4 * (s * kSeg + q0 + u * kExpThreads) - h;
+                            float4 w = v[u];
+                            if (j0 < 0 || j0 >= V) w.x = -kInf;
+                            if (j0 + 1 < 0 || j0 + 1 >= V) w.y = -kInf;
+                            if (j0 + 2 < 0 || j0 + 2 >= V) w.z = -kInf;
+                            if (j0 + 3 >= V) w.w = -kInf;
+                            top = max4(w);
+                            if (j0 < 0 || j0 >= V) v[u].x = m;
+                            if (j0 + 1 < 0 || j0 + 1 >= V) v[u].y = m;
+                            if (j0 + 2 < 0 || j0 + 2 >= V) v[u].z = m;
+                            if (j0 + 3 >= V) v[u].w = m;
+                        } else {
+                            top = max4(v[u]);
+                        }
+                        most = fmaxf(most, top);
+                        least = fminf(least, exp_and_t(v[u], m2, e[u], t[u]));
+                    }
+                    if (!(least >= kFast) || !finite_m) {
+#pragma unroll
+                        for (int u = 0; u < kSets; ++u) {
+                            const ExpT x2 = exp_slow(v[u], m, old[u]);
+                            e[u] = x2.e;
+                            t[u] = x2.t;
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < kSets; ++u) b[q0 + u * kExpThreads] = e[u];
+                    if (most >= bound)
+#pragma unroll
+                        for (int u = 0; u < kSets; ++u) {
+                            float4 w = v[u];
+                            const int j0 = 4 * (s * kSeg + q0 + u * kExpThreads) - h;
+                            if (ends) {
+                                if (j0 < 0 || j0 >= V) w.x = -kInf;
+                                if (j0 + 1 < 0 || j0 + 1 >= V) w.y = -kInf;
+                                if (j0 + 2 < 0 || j0 + 2 >= V) w.z = -kInf;
+                                if (j0 + 3 >= V) w.w = -kInf;
+                            }
+                            if (max4(w) >= bound)
+                                list_granule(R.list, &R.listed, w, j0, bound);
+                        }
+                    if (keep && q0 == et) flush(0, fresh, 0, keep);
+                }
+                if (turn) fresh = false;
                 arrive(sh.exped[seg % kRing]);
             }
             if (!ok) break;
 #pragma unroll
-            for (int u = 0; u < kSets; ++u) {
-                flush(tt[u], tb[u], 0, 4);
-                const int c = 4 * (et + u * kExpThreads) - h;
-                R.T[c & (kTChains - 1)] = tt[u].x;
-                R.T[(c + 1) & (kTChains - 1)] = tt[u].y;
-                R.T[(c + 2) & (kTChains - 1)] = tt[u].z;
-                R.T[(c + 3) & (kTChains - 1)] = tt[u].w;
-            }
+            for (int u = 0; u < kSets; ++u) flush(u, fresh, 0, 4);
             arrive(sh.done[k & 1]);
         }
     } else if (warp < kChainWarps + kExpWarps + kMaxWarps) {
@@ -490,7 +567,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
 #pragma unroll
                 for (int u = 0; u < kMaxLoads; ++u)
                     if (q0 + u * kMaxThreads < hi)
-                        m = max_nan(m, max_nan(max_nan(v[u].x, v[u].y), max_nan(v[u].z, v[u].w)));
+                        m = more_max(m, v[u]);
             }
             // the elements before and after those granules
             const int head = h ? 4 - h : 0, tail = 4 * hi - h;
@@ -527,7 +604,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
                 for (int q = 0; q < nch; q += kSeg, ++seg) {
                     const int at = seg % kRing;
                     if (seg >= kRing &&
-                        !mbar_wait_or_abort(bar(sh.freed[at]), (seg / kRing - 1) & 1u, abort)) {
+                        !mbar_wait_suspended_or_abort(bar(sh.freed[at]), (seg / kRing - 1) & 1u, abort)) {
                         ok = false;
                         break;
                     }
@@ -540,15 +617,25 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
         // ---- the results
         for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, ++k) {
             RowState &R = sh.row[k & 1];
-            if (!wait(sh.done[k & 1], k / 2)) break;
             const float *x = start_of(row);
+            const int h = shift_of(x);
+            const Asked asked = ask(A, row, x);
+            if (!wait(sh.done[k & 1], k / 2)) break;
             float T = 0.0f;
-#pragma unroll 4
-            for (int i = 0; i < 32; ++i) {
-                const float4 c = *reinterpret_cast<const float4 *>(&R.T[4 * (32 * i + lane)]);
-                const float t =
-                    warp_butterfly_sum(__fadd_rn(__fadd_rn(__fadd_rn(c.x, c.y), c.z), c.w));
-                if (lane == i) T = t;
+            for (int i = 0; i < 4; ++i) {
+                float v[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    const int g = 256 * i + 32 * w + lane;
+                    const float4 c = R.T[g], c1 = R.T[(g + 1) & (kSweep - 1)];
+                    const float4 f = h == 0   ? c
+                                     : h == 1 ? group_of<1>(c, c1)
+                                     : h == 2 ? group_of<2>(c, c1)
+                                              : group_of<3>(c, c1);
+                    v[w] = __fadd_rn(__fadd_rn(__fadd_rn(f.x, f.y), f.z), f.w);
+                }
+                const float t = __shfl_sync(0xffffffffu, butterfly8(v, lane), lane_of_row(lane & 7));
+                if (lane >> 3 == i) T = t;
             }
             T = warp_butterfly_sum(T);
             const float *t = R.red;
@@ -561,7 +648,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
                 rank = R.listed > kListed || !(fabsf(m) <= 0x1.fffffep127f)
                            ? top_by_rounds(x, V, A.top_k, lane)
                            : rank_list(R.list, R.listed, A.top_k, R.top, lane);
-            write_row(A, row, x, m, S, T, rank, lane);
+            write_row(A, row, asked, m, S, T, rank, lane);
             __syncwarp();
             if (lane == 0) R.listed = 0;
             arrive(sh.taken[k & 1]);
@@ -576,27 +663,45 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
     }
 }
 
-// A warp a row of at most 4096 logits, read once a pass (the row stays in L1); a
-// lane has the groups lane + 32 w + 256 t, so chain lane + 32 w of S adds its
-// groups in ascending t, and T's chains have an element each.
-__global__ void __launch_bounds__(kSmallWarps * 32) logprob_small_kernel(LogprobArgs A) {
+// A warp a row of at most 4096 logits, 1024 (a sweep) at a time: read once where
+// that is the whole row, else once a pass (the row stays in L1). A lane has the
+// groups lane + 32 w + 256 t, so chain lane + 32 w of S adds its groups in ascending
+// t, and T's chains have an element each.
+template <bool ONE>
+__global__ void __launch_bounds__(kSmallWarps * 32, ONE ? 2 : 3) logprob_small_kernel(LogprobArgs A) {
     __shared__ uint64_t lists[kSmallWarps][kSmallListed], tops[kSmallWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, V = A.V;
     for (int64_t row = blockIdx.x * int64_t(kSmallWarps) + warp; row < A.rows;
          row += gridDim.x * int64_t(kSmallWarps)) {
         const float *x = A.logits + row * A.ld;
         const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0;
-        auto group = [&](int g, float fill) {
-            const int j = 4 * g;
-            if (vec && j + 3 < V) return *reinterpret_cast<const float4 *>(x + j);
-            return make_float4(j < V ? x[j] : fill, j + 1 < V ? x[j + 1] : fill,
-                               j + 2 < V ? x[j + 2] : fill, j + 3 < V ? x[j + 3] : fill);
+        const Asked asked = ask(A, row, x);
+        float4 v[8];                         // a sweep's groups; -inf past the row's end
+        auto load = [&](int g0) {
+            if (vec && 4 * g0 + 1024 <= V) {
+#pragma unroll
+                for (int w = 0; w < 8; ++w)
+                    v[w] = *reinterpret_cast<const float4 *>(x + 4 * (g0 + 32 * w + lane));
+                return;
+            }
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                const int j = 4 * (g0 + 32 * w + lane);
+                if (vec && j + 3 < V) {
+                    v[w] = *reinterpret_cast<const float4 *>(x + j);
+                } else {
+                    v[w].x = j < V ? x[j] : -kInf;
+                    v[w].y = j + 1 < V ? x[j + 1] : -kInf;
+                    v[w].z = j + 2 < V ? x[j + 2] : -kInf;
+                    v[w].w = j + 3 < V ? x[j + 3] : -kInf;
+                }
+            }
         };
         float mine = -kInf;
-#pragma unroll 8
-        for (int g = lane; 4 * g < V; g += 32) {
-            const float4 v = group(g, -kInf);
-            mine = max_nan(mine, max_nan(max_nan(v.x, v.y), max_nan(v.z, v.w)));
+        for (int g0 = 0; 4 * g0 < V; g0 += kXentLanes) {
+            load(g0);
+#pragma unroll
+            for (int w = 0; w < 8; ++w) mine = more_max(mine, v[w]);
         }
         float m = mine;
 #pragma unroll
@@ -612,53 +717,61 @@ __global__ void __launch_bounds__(kSmallWarps * 32) logprob_small_kernel(Logprob
         for (int w = 0; w < 8; ++w) s[w] = 0.0f;
         int listed = 0;
         for (int g0 = 0; 4 * g0 < V; g0 += kXentLanes) {
+            if (!ONE) load(g0);
+            if (list) {
+                float best = -kInf;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                if (4 * (g0 + 32 * w) >= V) break;       // uniform across the warp
-                const int g = g0 + 32 * w + lane, j = 4 * g;
-                const float4 v = group(g, -kInf);
-                float4 t = make_float4(0.f, 0.f, 0.f, 0.f), e = t;
-                if (finite_m) {
-                    e = exp_and_t(v, m2, m, t);          // e = 0 past the row's end
-                } else if (j < V) {                      // every e of the row is NaN or 0
-                    e.x = det_exp(__fsub_rn(v.x, m));
-                    e.y = j + 1 < V ? det_exp(__fsub_rn(v.y, m)) : 0.0f;
-                    e.z = j + 2 < V ? det_exp(__fsub_rn(v.z, m)) : 0.0f;
-                    e.w = j + 3 < V ? det_exp(__fsub_rn(v.w, m)) : 0.0f;
-                    if (e.x != 0.0f) t.x = __fmaf_rn(e.x, __fsub_rn(v.x, m), 0.0f);
-                    if (e.y != 0.0f) t.y = __fmaf_rn(e.y, __fsub_rn(v.y, m), 0.0f);
-                    if (e.z != 0.0f) t.z = __fmaf_rn(e.z, __fsub_rn(v.z, m), 0.0f);
-                    if (e.w != 0.0f) t.w = __fmaf_rn(e.w, __fsub_rn(v.w, m), 0.0f);
-                }
-                s[w] = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(s[w], e.x), e.y), e.z), e.w);
-                // each chain's one block, added to +0
-                t.x = __fadd_rn(t.x, 0.0f);
-                t.y = __fadd_rn(t.y, 0.0f);
-                t.z = __fadd_rn(t.z, 0.0f);
-                t.w = __fadd_rn(t.w, 0.0f);
-                const float u =
-                    warp_butterfly_sum(__fadd_rn(__fadd_rn(__fadd_rn(t.x, t.y), t.z), t.w));
-                if (lane == g0 / 32 + w) T = u;
-                if (list) {
-                    const float best = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-                    if (__any_sync(0xffffffffu, best >= bound && j < V)) {
+                for (int w = 0; w < 8; ++w) best = fmaxf(best, max4(v[w]));
+                if (__any_sync(0xffffffffu, best >= bound)) {
+#pragma unroll
+                    for (int w = 0; w < 8; ++w) {
+                        const int j = 4 * (g0 + 32 * w + lane);
+                        if (!__any_sync(0xffffffffu, max4(v[w]) >= bound)) continue;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const bool in = comp(v, c) >= bound && j + c < V;
+                            const bool in = comp(v[w], c) >= bound && j + c < V;
                             const unsigned who = __ballot_sync(0xffffffffu, in);
                             const int at = listed + __popc(who & ((1u << lane) - 1u));
                             if (in && at < kSmallListed)
-                                lists[warp][at] = rank_of(comp(v, c), j + c);
+                                lists[warp][at] = rank_of(comp(v[w], c), j + c);
                             listed += __popc(who);
                         }
                     }
                 }
             }
+            float u[8];                      // T's sums in fours
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                const int j = 4 * (g0 + 32 * w + lane);
+                float4 t = make_float4(0.f, 0.f, 0.f, 0.f), e = t;
+                if (4 * (g0 + 32 * w) < V) {
+                    const float least = exp_and_t(v[w], m2, e, t);
+                    if (!(least >= kFast) || !finite_m) {
+                        const ExpT x2 = exp_slow(v[w], m, make_float4(0.f, 0.f, 0.f, 0.f));
+                        e = x2.e;
+                        t = x2.t;
+                        if (!finite_m) {     // past the end -inf - m need not be 0
+                            if (j >= V) { e.x = 0.0f; t.x = 0.0f; }
+                            if (j + 1 >= V) { e.y = 0.0f; t.y = 0.0f; }
+                            if (j + 2 >= V) { e.z = 0.0f; t.z = 0.0f; }
+                            if (j + 3 >= V) { e.w = 0.0f; t.w = 0.0f; }
+                        }
+                    }
+                }
+                s[w] = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(s[w], e.x), e.y), e.z), e.w);
+                // each chain's one block, added to +0
+                u[w] = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(t.x, 0.0f), __fadd_rn(t.y, 0.0f)),
+                                           __fadd_rn(t.z, 0.0f)),
+                                 __fadd_rn(t.w, 0.0f));
+            }
+            const float t = __shfl_sync(0xffffffffu, butterfly8(u, lane), lane_of_row(lane & 7));
+            if (lane >> 3 == g0 / kXentLanes) T = t;
         }
         T = warp_butterfly_sum(T);
+        const float part = butterfly8(s, lane);
         float f[8];
 #pragma unroll
-        for (int w = 0; w < 8; ++w) f[w] = warp_butterfly_sum(s[w]);
+        for (int w = 0; w < 8; ++w) f[w] = __shfl_sync(0xffffffffu, part, lane_of_row(w));
         const float S = __fadd_rn(__fadd_rn(__fadd_rn(f[0], f[1]), __fadd_rn(f[2], f[3])),
                                   __fadd_rn(__fadd_rn(f[4], f[5]), __fadd_rn(f[6], f[7])));
         uint64_t rank = 0;
@@ -667,7 +780,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) logprob_small_kernel(Logprob
             rank = !list || listed > kSmallListed
                        ? top_by_rounds(x, V, A.top_k, lane)
                        : rank_list(lists[warp], listed, A.top_k, tops[warp], lane);
-        write_row(A, row, x, m, S, T, rank, lane);
+        write_row(A, row, asked, m, S, T, rank, lane);
         __syncwarp();
     }
 }
@@ -763,7 +876,10 @@ cudaError_t launch_logprob(int64_t rows, int64_t V, const float *logits, int64_t
     const int64_t sms = sm_count_current_device();
     if (V <= kSmallVocab) {
         const int64_t blocks = std::min<int64_t>((rows + kSmallWarps - 1) / kSmallWarps, sms * 8);
-        logprob_small_kernel<<<unsigned(blocks), kSmallWarps * 32, 0, s>>>(A);
+        if (V <= 1024)
+            logprob_small_kernel<true><<<unsigned(blocks), kSmallWarps * 32, 0, s>>>(A);
+        else
+            logprob_small_kernel<false><<<unsigned(blocks), kSmallWarps * 32, 0, s>>>(A);
         return cudaGetLastError();
     }
     const int64_t grid = std::min<int64_t>(rows, sms);

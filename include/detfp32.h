@@ -788,7 +788,7 @@ det_status detdecode_attention_workspace_bytes(const det_profile_v1 *prof, int64
  *   consecutive i and the same butterfly over the 32 totals;
  *   the alternatives: the top_k largest logits, the lowest id first among equal
  *   ones (+0 and -0 are equal; NaN counts as larger than +Inf), each with
- *   (x - m) - log(S).
+ *   (x - m) - log(S), a zero x taken as +0.
  * A row whose maximum is NaN or infinite has NaN scores (its ids are still
  * ordered); a -Inf logit elsewhere has probability 0.
  * tokens: rows int32. -1 asks for no token: logp +0. Any other outside [0, V) gives

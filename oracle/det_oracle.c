@@ -871,7 +871,7 @@ static void xent_rows(int64_t lo, int64_t hi, int tix, void *c) {
  * a chain's blocks added left to right from +0, then folded in fours left to right, then by the butterfly within each 32 of the 1024 sums and over the
  * 32 totals; entropy = log(S) - T / S; stats = (m, 1 / S, log S, entropy). The
  * k alternatives: the largest logits, lowest id first among equals, NaN above
- * all; each with (x - m) - log(S). Token -1: logp +0; others outside: NaN. */
+ * all; each with (x - m) - log(S), a zero x taken as +0. Token -1: logp +0; others outside: NaN. */
 typedef struct {
     int64_t V, ld, k;
     const float *x;
@@ -931,7 +931,7 @@ static void logprob_rows(int64_t lo, int64_t hi, int tix, void *c) {
                 if (best < 0 || goes_before(x[j], j, x[best], best)) best = j;
             }
             q->top_ids[r * q->k + k] = (int32_t)best;
-            q->top_logp[r * q->k + k] = (x[best] - m) - logS;
+            q->top_logp[r * q->k + k] = ((x[best] + 0.0f) - m) - logS;
         }
     }
 }
