@@ -424,28 +424,6 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t parity
     }
 }
 
-// mbar_try_wait that may suspend the thread for up to about `ns` first, so a warp
-// that waits long leaves the issue slots to the others.
-__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(ns)
-        : "memory");
-    return ok != 0;
-}
-
-// mbar_wait_or_abort for the warps of a pipeline, suspended between looks.
-__device__ __forceinline__ bool mbar_wait_suspended_or_abort(uint32_t bar, uint32_t parity,
-                                                             volatile int *abort) {
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait_for(bar, parity, 20000)) return true;
-    return mbar_wait_or_abort(bar, parity, abort);
-}
-
 // 2-D tiled TMA load into shared memory, completing on an mbarrier.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map,
                                             int c0, int c1, uint32_t bar) {

@@ -12,19 +12,20 @@
 // close behind (about 14 instructions an element).
 //
 // Forward, rows of more than 4096 logits: one persistent CTA an SM, its warps in
-// roles that follow one another down the rows, so that the max of one row, the
-// exps of the row before and its sums run at the same time:
-//   max    8 warps read a row straight from global memory (it stays in L2): its
+// roles that follow one another down the rows, so that the max of one row and the
+// exps and sums of the row before run at the same time:
+//   max    6 warps read a row straight from global memory (it stays in L2): its
 //          max and the maxima of 32 groups of threads, up to three rows ahead
-//   load   a lane brings the rows a second time, from L2, in segments of 2048
-//          granules (row_stage.cuh) through a ring in shared memory
-//   exp    16 warps: e in place and T's chains (a chain belongs to the thread that
-//          owns its granules), and a list of the elements that may be alternatives
-//   chain  4 warps: the 256 chains of S, a segment behind where a group straddles
-//   final  a warp folds S and T, ranks the list and writes the row's results
-// They meet at mbarriers only, every wait bounded. Staging whole rows and going
-// through them phase by phase with all warps measured 2.6 times slower (874 us for
-// 8192 x 50257 with 5 alternatives).
+//   load   a lane brings the rows a second time, from L2, in segments of 4096
+//          elements through a ring in shared memory
+//   sum    8 warps, thread l the profile's chain l: four groups of 4 elements at a
+//          time, straight-line, for enough independent work on few warps: e, the
+//          chain of S, T's 16 chains of the thread, and a list of the groups that
+//          may hold alternatives
+//   final  a warp folds the totals, ranks the list and writes the row's results
+// They meet at mbarriers only, every wait bounded. us for 8192 x 50257 with 5
+// alternatives: whole rows staged and gone through phase by phase by all warps
+// 874; 16 warps of exps handing e to 8 warps of chains through shared memory 668.
 // Rows of at most 4096 logits: a warp a row, each chain of T one element.
 // The alternatives: with t the top_k-th largest of 32 group maxima, at least
 // top_k elements are >= t, and few more; they are listed while the exps are
@@ -48,23 +49,21 @@ namespace {
 
 constexpr int kTChains = 4096;
 constexpr int kTBlock = 16384;          // elements
-constexpr int kSweep = kTChains / 4;    // granules that cover T's chains once
-constexpr int kSeg = 2 * kSweep;        // granules of a segment
-constexpr int kRing = 4;                // segments in shared memory
-constexpr int kChainWarps = 4, kExpWarps = 16, kMaxWarps = 8;
-constexpr int kChainThreads = kChainWarps * 32, kChains = kXentLanes / kChainThreads;
-constexpr int kExpThreads = kExpWarps * 32, kMaxThreads = kMaxWarps * 32;
-constexpr int kWarps = kChainWarps + kExpWarps + kMaxWarps + 2;
+constexpr int kSeg = kTChains / 4;      // groups of a segment: T's chains once
+constexpr int kRing = 8;                // segments in shared memory
+constexpr int kSumWarps = kXentLanes / 32, kMaxWarps = 6;
+constexpr int kMaxThreads = kMaxWarps * 32;
+constexpr int kWarps = kSumWarps + kMaxWarps + 2;
 constexpr int kStreamThreads = kWarps * 32;
-constexpr int kSets = kSweep / kExpThreads;  // granules a thread has in a sweep
-constexpr int kMaxLoads = 6;            // granules a max thread reads at once
+constexpr int kSets = kSeg / kXentLanes;     // groups a thread has in a segment
+constexpr int kMaxLoads = 8;            // granules a max thread reads at once
 constexpr int kAhead = 3;               // rows whose max may wait for its exps
-constexpr int kListed = 512;
+constexpr int kFound = 256, kListed = 512;    // granules, elements that may be alternatives
 constexpr int kSmallVocab = kTChains;   // a warp a row up to here
 constexpr int kSmallWarps = 8, kSmallListed = 128;
 constexpr unsigned kWatchdogLogprob = 64u;   // det_watchdog_status bit 6
 constexpr float kInf = __builtin_inff();
-static_assert(kSeg % kXentLanes == 0 && kTBlock % (4 * kSeg) == 0, "whole sweeps");
+static_assert(kSets * kSumWarps == 32 && kTBlock % kTChains == 0, "T's tree and blocks");
 
 // Order of the alternatives as a key: larger logits have larger keys, +0 and -0
 // the same, NaN the largest; the lower id wins among equal keys. A 64-bit rank
@@ -297,76 +296,119 @@ __device__ __noinline__ ExpT exp_slow(float4 v, float m, float4 t) {
     return {make_float4(e[0], e[1], e[2], e[3]), make_float4(c[0], c[1], c[2], c[3])};
 }
 
-// Lists the elements of granule v (the first is element j0) at or above the bound.
-__device__ __noinline__ void list_granule(uint64_t *list, int *listed, float4 v, int j0,
-                                          float bound) {
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i)
-        if (comp(v, i) >= bound) {
-            const int at = atomicAdd(listed, 1);
-            if (at < kListed) list[at] = rank_of(comp(v, i), j0 + i);
-        }
-}
-
-struct alignas(16) RowState {           // of the rows 0 and 1 mod 2 of a CTA
-    float4 T[kSweep];                   // by granule: chain c at float c + h mod 4096
-    uint64_t list[kListed];
-    uint64_t top[32];
-    float red[kXentLanes / 32];
-    int listed;
+struct RowState {                       // of the rows 0 and 1 mod 2 of a CTA
+    float4 found[kFound];               // the listed groups, and where they start
+    int found_at[kFound];
+    uint64_t list[kListed], top[32];
+    float red[kSumWarps], tsum[32];
+    int listed, pad[3];
 };
 struct RowMax {                         // of the rows 0 .. kAhead - 1 mod kAhead
     float parts[kMaxWarps][32];         // the max threads' own maxima
-    float m, bound;
+    float m, bound, pad[2];
 };
 struct Stream {
-    float4 ring[kRing][kSeg];
+    float4 ring[kRing][kSeg + 1];       // a segment and the granule after it
     RowState row[2];
     RowMax max[kAhead];
-    uint64_t loaded[kRing], exped[kRing], freed[kRing];
+    uint64_t loaded[kRing], freed[kRing];
     uint64_t parted[kAhead], maxed[kAhead], passed[kAhead], done[2], taken[2];
     int abort;
 };
-
-static_assert(sizeof(RowState) % 16 == 0 && offsetof(Stream, row) % 16 == 0 &&
-                  offsetof(Stream, max) % 16 == 0 && offsetof(Stream, loaded) % 8 == 0 &&
-                  offsetof(RowState, T) == 0 && sizeof(Stream) <= 227 * 1024,
-              "16-byte reads of T, 8-byte barriers");
+static_assert(sizeof(RowState) % 16 == 0 && sizeof(RowMax) % 16 == 0 &&
+                  offsetof(Stream, row) % 16 == 0 && offsetof(Stream, max) % 16 == 0 &&
+                  offsetof(Stream, loaded) % 8 == 0 && sizeof(Stream) <= 227 * 1024,
+              "16-byte reads, 8-byte barriers");
 
 __device__ __forceinline__ void fence_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// The groups of chains l, l + kChainThreads, ... in a staged segment (granules at
-// `at`, `next` the address of the granule after it), in ascending order. inner:
-// every group is inside the row.
-template <int H>
-__device__ __forceinline__ void chain_segment(uint32_t at, uint32_t next, int l, int left,
-                                              bool inner, float (&s)[kChains]) {
-    if (inner) {
+// A thread's chain of S over one row, its groups l + 256 i of the segments, and its
+// chains of T: 4 sums in fours. H: the row's misalignment. wait(segment number)
+// and freed(segment number) are the ring's barriers; false when a wait gave up.
+struct RowSums { float S, u[kSets]; };
+template <int H, class Wait, class Freed>
+__device__ __forceinline__ bool sum_row(Stream &sh, RowState &R, int V, float m, float bound,
+                                        uint32_t &seg, Wait wait, Freed freed, RowSums &out) {
+    const int l = threadIdx.x, ns = (V + 4 * kSeg - 1) / (4 * kSeg);
+    const bool finite_m = fabsf(m) <= 0x1.fffffep127f;
+    const f32x2 m2 = splat2(m);
+    float S = 0.0f;
+    float4 t[kSets], all[kSets];             // T of the current block, and in all
 #pragma unroll
-        for (int i = 0; i < kSeg / kChainThreads; ++i) {
-            const int g = l + kChainThreads * i;
-            const float4 c0 = lds4(at + 16u * g);
-            const float4 c1 =
-                H ? lds4(i + 1 < kSeg / kChainThreads || g + 1 < kSeg ? at + 16u * (g + 1) : next)
-                  : c0;
-            const float4 v = group_of<H>(c0, c1);
-            float &c = s[i % kChains];
-            c = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(c, v.x), v.y), v.z), v.w);
+    for (int u = 0; u < kSets; ++u) t[u] = all[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto flush = [&]() {
+#pragma unroll
+        for (int u = 0; u < kSets; ++u) {
+            all[u] = make_float4(__fadd_rn(all[u].x, t[u].x), __fadd_rn(all[u].y, t[u].y),
+                                 __fadd_rn(all[u].z, t[u].z), __fadd_rn(all[u].w, t[u].w));
+            t[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        return;
-    }
+    };
+    for (int s = 0; s < ns; ++s, ++seg) {
+        if (!wait(seg)) return false;
+        const uint32_t at = smem_u32(sh.ring[seg % kRing]) + 16u * l;
+        if (s > 0 && s % (kTBlock / kTChains) == 0) flush();
+        const bool tail = 4 * kSeg * (s + 1) > V;
+        const int j0 = 4 * (s * kSeg + l);
+        float4 v[kSets], e[kSets], old[kSets];
+        float least = kInf, most = -kInf;
 #pragma unroll
-    for (int k = 0; k < kChains; ++k)
-        for (int i = k; i < kSeg / kChainThreads; i += kChains) {
-            const int g = l + kChainThreads * i;
-            for (int j = 4 * g; j < min(left, 4 * g + 4); ++j) {
-                const int at_j = j + H;      // past the segment: in the next one
-                s[k] = __fadd_rn(s[k], lds1(at_j < 4 * kSeg ? at + 4u * at_j
-                                                            : next + 4u * (at_j - 4 * kSeg)));
+        for (int u = 0; u < kSets; ++u) {
+            const float4 c0 = lds4(at + 16u * kXentLanes * u);
+            const float4 c1 = H ? lds4(at + 16u * kXentLanes * u + 16u) : c0;
+            v[u] = group_of<H>(c0, c1);
+            if (tail) {                      // past the row's end: as m, and e = 0 below
+                const int j = j0 + 4 * kXentLanes * u;
+                if (j >= V) v[u].x = m;
+                if (j + 1 >= V) v[u].y = m;
+                if (j + 2 >= V) v[u].z = m;
+                if (j + 3 >= V) v[u].w = m;
+            }
+            most = fmaxf(most, max4(v[u]));
+            old[u] = t[u];
+            least = fminf(least, exp_and_t(v[u], m2, e[u], t[u]));
+        }
+        if (!(least >= kFast) || !finite_m) {
+#pragma unroll
+            for (int u = 0; u < kSets; ++u) {
+                const ExpT x = exp_slow(v[u], m, old[u]);
+                e[u] = x.e;
+                t[u] = x.t;
             }
         }
+        if (tail) {
+#pragma unroll
+            for (int u = 0; u < kSets; ++u) {
+                const int j = j0 + 4 * kXentLanes * u;
+                if (j >= V) e[u].x = 0.0f;
+                if (j + 1 >= V) e[u].y = 0.0f;
+                if (j + 2 >= V) e[u].z = 0.0f;
+                if (j + 3 >= V) e[u].w = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kSets; ++u)
+            S = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(S, e[u].x), e[u].y), e[u].z), e[u].w);
+        if (most >= bound)
+#pragma unroll
+            for (int u = 0; u < kSets; ++u)
+                if (max4(v[u]) >= bound && j0 + 4 * kXentLanes * u < V) {
+                    const int slot = atomicAdd(&R.listed, 1);
+                    if (slot < kFound) {
+                        R.found[slot] = v[u];
+                        R.found_at[slot] = j0 + 4 * kXentLanes * u;
+                    }
+                }
+        freed(seg);
+    }
+    flush();
+    out.S = S;
+#pragma unroll
+    for (int u = 0; u < kSets; ++u)
+        out.u[u] = __fadd_rn(__fadd_rn(__fadd_rn(all[u].x, all[u].y), all[u].z), all[u].w);
+    return true;
 }
 
 __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(LogprobArgs A) {
@@ -377,8 +419,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
     if (tid == 0) {
         for (int i = 0; i < kRing; ++i) {
             mbar_init(bar(sh.loaded[i]), 1);
-            mbar_init(bar(sh.exped[i]), kExpWarps);
-            mbar_init(bar(sh.freed[i]), kChainWarps);
+            mbar_init(bar(sh.freed[i]), kSumWarps);
         }
         for (int i = 0; i < kAhead; ++i) {
             mbar_init(bar(sh.parted[i]), kMaxWarps);
@@ -386,7 +427,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
             mbar_init(bar(sh.passed[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(sh.done[i]), kExpWarps + kChainWarps);
+            mbar_init(bar(sh.done[i]), kSumWarps);
             mbar_init(bar(sh.taken[i]), 1);
             sh.row[i].listed = 0;
         }
@@ -397,7 +438,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
     volatile int *abort = &sh.abort;
     // waits of a whole warp; false once any wait of the CTA has given up
     auto wait = [&](uint64_t &b, uint32_t phase) {
-        return __all_sync(0xffffffffu, mbar_wait_suspended_or_abort(bar(b), phase & 1u, abort)) != 0;
+        return __all_sync(0xffffffffu, mbar_wait_or_abort(bar(b), phase & 1u, abort)) != 0;
     };
     auto arrive = [&](uint64_t &b) {
         __syncwarp();
@@ -408,145 +449,36 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
         return int((reinterpret_cast<uintptr_t>(x) >> 2) & 3);
     };
     uint32_t k = 0, seg = 0;            // rows and segments done so far
-    if (warp < kChainWarps) {
-        // ---- the chains of S
+    if (warp < kSumWarps) {
+        // ---- e, S, T, the list
+        auto loaded = [&](uint32_t i) { return wait(sh.loaded[i % kRing], i / kRing); };
+        auto freed = [&](uint32_t i) { arrive(sh.freed[i % kRing]); };
         for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, ++k) {
-            const int h = shift_of(start_of(row)), ns = ((V + h + 3) / 4 + kSeg - 1) / kSeg;
-            float S[kChains];
-#pragma unroll
-            for (int c = 0; c < kChains; ++c) S[c] = 0.0f;
-            bool ok = true;
-            for (int s = 0; s < ns && ok; ++s, ++seg) {
-                ok = wait(sh.exped[seg % kRing], seg / kRing);
-                if (h && s + 1 < ns && ok)
-                    ok = wait(sh.exped[(seg + 1) % kRing], (seg + 1) / kRing);
-                if (!ok) break;
-                const uint32_t at = smem_u32(sh.ring[seg % kRing]);
-                const uint32_t next = smem_u32(sh.ring[(seg + 1) % kRing]);
-                const int left = V - 4 * kSeg * s;
-                const bool inner = left >= 4 * kSeg;
-                if (h == 0) chain_segment<0>(at, next, tid, left, inner, S);
-                else if (h == 1) chain_segment<1>(at, next, tid, left, inner, S);
-                else if (h == 2) chain_segment<2>(at, next, tid, left, inner, S);
-                else chain_segment<3>(at, next, tid, left, inner, S);
-                arrive(sh.freed[seg % kRing]);
-            }
-            if (!ok) break;
-#pragma unroll
-            for (int c = 0; c < kChains; ++c) {
-                const float t = warp_butterfly_sum(S[c]);
-                if (lane == 0) sh.row[k & 1].red[c * kChainWarps + warp] = t;
-            }
-            arrive(sh.done[k & 1]);
-        }
-    } else if (warp < kChainWarps + kExpWarps) {
-        // ---- e in place, T, the list
-        const int et = tid - kChainThreads;
-        for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, ++k) {
-            const int h = shift_of(start_of(row)), nch = (V + h + 3) / 4;
-            const int ns = (nch + kSeg - 1) / kSeg;
             RowState &R = sh.row[k & 1];
             if (!wait(sh.maxed[k % kAhead], k / kAhead)) break;
             if (k >= 2 && !wait(sh.taken[k & 1], k / 2 - 1)) break;
             const float m = sh.max[k % kAhead].m, bound = sh.max[k % kAhead].bound;
-            const bool finite_m = fabsf(m) <= 0x1.fffffep127f;
-            const f32x2 m2 = splat2(m);
-            // T of the current block; the blocks add up in R.T, from +0
-            float4 t[kSets];
-            auto flush = [&](int u, bool first, int from, int to) {
-                float4 &all = R.T[et + u * kExpThreads];
-                float4 a = all;
-                auto one = [&](float &x, float &y) {
-                    x = __fadd_rn(first ? 0.0f : x, y);
-                    y = 0.0f;
-                };
-                if (from <= 0 && 0 < to) one(a.x, t[u].x);
-                if (from <= 1 && 1 < to) one(a.y, t[u].y);
-                if (from <= 2 && 2 < to) one(a.z, t[u].z);
-                if (from <= 3 && 3 < to) one(a.w, t[u].w);
-                all = a;
-            };
-#pragma unroll
-            for (int u = 0; u < kSets; ++u) t[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            bool ok = true, fresh = true;        // fresh: R.T holds nothing of this row
-            for (int s = 0; s < ns; ++s, ++seg) {
-                ok = wait(sh.loaded[seg % kRing], seg / kRing);
-                if (!ok) break;
-                float4 *b = sh.ring[seg % kRing];
-                // a block's first granule holds h elements of the block before: the
-                // rest of the thread's chains are flushed before it, those after
-                const bool turn = s > 0 && s % (kTBlock / (4 * kSeg)) == 0;
-                const int keep = turn && et == 0 ? h : 0;
-                if (turn) {
-#pragma unroll
-                    for (int u = 0; u < kSets; ++u) flush(u, fresh, u == 0 ? keep : 0, 4);
-                }
-                const bool ends = s == 0 || s + 1 == ns;
-#pragma unroll 1
-                for (int q0 = et; q0 < kSeg; q0 += kSweep) {
-                    float4 v[kSets], e[kSets], old[kSets];
-                    float least = kInf, most = -kInf;
-#pragma unroll
-                    for (int u = 0; u < kSets; ++u) {
-                        old[u] = t[u];
-                        v[u] = b[q0 + u * kExpThreads];
-                        float top = 0.0f;
-                        if (ends) {
-                            // elements outside the row count as m: e = 1 and T as it was
-                            const int j0 = 4 * (s * kSeg + q0 + u * kExpThreads) - h;
-                            float4 w = v[u];
-                            if (j0 < 0 || j0 >= V) w.x = -kInf;
-                            if (j0 + 1 < 0 || j0 + 1 >= V) w.y = -kInf;
-                            if (j0 + 2 < 0 || j0 + 2 >= V) w.z = -kInf;
-                            if (j0 + 3 >= V) w.w = -kInf;
-                            top = max4(w);
-                            if (j0 < 0 || j0 >= V) v[u].x = m;
-                            if (j0 + 1 < 0 || j0 + 1 >= V) v[u].y = m;
-                            if (j0 + 2 < 0 || j0 + 2 >= V) v[u].z = m;
-                            if (j0 + 3 >= V) v[u].w = m;
-                        } else {
-                            top = max4(v[u]);
-                        }
-                        most = fmaxf(most, top);
-                        least = fminf(least, exp_and_t(v[u], m2, e[u], t[u]));
-                    }
-                    if (!(least >= kFast) || !finite_m) {
-#pragma unroll
-                        for (int u = 0; u < kSets; ++u) {
-                            const ExpT x2 = exp_slow(v[u], m, old[u]);
-                            e[u] = x2.e;
-                            t[u] = x2.t;
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < kSets; ++u) b[q0 + u * kExpThreads] = e[u];
-                    if (most >= bound)
-#pragma unroll
-                        for (int u = 0; u < kSets; ++u) {
-                            float4 w = v[u];
-                            const int j0 = 4 * (s * kSeg + q0 + u * kExpThreads) - h;
-                            if (ends) {
-                                if (j0 < 0 || j0 >= V) w.x = -kInf;
-                                if (j0 + 1 < 0 || j0 + 1 >= V) w.y = -kInf;
-                                if (j0 + 2 < 0 || j0 + 2 >= V) w.z = -kInf;
-                                if (j0 + 3 >= V) w.w = -kInf;
-                            }
-                            if (max4(w) >= bound)
-                                list_granule(R.list, &R.listed, w, j0, bound);
-                        }
-                    if (keep && q0 == et) flush(0, fresh, 0, keep);
-                }
-                if (turn) fresh = false;
-                arrive(sh.exped[seg % kRing]);
+            RowSums o;
+            bool ok;
+            switch (shift_of(start_of(row))) {
+                case 0: ok = sum_row<0>(sh, R, V, m, bound, seg, loaded, freed, o); break;
+                case 1: ok = sum_row<1>(sh, R, V, m, bound, seg, loaded, freed, o); break;
+                case 2: ok = sum_row<2>(sh, R, V, m, bound, seg, loaded, freed, o); break;
+                default: ok = sum_row<3>(sh, R, V, m, bound, seg, loaded, freed, o); break;
             }
             if (!ok) break;
+            // the first level of the folds: 32 chains of S, 32 sums in fours of T
+            float v[8] = {o.S, o.u[0], o.u[1], o.u[2], o.u[3], 0.0f, 0.0f, 0.0f};
+            const float f = butterfly8(v, lane);
+            if (lane == lane_of_row(0)) R.red[warp] = f;
 #pragma unroll
-            for (int u = 0; u < kSets; ++u) flush(u, fresh, 0, 4);
+            for (int u = 0; u < kSets; ++u)
+                if (lane == lane_of_row(u + 1)) R.tsum[kSumWarps * u + warp] = f;
             arrive(sh.done[k & 1]);
         }
-    } else if (warp < kChainWarps + kExpWarps + kMaxWarps) {
+    } else if (warp < kSumWarps + kMaxWarps) {
         // ---- the max, and the 32 groups' (the lanes of the same number)
-        const int mw = warp - kChainWarps - kExpWarps, mt = mw * 32 + lane;
+        const int mw = warp - kSumWarps, mt = mw * 32 + lane;
         for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, ++k) {
             RowMax &R = sh.max[k % kAhead];
             if (k >= kAhead && !wait(sh.passed[k % kAhead], k / kAhead - 1)) break;
@@ -566,8 +498,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
                     if (q0 + u * kMaxThreads < hi) v[u] = __ldcg(xa + q0 + u * kMaxThreads);
 #pragma unroll
                 for (int u = 0; u < kMaxLoads; ++u)
-                    if (q0 + u * kMaxThreads < hi)
-                        m = more_max(m, v[u]);
+                    if (q0 + u * kMaxThreads < hi) m = more_max(m, v[u]);
             }
             // the elements before and after those granules
             const int head = h ? 4 - h : 0, tail = 4 * hi - h;
@@ -600,16 +531,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
             bool ok = true;
             for (int64_t row = blockIdx.x; row < A.rows && ok; row += gridDim.x) {
                 const float *x = start_of(row);
-                const int h = shift_of(x), nch = (V + h + 3) / 4;
-                for (int q = 0; q < nch; q += kSeg, ++seg) {
+                const int h = shift_of(x), nch = (V + h + 3) / 4, groups = (V + 3) / 4;
+                for (int q = 0; q < groups; q += kSeg, ++seg) {
                     const int at = seg % kRing;
                     if (seg >= kRing &&
-                        !mbar_wait_suspended_or_abort(bar(sh.freed[at]), (seg / kRing - 1) & 1u, abort)) {
+                        !mbar_wait_or_abort(bar(sh.freed[at]), (seg / kRing - 1) & 1u, abort)) {
                         ok = false;
                         break;
                     }
-                    fence_async_shared();    // the exps written there come before the copy
-                    load_granules(sh.ring[at] - q, x - h, q, min(nch, q + kSeg), &sh.loaded[at]);
+                    fence_async_shared();
+                    load_granules(sh.ring[at] - q, x - h, q, min(nch, q + kSeg + 1),
+                                  &sh.loaded[at]);
                 }
             }
         }
@@ -618,36 +550,36 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
         for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, ++k) {
             RowState &R = sh.row[k & 1];
             const float *x = start_of(row);
-            const int h = shift_of(x);
             const Asked asked = ask(A, row, x);
             if (!wait(sh.done[k & 1], k / 2)) break;
-            float T = 0.0f;
-            for (int i = 0; i < 4; ++i) {
-                float v[8];
-#pragma unroll
-                for (int w = 0; w < 8; ++w) {
-                    const int g = 256 * i + 32 * w + lane;
-                    const float4 c = R.T[g], c1 = R.T[(g + 1) & (kSweep - 1)];
-                    const float4 f = h == 0   ? c
-                                     : h == 1 ? group_of<1>(c, c1)
-                                     : h == 2 ? group_of<2>(c, c1)
-                                              : group_of<3>(c, c1);
-                    v[w] = __fadd_rn(__fadd_rn(__fadd_rn(f.x, f.y), f.z), f.w);
-                }
-                const float t = __shfl_sync(0xffffffffu, butterfly8(v, lane), lane_of_row(lane & 7));
-                if (lane >> 3 == i) T = t;
-            }
-            T = warp_butterfly_sum(T);
+            const float T = warp_butterfly_sum(R.tsum[lane]);
             const float *t = R.red;
             const float S =
                 __fadd_rn(__fadd_rn(__fadd_rn(t[0], t[1]), __fadd_rn(t[2], t[3])),
                           __fadd_rn(__fadd_rn(t[4], t[5]), __fadd_rn(t[6], t[7])));
-            const float m = sh.max[k % kAhead].m;
+            const float m = sh.max[k % kAhead].m, bound = sh.max[k % kAhead].bound;
             uint64_t rank = 0;
-            if (A.top_k > 0)
-                rank = R.listed > kListed || !(fabsf(m) <= 0x1.fffffep127f)
-                           ? top_by_rounds(x, V, A.top_k, lane)
-                           : rank_list(R.list, R.listed, A.top_k, R.top, lane);
+            if (A.top_k > 0) {
+                // the elements of the listed groups, then their order
+                int n = 0;
+                const bool all = R.listed <= kFound && fabsf(m) <= 0x1.fffffep127f;
+                for (int c0 = 0; all && c0 < R.listed; c0 += 32) {
+                    const bool in = c0 + lane < R.listed;
+                    const float4 v = in ? R.found[c0 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const int j0 = in ? R.found_at[c0 + lane] : 0;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const bool is = in && comp(v, c) >= bound && j0 + c < V;
+                        const unsigned who = __ballot_sync(0xffffffffu, is);
+                        const int at = n + __popc(who & ((1u << lane) - 1u));
+                        if (is && at < kListed) R.list[at] = rank_of(comp(v, c), j0 + c);
+                        n += __popc(who);
+                    }
+                }
+                __syncwarp();
+                rank = !all || n > kListed ? top_by_rounds(x, V, A.top_k, lane)
+                                           : rank_list(R.list, n, A.top_k, R.top, lane);
+            }
             write_row(A, row, asked, m, S, T, rank, lane);
             __syncwarp();
             if (lane == 0) R.listed = 0;
