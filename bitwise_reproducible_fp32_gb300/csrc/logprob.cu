@@ -14,18 +14,22 @@
 // Forward, rows of more than 4096 logits: one persistent CTA an SM, its warps in
 // roles that follow one another down the rows, so that the max of one row and the
 // exps and sums of the row before run at the same time:
-//   max    6 warps read a row straight from global memory (it stays in L2): its
-//          max and the maxima of 32 groups of threads, up to three rows ahead
+//   max    8 warps read a row straight from global memory (it stays in L2): its
+//          max and the maxima of 32 groups of threads, ahead of the sums
 //   load   a lane brings the rows a second time, from L2, in segments of 4096
 //          elements through a ring in shared memory
-//   sum    8 warps, thread l the profile's chain l: four groups of 4 elements at a
-//          time, straight-line, for enough independent work on few warps: e, the
-//          chain of S, T's 16 chains of the thread, and a list of the groups that
-//          may hold alternatives
+//   sum    8 warps, thread l the profile's chain l: groups of 4 elements two at a
+//          time, straight-line, step by step over both: e, the chain of S, T's 16
+//          chains of the thread, and a list of the groups that may hold alternatives
 //   final  a warp folds the totals, ranks the list and writes the row's results
-// They meet at mbarriers only, every wait bounded. us for 8192 x 50257 with 5
-// alternatives: whole rows staged and gone through phase by phase by all warps
-// 874; 16 warps of exps handing e to 8 warps of chains through shared memory 668.
+// Two teams of load, sum and final warps take every other row. They meet at
+// mbarriers only, every wait bounded. us for 8192 x 50257 / 16384 x 16000 /
+// 2720 x 151936 with 5 alternatives: 585 / 369 / 529 (2.8, 2.8, 3.1 TB/s); one
+// team, four groups at a time 576 / 410 / 564; 16 warps of exps handing e to 8
+// warps of chains through shared memory 668 / 582 / 501; whole rows staged and
+// gone through phase by phase by all warps 874 / 788 / 846. Both roles are busy
+// nearly all of the time: the sums by issue and the latency between their steps,
+// the max by the latency of its loads.
 // Rows of at most 4096 logits: a warp a row, each chain of T one element.
 // The alternatives: with t the top_k-th largest of 32 group maxima, at least
 // top_k elements are >= t, and few more; they are listed while the exps are
@@ -50,14 +54,19 @@ namespace {
 constexpr int kTChains = 4096;
 constexpr int kTBlock = 16384;          // elements
 constexpr int kSeg = kTChains / 4;      // groups of a segment: T's chains once
-constexpr int kRing = 8;                // segments in shared memory
-constexpr int kSumWarps = kXentLanes / 32, kMaxWarps = 6;
+constexpr int kTeams = 2;               // teams of sum warps, a row each
+constexpr int kRing = 3;                // segments of a team in shared memory
+constexpr int kSumWarps = kXentLanes / 32, kMaxWarps = 8;
 constexpr int kMaxThreads = kMaxWarps * 32;
-constexpr int kWarps = kSumWarps + kMaxWarps + 2;
+constexpr int kFirstMax = kTeams * kSumWarps, kFirstLoad = kFirstMax + kMaxWarps;
+constexpr int kFirstFinal = kFirstLoad + kTeams, kWarps = kFirstFinal + kTeams;
 constexpr int kStreamThreads = kWarps * 32;
 constexpr int kSets = kSeg / kXentLanes;     // groups a thread has in a segment
 constexpr int kMaxLoads = 8;            // granules a max thread reads at once
-constexpr int kAhead = 3;               // rows whose max may wait for its exps
+// Rows between the start of the max and the results. A team waits on every other
+// use of a max slot only; the use between is of a row before the team's last one,
+// so it is over by then.
+constexpr int kAhead = 3;
 constexpr int kFound = 256, kListed = 512;    // granules, elements that may be alternatives
 constexpr int kSmallVocab = kTChains;   // a warp a row up to here
 constexpr int kSmallWarps = 8, kSmallListed = 128;
@@ -241,40 +250,67 @@ __device__ __forceinline__ uint64_t rank_list(const uint64_t *list, int n, int t
     return lane < top_k ? top[lane] : 0;
 }
 
-// e = exp(x - m) for the 4 elements of a granule and T's fmaf on their chains,
-// for a finite m, without branches: exp4's bits where the returned value, the
-// least n = rint(d log2 e) plus kRoundMagic, is at least kFast; below (and at
-// -inf) both are formed again by exp_slow from the old t. n sits in the low bits
-// of tm, so p 2^n is p's bits plus tm's shifted up.
+// e = exp(x - m) for N groups of 4 elements and T's fmaf on their chains, for a
+// finite m, without branches and step by step over all of them, so that each
+// instruction finds 2N independent ones around it. exp4's bits where the returned
+// value, the least n = rint(d log2 e) plus kRoundMagic, is at least kFast; below
+// (and at -inf) both are formed again by exp_slow from the old t. n sits in the
+// low bits of tm, so p 2^n is p's bits plus tm's shifted up.
 constexpr float kFast = kRoundMagic - 125.0f;
-__device__ __forceinline__ float exp_and_t(float4 v, f32x2 m2, float4 &e, float4 &t) {
-    const f32x2 d01 = sub2(pack2(v.x, v.y), m2), d23 = sub2(pack2(v.z, v.w), m2);
+template <int N>
+__device__ __forceinline__ float exp_and_t(const float4 (&v)[N], f32x2 m2, float4 (&e)[N],
+                                           float4 (&t)[N]) {
+    f32x2 d[2 * N], tm[2 * N], p[2 * N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        d[2 * i] = sub2(pack2(v[i].x, v[i].y), m2);
+        d[2 * i + 1] = sub2(pack2(v[i].z, v[i].w), m2);
+    }
     // d log2 e rounded on its own: a fused step with -0 (which changes no product),
     // as a packed multiply that feeds a packed add rounds as if fused with it
-    const f32x2 magic = splat2(kRoundMagic), l2e = splat2(kLog2e), none = splat2(-0.0f);
-    const f32x2 tm01 = add2(fma2(d01, l2e, none), magic), tm23 = add2(fma2(d23, l2e, none), magic);
-    const f32x2 n01 = sub2(tm01, magic), n23 = sub2(tm23, magic);
-    const f32x2 hi = splat2(-kLn2Hi), lo = splat2(-kLn2Lo);
-    const f32x2 r01 = fma2(n01, lo, fma2(n01, hi, d01)), r23 = fma2(n23, lo, fma2(n23, hi, d23));
-    f32x2 p01 = fma2(splat2(kC7), r01, splat2(kC6)), p23 = fma2(splat2(kC7), r23, splat2(kC6));
-    p01 = fma2(p01, r01, splat2(kC5)); p23 = fma2(p23, r23, splat2(kC5));
-    p01 = fma2(p01, r01, splat2(kC4)); p23 = fma2(p23, r23, splat2(kC4));
-    p01 = fma2(p01, r01, splat2(kC3)); p23 = fma2(p23, r23, splat2(kC3));
-    p01 = fma2(p01, r01, splat2(kC2)); p23 = fma2(p23, r23, splat2(kC2));
-    p01 = fma2(p01, r01, splat2(1.0f)); p23 = fma2(p23, r23, splat2(1.0f));
-    p01 = fma2(p01, r01, splat2(1.0f)); p23 = fma2(p23, r23, splat2(1.0f));
-    float a0, a1, a2, a3, q0, q1, q2, q3;
-    unpack2(tm01, a0, a1);
-    unpack2(tm23, a2, a3);
-    unpack2(p01, q0, q1);
-    unpack2(p23, q2, q3);
-    auto scaled = [](float p, float tm) {
-        return __int_as_float(__float_as_int(p) + int(__float_as_uint(tm) << 23));
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) tm[i] = fma2(d[i], splat2(kLog2e), splat2(-0.0f));
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) tm[i] = add2(tm[i], splat2(kRoundMagic));
+    f32x2 n[2 * N], r[2 * N];
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) n[i] = sub2(tm[i], splat2(kRoundMagic));
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) r[i] = fma2(n[i], splat2(-kLn2Hi), d[i]);
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) r[i] = fma2(n[i], splat2(-kLn2Lo), r[i]);
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) p[i] = fma2(splat2(kC7), r[i], splat2(kC6));
+    auto step = [&](float c) {
+#pragma unroll
+        for (int i = 0; i < 2 * N; ++i) p[i] = fma2(p[i], r[i], splat2(c));
     };
-    e = make_float4(scaled(q0, a0), scaled(q1, a1), scaled(q2, a2), scaled(q3, a3));
-    unpack2(fma2(pack2(e.x, e.y), d01, pack2(t.x, t.y)), t.x, t.y);
-    unpack2(fma2(pack2(e.z, e.w), d23, pack2(t.z, t.w)), t.z, t.w);
-    return min4(a0, a1, a2, a3);
+    step(kC5);
+    step(kC4);
+    step(kC3);
+    step(kC2);
+    step(1.0f);
+    step(1.0f);
+    float least = kInf;
+    auto scaled = [](float q, float a) {
+        return __int_as_float(__float_as_int(q) + int(__float_as_uint(a) << 23));
+    };
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float a0, a1, a2, a3, q0, q1, q2, q3;
+        unpack2(tm[2 * i], a0, a1);
+        unpack2(tm[2 * i + 1], a2, a3);
+        unpack2(p[2 * i], q0, q1);
+        unpack2(p[2 * i + 1], q2, q3);
+        least = fminf(least, min4(a0, a1, a2, a3));
+        e[i] = make_float4(scaled(q0, a0), scaled(q1, a1), scaled(q2, a2), scaled(q3, a3));
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        unpack2(fma2(pack2(e[i].x, e[i].y), d[2 * i], pack2(t[i].x, t[i].y)), t[i].x, t[i].y);
+        unpack2(fma2(pack2(e[i].z, e[i].w), d[2 * i + 1], pack2(t[i].z, t[i].w)), t[i].z, t[i].w);
+    }
+    return least;
 }
 
 // The general form of it, for any m: elements with e == 0 leave T alone. e in
@@ -307,107 +343,119 @@ struct RowMax {                         // of the rows 0 .. kAhead - 1 mod kAhea
     float parts[kMaxWarps][32];         // the max threads' own maxima
     float m, bound, pad[2];
 };
-struct Stream {
+struct Team {
     float4 ring[kRing][kSeg + 1];       // a segment and the granule after it
+    float4 T[kSets][kXentLanes];        // each thread's chains over the blocks so far
     RowState row[2];
+    uint64_t loaded[kRing], freed[kRing], done[2], taken[2];
+};
+struct Stream {
+    Team team[kTeams];
     RowMax max[kAhead];
-    uint64_t loaded[kRing], freed[kRing];
-    uint64_t parted[kAhead], maxed[kAhead], passed[kAhead], done[2], taken[2];
+    uint64_t parted[kAhead], maxed[kAhead], passed[kAhead];
     int abort;
 };
-static_assert(sizeof(RowState) % 16 == 0 && sizeof(RowMax) % 16 == 0 &&
-                  offsetof(Stream, row) % 16 == 0 && offsetof(Stream, max) % 16 == 0 &&
-                  offsetof(Stream, loaded) % 8 == 0 && sizeof(Stream) <= 227 * 1024,
+static_assert(sizeof(RowState) % 16 == 0 && sizeof(RowMax) % 16 == 0 && sizeof(Team) % 16 == 0 &&
+                  offsetof(Team, T) % 16 == 0 && offsetof(Team, row) % 16 == 0 &&
+                  offsetof(Team, loaded) % 8 == 0 && offsetof(Stream, max) % 16 == 0 &&
+                  offsetof(Stream, parted) % 8 == 0 && sizeof(Stream) <= 227 * 1024,
               "16-byte reads, 8-byte barriers");
-
-__device__ __forceinline__ void fence_async_shared() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 
 // A thread's chain of S over one row, its groups l + 256 i of the segments, and its
 // chains of T: 4 sums in fours. H: the row's misalignment. wait(segment number)
 // and freed(segment number) are the ring's barriers; false when a wait gave up.
 struct RowSums { float S, u[kSets]; };
 template <int H, class Wait, class Freed>
-__device__ __forceinline__ bool sum_row(Stream &sh, RowState &R, int V, float m, float bound,
+__device__ __forceinline__ bool sum_row(Team &team, RowState &R, int V, float m, float bound,
                                         uint32_t &seg, Wait wait, Freed freed, RowSums &out) {
-    const int l = threadIdx.x, ns = (V + 4 * kSeg - 1) / (4 * kSeg);
+    constexpr int kPair = 2;                 // sets taken at once
+    const int l = threadIdx.x % kXentLanes, ns = (V + 4 * kSeg - 1) / (4 * kSeg);
     const bool finite_m = fabsf(m) <= 0x1.fffffep127f;
     const f32x2 m2 = splat2(m);
     float S = 0.0f;
-    float4 t[kSets], all[kSets];             // T of the current block, and in all
+    float4 t[kSets];                         // T of the current block
 #pragma unroll
-    for (int u = 0; u < kSets; ++u) t[u] = all[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto flush = [&]() {
-#pragma unroll
-        for (int u = 0; u < kSets; ++u) {
-            all[u] = make_float4(__fadd_rn(all[u].x, t[u].x), __fadd_rn(all[u].y, t[u].y),
-                                 __fadd_rn(all[u].z, t[u].z), __fadd_rn(all[u].w, t[u].w));
-            t[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+    for (int u = 0; u < kSets; ++u) t[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool fresh = true;                       // team.T holds nothing of this row
+    auto flush = [&](int u) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!fresh) a = team.T[u][l];
+        a = make_float4(__fadd_rn(a.x, t[u].x), __fadd_rn(a.y, t[u].y), __fadd_rn(a.z, t[u].z),
+                        __fadd_rn(a.w, t[u].w));
+        t[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        return a;
     };
     for (int s = 0; s < ns; ++s, ++seg) {
         if (!wait(seg)) return false;
-        const uint32_t at = smem_u32(sh.ring[seg % kRing]) + 16u * l;
-        if (s > 0 && s % (kTBlock / kTChains) == 0) flush();
+        const uint32_t at = smem_u32(team.ring[seg % kRing]) + 16u * l;
+        if (s > 0 && s % (kTBlock / kTChains) == 0) {
+#pragma unroll
+            for (int u = 0; u < kSets; ++u) team.T[u][l] = flush(u);
+            fresh = false;
+        }
         const bool tail = 4 * kSeg * (s + 1) > V;
         const int j0 = 4 * (s * kSeg + l);
-        float4 v[kSets], e[kSets], old[kSets];
-        float least = kInf, most = -kInf;
 #pragma unroll
-        for (int u = 0; u < kSets; ++u) {
-            const float4 c0 = lds4(at + 16u * kXentLanes * u);
-            const float4 c1 = H ? lds4(at + 16u * kXentLanes * u + 16u) : c0;
-            v[u] = group_of<H>(c0, c1);
-            if (tail) {                      // past the row's end: as m, and e = 0 below
-                const int j = j0 + 4 * kXentLanes * u;
-                if (j >= V) v[u].x = m;
-                if (j + 1 >= V) v[u].y = m;
-                if (j + 2 >= V) v[u].z = m;
-                if (j + 3 >= V) v[u].w = m;
+        for (int u0 = 0; u0 < kSets; u0 += kPair) {
+            float4 v[kPair], e[kPair], tn[kPair];
+            float most = -kInf;
+#pragma unroll
+            for (int i = 0; i < kPair; ++i) {
+                const uint32_t here = at + 16u * kXentLanes * (u0 + i);
+                const float4 c0 = lds4(here), c1 = H ? lds4(here + 16u) : c0;
+                v[i] = group_of<H>(c0, c1);
+                if (tail) {                  // past the row's end: as m, and e = 0 below
+                    const int j = j0 + 4 * kXentLanes * (u0 + i);
+                    if (j >= V) v[i].x = m;
+                    if (j + 1 >= V) v[i].y = m;
+                    if (j + 2 >= V) v[i].z = m;
+                    if (j + 3 >= V) v[i].w = m;
+                }
+                most = fmaxf(most, max4(v[i]));
+                tn[i] = t[u0 + i];
             }
-            most = fmaxf(most, max4(v[u]));
-            old[u] = t[u];
-            least = fminf(least, exp_and_t(v[u], m2, e[u], t[u]));
-        }
-        if (!(least >= kFast) || !finite_m) {
+            const float least = exp_and_t<kPair>(v, m2, e, tn);
+            if (!(least >= kFast) || !finite_m) {
 #pragma unroll
-            for (int u = 0; u < kSets; ++u) {
-                const ExpT x = exp_slow(v[u], m, old[u]);
-                e[u] = x.e;
-                t[u] = x.t;
+                for (int i = 0; i < kPair; ++i) {
+                    const ExpT x = exp_slow(v[i], m, t[u0 + i]);
+                    e[i] = x.e;
+                    tn[i] = x.t;
+                }
             }
-        }
-        if (tail) {
 #pragma unroll
-            for (int u = 0; u < kSets; ++u) {
-                const int j = j0 + 4 * kXentLanes * u;
-                if (j >= V) e[u].x = 0.0f;
-                if (j + 1 >= V) e[u].y = 0.0f;
-                if (j + 2 >= V) e[u].z = 0.0f;
-                if (j + 3 >= V) e[u].w = 0.0f;
+            for (int i = 0; i < kPair; ++i) {
+                t[u0 + i] = tn[i];
+                if (tail) {
+                    const int j = j0 + 4 * kXentLanes * (u0 + i);
+                    if (j >= V) e[i].x = 0.0f;
+                    if (j + 1 >= V) e[i].y = 0.0f;
+                    if (j + 2 >= V) e[i].z = 0.0f;
+                    if (j + 3 >= V) e[i].w = 0.0f;
+                }
+                S = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(S, e[i].x), e[i].y), e[i].z), e[i].w);
             }
-        }
+            if (most >= bound)
 #pragma unroll
-        for (int u = 0; u < kSets; ++u)
-            S = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(S, e[u].x), e[u].y), e[u].z), e[u].w);
-        if (most >= bound)
-#pragma unroll
-            for (int u = 0; u < kSets; ++u)
-                if (max4(v[u]) >= bound && j0 + 4 * kXentLanes * u < V) {
-                    const int slot = atomicAdd(&R.listed, 1);
-                    if (slot < kFound) {
-                        R.found[slot] = v[u];
-                        R.found_at[slot] = j0 + 4 * kXentLanes * u;
+                for (int i = 0; i < kPair; ++i) {
+                    const int j = j0 + 4 * kXentLanes * (u0 + i);
+                    if (max4(v[i]) >= bound && j < V) {
+                        const int slot = atomicAdd(&R.listed, 1);
+                        if (slot < kFound) {
+                            R.found[slot] = v[i];
+                            R.found_at[slot] = j;
+                        }
                     }
                 }
+        }
         freed(seg);
     }
-    flush();
     out.S = S;
 #pragma unroll
-    for (int u = 0; u < kSets; ++u)
-        out.u[u] = __fadd_rn(__fadd_rn(__fadd_rn(all[u].x, all[u].y), all[u].z), all[u].w);
+    for (int u = 0; u < kSets; ++u) {
+        const float4 a = flush(u);
+        out.u[u] = __fadd_rn(__fadd_rn(__fadd_rn(a.x, a.y), a.z), a.w);
+    }
     return true;
 }
 
@@ -417,19 +465,21 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = A.V;
     auto bar = [](uint64_t &b) { return smem_u32(&b); };
     if (tid == 0) {
-        for (int i = 0; i < kRing; ++i) {
-            mbar_init(bar(sh.loaded[i]), 1);
-            mbar_init(bar(sh.freed[i]), kSumWarps);
+        for (Team &t : sh.team) {
+            for (int i = 0; i < kRing; ++i) {
+                mbar_init(bar(t.loaded[i]), 1);
+                mbar_init(bar(t.freed[i]), kSumWarps);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(bar(t.done[i]), kSumWarps);
+                mbar_init(bar(t.taken[i]), 1);
+                t.row[i].listed = 0;
+            }
         }
         for (int i = 0; i < kAhead; ++i) {
             mbar_init(bar(sh.parted[i]), kMaxWarps);
             mbar_init(bar(sh.maxed[i]), 1);
             mbar_init(bar(sh.passed[i]), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(sh.done[i]), kSumWarps);
-            mbar_init(bar(sh.taken[i]), 1);
-            sh.row[i].listed = 0;
         }
         sh.abort = 0;
         fence_mbar_init();
@@ -448,37 +498,43 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
     auto shift_of = [](const float *x) {
         return int((reinterpret_cast<uintptr_t>(x) >> 2) & 3);
     };
+    // a team's rows are every kTeams-th of the CTA's: row number k of them is the
+    // CTA's row kTeams * k + the team's number
+    const int64_t step = gridDim.x * int64_t(kTeams);
     uint32_t k = 0, seg = 0;            // rows and segments done so far
-    if (warp < kSumWarps) {
+    if (warp < kFirstMax) {
         // ---- e, S, T, the list
-        auto loaded = [&](uint32_t i) { return wait(sh.loaded[i % kRing], i / kRing); };
-        auto freed = [&](uint32_t i) { arrive(sh.freed[i % kRing]); };
-        for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, ++k) {
-            RowState &R = sh.row[k & 1];
-            if (!wait(sh.maxed[k % kAhead], k / kAhead)) break;
-            if (k >= 2 && !wait(sh.taken[k & 1], k / 2 - 1)) break;
-            const float m = sh.max[k % kAhead].m, bound = sh.max[k % kAhead].bound;
+        const int ti = warp / kSumWarps, w8 = warp % kSumWarps;
+        Team &team = sh.team[ti];
+        auto loaded = [&](uint32_t i) { return wait(team.loaded[i % kRing], i / kRing); };
+        auto freed = [&](uint32_t i) { arrive(team.freed[i % kRing]); };
+        for (int64_t row = blockIdx.x + ti * int64_t(gridDim.x); row < A.rows; row += step, ++k) {
+            RowState &R = team.row[k & 1];
+            const uint32_t r = kTeams * k + ti;
+            if (!wait(sh.maxed[r % kAhead], r / kAhead)) break;
+            if (k >= 2 && !wait(team.taken[k & 1], k / 2 - 1)) break;
+            const float m = sh.max[r % kAhead].m, bound = sh.max[r % kAhead].bound;
             RowSums o;
             bool ok;
             switch (shift_of(start_of(row))) {
-                case 0: ok = sum_row<0>(sh, R, V, m, bound, seg, loaded, freed, o); break;
-                case 1: ok = sum_row<1>(sh, R, V, m, bound, seg, loaded, freed, o); break;
-                case 2: ok = sum_row<2>(sh, R, V, m, bound, seg, loaded, freed, o); break;
-                default: ok = sum_row<3>(sh, R, V, m, bound, seg, loaded, freed, o); break;
+                case 0: ok = sum_row<0>(team, R, V, m, bound, seg, loaded, freed, o); break;
+                case 1: ok = sum_row<1>(team, R, V, m, bound, seg, loaded, freed, o); break;
+                case 2: ok = sum_row<2>(team, R, V, m, bound, seg, loaded, freed, o); break;
+                default: ok = sum_row<3>(team, R, V, m, bound, seg, loaded, freed, o); break;
             }
             if (!ok) break;
             // the first level of the folds: 32 chains of S, 32 sums in fours of T
             float v[8] = {o.S, o.u[0], o.u[1], o.u[2], o.u[3], 0.0f, 0.0f, 0.0f};
             const float f = butterfly8(v, lane);
-            if (lane == lane_of_row(0)) R.red[warp] = f;
+            if (lane == lane_of_row(0)) R.red[w8] = f;
 #pragma unroll
             for (int u = 0; u < kSets; ++u)
-                if (lane == lane_of_row(u + 1)) R.tsum[kSumWarps * u + warp] = f;
-            arrive(sh.done[k & 1]);
+                if (lane == lane_of_row(u + 1)) R.tsum[kSumWarps * u + w8] = f;
+            arrive(team.done[k & 1]);
         }
-    } else if (warp < kSumWarps + kMaxWarps) {
+    } else if (warp < kFirstLoad) {
         // ---- the max, and the 32 groups' (the lanes of the same number)
-        const int mw = warp - kSumWarps, mt = mw * 32 + lane;
+        const int mw = warp - kFirstMax, mt = mw * 32 + lane;
         for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, ++k) {
             RowMax &R = sh.max[k % kAhead];
             if (k >= kAhead && !wait(sh.passed[k % kAhead], k / kAhead - 1)) break;
@@ -525,39 +581,43 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
                 arrive(sh.maxed[k % kAhead]);
             }
         }
-    } else if (warp == kWarps - 2) {
+    } else if (warp < kFirstFinal) {
         // ---- the loads
+        Team &team = sh.team[warp - kFirstLoad];
         if (lane == 0) {
             bool ok = true;
-            for (int64_t row = blockIdx.x; row < A.rows && ok; row += gridDim.x) {
+            for (int64_t row = blockIdx.x + (warp - kFirstLoad) * int64_t(gridDim.x);
+                 row < A.rows && ok; row += step) {
                 const float *x = start_of(row);
                 const int h = shift_of(x), nch = (V + h + 3) / 4, groups = (V + 3) / 4;
                 for (int q = 0; q < groups; q += kSeg, ++seg) {
                     const int at = seg % kRing;
                     if (seg >= kRing &&
-                        !mbar_wait_or_abort(bar(sh.freed[at]), (seg / kRing - 1) & 1u, abort)) {
+                        !mbar_wait_or_abort(bar(team.freed[at]), (seg / kRing - 1) & 1u, abort)) {
                         ok = false;
                         break;
                     }
-                    fence_async_shared();
-                    load_granules(sh.ring[at] - q, x - h, q, min(nch, q + kSeg + 1),
-                                  &sh.loaded[at]);
+                    load_granules(team.ring[at] - q, x - h, q, min(nch, q + kSeg + 1),
+                                  &team.loaded[at]);
                 }
             }
         }
     } else {
         // ---- the results
-        for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, ++k) {
-            RowState &R = sh.row[k & 1];
+        const int ti = warp - kFirstFinal;
+        Team &team = sh.team[ti];
+        for (int64_t row = blockIdx.x + ti * int64_t(gridDim.x); row < A.rows; row += step, ++k) {
+            RowState &R = team.row[k & 1];
+            const uint32_t r = kTeams * k + ti;
             const float *x = start_of(row);
             const Asked asked = ask(A, row, x);
-            if (!wait(sh.done[k & 1], k / 2)) break;
+            if (!wait(team.done[k & 1], k / 2)) break;
             const float T = warp_butterfly_sum(R.tsum[lane]);
             const float *t = R.red;
             const float S =
                 __fadd_rn(__fadd_rn(__fadd_rn(t[0], t[1]), __fadd_rn(t[2], t[3])),
                           __fadd_rn(__fadd_rn(t[4], t[5]), __fadd_rn(t[6], t[7])));
-            const float m = sh.max[k % kAhead].m, bound = sh.max[k % kAhead].bound;
+            const float m = sh.max[r % kAhead].m, bound = sh.max[r % kAhead].bound;
             uint64_t rank = 0;
             if (A.top_k > 0) {
                 // the elements of the listed groups, then their order
@@ -583,15 +643,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
             write_row(A, row, asked, m, S, T, rank, lane);
             __syncwarp();
             if (lane == 0) R.listed = 0;
-            arrive(sh.taken[k & 1]);
-            arrive(sh.passed[k % kAhead]);
+            arrive(team.taken[k & 1]);
+            arrive(sh.passed[r % kAhead]);
         }
     }
     __syncthreads();
-    if (sh.abort && warp == kWarps - 2 && lane == 0) {     // let the copies in flight land
+    if (sh.abort && warp >= kFirstLoad && warp < kFirstFinal && lane == 0) {
+        // let the copies in flight land
         atomicOr(&g_logprob_watchdog, kWatchdogLogprob);
+        Team &team = sh.team[warp - kFirstLoad];
         for (uint32_t i = seg > uint32_t(kRing) ? seg - kRing : 0; i < seg; ++i)
-            (void)mbar_wait_bounded(bar(sh.loaded[i % kRing]), (i / kRing) & 1u);
+            (void)mbar_wait_bounded(bar(team.loaded[i % kRing]), (i / kRing) & 1u);
     }
 }
 
@@ -673,28 +735,37 @@ __global__ void __launch_bounds__(kSmallWarps * 32, ONE ? 2 : 3) logprob_small_k
             }
             float u[8];                      // T's sums in fours
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const int j = 4 * (g0 + 32 * w + lane);
-                float4 t = make_float4(0.f, 0.f, 0.f, 0.f), e = t;
-                if (4 * (g0 + 32 * w) < V) {
-                    const float least = exp_and_t(v[w], m2, e, t);
-                    if (!(least >= kFast) || !finite_m) {
-                        const ExpT x2 = exp_slow(v[w], m, make_float4(0.f, 0.f, 0.f, 0.f));
-                        e = x2.e;
-                        t = x2.t;
-                        if (!finite_m) {     // past the end -inf - m need not be 0
-                            if (j >= V) { e.x = 0.0f; t.x = 0.0f; }
-                            if (j + 1 >= V) { e.y = 0.0f; t.y = 0.0f; }
-                            if (j + 2 >= V) { e.z = 0.0f; t.z = 0.0f; }
-                            if (j + 3 >= V) { e.w = 0.0f; t.w = 0.0f; }
+            for (int w0 = 0; w0 < 8; w0 += 2) {
+                float4 es[2], ts[2], vs[2] = {v[w0], v[w0 + 1]};
+                ts[0] = ts[1] = es[0] = es[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (4 * (g0 + 32 * w0) < V) {
+                    const float least = exp_and_t<2>(vs, m2, es, ts);
+                    if (!(least >= kFast) || !finite_m)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int j = 4 * (g0 + 32 * (w0 + i) + lane);
+                            const ExpT x2 =
+                                exp_slow(vs[i], m, make_float4(0.f, 0.f, 0.f, 0.f));
+                            es[i] = x2.e;
+                            ts[i] = x2.t;
+                            if (!finite_m) {     // past the end -inf - m need not be -inf
+                                if (j >= V) es[i].x = ts[i].x = 0.0f;
+                                if (j + 1 >= V) es[i].y = ts[i].y = 0.0f;
+                                if (j + 2 >= V) es[i].z = ts[i].z = 0.0f;
+                                if (j + 3 >= V) es[i].w = ts[i].w = 0.0f;
+                            }
                         }
-                    }
                 }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                const int w = w0 + i;
+                const float4 e = es[i], t = ts[i];
                 s[w] = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(s[w], e.x), e.y), e.z), e.w);
                 // each chain's one block, added to +0
                 u[w] = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(t.x, 0.0f), __fadd_rn(t.y, 0.0f)),
                                            __fadd_rn(t.z, 0.0f)),
                                  __fadd_rn(t.w, 0.0f));
+                }
             }
             const float t = __shfl_sync(0xffffffffu, butterfly8(u, lane), lane_of_row(lane & 7));
             if (lane >> 3 == g0 / kXentLanes) T = t;
