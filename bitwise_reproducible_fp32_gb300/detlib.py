@@ -826,58 +826,97 @@ def detadamw_f32(p, g, m, v, lr, beta1, beta2, eps, weight_decay, step,
 
 
 # ---------------------------------------------------------------- generation
-def _here(first, *rest):
-    """Every tensor lies on the current device, where the call runs."""
-    import torch
-    dev = torch.cuda.current_device()
-    if first.device.index != dev or any(t is not None and t.device.index != dev for t in rest):
-        raise ValueError(f"tensors must be on the current device, cuda:{dev}")
+# A generation step makes these calls once a layer on a few rows, where the time
+# a call takes on the host is what counts. So their checks look at each property
+# once, by the cheapest way torch has, and the names they need are looked up at
+# the first call.
+class _Names:
+    ready = False
+
+    @classmethod
+    def look_up(cls):
+        import torch
+        cls.i32, cls.i64, cls.f32 = torch.int32, torch.int64, torch.float32
+        cls.empty = torch.empty
+        cls.stream_scope = torch.cuda.stream
+        cls.device = torch.cuda.current_device
+        cls.raw_stream = lambda dev: torch.cuda.current_stream().cuda_stream
+        # the same two without the Python around them, where torch has them
+        cls.device = getattr(torch._C, "_cuda_getDevice", cls.device)
+        cls.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", cls.raw_stream)
+        cls.ready = True
 
 
-def _empty(shape, like, stream, dtype=None):
+_N = _Names
+_default_profile = None
+
+
+def _gen_begin(profile, first, name):
+    """(library, profile, current device) of a generation call whose first tensor
+    is `first`."""
+    global _default_profile
+    if not _N.ready:
+        _N.look_up()
+    if not getattr(first, "is_cuda", False):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if profile is None:
+        if _default_profile is None:
+            _default_profile = ctypes.pointer(det_profile_default())
+        profile = _default_profile
+    else:
+        profile = ctypes.byref(profile)
+    return _lib if _lib is not None else load(), profile, _N.device()
+
+
+def _gen_stream(stream, dev):
+    return _N.raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _gen_empty(shape, like, stream, dtype=None):
     """A tensor for this call's outputs, allocated for the stream it runs on."""
-    import torch
-    dtype = torch.float32 if dtype is None else dtype
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+    with _N.stream_scope(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _cuda_int(t, name, dtype, n=None):
-    """A contiguous 1-D CUDA tensor of dtype (of n elements where given)."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or t.dtype != dtype:
+def _at(t, name, dtype, dev):
+    """t's data pointer, if it is a tensor of dtype on the current device."""
+    if not getattr(t, "is_cuda", False) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device, cuda:{dev}")
+    return t.data_ptr()
+
+
+def _vec(t, name, dtype, dev, n=None):
+    """As _at, for a contiguous 1-D tensor (of n values)."""
+    p = _at(t, name, dtype, dev)
     if t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be 1-D and contiguous")
     if n is not None and t.numel() != n:
         raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
-    return t
+    return p
 
 
-def _cuda_rows(t, name, dtype, rows=None, cols=None):
-    """A 2-D CUDA tensor of dtype with contiguous rows (of the given shape)."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or t.dtype != dtype:
-        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
-    if t.dim() != 2 or (t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with contiguous rows")
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must be {rows} x {cols}, got {tuple(t.shape)}")
-    return t
+def _mat(t, name, dtype, dev, rows=None, cols=None):
+    """(pointer, row stride) as _at, for a 2-D tensor with contiguous rows, `rows`
+    of them of at least `cols`."""
+    p = _at(t, name, dtype, dev)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    n, m = t.size(0), t.size(1)
+    if m > 1 and n > 0 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if (rows is not None and n != rows) or (cols is not None and m < cols):
+        raise ValueError(f"{name} must be {rows if rows is not None else n} rows of at least "
+                         f"{cols} columns, got {n} x {m}")
+    # a single row has no stride to speak of: its length
+    return p, (t.stride(0) if n > 1 else max(m, 1))
 
 
-def _row_stride(t):
-    # a single row has no stride to speak of: report its length
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
-
-
-def _status_word(t):
-    import torch
-    if t is not None:
-        _cuda_int(t, "dev_status", torch.int32, 1)
-    return t
+def _word(t, dev):
+    return None if t is None else _vec(t, "dev_status", _N.i32, dev, 1)
 
 
 def rope_turns(rot_dim, theta=10000.0, factor=1.0, low=None, high=None, trained=None,
@@ -912,19 +951,19 @@ def rope_turns(rot_dim, theta=10000.0, factor=1.0, low=None, high=None, trained=
     return torch.from_numpy(turns.view(np.int64)).to(device)
 
 
-def _rotary(head_dim, theta, turns, rot_dim, half):
-    import torch
+def _rotary(head_dim, theta, turns, rot_dim, half, dev):
+    p = None
     if turns is not None:
-        _cuda_int(turns, "turns", torch.int64)
+        p = _vec(turns, "turns", _N.i64, dev)
         if rot_dim is None:
             rot_dim = 2 * turns.numel()
-        if turns.numel() != rot_dim // 2:
+        if turns.numel() * 2 != rot_dim:
             raise ValueError(f"turns must hold {rot_dim // 2} values")
     elif rot_dim is None:
         rot_dim = head_dim
     if rot_dim % 2 or not 2 <= rot_dim <= head_dim:
         raise ValueError(f"rot_dim must be even, 2..{head_dim}")
-    return Rotary(rot_dim, int(bool(half)), theta, turns.data_ptr() if turns is not None else None)
+    return Rotary(rot_dim, 1 if half else 0, theta, p)
 
 
 def detrope_at_f32(x, positions, heads, head_dim, theta=10000.0, turns=None, rot_dim=None,
@@ -935,45 +974,40 @@ def detrope_at_f32(x, positions, heads, head_dim, theta=10000.0, turns=None, rot
     rope_turns (rot_dim defaults to all of them); None: theta, the bits of
     detrope_f32. half: pairs (i, i + rot_dim / 2) instead of (2i, 2i+1). inverse:
     the backward (dx from dy). Returns out."""
-    import torch
-    _cuda_rows(x, "x", torch.float32)
-    rows, width = x.shape[0], heads * head_dim
-    _cuda_int(positions, "positions", torch.int32, rows)
-    ro = _rotary(head_dim, theta, turns, rot_dim, half)
-    if x.shape[1] < width:
-        raise ValueError(f"x must have at least {width} columns")
+    lib, prof, dev = _gen_begin(profile, x, "x")
+    width = heads * head_dim
+    xp, ldx = _mat(x, "x", _N.f32, dev, None, width)
+    rows = x.size(0)
+    pp = _vec(positions, "positions", _N.i32, dev, rows)
+    ro = _rotary(head_dim, theta, turns, rot_dim, half, dev)
     if out is None:
-        out = _empty((rows, width), x, stream)
-    _cuda_rows(out, "out", torch.float32)
-    if out.shape[0] != rows or out.shape[1] < width:
-        raise ValueError(f"out must be {rows} rows of at least {width} columns")
-    _here(x, positions, turns, out)
-    _check("detrope_at_f32",
-           load().detrope_at_f32(_prof(profile), rows, heads, head_dim, x.data_ptr(),
-                                 _row_stride(x), positions.data_ptr(), ctypes.byref(ro),
-                                 int(bool(inverse)), out.data_ptr(), _row_stride(out),
-                                 _stream(stream)))
+        out = _gen_empty((rows, width), x, stream)
+        op, ldo = out.data_ptr(), width
+    else:
+        op, ldo = _mat(out, "out", _N.f32, dev, rows, width)
+    st = lib.detrope_at_f32(prof, rows, heads, head_dim, xp, ldx, pp, ro, 1 if inverse else 0, op,
+                            ldo, _gen_stream(stream, dev))
+    if st:
+        _check("detrope_at_f32", st)
     return out
 
 
-def _kv_cache(k_cache, v_cache):
-    import torch
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if t.dtype != torch.float32:
-            raise TypeError(f"{name} must be float32 (the profile is FP32 only), got {t.dtype}")
-        if t.dim() != 4 or t.numel() == 0:
-            raise ValueError(f"{name} must be pages x page_size x kv_heads x head_dim")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+def _kv_cache(k_cache, v_cache, dev):
+    kp, vp = _at(k_cache, "k_cache", _N.f32, dev), _at(v_cache, "v_cache", _N.f32, dev)
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or k_cache.numel() == 0:
+        raise ValueError("k_cache must be pages x page_size x kv_heads x head_dim")
+    if v_cache.shape != shape or v_cache.stride() != strides:
         raise ValueError("k_cache and v_cache must agree in shape and strides")
-    P, ps, G, d = k_cache.shape
-    sp, stok, sh, sd = k_cache.stride()
-    if d > 1 and sd != 1:
+    P, ps, G, d = shape
+    sp, stok, sh, sd = strides
+    if sd != 1 and d > 1:
         raise ValueError("the cache's last dimension must be contiguous")
-    # a dimension of one entry has no stride to speak of
-    sp, stok, sh = (s if n > 1 else (d + 3) // 4 * 4 for s, n in ((sp, P), (stok, ps), (sh, G)))
-    return KVCache(k_cache.data_ptr(), v_cache.data_ptr(), P, ps, G, d, sp, stok, sh)
+    if P == 1 or ps == 1 or G == 1:
+        # a dimension of one entry has no stride to speak of
+        pad = (d + 3) // 4 * 4
+        sp, stok, sh = (s if n > 1 else pad for s, n in ((sp, P), (stok, ps), (sh, G)))
+    return KVCache(kp, vp, P, ps, G, d, sp, stok, sh)
 
 
 def detkv_append_f32(qkv, slots, k_cache, v_cache, heads, positions=None, theta=10000.0,
@@ -987,35 +1021,27 @@ def detkv_append_f32(qkv, slots, k_cache, v_cache, heads, positions=None, theta=
     q_out, by default the Q block of qkv itself; None: K is stored as it is and Q
     stays. Rows that share a slot: the last one is kept. Returns q_out (None
     without positions)."""
-    import torch
-    c = _kv_cache(k_cache, v_cache)
-    _cuda_rows(qkv, "qkv", torch.float32)
-    rows = qkv.shape[0]
-    if qkv.shape[1] < (heads + 2 * c.kv_heads) * c.head_dim:
-        raise ValueError(f"qkv must have {(heads + 2 * c.kv_heads) * c.head_dim} columns")
-    _cuda_int(slots, "slots", torch.int64, rows)
-    ro = None
+    lib, prof, dev = _gen_begin(profile, qkv, "qkv")
+    c = _kv_cache(k_cache, v_cache, dev)
+    d = c.head_dim
+    xp, ldx = _mat(qkv, "qkv", _N.f32, dev, None, (heads + 2 * c.kv_heads) * d)
+    rows = qkv.size(0)
+    sp = _vec(slots, "slots", _N.i64, dev, rows)
+    ro, pp, qp, ldq = None, None, None, 0
     if positions is not None:
-        _cuda_int(positions, "positions", torch.int32, rows)
-        ro = _rotary(c.head_dim, theta, turns, rot_dim, half)
-        width = heads * c.head_dim
+        pp = _vec(positions, "positions", _N.i32, dev, rows)
+        ro = _rotary(d, theta, turns, rot_dim, half, dev)
         if q_out is None:
-            q_out = qkv
-        _cuda_rows(q_out, "q_out", torch.float32)
-        if q_out.shape[0] != rows or q_out.shape[1] < width:
-            raise ValueError(f"q_out must be {rows} rows of at least {width} columns")
+            qp, ldq, q_out = xp, ldx, qkv[:, :heads * d]
+        else:
+            qp, ldq = _mat(q_out, "q_out", _N.f32, dev, rows, heads * d)
     elif turns is not None or q_out is not None:
         raise ValueError("turns and q_out need positions")
-    _status_word(dev_status)
-    _here(qkv, slots, k_cache, v_cache, positions, turns, q_out, dev_status)
-    _check("detkv_append_f32",
-           load().detkv_append_f32(_prof(profile), rows, heads, qkv.data_ptr(),
-                                   _row_stride(qkv), slots.data_ptr(), _ptr(positions),
-                                   ctypes.byref(ro) if ro is not None else None,
-                                   ctypes.byref(c), _ptr(q_out),
-                                   _row_stride(q_out) if q_out is not None else 0,
-                                   _ptr(dev_status), _stream(stream)))
-    return q_out[:, :heads * c.head_dim] if q_out is qkv else q_out
+    st = lib.detkv_append_f32(prof, rows, heads, xp, ldx, sp, pp, ro, c, qp, ldq,
+                              _word(dev_status, dev), _gen_stream(stream, dev))
+    if st:
+        _check("detkv_append_f32", st)
+    return q_out
 
 
 def detpages_extend(lens, new_tokens, table, free_pages, free_count, page_size, max_rows,
@@ -1030,34 +1056,38 @@ def detpages_extend(lens, new_tokens, table, free_pages, free_count, page_size, 
     of the max_rows rows its position (int32) and slot (int64), -1 where there is
     none. A request that cannot have all its tokens gets none (dev_status bits: 1
     a length or count out of range, 2 out of pages, 4 past max_rows)."""
-    import torch
-    i32 = torch.int32
+    lib, prof, dev = _gen_begin(profile, lens, "lens")
+    i32 = _N.i32
+    lp = _vec(lens, "lens", i32, dev)
     batch = lens.numel()
-    _cuda_int(lens, "lens", i32)
-    _cuda_int(new_tokens, "new_tokens", i32, batch)
-    _cuda_rows(table, "table", i32)
-    if table.shape[0] != batch:
-        raise ValueError(f"table must have {batch} rows")
-    _cuda_int(free_pages, "free_pages", i32)
-    _cuda_int(free_count, "free_count", i32, 1)
-    new = lambda t, name, n, dt: (_cuda_int(t, name, dt, n) if t is not None  # noqa: E731
-                                  else _empty((n,), lens, stream, dt))
-    lens_out = new(lens_out, "lens_out", batch, i32)
-    free_count_out = new(free_count_out, "free_count_out", 1, i32)
-    row_start = new(row_start, "row_start", batch + 1, i32)
-    positions = new(positions, "positions", max_rows, i32)
-    slots = new(slots, "slots", max_rows, torch.int64)
-    _status_word(dev_status)
-    _here(lens, new_tokens, table, free_pages, free_count, lens_out, free_count_out, row_start,
-          positions, slots, dev_status)
-    _check("detpages_extend",
-           load().detpages_extend(_prof(profile), batch, page_size, lens.data_ptr(),
-                                  new_tokens.data_ptr(), table.data_ptr(), table.shape[1],
-                                  _row_stride(table), free_pages.data_ptr(), free_pages.numel(),
-                                  free_count.data_ptr(), max_rows, lens_out.data_ptr(),
-                                  free_count_out.data_ptr(), row_start.data_ptr(),
-                                  positions.data_ptr(), slots.data_ptr(), _ptr(dev_status),
-                                  _stream(stream)))
+    np_ = _vec(new_tokens, "new_tokens", i32, dev, batch)
+    tp, ldt = _mat(table, "table", i32, dev, batch)
+    fp = _vec(free_pages, "free_pages", i32, dev)
+    cp = _vec(free_count, "free_count", i32, dev, 1)
+    if lens_out is None and free_count_out is None and row_start is None and positions is None:
+        # one allocation for the four
+        lens_out, free_count_out, row_start, positions = _gen_empty(
+            (2 * batch + 2 + max_rows,), lens, stream).split((batch, 1, batch + 1, max_rows))
+    if lens_out is None:
+        lens_out = _gen_empty((batch,), lens, stream)
+    if free_count_out is None:
+        free_count_out = _gen_empty((1,), lens, stream)
+    if row_start is None:
+        row_start = _gen_empty((batch + 1,), lens, stream)
+    if positions is None:
+        positions = _gen_empty((max_rows,), lens, stream)
+    if slots is None:
+        slots = _gen_empty((max_rows,), lens, stream, _N.i64)
+    st = lib.detpages_extend(prof, batch, page_size, lp, np_, tp, table.size(1), ldt, fp,
+                             free_pages.numel(), cp, max_rows,
+                             _vec(lens_out, "lens_out", i32, dev, batch),
+                             _vec(free_count_out, "free_count_out", i32, dev, 1),
+                             _vec(row_start, "row_start", i32, dev, batch + 1),
+                             _vec(positions, "positions", i32, dev, max_rows),
+                             _vec(slots, "slots", _N.i64, dev, max_rows),
+                             _word(dev_status, dev), _gen_stream(stream, dev))
+    if st:
+        _check("detpages_extend", st)
     return lens_out, free_count_out, row_start, positions, slots
 
 
@@ -1067,29 +1097,25 @@ def detpages_release(lens, done, table, free_pages, free_count, page_size, lens_
     free_pages, from free_count[0] on. Returns (lens_out, free_count_out), the
     lengths (0 for those) and the count after. dev_status bits: 1 a length out of
     range, 2 the free list is full."""
-    import torch
-    i32 = torch.int32
+    lib, prof, dev = _gen_begin(profile, lens, "lens")
+    i32 = _N.i32
+    lp = _vec(lens, "lens", i32, dev)
     batch = lens.numel()
-    _cuda_int(lens, "lens", i32)
-    _cuda_int(done, "done", i32, batch)
-    _cuda_rows(table, "table", i32)
-    if table.shape[0] != batch:
-        raise ValueError(f"table must have {batch} rows")
-    _cuda_int(free_pages, "free_pages", i32)
-    _cuda_int(free_count, "free_count", i32, 1)
-    lens_out = (_empty((batch,), lens, stream, i32) if lens_out is None
-                else _cuda_int(lens_out, "lens_out", i32, batch))
-    free_count_out = (_empty((1,), lens, stream, i32) if free_count_out is None
-                      else _cuda_int(free_count_out, "free_count_out", i32, 1))
-    _status_word(dev_status)
-    _here(lens, done, table, free_pages, free_count, lens_out, free_count_out, dev_status)
-    _check("detpages_release",
-           load().detpages_release(_prof(profile), batch, page_size, lens.data_ptr(),
-                                   done.data_ptr(), table.data_ptr(), table.shape[1],
-                                   _row_stride(table), free_pages.data_ptr(),
-                                   free_pages.numel(), free_count.data_ptr(),
-                                   lens_out.data_ptr(), free_count_out.data_ptr(),
-                                   _ptr(dev_status), _stream(stream)))
+    dp = _vec(done, "done", i32, dev, batch)
+    tp, ldt = _mat(table, "table", i32, dev, batch)
+    fp = _vec(free_pages, "free_pages", i32, dev)
+    cp = _vec(free_count, "free_count", i32, dev, 1)
+    if lens_out is None:
+        lens_out = _gen_empty((batch,), lens, stream)
+    if free_count_out is None:
+        free_count_out = _gen_empty((1,), lens, stream)
+    st = lib.detpages_release(prof, batch, page_size, lp, dp, tp, table.size(1), ldt, fp,
+                              free_pages.numel(), cp,
+                              _vec(lens_out, "lens_out", i32, dev, batch),
+                              _vec(free_count_out, "free_count_out", i32, dev, 1),
+                              _word(dev_status, dev), _gen_stream(stream, dev))
+    if st:
+        _check("detpages_release", st)
     return lens_out, free_count_out
 
 
@@ -1111,41 +1137,38 @@ def detdecode_attention_f32(q, k_cache, v_cache, table, kv_lens, heads, scale=No
     those tokens; a length of 0 gives 0. dev_status bits: 1 a length out of range,
     2 a page out of range (the row is NaN). Returns out (requests x heads *
     head_dim)."""
-    import torch
-    c = _kv_cache(k_cache, v_cache)
-    _cuda_rows(q, "q", torch.float32)
-    batch, width = q.shape[0], heads * c.head_dim
-    if q.shape[1] < width:
-        raise ValueError(f"q must have at least {width} columns")
-    _cuda_rows(table, "table", torch.int32)
-    if table.shape[0] != batch:
-        raise ValueError(f"table must have {batch} rows")
-    _cuda_int(kv_lens, "kv_lens", torch.int32, batch)
+    lib, prof, dev = _gen_begin(profile, q, "q")
+    c = _kv_cache(k_cache, v_cache, dev)
+    d = c.head_dim
+    width = heads * d
+    qp, ldq = _mat(q, "q", _N.f32, dev, None, width)
+    batch = q.size(0)
+    tp, ldt = _mat(table, "table", _N.i32, dev, batch)
+    lp = _vec(kv_lens, "kv_lens", _N.i32, dev, batch)
     if out is None:
-        out = _empty((batch, width), q, stream)
-    _cuda_rows(out, "out", torch.float32)
-    if out.shape[0] != batch or out.shape[1] < width:
-        raise ValueError(f"out must be {batch} rows of at least {width} columns")
-    if scale is None:
-        scale = 1.0 / float(c.head_dim) ** 0.5
-    max_pages = table.shape[1]
-    if workspace is None:
-        need = detdecode_attention_workspace_bytes(batch, heads, c.kv_heads, c.head_dim,
-                                                   max_pages * c.page_size, profile)
-        if need:
-            workspace = _empty(((need + 3) // 4,), q, stream)
+        out = _gen_empty((batch, width), q, stream)
+        op, ldo = out.data_ptr(), width
     else:
-        _cuda_f32(workspace, "workspace", 1)
-    _status_word(dev_status)
-    _here(q, k_cache, v_cache, table, kv_lens, out, workspace, dev_status)
-    _check("detdecode_attention_f32",
-           load().detdecode_attention_f32(_prof(profile), batch, heads, q.data_ptr(),
-                                          _row_stride(q), ctypes.byref(c), table.data_ptr(),
-                                          max_pages, _row_stride(table), kv_lens.data_ptr(),
-                                          scale, out.data_ptr(), _row_stride(out),
-                                          _ptr(workspace),
-                                          workspace.numel() * 4 if workspace is not None else 0,
-                                          _ptr(dev_status), _stream(stream)))
+        op, ldo = _mat(out, "out", _N.f32, dev, batch, width)
+    if scale is None:
+        scale = 1.0 / float(d) ** 0.5
+    max_pages = table.size(1)
+    wp, wn = None, 0
+    if workspace is None:
+        need = ctypes.c_size_t(0)
+        st = lib.detdecode_attention_workspace_bytes(prof, batch, heads, c.kv_heads, d,
+                                                     max_pages * c.page_size, need)
+        if st:
+            _check("detdecode_attention_workspace_bytes", st)
+        if need.value:
+            workspace = _gen_empty(((need.value + 3) // 4,), q, stream)
+    if workspace is not None:
+        wp, wn = _vec(workspace, "workspace", _N.f32, dev), workspace.numel() * 4
+    st = lib.detdecode_attention_f32(prof, batch, heads, qp, ldq, c, tp, max_pages, ldt, lp, scale,
+                                     op, ldo, wp, wn, _word(dev_status, dev),
+                                     _gen_stream(stream, dev))
+    if st:
+        _check("detdecode_attention_f32", st)
     return out
 
 
@@ -1157,31 +1180,38 @@ def detlogprob_f32(logits, tokens, top_k=0, want_stats=True, logp=None, entropy=
     Returns (logp, entropy, top_ids, top_logp, stats): rows, rows, rows x top_k
     int32 and float, and the rows x 4 floats that detlogprob_bwd_f32 reads (None
     unless want_stats)."""
-    import torch
-    f32 = torch.float32
-    _cuda_rows(logits, "logits", f32)
-    rows, V = logits.shape
-    _cuda_int(tokens, "tokens", torch.int32, rows)
-    logp = _empty((rows,), logits, stream) if logp is None else _cuda_f32(logp, "logp", 1)
-    entropy = (_empty((rows,), logits, stream) if entropy is None
-               else _cuda_f32(entropy, "entropy", 1))
+    lib, prof, dev = _gen_begin(profile, logits, "logits")
+    f32, i32 = _N.f32, _N.i32
+    xp, ld = _mat(logits, "logits", f32, dev)
+    rows, V = logits.size(0), logits.size(1)
+    yp = _vec(tokens, "tokens", i32, dev, rows)
+    if logp is None and entropy is None:
+        logp, entropy = _gen_empty((2, rows), logits, stream).unbind(0)
+    if logp is None:
+        logp = _gen_empty((rows,), logits, stream)
+    if entropy is None:
+        entropy = _gen_empty((rows,), logits, stream)
     if stats is None and want_stats:
-        stats = _empty((rows, 4), logits, stream)
-    top_ids = (_empty((rows, top_k), logits, stream, torch.int32) if top_ids is None else top_ids)
-    top_logp = _empty((rows, top_k), logits, stream) if top_logp is None else top_logp
-    if logp.numel() != rows or entropy.numel() != rows:
-        raise ValueError(f"logp and entropy must hold {rows} values")
-    for t, name, dt, n in ((stats, "stats", f32, 4), (top_ids, "top_ids", torch.int32, top_k),
-                           (top_logp, "top_logp", f32, top_k)):
-        if t is not None and not _cuda_rows(t, name, dt, rows, n).is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    _status_word(dev_status)
-    _here(logits, tokens, logp, entropy, stats, top_ids, top_logp, dev_status)
-    _check("detlogprob_f32",
-           load().detlogprob_f32(_prof(profile), rows, V, logits.data_ptr(), _row_stride(logits),
-                                 tokens.data_ptr(), top_k, logp.data_ptr(), entropy.data_ptr(),
-                                 _ptr(stats), top_ids.data_ptr(), top_logp.data_ptr(),
-                                 _ptr(dev_status), _stream(stream)))
+        stats = _gen_empty((rows, 4), logits, stream)
+    if top_ids is None:
+        top_ids = _gen_empty((rows, top_k), logits, stream, i32)
+    if top_logp is None:
+        top_logp = _gen_empty((rows, top_k), logits, stream)
+    sp = None
+    if stats is not None:
+        sp, _ = _mat(stats, "stats", f32, dev, rows, 4)
+        if stats.size(1) != 4 or not stats.is_contiguous():
+            raise ValueError("stats must be contiguous rows of 4")
+    ip, _ = _mat(top_ids, "top_ids", i32, dev, rows, top_k)
+    tp, _ = _mat(top_logp, "top_logp", f32, dev, rows, top_k)
+    if (top_ids.size(1) != top_k or top_logp.size(1) != top_k
+            or not (top_ids.is_contiguous() and top_logp.is_contiguous())):
+        raise ValueError(f"top_ids and top_logp must be contiguous rows of {top_k}")
+    st = lib.detlogprob_f32(prof, rows, V, xp, ld, yp, top_k, _vec(logp, "logp", f32, dev, rows),
+                            _vec(entropy, "entropy", f32, dev, rows), sp, ip, tp,
+                            _word(dev_status, dev), _gen_stream(stream, dev))
+    if st:
+        _check("detlogprob_f32", st)
     return logp, entropy, top_ids, top_logp, stats
 
 
@@ -1190,24 +1220,25 @@ def detlogprob_bwd_f32(logits, tokens, stats, dlogp, dentropy=None, dlogits=None
     """The gradient of sum(dlogp * logp) + sum(dentropy * entropy) with respect to
     the logits, from detlogprob_f32's stats. dlogits may be the logits (in place).
     Returns dlogits."""
-    import torch
-    f32 = torch.float32
-    _cuda_rows(logits, "logits", f32)
-    rows, V = logits.shape
-    _cuda_int(tokens, "tokens", torch.int32, rows)
-    if not _cuda_rows(stats, "stats", f32, rows, 4).is_contiguous():
-        raise ValueError("stats must be contiguous")
-    for t, name in ((dlogp, "dlogp"), (dentropy, "dentropy")):
-        if t is not None and _cuda_f32(t, name, 1).numel() != rows:
-            raise ValueError(f"{name} must hold {rows} values")
-    dlogits = _empty((rows, V), logits, stream) if dlogits is None else dlogits
-    _cuda_rows(dlogits, "dlogits", f32, rows, V)
-    _here(logits, tokens, stats, dlogp, dentropy, dlogits)
-    _check("detlogprob_bwd_f32",
-           load().detlogprob_bwd_f32(_prof(profile), rows, V, logits.data_ptr(),
-                                     _row_stride(logits), tokens.data_ptr(), stats.data_ptr(),
-                                     dlogp.data_ptr(), _ptr(dentropy), dlogits.data_ptr(),
-                                     _row_stride(dlogits), _stream(stream)))
+    lib, prof, dev = _gen_begin(profile, logits, "logits")
+    f32 = _N.f32
+    xp, ld = _mat(logits, "logits", f32, dev)
+    rows, V = logits.size(0), logits.size(1)
+    yp = _vec(tokens, "tokens", _N.i32, dev, rows)
+    sp, _ = _mat(stats, "stats", f32, dev, rows, 4)
+    if stats.size(1) != 4 or not stats.is_contiguous():
+        raise ValueError("stats must be contiguous rows of 4")
+    gp = _vec(dlogp, "dlogp", f32, dev, rows)
+    hp = None if dentropy is None else _vec(dentropy, "dentropy", f32, dev, rows)
+    if dlogits is None:
+        dlogits = _gen_empty((rows, V), logits, stream)
+    dp, ldd = _mat(dlogits, "dlogits", f32, dev, rows, V)
+    if dlogits.size(1) != V:
+        raise ValueError(f"dlogits must have {V} columns")
+    st = lib.detlogprob_bwd_f32(prof, rows, V, xp, ld, yp, sp, gp, hp, dp, ldd,
+                                _gen_stream(stream, dev))
+    if st:
+        _check("detlogprob_bwd_f32", st)
     return dlogits
 
 
