@@ -1067,7 +1067,8 @@ def detpages_extend(lens, new_tokens, table, free_pages, free_count, page_size, 
     if lens_out is None and free_count_out is None and row_start is None and positions is None:
         # one allocation for the four
         lens_out, free_count_out, row_start, positions = _gen_empty(
-            (2 * batch + 2 + max_rows,), lens, stream).split((batch, 1, batch + 1, max_rows))
+            (2 * batch + 2 + max_rows,), lens, stream).unsafe_split_with_sizes(
+                (batch, 1, batch + 1, max_rows))
     if lens_out is None:
         lens_out = _gen_empty((batch,), lens, stream)
     if free_count_out is None:
