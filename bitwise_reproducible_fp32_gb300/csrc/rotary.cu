@@ -8,8 +8,13 @@
 // owns one unit of a row -- 16 bytes of a head: two interleaved pairs, or four
 // pairs of the half layout (two 16-byte pieces) -- and walks the heads of a
 // group, kBatch loads in flight, so an angle's sin and cos are formed once a
-// group and not once a head. Rows with other alignments or odd sizes take units
-// of one pair (or one element where nothing turns).
+// group and not once a head; the first batch is on its way while they are. Rows
+// with other alignments or odd sizes take units of one pair (or one element where
+// nothing turns).
+// Measured in a graph, inputs beyond L2: 8192 rows of 24 heads of 64 turned in
+// 14.9 us (6.8 TB/s); the backward of 4099 rows of 40 heads of 128, half of each
+// turned, 34 us (4.9 TB/s); 8192 rows of 32 + 2 x 8 heads of 128, 7/8 of them
+// kept, appended in 70 us (5.0 TB/s).
 #include <algorithm>
 
 #include "det_internal.cuh"
@@ -60,7 +65,7 @@ struct Unit {
     int at0, at1;       // offsets of the pieces in a head (at1: the partner's)
     bool turns;
 
-    __device__ __forceinline__ Unit(const Angles &a, float log_theta, int u, int pos) {
+    __device__ __forceinline__ Unit(const Angles &a, int u, int pos) {
         const int nturn = a.rot / (2 * kPairs);
         turns = u < nturn && pos >= 0;
         if (u >= nturn) {
@@ -76,10 +81,13 @@ struct Unit {
             at0 = a.half ? u : 2 * u;
             at1 = a.half ? a.rot / 2 + u : 2 * u + 1;
         }
-        if (turns)
+    }
+    __device__ __forceinline__ void angles(const Angles &a, int u, int pos) {
+        if (!turns) return;
+        const float log_theta = a.turns ? 0.0f : det_log(a.theta);
 #pragma unroll
-            for (int k = 0; k < kPairs; ++k)
-                pair_sincos(a, log_theta, pos, u * kPairs + k, sn[k], cs[k]);
+        for (int k = 0; k < kPairs; ++k)
+            pair_sincos(a, log_theta, pos, u * kPairs + k, sn[k], cs[k]);
     }
 };
 
@@ -143,16 +151,21 @@ __global__ void __launch_bounds__(256)
     const int64_t t = e / units;
     if (t >= rows) return;
     const int pos = positions[t];
-    const Unit<MODE> u(ang, ang.turns ? 0.0f : det_log(ang.theta), int(e - t * units), pos);
+    Unit<MODE> u(ang, int(e - t * units), pos);
     if (!u.turns && out == x) return;
     const int h0 = blockIdx.y * group, h1 = min(heads, h0 + group);
     const float *src = x + t * ldx;
     float *dst = out + t * ldo;
-    for (int h = h0; h < h1; h += kBatch) {
-        typename PieceOf<MODE>::type p[kBatch];
+    typename PieceOf<MODE>::type p[kBatch];
+    auto load = [&](int h) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
             if (h + k < h1) p[k] = load_unit<MODE>(src + int64_t(h + k) * head_dim, u);
+    };
+    load(h0);
+    u.angles(ang, int(e - t * units), pos);
+    for (int h = h0; h < h1; h += kBatch) {
+        if (h > h0) load(h);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
             if (h + k < h1) {
@@ -178,59 +191,80 @@ struct AppendArgs {
 };
 
 constexpr int kAppendTile = 16;
+constexpr int kScan = 8;          // slots a thread has in flight
+constexpr int kFilterBits = 4096;
 
 // A CTA takes `tile` rows and a group of the row's heads (Q, then K, then V;
 // grid.y), a thread one unit of one row. Where a later row names the same slot,
 // the earlier row's K and V are not written, so the cache always holds the last
-// one: each CTA with K or V heads looks through the slots after its rows.
+// one: each CTA with K or V heads looks through the slots after its rows, most of
+// which a bit filter of its own slots' low bits passes over at once (comparing
+// each with the tile's 16: 63 us instead of 32 for 8192 rows of 36 heads of 64).
+// Four CTAs an SM: with more registers for loads over the search, 96 us instead of
+// 70 for the 8192 rows above.
 template <int MODE>
-__global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs A, Angles ang) {
+__global__ void __launch_bounds__(256, 4) kv_append_kernel(AppendArgs A, Angles ang) {
     __shared__ int64_t slot_of[kAppendTile];
-    __shared__ int later[kAppendTile];
+    __shared__ int later[kAppendTile], pos_of[kAppendTile];
+    __shared__ unsigned filter[kFilterBits / 32];
     const int tid = threadIdx.x;
     const int64_t row0 = int64_t(blockIdx.x) * A.tile;
     const int all = A.heads + 2 * A.kv_heads;
     const int first = A.q_out ? 0 : A.heads;
     const int h0 = first + blockIdx.y * A.group, h1 = min(all, h0 + A.group);
+    for (int i = tid; i < kFilterBits / 32; i += blockDim.x) filter[i] = 0;
+    __syncthreads();
     if (tid < A.tile) {
         slot_of[tid] = row0 + tid < A.rows ? A.slots[row0 + tid] : -1;
+        pos_of[tid] = row0 + tid < A.rows && A.positions ? A.positions[row0 + tid] : 0;
         later[tid] = 0;
+        const unsigned b = unsigned(slot_of[tid]) % kFilterBits;
+        if (slot_of[tid] >= 0) atomicOr(&filter[b / 32], 1u << b % 32);
         if (blockIdx.y == 0 && slot_of[tid] >= A.nslots && A.dev_status &&
-            (!A.positions || A.positions[row0 + tid] >= 0))
+            pos_of[tid] >= 0)
             atomicOr(reinterpret_cast<int *>(A.dev_status), 1);
     }
     __syncthreads();
     if (h1 > A.heads) {
-        for (int64_t j = row0 + 1 + tid; j < A.rows; j += blockDim.x) {
-            const int64_t s = A.slots[j];
-            if (s >= 0)
-                for (int r = 0; r < A.tile; ++r)
-                    if (s == slot_of[r] && j > row0 + r &&
+        for (int64_t j0 = row0 + 1 + tid; j0 < A.rows; j0 += kScan * blockDim.x) {
+            int64_t s[kScan];
+#pragma unroll
+            for (int k = 0; k < kScan; ++k) {
+                const int64_t j = j0 + k * blockDim.x;
+                s[k] = j < A.rows ? A.slots[j] : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < kScan; ++k) {
+                const unsigned b = unsigned(s[k]) % kFilterBits;
+                if (!(filter[b / 32] >> (b % 32) & 1)) continue;
+                const int64_t j = j0 + k * blockDim.x;
+                for (int i = 0; i < A.tile; ++i)
+                    if (s[k] >= 0 && s[k] == slot_of[i] && j > row0 + i &&
                         (!A.positions || A.positions[j] >= 0))
-                        later[r] = 1;
+                        later[i] = 1;
+            }
         }
         __syncthreads();
     }
-    const int r = tid / A.units;
+    const int r = tid / A.units, unit = tid - r * A.units;
     const int64_t t = row0 + r;
-    if (r >= A.tile || t >= A.rows) return;
-    const int64_t slot = slot_of[r];
-    if (slot < 0 || slot >= A.nslots) return;
-    int pos = -1;
-    if (A.positions) {
-        pos = A.positions[t];
-        if (pos < 0) return;
-    }
-    const Unit<MODE> u(ang, pos < 0 || ang.turns ? 0.0f : det_log(ang.theta), tid - r * A.units,
-                       pos);
+    const int64_t slot = r < A.tile ? slot_of[r] : -1;
+    if (slot < 0 || slot >= A.nslots || pos_of[r] < 0) return;
+    const int pos = A.positions ? pos_of[r] : -1;
+    Unit<MODE> u(ang, unit, pos);
     const float *src = A.qkv + t * A.ldqkv;
-    const int64_t at = (slot / A.page_size) * A.page_stride + (slot % A.page_size) * A.token_stride;
-    const bool keep = !later[r];
-    for (int h = h0; h < h1; h += kBatch) {
-        typename PieceOf<MODE>::type p[kBatch];
+    typename PieceOf<MODE>::type p[kBatch];
+    auto load = [&](int h) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
             if (h + k < h1) p[k] = load_unit<MODE>(src + int64_t(h + k) * A.head_dim, u);
+    };
+    load(h0);
+    u.angles(ang, unit, pos);
+    const int64_t at = (slot / A.page_size) * A.page_stride + (slot % A.page_size) * A.token_stride;
+    const bool keep = !later[r];
+    for (int h = h0; h < h1; h += kBatch) {
+        if (h > h0) load(h);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int hh = h + k;
@@ -262,12 +296,16 @@ int units_of(UnitMode m, int head_dim, int rot) {
     return rot / (2 * pairs) + (head_dim - rot) / wide;
 }
 
-// Heads a thread walks: all of them where the rows alone fill the GPU (each
-// angle is formed once), fewer, down to one batch of loads, where they do not.
+// Heads a thread walks: as many as leave the GPU one full load of threads, in
+// equal groups of whole batches. Fewer heads form each angle more often (8192
+// rows of 32 + 16 heads of 128 appended: 16 heads 70 us, 4 heads 85), more leave
+// SMs idle (64 rows of 36 heads of 64: 4 heads 5.2 us, 48 heads 9.8) or the last
+// group short (4099 rows of 40 heads turned: 12 heads 34 us, 16 heads 37).
 int head_group(int64_t threads, int heads) {
     const int64_t full = int64_t(sm_count_current_device()) * 2048;
-    const int64_t want = (heads * threads + full - 1) / full;
-    return int(std::min<int64_t>(heads, (std::max<int64_t>(want, 1) + kBatch - 1) / kBatch * kBatch));
+    const int64_t want = std::max<int64_t>((heads * threads + full - 1) / full, 1);
+    const int64_t groups = (heads + want - 1) / want, even = (heads + groups - 1) / groups;
+    return int(std::min<int64_t>(heads, (even + kBatch - 1) / kBatch * kBatch));
 }
 
 }  // namespace
