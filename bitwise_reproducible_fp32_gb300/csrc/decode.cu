@@ -51,6 +51,7 @@ constexpr int kTokens = 64;                 // of a piece, 32 dimensions each
 constexpr int kPieceBytes = kTokens * 128;
 constexpr int kMaxHeads = 8;
 constexpr int kMaxCluster = 16;
+constexpr int kDeep = 4;                    // groups of a chain of S in flight
 constexpr int kPageCache = 512;             // page ids of a CTA kept on chip
 enum Loader { kTma, kCopy16, kCopy4 };
 constexpr unsigned kWatchdogDecode = 32u;   // det_watchdog_status bit 5
@@ -429,46 +430,50 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         m[h] = F.top[0][h];
         for (int r = 1; r < C; ++r) m[h] = max_nan(m[h], F.top[r][h]);
     }
-    // ---- e in place (slots past t1 hold anything and are never added)
-    const int quads = (t1 - t0 + 3) >> 2;
+    // ---- e in place of x, and the chains of S: a warp 32 chains of a head, which
+    // it walks through the cluster's runs kDeep groups at a time (slots past n
+    // hold anything and are not added); the total goes to every CTA
+    for (int i = warp * C + rank; i < nh * 8; i += C * kWarps) {
+        const int h = i >> 3, l = (i & 7) * 32 + lane;
+        float top = m[0];
 #pragma unroll
-    for (int h = 0; h < NH; ++h) {
-        if (h >= nh) break;
-        float4 *x4 = reinterpret_cast<float4 *>(xs + h * xs_ld);
-        if (fabsf(m[h]) <= 0x1.fffffep127f) {
-            for (int i = tid; i < quads; i += kThreads) x4[i] = exp4(x4[i], m[h]);
-        } else {
-            for (int i = tid; i < quads; i += kThreads) {
-                const float4 v = x4[i];
-                x4[i] = make_float4(
-                    det_exp_call(__fsub_rn(v.x, m[h])), det_exp_call(__fsub_rn(v.y, m[h])),
-                    det_exp_call(__fsub_rn(v.z, m[h])), det_exp_call(__fsub_rn(v.w, m[h])));
+        for (int k = 1; k < NH; ++k) top = h == k ? m[k] : top;
+        const bool finite = fabsf(top) <= 0x1.fffffep127f;
+        float sum = 0.0f;
+        for (int t = 4 * l; t < n; t += 1024 * kDeep) {
+            float4 *at[kDeep], e[kDeep];
+#pragma unroll
+            for (int u = 0; u < kDeep; ++u) {
+                const int tu = t + 1024 * u;
+                if (tu >= n) break;
+                int r = 0, c = tu >> 8;           // the chunk's CTA, its place there
+                if (C > 1) {
+                    const int longer = rem * (base + 1);
+                    r = c < longer ? c / (base + 1) : rem + (c - longer) / base;
+                    c -= first_chunk(r);
+                }
+                at[u] = reinterpret_cast<float4 *>(scores_of(r) + h * xs_ld + c * kKChunk +
+                                                   (tu & 255));
+                e[u] = *at[u];
+            }
+#pragma unroll
+            for (int u = 0; u < kDeep; ++u) {
+                const int tu = t + 1024 * u;
+                if (tu >= n) break;
+                const float4 x = e[u];
+                e[u] = finite ? exp4(x, top)
+                              : make_float4(det_exp_call(__fsub_rn(x.x, top)),
+                                            det_exp_call(__fsub_rn(x.y, top)),
+                                            det_exp_call(__fsub_rn(x.z, top)),
+                                            det_exp_call(__fsub_rn(x.w, top)));
+                *at[u] = e[u];
+                sum = __fadd_rn(sum, e[u].x);
+                if (tu + 1 < n) sum = __fadd_rn(sum, e[u].y);
+                if (tu + 2 < n) sum = __fadd_rn(sum, e[u].z);
+                if (tu + 3 < n) sum = __fadd_rn(sum, e[u].w);
             }
         }
-    }
-    meet();
-    // ---- chains of S: (head, chain) over the cluster's threads; the total goes
-    // to every CTA
-    for (int i = rank * kThreads + tid; i < nh * 256; i += C * kThreads) {
-        const int h = i >> 8, l = i & 255;
-        float s = 0.0f;
-        int r = 0, next = first_chunk(1);
-        const float *src = scores_of(0) + h * xs_ld;
-        int start = 0;
-        for (int t = 4 * l; t < n; t += 1024) {
-            while ((t >> 8) >= next) {
-                ++r;
-                start = next * kKChunk;
-                next = first_chunk(r + 1);
-                src = scores_of(r) + h * xs_ld;
-            }
-            const float4 e = *reinterpret_cast<const float4 *>(src + (t - start));
-            s = __fadd_rn(s, e.x);
-            if (t + 1 < n) s = __fadd_rn(s, e.y);
-            if (t + 2 < n) s = __fadd_rn(s, e.z);
-            if (t + 3 < n) s = __fadd_rn(s, e.w);
-        }
-        for (r = 0; r < C; ++r) *cluster.map_shared_rank(&F.chain[h][l], r) = s;
+        for (int r = 0; r < C; ++r) *cluster.map_shared_rank(&F.chain[h][l], r) = sum;
     }
     meet();
     for (int i = warp; i < nh * 8; i += kWarps) {
@@ -476,19 +481,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (lane == 0) F.red[i >> 3][i & 7] = s;
     }
     __syncthreads();
-    // ---- p in place
+    // ---- p in place, or, from the workspace, with each piece
+    float inv[NH];
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
-        if (h >= nh) break;
-        const float *t = F.red[h];
-        const float inv = __fdiv_rn(
+        const float *t = F.red[min(h, nh - 1)];
+        inv[h] = __fdiv_rn(
             1.0f, __fadd_rn(__fadd_rn(__fadd_rn(t[0], t[1]), __fadd_rn(t[2], t[3])),
                             __fadd_rn(__fadd_rn(t[4], t[5]), __fadd_rn(t[6], t[7]))));
-        float4 *x4 = reinterpret_cast<float4 *>(xs + h * xs_ld);
-        for (int i = tid; i < quads; i += kThreads) {
-            const float4 e = x4[i];
-            x4[i] = make_float4(__fmul_rn(e.x, inv), __fmul_rn(e.y, inv), __fmul_rn(e.z, inv),
-                                __fmul_rn(e.w, inv));
+        if (on_chip && h < nh) {
+            float4 *x4 = reinterpret_cast<float4 *>(xs + h * xs_ld);
+            for (int i = tid; i < (t1 - t0 + 3) >> 2; i += kThreads) {
+                const float4 e = x4[i];
+                x4[i] = make_float4(__fmul_rn(e.x, inv[h]), __fmul_rn(e.y, inv[h]),
+                                    __fmul_rn(e.z, inv[h]), __fmul_rn(e.w, inv[h]));
+            }
         }
     }
     __syncthreads();
@@ -519,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             if (!on_chip) {
 #pragma unroll
                 for (int i = 0; i < 2 * NH; ++i)
-                    sts1(copies + (i * 32 + lane) * 4, keep[i]);
+                    sts1(copies + (i * 32 + lane) * 4, __fmul_rn(keep[i], inv[i / 2]));
                 __syncwarp();
             }
             const uint32_t po = on_chip ? t * 4 : 0;
@@ -600,9 +607,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int r = 0; r < C; ++r) {
             const float *p = scores_of(r) + part_at + int64_t(h) * most * d + (i - h * d);
             const int chunks = base + (r < rem);
-            for (int c = 0; c < chunks; ++c) {
-                const float v = p[int64_t(c) * d];
-                t = r == 0 && c == 0 ? v : __fadd_rn(t, v);
+            for (int cg = 0; cg < chunks; cg += 8) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (cg + k < chunks) v[k] = p[int64_t(cg + k) * d];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (cg + k < chunks) t = r + cg + k == 0 ? v[k] : __fadd_rn(t, v[k]);
             }
         }
         o[i] = lost ? __uint_as_float(0x7fc00000u) : t;

@@ -661,8 +661,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
 // that is the whole row, else once a pass (the row stays in L1). A lane has the
 // groups lane + 32 w + 256 t, so chain lane + 32 w of S adds its groups in ascending
 // t, and T's chains have an element each.
-template <bool ONE>
-__global__ void __launch_bounds__(kSmallWarps * 32, ONE ? 2 : 3) logprob_small_kernel(LogprobArgs A) {
+template <int W, bool ONE>
+__global__ void __launch_bounds__(kSmallWarps * 32, W == 2 ? 4 : ONE ? 2 : 3) logprob_small_kernel(LogprobArgs A) {
     __shared__ uint64_t lists[kSmallWarps][kSmallListed], tops[kSmallWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, V = A.V;
     for (int64_t row = blockIdx.x * int64_t(kSmallWarps) + warp; row < A.rows;
@@ -670,16 +670,16 @@ __global__ void __launch_bounds__(kSmallWarps * 32, ONE ? 2 : 3) logprob_small_k
         const float *x = A.logits + row * A.ld;
         const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0;
         const Asked asked = ask(A, row, x);
-        float4 v[8];                         // a sweep's groups; -inf past the row's end
+        float4 v[W];                         // a sweep's groups; -inf past the row's end
         auto load = [&](int g0) {
-            if (vec && 4 * g0 + 1024 <= V) {
+            if (vec && 4 * g0 + 128 * W <= V) {
 #pragma unroll
-                for (int w = 0; w < 8; ++w)
+                for (int w = 0; w < W; ++w)
                     v[w] = *reinterpret_cast<const float4 *>(x + 4 * (g0 + 32 * w + lane));
                 return;
             }
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const int j = 4 * (g0 + 32 * w + lane);
                 if (vec && j + 3 < V) {
                     v[w] = *reinterpret_cast<const float4 *>(x + j);
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, ONE ? 2 : 3) logprob_small_k
         for (int g0 = 0; 4 * g0 < V; g0 += kXentLanes) {
             load(g0);
 #pragma unroll
-            for (int w = 0; w < 8; ++w) mine = more_max(mine, v[w]);
+            for (int w = 0; w < W; ++w) mine = more_max(mine, v[w]);
         }
         float m = mine;
 #pragma unroll
@@ -715,10 +715,10 @@ __global__ void __launch_bounds__(kSmallWarps * 32, ONE ? 2 : 3) logprob_small_k
             if (list) {
                 float best = -kInf;
 #pragma unroll
-                for (int w = 0; w < 8; ++w) best = fmaxf(best, max4(v[w]));
+                for (int w = 0; w < W; ++w) best = fmaxf(best, max4(v[w]));
                 if (__any_sync(0xffffffffu, best >= bound)) {
 #pragma unroll
-                    for (int w = 0; w < 8; ++w) {
+                    for (int w = 0; w < W; ++w) {
                         const int j = 4 * (g0 + 32 * w + lane);
                         if (!__any_sync(0xffffffffu, max4(v[w]) >= bound)) continue;
 #pragma unroll
@@ -733,9 +733,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, ONE ? 2 : 3) logprob_small_k
                     }
                 }
             }
-            float u[8];                      // T's sums in fours
+            float u[8] = {};                 // T's sums in fours
 #pragma unroll
-            for (int w0 = 0; w0 < 8; w0 += 2) {
+            for (int w0 = 0; w0 < W; w0 += 2) {
                 float4 es[2], ts[2], vs[2] = {v[w0], v[w0 + 1]};
                 ts[0] = ts[1] = es[0] = es[1] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (4 * (g0 + 32 * w0) < V) {
@@ -879,10 +879,12 @@ cudaError_t launch_logprob(int64_t rows, int64_t V, const float *logits, int64_t
     const int64_t sms = sm_count_current_device();
     if (V <= kSmallVocab) {
         const int64_t blocks = std::min<int64_t>((rows + kSmallWarps - 1) / kSmallWarps, sms * 8);
-        if (V <= 1024)
-            logprob_small_kernel<true><<<unsigned(blocks), kSmallWarps * 32, 0, s>>>(A);
+        if (V <= 256)
+            logprob_small_kernel<2, true><<<unsigned(blocks), kSmallWarps * 32, 0, s>>>(A);
+        else if (V <= 1024)
+            logprob_small_kernel<8, true><<<unsigned(blocks), kSmallWarps * 32, 0, s>>>(A);
         else
-            logprob_small_kernel<false><<<unsigned(blocks), kSmallWarps * 32, 0, s>>>(A);
+            logprob_small_kernel<8, false><<<unsigned(blocks), kSmallWarps * 32, 0, s>>>(A);
         return cudaGetLastError();
     }
     const int64_t grid = std::min<int64_t>(rows, sms);
