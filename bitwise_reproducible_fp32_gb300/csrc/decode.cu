@@ -127,6 +127,12 @@ __device__ __forceinline__ float butterfly32(float s) {
     return s;
 }
 
+// exp4 where the maximum is not finite.
+__device__ __noinline__ float4 exp4_any(float4 x, float m) {
+    return make_float4(det_exp(__fsub_rn(x.x, m)), det_exp(__fsub_rn(x.y, m)),
+                       det_exp(__fsub_rn(x.z, m)), det_exp(__fsub_rn(x.w, m)));
+}
+
 template <int NH>
 struct Fixed {                          // a CTA's shared memory after the rings
     uint64_t full[kWarps][4];
@@ -461,11 +467,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 const int tu = t + 1024 * u;
                 if (tu >= n) break;
                 const float4 x = e[u];
-                e[u] = finite ? exp4(x, top)
-                              : make_float4(det_exp_call(__fsub_rn(x.x, top)),
-                                            det_exp_call(__fsub_rn(x.y, top)),
-                                            det_exp_call(__fsub_rn(x.z, top)),
-                                            det_exp_call(__fsub_rn(x.w, top)));
+                e[u] = finite ? exp4(x, top) : exp4_any(x, top);
                 *at[u] = e[u];
                 sum = __fadd_rn(sum, e[u].x);
                 if (tu + 1 < n) sum = __fadd_rn(sum, e[u].y);
