@@ -136,23 +136,21 @@ __device__ __noinline__ float4 exp4_any(float4 x, float m) {
 template <int NH>
 struct Fixed {                          // a CTA's shared memory after the rings
     uint64_t full[kWarps][4];
-    float q[NH][256];
-    float chain[NH][256];
+    float rows[NH][256];                // q, then the chains of S, then each warp's
+                                        // probabilities of a piece (rows in the workspace)
     float red[NH][8];
     float top[kMaxCluster][NH];         // each CTA's maxima
     int lost[kMaxCluster];
     int pages[kPageCache];
 };
-// Beside it there is room for the scores and partials of short rows, or, for
-// longer ones, at least for the warps' copies of a piece's probabilities.
+// Beside it there is room for the scores and partials of short rows.
 constexpr int kRingBytes = kWarps * kPieceBytes;      // a stage of all warps
-// Stages where rows are long: units of many heads need the room for scores.
-constexpr int stages_of(int nh) { return nh <= 2 ? 3 : 2; }
+constexpr int kStages = 3;
 template <int NH>
 constexpr bool kFits = sizeof(Fixed<NH>) % 16 == 0 &&
-                       stages_of(NH) * kRingBytes + int(sizeof(Fixed<NH>)) +
-                               kWarps * NH * kTokens * 4 <= kSmemPerCta;
+                       kStages * kRingBytes + int(sizeof(Fixed<NH>)) <= kSmemPerCta;
 static_assert(kFits<1> && kFits<2> && kFits<4> && kFits<kMaxHeads>, "shared memory");
+static_assert(kWarps * kTokens <= 256, "a piece's probabilities of all warps");
 
 // NH: the heads of a unit the registers hold (nh <= NH of them live).
 template <int NH, Loader LOAD>
@@ -188,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             early[i] = tid + i * kThreads < A.max_pages ? pages[tid + i * kThreads] : 0;
     for (int i = tid; i < nh * d; i += kThreads) {
         const int h = i / d;
-        F.q[h][i - h * d] = A.q[b * A.ldq + int64_t(h0) * d + i];
+        F.rows[h][i - h * d] = A.q[b * A.ldq + int64_t(h0) * d + i];
     }
     const int n = A.kv_lens[b];
     if (n <= 0 || n > A.max_len) {      // the whole cluster
@@ -360,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int sl = 0; sl < nsl; ++sl) {
             const uint32_t piece = next_piece();
             const int width = min(32, d - 32 * sl);
-            const float *q = &F.q[0][32 * sl];
+            const float *q = &F.rows[0][32 * sl];
             auto four = [&](int i) {
                 const float4 k0 = lds4(piece + kat[i]), k1 = lds4(piece + 4096 + kat[i]);
 #pragma unroll
@@ -475,11 +473,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 if (tu + 3 < n) sum = __fadd_rn(sum, e[u].w);
             }
         }
-        for (int r = 0; r < C; ++r) *cluster.map_shared_rank(&F.chain[h][l], r) = sum;
+        for (int r = 0; r < C; ++r) *cluster.map_shared_rank(&F.rows[h][l], r) = sum;
     }
     meet();
     for (int i = warp; i < nh * 8; i += kWarps) {
-        const float s = butterfly32(F.chain[i >> 3][(i & 7) * 32 + lane]);
+        const float s = butterfly32(F.rows[i >> 3][(i & 7) * 32 + lane]);
         if (lane == 0) F.red[i >> 3][i & 7] = s;
     }
     __syncthreads();
@@ -503,33 +501,40 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     __syncthreads();
     // ---- P V: chunk partials (registers past the unit's heads repeat its last)
     uint32_t pat[NH];             // shared-memory addresses of the heads' rows
-    const uint32_t copies = smem_u32(room) + warp * (NH * kTokens * 4);
+    const uint32_t copies = smem_u32(&F.rows[0][0]) + warp * (NH * kTokens * 4);
 #pragma unroll
     for (int h = 0; h < NH; ++h)
         pat[h] = on_chip ? smem_u32(room) + min(h, nh - 1) * int(xs_ld) * 4
                          : copies + h * (kTokens * 4);
+    float keep[2 * NH];           // of the next piece, from the workspace
+    auto ask = [&](int t, int end) {
+#pragma unroll
+        for (int i = 0; i < 2 * NH; ++i) {
+            const int at = t + 32 * (i & 1) + lane;
+            keep[i] = at < end ? xs[min(i >> 1, nh - 1) * xs_ld + at] : 0.0f;
+        }
+    };
+    auto end_of = [&](int c) { return min(t1 - t0, (c + 1) * kKChunk); };
+    if (!on_chip && warp < jobs) ask(warp / nsl * kKChunk, end_of(warp / nsl));
     for (int j = warp; j < jobs; j += kWarps) {
         const int c = j / nsl, sl = j - c * nsl;
-        const int end = min(t1 - t0, (c + 1) * kKChunk);
+        const int end = end_of(c);
         float acc[NH];
 #pragma unroll
         for (int h = 0; h < NH; ++h) acc[h] = 0.0f;
         for (int t = c * kKChunk; t < end; t += kTokens) {
-            float keep[2 * NH];
-            if (!on_chip)             // the piece's probabilities, from L2
-#pragma unroll
-                for (int h = 0; h < NH; ++h)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        keep[2 * h + k] = t + 32 * k + lane < end
-                                              ? xs[min(h, nh - 1) * xs_ld + t + 32 * k + lane]
-                                              : 0.0f;
             const uint32_t piece = next_piece();
             if (!on_chip) {
 #pragma unroll
                 for (int i = 0; i < 2 * NH; ++i)
                     sts1(copies + (i * 32 + lane) * 4, __fmul_rn(keep[i], inv[i / 2]));
                 __syncwarp();
+                if (t + kTokens < end) {
+                    ask(t + kTokens, end);
+                } else if (j + kWarps < jobs) {
+                    const int next = (j + kWarps) / nsl;
+                    ask(next * kKChunk, end_of(next));
+                }
             }
             const uint32_t po = on_chip ? t * 4 : 0;
             auto four = [&](int r) {
@@ -609,13 +614,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int r = 0; r < C; ++r) {
             const float *p = scores_of(r) + part_at + int64_t(h) * most * d + (i - h * d);
             const int chunks = base + (r < rem);
-            for (int cg = 0; cg < chunks; cg += 8) {
-                float v[8];
+            for (int cg = 0; cg < chunks; cg += 16) {
+                float v[16];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < 16; ++k)
                     if (cg + k < chunks) v[k] = p[int64_t(cg + k) * d];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < 16; ++k)
                     if (cg + k < chunks) t = r + cg + k == 0 ? v[k] : __fadd_rn(t, v[k]);
             }
         }
@@ -664,7 +669,7 @@ DecodePlan decode_plan(int64_t batch, int64_t heads, int64_t kv_heads, int64_t h
     while (2 * c <= kMaxCluster && 2 * c * units <= slots && 2 * c <= chunks) c *= 2;
     p.cluster = int(c);
     const int64_t run = (chunks + c - 1) / c;         // a CTA's most chunks
-    p.stages = run <= 2 ? 2 : stages_of(p.unit_heads);
+    p.stages = run <= 2 ? 2 : kStages;
     const int64_t need = int64_t(p.unit_heads) * run * (kKChunk + head_dim);
     const int64_t cap =
         (kSmemPerCta - p.stages * kRingBytes - int64_t(fixed_bytes(p.unit_heads))) / 4;
