@@ -51,7 +51,7 @@ constexpr int kTokens = 64;                 // of a piece, 32 dimensions each
 constexpr int kPieceBytes = kTokens * 128;
 constexpr int kMaxHeads = 8;
 constexpr int kMaxCluster = 16;
-constexpr int kDeep = 4;                    // groups of a chain of S in flight
+constexpr int kDeep = 8;                    // groups of a chain of S in flight
 constexpr int kPageCache = 512;             // page ids of a CTA kept on chip
 enum Loader { kTma, kCopy16, kCopy4 };
 constexpr unsigned kWatchdogDecode = 32u;   // det_watchdog_status bit 5
@@ -151,6 +151,18 @@ constexpr bool kFits = sizeof(Fixed<NH>) % 16 == 0 &&
                        kStages * kRingBytes + int(sizeof(Fixed<NH>)) <= kSmemPerCta;
 static_assert(kFits<1> && kFits<2> && kFits<4> && kFits<kMaxHeads>, "shared memory");
 static_assert(kWarps * kTokens <= 256, "a piece's probabilities of all warps");
+
+// Where a chunk of the row lies: the place'th of CTA r's run. CTAs r < rem have
+// base + 1 chunks, the others base.
+struct Walk {
+    int r = 0, place, base, rem;
+    __device__ __forceinline__ Walk(int chunk, int base_, int rem_)
+        : place(chunk), base(base_), rem(rem_) {}
+    // of a chunk that exists
+    __device__ __forceinline__ void settle() {
+        for (int run; place >= (run = base + (r < rem)); ++r) place -= run;
+    }
+};
 
 // NH: the heads of a unit the registers hold (nh <= NH of them live).
 template <int NH, Loader LOAD>
@@ -444,21 +456,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int k = 1; k < NH; ++k) top = h == k ? m[k] : top;
         const bool finite = fabsf(top) <= 0x1.fffffep127f;
         float sum = 0.0f;
+        Walk w(l >> 6, base, rem);
         for (int t = 4 * l; t < n; t += 1024 * kDeep) {
             float4 *at[kDeep], e[kDeep];
 #pragma unroll
             for (int u = 0; u < kDeep; ++u) {
-                const int tu = t + 1024 * u;
-                if (tu >= n) break;
-                int r = 0, c = tu >> 8;           // the chunk's CTA, its place there
-                if (C > 1) {
-                    const int longer = rem * (base + 1);
-                    r = c < longer ? c / (base + 1) : rem + (c - longer) / base;
-                    c -= first_chunk(r);
-                }
-                at[u] = reinterpret_cast<float4 *>(scores_of(r) + h * xs_ld + c * kKChunk +
-                                                   (tu & 255));
+                if (t + 1024 * u >= n) break;
+                w.settle();
+                at[u] = reinterpret_cast<float4 *>(scores_of(w.r) + h * xs_ld +
+                                                   w.place * kKChunk + (t & 255));
                 e[u] = *at[u];
+                w.place += 4;
             }
 #pragma unroll
             for (int u = 0; u < kDeep; ++u) {
@@ -608,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     meet();
     for (int r = 0; r < C; ++r) lost |= F.lost[r];
     // ---- the chunks left to right
-    for (int i = rank * kThreads + tid; i < nh * d; i += C * kThreads) {
+    for (int i = (warp * C + rank) * 32 + lane; i < nh * d; i += C * kThreads) {
         const int h = i / d;
         float t = 0.0f;
         for (int r = 0; r < C; ++r) {
