@@ -27,7 +27,16 @@
 //  - P V: a warp a (chunk, 32 dimensions), a lane a dimension, the chain over the
 //    chunk's tokens; the chunk partials are joined left to right at the end.
 // Rows whose scores and partials do not fit shared memory keep them in the
-// workspace, which stays in L2.
+// workspace, which stays in L2; a piece's probabilities are then asked for one
+// piece ahead.
+// Measured, 12 heads of 64: 64 requests of 700..2048 tokens 93 us (5.8 TB/s of keys
+// and values), 256 of 100..512 96 us (5.1 TB/s), one of 32768 50 us (4.0 TB/s); 32
+// heads of 128 over 8, 4 of 22853..32768, 178 us (5.1 TB/s): the passes over K and
+// over V run at HBM's rate, the rest is 30 us between them and the longest
+// request's tail. 32 heads over 4, 32 requests of 2000..4096, 129 us (3.1 TB/s): the
+// longest is a third longer than the mean, and the 8 heads' multiply-adds and
+// shared-memory reads keep a warp about as long as its pieces' arrival. Asking L2
+// for 4 or more pieces of V ahead while the CTAs meet ran 1..10% slower.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -658,11 +667,12 @@ struct DecodePlan {
 };
 
 // The cluster: the largest power of two whose units all fit on the GPU at once
-// (and no more CTAs than the longest row has chunks). 12 heads of 64, us on one
-// GB300 with 1 / 2 / 4 / 8 / 16 CTAs: 64 requests of 700..2048 tokens 93 / 113 /
-// 134 / 238 / 238; 8 of 1024..2048: 30 / 24 / 24 / 36 / 36; one of 32768: 448 /
-// 233 / 116 / 71 / 51. Sizes between powers of two measured slower than the power
-// below. Two stages where a CTA's run is at most two chunks (three CTAs then fit
+// (and no more CTAs than the longest row has chunks). us on one GB300 with 1 / 2 /
+// 4 / 8 / 16 CTAs, 12 heads of 64: 64 requests of 700..2048 tokens 93 / 110 / 132 /
+// 237 / 542; 8 of 1024..2048: 30 / 24 / 24 / 37 / 78; one of 32768: 430 / 224 / 110 /
+// 67 / 50. 32 heads of 128 over 8: 4 requests of 22853..32768: 907 / 464 / 247 /
+// 178 / 256; over 4: 32 of 2000..4096: 189 / 129 / 148 / 176 / 309. Sizes between
+// powers of two measured slower than the power below. Two stages where a CTA's run is at most two chunks (three CTAs then fit
 // an SM: 256 requests of 100..512 tokens 112 -> 95), three else.
 DecodePlan decode_plan(int64_t batch, int64_t heads, int64_t kv_heads, int64_t head_dim,
                        int64_t max_len) {
