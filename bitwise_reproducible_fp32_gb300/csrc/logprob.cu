@@ -30,19 +30,25 @@
 // gone through phase by phase by all warps 874 / 788 / 846. Both roles are busy
 // nearly all of the time: the sums by issue and the latency between their steps,
 // the max by the latency of its loads.
-// Rows of at most 4096 logits: a warp a row, each chain of T one element.
+// Few rows of more than 4096 logits: a cluster of 4..16 CTAs a row (below).
+// Rows of at most 4096 logits: a warp a row, each chain of T one element (2048 x
+// 256: 5.7 us, 16384 x 256: 21, 65536 x 1024: 146, 65536 x 4096: 531).
 // The alternatives: with t the top_k-th largest of 32 group maxima, at least
 // top_k elements are >= t, and few more; they are listed while the exps are
 // formed and ranked by (value, lowest id) with a count of the better ones. A list
 // that overflows (many equal logits) or a row without a finite max is done by
 // top_k maxima over the row instead. Neither way depends on the order of arrival.
 // Gradient: a thread four granules of a row; the exps again from the row's m.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <cstddef>
 
 #include "det_internal.cuh"
 #include "det_math.cuh"
 #include "row_stage.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace det {
 
@@ -788,6 +794,158 @@ __global__ void __launch_bounds__(kSmallWarps * 32, W == 2 ? 4 : ONE ? 2 : 3) lo
     }
 }
 
+// Few rows: a cluster of C CTAs a row. Of each 1024 logits CTA r has the 1024 / C
+// from 1024 r / C on, so its elements make up whole chains of S (j mod 1024 picks
+// the chain) and of T (j mod 4096), and only the maxima, the chains' sums and the
+// listed alternatives cross the cluster. Latency bounds it: the row's load, three
+// meetings of the cluster and the chain of V / 256 additions (8.3 us for one row of
+// 50257, 15 for one of 256000).
+struct Split {
+    float parts[16], groups[32];        // maxima of this CTA, of the row's 32 groups
+    float chain[kXentLanes], u[kSeg];   // of the row, in its first CTA: S, T in fours
+    float red[8], tsum[32];
+    uint64_t list[kListed], top[32];
+    int listed, pad[3];
+};
+static_assert(sizeof(Split) % 16 == 0 && offsetof(Split, list) % 8 == 0, "aligned float4s");
+
+__global__ void __launch_bounds__(kXentLanes, 2) logprob_split_kernel(LogprobArgs A) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    Split &sh = *reinterpret_cast<Split *>(smem_raw);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = A.V;
+    const int64_t row = blockIdx.x / C;
+    const float *x = A.logits + row * A.ld;
+    // stripes of 1024 logits; this CTA's groups of 4 in each, in order
+    const int stripes = (V + 4 * kXentLanes - 1) / (4 * kXentLanes), width = kXentLanes / C;
+    const int mine = stripes * width;
+    float4 *xs = reinterpret_cast<float4 *>(&sh + 1), *es = xs + mine;
+    auto element_of = [&](int i) {       // the first of local group i
+        return 4 * (i / width * kXentLanes + rank * width + i % width);
+    };
+    if (tid == 0) sh.listed = 0;
+    cluster.barrier_arrive();
+    const Asked asked = ask(A, row, x);
+    const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0;
+    float most = -kInf;
+    for (int i0 = tid; i0 < mine; i0 += 4 * kXentLanes) {
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * kXentLanes, j = element_of(i);
+            if (i >= mine) break;
+            if (vec && j + 3 < V) {
+                v[k] = *reinterpret_cast<const float4 *>(x + j);
+            } else {
+                v[k].x = j < V ? x[j] : -kInf;
+                v[k].y = j + 1 < V ? x[j + 1] : -kInf;
+                v[k].z = j + 2 < V ? x[j + 2] : -kInf;
+                v[k].w = j + 3 < V ? x[j + 3] : -kInf;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * kXentLanes;
+            if (i >= mine) break;
+            xs[i] = v[k];
+            most = more_max(most, v[k]);
+        }
+    }
+    // the maxima of 32 groups of 8 C threads of the cluster
+    const int team = min(32, 8 * C), teams = kXentLanes / team, per = 8 * C / team;
+    for (int off = team / 2; off >= 1; off >>= 1)
+        most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, off));
+    if (lane % team == 0) sh.parts[tid / team] = most;
+    __syncthreads();
+    cluster.barrier_wait();
+    if (tid < teams / per) {
+        float g = sh.parts[tid * per];
+        for (int i = 1; i < per; ++i) g = max_nan(g, sh.parts[tid * per + i]);
+        for (int r = 0; r < C; ++r)
+            *cluster.map_shared_rank(&sh.groups[rank * (teams / per) + tid], r) = g;
+    }
+    cluster.sync();
+    float m = sh.groups[lane];
+    const float group = m;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1)
+        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+    m = __fadd_rn(m, 0.0f);              // a zero maximum is +0
+    const bool finite_m = fabsf(m) <= 0x1.fffffep127f;
+    const bool list = A.top_k > 0 && finite_m;
+    const float bound = list ? list_bound(group, A.top_k, lane) : kInf;
+    Split &first = *cluster.map_shared_rank(&sh, 0);
+    for (int i = tid; i < mine; i += kXentLanes) {
+        const float4 v = xs[i];
+        const int j = element_of(i);
+        float4 e = finite_m ? exp4(v, m) : exp_slow(v, m, make_float4(0.f, 0.f, 0.f, 0.f)).e;
+        if (j >= V) e.x = 0.0f;
+        if (j + 1 >= V) e.y = 0.0f;
+        if (j + 2 >= V) e.z = 0.0f;
+        if (j + 3 >= V) e.w = 0.0f;
+        es[i] = e;
+        if (list && max4(v) >= bound)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (comp(v, c) >= bound && j + c < V) {
+                    const int at = atomicAdd(&first.listed, 1);
+                    if (at < kListed) first.list[at] = rank_of(comp(v, c), j + c);
+                }
+    }
+    __syncthreads();
+    if (tid >= kXentLanes - width) {     // the chains of S
+        const int p = tid - (kXentLanes - width);
+        float s = 0.0f;
+#pragma unroll 4
+        for (int i = p; i < mine; i += width) {
+            const float4 e = es[i];
+            s = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(s, e.x), e.y), e.z), e.w);
+        }
+        first.chain[rank * width + p] = s;
+    }
+    for (int f = tid; f < 4 * width; f += kXentLanes) {      // the chains of T, in fours
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b = f; b < mine; b += 16 * width) {         // the blocks of 16 stripes
+            float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = b + 4 * k * width;
+                if (i >= mine) break;
+                const float4 e = es[i], v = xs[i];
+                if (e.x != 0.0f) t.x = __fmaf_rn(e.x, __fsub_rn(v.x, m), t.x);
+                if (e.y != 0.0f) t.y = __fmaf_rn(e.y, __fsub_rn(v.y, m), t.y);
+                if (e.z != 0.0f) t.z = __fmaf_rn(e.z, __fsub_rn(v.z, m), t.z);
+                if (e.w != 0.0f) t.w = __fmaf_rn(e.w, __fsub_rn(v.w, m), t.w);
+            }
+            a = make_float4(__fadd_rn(a.x, t.x), __fadd_rn(a.y, t.y), __fadd_rn(a.z, t.z),
+                            __fadd_rn(a.w, t.w));
+        }
+        first.u[f / width * kXentLanes + rank * width + f % width] =
+            __fadd_rn(__fadd_rn(__fadd_rn(a.x, a.y), a.z), a.w);
+    }
+    cluster.sync();
+    if (rank != 0) return;
+    const float s = warp_butterfly_sum(sh.chain[tid]);
+    if (lane == 0) sh.red[warp] = s;
+#pragma unroll
+    for (int q = 0; q < kSets; ++q) {
+        const float t = warp_butterfly_sum(sh.u[q * kXentLanes + tid]);
+        if (lane == 0) sh.tsum[q * kSumWarps + warp] = t;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    const float T = warp_butterfly_sum(sh.tsum[lane]);
+    const float *f = sh.red;
+    const float S = __fadd_rn(__fadd_rn(__fadd_rn(f[0], f[1]), __fadd_rn(f[2], f[3])),
+                              __fadd_rn(__fadd_rn(f[4], f[5]), __fadd_rn(f[6], f[7])));
+    uint64_t got = 0;
+    if (A.top_k > 0)
+        got = !list || sh.listed > kListed ? top_by_rounds(x, V, A.top_k, lane)
+                                           : rank_list(sh.list, sh.listed, A.top_k, sh.top, lane);
+    write_row(A, row, asked, m, S, T, got, lane);
+}
+
 constexpr int kBwdThreads = 256;
 constexpr int kBwdGranules = 4;              // of a thread
 
@@ -870,6 +1028,34 @@ cudaError_t logprob_watchdog(unsigned int *code, int clear) {
     return e;
 }
 
+namespace {
+size_t split_bytes(int64_t V, int64_t cluster) {
+    const int64_t stripes = (V + 4 * kXentLanes - 1) / (4 * kXentLanes);
+    return sizeof(Split) + size_t(stripes * (kXentLanes / cluster) * 2 * int(sizeof(float4)));
+}
+
+// The CTAs a row is split over where rows are few; 0: a CTA a row (the stream
+// kernel). The most whose clusters run at once, two CTAs an SM; where only that
+// many fit an SM's shared memory, 7/8 of it, as not every SM finds a place in a
+// cluster then. Rows of more than 65536 logits, whose stream takes long, may also
+// take two turns of 16. us, stream / split over 4 / 8 / 16: 1 x 50257 18.5 / 11.8 /
+// 8.9 / 8.3; 19 x 50257 19.5 / 12.5 / 10.3 / 9.9; 38: 19.6 / 14.4 / 12.2 / 12.8; 64:
+// 20.0 / 14.6 / 19.4 / 20.0; 76: 20.0 / 23.1 / 20.6 / 23.8; 64 x 16000 10.1 / 8.9 / 9.3 /
+// 16.4; 38 x 128000 42 / - / - / 24; 1 x 256000 67 / - / - / 15. Over 2 it was no
+// faster anywhere.
+int split_cluster(int64_t rows, int64_t V, int64_t sms) {
+    constexpr int64_t kSmem = 227 * 1024;
+    if (V > (int64_t(1) << 20)) return 0;        // no share fits
+    for (int c = 16; c >= 4; c /= 2) {
+        const int64_t fit = kSmem / int64_t(split_bytes(V, c) + 1024);
+        const int64_t two = std::min<int64_t>(fit, 2) * sms;
+        if (fit > 0 && rows * c <= (fit > 2 ? two : two * 7 / 8)) return c;
+    }
+    const int64_t fit = kSmem / int64_t(split_bytes(V, 16) + 1024);
+    return V > 65536 && rows * 16 <= 2 * fit * sms ? 16 : 0;
+}
+}  // namespace
+
 cudaError_t launch_logprob(int64_t rows, int64_t V, const float *logits, int64_t ld,
                            const int32_t *tokens, int top_k, float *logp, float *entropy,
                            float *stats, int32_t *top_ids, float *top_logp, int32_t *dev_status,
@@ -879,6 +1065,7 @@ cudaError_t launch_logprob(int64_t rows, int64_t V, const float *logits, int64_t
     const int64_t sms = sm_count_current_device();
     if (V <= kSmallVocab) {
         const int64_t blocks = std::min<int64_t>((rows + kSmallWarps - 1) / kSmallWarps, sms * 8);
+        // two groups a lane up to 256 logits: 21 us instead of 33 for 16384 x 256
         if (V <= 256)
             logprob_small_kernel<2, true><<<unsigned(blocks), kSmallWarps * 32, 0, s>>>(A);
         else if (V <= 1024)
@@ -886,6 +1073,28 @@ cudaError_t launch_logprob(int64_t rows, int64_t V, const float *logits, int64_t
         else
             logprob_small_kernel<8, false><<<unsigned(blocks), kSmallWarps * 32, 0, s>>>(A);
         return cudaGetLastError();
+    }
+    if (const int cluster = split_cluster(rows, V, sms)) {
+        const size_t share = split_bytes(V, cluster);
+        cudaError_t e = cudaFuncSetAttribute(
+            logprob_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e == cudaSuccess && cluster > 8)
+            e = cudaFuncSetAttribute(logprob_split_kernel,
+                                     cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(unsigned(rows * cluster));
+        cfg.blockDim = dim3(kXentLanes);
+        cfg.dynamicSmemBytes = share;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = unsigned(cluster);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, logprob_split_kernel, A);
+        return e == cudaSuccess ? cudaGetLastError() : e;
     }
     const int64_t grid = std::min<int64_t>(rows, sms);
     // the rows between max and exps in L2, and the next one asked for where it fits

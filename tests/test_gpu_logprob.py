@@ -182,3 +182,48 @@ def test_no_rows(dev):
     out = detlib.detlogprob_f32(e, t, top_k=3)
     assert [tuple(o.shape) for o in out] == [(0,), (0,), (0, 3), (0, 3), (0, 4)]
     assert detlib.detlogprob_bwd_f32(e, t, out[4], out[0]).shape == (0, 10)
+
+
+@pytest.mark.parametrize("V", [4097, 4099, 16001, 50257, 70001, 151936, 256003])
+@pytest.mark.parametrize("layout", ["dense", "padded", "offset"])
+def test_the_number_of_rows_changes_no_bit(dev, V, layout):
+    # few rows are split over clusters, many are not: the same rows in calls of
+    # 1, 12, 24, 36, 60 and 168, with ties, equal logits, infinities, NaN and
+    # masks at the lowest value among them
+    rng = np.random.default_rng(V)
+    x = (3 * rng.standard_normal((12, V))).astype(F)
+    x[1] = rng.integers(-3, 4, V)
+    x[2] = 0.25
+    x[3, rng.random(V) < 0.9] = -np.inf
+    x[4, :] = -np.inf
+    x[5, V // 3] = np.inf
+    x[6, V - 1] = np.nan
+    x[7, rng.random(V) < 0.5] = np.finfo(F).min
+    x[8] = np.where(np.arange(V) % 2, F(0.0), F(-0.0))
+    x[9] = np.arange(V) / V * 200
+    x[10, :] = -np.inf
+    x[10, V - 1] = 2.0
+    x[11] = x[11] * 40
+    y = rng.integers(0, V, 12).astype(np.int32)
+    y[:2] = [-1, V - 1]
+    want = check(x, y, 32, layout)
+    full = np.tile(x, (14, 1)), np.tile(y, 14)
+    for rows in (1, 24, 36, 60, 168):
+        xd = to_dev(full[0][:rows], layout)
+        yd = torch.from_numpy(full[1][:rows]).cuda()
+        logp, ent, ids, top, stats = (host(t) for t in detlib.detlogprob_f32(xd, yd, top_k=32))
+        for r in range(0, rows, 12):
+            n = min(12, rows - r)
+            for got, w, name in zip((logp, ent, stats, ids, top), want,
+                                    ("logp", "entropy", "stats", "ids", "top")):
+                if name == "ids":
+                    assert np.array_equal(got[r:r + n], w[:n]), (rows, r)
+                else:
+                    assert_bitwise(got[r:r + n], w[:n], f"{name}, row {r} of {rows}")
+
+
+@pytest.mark.parametrize("V", [400001, 444416, 444417, 600000, 1048577])
+def test_long_rows(dev, V):
+    # the longest share of a cluster, and rows past it
+    rng = np.random.default_rng(V)
+    check((2 * rng.standard_normal((2, V))).astype(F), np.array([V - 1, 5], np.int32), 7, "offset")
