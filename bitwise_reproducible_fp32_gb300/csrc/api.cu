@@ -1032,6 +1032,7 @@ DET_API det_status detlog_f32(const det_profile_v1 *prof, int64_t n, const float
 namespace {
 constexpr int64_t kLenMax = int64_t(1) << 30;     // tokens of a request
 constexpr int64_t kTopMax = 32;
+constexpr int64_t kAppendMax = int64_t(1) << 20;  // rows: each looks through the slots after it
 constexpr int64_t kVocabMax = int64_t(1) << 30;   // sweeps past a row's end stay in int
 
 bool rotary_ok(const det_rotary &r, int64_t head_dim) {
@@ -1084,7 +1085,7 @@ DET_API det_status detkv_append_f32(const det_profile_v1 *prof, int64_t rows, in
                                     int32_t *dev_status, det_stream_t stream) {
     det_status st = check_profile(prof);
     if (st != DET_OK) return st;
-    if (rows < 0 || rows > kDimMax || heads < 1 || heads > 65536 || !cache_ok(cache))
+    if (rows < 0 || rows > kAppendMax || heads < 1 || heads > 65536 || !cache_ok(cache))
         return DET_ERR_INVALID_ARG;
     const int64_t d = cache->head_dim;
     if (ldqkv < (heads + 2 * cache->kv_heads) * d || (rotary && !rotary_ok(*rotary, d)))

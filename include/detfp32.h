@@ -687,9 +687,10 @@ typedef struct det_kv_cache {
  * is read or written for the row. A slot at or past num_pages * page_size ORs
  * 1 into *dev_status (device int32, may be NULL) and is skipped likewise.
  * Where several rows name the same slot, the cache holds the last such row.
- * Errors: DET_ERR_INVALID_ARG for negative rows, heads outside 1..65536, a
- * cache with null pointers, sizes below 1, head_dim above 256, kv_heads above
- * 65536 or a stride below head_dim, and the rotary's and the strides' rules. */
+ * Errors: DET_ERR_INVALID_ARG for rows outside 0..1048576 (the search for slots
+ * named twice grows with their square), heads outside 1..65536, a cache with null
+ * pointers, sizes below 1, head_dim above 256, kv_heads above 65536 or a stride
+ * below head_dim, and the rotary's and the strides' rules. */
 det_status detkv_append_f32(const det_profile_v1 *prof, int64_t rows, int64_t heads,
                             const float *qkv, int64_t ldqkv, const int64_t *slots,
                             const int32_t *positions, const det_rotary *rotary,
@@ -755,8 +756,8 @@ det_status detpages_release(const det_profile_v1 *prof, int64_t batch, int64_t p
  * requests. kv_lens[b] == 0 gives +0. A negative length or one past max_pages *
  * page_size ORs 1 into *dev_status (may be NULL), a page outside
  * 0..num_pages-1 among the request's ORs 2; the request's row is NaN then.
- * Entries of the table past a request's pages are not read, nor are the slots
- * past its length. out: row stride ldo, must not overlap q or the cache.
+ * Entries of the table past a request's pages and the slots past its length are
+ * not used. out: row stride ldo, must not overlap q or the cache.
  * workspace: at least detdecode_attention_workspace_bytes (16-byte aligned, no
  * contents assumed); calls that share one must be ordered (one stream). A wait
  * for a piece of the cache that gives up after 2 s sets bit 5 of

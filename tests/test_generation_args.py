@@ -67,7 +67,8 @@ def test_append_refusals(lib):
     f = lambda rows=4, heads=2, qkv=D, ld=384, slots=D, pos=D, ro=rotary(), c=cache(), q=D, \
         ldq=384: lib.detkv_append_f32(prof(), rows, heads, qkv, ld, slots, pos, ro, c, q, ldq, N,
                                       N)  # noqa: E731
-    for kw in (dict(rows=-1), dict(heads=0), dict(qkv=N), dict(ld=383), dict(slots=N),
+    for kw in (dict(rows=-1), dict(rows=2 ** 20 + 1), dict(heads=0), dict(qkv=N), dict(ld=383),
+               dict(slots=N),
                dict(pos=N), dict(ro=rotary(128)), dict(c=None), dict(ldq=127), dict(ldq=400),
                dict(c=cache(k=None)), dict(c=cache(v=None)), dict(c=cache(num_pages=0)),
                dict(c=cache(page_size=0)), dict(c=cache(kv_heads=0)), dict(c=cache(head_dim=0)),
