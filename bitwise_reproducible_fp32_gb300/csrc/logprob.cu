@@ -24,7 +24,7 @@
 //   final  a warp folds the totals, ranks the list and writes the row's results
 // Two teams of load, sum and final warps take every other row. They meet at
 // mbarriers only, every wait bounded. us for 8192 x 50257 / 16384 x 16000 /
-// 2720 x 151936 with 5 alternatives: 585 / 369 / 529 (2.8, 2.8, 3.1 TB/s); one
+// 2720 x 151936 with 5 alternatives: 576 / 366 / 522 (2.9, 2.9, 3.2 TB/s); one
 // team, four groups at a time 576 / 410 / 564; 16 warps of exps handing e to 8
 // warps of chains through shared memory 668 / 582 / 501; whole rows staged and
 // gone through phase by phase by all warps 874 / 788 / 846. Both roles are busy
@@ -32,7 +32,7 @@
 // the max by the latency of its loads.
 // Few rows of more than 4096 logits: a cluster of 4..16 CTAs a row (below).
 // Rows of at most 4096 logits: a warp a row, each chain of T one element (2048 x
-// 256: 5.7 us, 16384 x 256: 21, 65536 x 1024: 146, 65536 x 4096: 531).
+// 256: 5.5 us, 16384 x 256: 17, 65536 x 1024: 145, 65536 x 4096: 525).
 // The alternatives: with t the top_k-th largest of 32 group maxima, at least
 // top_k elements are >= t, and few more; they are listed while the exps are
 // formed and ranked by (value, lowest id) with a count of the better ones. A list
@@ -73,6 +73,7 @@ constexpr int kMaxLoads = 8;            // granules a max thread reads at once
 // use of a max slot only; the use between is of a row before the team's last one,
 // so it is over by then.
 constexpr int kAhead = 3;
+constexpr int kRounds = 8;               // alternatives whose bound is found in rounds
 constexpr int kFound = 256, kListed = 512;    // granules, elements that may be alternatives
 constexpr int kSmallVocab = kTChains;   // a warp a row up to here
 constexpr int kSmallWarps = 8, kSmallListed = 128;
@@ -222,8 +223,18 @@ __device__ __noinline__ uint64_t top_by_rounds(const float *x, int V, int top_k,
 }
 
 // The bound for the list: the top_k-th largest of the lanes' values (group
-// maxima), the lower lane first among equals.
+// maxima), the lower lane first among equals; for few by rounds (5 alternatives of
+// 16384 x 256 17 us, by counting 20.5; 20 the same either way).
 __device__ __forceinline__ float list_bound(float v, int top_k, int lane) {
+    if (top_k <= kRounds) {              // one maximum after the other
+        uint32_t key = key_of(v);
+        for (int k = 1;; ++k) {
+            const uint32_t best = __reduce_max_sync(0xffffffffu, key);
+            const int who = __ffs(__ballot_sync(0xffffffffu, key == best)) - 1;
+            if (k == top_k) return __shfl_sync(0xffffffffu, v, who);
+            if (lane == who) key = 0;
+        }
+    }
     int before = 0;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
@@ -257,6 +268,14 @@ __device__ __noinline__ float list_bound_64(float v, float w, int top_k, int lan
 // The ranks of a list of n candidates in order: the k-th in lane k.
 __device__ __forceinline__ uint64_t rank_list(const uint64_t *list, int n, int top_k,
                                               uint64_t *top, int lane) {
+    if (n <= 32) {                       // as nearly always: one a lane
+        const uint64_t r = lane < n ? list[lane] : 0;
+        int better = 0;
+        for (int k = 0; k < n; ++k) better += list[k] > r;
+        if (r && better < top_k) top[better] = r;
+        __syncwarp();
+        return lane < top_k ? top[lane] : 0;
+    }
     for (int c0 = 0; c0 < n; c0 += 128) {
         uint64_t r[4];
         int better[4] = {0, 0, 0, 0};
