@@ -31,8 +31,9 @@
 // nearly all of the time: the sums by issue and the latency between their steps,
 // the max by the latency of its loads.
 // Few rows of more than 4096 logits: a cluster of 4..16 CTAs a row (below).
-// Rows of at most 4096 logits: a warp a row, each chain of T one element (2048 x
-// 256: 5.5 us, 16384 x 256: 17, 65536 x 1024: 145, 65536 x 4096: 525).
+// Rows of at most 4096 logits: a warp a row, each chain of T one element (with 5
+// alternatives 2048 x 256: 5.5 us, 16384 x 256: 17, 65536 x 1000: 171, of which 38
+// are the alternatives').
 // The alternatives: with t the top_k-th largest of 32 group maxima, at least
 // top_k elements are >= t, and few more; they are listed while the exps are
 // formed and ranked by (value, lowest id) with a count of the better ones. A list
@@ -715,6 +716,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
 template <int W, bool ONE>
 __global__ void __launch_bounds__(kSmallWarps * 32, W == 2 ? 4 : ONE ? 2 : 3) logprob_small_kernel(LogprobArgs A) {
     __shared__ uint64_t lists[kSmallWarps][kSmallListed], tops[kSmallWarps][32];
+    __shared__ int counts[kSmallWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, V = A.V;
     for (int64_t row = blockIdx.x * int64_t(kSmallWarps) + warp; row < A.rows;
          row += gridDim.x * int64_t(kSmallWarps)) {
@@ -763,29 +765,28 @@ __global__ void __launch_bounds__(kSmallWarps * 32, W == 2 ? 4 : ONE ? 2 : 3) lo
         float s[8], T = 0.0f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) s[w] = 0.0f;
-        int listed = 0;
+        if (lane == 0) counts[warp] = 0;
+        __syncwarp();
         for (int g0 = 0; 4 * g0 < V; g0 += kXentLanes) {
             if (!ONE) load(g0);
             if (list) {
                 float best = -kInf;
 #pragma unroll
                 for (int w = 0; w < W; ++w) best = fmaxf(best, max4(v[w]));
-                if (__any_sync(0xffffffffu, best >= bound)) {
+                if (best >= bound)
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
                         const int j = 4 * (g0 + 32 * w + lane);
-                        if (!__any_sync(0xffffffffu, max4(v[w]) >= bound)) continue;
+                        if (max4(v[w]) >= bound)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const bool in = comp(v[w], c) >= bound && j + c < V;
-                            const unsigned who = __ballot_sync(0xffffffffu, in);
-                            const int at = listed + __popc(who & ((1u << lane) - 1u));
-                            if (in && at < kSmallListed)
-                                lists[warp][at] = rank_of(comp(v[w], c), j + c);
-                            listed += __popc(who);
-                        }
+                            for (int c = 0; c < 4; ++c)
+                                if (comp(v[w], c) >= bound && j + c < V) {
+                                    const int at = atomicAdd(&counts[warp], 1);
+                                    if (at < kSmallListed)
+                                        lists[warp][at] = rank_of(comp(v[w], c), j + c);
+                                }
                     }
-                }
+                __syncwarp();
             }
             float u[8] = {};                 // T's sums in fours
 #pragma unroll
@@ -833,6 +834,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, W == 2 ? 4 : ONE ? 2 : 3) lo
                                   __fadd_rn(__fadd_rn(f[4], f[5]), __fadd_rn(f[6], f[7])));
         uint64_t rank = 0;
         __syncwarp();
+        const int listed = counts[warp];
         if (A.top_k > 0)
             rank = !list || listed > kSmallListed
                        ? top_by_rounds(x, V, A.top_k, lane)
