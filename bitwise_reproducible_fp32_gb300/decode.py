@@ -93,7 +93,8 @@ class Decoder:
         """Takes one prompt (a sequence of token ids) for each of the given empty
         requests, fills their cache, and returns what comes next after each (rows
         in the order of requests; no targets). The prompts run as one padded
-        batch of the blocks' forward."""
+        batch of the blocks' forward. A request that finds too few free pages
+        stays empty, and check() raises."""
         import torch
 
         from bitwise_reproducible_fp32_gb300 import block, detlib as L

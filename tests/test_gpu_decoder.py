@@ -154,3 +154,33 @@ def test_refusals(dev):
     dec.check()
     with pytest.raises(ValueError):
         Decoder(cd, 0, 16, device)
+
+
+def test_two_decoders_on_two_streams(dev):
+    # rows long enough for the attention's workspace, two steps under way at once
+    c = inputs.byte_lm_cfg2(batch=2, seq=700, heads=4)
+    cd = upload(c)
+    toks = c["tokens"].reshape(2, 700)
+    logits, _ = whole(cd, toks)
+    device = torch.device("cuda")
+    decs = [Decoder(cd, 2, 4096, device, page_size=16, top_k=k) for k in (0, 32)]
+    streams = [torch.cuda.Stream() for _ in decs]
+    for dec, s, n in zip(decs, streams, (600, 690)):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            dec.prefill([0, 1], [toks[0, :n], toks[1, :n]])
+    feeds = [[i32([toks[0, n + t], toks[1, n + t]]) for t in range(10)] for n in (600, 690)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    seen = [[], []]
+    for t in range(10):
+        for i, (dec, s) in enumerate(zip(decs, streams)):
+            with torch.cuda.stream(s):
+                seen[i].append(dec.step(feeds[i][t]).logits.clone())
+    torch.cuda.synchronize()
+    for i, n in enumerate((600, 690)):
+        decs[i].check()
+        for t in range(10):
+            assert_bitwise(host(seen[i][t]), logits[:, n + t], f"decoder {i} step {t}")
+    with pytest.raises(ValueError):
+        decs[0].generate([toks[0, :3]], 2)              # no ids without top_k
