@@ -34,7 +34,7 @@
 // Rows of at most 4096 logits: a warp a row, each chain of T one element (with 5
 // alternatives 2048 x 256: 5.5 us, 16384 x 256: 17, 65536 x 1000: 171, of which 38
 // are the alternatives').
-// The alternatives: with t the top_k-th largest of 32 group maxima, at least
+// The alternatives: with t the top_k-th largest of 32 (or 64) group maxima, at least
 // top_k elements are >= t, and few more; they are listed while the exps are
 // formed and ranked by (value, lowest id) with a count of the better ones. A list
 // that overflows (many equal logits) or a row without a finite max is done by
