@@ -848,6 +848,7 @@ class _Names:
 
 
 _N = _Names
+_decode_workspaces = {}
 _default_profile = None
 
 
@@ -1064,11 +1065,21 @@ def detpages_extend(lens, new_tokens, table, free_pages, free_count, page_size, 
     tp, ldt = _mat(table, "table", i32, dev, batch)
     fp = _vec(free_pages, "free_pages", i32, dev)
     cp = _vec(free_count, "free_count", i32, dev, 1)
-    if lens_out is None and free_count_out is None and row_start is None and positions is None:
-        # one allocation for the four
-        lens_out, free_count_out, row_start, positions = _gen_empty(
-            (2 * batch + 2 + max_rows,), lens, stream).unsafe_split_with_sizes(
-                (batch, 1, batch + 1, max_rows))
+    if (lens_out is None and free_count_out is None and row_start is None and positions is None
+            and slots is None):
+        # one allocation for the four, taken apart once the launch is on its way
+        both = _gen_empty((2 * batch + 2 + max_rows,), lens, stream)
+        slots = _gen_empty((max_rows,), lens, stream, _N.i64)
+        p = both.data_ptr()
+        st = lib.detpages_extend(prof, batch, page_size, lp, np_, tp, table.size(1), ldt, fp,
+                                 free_pages.numel(), cp, max_rows, p, p + 4 * batch,
+                                 p + 4 * batch + 4, p + 8 * batch + 8, slots.data_ptr(),
+                                 _word(dev_status, dev), _gen_stream(stream, dev))
+        if st:
+            _check("detpages_extend", st)
+        lens_out, free_count_out, row_start, positions = both.unsafe_split_with_sizes(
+            (batch, 1, batch + 1, max_rows))
+        return lens_out, free_count_out, row_start, positions, slots
     if lens_out is None:
         lens_out = _gen_empty((batch,), lens, stream)
     if free_count_out is None:
@@ -1155,16 +1166,20 @@ def detdecode_attention_f32(q, k_cache, v_cache, table, kv_lens, heads, scale=No
         scale = 1.0 / float(d) ** 0.5
     max_pages = table.size(1)
     wp, wn = None, 0
-    if workspace is None:
-        need = ctypes.c_size_t(0)
-        st = lib.detdecode_attention_workspace_bytes(prof, batch, heads, c.kv_heads, d,
-                                                     max_pages * c.page_size, need)
-        if st:
-            _check("detdecode_attention_workspace_bytes", st)
-        if need.value:
-            workspace = _gen_empty(((need.value + 3) // 4,), q, stream)
     if workspace is not None:
         wp, wn = _vec(workspace, "workspace", _N.f32, dev), workspace.numel() * 4
+    else:
+        # the query's answer depends on these sizes and the device alone
+        key = (batch, heads, c.kv_heads, d, max_pages * c.page_size, dev)
+        need = _decode_workspaces.get(key)
+        if need is None:
+            need = detdecode_attention_workspace_bytes(*key[:-1], profile)
+            if len(_decode_workspaces) >= 1024:
+                _decode_workspaces.clear()
+            _decode_workspaces[key] = need
+        if need:
+            workspace = _gen_empty(((need + 3) // 4,), q, stream)
+            wp, wn = workspace.data_ptr(), workspace.numel() * 4
     st = lib.detdecode_attention_f32(prof, batch, heads, qp, ldq, c, tp, max_pages, ldt, lp, scale,
                                      op, ldo, wp, wn, _word(dev_status, dev),
                                      _gen_stream(stream, dev))
@@ -1186,8 +1201,23 @@ def detlogprob_f32(logits, tokens, top_k=0, want_stats=True, logp=None, entropy=
     xp, ld = _mat(logits, "logits", f32, dev)
     rows, V = logits.size(0), logits.size(1)
     yp = _vec(tokens, "tokens", i32, dev, rows)
-    if logp is None and entropy is None:
-        logp, entropy = _gen_empty((2, rows), logits, stream).unbind(0)
+    if logp is None and entropy is None and top_logp is None and top_ids is None and stats is None:
+        # one allocation for the floats, the stats first (16-byte alignment), taken
+        # apart once the launch is on its way
+        floats = _gen_empty((rows * ((6 if want_stats else 2) + top_k),), logits, stream)
+        top_ids = _gen_empty((rows, top_k), logits, stream, i32)
+        p = floats.data_ptr()
+        at = p + (16 * rows if want_stats else 0)
+        st = lib.detlogprob_f32(prof, rows, V, xp, ld, yp, top_k, at, at + 4 * rows,
+                                p if want_stats else None, top_ids.data_ptr(), at + 8 * rows,
+                                _word(dev_status, dev), _gen_stream(stream, dev))
+        if st:
+            _check("detlogprob_f32", st)
+        parts = floats.unsafe_split_with_sizes(
+            (4 * rows, rows, rows, top_k * rows) if want_stats else (rows, rows, top_k * rows))
+        if want_stats:
+            stats = parts[0].view(rows, 4)
+        return parts[-3], parts[-2], top_ids, parts[-1].view(rows, top_k), stats
     if logp is None:
         logp = _gen_empty((rows,), logits, stream)
     if entropy is None:
