@@ -157,7 +157,6 @@ struct LogprobArgs {
     int32_t *top_ids;
     float *top_logp;
     int32_t *dev_status;
-    int ahead;                  // 1: rows are prefetched into L2
 };
 
 // The logit whose rank this is (+0 for -0, which x - m does not tell apart).
@@ -586,10 +585,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
             if (k >= kAhead && !wait(sh.passed[k % kAhead], k / kAhead - 1)) break;
             const float *x = start_of(row);
             const int h = shift_of(x);
-            if (A.ahead && mt == 0 && row + gridDim.x < A.rows) {
-                const float *y = start_of(row + gridDim.x);
-                prefetch_granules_l2(y - shift_of(y), (V + shift_of(y) + 3) / 4);
-            }
             const int lo = h ? 1 : 0, hi = (V + h) / 4;      // granules inside the row
             const float4 *xa = reinterpret_cast<const float4 *>(x - h);
             float m = -kInf;
@@ -1111,7 +1106,7 @@ cudaError_t launch_logprob(int64_t rows, int64_t V, const float *logits, int64_t
                            float *stats, int32_t *top_ids, float *top_logp, int32_t *dev_status,
                            cudaStream_t s) {
     LogprobArgs A = {rows, int(V), logits, ld, tokens, top_k, logp, entropy,
-                     reinterpret_cast<float4 *>(stats), top_ids, top_logp, dev_status, 0};
+                     reinterpret_cast<float4 *>(stats), top_ids, top_logp, dev_status};
     const int64_t sms = sm_count_current_device();
     if (V <= kSmallVocab) {
         const int64_t blocks = std::min<int64_t>((rows + kSmallWarps - 1) / kSmallWarps, sms * 8);
@@ -1147,8 +1142,6 @@ cudaError_t launch_logprob(int64_t rows, int64_t V, const float *logits, int64_t
         return e == cudaSuccess ? cudaGetLastError() : e;
     }
     const int64_t grid = std::min<int64_t>(rows, sms);
-    // the rows between max and exps in L2, and the next one asked for where it fits
-    A.ahead = 3 * grid * V * 4 <= int64_t(96) << 20;
     const cudaError_t e = cudaFuncSetAttribute(
         logprob_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Stream)));
     if (e != cudaSuccess) return e;
