@@ -16,15 +16,17 @@
 // exps and sums of the row before run at the same time:
 //   max    8 warps read a row straight from global memory (it stays in L2): its
 //          max and the maxima of 32 groups of threads, ahead of the sums
-//   load   a lane brings the rows a second time, from L2, in segments of 4096
-//          elements through a ring in shared memory
+//   load   a lane brings the rows a second time, from L2, which may drop them then,
+//          in segments of 4096 elements through a ring in shared memory
 //   sum    8 warps, thread l the profile's chain l: groups of 4 elements two at a
 //          time, straight-line, step by step over both: e, the chain of S, T's 16
 //          chains of the thread, and a list of the groups that may hold alternatives
 //   final  a warp folds the totals, ranks the list and writes the row's results
 // Two teams of load, sum and final warps take every other row. They meet at
 // mbarriers only, every wait bounded. us for 8192 x 50257 / 16384 x 16000 /
-// 2720 x 151936 with 5 alternatives: 576 / 366 / 522 (2.9, 2.9, 3.2 TB/s); one
+// 2720 x 151936 with 5 alternatives: 541 / 363 / 512 (3.0, 2.9, 3.2 TB/s; longer
+// rows outgrow L2 between their readings, which is what bounds them: the second
+// reading kept in L2 556 / 363 / 523, the next row prefetched 576 / 364 / 695); one
 // team, four groups at a time 576 / 410 / 564; 16 warps of exps handing e to 8
 // warps of chains through shared memory 668 / 582 / 501; whole rows staged and
 // gone through phase by phase by all warps 874 / 788 / 846. Both roles are busy
@@ -632,6 +634,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
         // ---- the loads
         Team &team = sh.team[warp - kFirstLoad];
         if (lane == 0) {
+            const uint64_t evict_first = l2_policy_evict_first();
             bool ok = true;
             for (int64_t row = blockIdx.x + (warp - kFirstLoad) * int64_t(gridDim.x);
                  row < A.rows && ok; row += step) {
@@ -644,8 +647,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) logprob_stream_kernel(Logpr
                         ok = false;
                         break;
                     }
-                    load_granules(team.ring[at] - q, x - h, q, min(nch, q + kSeg + 1),
-                                  &team.loaded[at]);
+                    load_granules_last(team.ring[at] - q, x - h, q, min(nch, q + kSeg + 1),
+                                       &team.loaded[at], evict_first);
                 }
             }
         }

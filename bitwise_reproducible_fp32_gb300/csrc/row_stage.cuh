@@ -68,6 +68,27 @@ __device__ __forceinline__ void load_granules(float4 *buf, const float *xa, int 
     }
 }
 
+__device__ __forceinline__ uint64_t l2_policy_evict_first() {
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
+    return pol;
+}
+
+// load_granules of a row that is not read again: L2 may drop it first.
+__device__ __forceinline__ void load_granules_last(float4 *buf, const float *xa, int q0, int q1,
+                                                   uint64_t *bar, uint64_t evict_first) {
+    const uint32_t b = smem_u32(bar);
+    mbar_arrive_expect_tx(b, uint32_t(q1 - q0) * 16u);
+    for (int q = q0; q < q1; q += kXsPiece) {
+        const int n = min(kXsPiece, q1 - q);
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(buf + q)),
+            "l"(xa + 4 * q), "r"(uint32_t(n) * 16u), "r"(b), "l"(evict_first)
+            : "memory");
+    }
+}
+
 // Stage D for a row with misalignment H: chain l (< 256) adds the exps of its
 // groups g = l, l + 256, ... in ascending order. Group g is the last 4 - H
 // elements of granule g and the first H of granule g + 1; both granules are
