@@ -41,7 +41,8 @@
 // formed and ranked by (value, lowest id) with a count of the better ones. A list
 // that overflows (many equal logits) or a row without a finite max is done by
 // top_k maxima over the row instead. Neither way depends on the order of arrival.
-// Gradient: a thread four granules of a row; the exps again from the row's m.
+// Gradient: a thread four granules of a row; the exps again from the row's m (8192 x
+// 50257 with the entropy's 483 us, 6.8 TB/s, the rate of a copy).
 #include <cooperative_groups.h>
 
 #include <algorithm>
