@@ -63,10 +63,14 @@ class Decoder:
         self.lens, self.count = self.state[:B], self.state[B:]
         self.status = i(1)
         self.ones, self.none = i(B) + 1, torch.full((B,), -1, dtype=torch.int32, device=device)
-        # one row more than requests: an inactive request reads that one, which
-        # has no position and no slot
+        # one row more than requests: a request that takes no row in a step reads
+        # that one, which has no position and no slot
         self.row_start, self.positions = i(B + 1), i(B + 1)
         self.slots = torch.zeros(B + 1, dtype=torch.int64, device=device)
+        self.first, self.end, self.past = self.row_start[:B], self.row_start[1:], i(B) + B
+        self.took = torch.zeros(B, dtype=torch.bool, device=device)
+        self.row, self.pos = i(B), i(B)
+        self.slot = torch.zeros(B, dtype=torch.int64, device=device)
         self.buf = dict(x=f(B, D), h=f(B, D), qkv=f(B, 3 * D), att=f(B, D), o=f(B, D), x1=f(B, D),
                         h2=f(B, D), gate=f(B, Fd), up=f(B, Fd), s=f(B, Fd), dn=f(B, D), y=f(B, D))
         self.inv = f(B)
@@ -147,17 +151,20 @@ class Decoder:
         same). targets: max_batch int32 ids whose log probabilities as the next
         tokens are wanted (default: none). Returns this object's Next buffers,
         which the next step overwrites. A request that is at max_len or finds no
-        free page keeps its length, and check() raises."""
+        free page keeps its length and its cache, its rows hold nothing of use, and
+        check() raises; the others go on as if it were inactive."""
         import torch
 
         from bitwise_reproducible_fp32_gb300 import detlib as L
         c, b, B = self.model, self.buf, self.B
         new = self.ones if active is None else active
         self._extend(new, B + 1, self.row_start, self.positions, self.slots)
-        pos, slots = self.positions[:B], self.slots[:B]
-        if active is not None:
-            at = torch.where(active > 0, self.row_start[:B], B)
-            pos, slots = self.positions.index_select(0, at), self.slots.index_select(0, at)
+        # an inactive request and one refused for its length take no row, so the
+        # rows of those after them move up
+        torch.gt(self.end, self.first, out=self.took)
+        torch.where(self.took, self.first, self.past, out=self.row)
+        pos = torch.index_select(self.positions, 0, self.row, out=self.pos)
+        slots = torch.index_select(self.slots, 0, self.row, out=self.slot)
         x = L.detembedding_f32(c["emb"], tokens, out=b["x"], dev_status=self.status)
         for j, (w, (kc, vc)) in enumerate(zip(c["blocks"], self.cache)):
             if j:

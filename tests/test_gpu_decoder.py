@@ -184,3 +184,54 @@ def test_two_decoders_on_two_streams(dev):
             assert_bitwise(host(seen[i][t]), logits[:, n + t], f"decoder {i} step {t}")
     with pytest.raises(ValueError):
         decs[0].generate([toks[0, :3]], 2)              # no ids without top_k
+
+
+@pytest.mark.parametrize("full", [0, 1, 2, 3])
+@pytest.mark.parametrize("masked", [False, True])
+def test_a_full_request_leaves_the_others_alone(dev, full, masked):
+    # one request at max_len, refused in every step; one inactive when masked;
+    # the others' logits stay the forward's, step after step
+    c = inputs.byte_lm_cfg2(batch=4, seq=16)
+    cd = upload(c)
+    toks = c["tokens"].reshape(4, 16)
+    logits, _ = whole(cd, toks)
+    dec = Decoder(cd, 4, 16, torch.device("cuda"), page_size=4)
+    lens = [5, 9, 2, 7]
+    lens[full] = 16
+    dec.prefill([0, 1, 2, 3], [toks[b, :n] for b, n in enumerate(lens)])
+    on = [1] * 4
+    if masked:
+        on[(full + 2) % 4] = 0
+    active = i32(on) if masked else None
+    for t in range(5):
+        nx = dec.step(i32([int(toks[b, min(n, 15)]) for b, n in enumerate(lens)]), active)
+        got = host(nx.logits)
+        for b in range(4):
+            if on[b] and b != full:
+                assert_bitwise(got[b], logits[b, lens[b]], f"step {t}, request {b}")
+                lens[b] += 1
+        assert host(dec.lens).tolist() == lens
+    with pytest.raises(ValueError, match="status 1"):
+        dec.check()
+
+
+@pytest.mark.parametrize("masked", [False, True])
+def test_refusals_for_length_and_for_pages_in_one_step(dev, masked):
+    # request 0 is full and 2 finds no page: 1 and 3 go on as the forward does
+    c = inputs.byte_lm_cfg2(batch=4, seq=16)
+    cd = upload(c)
+    toks = c["tokens"].reshape(4, 16)
+    logits, _ = whole(cd, toks)
+    dec = Decoder(cd, 4, 16, torch.device("cuda"), page_size=4, pages=4 + 2 + 2 + 3)
+    lens = [16, 5, 8, 9]
+    dec.prefill([0, 1, 2, 3], [toks[b, :n] for b, n in enumerate(lens)])
+    dec.check()
+    for t in range(3):
+        nx = dec.step(i32([int(toks[b, min(n, 15)]) for b, n in enumerate(lens)]),
+                      i32([1] * 4) if masked else None)
+        for b in (1, 3):
+            assert_bitwise(host(nx.logits)[b], logits[b, lens[b]], f"step {t}, request {b}")
+            lens[b] += 1
+        assert host(dec.lens).tolist() == lens
+    with pytest.raises(ValueError, match="status 3"):
+        dec.check()
