@@ -1071,7 +1071,8 @@ DET_API det_status detrope_at_f32(const det_profile_v1 *prof, int64_t rows, int6
         ldo < heads * head_dim)
         return DET_ERR_INVALID_ARG;
     if (rows == 0) return DET_OK;
-    if (!x || !out || !positions || (x == out && ldx != ldo)) return DET_ERR_INVALID_ARG;
+    if (!x || !out || !positions || (x == out && rows > 1 && ldx != ldo))
+        return DET_ERR_INVALID_ARG;
     if ((st = check_device()) != DET_OK) return st;
     const RotaryArgs ro = {rotary->turns, rotary->theta, int(rotary->rot_dim), rotary->half != 0};
     return from_cuda(launch_rope_at(rows, int(heads), int(head_dim), x, ldx, positions, ro, inverse,
@@ -1093,7 +1094,7 @@ DET_API det_status detkv_append_f32(const det_profile_v1 *prof, int64_t rows, in
     if (!rotary) q_out = nullptr;
     if (q_out && ldq < heads * d) return DET_ERR_INVALID_ARG;
     if (rows == 0) return DET_OK;
-    if (!qkv || !slots || (rotary && !positions) || (q_out == qkv && ldq != ldqkv))
+    if (!qkv || !slots || (rotary && !positions) || (q_out == qkv && rows > 1 && ldq != ldqkv))
         return DET_ERR_INVALID_ARG;
     if ((st = check_device()) != DET_OK) return st;
     RotaryArgs ro = {nullptr, 1.0f, 0, 0};

@@ -654,11 +654,11 @@ typedef struct det_rotary {
  * position positions[t] (device int32) into out (row stride ldo). inverse != 0
  * turns by the negative angle: the backward, dx from dy. A negative position
  * marks padding: the row passes through unturned. out may equal x when
- * ldo == ldx (in place) and must not otherwise overlap it; columns past
- * heads * head_dim are not touched. rows may be 0.
+ * ldo == ldx or rows is 1 (in place) and must not otherwise overlap it; columns
+ * past heads * head_dim are not touched. rows may be 0.
  * Errors: DET_ERR_INVALID_ARG for negative rows, heads or head_dim outside
  * 1..65536, rot_dim odd or outside 2..head_dim, a stride below its row, null
- * pointers, or out == x with another stride. */
+ * pointers, or out == x with another stride and several rows. */
 det_status detrope_at_f32(const det_profile_v1 *prof, int64_t rows, int64_t heads,
                           int64_t head_dim, const float *x, int64_t ldx,
                           const int32_t *positions, const det_rotary *rotary, int inverse,
@@ -681,7 +681,7 @@ typedef struct det_kv_cache {
  * slots[t] (device int64), its K too, turned at positions[t], and its Q, turned,
  * to q_out (row stride ldq). rotary NULL (positions may be NULL then): K and V
  * are stored as they are and q_out is not used. q_out NULL: Q is left out; q_out
- * may be qkv itself with ldq == ldqkv (Q in place) and must not otherwise
+ * may be qkv itself with ldq == ldqkv or one row (Q in place) and must not otherwise
  * overlap qkv. The K and V blocks of qkv are not changed.
  * A negative slot (or, with rotary, a negative position) marks padding: nothing
  * is read or written for the row. A slot at or past num_pages * page_size ORs

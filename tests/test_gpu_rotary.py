@@ -245,3 +245,29 @@ def test_on_another_stream_and_captured(dev):
     xd.copy_(to_dev(2 * x))
     g.replay()
     assert_bitwise(host(out), oracle.rope_at(2 * x, pos, 4, 64))
+
+
+@pytest.mark.parametrize("rows", [1, 2])
+def test_in_place_on_the_first_columns(dev, rows):
+    # out (q_out) is a view of the rows' first columns: one row as well as several
+    rng = np.random.default_rng(15)
+    H, G, d = 4, 2, 32
+    qkv = rng.standard_normal((rows, (H + 2 * G) * d)).astype(F)
+    pos = np.arange(rows, dtype=np.int32) * 9 + 3
+    want = oracle.rope_at(qkv[:, :H * d], pos, H, d)
+    src = to_dev(qkv)
+    view = src[:, :H * d]
+    assert detlib.detrope_at_f32(src, on_gpu(pos), H, d, out=view) is view
+    assert_bitwise(host(view), want)
+    assert_bitwise(host(src)[:, H * d:], qkv[:, H * d:], "the other columns stay")
+    src = to_dev(qkv)
+    view = src[:, :H * d]
+    kc, vc = make_cache(1, 16, G, d)
+    out = detlib.detkv_append_f32(src, on_gpu(np.arange(rows, dtype=np.int64)), kc, vc, H,
+                                  positions=on_gpu(pos), q_out=view)
+    assert out is view
+    assert_bitwise(host(view), want)
+    assert_bitwise(host(src)[:, H * d:], qkv[:, H * d:], "keys and values stay")
+    assert_bitwise(host(kc)[0, :rows].reshape(rows, -1),
+                   oracle.rope_at(qkv[:, H * d:(H + G) * d], pos, G, d))
+    assert_bitwise(host(vc)[0, :rows].reshape(rows, -1), qkv[:, (H + G) * d:])
