@@ -16,6 +16,8 @@ from __future__ import annotations
 
 from typing import NamedTuple
 
+APPEND_ROWS = 1 << 20           # detkv_append_f32 takes so many rows in a call
+
 
 class Next(NamedTuple):
     """What a step (or a prompt) says about each request's next token: its logits,
@@ -135,7 +137,8 @@ class Decoder:
         for w, (kc, vc) in zip(c["blocks"], self.cache):
             x = blk.forward(x, w)
             # the block's K is turned already
-            L.detkv_append_f32(blk.qkv, slots, kc, vc, self.H, dev_status=self.status)
+            for qkv, at in zip(blk.qkv.split(APPEND_ROWS), slots.split(APPEND_ROWS)):
+                L.detkv_append_f32(qkv, at, kc, vc, self.H, dev_status=self.status)
         x = x.index_select(0, last.to(self.device))
         logits = L.detgemm_f32(x, c["head"], transB=True)
         none = torch.full((k,), -1, dtype=torch.int32, device=self.device)

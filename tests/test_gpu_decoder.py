@@ -235,3 +235,24 @@ def test_refusals_for_length_and_for_pages_in_one_step(dev, masked):
         assert host(dec.lens).tolist() == lens
     with pytest.raises(ValueError, match="status 3"):
         dec.check()
+
+
+def test_a_prompt_batch_of_more_rows_than_one_append_takes(dev):
+    # 8192 prompts, the last of 129 tokens and the others of 1: 1,056,768 padded rows
+    c = inputs.byte_lm_cfg2(batch=16, seq=132)
+    cd = upload(c)
+    toks = c["tokens"].reshape(16, 132)
+    logits, _ = whole(cd, toks)
+    B = 8192
+    dec = Decoder(cd, B, 132, torch.device("cuda"), page_size=16, pages=B + 8)
+    lens = [1] * (B - 1) + [129]
+    nx = dec.prefill(list(range(B)), [toks[b % 16, :n] for b, n in enumerate(lens)])
+    look = list(range(16)) + list(range(B - 17, B))
+    got = host(nx.logits)
+    for b in look:
+        assert_bitwise(got[b], logits[b % 16, lens[b] - 1], f"prompt {b}")
+    nx = dec.step(i32([int(toks[b % 16, n]) for b, n in enumerate(lens)]))
+    got = host(nx.logits)
+    for b in look:
+        assert_bitwise(got[b], logits[b % 16, lens[b]], f"step, request {b}")
+    dec.check()
