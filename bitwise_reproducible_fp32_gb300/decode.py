@@ -99,8 +99,9 @@ class Decoder:
         """Takes one prompt (a sequence of token ids) for each of the given empty
         requests, fills their cache, and returns what comes next after each (rows
         in the order of requests; no targets). The prompts run as one padded
-        batch of the blocks' forward. A request that finds too few free pages
-        stays empty, and check() raises."""
+        batch of the blocks' forward (at most 65,536 tokens each, what its attention
+        takes). A request that finds too few free pages stays empty, and check()
+        raises."""
         import torch
 
         from bitwise_reproducible_fp32_gb300 import block, detlib as L
@@ -114,6 +115,8 @@ class Decoder:
         if any(self.lens[torch.tensor(requests)].tolist()):
             raise ValueError("a request still holds tokens; release it first")
         T, k = max(n), len(requests)
+        # first what may refuse the sizes or find no memory: nothing is taken then
+        blk = block.Block(k, T, c["d"], c["dff"], c["heads"], self.device, self.eps, self.theta)
         order = sorted(range(k), key=lambda a: requests[a])
         new = torch.zeros(self.B, dtype=torch.int32)
         tok = torch.zeros((k, T), dtype=torch.int32)
@@ -133,7 +136,6 @@ class Decoder:
         self._extend(new.to(self.device), rows, i32(self.B + 1), i32(rows), slots)
         slots = slots.index_select(0, at.view(-1).to(self.device))
         x = L.detembedding_f32(c["emb"], tok.view(-1).to(self.device), dev_status=self.status)
-        blk = block.Block(k, T, c["d"], c["dff"], c["heads"], self.device, self.eps, self.theta)
         for w, (kc, vc) in zip(c["blocks"], self.cache):
             x = blk.forward(x, w)
             # the block's K is turned already

@@ -256,3 +256,18 @@ def test_a_prompt_batch_of_more_rows_than_one_append_takes(dev):
     for b in look:
         assert_bitwise(got[b], logits[b % 16, lens[b]], f"step, request {b}")
     dec.check()
+
+
+def test_a_refused_prompt_changes_nothing(dev):
+    # longer than the attention takes: the requests stay empty and usable
+    c = inputs.byte_lm_cfg2(batch=2, seq=16)
+    cd = upload(c)
+    toks = c["tokens"].reshape(2, 16)
+    logits, _ = whole(cd, toks)
+    dec = Decoder(cd, 2, 70000, torch.device("cuda"), page_size=16, pages=5000)
+    with pytest.raises(detlib.DetError):
+        dec.prefill([1], [np.zeros(65537, np.int32)])
+    assert host(dec.lens).tolist() == [0, 0] and int(dec.count) == 5000
+    nx = dec.prefill([1, 0], [toks[1, :5], toks[0, :16]])
+    assert_bitwise(host(nx.logits), logits[[1, 0], [4, 15]])
+    dec.check()
