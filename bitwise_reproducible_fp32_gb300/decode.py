@@ -44,8 +44,13 @@ class Decoder:
         import torch
 
         from bitwise_reproducible_fp32_gb300 import detlib as L
-        if max_batch < 1 or max_len < 1 or page_size < 1:
-            raise ValueError("max_batch, max_len and page_size must be at least 1")
+        # what a step's calls would refuse, before anything depends on it
+        if not 1 <= max_batch <= 8192:
+            raise ValueError("max_batch must be in 1..8192")
+        if max_len < 1 or page_size < 1 or (pages is not None and pages < 1):
+            raise ValueError("max_len, page_size and pages must be at least 1")
+        if not 0 <= top_k <= min(32, model["vocab"]):
+            raise ValueError(f"top_k must be in 0..{min(32, model['vocab'])}")
         self.model, self.B, self.max_len, self.device = model, max_batch, max_len, device
         self.page_size, self.top_k, self.eps, self.theta = page_size, top_k, eps, theta
         self.H, D, Fd, V = model["heads"], model["d"], model["dff"], model["vocab"]

@@ -209,3 +209,14 @@ def test_oracle_rotary_in_64_bits():
             got = oracle.rope_at(x, pos, 3, 64, turns=t, rot=rot, half=half)
             err = np.abs(got - rotate64(x, pos, t, 3, 64, half)).max(1)
             assert (err <= 7 * U * 2 * np.abs(x).max(1)).all()
+
+
+def test_a_decoder_refuses_what_its_calls_would(lib):
+    from bitwise_reproducible_fp32_gb300.decode import Decoder
+    model = dict(heads=4, d=64, dff=172, vocab=20, blocks=[])
+    for kw in (dict(max_batch=0), dict(max_batch=8193), dict(max_len=0), dict(page_size=0),
+               dict(top_k=-1), dict(top_k=21), dict(pages=0)):
+        with pytest.raises(ValueError):
+            Decoder(model, **{"max_batch": 2, "max_len": 16, "device": "cpu", **kw})
+    with pytest.raises(ValueError):
+        Decoder(dict(model, vocab=256), 2, 16, "cpu", top_k=33)
