@@ -227,3 +227,82 @@ def test_long_rows(dev, V):
     # the longest share of a cluster, and rows past it
     rng = np.random.default_rng(V)
     check((2 * rng.standard_normal((2, V))).astype(F), np.array([V - 1, 5], np.int32), 7, "offset")
+
+
+def special_rows(x, rng):
+    """Rows that leave the ordinary way, mixed between ordinary ones: a list of
+    alternatives that overflows, NaN, infinities, masks that leave a few or none."""
+    V = x.shape[1]
+    for r in range(0, len(x), 9):
+        kind = r // 9 % 7
+        if kind == 0:
+            x[r] = 0.25
+        elif kind == 1:
+            x[r, rng.integers(0, V)] = np.nan
+        elif kind == 2:
+            x[r] = -np.inf
+        elif kind == 3:
+            x[r, rng.integers(0, V)] = np.inf
+        elif kind == 4:
+            keep = rng.permutation(V)[:min(V, 10)]
+            some = x[r, keep].copy()
+            x[r] = -np.inf
+            x[r, keep] = some
+        elif kind == 5:
+            x[r, rng.random(V) < 0.5] = -np.inf
+        else:
+            x[r] = rng.integers(-2, 3, V)
+    return x
+
+
+@pytest.mark.parametrize("V,k,layout", [(4099, 32, "dense"), (4099, 5, "offset"),
+                                        (5003, 20, "padded"), (16001, 20, "dense"),
+                                        (16001, 5, "offset"), (50257, 5, "dense")])
+def test_a_cta_takes_many_rows(dev, V, k, layout):
+    # the persistent kernel: 16 rows a CTA (8 a team) and a few more, so that
+    # every slot, barrier phase and list is used again several times; 50257: 5
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = (16 if V < 50000 else 5) * sms + 5
+    rng = np.random.default_rng(V + k)
+    x = special_rows((2 * rng.standard_normal((rows, V), dtype=F)), rng)
+    y = rng.integers(0, V, rows)
+    y[::11] = -1
+    check(x, y, k, layout)
+    assert detlib.det_watchdog_status() == 0
+
+
+@pytest.mark.parametrize("rows,V", [(12001, 300), (12001, 20), (10007, 1500), (70003, 7)])
+def test_a_warp_takes_many_rows(dev, rows, V):
+    # more rows than the short rows' kernel has warps; 70003: more than the
+    # gradient's grid has rows
+    rng = np.random.default_rng(V)
+    x = special_rows((2 * rng.standard_normal((rows, V), dtype=F)), rng)
+    y = rng.integers(0, V, rows)
+    y[::13] = -1
+    check(x, y, min(V, 20), "padded")
+
+
+@pytest.mark.parametrize("rows", [3, 700])
+def test_long_rows_captured(dev, rows):
+    # over clusters (3 rows) and over persistent CTAs
+    rng = np.random.default_rng(rows)
+    V = 20011
+    x = (2 * rng.standard_normal((rows, V))).astype(F)
+    y = rng.integers(0, V, rows).astype(np.int32)
+    want = oracle.logprob(x, y, 6)
+    xd, yd = to_dev(x), on_gpu(y)
+    outs = [torch.empty_like(t) for t in detlib.detlogprob_f32(xd, yd, top_k=6)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        detlib.detlogprob_f32(xd, yd, top_k=6, logp=outs[0], entropy=outs[1], top_ids=outs[2],
+                              top_logp=outs[3], stats=outs[4])
+    for flip in (True, False, True):
+        xd.copy_(to_dev(x[::-1].copy() if flip else x))
+        yd.copy_(on_gpu(y[::-1].copy() if flip else y))
+        for o in outs:
+            o.fill_(7)
+        g.replay()
+        step = -1 if flip else 1
+        for o, w in ((0, 0), (1, 1), (3, 4), (4, 2)):
+            assert_bitwise(host(outs[o]), np.ascontiguousarray(want[w][::step]))
+        assert np.array_equal(host(outs[2]), want[3][::step])
