@@ -24,7 +24,7 @@
 //   final  a warp folds the totals, ranks the list and writes the row's results
 // Two teams of load, sum and final warps take every other row. They meet at
 // mbarriers only, every wait bounded. us for 8192 x 50257 / 16384 x 16000 /
-// 2720 x 151936 with 5 alternatives: 541 / 363 / 512 (3.0, 2.9, 3.2 TB/s; longer
+// 2720 x 151936 with 5 alternatives: 544 / 364 / 513 (3.0, 2.9, 3.2 TB/s; longer
 // rows outgrow L2 between their readings, which is what bounds them: the second
 // reading kept in L2 556 / 363 / 523, the next row prefetched 576 / 364 / 695); one
 // team, four groups at a time 576 / 410 / 564; 16 warps of exps handing e to 8
@@ -34,7 +34,7 @@
 // the max by the latency of its loads.
 // Few rows of more than 4096 logits: a cluster of 4..16 CTAs a row (below).
 // Rows of at most 4096 logits: a warp a row, each chain of T one element (with 5
-// alternatives 2048 x 256: 5.5 us, 16384 x 256: 17, 65536 x 1000: 171, of which 38
+// alternatives 2048 x 256: 5.5 us, 16384 x 256: 16, 65536 x 1000: 172, of which 38
 // are the alternatives').
 // The alternatives: with t the top_k-th largest of 32 (or 64) group maxima, at least
 // top_k elements are >= t, and few more; they are listed while the exps are
@@ -314,10 +314,14 @@ __device__ __forceinline__ float exp_and_t(const float4 (&v)[N], f32x2 m2, float
         d[2 * i] = sub2(pack2(v[i].x, v[i].y), m2);
         d[2 * i + 1] = sub2(pack2(v[i].z, v[i].w), m2);
     }
-    // d log2 e rounded on its own: a fused step with -0 (which changes no product),
-    // as a packed multiply that feeds a packed add rounds as if fused with it
+    // d log2 e rounded on its own by scalar multiplies: a packed multiply that feeds a
+    // packed add rounds as if fused with it, and so does a packed fma with -0
 #pragma unroll
-    for (int i = 0; i < 2 * N; ++i) tm[i] = fma2(d[i], splat2(kLog2e), splat2(-0.0f));
+    for (int i = 0; i < 2 * N; ++i) {
+        float d0, d1;
+        unpack2(d[i], d0, d1);
+        tm[i] = pack2(__fmul_rn(d0, kLog2e), __fmul_rn(d1, kLog2e));
+    }
 #pragma unroll
     for (int i = 0; i < 2 * N; ++i) tm[i] = add2(tm[i], splat2(kRoundMagic));
     f32x2 n[2 * N], r[2 * N];

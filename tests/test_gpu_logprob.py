@@ -6,6 +6,7 @@ import pytest
 import oracle
 from bitcmp import assert_bitwise
 from bitwise_reproducible_fp32_gb300 import detlib
+from exp_cases import exp_tie_arguments
 from gen_util import F, U, logprob64
 from gpu_util import host, need_gpu, to_dev, torch
 
@@ -306,3 +307,48 @@ def test_long_rows_captured(dev, rows):
         for o, w in ((0, 0), (1, 1), (3, 4), (4, 2)):
             assert_bitwise(host(outs[o]), np.ascontiguousarray(want[w][::step]))
         assert np.array_equal(host(outs[2]), want[3][::step])
+
+
+@pytest.mark.parametrize("V,rows", [(2, None), (30, None), (256, None), (300, None), (1023, None),
+                                    (1500, None), (4096, None), (4099, None), (5003, 6),
+                                    (50257, 2)])
+@pytest.mark.parametrize("layout", ["dense", "offset"])
+def test_exps_at_the_ties_of_their_rounding(dev, V, rows, layout):
+    # rows [0, d, d, ...]: at these d the exp's integer n is d log2 e rounded to a
+    # float and then to an integer; rounded once, it is another one, and e and
+    # with it S and T move by a step
+    d = exp_tie_arguments(-127, 0)
+    x = np.repeat(d[:, None], V, 1)
+    x[:, 0] = 0.0
+    y = np.ones(len(d), np.int32)
+    want = oracle.logprob(x, y, 1)
+    for r0 in range(0, len(d), rows or len(d)):
+        part = slice(r0, r0 + (rows or len(d)))
+        logp, ent, _, _, stats = detlib.detlogprob_f32(to_dev(x[part], layout), on_gpu(y[part]))
+        for got, w, name in ((logp, want[0], "logp"), (ent, want[1], "entropy"),
+                             (stats, want[2], "stats")):
+            assert_bitwise(host(got), w[part], f"{name} of rows from {r0}")
+
+
+def test_every_float_below_0_in_short_rows(dev):
+    # rows [0, d, d, d, -inf ..., d, d, d, d, -inf ...]: one lane forms all seven exps,
+    # in its groups 0 and 32, for every d in [-104, -2^-26]; what S and T are then is
+    # formed from detexp_f32 and detlog_f32 (themselves tested on every float)
+    lo, hi = (int(np.array(v, F).view(np.uint32)) for v in (-2.0 ** -26, -104.0))
+    step = 1 << 22
+    x = torch.full((step, 256), -np.inf, device="cuda")
+    x[:, 0] = 0.0
+    y = torch.ones(step, dtype=torch.int32, device="cuda")
+    for at in range(lo, hi + 1, step):
+        d = torch.arange(at, at + step, device="cuda").int().view(torch.float32)
+        x[:, 1:4] = d[:, None]
+        x[:, 128:132] = d[:, None]
+        logp, ent, _, _, _ = detlib.detlogprob_f32(x, y, want_stats=False)
+        e = detlib.detexp_f32(d)
+        t = e * d
+        S = (((1.0 + e) + e) + e) + (((e + e) + e) + e)
+        T = ((t + t) + t) + (((t + t) + t) + t)
+        log_s = detlib.detlog_f32(S)
+        for got, w, name in ((logp, d - log_s, "logp"), (ent, log_s - T / S, "entropy")):
+            diff = got.view(torch.int32) != w.view(torch.int32)
+            assert not diff.any(), (name, int(diff.sum()), d[diff][:5].tolist())
