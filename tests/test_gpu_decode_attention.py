@@ -7,6 +7,7 @@ import pytest
 
 from bitcmp import assert_bitwise
 from bitwise_reproducible_fp32_gb300 import detlib
+from exp_cases import exp_tie_arguments
 from gen_util import F, LAYOUTS, decode64, decode_oracle, fill_cache
 from gpu_util import host, need_gpu, to_dev, torch
 
@@ -178,3 +179,30 @@ def test_captured_replayed_and_on_another_stream(dev):
         g.replay()
         assert_bitwise(host(out), decode_oracle(q, [k[:m] for k, m in zip(Ks, n)],
                                                 [v[:m] for v, m in zip(Vs, n)], 4, 0.125))
+
+
+@pytest.mark.parametrize("H,G", [(1, 1), (2, 1), (4, 1), (8, 1), (3, 3)])
+@pytest.mark.parametrize("n", [256, 3000])
+def test_exps_at_the_ties_of_their_rounding(dev, H, G, n):
+    # scores 0, then every d at which rounding d log2 e once or twice differs, 128 a
+    # request; a value has a one where its token is, so the outputs are the
+    # probabilities one by one
+    ties, w = exp_tie_arguments(-127, 0), 128
+    rng = np.random.default_rng(n + H)
+    Ks, Vs = [], []
+    for r in range(-(-len(ties) // w)):
+        part = ties[r * w:(r + 1) * w]
+        K, V = np.zeros((n, G, w), F), np.zeros((n, G, w), F)
+        K[1:, :, 0] = -F(200.0)
+        at = 1 + rng.permutation(n - 1)[:len(part)]
+        K[at, :, 0] = part[:, None]
+        V[at, :, np.arange(len(part))] = 1.0
+        Ks.append(K)
+        Vs.append(V)
+    lens = [n] * len(Ks)
+    kc, vc, table, _, _ = fill_cache(lens, 16, G, w, "token", rng, K=Ks, V=Vs)
+    q = np.zeros((len(Ks), H * w), F)
+    q[:, ::w] = 1.0
+    got = host(run(q, kc, vc, table, lens, H, scale=1.0))
+    assert_bitwise(got, decode_oracle(q, Ks, Vs, H, 1.0))
+    assert (got != 0).sum() > 300 * H

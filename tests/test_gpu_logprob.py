@@ -352,3 +352,14 @@ def test_every_float_below_0_in_short_rows(dev):
         for got, w, name in ((logp, d - log_s, "logp"), (ent, log_s - T / S, "entropy")):
             diff = got.view(torch.int32) != w.view(torch.int32)
             assert not diff.any(), (name, int(diff.sum()), d[diff][:5].tolist())
+
+
+def test_gradient_at_the_ties_of_the_exps_rounding(dev):
+    # rows [0, every such d, -inf ...]: the probabilities one by one
+    d = exp_tie_arguments(-127, 0)
+    for V in (len(d) + 1, 5003):
+        x = np.full((3, V), -np.inf, F)
+        x[:, 0] = 0.0
+        for r in range(3):
+            x[r, 1:len(d) + 1] = np.roll(d, r)
+        check(x, np.array([-1, 0, 7]), 20, "offset")
