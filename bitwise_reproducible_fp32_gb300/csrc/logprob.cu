@@ -384,6 +384,23 @@ __device__ __noinline__ ExpT exp_slow(float4 v, float m, float4 t) {
     return {make_float4(e[0], e[1], e[2], e[3]), make_float4(c[0], c[1], c[2], c[3])};
 }
 
+// One thread: copies granules [q0, q1) of the row whose aligned base is xa into
+// the same granules of buf, completing on bar; the row is not read again, so L2
+// may drop it first.
+__device__ __forceinline__ void load_granules_last(float4 *buf, const float *xa, int q0, int q1,
+                                                   uint64_t *bar, uint64_t evict_first) {
+    const uint32_t b = smem_u32(bar);
+    mbar_arrive_expect_tx(b, uint32_t(q1 - q0) * 16u);
+    for (int q = q0; q < q1; q += kXsPiece) {
+        const int n = min(kXsPiece, q1 - q);
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(buf + q)),
+            "l"(xa + 4 * q), "r"(uint32_t(n) * 16u), "r"(b), "l"(evict_first)
+            : "memory");
+    }
+}
+
 struct RowState {                       // of the rows 0 and 1 mod 2 of a CTA
     float4 found[kFound];               // the listed groups, and where they start
     int found_at[kFound];
