@@ -47,8 +47,11 @@ class Decoder:
         # what a step's calls would refuse, before anything depends on it
         if not 1 <= max_batch <= 8192:
             raise ValueError("max_batch must be in 1..8192")
-        if max_len < 1 or page_size < 1 or (pages is not None and pages < 1):
-            raise ValueError("max_len, page_size and pages must be at least 1")
+        # past 2^20 the rotary's angles are NaN
+        if not 1 <= max_len <= 1 << 20:
+            raise ValueError("max_len must be in 1..2^20")
+        if page_size < 1 or (pages is not None and pages < 1):
+            raise ValueError("page_size and pages must be at least 1")
         if not 0 <= top_k <= min(32, model["vocab"]):
             raise ValueError(f"top_k must be in 0..{min(32, model['vocab'])}")
         self.model, self.B, self.max_len, self.device = model, max_batch, max_len, device

@@ -214,7 +214,8 @@ def test_oracle_rotary_in_64_bits():
 def test_a_decoder_refuses_what_its_calls_would(lib):
     from bitwise_reproducible_fp32_gb300.decode import Decoder
     model = dict(heads=4, d=64, dff=172, vocab=20, blocks=[])
-    for kw in (dict(max_batch=0), dict(max_batch=8193), dict(max_len=0), dict(page_size=0),
+    for kw in (dict(max_batch=0), dict(max_batch=8193), dict(max_len=0), dict(max_len=2 ** 20 + 1, pages=9),
+               dict(page_size=0),
                dict(top_k=-1), dict(top_k=21), dict(pages=0)):
         with pytest.raises(ValueError):
             Decoder(model, **{"max_batch": 2, "max_len": 16, "device": "cpu", **kw})
