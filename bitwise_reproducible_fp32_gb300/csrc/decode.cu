@@ -35,8 +35,11 @@
 // over V run at HBM's rate, the rest is 30 us between them and the longest
 // request's tail. 32 heads over 4, 32 requests of 2000..4096, 129 us (3.1 TB/s): the
 // longest is a third longer than the mean, and the 8 heads' multiply-adds and
-// shared-memory reads keep a warp about as long as its pieces' arrival. Asking L2
-// for 4 or more pieces of V ahead while the CTAs meet ran 1..10% slower.
+// shared-memory reads keep a warp about as long as its pieces' arrival. A unit has at
+// most 16 CTAs, so few requests of few key-value heads leave most of the GPU idle: one
+// of 32768 tokens takes 107 us over one head of 128 for 8 query heads (33.6 MB, 0.3
+// TB/s), 102 over 8 such heads for 32, 40 over one head of 64. Asking L2 for 4 or more
+// pieces of V ahead while the CTAs meet ran 1..10% slower.
 #include <cooperative_groups.h>
 
 #include <algorithm>

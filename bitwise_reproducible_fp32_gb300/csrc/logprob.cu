@@ -30,17 +30,29 @@
 // team, four groups at a time 576 / 410 / 564; 16 warps of exps handing e to 8
 // warps of chains through shared memory 668 / 582 / 501; whole rows staged and
 // gone through phase by phase by all warps 874 / 788 / 846. Both roles are busy
-// nearly all of the time: the sums by issue and the latency between their steps,
-// the max by the latency of its loads.
+// nearly all of the time: the sums by the latency between their steps, the max by
+// that of its loads; instructions issue in 48% of the cycles. All 28 warps have the
+// same 72 registers, too few for the sums, which spill 172 bytes.
 // Few rows of more than 4096 logits: a cluster of 4..16 CTAs a row (below).
 // Rows of at most 4096 logits: a warp a row, each chain of T one element (with 5
 // alternatives 2048 x 256: 5.5 us, 16384 x 256: 16, 65536 x 1000: 172, of which 38
-// are the alternatives').
+// are the alternatives'). A row that does not fill its last sweep pays for it: what
+// is past its end counts as -inf, and the exps of a thread that has any of it are
+// formed again in the general way (65536 x 1024: 124 us; 32768 x 4000: 202, 32768 x
+// 4096: 162).
 // The alternatives: with t the top_k-th largest of 32 (or 64) group maxima, at least
 // top_k elements are >= t, and few more; they are listed while the exps are
 // formed and ranked by (value, lowest id) with a count of the better ones. A list
-// that overflows (many equal logits) or a row without a finite max is done by
-// top_k maxima over the row instead. Neither way depends on the order of arrival.
+// that overflows or a row without a finite max is done by top_k maxima over the row
+// instead, by one warp. Neither way depends on the order of arrival. Lists overflow
+// with many equal logits, and where fewer than top_k groups hold a logit above -inf
+// (t is -inf then): in rows masked down to a few tokens, and over a cluster of 16 in
+// rows of at most 8192 logits, of 8 in rows of at most 6144, whose shares leave groups
+// empty (8 x 8000 for 16 alternatives 7.8 us, for 17 30).
+// Masks: a -inf among a thread's 8 elements takes all 8 through the general exps. us
+// for 5 / 20 alternatives with nothing, half, 99% and all but 10 masked: 8192 x 50257
+// 544 / 589, 1913 / 1931, 1505 / 1532, 1347 / 5152; 64 x 50257 15 / 16, 19 / 20,
+// 19 / 20, 18 / 151.
 // Gradient: a thread four granules of a row; the exps again from the row's m (8192 x
 // 50257 with the entropy's 483 us, 6.8 TB/s, the rate of a copy).
 #include <cooperative_groups.h>

@@ -11,10 +11,11 @@
 // group and not once a head; the first batch is on its way while they are. Rows
 // with other alignments or odd sizes take units of one pair (or one element where
 // nothing turns).
-// Measured in a graph, inputs beyond L2: 8192 rows of 24 heads of 64 turned in
-// 14.9 us (6.8 TB/s); the backward of 4099 rows of 40 heads of 128, half of each
-// turned, 34 us (4.9 TB/s); 8192 rows of 32 + 2 x 8 heads of 128, 7/8 of them
-// kept, appended in 70 us (5.0 TB/s).
+// Measured in a graph, inputs and outputs beyond L2: 8192 rows of 24 heads of 64
+// turned in 17.9 us (5.6 TB/s; 14.3 where the calls share an output, which stays in
+// L2), in the half layout 22.4 (4.5 TB/s); the backward of 4099 rows of 40 heads of
+// 128, half of each turned, 34 us (4.9 TB/s); 8192 rows of 32 + 2 x 8 heads of 128,
+// 7/8 of them kept, appended in 70 us (5.0 TB/s).
 #include <algorithm>
 
 #include "det_internal.cuh"
@@ -199,7 +200,9 @@ constexpr int kFilterBits = 4096;
 // the earlier row's K and V are not written, so the cache always holds the last
 // one: each CTA with K or V heads looks through the slots after its rows, most of
 // which a bit filter of its own slots' low bits passes over at once (comparing
-// each with the tile's 16: 63 us instead of 32 for 8192 rows of 36 heads of 64).
+// each with the tile's 16: 63 us instead of 32 for 8192 rows of 36 heads of 64). The
+// search grows with the square of the rows: 8192 rows of 1 + 2 x 1 heads of 64 take
+// 15.5 us, 65536 252 us, 2^18 3.6 ms, 2^20 55 ms.
 // Four CTAs an SM: with more registers for loads over the search, 96 us instead of
 // 70 for the 8192 rows above.
 template <int MODE>
@@ -296,8 +299,12 @@ int units_of(UnitMode m, int head_dim, int rot) {
     return rot / (2 * pairs) + (head_dim - rot) / wide;
 }
 
-// Heads a thread walks: as many as leave the GPU one full load of threads, in
-// equal groups of whole batches. Fewer heads form each angle more often (8192
+// Heads a thread walks: as many as leave the GPU 2048 threads an SM, in groups of
+// whole batches, equal but for the last. The kernels' registers let 1024 (half
+// layout, append) or 1280 (interleaved) run at once, so this is about two waves; the
+// last one is not full (4099 rows of 40 heads: 1540 CTAs on 608 places; 8192 rows of 24
+// heads of 64, interleaved: 1536 on 760). Fewer
+// heads form each angle more often (8192
 // rows of 32 + 16 heads of 128 appended: 16 heads 70 us, 4 heads 85), more leave
 // SMs idle (64 rows of 36 heads of 64: 4 heads 5.2 us, 48 heads 9.8) or the last
 // group short (4099 rows of 40 heads turned: 12 heads 34 us, 16 heads 37).

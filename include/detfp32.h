@@ -713,9 +713,9 @@ det_status detkv_append_f32(const det_profile_v1 *prof, int64_t rows, int64_t he
  * the step; they must not overlap lens and free_count.
  * A request gets all of its tokens or none: one with a negative length or
  * count, or more tokens than its table row holds, takes no rows and ORs 1 into
- * *dev_status (may be NULL); one whose pages or those of the requests before
- * it run out ORs 2, and one whose rows end past max_rows ORs 4: the rows of
- * these hold -1 and their lengths stay. A *free_count outside 0..capacity
+ * *dev_status (may be NULL); one that needs pages where they run out, for it or a
+ * request before it, ORs 2, and one whose rows end past max_rows ORs 4: the rows
+ * of these hold -1 and their lengths stay. A *free_count outside 0..capacity
  * counts as 0 and ORs 1.
  * batch 0..8192; one launch. Errors: DET_ERR_INVALID_ARG for sizes outside
  * their ranges (page_size >= 1, max_pages >= 1, ldt >= max_pages, 0 <= max_rows,
@@ -733,9 +733,10 @@ det_status detpages_extend(const det_profile_v1 *prof, int64_t batch, int64_t pa
  * *free_count on, by ascending request, then position; lens_out[b] = 0. The
  * other requests' lengths are copied to lens_out, and free_count_out is the
  * count after. The table is not changed. A done request with a length outside
- * its table row ORs 1 into *dev_status; one whose pages do not fit the
- * free list's capacity ORs 2; both keep their length. Sizes and errors as
- * detpages_extend. */
+ * its table row ORs 1 into *dev_status; one whose pages, after those of the done
+ * requests before it, do not fit the free list's capacity ORs 2; both keep their
+ * length. A *free_count outside 0..capacity counts as 0 and ORs 1. Sizes and
+ * errors as detpages_extend. */
 det_status detpages_release(const det_profile_v1 *prof, int64_t batch, int64_t page_size,
                             const int32_t *lens, const int32_t *done, const int32_t *table,
                             int64_t max_pages, int64_t ldt, int32_t *free_pages,
