@@ -739,8 +739,10 @@ cudaError_t launch_decode_attention(int64_t batch, int heads, const float *q, in
     auto run = [&](auto kern) {
         const size_t smem =
             size_t(p.stages) * kRingBytes + fixed_bytes(p.unit_heads) + size_t(p.room) * 4;
+        // the most any plan takes: the limit is the kernel's, and another thread's call
+        // of another size may come between this line and the launch
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(smem));
+                                             kSmemPerCta);
         if (e == cudaSuccess && p.cluster > 8)
             e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;

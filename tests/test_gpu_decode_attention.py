@@ -2,6 +2,8 @@
 against the last row of the training attention, and against 64 bits within a
 derived bound; lengths from 0 to long, page sizes that end inside every tile,
 layouts, shared heads, infinities and NaN, bad lengths and pages."""
+import threading
+
 import numpy as np
 import pytest
 
@@ -206,3 +208,34 @@ def test_exps_at_the_ties_of_their_rounding(dev, H, G, n):
     got = host(run(q, kc, vc, table, lens, H, scale=1.0))
     assert_bitwise(got, decode_oracle(q, Ks, Vs, H, 1.0))
     assert (got != 0).sum() > 300 * H
+
+
+def test_two_threads_at_once(dev):
+    # short rows, and many of four chunks a CTA, whose launches take different amounts
+    # of shared memory, from two host threads on streams of their own
+    rng = np.random.default_rng(27)
+    jobs = []
+    for lens in ([200, 17], [1000] * 40):
+        kc, vc, table, Ks, Vs = fill_cache(lens, 16, 4, 64, "token", rng)
+        q = rng.standard_normal((len(lens), 256)).astype(F)
+        jobs.append((to_dev(q), kc, vc, table, on_gpu(np.array(lens, np.int32)),
+                     decode_oracle(q, Ks, Vs, 4, 0.125)))
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(job):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(4000):
+                    out = detlib.detdecode_attention_f32(*job[:5], 4)
+                got = host(out)
+            assert_bitwise(got, job[5])
+        except Exception as e:      # noqa: BLE001 (an error of the other thread)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(job,)) for job in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
