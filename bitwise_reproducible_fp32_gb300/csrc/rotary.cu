@@ -303,11 +303,10 @@ int units_of(UnitMode m, int head_dim, int rot) {
 // whole batches, equal but for the last. The kernels' registers let 1024 (half
 // layout, append) or 1280 (interleaved) run at once, so this is about two waves; the
 // last one is not full (4099 rows of 40 heads: 1540 CTAs on 608 places; 8192 rows of 24
-// heads of 64, interleaved: 1536 on 760). Fewer
-// heads form each angle more often (8192
-// rows of 32 + 16 heads of 128 appended: 16 heads 70 us, 4 heads 85), more leave
-// SMs idle (64 rows of 36 heads of 64: 4 heads 5.2 us, 48 heads 9.8) or the last
-// group short (4099 rows of 40 heads turned: 12 heads 34 us, 16 heads 37).
+// heads of 64, interleaved: 1536 on 760). Fewer heads form each angle more often
+// (8192 rows of 32 + 16 heads of 128 appended: 16 heads 70 us, 4 heads 85), more
+// leave SMs idle (64 rows of 36 heads of 64: 4 heads 5.2 us, 48 heads 9.8) or the
+// last group short (4099 rows of 40 heads turned: 12 heads 34 us, 16 heads 37).
 int head_group(int64_t threads, int heads) {
     const int64_t full = int64_t(sm_count_current_device()) * 2048;
     const int64_t want = std::max<int64_t>((heads * threads + full - 1) / full, 1);
