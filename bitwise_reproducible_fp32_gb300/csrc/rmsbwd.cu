@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rmsbwd_rows_bulk_kernel(const 
     fold_partials(a);
 }
 
+constexpr size_t kRowsBulkMax = 200 * 1024;
 size_t rows_bulk_smem(int64_t D) { return 128 + size_t(2 * kRowWarps + 1) * size_t(D) * 4 + 8; }
 
 // Any alignment and any D: the same operations with scalar loads, in two
@@ -325,15 +326,16 @@ cudaError_t launch_rmsnorm_bwd(int64_t rows, int64_t D, const float *x, int64_t 
     if (nchunks > 1) blocks = std::max<int64_t>(blocks, (D + kRowWarps * 32 - 1) / (kRowWarps * 32));
     const dim3 grid{unsigned(blocks)}, block{unsigned(kRowWarps * 32)};
     const size_t bulk_smem = rows_bulk_smem(D);
-    const bool bulk = D % 4 == 0 && bulk_smem <= 200 * 1024 && aligned16(x) && aligned16(dy) &&
+    const bool bulk = D % 4 == 0 && bulk_smem <= kRowsBulkMax && aligned16(x) && aligned16(dy) &&
                       aligned16(dx) && aligned16(gain) && ldx == D && lddy == D &&
                       lddx % 4 == 0;
     if (!bulk) {
         rmsbwd_rows_kernel<<<grid, block, 0, s>>>(ra);
         return cudaGetLastError();
     }
+    // the limit at its most, not this call's: another thread's may come in between
     e = cudaFuncSetAttribute(rmsbwd_rows_bulk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(bulk_smem));
+                             int(kRowsBulkMax));
     if (e != cudaSuccess) return e;
     // launched as a programmatic dependent of the column kernel: its rows run
     // alongside the column chains, and the fold waits for them

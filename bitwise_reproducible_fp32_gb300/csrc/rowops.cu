@@ -728,6 +728,10 @@ constexpr int stream_slots(int64_t D, int inputs) {
 __host__ __device__ constexpr size_t stream_smem(int D, int S, int inputs = 1) {
     return 128 + size_t(inputs * S * kRowsPerSlot + 1) * size_t(D) * 4 + size_t(2 * S + 1) * 8;
 }
+// The most it gives: what the kernel's limit is set to in every call (as the other
+// kernels' limits are set to constants), for a call of another size from another
+// thread may come between the setting and the launch.
+constexpr int kStreamSmemMax = int(kStreamSmemBudget) - 128 + (2 * kStreamMaxSlots + 1) * 8;
 
 // With b_in given (the fused residual add), a slot holds the rows of x and of
 // b_in (two bulk copies on its mbarrier; both dense with row stride ldx), each
@@ -920,7 +924,7 @@ cudaError_t launch_rmsnorm(int64_t rows, int64_t D, const float *x, int64_t ldx,
         const size_t smem = stream_smem(int(D), S);
         cudaError_t e = cudaFuncSetAttribute(rmsnorm_stream_kernel,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(smem));
+                                             kStreamSmemMax);
         if (e != cudaSuccess) return e;
         const int64_t g = std::min<int64_t>(rows, sm_count_current_device());
         return launch_dependent(rmsnorm_stream_kernel, dim3(unsigned(g)), dim3(kStreamThreads),
@@ -959,7 +963,7 @@ cudaError_t launch_add_rmsnorm(int64_t rows, int64_t D, const float *a, const fl
         const size_t smem = stream_smem(int(D), S, 2);
         cudaError_t e = cudaFuncSetAttribute(rmsnorm_stream_kernel,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(smem));
+                                             kStreamSmemMax);
         if (e != cudaSuccess) return e;
         const int64_t g = std::min<int64_t>(rows, sm_count_current_device());
         return launch_dependent(rmsnorm_stream_kernel, dim3(unsigned(g)), dim3(kStreamThreads),
@@ -979,7 +983,7 @@ cudaError_t launch_xent(int64_t rows, int64_t V, const float *logits, int64_t ld
     if (max_granules <= kXsMaxGranules) {
         const size_t smem = size_t(max_granules) * 16;
         e = cudaFuncSetAttribute(xent_smem_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 int(smem));
+                                 kXsMaxGranules * 16);
         if (e != cudaSuccess) return e;
         const int64_t grid = std::min<int64_t>(rows, int64_t(sm_count_current_device()));
         xent_smem_kernel<<<unsigned(grid), kXsThreads, smem, s>>>(
