@@ -65,7 +65,7 @@ typedef enum det_status {
     DET_ERR_INVALID_ARG = 1,        /* null pointer, negative size, ld too small */
     DET_ERR_PROFILE = 2,            /* profile version or field not implemented */
     DET_ERR_UNSUPPORTED_DEVICE = 3, /* current device is not compute capability 10.3 */
-    DET_ERR_ALIGNMENT = 4,          /* reserved */
+    DET_ERR_ALIGNMENT = 4,          /* detlogprob's stats not 16-byte aligned */
     DET_ERR_WORKSPACE = 5,          /* workspace too small or misaligned */
     DET_ERR_TIMEOUT = 6,            /* a device-side bounded wait gave up */
     DET_ERR_CUDA = 7                /* a CUDA runtime call or launch failed */
