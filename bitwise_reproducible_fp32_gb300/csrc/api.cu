@@ -1230,6 +1230,125 @@ DET_API det_status detlogprob_bwd_f32(const det_profile_v1 *prof, int64_t rows, 
                                         dlogits, ldd, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------- several answers of a prompt
+namespace {
+constexpr int64_t kBeamsMax = 32;
+constexpr int64_t kPagesMax = int64_t(1) << 23;   // page marks fit a cluster's shared memory
+}  // namespace
+
+DET_API det_status detbeam_select_f32(const det_profile_v1 *prof, int64_t requests,
+                                      const det_beams *in, const det_beams *out, int64_t top_k,
+                                      const int32_t *top_ids, const float *top_logp, int32_t eos,
+                                      const float *weights, int64_t nweights, int64_t hist_cols,
+                                      int32_t *tokens, int32_t *parents, int32_t *forks,
+                                      int32_t *dev_status, det_stream_t stream) {
+    det_status st = check_profile(prof);
+    if (st != DET_OK) return st;
+    if (!in || !out || in->beams < 1 || in->beams > kBeamsMax || out->beams < 1 ||
+        out->beams > kBeamsMax || top_k < 1 || top_k > kTopMax || requests < 0 ||
+        requests * std::max(in->beams, out->beams) > kDimMax || requests > kDimMax ||
+        hist_cols < 0 || hist_cols > kDimMax || (weights && nweights < 1))
+        return DET_ERR_INVALID_ARG;
+    if (requests == 0) return DET_OK;
+    if (!in->hist != !out->hist || ((in->hist || weights || out->lens) && !in->lens) ||
+        (in->hist && (in->ldh < hist_cols || out->ldh < hist_cols)))
+        return DET_ERR_INVALID_ARG;
+    if (!in->scores || !out->scores || !top_ids || !top_logp || !tokens || !parents ||
+        in->scores == out->scores || (in->finished && in->finished == out->finished) ||
+        (in->lens && in->lens == out->lens) || (in->hist && in->hist == out->hist))
+        return DET_ERR_INVALID_ARG;
+    if ((st = check_device()) != DET_OK) return st;
+    return from_cuda(launch_beam_select(requests, *in, *out, int(top_k), top_ids, top_logp, eos,
+                                        weights, nweights, hist_cols, tokens, parents, forks,
+                                        dev_status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+DET_API det_status detpages_fork(const det_profile_v1 *prof, int64_t batch, int64_t batch_out,
+                                 int64_t page_size, int64_t num_pages, const int32_t *lens,
+                                 const int32_t *parents, const int32_t *table, int64_t max_pages,
+                                 int64_t ldt, int32_t *table_out, int64_t ldto,
+                                 int32_t *free_pages, int64_t capacity, const int32_t *free_count,
+                                 int32_t *lens_out, int32_t *free_count_out, int32_t *src,
+                                 int32_t *dst, int32_t *tokens, int32_t *dev_status,
+                                 det_stream_t stream) {
+    det_status st = check_profile(prof);
+    if (st != DET_OK) return st;
+    if (!pages_ok(batch, page_size, max_pages, ldt, capacity) || batch_out < 0 ||
+        batch_out > 8192 || ldto < max_pages || num_pages < 0 || num_pages > kPagesMax)
+        return DET_ERR_INVALID_ARG;
+    if (!free_count || !free_count_out || free_count == free_count_out ||
+        (capacity > 0 && !free_pages) || (batch > 0 && (!lens || !table)))
+        return DET_ERR_INVALID_ARG;
+    if (batch_out > 0 && (!parents || !table_out || !lens_out || !src || !dst || !tokens ||
+                          lens == lens_out || table == table_out))
+        return DET_ERR_INVALID_ARG;
+    if ((st = check_device()) != DET_OK) return st;
+    return from_cuda(launch_pages_fork(batch, batch_out, page_size, num_pages, lens, parents,
+                                       table, max_pages, ldt, table_out, ldto, free_pages, capacity,
+                                       free_count, lens_out, free_count_out, src, dst, tokens,
+                                       dev_status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+DET_API det_status detpages_compact(const det_profile_v1 *prof, int64_t batch, int64_t page_size,
+                                    int64_t num_pages, const int32_t *lens, const int32_t *table,
+                                    int64_t max_pages, int64_t ldt, int32_t *table_out,
+                                    int64_t ldto, int32_t *free_pages, int32_t *free_count_out,
+                                    int32_t *src, int32_t *dst, int64_t max_moves, int32_t *moves,
+                                    int32_t *dev_status, det_stream_t stream) {
+    det_status st = check_profile(prof);
+    if (st != DET_OK) return st;
+    if (!pages_ok(batch, page_size, max_pages, ldt, 0) || ldto < max_pages || num_pages < 0 ||
+        num_pages > kPagesMax || max_moves < num_pages / 2 || (table == table_out && ldt != ldto))
+        return DET_ERR_INVALID_ARG;
+    if (!free_count_out || !moves || (num_pages > 0 && !free_pages) ||
+        (num_pages > 1 && (!src || !dst)) || (batch > 0 && (!lens || !table || !table_out)))
+        return DET_ERR_INVALID_ARG;
+    if ((st = check_device()) != DET_OK) return st;
+    return from_cuda(launch_pages_compact(batch, page_size, num_pages, lens, table, max_pages, ldt,
+                                          table_out, ldto, free_pages, free_count_out, src, dst,
+                                          moves, dev_status,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+DET_API det_status detkv_copy_f32(const det_profile_v1 *prof, int64_t pairs, const int32_t *src,
+                                  const int32_t *dst, const int32_t *tokens, const int32_t *count,
+                                  const det_kv_cache *cache, int32_t *dev_status,
+                                  det_stream_t stream) {
+    det_status st = check_profile(prof);
+    if (st != DET_OK) return st;
+    if (pairs < 0 || pairs > kPagesMax || !cache_ok(cache)) return DET_ERR_INVALID_ARG;
+    if (pairs == 0) return DET_OK;
+    if (!src || !dst) return DET_ERR_INVALID_ARG;
+    if ((st = check_device()) != DET_OK) return st;
+    return from_cuda(launch_kv_copy(pairs, src, dst, tokens, count, *cache, dev_status,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+DET_API det_status detdecode_attention_shared_workspace_bytes(
+    const det_profile_v1 *prof, int64_t batch, int64_t group, int64_t heads, int64_t kv_heads,
+    int64_t head_dim, int64_t max_len, size_t *bytes) {
+    if (group < 1) {
+        const det_status st = check_profile(prof);
+        return st != DET_OK ? st : DET_ERR_INVALID_ARG;
+    }
+    return detdecode_attention_workspace_bytes(prof, batch, heads, kv_heads, head_dim, max_len,
+                                               bytes);
+}
+
+DET_API det_status detdecode_attention_shared_f32(
+    const det_profile_v1 *prof, int64_t batch, int64_t group, int64_t heads, const float *q,
+    int64_t ldq, const det_kv_cache *cache, const int32_t *table, int64_t max_pages, int64_t ldt,
+    const int32_t *kv_lens, float scale, float *out, int64_t ldo, void *workspace,
+    size_t workspace_bytes, int32_t *dev_status, det_stream_t stream) {
+    if (group < 1) {
+        const det_status st = check_profile(prof);
+        return st != DET_OK ? st : DET_ERR_INVALID_ARG;
+    }
+    return detdecode_attention_f32(prof, batch, heads, q, ldq, cache, table, max_pages, ldt,
+                                   kv_lens, scale, out, ldo, workspace, workspace_bytes,
+                                   dev_status, stream);
+}
+
 DET_API det_status det_watchdog_status(int32_t *code, int clear) {
     if (!code) return DET_ERR_INVALID_ARG;
     unsigned int c = 0, c2 = 0;

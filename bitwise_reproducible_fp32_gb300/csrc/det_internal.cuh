@@ -230,6 +230,27 @@ cudaError_t launch_logprob_bwd(int64_t rows, int64_t V, const float *logits, int
                                const int32_t *tokens, const float *stats, const float *dlogp,
                                const float *dentropy, float *dlogits, int64_t ldd,
                                cudaStream_t s);
+cudaError_t launch_beam_select(int64_t requests, const det_beams &in, const det_beams &out,
+                               int top_k, const int32_t *top_ids, const float *top_logp,
+                               int32_t eos, const float *weights, int64_t nweights, int64_t cols,
+                               int32_t *tokens, int32_t *parents, int32_t *forks,
+                               int32_t *dev_status, cudaStream_t s);
+cudaError_t launch_pages_fork(int64_t batch, int64_t batch_out, int64_t page_size,
+                              int64_t num_pages, const int32_t *lens, const int32_t *parents,
+                              const int32_t *table, int64_t max_pages, int64_t ldt,
+                              int32_t *table_out, int64_t ldto, int32_t *free_pages,
+                              int64_t capacity, const int32_t *free_count, int32_t *lens_out,
+                              int32_t *free_count_out, int32_t *src, int32_t *dst,
+                              int32_t *tokens, int32_t *dev_status, cudaStream_t s);
+cudaError_t launch_pages_compact(int64_t batch, int64_t page_size, int64_t num_pages,
+                                 const int32_t *lens, const int32_t *table, int64_t max_pages,
+                                 int64_t ldt, int32_t *table_out, int64_t ldto,
+                                 int32_t *free_pages, int32_t *free_count_out, int32_t *src,
+                                 int32_t *dst, int32_t *moves, int32_t *dev_status,
+                                 cudaStream_t s);
+cudaError_t launch_kv_copy(int64_t pairs, const int32_t *src, const int32_t *dst,
+                           const int32_t *tokens, const int32_t *count, const det_kv_cache &c,
+                           int32_t *dev_status, cudaStream_t s);
 // Host: bc = 1 - beta^t for both betas (beta^t by t-1 sequential products).
 void adamw_bias_correction(int64_t step, float beta1, float beta2, float *bc1, float *bc2);
 

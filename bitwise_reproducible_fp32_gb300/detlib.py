@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdetfp32.so")
@@ -56,6 +57,26 @@ class KVCache(ctypes.Structure):
                 ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
                 ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64)]
+
+
+class BeamsArg(ctypes.Structure):
+    """det_beams."""
+    _fields_ = [("beams", ctypes.c_int64), ("scores", ctypes.c_void_p),
+                ("finished", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("hist", ctypes.c_void_p), ("ldh", ctypes.c_int64)]
+
+
+class Beams(NamedTuple):
+    """The beams that detbeam_select_f32 keeps: scores (requests x beams), and of each
+    row its token, the row it goes on from, that row or -1 where the beam has ended,
+    whether it has, its length and its history (None where there are none)."""
+    scores: object
+    tokens: object
+    parents: object
+    forks: object
+    finished: object
+    lens: object
+    hist: object
 
 
 class AdamWHP(ctypes.Structure):
@@ -150,6 +171,19 @@ SIGNATURES = [
                               _vp, _vp]),
     ("detlogprob_bwd_f32", _int, [_PROF, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64,
                                   _vp]),
+    ("detbeam_select_f32", _int, [_PROF, _i64, ctypes.POINTER(BeamsArg), ctypes.POINTER(BeamsArg), _i64,
+                                  _vp, _vp, ctypes.c_int32, _vp, _i64, _i64, _vp, _vp, _vp, _vp,
+                                  _vp]),
+    ("detpages_fork", _int, [_PROF, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp,
+                             _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    ("detpages_compact", _int, [_PROF, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp,
+                                _vp, _vp, _i64, _vp, _vp, _vp]),
+    ("detkv_copy_f32", _int, [_PROF, _i64, _vp, _vp, _vp, _vp, ctypes.POINTER(KVCache), _vp, _vp]),
+    ("detdecode_attention_shared_f32", _int, [_PROF, _i64, _i64, _i64, _vp, _i64,
+                                              ctypes.POINTER(KVCache), _vp, _i64, _i64, _vp, _f,
+                                              _vp, _i64, _vp, ctypes.c_size_t, _vp, _vp]),
+    ("detdecode_attention_shared_workspace_bytes", _int, [_PROF, _i64, _i64, _i64, _i64, _i64, _i64,
+                                                          ctypes.POINTER(ctypes.c_size_t)]),
     ("det_watchdog_status", _int, [ctypes.POINTER(ctypes.c_int32), _int]),
 ]
 
@@ -1149,6 +1183,13 @@ def detdecode_attention_f32(q, k_cache, v_cache, table, kv_lens, heads, scale=No
     those tokens; a length of 0 gives 0. dev_status bits: 1 a length out of range,
     2 a page out of range (the row is NaN). Returns out (requests x heads *
     head_dim)."""
+    return _decode(q, k_cache, v_cache, table, kv_lens, heads, None, scale, out, workspace,
+                   dev_status, profile, stream)
+
+
+def _decode(q, k_cache, v_cache, table, kv_lens, heads, group, scale, out, workspace, dev_status,
+            profile, stream):
+    """Decode attention; group: the requests read together, None: each for itself."""
     lib, prof, dev = _gen_begin(profile, q, "q")
     c = _kv_cache(k_cache, v_cache, dev)
     d = c.head_dim
@@ -1170,22 +1211,256 @@ def detdecode_attention_f32(q, k_cache, v_cache, table, kv_lens, heads, scale=No
         wp, wn = _vec(workspace, "workspace", _N.f32, dev), workspace.numel() * 4
     else:
         # the query's answer depends on these sizes and the device alone
-        key = (batch, heads, c.kv_heads, d, max_pages * c.page_size, dev)
+        key = (batch, group, heads, c.kv_heads, d, max_pages * c.page_size, dev)
         need = _decode_workspaces.get(key)
         if need is None:
-            need = detdecode_attention_workspace_bytes(*key[:-1], profile)
+            if group is None:
+                need = detdecode_attention_workspace_bytes(batch, *key[2:-1], profile)
+            else:
+                need = detdecode_attention_shared_workspace_bytes(*key[:-1], profile)
             if len(_decode_workspaces) >= 1024:
                 _decode_workspaces.clear()
             _decode_workspaces[key] = need
         if need:
             workspace = _gen_empty(((need + 3) // 4,), q, stream)
             wp, wn = workspace.data_ptr(), workspace.numel() * 4
-    st = lib.detdecode_attention_f32(prof, batch, heads, qp, ldq, c, tp, max_pages, ldt, lp, scale,
-                                     op, ldo, wp, wn, _word(dev_status, dev),
-                                     _gen_stream(stream, dev))
+    if group is None:
+        st = lib.detdecode_attention_f32(prof, batch, heads, qp, ldq, c, tp, max_pages, ldt, lp,
+                                         scale, op, ldo, wp, wn, _word(dev_status, dev),
+                                         _gen_stream(stream, dev))
+        name = "detdecode_attention_f32"
+    else:
+        st = lib.detdecode_attention_shared_f32(prof, batch, group, heads, qp, ldq, c, tp, max_pages,
+                                                ldt, lp, scale, op, ldo, wp, wn,
+                                                _word(dev_status, dev), _gen_stream(stream, dev))
+        name = "detdecode_attention_shared_f32"
     if st:
-        _check("detdecode_attention_f32", st)
+        _check(name, st)
     return out
+
+
+def detbeam_select_f32(scores, top_ids, top_logp, beams, eos=-1, finished=None, lens=None,
+                       weights=None, hist=None, hist_out=None, scores_out=None, tokens=None,
+                       parents=None, forks=None, finished_out=None, lens_out=None,
+                       dev_status=None, profile=None, stream=None):
+    """The next `beams` beams (1..32) of each request from the present ones and their
+    alternatives. scores: requests x beams so far; of each of their rows (request by
+    request) top_ids and top_logp (rows x k) as detlogprob_f32 gives them, finished
+    (int32, default: none has ended), lens (int32, tokens of the answer) and hist
+    (int32, rows of at least that many tokens; goes to hist_out, of as many columns).
+    A beam goes on with each of its alternatives, score + logp, or, where it has
+    ended, as it is; the largest scores are kept, with weights (floats) the largest
+    score * weights[length]; the lowest beam, then the lowest id first among equals.
+    eos: the id that ends an answer. Returns Beams; tensors not given for its outputs
+    are made (hist_out: only with hist). A row past the candidates has score -inf,
+    token and parent -1. dev_status bits: 1 a NaN, 2 a history that does not fit."""
+    lib, prof, dev = _gen_begin(profile, scores, "scores")
+    f32, i32 = _N.f32, _N.i32
+    sp, lds = _mat(scores, "scores", f32, dev)
+    requests, old = scores.size(0), scores.size(1)
+    if requests > 1 and lds != old:
+        raise ValueError("scores must be contiguous")
+    rows, new = requests * old, requests * beams
+    ip, ldi = _mat(top_ids, "top_ids", i32, dev, rows)
+    k = top_ids.size(1)
+    tp, ldt = _mat(top_logp, "top_logp", f32, dev, rows, k)
+    if top_logp.size(1) != k or (rows > 1 and (ldi != k or ldt != k)):
+        raise ValueError("top_ids and top_logp must be contiguous rows of one length")
+    fp = None if finished is None else _vec(finished, "finished", i32, dev, rows)
+    lp = None if lens is None else _vec(lens, "lens", i32, dev, rows)
+    wp, wn = None, 0
+    if weights is not None:
+        wp, wn = _vec(weights, "weights", f32, dev), weights.numel()
+    if lens is None and (weights is not None or hist is not None or lens_out is not None):
+        raise ValueError("weights, hist and lens_out need lens")
+    if not 1 <= beams <= 32:
+        raise ValueError("beams must be in 1..32")
+    hp, ldh, hop, ldho, cols = None, 0, None, 0, 0
+    if hist is not None:
+        hp, ldh = _mat(hist, "hist", i32, dev, rows)
+        cols = hist.size(1)
+        if cols < 1:
+            raise ValueError("hist must have at least one column")
+        if hist_out is None:
+            hist_out = _gen_empty((new, cols), scores, stream, i32)
+        hop, ldho = _mat(hist_out, "hist_out", i32, dev, new, cols)
+        if hist_out.size(1) != cols:
+            raise ValueError(f"hist_out must have {cols} columns")
+    elif hist_out is not None:
+        raise ValueError("hist_out needs hist")
+    if scores_out is None:
+        scores_out = _gen_empty((requests, beams), scores, stream)
+    sop, lds = _mat(scores_out, "scores_out", f32, dev, requests, beams)
+    if scores_out.size(1) != beams or (requests > 1 and lds != beams):
+        raise ValueError(f"scores_out must be contiguous rows of {beams}")
+    parts = None
+    if (tokens is None and parents is None and forks is None and finished_out is None
+            and lens_out is None):
+        # one allocation for the whole numbers, taken apart once the launch is on its way
+        parts = _gen_empty(((4 if lens is None else 5) * new,), scores, stream, i32)
+        p = parts.data_ptr()
+        at = [p, p + 4 * new, p + 8 * new, p + 12 * new, None if lens is None else p + 16 * new]
+    else:
+        if tokens is None:
+            tokens = _gen_empty((new,), scores, stream, i32)
+        if parents is None:
+            parents = _gen_empty((new,), scores, stream, i32)
+        if forks is None:
+            forks = _gen_empty((new,), scores, stream, i32)
+        if finished_out is None:
+            finished_out = _gen_empty((new,), scores, stream, i32)
+        if lens_out is None and lens is not None:
+            lens_out = _gen_empty((new,), scores, stream, i32)
+        at = [None if t is None else _vec(t, n, i32, dev, new)
+              for t, n in ((tokens, "tokens"), (parents, "parents"), (forks, "forks"),
+                           (finished_out, "finished_out"), (lens_out, "lens_out"))]
+    st = lib.detbeam_select_f32(prof, requests, BeamsArg(old, sp, fp, lp, hp, ldh),
+                                BeamsArg(beams, sop, at[3], at[4], hop, ldho), k, ip, tp, eos, wp, wn,
+                                cols, at[0], at[1], at[2], _word(dev_status, dev),
+                                _gen_stream(stream, dev))
+    if st:
+        _check("detbeam_select_f32", st)
+    if parts is not None:
+        parts = parts.unsafe_split(new) if new else [parts] * 5
+        tokens, parents, forks, finished_out = parts[:4]
+        lens_out = None if lens is None else parts[4]
+    return Beams(scores_out, tokens, parents, forks, finished_out, lens_out, hist_out)
+
+
+def detpages_fork(lens, parents, table, free_pages, free_count, page_size, num_pages,
+                  table_out=None, lens_out=None, free_count_out=None, src=None, dst=None,
+                  tokens=None, dev_status=None, profile=None, stream=None):
+    """New rows of a block table from old ones: row r goes on from row parents[r]
+    (int32; -1: it is empty) with its length and pages. Rows of one parent share its
+    full pages; the first keeps a partly filled last page, the others get a page of
+    their own to copy tokens[r] tokens into, from page src[r] to dst[r]
+    (detkv_copy_f32; -1 for the other rows). Pages that only rows without a child held
+    go back to free_pages, then the new ones are taken from its end. num_pages: the
+    cache's. table_out: another tensor than table, of its columns. Returns (table_out,
+    lens_out, free_count_out, src, dst, tokens). dev_status bits: 1 a length, parent
+    or count out of range, 2 out of pages (the row is empty), 4 a page out of range."""
+    lib, prof, dev = _gen_begin(profile, lens, "lens")
+    i32 = _N.i32
+    lp = _vec(lens, "lens", i32, dev)
+    batch = lens.numel()
+    pp = _vec(parents, "parents", i32, dev)
+    new = parents.numel()
+    tp, ldt = _mat(table, "table", i32, dev, batch)
+    width = table.size(1)
+    fp = _vec(free_pages, "free_pages", i32, dev)
+    cp = _vec(free_count, "free_count", i32, dev, 1)
+    if table_out is None:
+        table_out = _gen_empty((new, width), lens, stream)
+    op, ldo = _mat(table_out, "table_out", i32, dev, new, width)
+    parts = None
+    if lens_out is None and free_count_out is None and src is None and dst is None and tokens is None:
+        # one allocation for the five, taken apart once the launch is on its way
+        parts = _gen_empty((4 * new + 1,), lens, stream)
+        p = parts.data_ptr()
+        at = [p, p + 16 * new, p + 4 * new, p + 8 * new, p + 12 * new]
+    else:
+        if lens_out is None:
+            lens_out = _gen_empty((new,), lens, stream)
+        if free_count_out is None:
+            free_count_out = _gen_empty((1,), lens, stream)
+        if src is None:
+            src = _gen_empty((new,), lens, stream)
+        if dst is None:
+            dst = _gen_empty((new,), lens, stream)
+        if tokens is None:
+            tokens = _gen_empty((new,), lens, stream)
+        at = [_vec(lens_out, "lens_out", i32, dev, new),
+              _vec(free_count_out, "free_count_out", i32, dev, 1),
+              _vec(src, "src", i32, dev, new), _vec(dst, "dst", i32, dev, new),
+              _vec(tokens, "tokens", i32, dev, new)]
+    st = lib.detpages_fork(prof, batch, new, page_size, num_pages, lp, pp, tp, width, ldt, op, ldo,
+                           fp, free_pages.numel(), cp, at[0], at[1], at[2], at[3], at[4],
+                           _word(dev_status, dev), _gen_stream(stream, dev))
+    if st:
+        _check("detpages_fork", st)
+    if parts is not None:
+        lens_out, src, dst, tokens, free_count_out = parts.unsafe_split_with_sizes(
+            (new, new, new, new, 1))
+    return table_out, lens_out, free_count_out, src, dst, tokens
+
+
+def detpages_compact(lens, table, free_pages, page_size, table_out=None, free_count_out=None,
+                     src=None, dst=None, moves=None, dev_status=None, profile=None, stream=None):
+    """Moves the pages that the rows hold to the lowest ids: the new table (table_out;
+    table itself works in place), the moves (src and dst, moves[0] of them: what
+    detkv_copy_f32 takes, with count=moves) and the free list (free_pages, one
+    entry a page of the cache) and count. Every page in use must be in a row. Returns
+    (table_out, free_count_out, moves, src, dst). dev_status bits: 1 a length out of
+    range, 4 a page out of range."""
+    lib, prof, dev = _gen_begin(profile, lens, "lens")
+    i32 = _N.i32
+    lp = _vec(lens, "lens", i32, dev)
+    batch = lens.numel()
+    tp, ldt = _mat(table, "table", i32, dev, batch)
+    width = table.size(1)
+    fp = _vec(free_pages, "free_pages", i32, dev)
+    pages = free_pages.numel()
+    if table_out is None:
+        table_out = _gen_empty((batch, width), lens, stream)
+    op, ldo = _mat(table_out, "table_out", i32, dev, batch, width)
+    if src is None:
+        src = _gen_empty((pages // 2,), lens, stream)
+    if dst is None:
+        dst = _gen_empty((pages // 2,), lens, stream)
+    if free_count_out is None:
+        free_count_out = _gen_empty((1,), lens, stream)
+    if moves is None:
+        moves = _gen_empty((1,), lens, stream)
+    st = lib.detpages_compact(prof, batch, page_size, pages, lp, tp, width, ldt, op, ldo, fp,
+                              _vec(free_count_out, "free_count_out", i32, dev, 1),
+                              _vec(src, "src", i32, dev), _vec(dst, "dst", i32, dev, src.numel()),
+                              src.numel(), _vec(moves, "moves", i32, dev, 1),
+                              _word(dev_status, dev), _gen_stream(stream, dev))
+    if st:
+        _check("detpages_compact", st)
+    return table_out, free_count_out, moves, src, dst
+
+
+def detkv_copy_f32(k_cache, v_cache, src, dst, tokens=None, count=None, dev_status=None,
+                   profile=None, stream=None):
+    """Copies pages of a paged cache: the first tokens[i] (int32; default: all) tokens
+    of page src[i] to page dst[i], keys and values, for i below count[0] (default: all
+    pairs; int32). Negative pages: nothing. Of several copies to one page the last
+    counts; a page that any pair reads is not written (dev_status bit 2; bit 1: a page
+    or number of tokens out of range)."""
+    lib, prof, dev = _gen_begin(profile, k_cache, "k_cache")
+    i32 = _N.i32
+    c = _kv_cache(k_cache, v_cache, dev)
+    sp = _vec(src, "src", i32, dev)
+    n = src.numel()
+    dp = _vec(dst, "dst", i32, dev, n)
+    tp = None if tokens is None else _vec(tokens, "tokens", i32, dev, n)
+    np_ = None if count is None else _vec(count, "count", i32, dev, 1)
+    st = lib.detkv_copy_f32(prof, n, sp, dp, tp, np_, c, _word(dev_status, dev),
+                            _gen_stream(stream, dev))
+    if st:
+        _check("detkv_copy_f32", st)
+
+
+def detdecode_attention_shared_workspace_bytes(batch, group, heads, kv_heads, head_dim, max_len,
+                                               profile=None) -> int:
+    n = ctypes.c_size_t(0)
+    _check("detdecode_attention_shared_workspace_bytes",
+           load().detdecode_attention_shared_workspace_bytes(_prof(profile), batch, group, heads,
+                                                             kv_heads, head_dim, max_len,
+                                                             ctypes.byref(n)))
+    return n.value
+
+
+def detdecode_attention_shared_f32(q, k_cache, v_cache, table, kv_lens, heads, group, scale=None,
+                                   out=None, workspace=None, dev_status=None, profile=None,
+                                   stream=None):
+    """detdecode_attention_f32, the same bits, for requests that share pages: each
+    `group` consecutive requests are read together where they hold the same pages
+    (found on the device from the table: whole chunks of 256 tokens from the start).
+    Arguments and result as there."""
+    return _decode(q, k_cache, v_cache, table, kv_lens, heads, group, scale, out, workspace,
+                   dev_status, profile, stream)
 
 
 def detlogprob_f32(logits, tokens, top_k=0, want_stats=True, logp=None, entropy=None, stats=None,

@@ -823,6 +823,152 @@ det_status detlogprob_bwd_f32(const det_profile_v1 *prof, int64_t rows, int64_t 
                               const float *stats, const float *dlogp, const float *dentropy,
                               float *dlogits, int64_t ldd, det_stream_t stream);
 
+/* ------------------------------------------------------------------ several answers of a prompt
+ * Beam search, and any other use of several continuations of one text: the choice
+ * of the next beams, rows of the cache that share pages, and attention that reads
+ * a shared prefix once. */
+
+/* The beams of some requests (host struct, read during the call): `beams` rows a
+ * request, request r's from row r * beams. Device arrays over the rows: scores;
+ * finished (nonzero: the beam has ended; NULL as input: none has); lens (tokens of
+ * the answer so far) and hist (the answers, rows of int32 tokens, row stride ldh),
+ * NULL where there are none. */
+typedef struct det_beams {
+    int64_t beams;
+    float *scores;
+    int32_t *finished, *lens, *hist;
+    int64_t ldh;
+} det_beams;
+
+/* The next beams from the present ones and their alternatives (top_ids, top_logp:
+ * rows x top_k, dense, as detlogprob_f32 gives them). The candidates of a beam w:
+ *   not ended: its alternatives j, score s_w + top_logp_j (one rounding), length
+ *     lens_w + 1;
+ *   ended: itself, token eos, score s_w, length lens_w.
+ * rank = the score, or with weights (nweights floats, device) score *
+ * weights[length] (one rounding; lengths past nweights - 1 or below 0 take the
+ * nearest weight). A score of -Inf is no candidate (a beam of score -Inf has
+ * none); a NaN rank is none and ORs 1 into *dev_status. The out->beams largest
+ * ranks of the request are kept, in descending order, among equal ones (+0 and -0
+ * are equal) the lowest beam first, then the lowest id, then the lowest j.
+ * Per row of the new beams: out->scores the score; tokens its token; parents the
+ * row it goes on from; forks the same, or -1 where the new beam has ended (what
+ * detpages_fork takes: the pages of ended beams are given back); out->finished 1
+ * where it had ended or its token is eos; out->lens its length; out->hist its
+ * parent's lens_w first tokens and then, unless it had ended, its token (columns
+ * past that are not touched). Where there are fewer candidates than beams the rest
+ * of the rows are dead: score -Inf, token and parent -1, finished 1, length 0,
+ * history not touched.
+ * eos: the id that ends an answer, or a negative value for none. hist_cols: tokens
+ * a row of either history holds; a history that does not fit (or a negative
+ * length) is cut there and ORs 2.
+ * in->hist and out->hist go together and need in->lens, as weights do; forks,
+ * out->finished and out->lens may be NULL. The outputs must not overlap the
+ * inputs. requests may be 0.
+ * Errors: DET_ERR_INVALID_ARG for beams or top_k outside 1..32, requests < 0 or
+ * rows >= 2^31, strides below hist_cols, hist_cols < 0, nweights < 1 with weights,
+ * or null pointers. */
+det_status detbeam_select_f32(const det_profile_v1 *prof, int64_t requests, const det_beams *in,
+                              const det_beams *out, int64_t top_k, const int32_t *top_ids,
+                              const float *top_logp, int32_t eos, const float *weights,
+                              int64_t nweights, int64_t hist_cols, int32_t *tokens,
+                              int32_t *parents, int32_t *forks, int32_t *dev_status,
+                              det_stream_t stream);
+
+/* New rows of a block table from old ones: row r of table_out (batch_out rows) goes
+ * on from row parents[r] of table (batch rows; device int32), with its length and
+ * its pages; parents[r] == -1 leaves it empty. Several rows with one parent share
+ * its pages, but for a partly filled last page: the first of them (the lowest r)
+ * keeps it, each other gets a page of its own in its place, and src[r], dst[r] and
+ * tokens[r] (device int32, batch_out each) say what to copy there: tokens[r] tokens
+ * of page src[r] to page dst[r] (detkv_copy_f32); -1, -1 and 0 for the other rows.
+ * Pages that only rows without a child held are given back. So rows may share
+ * pages that are full; a page of the free list, and a partly filled one, must be
+ * no other row's.
+ * free_pages (capacity page ids), free_count, page_size, max_pages: as
+ * detpages_extend. The pages given back are written from *free_count on in
+ * ascending order; then the new pages are taken from the end by ascending r. lens_out
+ * (batch_out): the new lengths; free_count_out: the count after. Entries of
+ * table_out past a row's pages are not touched.
+ * *dev_status (may be NULL): 1 for a length outside the table's row (the row counts
+ * as empty), a parent outside -1..batch - 1 (the new row is empty) or a free count
+ * outside 0..capacity (counts as 0, or where the pages given back do not fit: they
+ * are not); 2 where the free list has run out, 4 for a page outside
+ * 0..num_pages - 1 (left as it is in a table; in the free list as if it had run
+ * out): a row that needs a page then is left empty.
+ * The outputs must not overlap the inputs, but for free_pages. One launch.
+ * Errors: DET_ERR_INVALID_ARG as detpages_extend (batch and batch_out 0..8192),
+ * num_pages outside 0..2^23, or lens_out, table_out or free_count_out equal to their
+ * input. */
+det_status detpages_fork(const det_profile_v1 *prof, int64_t batch, int64_t batch_out,
+                         int64_t page_size, int64_t num_pages, const int32_t *lens,
+                         const int32_t *parents, const int32_t *table, int64_t max_pages,
+                         int64_t ldt, int32_t *table_out, int64_t ldto, int32_t *free_pages,
+                         int64_t capacity, const int32_t *free_count, int32_t *lens_out,
+                         int32_t *free_count_out, int32_t *src, int32_t *dst, int32_t *tokens,
+                         int32_t *dev_status, det_stream_t stream);
+
+/* Moves the pages that the rows hold, U different ones, to the ids 0..U - 1: those
+ * at or past U, in ascending order, go to the free ids below U, in ascending
+ * order. src and dst (device int32, max_moves >= num_pages / 2 each) get the moves,
+ * *moves their number, for detkv_copy_f32; entries past it are not touched. The new
+ * rows go to table_out, which may be table (ldto == ldt); entries past a row's
+ * pages are not touched. free_pages (num_pages) gets the free ids num_pages - 1
+ * down to U, so the lowest are taken first, and *free_count_out their number. Every
+ * page in use must be in a row: others count as free.
+ * *dev_status (may be NULL): 1 for a length outside the table's row (the row counts
+ * as empty), 4 for a page outside 0..num_pages - 1 (left as it is). One launch.
+ * Errors: DET_ERR_INVALID_ARG as detpages_extend, num_pages outside 0..2^23,
+ * max_moves < num_pages / 2, or table_out == table with another stride. */
+det_status detpages_compact(const det_profile_v1 *prof, int64_t batch, int64_t page_size,
+                            int64_t num_pages, const int32_t *lens, const int32_t *table,
+                            int64_t max_pages, int64_t ldt, int32_t *table_out, int64_t ldto,
+                            int32_t *free_pages, int32_t *free_count_out, int32_t *src,
+                            int32_t *dst, int64_t max_moves, int32_t *moves,
+                            int32_t *dev_status, det_stream_t stream);
+
+/* Copies pages of a cache: the first tokens[i] tokens (NULL: all) of page src[i], K
+ * and V of every head, to page dst[i], for i < min(pairs, *count) (device int32;
+ * count may be NULL). A pair with a negative page, without tokens or from a page to
+ * itself copies nothing. Where several pairs have one destination, the last of
+ * them is copied. A destination that is a source of any pair is not written and ORs
+ * 2 into *dev_status (may be NULL), so the sources are read as they were before the
+ * call. A page past num_pages or a number of tokens outside 0..page_size ORs 1,
+ * and the pair copies nothing; a *count outside 0..pairs ORs 1 and counts as the
+ * nearest of them.
+ * pairs 0..2^23. Errors: DET_ERR_INVALID_ARG for that, the cache's rules
+ * (detkv_append_f32) or null pointers. */
+det_status detkv_copy_f32(const det_profile_v1 *prof, int64_t pairs, const int32_t *src,
+                          const int32_t *dst, const int32_t *tokens, const int32_t *count,
+                          const det_kv_cache *cache, int32_t *dev_status, det_stream_t stream);
+
+/* detdecode_attention_f32, the same results bit for bit, for requests that share
+ * pages: requests group * i .. group * i + group - 1 (the last group may be
+ * smaller) are read together where they hold the same pages. On the device, each
+ * group's first 256-token chunks whose pages are the same ids in all its requests
+ * (those of length 0 or out of range left out; every request keeps one token of its
+ * own at least) are found from the table; their keys and values are read once for
+ * the group instead of once a request. Pages need not be shared: group only says
+ * where to look.
+ * Arguments, status bits and errors as detdecode_attention_f32, and
+ * DET_ERR_INVALID_ARG for group < 1. workspace: at least
+ * detdecode_attention_shared_workspace_bytes (16-byte aligned, no contents
+ * assumed). A wait for a piece of the cache that gives up after 2 s sets bit 5 of
+ * det_watchdog_status(), and the rows of the requests it was for are NaN. */
+det_status detdecode_attention_shared_f32(const det_profile_v1 *prof, int64_t batch,
+                                          int64_t group, int64_t heads, const float *q,
+                                          int64_t ldq, const det_kv_cache *cache,
+                                          const int32_t *table, int64_t max_pages, int64_t ldt,
+                                          const int32_t *kv_lens, float scale, float *out,
+                                          int64_t ldo, void *workspace, size_t workspace_bytes,
+                                          int32_t *dev_status, det_stream_t stream);
+/* Workspace detdecode_attention_shared_f32 needs for requests of up to max_len tokens
+ * (max_len = max_pages * page_size there), written to *bytes. */
+det_status detdecode_attention_shared_workspace_bytes(const det_profile_v1 *prof, int64_t batch,
+                                                      int64_t group, int64_t heads,
+                                                      int64_t kv_heads, int64_t head_dim,
+                                                      int64_t max_len, size_t *bytes);
+
 /* Reads, and optionally clears, the current device's watchdog word.
  * *code == 0 means no bounded device wait has ever given up; otherwise bit k
  * identifies the kernel family that gave up (bit 0: GEMM operand staging,
