@@ -1058,6 +1058,13 @@ bool decode_sizes_ok(int64_t batch, int64_t heads, int64_t kv_heads, int64_t hea
     return batch >= 0 && batch <= 65535 && heads >= 1 && heads <= 65536 && kv_heads >= 1 &&
            heads % kv_heads == 0 && head_dim >= 1 && head_dim <= 256;
 }
+
+bool decode_args_ok(int64_t batch, int64_t heads, const det_kv_cache *cache, int64_t max_pages,
+                    int64_t ldt, int64_t ldq, int64_t ldo) {
+    return cache_ok(cache) && decode_sizes_ok(batch, heads, cache->kv_heads, cache->head_dim) &&
+           max_pages >= 1 && max_pages <= kLenMax && max_pages * cache->page_size <= kLenMax &&
+           ldt >= max_pages && ldq >= heads * cache->head_dim && ldo >= heads * cache->head_dim;
+}
 }  // namespace
 
 DET_API det_status detrope_at_f32(const det_profile_v1 *prof, int64_t rows, int64_t heads,
@@ -1174,10 +1181,7 @@ DET_API det_status detdecode_attention_f32(const det_profile_v1 *prof, int64_t b
                                            int32_t *dev_status, det_stream_t stream) {
     det_status st = check_profile(prof);
     if (st != DET_OK) return st;
-    if (!cache_ok(cache) || !decode_sizes_ok(batch, heads, cache->kv_heads, cache->head_dim) ||
-        max_pages < 1 || max_pages > kLenMax || max_pages * cache->page_size > kLenMax ||
-        ldt < max_pages || ldq < heads * cache->head_dim || ldo < heads * cache->head_dim)
-        return DET_ERR_INVALID_ARG;
+    if (!decode_args_ok(batch, heads, cache, max_pages, ldt, ldq, ldo)) return DET_ERR_INVALID_ARG;
     if (batch == 0) return DET_OK;
     if (!q || !table || !kv_lens || !out) return DET_ERR_INVALID_ARG;
     const size_t need = decode_workspace_bytes(batch, heads, cache->kv_heads, cache->head_dim,
@@ -1327,12 +1331,13 @@ DET_API det_status detkv_copy_f32(const det_profile_v1 *prof, int64_t pairs, con
 DET_API det_status detdecode_attention_shared_workspace_bytes(
     const det_profile_v1 *prof, int64_t batch, int64_t group, int64_t heads, int64_t kv_heads,
     int64_t head_dim, int64_t max_len, size_t *bytes) {
-    if (group < 1) {
-        const det_status st = check_profile(prof);
-        return st != DET_OK ? st : DET_ERR_INVALID_ARG;
-    }
-    return detdecode_attention_workspace_bytes(prof, batch, heads, kv_heads, head_dim, max_len,
-                                               bytes);
+    det_status st = check_profile(prof);
+    if (st != DET_OK) return st;
+    if (!bytes || !decode_sizes_ok(batch, heads, kv_heads, head_dim) || group < 1 || max_len < 1 ||
+        max_len > kLenMax)
+        return DET_ERR_INVALID_ARG;
+    *bytes = shared_decode_workspace_bytes(batch, group, heads, kv_heads, head_dim, max_len);
+    return DET_OK;
 }
 
 DET_API det_status detdecode_attention_shared_f32(
@@ -1340,13 +1345,23 @@ DET_API det_status detdecode_attention_shared_f32(
     int64_t ldq, const det_kv_cache *cache, const int32_t *table, int64_t max_pages, int64_t ldt,
     const int32_t *kv_lens, float scale, float *out, int64_t ldo, void *workspace,
     size_t workspace_bytes, int32_t *dev_status, det_stream_t stream) {
-    if (group < 1) {
-        const det_status st = check_profile(prof);
-        return st != DET_OK ? st : DET_ERR_INVALID_ARG;
-    }
-    return detdecode_attention_f32(prof, batch, heads, q, ldq, cache, table, max_pages, ldt,
-                                   kv_lens, scale, out, ldo, workspace, workspace_bytes,
-                                   dev_status, stream);
+    det_status st = check_profile(prof);
+    if (st != DET_OK) return st;
+    if (!decode_args_ok(batch, heads, cache, max_pages, ldt, ldq, ldo) || group < 1)
+        return DET_ERR_INVALID_ARG;
+    if (batch == 0) return DET_OK;
+    if (!q || !table || !kv_lens || !out) return DET_ERR_INVALID_ARG;
+    const size_t need =
+        shared_decode_workspace_bytes(batch, group, heads, cache->kv_heads, cache->head_dim,
+                                      max_pages * cache->page_size);
+    if (need > 0 && (!workspace || workspace_bytes < need ||
+                     reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
+        return DET_ERR_WORKSPACE;
+    if ((st = check_device()) != DET_OK) return st;
+    return from_cuda(launch_shared_decode(batch, group, int(heads), q, ldq, *cache, table,
+                                          max_pages, ldt, kv_lens, scale, out, ldo,
+                                          static_cast<float *>(workspace), dev_status,
+                                          reinterpret_cast<cudaStream_t>(stream)));
 }
 
 DET_API det_status det_watchdog_status(int32_t *code, int clear) {
@@ -1366,6 +1381,8 @@ DET_API det_status det_watchdog_status(int32_t *code, int clear) {
     if (e == cudaSuccess) e = decode_watchdog(&c6, clear);
     unsigned int c7 = 0;
     if (e == cudaSuccess) e = logprob_watchdog(&c7, clear);
-    *code = int32_t(c | c2 | c3 | c5 | c6 | c7);
+    unsigned int c8 = 0;
+    if (e == cudaSuccess) e = shared_decode_watchdog(&c8, clear);
+    *code = int32_t(c | c2 | c3 | c5 | c6 | c7 | c8);
     return from_cuda(e);
 }

@@ -45,7 +45,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "det_internal.cuh"
+#include "decode.cuh"
 #include "det_math.cuh"
 
 namespace cg = cooperative_groups;
@@ -65,28 +65,9 @@ constexpr int kMaxHeads = 8;
 constexpr int kMaxCluster = 16;
 constexpr int kDeep = 8;                    // groups of a chain of S in flight
 constexpr int kPageCache = 512;             // page ids of a CTA kept on chip
-enum Loader { kTma, kCopy16, kCopy4 };
 constexpr unsigned kWatchdogDecode = 32u;   // det_watchdog_status bit 5
 constexpr int kCtasPerSm = 2;
 constexpr int kSmemPerCta = (227 / kCtasPerSm - 1) * 1024;
-
-__device__ __forceinline__ float4 lds4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ float lds1(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void sts1(uint32_t addr, float v) {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
 
 struct DecodeArgs {
     int heads, kv_heads, head_dim;
@@ -111,33 +92,8 @@ struct DecodeArgs {
     int stages;               // slots of a warp's ring
     int64_t max_pages;
     int32_t *dev_status;
+    SharedPrefix sh;          // of the SHARED instances
 };
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ float butterfly32(float s) {
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1)
-        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
-    return s;
-}
 
 // exp4 where the maximum is not finite.
 __device__ __noinline__ float4 exp4_any(float4 x, float m) {
@@ -176,8 +132,13 @@ struct Walk {
     }
 };
 
-// NH: the heads of a unit the registers hold (nh <= NH of them live).
-template <int NH, Loader LOAD>
+// NH: the heads of a unit the registers hold (nh <= NH of them live). SHARED: the
+// scores of the group's shared chunks are there, with their maxima, and the unit
+// takes the tokens after them: m is over both, the chains of S walk the shared tokens
+// first (writing their exps for the kernel that multiplies them with V), and the
+// chunk partials go to memory, where they are joined with the shared ones. A unit
+// whose group shares nothing ends as without.
+template <int NH, Loader LOAD, bool SHARED>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_kernel(const DecodeArgs A, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
@@ -204,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // the length, the query and, for a unit of one CTA, the first page ids are
     // asked for together
     int early[kPageCache / kThreads];
-    if (C == 1)
+    if (C == 1 && !SHARED)
 #pragma unroll
         for (int i = 0; i < kPageCache / kThreads; ++i)
             early[i] = tid + i * kThreads < A.max_pages ? pages[tid + i * kThreads] : 0;
@@ -225,10 +186,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (C > 1) cluster.sync(); else __syncthreads();
     };
     // this CTA's run of chunks and tokens
-    const int nch = (n + kKChunk - 1) / kKChunk, base = nch / C, rem = nch % C;
+    const int skip = SHARED ? A.sh.chunks[b / A.sh.group] : 0;     // chunks, less than the row's
+    const int nch = (n + kKChunk - 1) / kKChunk - skip, base = nch / C, rem = nch % C;
+    const int64_t row0 = int64_t(b) * A.heads + h0;
     auto first_chunk = [&](int r) { return r * base + min(r, rem); };
     const int c0 = first_chunk(rank), my = base + (rank < rem), most = base + (rem > 0);
-    const int t0 = c0 * kKChunk, t1 = min(n, t0 + my * kKChunk);
+    const int t0 = (skip + c0) * kKChunk, t1 = min(n, t0 + my * kKChunk);
     // scores [head][token], then partials [head][chunk][d], here or in L2
     const int64_t xs_ld = int64_t(most) * kKChunk, part_at = nh * xs_ld;
     const bool on_chip = int64_t(nh) * most * (kKChunk + d) <= A.room;
@@ -253,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         if (cached) F.pages[i] = id;
     };
-    if (C == 1 && cached) {
+    if (C == 1 && cached && !SHARED) {
 #pragma unroll
         for (int i = 0; i < kPageCache / kThreads; ++i)
             if (unsigned(tid + i * kThreads) < pgs) check(tid + i * kThreads, early[i]);
@@ -457,6 +420,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     for (int h = 0; h < NH; ++h) {
         m[h] = F.top[0][h];
         for (int r = 1; r < C; ++r) m[h] = max_nan(m[h], F.top[r][h]);
+        if (SHARED && skip > 0)
+            m[h] = max_nan(m[h], max_of_key(A.sh.top[row0 + min(h, nh - 1)]));
     }
     // ---- e in place of x, and the chains of S: a warp 32 chains of a head, which
     // it walks through the cluster's runs kDeep groups at a time (slots past n
@@ -468,8 +433,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int k = 1; k < NH; ++k) top = h == k ? m[k] : top;
         const bool finite = fabsf(top) <= 0x1.fffffep127f;
         float sum = 0.0f;
-        Walk w(l >> 6, base, rem);
-        for (int t = 4 * l; t < n; t += 1024 * kDeep) {
+        int chunk = l >> 6;             // the chain's first of the unit's own
+        if (SHARED && skip > 0) {
+            float *x = A.sh.x + (row0 + h) * A.sh.ldx;
+            const int past = skip * kKChunk;
+            for (int t = 4 * l; t < past; t += 1024 * kDeep) {
+                float4 e[kDeep];
+#pragma unroll
+                for (int u = 0; u < kDeep; ++u)
+                    if (t + 1024 * u < past)
+                        e[u] = *reinterpret_cast<const float4 *>(x + t + 1024 * u);
+#pragma unroll
+                for (int u = 0; u < kDeep; ++u) {
+                    if (t + 1024 * u >= past) break;
+                    e[u] = finite ? exp4(e[u], top) : exp4_any(e[u], top);
+                    *reinterpret_cast<float4 *>(x + t + 1024 * u) = e[u];
+                    sum = __fadd_rn(sum, e[u].x);
+                    sum = __fadd_rn(sum, e[u].y);
+                    sum = __fadd_rn(sum, e[u].z);
+                    sum = __fadd_rn(sum, e[u].w);
+                }
+            }
+            if (chunk < skip) chunk += (skip - chunk + 3) / 4 * 4;
+        }
+        Walk w(chunk - skip, base, rem);
+        for (int t = 4 * l + (chunk - (l >> 6)) * kKChunk; t < n; t += 1024 * kDeep) {
             float4 *at[kDeep], e[kDeep];
 #pragma unroll
             for (int u = 0; u < kDeep; ++u) {
@@ -518,6 +506,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
         }
     }
+    if (SHARED && skip > 0 && rank == 0 && tid == 0)
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+            if (h < nh) A.sh.inv[row0 + h] = lost ? __uint_as_float(0x7fc00000u) : inv[h];
     __syncthreads();
     // ---- P V: chunk partials (registers past the unit's heads repeat its last)
     uint32_t pat[NH];             // shared-memory addresses of the heads' rows
@@ -609,7 +601,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (32 * sl + lane < d)
 #pragma unroll
             for (int h = 0; h < NH; ++h)
-                if (h < nh) xs[part_at + (int64_t(h) * most + c) * d + 32 * sl + lane] = acc[h];
+                if (h < nh) {
+                    if (SHARED && skip > 0)
+                        A.sh.part[((row0 + h) * A.sh.ldpart + skip + c0 + c) * d + 32 * sl + lane] =
+                            acc[h];
+                    else
+                        xs[part_at + (int64_t(h) * most + c) * d + 32 * sl + lane] = acc[h];
+                }
     }
     if (LOAD != kTma) cp_wait<0>();
     if (LOAD == kTma && stuck) {        // let the copies in flight land, tell the cluster
@@ -627,6 +625,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     meet();
     for (int r = 0; r < C; ++r) lost |= F.lost[r];
+    if (SHARED && skip > 0) {           // joined with the shared ones later
+        if (lost)
+            for (int i = tid; i < nh * my * d; i += kThreads) {
+                const int h = i / (my * d);
+                A.sh.part[((row0 + h) * A.sh.ldpart + skip + c0) * d + (i - h * my * d)] =
+                    __uint_as_float(0x7fc00000u);
+            }
+        if ((lost & 1) && rank == 0 && tid == 0 && A.dev_status)
+            atomicOr(reinterpret_cast<int *>(A.dev_status), 2);
+        if (C > 1) cluster.sync();
+        return;
+    }
     // ---- the chunks left to right
     for (int i = (warp * C + rank) * 32 + lane; i < nh * d; i += C * kThreads) {
         const int h = i / d;
@@ -711,13 +721,15 @@ cudaError_t launch_decode_attention(int64_t batch, int heads, const float *q, in
                                     const det_kv_cache &c, const int32_t *table,
                                     int64_t max_pages, int64_t ldt, const int32_t *kv_lens,
                                     float scale, float *out, int64_t ldo, float *workspace,
-                                    int32_t *dev_status, cudaStream_t s) {
+                                    int32_t *dev_status, cudaStream_t s,
+                                    const SharedPrefix *shared) {
     const int64_t max_len = max_pages * c.page_size;
     const DecodePlan p = decode_plan(batch, heads, c.kv_heads, c.head_dim, max_len);
     DecodeArgs A = {heads, int(c.kv_heads), int(c.head_dim), q, ldq, c.k, c.v, c.num_pages,
                     unsigned(c.page_size), -1, c.page_stride, c.token_stride, c.head_stride,
                     table, ldt, kv_lens, scale, out, ldo, workspace, max_len, p.ws_cta, p.room,
-                    0, p.unit_heads, p.batches, p.stages, max_pages, dev_status};
+                    0, p.unit_heads, p.batches, p.stages, max_pages, dev_status, {}};
+    if (shared) A.sh = *shared;
     for (int i = 0; i < 31; ++i)
         if (c.page_size == int64_t(1) << i) A.page_shift = i;
     auto al16 = [](const void *x) { return reinterpret_cast<uintptr_t>(x) % 16 == 0; };
@@ -762,9 +774,13 @@ cudaError_t launch_decode_attention(int64_t batch, int heads, const float *q, in
     };
     auto pick = [&](auto heads_in) {
         constexpr int NH = decltype(heads_in)::value;
-        return load == kTma      ? run(decode_kernel<NH, kTma>)
-               : load == kCopy16 ? run(decode_kernel<NH, kCopy16>)
-                                 : run(decode_kernel<NH, kCopy4>);
+        if (shared)
+            return load == kTma      ? run(decode_kernel<NH, kTma, true>)
+                   : load == kCopy16 ? run(decode_kernel<NH, kCopy16, true>)
+                                     : run(decode_kernel<NH, kCopy4, true>);
+        return load == kTma      ? run(decode_kernel<NH, kTma, false>)
+               : load == kCopy16 ? run(decode_kernel<NH, kCopy16, false>)
+                                 : run(decode_kernel<NH, kCopy4, false>);
     };
     switch (register_heads(p.unit_heads)) {
         case 1: return pick(std::integral_constant<int, 1>());

@@ -1,0 +1,84 @@
+// decode.cuh -- what the kernels of decode attention share: loads of pieces of the
+// paged cache, and what the requests' own kernel (decode.cu) has from the kernels
+// that read a shared prefix once a group (decode_shared.cu).
+#pragma once
+
+#include "det_internal.cuh"
+
+namespace det {
+
+// Requests that share a prefix: chunks of 256 tokens that a group's requests hold
+// the same pages of, and what passes between the kernels, rows (b, h) = b * heads
+// + h of the heads in hand.
+struct SharedPrefix {
+    const int32_t *chunks;    // of each group
+    int group;                // requests
+    float *x;                 // their scores, then exps: row * ldx + token
+    int64_t ldx;
+    const unsigned *top;      // the rows' maxima over them, as max_key gives them
+    float *inv;               // 1 / S of the rows (NaN: a bad page)
+    float *part;              // chunk partials of P V: (row * ldpart + chunk) * head_dim
+    int64_t ldpart;
+};
+
+namespace {
+
+enum Loader { kTma, kCopy16, kCopy4 };
+
+__device__ __forceinline__ float4 lds4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float lds1(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void sts1(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float butterfly32(float s) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1)
+        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
+    return s;
+}
+
+
+// Floats as whole numbers in their order, NaN above all; 0 is below every float's.
+__device__ __forceinline__ unsigned max_key(float x) {
+    const unsigned b = __float_as_uint(x);
+    return x != x ? 0xffffffffu : b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float max_of_key(unsigned k) {
+    if (k == 0xffffffffu) return __uint_as_float(0x7fc00000u);
+    return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
+}
+
+}  // namespace
+}  // namespace det

@@ -27,7 +27,7 @@ constexpr unsigned int kWatchdogGemm = 1u;   // GEMM operand staging
 // bit 1 (2u): cross-entropy row staging, defined in rowops.cu; bit 2 (4u):
 // RMSNorm-backward staging (rmsbwd.cu); bit 3 (8u): RMSNorm row staging
 // (rowops.cu); bit 4 (16u): causal-softmax row staging (block.cu); bit 5 (32u):
-// decode attention's pieces (decode.cu); bit 6 (64u): log-probability row
+// decode attention's pieces (decode.cu, decode_shared.cu); bit 6 (64u): log-probability row
 // staging (logprob.cu)
 
 // ---------------------------------------------------------------- launchers
@@ -130,6 +130,7 @@ cudaError_t rowops_watchdog(unsigned int *code, int clear);
 cudaError_t rmsbwd_watchdog(unsigned int *code, int clear);
 cudaError_t block_watchdog(unsigned int *code, int clear);
 cudaError_t decode_watchdog(unsigned int *code, int clear);
+cudaError_t shared_decode_watchdog(unsigned int *code, int clear);
 cudaError_t logprob_watchdog(unsigned int *code, int clear);
 
 // 2-D fp32 TMA descriptor over a row-major matrix: inner = contiguous extent,
@@ -221,7 +222,16 @@ cudaError_t launch_decode_attention(int64_t batch, int heads, const float *q, in
                                     const det_kv_cache &c, const int32_t *table,
                                     int64_t max_pages, int64_t ldt, const int32_t *kv_lens,
                                     float scale, float *out, int64_t ldo, float *workspace,
-                                    int32_t *dev_status, cudaStream_t s);
+                                    int32_t *dev_status, cudaStream_t s,
+                                    const struct SharedPrefix *shared = nullptr);
+// The same with requests read together in groups (decode_shared.cu).
+size_t shared_decode_workspace_bytes(int64_t batch, int64_t group, int64_t heads,
+                                     int64_t kv_heads, int64_t head_dim, int64_t max_len);
+cudaError_t launch_shared_decode(int64_t batch, int64_t group, int heads, const float *q,
+                                 int64_t ldq, const det_kv_cache &c, const int32_t *table,
+                                 int64_t max_pages, int64_t ldt, const int32_t *kv_lens,
+                                 float scale, float *out, int64_t ldo, float *workspace,
+                                 int32_t *dev_status, cudaStream_t s);
 cudaError_t launch_logprob(int64_t rows, int64_t V, const float *logits, int64_t ld,
                            const int32_t *tokens, int top_k, float *logp, float *entropy,
                            float *stats, int32_t *top_ids, float *top_logp, int32_t *dev_status,
