@@ -46,7 +46,6 @@
 #include <type_traits>
 
 #include "decode.cuh"
-#include "det_math.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -92,14 +91,7 @@ struct DecodeArgs {
     int stages;               // slots of a warp's ring
     int64_t max_pages;
     int32_t *dev_status;
-    SharedPrefix sh;          // of the SHARED instances
 };
-
-// exp4 where the maximum is not finite.
-__device__ __noinline__ float4 exp4_any(float4 x, float m) {
-    return make_float4(det_exp(__fsub_rn(x.x, m)), det_exp(__fsub_rn(x.y, m)),
-                       det_exp(__fsub_rn(x.z, m)), det_exp(__fsub_rn(x.w, m)));
-}
 
 template <int NH>
 struct Fixed {                          // a CTA's shared memory after the rings
@@ -132,13 +124,8 @@ struct Walk {
     }
 };
 
-// NH: the heads of a unit the registers hold (nh <= NH of them live). SHARED: the
-// scores of the group's shared chunks are there, with their maxima, and the unit
-// takes the tokens after them: m is over both, the chains of S walk the shared tokens
-// first (writing their exps for the kernel that multiplies them with V), and the
-// chunk partials go to memory, where they are joined with the shared ones. A unit
-// whose group shares nothing ends as without.
-template <int NH, Loader LOAD, bool SHARED>
+// NH: the heads of a unit the registers hold (nh <= NH of them live).
+template <int NH, Loader LOAD>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_kernel(const DecodeArgs A, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
@@ -165,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // the length, the query and, for a unit of one CTA, the first page ids are
     // asked for together
     int early[kPageCache / kThreads];
-    if (C == 1 && !SHARED)
+    if (C == 1)
 #pragma unroll
         for (int i = 0; i < kPageCache / kThreads; ++i)
             early[i] = tid + i * kThreads < A.max_pages ? pages[tid + i * kThreads] : 0;
@@ -186,12 +173,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (C > 1) cluster.sync(); else __syncthreads();
     };
     // this CTA's run of chunks and tokens
-    const int skip = SHARED ? A.sh.chunks[b / A.sh.group] : 0;     // chunks, less than the row's
-    const int nch = (n + kKChunk - 1) / kKChunk - skip, base = nch / C, rem = nch % C;
-    const int64_t row0 = int64_t(b) * A.heads + h0;
+    const int nch = (n + kKChunk - 1) / kKChunk, base = nch / C, rem = nch % C;
     auto first_chunk = [&](int r) { return r * base + min(r, rem); };
     const int c0 = first_chunk(rank), my = base + (rank < rem), most = base + (rem > 0);
-    const int t0 = (skip + c0) * kKChunk, t1 = min(n, t0 + my * kKChunk);
+    const int t0 = c0 * kKChunk, t1 = min(n, t0 + my * kKChunk);
     // scores [head][token], then partials [head][chunk][d], here or in L2
     const int64_t xs_ld = int64_t(most) * kKChunk, part_at = nh * xs_ld;
     const bool on_chip = int64_t(nh) * most * (kKChunk + d) <= A.room;
@@ -216,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         if (cached) F.pages[i] = id;
     };
-    if (C == 1 && cached && !SHARED) {
+    if (C == 1 && cached) {
 #pragma unroll
         for (int i = 0; i < kPageCache / kThreads; ++i)
             if (unsigned(tid + i * kThreads) < pgs) check(tid + i * kThreads, early[i]);
@@ -420,8 +405,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     for (int h = 0; h < NH; ++h) {
         m[h] = F.top[0][h];
         for (int r = 1; r < C; ++r) m[h] = max_nan(m[h], F.top[r][h]);
-        if (SHARED && skip > 0)
-            m[h] = max_nan(m[h], max_of_key(A.sh.top[row0 + min(h, nh - 1)]));
     }
     // ---- e in place of x, and the chains of S: a warp 32 chains of a head, which
     // it walks through the cluster's runs kDeep groups at a time (slots past n
@@ -433,31 +416,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int k = 1; k < NH; ++k) top = h == k ? m[k] : top;
         const bool finite = fabsf(top) <= 0x1.fffffep127f;
         float sum = 0.0f;
-        int chunk = l >> 6;             // the chain's first of the unit's own
-        if (SHARED && skip > 0) {
-            float *x = A.sh.x + (row0 + h) * A.sh.ldx;
-            const int past = skip * kKChunk;
-            for (int t = 4 * l; t < past; t += 1024 * kDeep) {
-                float4 e[kDeep];
-#pragma unroll
-                for (int u = 0; u < kDeep; ++u)
-                    if (t + 1024 * u < past)
-                        e[u] = *reinterpret_cast<const float4 *>(x + t + 1024 * u);
-#pragma unroll
-                for (int u = 0; u < kDeep; ++u) {
-                    if (t + 1024 * u >= past) break;
-                    e[u] = finite ? exp4(e[u], top) : exp4_any(e[u], top);
-                    *reinterpret_cast<float4 *>(x + t + 1024 * u) = e[u];
-                    sum = __fadd_rn(sum, e[u].x);
-                    sum = __fadd_rn(sum, e[u].y);
-                    sum = __fadd_rn(sum, e[u].z);
-                    sum = __fadd_rn(sum, e[u].w);
-                }
-            }
-            if (chunk < skip) chunk += (skip - chunk + 3) / 4 * 4;
-        }
-        Walk w(chunk - skip, base, rem);
-        for (int t = 4 * l + (chunk - (l >> 6)) * kKChunk; t < n; t += 1024 * kDeep) {
+        Walk w(l >> 6, base, rem);
+        for (int t = 4 * l; t < n; t += 1024 * kDeep) {
             float4 *at[kDeep], e[kDeep];
 #pragma unroll
             for (int u = 0; u < kDeep; ++u) {
@@ -506,10 +466,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
         }
     }
-    if (SHARED && skip > 0 && rank == 0 && tid == 0)
-#pragma unroll
-        for (int h = 0; h < NH; ++h)
-            if (h < nh) A.sh.inv[row0 + h] = lost ? __uint_as_float(0x7fc00000u) : inv[h];
     __syncthreads();
     // ---- P V: chunk partials (registers past the unit's heads repeat its last)
     uint32_t pat[NH];             // shared-memory addresses of the heads' rows
@@ -601,13 +557,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (32 * sl + lane < d)
 #pragma unroll
             for (int h = 0; h < NH; ++h)
-                if (h < nh) {
-                    if (SHARED && skip > 0)
-                        A.sh.part[((row0 + h) * A.sh.ldpart + skip + c0 + c) * d + 32 * sl + lane] =
-                            acc[h];
-                    else
-                        xs[part_at + (int64_t(h) * most + c) * d + 32 * sl + lane] = acc[h];
-                }
+                if (h < nh) xs[part_at + (int64_t(h) * most + c) * d + 32 * sl + lane] = acc[h];
     }
     if (LOAD != kTma) cp_wait<0>();
     if (LOAD == kTma && stuck) {        // let the copies in flight land, tell the cluster
@@ -625,18 +575,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     meet();
     for (int r = 0; r < C; ++r) lost |= F.lost[r];
-    if (SHARED && skip > 0) {           // joined with the shared ones later
-        if (lost)
-            for (int i = tid; i < nh * my * d; i += kThreads) {
-                const int h = i / (my * d);
-                A.sh.part[((row0 + h) * A.sh.ldpart + skip + c0) * d + (i - h * my * d)] =
-                    __uint_as_float(0x7fc00000u);
-            }
-        if ((lost & 1) && rank == 0 && tid == 0 && A.dev_status)
-            atomicOr(reinterpret_cast<int *>(A.dev_status), 2);
-        if (C > 1) cluster.sync();
-        return;
-    }
     // ---- the chunks left to right
     for (int i = (warp * C + rank) * 32 + lane; i < nh * d; i += C * kThreads) {
         const int h = i / d;
@@ -721,15 +659,13 @@ cudaError_t launch_decode_attention(int64_t batch, int heads, const float *q, in
                                     const det_kv_cache &c, const int32_t *table,
                                     int64_t max_pages, int64_t ldt, const int32_t *kv_lens,
                                     float scale, float *out, int64_t ldo, float *workspace,
-                                    int32_t *dev_status, cudaStream_t s,
-                                    const SharedPrefix *shared) {
+                                    int32_t *dev_status, cudaStream_t s) {
     const int64_t max_len = max_pages * c.page_size;
     const DecodePlan p = decode_plan(batch, heads, c.kv_heads, c.head_dim, max_len);
     DecodeArgs A = {heads, int(c.kv_heads), int(c.head_dim), q, ldq, c.k, c.v, c.num_pages,
                     unsigned(c.page_size), -1, c.page_stride, c.token_stride, c.head_stride,
                     table, ldt, kv_lens, scale, out, ldo, workspace, max_len, p.ws_cta, p.room,
-                    0, p.unit_heads, p.batches, p.stages, max_pages, dev_status, {}};
-    if (shared) A.sh = *shared;
+                    0, p.unit_heads, p.batches, p.stages, max_pages, dev_status};
     for (int i = 0; i < 31; ++i)
         if (c.page_size == int64_t(1) << i) A.page_shift = i;
     auto al16 = [](const void *x) { return reinterpret_cast<uintptr_t>(x) % 16 == 0; };
@@ -774,13 +710,9 @@ cudaError_t launch_decode_attention(int64_t batch, int heads, const float *q, in
     };
     auto pick = [&](auto heads_in) {
         constexpr int NH = decltype(heads_in)::value;
-        if (shared)
-            return load == kTma      ? run(decode_kernel<NH, kTma, true>)
-                   : load == kCopy16 ? run(decode_kernel<NH, kCopy16, true>)
-                                     : run(decode_kernel<NH, kCopy4, true>);
-        return load == kTma      ? run(decode_kernel<NH, kTma, false>)
-               : load == kCopy16 ? run(decode_kernel<NH, kCopy16, false>)
-                                 : run(decode_kernel<NH, kCopy4, false>);
+        return load == kTma      ? run(decode_kernel<NH, kTma>)
+               : load == kCopy16 ? run(decode_kernel<NH, kCopy16>)
+                                 : run(decode_kernel<NH, kCopy4>);
     };
     switch (register_heads(p.unit_heads)) {
         case 1: return pick(std::integral_constant<int, 1>());

@@ -1,25 +1,11 @@
-// decode.cuh -- what the kernels of decode attention share: loads of pieces of the
-// paged cache, and what the requests' own kernel (decode.cu) has from the kernels
-// that read a shared prefix once a group (decode_shared.cu).
+// decode.cuh -- what the kernels of decode attention share (decode.cu: each request
+// for itself; decode_shared.cu: requests that share a prefix).
 #pragma once
 
 #include "det_internal.cuh"
+#include "det_math.cuh"
 
 namespace det {
-
-// Requests that share a prefix: chunks of 256 tokens that a group's requests hold
-// the same pages of, and what passes between the kernels, rows (b, h) = b * heads
-// + h of the heads in hand.
-struct SharedPrefix {
-    const int32_t *chunks;    // of each group
-    int group;                // requests
-    float *x;                 // their scores, then exps: row * ldx + token
-    int64_t ldx;
-    const unsigned *top;      // the rows' maxima over them, as max_key gives them
-    float *inv;               // 1 / S of the rows (NaN: a bad page)
-    float *part;              // chunk partials of P V: (row * ldpart + chunk) * head_dim
-    int64_t ldpart;
-};
 
 namespace {
 
@@ -69,6 +55,11 @@ __device__ __forceinline__ float butterfly32(float s) {
     return s;
 }
 
+// exp4 where the maximum is not finite.
+__device__ __noinline__ float4 exp4_any(float4 x, float m) {
+    return make_float4(det_exp(__fsub_rn(x.x, m)), det_exp(__fsub_rn(x.y, m)),
+                       det_exp(__fsub_rn(x.z, m)), det_exp(__fsub_rn(x.w, m)));
+}
 
 // Floats as whole numbers in their order, NaN above all; 0 is below every float's.
 __device__ __forceinline__ unsigned max_key(float x) {

@@ -1,21 +1,22 @@
 // decode_shared.cu -- decode attention of requests that share a prefix in a paged
 // cache, its keys and values read once a group, for sm_103a.
 //
-// The mathematics and every bit are decode.cu's; what changes is who forms the
-// scores and chunk partials of the tokens that a group's requests have in common:
+// The mathematics and every bit are decode.cu's; what changes is that scores and chunk
+// partials are formed by units: a group's shared tokens with all its query rows, and
+// each request's own tokens with its rows.
 //   1. plan: of each group, the 256-token chunks whose pages are the same ids in all
-//      its requests;
-//   2. scores: for a group, a key-value head and a chunk, S = Q K^T for all the
-//      group's query rows of that head, kept in the workspace, and the rows' maxima;
-//   3. decode.cu's kernel for each request's own tokens, which also takes the
-//      maximum over both, walks the chains of S through the shared scores (leaving
-//      their exps in place) and says 1 / S;
-//   4. partials: P V of each shared chunk for all rows of the group;
+//      its requests; of each request, the chunks of its own;
+//   2. scores: for a unit, a key-value head and a chunk, S = Q K^T, kept in the
+//      workspace, and the rows' maxima;
+//   3. sums: e = exp(x - m) in place, the 256 chains of S over the row, 1 / S;
+//   4. partials: for a unit, a key-value head and a chunk, P V;
 //   5. join: each row's chunk partials, left to right.
 // The profile's chains are of fmaf, so the products run on the CUDA cores: with R
-// rows a key and value (2 x 4 bytes a dimension) takes 2 R multiply-adds, and from R of
-// about 24 on they, not HBM, bound the shared part. As in the GEMM, shared memory's
-// rate sets the register tile: up to 16 rows x 8 tokens (or dimensions) a thread.
+// rows, a key and value (2 x 4 bytes a dimension) take 2 R multiply-adds, and from R of
+// about 24 on they, not HBM, bound a unit. As in the GEMM, shared memory's rate sets
+// the register tile: up to 16 rows x 8 tokens (or dimensions) a thread. Scores lie
+// in octets of 8 tokens, a group's rows side by side: [octet][row][8], so a warp's
+// stores of 4 rows x 8 tokens and its loads of exps are whole 128-byte lines.
 #include <algorithm>
 #include <type_traits>
 
@@ -31,15 +32,17 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanRows = 1024;                    // requests looked through at once
 constexpr unsigned kWatchdogDecode = 32u;          // det_watchdog_status bit 5
 constexpr int kScoreStage = kKChunk * 128;         // a chunk's tokens x 32 dimensions
 constexpr int kScoreStages = 2;
 constexpr int kPvTokens = 16;                      // of a step of P V
-constexpr int kPvSteps = kKChunk / kPvTokens;
 constexpr int kPvStages = 3;
+constexpr size_t kMaxSmem = 112 * 1024;            // of a CTA
 
 struct SharedArgs {
     int batch, group, groups, heads, kv_heads, per_kv, d;
+    int64_t rows;             // of a whole group and a key-value head: group * per_kv
     const float *q;
     int64_t ldq;
     const float *k, *v;
@@ -48,49 +51,58 @@ struct SharedArgs {
     int page_shift;           // log2(page_size), or -1
     int64_t page_stride, token_stride, head_stride;
     const int32_t *table;
-    int64_t max_pages, ldt;
+    int64_t ldt;
     const int32_t *kv_lens;
     int64_t max_len;
     float scale;
+    int wide;                 // 16-byte loads of the cache where TMA cannot be used
     int box;                  // tokens of a TMA box
     int row_blocks, dim_tiles;
     int *chunks, *lead;       // of each group: shared chunks, a request in order
-    unsigned *top;
-    float *x;
-    int64_t ldx;
-    const float *inv;
-    float *part;
+    int *own;                 // of each request: its own chunks, 0 if it is not in order
+    unsigned *top;            // of each row (b, h): the maximum of its scores, by max_key
+    float *inv;               // 1 / S
+    float *x;                 // ((group * kv_heads + head) * octets + octet) * rows + row) * 8
+    int64_t octets;
+    float *part;              // (row * ldpart + chunk) * d
     int64_t ldpart;
     float *out;
     int64_t ldo;
+    int32_t *dev_status;
 };
 
-__device__ __forceinline__ bool in_order(const SharedArgs &A, int n) {
-    return n > 0 && n <= A.max_len;
+__device__ __forceinline__ unsigned page_of(const SharedArgs &A, int t) {
+    return A.page_shift >= 0 ? unsigned(t) >> A.page_shift : unsigned(t) / A.page_size;
 }
 
 // ---------------------------------------------------------------- plan
 // A CTA a group. Every request keeps a token of its own, so a chunk is shared where
-// it ends before the shortest's last token.
+// it ends before the shortest's last token. A request whose own pages are not all in
+// order has no chunks and no part in the rest.
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedArgs A) {
-    __shared__ int s_least, s_lead, s_live, s_bad;
-    const int g = blockIdx.x, tid = threadIdx.x;
+    __shared__ int s_least, s_lead, s_live, s_bad, who[kPlanRows];
+    const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b0 = g * A.group, b1 = min(A.batch, b0 + A.group);
+    auto in_order = [&](int n) { return n > 0 && n <= A.max_len; };
     if (tid == 0) {
         s_least = s_lead = s_bad = INT32_MAX;
         s_live = 0;
     }
     __syncthreads();
-    int live = 0;
+    int live = 0, status = 0;
     for (int b = b0 + tid; b < b1; b += kPlanThreads) {
         const int n = A.kv_lens[b];
-        if (!in_order(A, n)) continue;
+        if (!in_order(n)) {
+            if (n != 0) status = 1;
+            continue;
+        }
         atomicMin(&s_least, n);
         atomicMin(&s_lead, b);
         ++live;
     }
     if (live) atomicAdd(&s_live, live);
-    for (int i = b0 * A.heads + tid; i < b1 * A.heads; i += kPlanThreads) A.top[i] = 0;
+    for (int64_t i = int64_t(b0) * A.heads + tid; i < int64_t(b1) * A.heads; i += kPlanThreads)
+        A.top[i] = 0;
     __syncthreads();
     int chunks = 0;
     if (s_live > 1) {
@@ -100,18 +112,23 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
         const int32_t *first = A.table + s_lead * A.ldt;
         // 256 pages at a time, the requests dealt out to four
         const int col = tid & 255, part = tid >> 8;
-        for (int j0 = 0; j0 < pages; j0 += 256) {
-            const int j = j0 + col;
-            bool bad = false;
-            if (j < pages) {
-                const int id = first[j];
-                bad = id < 0 || id >= A.num_pages;
+        for (int r0 = b0; r0 < b1; r0 += kPlanRows) {
+            const int rows = min(kPlanRows, b1 - r0);
+            __syncthreads();
+            if (tid < rows) who[tid] = in_order(A.kv_lens[r0 + tid]) ? r0 + tid : s_lead;
+            __syncthreads();
+            for (int j0 = 0; j0 < pages; j0 += 256) {
+                const int j = j0 + col;
+                bool bad = false;
+                if (j < pages) {
+                    const int id = first[j];
+                    bad = id < 0 || id >= A.num_pages;
 #pragma unroll 8
-                for (int b = b0 + part; b < b1; b += 4)
-                    bad |= A.table[b * A.ldt + j] != id && in_order(A, A.kv_lens[b]);
+                    for (int r = part; r < rows; r += 4) bad |= A.table[who[r] * A.ldt + j] != id;
+                }
+                if (bad) atomicMin(&s_bad, j);
+                if (__syncthreads_or(bad)) break;
             }
-            if (bad) atomicMin(&s_bad, j);
-            if (__syncthreads_or(bad)) break;
         }
         if (s_bad != INT32_MAX) chunks = min(chunks, int(s_bad * ps / kKChunk));
     }
@@ -119,31 +136,92 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
         A.chunks[g] = chunks;
         A.lead[g] = s_live ? s_lead : b0;
     }
+    // the requests' own pages
+    for (int b = b0 + warp; b < b1; b += kPlanThreads / 32) {
+        const int n = A.kv_lens[b];
+        int own = 0;
+        if (in_order(n)) {
+            const int32_t *row = A.table + b * A.ldt;
+            const int last = page_of(A, n - 1);
+            int bad = 0;
+            for (int j = int(page_of(A, chunks * kKChunk)) + lane; j <= last; j += 32) {
+                const int id = row[j];
+                bad |= id < 0 || id >= A.num_pages;
+            }
+            bad = __any_sync(0xffffffffu, bad);
+            own = bad ? 0 : (n + kKChunk - 1) / kKChunk - chunks;
+            if (bad) status |= 2;
+        }
+        if (lane == 0) A.own[b] = own;
+    }
+    if (A.dev_status) {
+        status = __reduce_or_sync(0xffffffffu, unsigned(status));
+        if (lane == 0 && status) atomicOr(reinterpret_cast<int *>(A.dev_status), status);
+    }
 }
 
 // ---------------------------------------------------------------- work
-// The items of a kernel: for each group `mul` runs (of heads and blocks of rows or
-// dimensions) of its shared chunks, the chunk fastest.
+// The items of a kernel: for each unit (OWN: a request with its own chunks; else a
+// group with the shared ones) `mul` runs (of heads and blocks of rows or dimensions)
+// of its chunks, the chunk fastest.
 struct Item {
-    int g, run, c, n;         // n: the group's chunks
+    int u, run, c, n;         // n: the unit's chunks
 };
+template <bool OWN>
+__device__ __forceinline__ int units(const SharedArgs &A) { return OWN ? A.batch : A.groups; }
+template <bool OWN>
+__device__ __forceinline__ int chunks_of(const SharedArgs &A, int u) {
+    return OWN ? A.own[u] : A.chunks[u];
+}
+// The item's first token, how many it has, and the table row of its pages.
+template <bool OWN>
+__device__ __forceinline__ int first_token(const SharedArgs &A, const Item &it) {
+    return (it.c + (OWN ? A.chunks[it.u / A.group] : 0)) * kKChunk;
+}
+template <bool OWN>
+__device__ __forceinline__ int tokens_from(const SharedArgs &A, const Item &it, int t0) {
+    return OWN ? min(kKChunk, A.kv_lens[it.u] - t0) : kKChunk;
+}
+template <bool OWN>
+__device__ __forceinline__ const int32_t *pages_of(const SharedArgs &A, const Item &it) {
+    return A.table + (OWN ? it.u : A.lead[it.u]) * A.ldt;
+}
+// Row r of the unit's rows of a key-value head: its place among its group's; the row
+// (b, h) of a place, -1 where there is none or its request is not in order.
+template <bool OWN>
+__device__ __forceinline__ int place_of(const SharedArgs &A, int u, int r) {
+    return OWN ? u % A.group * A.per_kv + r : r;
+}
+template <bool OWN>
+__device__ __forceinline__ int group_of(const SharedArgs &A, int u) {
+    return OWN ? u / A.group : u;
+}
+template <bool OWN>
+__device__ __forceinline__ int rows_of(const SharedArgs &A) {
+    return OWN ? A.per_kv : int(A.rows);
+}
+__device__ __forceinline__ int row_at(const SharedArgs &A, int g, int kv, int place) {
+    const int m = place / A.per_kv, b = g * A.group + m;
+    if (m >= A.group || b >= A.batch || A.own[b] == 0) return -1;
+    return b * A.heads + kv * A.per_kv + (place - m * A.per_kv);
+}
 
-// Every worker's share [lo, hi) of the items is an equal run of them; its first
-// item. All threads of the CTA call; worker w < workers of the CTA are numbers first
-// .. first + workers - 1 of `all`.
+// A worker's share [lo, hi) of the items is a run of them, all as long but for one;
+// the longer ones go to the first workers. All threads of the CTA call; the CTA has
+// the workers first, first + step, ... of `all`.
 struct Share {
-    int64_t lo, hi;
+    int64_t items;
     Item at;
 };
-template <int WORKERS>
-__device__ __forceinline__ void shares(const SharedArgs &A, int mul, int first, int all,
+template <bool OWN, int WORKERS>
+__device__ __forceinline__ void shares(const SharedArgs &A, int mul, int first, int step, int all,
                                        Share *out) {
     __shared__ int64_t warp_sums[kWarps];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (A.groups + kThreads - 1) / kThreads;
-    const int g0 = min(A.groups, tid * per), g1 = min(A.groups, g0 + per);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = units<OWN>(A);
+    const int per = (n + kThreads - 1) / kThreads;
+    const int u0 = min(n, tid * per), u1 = min(n, u0 + per);
     int64_t sum = 0;
-    for (int g = g0; g < g1; ++g) sum += A.chunks[g];
+    for (int u = u0; u < u1; ++u) sum += chunks_of<OWN>(A, u);
     int64_t in = sum;
 #pragma unroll
     for (int off = 1; off < 32; off *= 2) {
@@ -158,47 +236,36 @@ __device__ __forceinline__ void shares(const SharedArgs &A, int mul, int first, 
         total += warp_sums[w];
     }
     total *= mul;
+    const int64_t base = total / all, rem = total % all;
     for (int w = 0; w < WORKERS; ++w) {
-        const int64_t lo = total * (first + w) / all, hi = total * (first + w + 1) / all;
-        if (tid == 0) {
-            out[w].lo = lo;
-            out[w].hi = hi;
-        }
-        if (lo < hi && before * mul <= lo && lo < (before + sum) * mul) {
+        const int64_t i = first + int64_t(w) * step, lo = i * base + min(i, rem);
+        if (tid == 0) out[w].items = base + (i < rem);
+        if (base + (i < rem) > 0 && before * mul <= lo && lo < (before + sum) * mul) {
             int64_t at = before;
-            int g = g0;
-            while ((at + A.chunks[g]) * mul <= lo) at += A.chunks[g++];
-            const int n = A.chunks[g];
-            const int64_t i = lo - at * mul;
-            out[w].at = {g, int(i / n), int(i % n), n};
+            int u = u0;
+            while ((at + chunks_of<OWN>(A, u)) * mul <= lo) at += chunks_of<OWN>(A, u++);
+            const int c = chunks_of<OWN>(A, u);
+            const int64_t k = lo - at * mul;
+            out[w].at = {u, int(k / c), int(k % c), c};
         }
     }
     __syncthreads();
 }
+template <bool OWN>
 __device__ __forceinline__ void advance(const SharedArgs &A, int mul, Item &it) {
     if (++it.c < it.n) return;
     it.c = 0;
     if (++it.run < mul) return;
     it.run = 0;
     do {
-        ++it.g;
-    } while (it.g < A.groups && (it.n = A.chunks[it.g]) == 0);
+        ++it.u;
+    } while (it.u < units<OWN>(A) && (it.n = chunks_of<OWN>(A, it.u)) == 0);
 }
 
-__device__ __forceinline__ unsigned page_of(const SharedArgs &A, int t) {
-    return A.page_shift >= 0 ? unsigned(t) >> A.page_shift : unsigned(t) / A.page_size;
-}
 // A token's offset in the cache (its page is in order: the plan has seen it).
 __device__ __forceinline__ int64_t offset_of(const SharedArgs &A, const int32_t *pages, int t) {
     const unsigned p = page_of(A, t);
     return pages[p] * A.page_stride + int64_t(unsigned(t) - p * A.page_size) * A.token_stride;
-}
-// Row r of a group's rows of key-value head kv: its number b * heads + h, or -1
-// where there is none or its request is not in order.
-__device__ __forceinline__ int row_of(const SharedArgs &A, int g, int kv, int r) {
-    const int m = r / A.per_kv, b = g * A.group + m;
-    if (m >= A.group || b >= A.batch || !in_order(A, A.kv_lens[b])) return -1;
-    return b * A.heads + kv * A.per_kv + (r - m * A.per_kv);
 }
 
 // RT consecutive floats of shared memory as pairs.
@@ -222,97 +289,104 @@ __device__ __forceinline__ float part_of(const float4 &v, int i) {
 // ---------------------------------------------------------------- scores
 // An item: 4 RT rows, a chunk's 256 tokens; a warp 64 tokens (8 lanes x 8, tokens 8
 // apart, so that 16-byte reads along the dimensions of 8 keys meet no bank
-// conflict), 4 lanes x RT rows. Keys come 32 dimensions at a time, a stage ahead; the
-// query rows stay in shared memory, transposed, while they do not change.
-template <int RT, Loader LOAD>
+// conflict), 4 lanes x RT rows (4 apart). Keys come 32 dimensions at a time, a stage
+// ahead; the query rows stay in shared memory, transposed, while they do not change.
+template <int RT, bool OWN, bool TMA>
 __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
     shared_scores_kernel(const SharedArgs A, const __grid_constant__ CUtensorMap kmap) {
     constexpr int R = 4 * RT;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     float *qs = reinterpret_cast<float *>(smem_raw + kScoreStages * kScoreStage);
     __shared__ Share share;
-    __shared__ int rows[R];
+    __shared__ int rows[R];           // (b, h) of the row at qs's place
     __shared__ uint64_t full[kScoreStages];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tl = lane & 7, rl = lane >> 3;
     const int d = A.d, nsl = (d + 31) / 32, mul = A.kv_heads * A.row_blocks;
-    if (LOAD == kTma && tid == 0) {
+    if (TMA && tid == 0) {
         for (int i = 0; i < kScoreStages; ++i) mbar_init(smem_u32(full + i), 1);
         fence_mbar_init();
     }
-    shares<1>(A, mul, blockIdx.x, gridDim.x, &share);
-    const int64_t items = share.hi - share.lo;
+    shares<OWN, 1>(A, mul, blockIdx.x, 1, gridDim.x, &share);
+    const int64_t items = share.items;
     if (items <= 0) return;
     const uint32_t ring = smem_u32(smem_raw);
 
     // ---- keys
     Item in = share.at;
-    int in_sl = 0, in_slot = 0;
+    int in_sl = 0, in_slot = 0, in_t0 = 0, in_live = 0, in_boxes = 0, in_id = 0;
     int64_t left = items * nsl;
-    const int boxes = LOAD == kTma ? kKChunk / A.box : 1;      // at most 32
-    int id = 0;               // warp 0: the page of the lane's box
-    auto ask_page = [&]() {
-        if (LOAD == kTma && warp == 0 && lane < boxes && in.g < A.groups)
-            id = A.table[A.lead[in.g] * A.ldt + page_of(A, in.c * kKChunk + lane * A.box)];
+    auto look_up = [&]() {            // the item's tokens and, warp 0, the lane's box's page
+        if (in.u >= units<OWN>(A)) return;
+        in_t0 = first_token<OWN>(A, in);
+        in_live = tokens_from<OWN>(A, in, in_t0);
+        if (TMA) {
+            in_boxes = (in_live + A.box - 1) / A.box;             // at most 32
+            if (warp == 0 && lane < in_boxes)
+                in_id = pages_of<OWN>(A, in)[page_of(A, in_t0 + lane * A.box)];
+        }
     };
-    ask_page();
+    look_up();
     auto issue = [&]() {
         if (left > 0) {
             --left;
-            const int kv = in.run / A.row_blocks, t0 = in.c * kKChunk;
+            const int kv = in.run / A.row_blocks;
             const uint32_t dst = ring + in_slot * kScoreStage, bar = smem_u32(full + in_slot);
-            if constexpr (LOAD == kTma) {
+            if constexpr (TMA) {
                 if (warp == 0) {
-                    if (lane == 0) mbar_arrive_expect_tx(bar, kScoreStage);
+                    if (lane == 0) mbar_arrive_expect_tx(bar, in_boxes * A.box * 128);
                     __syncwarp();
-                    if (lane < boxes) {
-                        const int t = t0 + lane * A.box;
+                    if (lane < in_boxes) {
+                        const int t = in_t0 + lane * A.box;
                         tma_load_4d(dst + lane * A.box * 128, &kmap, 32 * in_sl, kv,
-                                    int(unsigned(t) - page_of(A, t) * A.page_size), id, bar);
+                                    int(unsigned(t) - page_of(A, t) * A.page_size), in_id, bar);
                     }
                 }
             } else {
-                const int32_t *pages = A.table + A.lead[in.g] * A.ldt;
+                const int32_t *pages = pages_of<OWN>(A, in);
                 const float *src = A.k + kv * A.head_stride + 32 * in_sl;
-                if constexpr (LOAD == kCopy16) {
+                if (A.wide) {
                     const int col = tid & 7;
                     if (4 * col < d - 32 * in_sl)
-                        for (int r = tid >> 3; r < kKChunk; r += kThreads / 8)
+                        for (int r = tid >> 3; r < in_live; r += kThreads / 8)
                             cp_async<16>(dst + r * 128 + ((col ^ (r & 7)) << 4),
-                                         src + offset_of(A, pages, t0 + r) + 4 * col);
-                } else {
-                    if (lane < d - 32 * in_sl)
-                        for (int r = warp; r < kKChunk; r += kWarps)
-                            cp_async<4>(dst + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) |
-                                                         (lane & 3) << 2),
-                                        src + offset_of(A, pages, t0 + r) + lane);
+                                         src + offset_of(A, pages, in_t0 + r) + 4 * col);
+                } else if (lane < d - 32 * in_sl) {
+                    for (int r = warp; r < in_live; r += kWarps)
+                        cp_async<4>(dst + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) |
+                                                     (lane & 3) << 2),
+                                    src + offset_of(A, pages, in_t0 + r) + lane);
                 }
             }
             in_slot ^= 1;
             if (++in_sl == nsl) {
                 in_sl = 0;
-                advance(A, mul, in);
-                ask_page();
+                advance<OWN>(A, mul, in);
+                look_up();
             }
         }
-        if (LOAD != kTma) cp_commit();
+        if (!TMA) cp_commit();
     };
     issue();
     Item it = share.at;
-    int held_g = -1, held_run = -1, slot = 0;
+    int held_u = -1, held_run = -1, slot = 0;
     uint32_t phase = 0;
     bool stuck = false;
     for (int64_t i = 0; i < items; ++i) {
-        const int kv = it.run / A.row_blocks, rb = it.run - kv * A.row_blocks;
-        if (it.g != held_g || it.run != held_run) {         // other rows
-            held_g = it.g;
+        const int kv = it.run / A.row_blocks, r0 = (it.run - kv * A.row_blocks) * R;
+        const int g = group_of<OWN>(A, it.u);
+        const int t0 = first_token<OWN>(A, it), live = tokens_from<OWN>(A, it, t0);
+        if (it.u != held_u || it.run != held_run) {         // other rows
+            held_u = it.u;
             held_run = it.run;
             __syncthreads();
-            for (int r = tid; r < R; r += kThreads) rows[r] = row_of(A, it.g, kv, rb * R + r);
-            const int r = tid % R, m = (rb * R + r) / A.per_kv, b = it.g * A.group + m;
-            const bool there = m < A.group && b < A.batch;
-            const float *q =
-                A.q + b * A.ldq + int64_t(kv * A.per_kv + rb * R + r - m * A.per_kv) * d;
-            for (int j = tid / R; j < d; j += kThreads / R) qs[j * R + r] = there ? q[j] : 0.0f;
+            // qs's place p has row p / RT + 4 (p mod RT)
+            const int p = tid % R, r = r0 + p / RT + 4 * (p % RT);
+            const int place = place_of<OWN>(A, it.u, r);
+            const int row = r < rows_of<OWN>(A) ? row_at(A, g, kv, place) : -1;
+            if (tid < R) rows[p] = row;
+            const int b = row / A.heads;
+            const float *q = A.q + b * A.ldq + int64_t(row - b * A.heads) * d;
+            for (int j = tid / R; j < d; j += kThreads / R) qs[j * R + p] = row >= 0 ? q[j] : 0.0f;
         }
         f32x2 acc[RT >= 2 ? RT / 2 : 1][8];
         float one[RT == 1 ? 8 : 1];
@@ -323,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
             if (RT == 1) one[c] = 0.0f;
         }
         for (int sl = 0; sl < nsl; ++sl) {
-            if constexpr (LOAD == kTma) {
+            if constexpr (TMA) {
                 if (!stuck) stuck = !mbar_wait_bounded(smem_u32(full + slot), phase);
                 stuck = __syncthreads_or(stuck);
                 if (stuck) break;
@@ -334,13 +408,13 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
             issue();              // into the slot consumed before this one
             const uint32_t keys = ring + slot * kScoreStage + (64 * warp + tl) * 128;
             const float *qp = qs + 32 * sl * R + rl * RT;
-            auto four = [&](int g4, int live) {
+            auto four = [&](int g4, int live4) {
                 float4 k[8];
 #pragma unroll
                 for (int c = 0; c < 8; ++c) k[c] = lds4(keys + c * 1024 + ((g4 ^ tl) << 4));
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                    if (kk >= live) break;
+                    if (kk >= live4) break;
                     const float *p = qp + (4 * g4 + kk) * R;
                     if constexpr (RT >= 2) {
                         f32x2 a[RT / 2];
@@ -360,7 +434,9 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
                 }
             };
             const int width = min(32, d - 32 * sl);
-            if (width == 32) {
+            if (OWN && 64 * warp >= live) {
+                // the request ends before this warp's tokens
+            } else if (width == 32) {
 #pragma unroll
                 for (int g4 = 0; g4 < 8; ++g4) four(g4, 4);
             } else {
@@ -370,16 +446,19 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
             phase ^= slot == 0;
         }
         if (stuck) {              // this and the other rows of the share are NaN
-            for (int r = tid; r < R; r += kThreads) {
-                const int row = row_of(A, it.g, kv, rb * R + r);
+            if (tid < R) {
+                const int r = r0 + tid;
+                const int row =
+                    r < rows_of<OWN>(A) ? row_at(A, g, kv, place_of<OWN>(A, it.u, r)) : -1;
                 if (row >= 0) atomicMax(A.top + row, 0xffffffffu);
             }
         } else {
+            const int64_t octet = (int64_t(g) * A.kv_heads + kv) * A.octets + t0 / 8 + 8 * warp;
+            float *x = A.x + (octet * A.rows + place_of<OWN>(A, it.u, r0 + rl)) * 8 + tl;
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 const int row = rows[rl * RT + r];
                 float most = __uint_as_float(0xff800000u);
-                float *to = A.x + row * A.ldx + it.c * kKChunk + 64 * warp + tl;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     float s, other;
@@ -389,9 +468,10 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
                         unpack2(acc[r / 2][c], s, other);
                         if (r & 1) s = other;
                     }
-                    const float x = __fmul_rn(s, A.scale);
-                    if (row >= 0) to[8 * c] = x;
-                    most = max_nan(most, x);
+                    const float v = __fmul_rn(s, A.scale);
+                    const bool here = !OWN || 64 * warp + 8 * c + tl < live;
+                    if (row >= 0 && here) x[c * A.rows * 8 + r * 32] = v;
+                    if (here) most = max_nan(most, v);
                 }
 #pragma unroll
                 for (int off = 4; off >= 1; off >>= 1)
@@ -399,9 +479,9 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
                 if (tl == 0 && row >= 0) atomicMax(A.top + row, max_key(most));
             }
         }
-        advance(A, mul, it);
+        advance<OWN>(A, mul, it);
     }
-    if (LOAD == kTma && stuck) {          // let the copies in flight land
+    if (TMA && stuck) {                   // let the copies in flight land
         for (int i = 0; i < kScoreStages; ++i) {
             (void)mbar_wait_bounded(smem_u32(full + slot), phase);
             slot ^= 1;
@@ -411,11 +491,66 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
     }
 }
 
+// ---------------------------------------------------------------- sums
+// A CTA four rows of a group and head: 8 lanes have the two halves of 4 octets of a
+// row, so 8 of its 256 chains; a thread two chains, each in ascending order.
+constexpr int kSumThreads = 512;
+constexpr int kSumRows = 4;
+constexpr int kSumDeep = 8;                        // groups of a chain in flight
+
+__global__ void __launch_bounds__(kSumThreads) shared_sums_kernel(const SharedArgs A) {
+    __shared__ float chains[kSumRows][256], red[kSumRows][8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int r = lane >> 3, place = blockIdx.x * kSumRows + r;
+    const int g = blockIdx.y / A.kv_heads, kv = blockIdx.y % A.kv_heads;
+    const int row = place < A.rows ? row_at(A, g, kv, place) : -1;
+    const int n = row >= 0 ? A.kv_lens[row / A.heads] : 0;
+    const float m = row >= 0 ? max_of_key(A.top[row]) : 0.0f;
+    const bool finite = fabsf(m) <= 0x1.fffffep127f;
+    float *x = A.x + (int64_t(blockIdx.y) * A.octets * A.rows + place) * 8;
+    for (int l = 8 * warp + (lane & 7); l < 256; l += 8 * (kSumThreads / 32)) {
+        float sum = 0.0f;
+        for (int t = 4 * l; t < n; t += 1024 * kSumDeep) {
+            float4 e[kSumDeep];
+#pragma unroll
+            for (int u = 0; u < kSumDeep; ++u)
+                if (t + 1024 * u < n)
+                    e[u] = *reinterpret_cast<const float4 *>(
+                        x + (t / 8 + 128 * u) * A.rows * 8 + (t & 4));
+#pragma unroll
+            for (int u = 0; u < kSumDeep; ++u) {
+                const int tu = t + 1024 * u;
+                if (tu >= n) break;
+                e[u] = finite ? exp4(e[u], m) : exp4_any(e[u], m);
+                *reinterpret_cast<float4 *>(x + (t / 8 + 128 * u) * A.rows * 8 + (t & 4)) = e[u];
+                sum = __fadd_rn(sum, e[u].x);
+                if (tu + 1 < n) sum = __fadd_rn(sum, e[u].y);
+                if (tu + 2 < n) sum = __fadd_rn(sum, e[u].z);
+                if (tu + 3 < n) sum = __fadd_rn(sum, e[u].w);
+            }
+        }
+        chains[r][l] = sum;
+    }
+    __syncthreads();
+    for (int i = warp; i < kSumRows * 8; i += kSumThreads / 32) {
+        const float s = butterfly32(chains[i >> 3][(i & 7) * 32 + lane]);
+        if (lane == 0) red[i >> 3][i & 7] = s;
+    }
+    __syncthreads();
+    if (warp == 0 && (lane & 7) == 0 && row >= 0) {
+        const float *t = red[r];
+        A.inv[row] = __fdiv_rn(
+            1.0f, __fadd_rn(__fadd_rn(__fadd_rn(t[0], t[1]), __fadd_rn(t[2], t[3])),
+                            __fadd_rn(__fadd_rn(t[4], t[5]), __fadd_rn(t[6], t[7]))));
+    }
+}
+
 // ---------------------------------------------------------------- partials
 // An item: 4 RT rows, 32 DH dimensions, a chunk; it is a warp's alone (4 lanes x RT
 // rows, 8 lanes x 4 DH dimensions), which walks the chunk's tokens 16 at a time:
 // values by its own ring, exps loaded a step ahead, multiplied by 1 / S and laid
-// down transposed.
+// down transposed (rows 16 apart swapped for every other four tokens, so that the two
+// halves of an octet go to different banks).
 template <int RT, int DH>
 struct PvWarp {
     static constexpr int kR = 4 * RT;
@@ -423,62 +558,68 @@ struct PvWarp {
     static constexpr int kBytes = (kPvStages * kStage + kPvTokens * kR * 4 + 1023) / 1024 * 1024;
 };
 
-template <int RT, int DH, Loader LOAD>
+template <int RT, int DH, bool OWN, bool TMA>
 __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
     shared_partials_kernel(const SharedArgs A, const __grid_constant__ CUtensorMap vmap) {
     using W = PvWarp<RT, DH>;
     constexpr int R = W::kR;
     constexpr int LOADS = R / 8 > 1 ? R / 8 : 1;      // 16-byte loads of exps a lane and step
-    constexpr int OWN = R == 64 ? 2 : 1;              // rows whose exps a lane loads
+    constexpr int OWNED = R / 16 > 1 ? R / 16 : 1;    // rows whose exps a lane loads
+    constexpr int SWAP = R >= 32 ? 16 : 0;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ Share share[kWarps];
     __shared__ uint64_t full[kWarps][kPvStages];
     __shared__ int rows[kWarps][R];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, dl = lane & 7, rl = lane >> 3;
     const int d = A.d, mul = A.kv_heads * A.row_blocks * A.dim_tiles;
-    if (LOAD == kTma && tid == 0) {
+    if (TMA && tid == 0) {
         for (int i = 0; i < kWarps * kPvStages; ++i) mbar_init(smem_u32(&full[0][i]), 1);
         fence_mbar_init();
     }
-    shares<kWarps>(A, mul, blockIdx.x * kWarps, gridDim.x * kWarps, share);
-    const int64_t items = share[warp].hi - share[warp].lo;
+    shares<OWN, kWarps>(A, mul, blockIdx.x, gridDim.x, gridDim.x * kWarps, share);
+    const int64_t items = share[warp].items;
     if (items <= 0) return;
     const uint32_t ring = smem_u32(smem_raw) + warp * W::kBytes;
     float *ps = reinterpret_cast<float *>(smem_raw + warp * W::kBytes + kPvStages * W::kStage);
 
     // ---- values
     Item in = share[warp].at;
-    int in_step = 0, in_slot = 0;
-    int64_t left = items * kPvSteps;
-    const int per_half = LOAD == kTma ? kPvTokens / A.box : 1;       // boxes of 32 dimensions
-    int id = 0;
-    auto ask_page = [&]() {
-        if (LOAD == kTma && lane < DH * per_half && in.g < A.groups)
-            id = A.table[A.lead[in.g] * A.ldt +
-                         page_of(A, in.c * kKChunk + in_step * kPvTokens + lane % per_half * A.box)];
+    int64_t in_items = items;
+    int in_t = 0, in_live = 0, in_slot = 0, in_id = 0;      // next token of the item, tokens left
+    const int per_half = TMA ? kPvTokens / A.box : 1;       // boxes of 32 dimensions
+    auto look_up = [&]() {            // the page of the lane's box of the next step
+        if (TMA && in_items > 0 && lane < DH * per_half && lane % per_half * A.box < in_live)
+            in_id = pages_of<OWN>(A, in)[page_of(A, in_t + lane % per_half * A.box)];
     };
-    ask_page();
+    auto start = [&]() {
+        if (in_items <= 0) return;
+        in_t = first_token<OWN>(A, in);
+        in_live = tokens_from<OWN>(A, in, in_t);
+    };
+    start();
+    look_up();
     auto issue = [&]() {
-        if (left > 0) {
-            --left;
+        if (in_items > 0) {
             const int kv = in.run / (A.row_blocks * A.dim_tiles), dim0 = in.run % A.dim_tiles * 32 * DH;
-            const int t0 = in.c * kKChunk + in_step * kPvTokens;
             const uint32_t dst = ring + in_slot * W::kStage, bar = smem_u32(&full[warp][in_slot]);
-            if constexpr (LOAD == kTma) {
-                if (lane == 0) mbar_arrive_expect_tx(bar, W::kStage);
+            const int live = min(kPvTokens, in_live);
+            if constexpr (TMA) {
+                const int boxes = (live + A.box - 1) / A.box;
+                if (lane == 0) mbar_arrive_expect_tx(bar, boxes * A.box * 128 * DH);
                 __syncwarp();
-                if (lane < DH * per_half) {
-                    const int half = lane / per_half, box = lane % per_half, t = t0 + box * A.box;
+                const int half = lane / per_half, box = lane % per_half;
+                if (half < DH && box < boxes) {
+                    const int t = in_t + box * A.box;
                     tma_load_4d(dst + half * kPvTokens * 128 + box * A.box * 128, &vmap,
                                 dim0 + 32 * half, kv,
-                                int(unsigned(t) - page_of(A, t) * A.page_size), id, bar);
+                                int(unsigned(t) - page_of(A, t) * A.page_size), in_id, bar);
                 }
             } else {
-                const int32_t *pages = A.table + A.lead[in.g] * A.ldt;
+                const int32_t *pages = pages_of<OWN>(A, in);
                 const float *src = A.v + kv * A.head_stride + dim0;
-                if constexpr (LOAD == kCopy16) {
-                    for (int r = lane >> 3; r < kPvTokens; r += 4) {
-                        const float *from = src + offset_of(A, pages, t0 + r);
+                if (A.wide) {
+                    for (int r = lane >> 3; r < live; r += 4) {
+                        const float *from = src + offset_of(A, pages, in_t + r);
 #pragma unroll
                         for (int half = 0; half < DH; ++half)
                             if (dim0 + 32 * half + 4 * dl < d)
@@ -487,8 +628,8 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
                                              from + 32 * half + 4 * dl);
                     }
                 } else {
-                    for (int r = 0; r < kPvTokens; ++r) {
-                        const float *from = src + offset_of(A, pages, t0 + r);
+                    for (int r = 0; r < live; ++r) {
+                        const float *from = src + offset_of(A, pages, in_t + r);
 #pragma unroll
                         for (int half = 0; half < DH; ++half)
                             if (dim0 + 32 * half + lane < d)
@@ -499,52 +640,60 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
                 }
             }
             in_slot = in_slot + 1 == kPvStages ? 0 : in_slot + 1;
-            if (++in_step == kPvSteps) {
-                in_step = 0;
-                advance(A, mul, in);
+            in_t += kPvTokens;
+            in_live -= kPvTokens;
+            if (in_live <= 0) {
+                advance<OWN>(A, mul, in);
+                --in_items;
+                start();
             }
-            ask_page();
+            look_up();
         }
-        if (LOAD != kTma) cp_commit();
+        if (!TMA) cp_commit();
     };
     for (int i = 0; i < kPvStages - 1; ++i) issue();
 
-    // ---- exps: load i of a lane is of row (lane + 32 i) mod R, tokens 4 ((lane + 32 i) / R) on
-    const float *from[OWN];
-    float inv[OWN];
+    // ---- exps: load k of a lane is number i = lane + 32 k of the step's 4 R: octet i /
+    // (2 R), row i mod 2 R / 2, half i mod 2
     float4 e[LOADS];
-    const bool loads = R >= 8 || lane < 16;
+    float inv[OWNED];
+    const float *from = nullptr;      // of the item's first octet and the block's first row
+    int alive = 0;                    // the block's rows
     auto ask = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            e[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (loads && from[i % OWN])
-                e[i] = *reinterpret_cast<const float4 *>(from[i % OWN] + t +
-                                                         4 * ((lane + 32 * i) / R));
+        for (int k = 0; k < LOADS; ++k) {
+            const int i = lane + 32 * k, row = i % (2 * R) / 2;
+            e[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i < 4 * R && row < alive)
+                e[k] = *reinterpret_cast<const float4 *>(
+                    from + (int64_t(t / 8 + i / (2 * R)) * A.rows + row) * 8 + 4 * (i & 1));
         }
     };
     Item it = share[warp].at;
-    int held_g = -1, held_run = -1, slot = 0;
+    int held_u = -1, held_run = -1, slot = 0;
     uint32_t phase = 0;
     bool stuck = false;
-    auto hold = [&]() {           // the item's rows
-        if (it.g == held_g && it.run == held_run) return;
-        held_g = it.g;
-        held_run = it.run;
+    auto hold = [&]() {               // the item's rows
         const int block = it.run / A.dim_tiles, kv = block / A.row_blocks;
-        const int r0 = (block - kv * A.row_blocks) * R;
+        const int r0 = (block - kv * A.row_blocks) * R, g = group_of<OWN>(A, it.u);
+        from = A.x + (((int64_t(g) * A.kv_heads + kv) * A.octets + first_token<OWN>(A, it) / 8) *
+                          A.rows + place_of<OWN>(A, it.u, r0)) * 8;
+        if (it.u == held_u && it.run == held_run) return;
+        held_u = it.u;
+        held_run = it.run;
+        alive = min(R, rows_of<OWN>(A) - r0);
         __syncwarp();
-        for (int r = lane; r < R; r += 32) rows[warp][r] = row_of(A, it.g, kv, r0 + r);
+        for (int r = lane; r < R; r += 32)
+            rows[warp][r] = r < alive ? row_at(A, g, kv, place_of<OWN>(A, it.u, r0 + r)) : -1;
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < OWN; ++i) {
-            const int row = rows[warp][(lane + 32 * i) % R];
-            from[i] = row >= 0 ? A.x + row * A.ldx : nullptr;
+        for (int i = 0; i < OWNED; ++i) {
+            const int row = rows[warp][(lane + 32 * i) % (2 * R) / 2];
             inv[i] = row >= 0 ? A.inv[row] : 0.0f;
         }
     };
     hold();
-    ask(it.c * kKChunk);
+    ask(0);
     constexpr bool kRowPairs = RT >= 8;
     for (int64_t i = 0; i < items; ++i) {
         constexpr int N0 = kRowPairs ? RT / 2 : RT, N1 = kRowPairs ? 4 * DH : 2 * DH;
@@ -553,30 +702,34 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
         for (int a = 0; a < N0; ++a)
 #pragma unroll
             for (int b = 0; b < N1; ++b) acc[a][b] = 0;
-        const Item now = it;
-        int mine[RT];             // the rows whose partials the lane has
+        const int t0 = first_token<OWN>(A, it), tokens = tokens_from<OWN>(A, it, t0);
+        const int dim0 = it.run % A.dim_tiles * 32 * DH + 4 * dl;
+        int mine[RT];                 // the rows whose partials the lane has
 #pragma unroll
         for (int r = 0; r < RT; ++r) mine[r] = rows[warp][rl * RT + r];
-        for (int step = 0; step < kPvSteps; ++step) {
+        for (int t1 = 0; t1 < tokens; t1 += kPvTokens) {
             __syncwarp();
 #pragma unroll
-            for (int k = 0; k < LOADS; ++k)
-                if (loads) {
-                    float *to = ps + 4 * ((lane + 32 * k) / R) * R + (lane + 32 * k) % R;
-                    const float w = inv[k % OWN];
+            for (int k = 0; k < LOADS; ++k) {
+                const int j = lane + 32 * k, half = j & 1;
+                if (j < 4 * R) {
+                    float *to = ps + (8 * (j / (2 * R)) + 4 * half) * R +
+                                (j % (2 * R) / 2 ^ SWAP * half);
+                    const float w = inv[k % OWNED];
                     to[0] = __fmul_rn(e[k].x, w);
                     to[R] = __fmul_rn(e[k].y, w);
                     to[2 * R] = __fmul_rn(e[k].z, w);
                     to[3 * R] = __fmul_rn(e[k].w, w);
                 }
-            if (step + 1 < kPvSteps) {
-                ask(it.c * kKChunk + (step + 1) * kPvTokens);
-            } else if (i + 1 < items) {
-                advance(A, mul, it);
-                hold();
-                ask(it.c * kKChunk);
             }
-            if constexpr (LOAD == kTma) {
+            if (t1 + kPvTokens < tokens) {
+                ask(t1 + kPvTokens);
+            } else if (i + 1 < items) {
+                advance<OWN>(A, mul, it);
+                hold();
+                ask(0);
+            }
+            if constexpr (TMA) {
                 if (!stuck)
                     stuck = __any_sync(0xffffffffu,
                                        !mbar_wait_bounded(smem_u32(&full[warp][slot]), phase));
@@ -586,9 +739,8 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
             __syncwarp();
             if (!stuck) issue();      // into the slot consumed before this one
             const uint32_t vals = ring + slot * W::kStage;
-#pragma unroll
-            for (int t = 0; t < kPvTokens; ++t) {
-                const float *p = ps + t * R + rl * RT;
+            auto token = [&](int t) {
+                const float *p = ps + t * R + (rl * RT ^ SWAP * (t >> 2 & 1));
                 const uint32_t at = vals + t * 128 + ((dl ^ (t & 7)) << 4);
                 if constexpr (kRowPairs) {
                     f32x2 w[RT / 2];
@@ -619,6 +771,12 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
                         for (int k = 0; k < 2 * DH; ++k) acc[r][k] = fma2(w, v[k], acc[r][k]);
                     }
                 }
+            };
+            if (!OWN || t1 + kPvTokens <= tokens) {
+#pragma unroll
+                for (int t = 0; t < kPvTokens; ++t) token(t);
+            } else {
+                for (int t = 0; t < tokens - t1; ++t) token(t);
             }
             if (++slot == kPvStages) {
                 slot = 0;
@@ -626,11 +784,10 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
             }
         }
         // ---- the partials of the lane's rows and dimensions
-        const int dim0 = now.run % A.dim_tiles * 32 * DH + 4 * dl;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             if (mine[r] < 0) continue;
-            float *to = A.part + (mine[r] * A.ldpart + now.c) * d;
+            float *to = A.part + (mine[r] * A.ldpart + t0 / kKChunk) * d;
 #pragma unroll
             for (int half = 0; half < DH; ++half) {
                 float4 o;
@@ -659,8 +816,8 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
             }
         }
     }
-    if (LOAD != kTma) cp_wait<0>();
-    if (LOAD == kTma && stuck) {          // let the copies in flight land
+    if (!TMA) cp_wait<0>();
+    if (TMA && stuck) {                   // let the copies in flight land
         for (int i = 0; i < kPvStages; ++i) {
             (void)mbar_wait_bounded(smem_u32(&full[warp][slot]), phase);
             if (++slot == kPvStages) {
@@ -673,15 +830,15 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
 }
 
 // ---------------------------------------------------------------- join
-// A thread an element of the output; rows whose group shares nothing are done.
+// A thread an element of the output.
 constexpr int kJoinDeep = 32;
 __global__ void __launch_bounds__(kThreads) shared_join_kernel(const SharedArgs A) {
     const int b = blockIdx.y, i = blockIdx.x * kThreads + threadIdx.x;
-    const int n = A.kv_lens[b];
-    if (i >= A.heads * A.d || A.chunks[b / A.group] == 0 || !in_order(A, n)) return;
-    const int h = i / A.d, chunks = (n + kKChunk - 1) / kKChunk;
+    if (i >= A.heads * A.d) return;
+    const int n = A.kv_lens[b], h = i / A.d;
+    const int chunks = A.own[b] ? (n + kKChunk - 1) / kKChunk : 0;
     const float *p = A.part + (int64_t(b) * A.heads + h) * A.ldpart * A.d + (i - h * A.d);
-    float t = 0.0f;
+    float t = chunks || n == 0 ? 0.0f : __uint_as_float(0x7fc00000u);
     for (int c = 0; c < chunks; c += kJoinDeep) {
         float v[kJoinDeep];
 #pragma unroll
@@ -697,93 +854,102 @@ __global__ void __launch_bounds__(kThreads) shared_join_kernel(const SharedArgs 
 // ---------------------------------------------------------------- host
 constexpr size_t kSliceBytes = size_t(1) << 30;     // scores and partials of a round of heads
 
+// Rows a thread takes of a unit's rows.
+int rows_a_thread(int64_t rows, int64_t head_dim) {
+    return rows <= 4 ? 1 : rows <= 8 ? 2 : rows <= 16 ? 4 : rows <= 32 || head_dim > 192 ? 8 : 16;
+}
+
 struct SharedPlan {
-    bool together;            // false: decode.cu alone
-    int rt, dh, row_blocks, dim_tiles;
+    bool together;            // false: decode.cu
     int64_t groups, kv, heads, ldx, ldpart;      // kv, heads: of a round
-    size_t top, inv, x, part, own, bytes;        // offsets in the workspace
+    size_t top, inv, x, part, bytes;             // offsets in the workspace
 };
 
 SharedPlan shared_plan(int64_t batch, int64_t group, int64_t heads, int64_t kv_heads,
                        int64_t head_dim, int64_t max_len) {
     SharedPlan p = {};
     group = std::min(group, batch);
-    const int64_t per_kv = heads / kv_heads, rows = group * per_kv;
-    p.together = group > 1 && max_len > 2 * kKChunk && rows <= 0x7fffffff / 2 &&
-                 batch * heads <= 0x7fffffff / 2;
+    const int64_t per_kv = heads / kv_heads;
+    p.groups = group > 0 ? (batch + group - 1) / group : 0;
+    p.together = group > 1 && max_len > 2 * kKChunk && p.groups * group * heads < 0x7fffffff / 8;
     if (!p.together) {
         p.bytes = decode_workspace_bytes(batch, heads, kv_heads, head_dim, max_len);
         return p;
     }
-    p.groups = (batch + group - 1) / group;
-    p.rt = rows <= 4 ? 1 : rows <= 8 ? 2 : rows <= 16 ? 4 : rows <= 32 || head_dim > 192 ? 8 : 16;
-    p.dh = head_dim <= 32 ? 1 : 2;
-    p.row_blocks = int((rows + 4 * p.rt - 1) / (4 * p.rt));
-    p.dim_tiles = int((head_dim + 32 * p.dh - 1) / (32 * p.dh));
-    p.ldx = (max_len - 1) / kKChunk * kKChunk;
     p.ldpart = (max_len + kKChunk - 1) / kKChunk;
-    const size_t head = size_t(batch) * per_kv * (p.ldx + p.ldpart * head_dim) * 4;
+    p.ldx = p.ldpart * kKChunk;
+    const int64_t rows = p.groups * group * per_kv;       // of a key-value head
+    const size_t head = size_t(rows) * (p.ldx + p.ldpart * head_dim) * 4;
     p.kv = std::max<int64_t>(1, std::min<int64_t>(kv_heads, int64_t(kSliceBytes / head)));
     p.heads = p.kv * per_kv;
     auto after = [](size_t at, size_t bytes) { return (at + bytes + 255) / 256 * 256; };
-    p.top = after(0, size_t(p.groups) * 8);
+    p.top = after(0, size_t(2 * p.groups + batch) * 4);
     p.inv = after(p.top, size_t(batch) * p.heads * 4);
     p.x = after(p.inv, size_t(batch) * p.heads * 4);
-    p.part = after(p.x, size_t(batch) * p.heads * p.ldx * 4);
-    p.own = after(p.part, size_t(batch) * p.heads * p.ldpart * head_dim * 4);
-    p.bytes = p.own + decode_workspace_bytes(batch, p.heads, p.kv, head_dim, max_len);
+    p.part = after(p.x, size_t(rows) * p.kv * p.ldx * 4);
+    p.bytes = after(p.part, size_t(batch) * p.heads * p.ldpart * head_dim * 4);
     return p;
 }
 
-template <class K, class... Args>
-cudaError_t run(K kern, int64_t grid, size_t smem, cudaStream_t s, Args... args) {
+template <class K>
+cudaError_t run(K kern, int64_t grid, size_t smem, cudaStream_t s, const SharedArgs &A,
+                const CUtensorMap &map) {
     // the most any call takes: the limit is the kernel's, and another thread's call may
     // come between this line and the launch
     const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxSmem));
     if (e != cudaSuccess) return e;
-    kern<<<unsigned(grid), kThreads, smem, s>>>(args...);
+    kern<<<unsigned(std::max<int64_t>(1, grid)), kThreads, smem, s>>>(A, map);
     return cudaGetLastError();
 }
 
-template <int RT, Loader LOAD>
-cudaError_t run_scores(const SharedArgs &A, const CUtensorMap &map, int64_t most, cudaStream_t s) {
+// most: the chunks of all units, at most.
+template <int RT, bool OWN>
+cudaError_t run_scores(SharedArgs A, const CUtensorMap *map, int64_t rows, int64_t most,
+                       cudaStream_t s) {
+    A.row_blocks = int((rows + 4 * RT - 1) / (4 * RT));
     const int64_t grid = std::min<int64_t>(
         most * A.kv_heads * A.row_blocks, int64_t(sm_count_current_device()) * (RT >= 8 ? 2 : 3));
     const size_t smem = kScoreStages * kScoreStage + size_t(A.d) * 4 * RT * 4;
-    return run(shared_scores_kernel<RT, LOAD>, grid, smem, s, A, map);
+    const CUtensorMap none = {};
+    return map ? run(shared_scores_kernel<RT, OWN, true>, grid, smem, s, A, *map)
+               : run(shared_scores_kernel<RT, OWN, false>, grid, smem, s, A, none);
 }
-template <int RT, int DH, Loader LOAD>
-cudaError_t run_partials(const SharedArgs &A, const CUtensorMap &map, int64_t most,
+template <bool OWN>
+cudaError_t scores(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
+    const int64_t rows = OWN ? A.per_kv : A.rows;
+    switch (rows_a_thread(rows, A.d)) {
+        case 1: return run_scores<1, OWN>(A, map, rows, most, s);
+        case 2: return run_scores<2, OWN>(A, map, rows, most, s);
+        case 4: return run_scores<4, OWN>(A, map, rows, most, s);
+        case 8: return run_scores<8, OWN>(A, map, rows, most, s);
+        default: return run_scores<16, OWN>(A, map, rows, most, s);
+    }
+}
+
+template <int RT, int DH, bool OWN>
+cudaError_t run_partials(SharedArgs A, const CUtensorMap *map, int64_t rows, int64_t most,
                          cudaStream_t s) {
+    A.row_blocks = int((rows + 4 * RT - 1) / (4 * RT));
+    A.dim_tiles = (A.d + 32 * DH - 1) / (32 * DH);
     const int64_t items = most * A.kv_heads * A.row_blocks * A.dim_tiles;
     const int64_t grid =
         std::min<int64_t>((items + kWarps - 1) / kWarps,
                           int64_t(sm_count_current_device()) * (RT >= 8 ? 2 : 3));
-    return run(shared_partials_kernel<RT, DH, LOAD>, grid, size_t(kWarps) * PvWarp<RT, DH>::kBytes,
-               s, A, map);
+    const size_t smem = size_t(kWarps) * PvWarp<RT, DH>::kBytes;
+    const CUtensorMap none = {};
+    return map ? run(shared_partials_kernel<RT, DH, OWN, true>, grid, smem, s, A, *map)
+               : run(shared_partials_kernel<RT, DH, OWN, false>, grid, smem, s, A, none);
 }
-
-template <Loader LOAD>
-cudaError_t scores_for(int rt, const SharedArgs &A, const CUtensorMap &map, int64_t most,
-                       cudaStream_t s) {
-    switch (rt) {
-        case 1: return run_scores<1, LOAD>(A, map, most, s);
-        case 2: return run_scores<2, LOAD>(A, map, most, s);
-        case 4: return run_scores<4, LOAD>(A, map, most, s);
-        case 8: return run_scores<8, LOAD>(A, map, most, s);
-        default: return run_scores<16, LOAD>(A, map, most, s);
-    }
-}
-template <int DH, Loader LOAD>
-cudaError_t partials_for(int rt, const SharedArgs &A, const CUtensorMap &map, int64_t most,
-                         cudaStream_t s) {
-    switch (rt) {
-        case 1: return run_partials<1, DH, LOAD>(A, map, most, s);
-        case 2: return run_partials<2, DH, LOAD>(A, map, most, s);
-        case 4: return run_partials<4, DH, LOAD>(A, map, most, s);
-        case 8: return run_partials<8, DH, LOAD>(A, map, most, s);
-        default: return run_partials<16, DH, LOAD>(A, map, most, s);
+template <int DH, bool OWN>
+cudaError_t partials(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
+    const int64_t rows = OWN ? A.per_kv : A.rows;
+    switch (rows_a_thread(rows, 0)) {
+        case 1: return run_partials<1, DH, OWN>(A, map, rows, most, s);
+        case 2: return run_partials<2, DH, OWN>(A, map, rows, most, s);
+        case 4: return run_partials<4, DH, OWN>(A, map, rows, most, s);
+        case 8: return run_partials<8, DH, OWN>(A, map, rows, most, s);
+        default: return run_partials<16, DH, OWN>(A, map, rows, most, s);
     }
 }
 
@@ -810,6 +976,7 @@ cudaError_t launch_shared_decode(int64_t batch, int64_t group, int heads, const 
     A.group = int(std::min(group, batch));
     A.groups = int(p.groups);
     A.per_kv = int(heads / c.kv_heads);
+    A.rows = int64_t(A.group) * A.per_kv;
     A.d = int(d);
     A.ldq = ldq;
     A.num_pages = c.num_pages;
@@ -821,73 +988,61 @@ cudaError_t launch_shared_decode(int64_t batch, int64_t group, int heads, const 
     A.token_stride = c.token_stride;
     A.head_stride = c.head_stride;
     A.table = table;
-    A.max_pages = max_pages;
     A.ldt = ldt;
     A.kv_lens = kv_lens;
     A.max_len = max_len;
     A.scale = scale;
-    A.row_blocks = p.row_blocks;
-    A.dim_tiles = p.dim_tiles;
     A.chunks = reinterpret_cast<int *>(ws);
     A.lead = A.chunks + p.groups;
+    A.own = A.lead + p.groups;
     A.top = reinterpret_cast<unsigned *>(ws + p.top);
+    A.inv = reinterpret_cast<float *>(ws + p.inv);
     A.x = reinterpret_cast<float *>(ws + p.x);
-    A.ldx = p.ldx;
-    float *inv = reinterpret_cast<float *>(ws + p.inv);
-    A.inv = inv;
+    A.octets = p.ldx / 8;
     A.part = reinterpret_cast<float *>(ws + p.part);
     A.ldpart = p.ldpart;
     A.ldo = ldo;
+    A.dev_status = dev_status;
     auto al16 = [](const void *x) { return reinterpret_cast<uintptr_t>(x) % 16 == 0; };
     const bool vec = al16(c.k) && al16(c.v) && c.page_stride % 4 == 0 &&
                      c.token_stride % 4 == 0 && c.head_stride % 4 == 0;
+    A.wide = vec && d % 4 == 0;
     const bool boxes = c.page_size == 8 || c.page_size == 16 || c.page_size == 32 ||
                        c.page_size % 64 == 0;
-    const int64_t most = p.groups * (p.ldx / kKChunk);       // items of a run, at most
+    const int64_t most = p.groups * p.ldpart, most_own = batch * p.ldpart;
     for (int64_t g0 = 0; g0 < c.kv_heads; g0 += p.kv) {
-        det_kv_cache part = c;
-        part.kv_heads = std::min(p.kv, c.kv_heads - g0);
-        part.k += g0 * c.head_stride;
-        part.v += g0 * c.head_stride;
-        A.kv_heads = int(part.kv_heads);
+        A.kv_heads = int(std::min(p.kv, c.kv_heads - g0));
         A.heads = A.kv_heads * A.per_kv;
-        A.k = part.k;
-        A.v = part.v;
+        A.k = c.k + g0 * c.head_stride;
+        A.v = c.v + g0 * c.head_stride;
         A.q = q + g0 * A.per_kv * d;
         A.out = out + g0 * A.per_kv * d;
-        Loader load = vec && d % 4 == 0 ? kCopy16 : kCopy4;
         CUtensorMap kmap = {}, vmap = {};
         const int kbox = int(std::min<int64_t>(c.page_size, 64));
         const int vbox = int(std::min<int64_t>(c.page_size, kPvTokens));
+        bool tma = false;
         if (vec && boxes) {
-            const int64_t extent[4] = {d, part.kv_heads, c.page_size, c.num_pages};
+            const int64_t extent[4] = {d, A.kv_heads, c.page_size, c.num_pages};
             const int64_t stride[3] = {c.head_stride, c.token_stride, c.page_stride};
-            if (make_tensor_map_4d(&kmap, part.k, extent, stride, {32, 1, uint32_t(kbox), 1}) &&
-                make_tensor_map_4d(&vmap, part.v, extent, stride, {32, 1, uint32_t(vbox), 1}))
-                load = kTma;
+            tma = make_tensor_map_4d(&kmap, A.k, extent, stride, {32, 1, uint32_t(kbox), 1}) &&
+                  make_tensor_map_4d(&vmap, A.v, extent, stride, {32, 1, uint32_t(vbox), 1});
         }
         shared_plan_kernel<<<unsigned(p.groups), kPlanThreads, 0, s>>>(A);
         cudaError_t e = cudaGetLastError();
         A.box = kbox;
-        if (e == cudaSuccess)
-            e = load == kTma      ? scores_for<kTma>(p.rt, A, kmap, most, s)
-                : load == kCopy16 ? scores_for<kCopy16>(p.rt, A, kmap, most, s)
-                                  : scores_for<kCopy4>(p.rt, A, kmap, most, s);
-        const SharedPrefix sh = {A.chunks, A.group, A.x, A.ldx, A.top, inv, A.part, A.ldpart};
-        if (e == cudaSuccess)
-            e = launch_decode_attention(batch, A.heads, A.q, ldq, part, table, max_pages, ldt,
-                                        kv_lens, scale, A.out, ldo,
-                                        reinterpret_cast<float *>(ws + p.own), dev_status, s, &sh);
+        if (e == cudaSuccess) e = scores<false>(A, tma ? &kmap : nullptr, most, s);
+        if (e == cudaSuccess) e = scores<true>(A, tma ? &kmap : nullptr, most_own, s);
+        if (e == cudaSuccess) {
+            shared_sums_kernel<<<dim3(unsigned((A.rows + kSumRows - 1) / kSumRows),
+                                      unsigned(p.groups * A.kv_heads)),
+                                 kSumThreads, 0, s>>>(A);
+            e = cudaGetLastError();
+        }
         A.box = vbox;
-        auto pv = [&](auto dh) {
-            constexpr int DH = decltype(dh)::value;
-            return load == kTma      ? partials_for<DH, kTma>(p.rt, A, vmap, most, s)
-                   : load == kCopy16 ? partials_for<DH, kCopy16>(p.rt, A, vmap, most, s)
-                                     : partials_for<DH, kCopy4>(p.rt, A, vmap, most, s);
-        };
+        const CUtensorMap *map = tma ? &vmap : nullptr;
         if (e == cudaSuccess)
-            e = p.dh == 1 ? pv(std::integral_constant<int, 1>())
-                          : pv(std::integral_constant<int, 2>());
+            e = d <= 32 ? partials<1, false>(A, map, most, s) : partials<2, false>(A, map, most, s);
+        if (e == cudaSuccess) e = partials<1, true>(A, map, most_own, s);
         if (e == cudaSuccess) {
             shared_join_kernel<<<dim3(unsigned((A.heads * d + kThreads - 1) / kThreads),
                                       unsigned(batch)),

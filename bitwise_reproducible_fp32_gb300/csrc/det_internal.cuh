@@ -222,8 +222,7 @@ cudaError_t launch_decode_attention(int64_t batch, int heads, const float *q, in
                                     const det_kv_cache &c, const int32_t *table,
                                     int64_t max_pages, int64_t ldt, const int32_t *kv_lens,
                                     float scale, float *out, int64_t ldo, float *workspace,
-                                    int32_t *dev_status, cudaStream_t s,
-                                    const struct SharedPrefix *shared = nullptr);
+                                    int32_t *dev_status, cudaStream_t s);
 // The same with requests read together in groups (decode_shared.cu).
 size_t shared_decode_workspace_bytes(int64_t batch, int64_t group, int64_t heads,
                                      int64_t kv_heads, int64_t head_dim, int64_t max_len);
