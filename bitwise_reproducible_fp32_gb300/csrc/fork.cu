@@ -3,17 +3,22 @@
 //
 // Fork and compaction are integers over the block tables: a step's are kilobytes,
 // and what bounds them is latency; large ones read and write each entry once. Each
-// is one cluster of up to 16 CTAs: the pages' marks are bitmaps cut over the
-// CTAs' shared memory (distributed, by atomic or, so in any order), which the
-// cluster's barriers part into phases. So one launch serves and no workspace or
-// memory that somebody has to clear is needed. An entry that is the one above it
-// in the table (a shared prefix) is not marked again.
+// is one cluster of up to 16 CTAs, whose shared memory has a bit a page and whose
+// barriers part the phases; so one launch serves a small table, and no workspace or
+// memory that somebody has to clear is needed. The bits are set by atomic or, so in
+// any order. Where all pages' fit, each CTA marks bits of its own, and the cluster
+// joins them slice by slice; past that (1.3 million pages) a CTA has a slice of
+// them and the others mark it from afar, at about 5 cycles a mark and SM. An entry
+// that is the one above it in the table (a shared prefix) is not marked again. What is
+// written entry by entry, the new table and the compacted free list, goes to the
+// whole GPU in launches of its own where it is large; a warp has kDeep loads in flight.
 //
 // The copy streams pages through registers, 16 bytes a thread where the layout
 // allows; HBM bounds it (each byte read and written once).
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "det_internal.cuh"
 
@@ -27,10 +32,13 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxBatch = 8192;
 constexpr int kPerThread = kMaxBatch / kThreads;
 constexpr int kMaxCluster = 16;
-constexpr int kSegment = 1024;                 // entries of a table row a warp takes at once
-constexpr int kSliceShift = 19;                // most pages of a CTA's marks: 2^19
-constexpr size_t kMaxSmem = (size_t(1) << kSliceShift) / 8 * 2 + 2 * kMaxBatch * 4;
-static_assert(kMaxSmem <= 220 * 1024, "shared memory of a CTA");
+constexpr int kSegment = 256;                  // entries of a table row a warp takes at once
+constexpr int kDeep = kSegment / 32;
+constexpr int64_t kLarge = 1 << 16;            // entries from which the whole GPU writes them
+constexpr int kSliceShift = 19;                // most pages of a slice from afar: 2^19
+constexpr int64_t kMaxBits = 160 * 1024;       // bytes of the pages' bits
+constexpr size_t kMaxSmem = kMaxBits + 2 * kMaxBatch * 4;
+static_assert(kMaxSmem <= 226 * 1024 && (1 << kSliceShift) / 8 <= kMaxBits, "shared memory of a CTA");
 
 // Exclusive prefix of v over the CTA's threads (all of them call); *total: the sum.
 __device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
@@ -55,16 +63,109 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
     return (warp ? before : 0) + in - v;
 }
 
-// The pages' marks: page p's bit is word (p & mask) / 32 of CTA p >> shift.
+// The pages' bits, cut into slices of `words` words, a CTA's after the other's. Near:
+// every CTA has all of them; else its own slice (of 2^shift pages).
 struct Marks {
     cg::cluster_group &cluster;
-    int shift;
-    __device__ __forceinline__ void set(uint32_t *own, int page) const {
-        uint32_t *w = cluster.map_shared_rank(own, page >> shift);
-        const int at = page & ((1 << shift) - 1);
-        atomicOr(w + (at >> 5), 1u << (at & 31));
+    uint32_t *bits;
+    int words, shift;
+    bool near;
+    __device__ __forceinline__ uint32_t *mine() const {
+        return near ? bits + int(cluster.block_rank()) * words : bits;
+    }
+    template <bool SET>
+    __device__ __forceinline__ void mark(int page) const {
+        const uint32_t bit = 1u << (page & 31);
+        if (near) {
+            if (SET) atomicOr(bits + (page >> 5), bit);
+            else atomicAnd(bits + (page >> 5), ~bit);
+            return;
+        }
+        uint32_t w;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;"
+            : "=r"(w)
+            : "r"(smem_u32(bits + ((page & ((1 << shift) - 1)) >> 5))), "r"(page >> shift));
+        if (SET)
+            asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(w), "r"(bit)
+                         : "memory");
+        else
+            asm volatile("red.relaxed.cluster.shared::cluster.and.b32 [%0], %1;" ::"r"(w), "r"(~bit)
+                         : "memory");
+    }
+    // All threads, after a phase of marks: mine() is the whole of them then (SET: a bit
+    // that any CTA has set; else one that none has cleared).
+    template <bool SET>
+    __device__ __forceinline__ void join() const {
+        cluster.sync();
+        const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+        if (!near || C == 1) return;
+        uint4 *own = reinterpret_cast<uint4 *>(mine());
+        for (int i = threadIdx.x; i < words / 4; i += kThreads) {
+            uint4 v = own[i];
+#pragma unroll 5
+            for (int r = 1; r < C; ++r) {
+                const uint4 o = *cluster.map_shared_rank(own + i, (rank + r) & (C - 1));
+                if (SET) v.x |= o.x, v.y |= o.y, v.z |= o.z, v.w |= o.w;
+                else v.x &= o.x, v.y &= o.y, v.z &= o.z, v.w &= o.w;
+            }
+            own[i] = v;
+        }
+        __syncthreads();
+    }
+    // All threads, after a join: everybody's bits are the whole ones.
+    __device__ __forceinline__ void spread() const {
+        const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+        if (!near || C == 1) return;
+        cluster.sync();
+        for (int i = threadIdx.x; i < words / 4; i += kThreads) {
+#pragma unroll 5
+            for (int k = 1; k < C; ++k) {
+                const int r = (rank + k) & (C - 1);
+                uint4 *at = reinterpret_cast<uint4 *>(bits + r * words) + i;
+                *at = *cluster.map_shared_rank(at, r);
+            }
+        }
+        cluster.sync();
     }
 };
+
+// The table's segments that a warp takes: w, w + all, ...
+struct Segments {
+    int row, seg, rows, segs, row_step, seg_step;
+    __device__ __forceinline__ Segments(int rows_, int64_t max_pages, int w, int all) : rows(rows_) {
+        segs = max(1, int((max_pages + kSegment - 1) / kSegment));
+        row = w / segs;
+        seg = w - row * segs;
+        row_step = all / segs;
+        seg_step = all - row_step * segs;
+    }
+    __device__ __forceinline__ bool more() const { return row < rows; }
+    __device__ __forceinline__ void next() {
+        row += row_step;
+        seg += seg_step;
+        if (seg >= segs) {
+            seg -= segs;
+            ++row;
+        }
+    }
+    // the lane's first entry, and how many of the row's n are left from there
+    __device__ __forceinline__ int64_t first() const {
+        return int64_t(seg) * kSegment + (threadIdx.x & 31);
+    }
+    __device__ __forceinline__ int left(int64_t n) const {
+        return int(max(int64_t(-1), min(n - first(), int64_t(kSegment))));
+    }
+};
+
+// Every 32nd of n entries from p, and of `above` <= n entries from up; -2 past them.
+__device__ __forceinline__ void load_entries(const int32_t *p, int n, const int32_t *up, int above,
+                                             int (&id)[kDeep], int (&over)[kDeep]) {
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+        id[k] = 32 * k < n ? p[32 * k] : -2;
+        over[k] = 32 * k < above ? up[32 * k] : -2;
+    }
+}
 
 // Every CTA's value to every CTA: the sum before this one's, and of all. The
 // cluster meets once; `slots` is not reused before it meets again.
@@ -93,20 +194,42 @@ struct ForkArgs {
     int64_t capacity;
     const int32_t *free_count;
     int32_t *lens_out, *free_count_out, *src, *dst, *tokens, *dev_status;
-    int shift;
+    int words, shift;         // of the pages' bits
+    bool near;
+    bool apart;               // the new table is written by a launch of its own
 };
 
+// The new table, from the rows' lengths and pages of their own: warp w of `all`.
+__device__ __forceinline__ void fork_rows(const ForkArgs &A, int w, int all) {
+    for (Segments at(A.batch_out, A.max_pages, w, all); at.more(); at.next()) {
+        const int r = at.row, own = __ldcg(A.dst + r);
+        const int64_t pages = (__ldcg(A.lens_out + r) + A.page_size - 1) / A.page_size;
+        const int n = at.left(pages);
+        if (n <= 0) continue;
+        const int32_t *from = A.table + A.parents[r] * A.ldt + at.first();
+        int32_t *to = A.table_out + r * A.ldto + at.first();
+        const int last = own >= 0 ? int(min(pages - 1 - at.first(), int64_t(kSegment))) : -1;
+        int id[kDeep];
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k)
+            if (32 * k < n) id[k] = from[32 * k];
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k)
+            if (32 * k < n) to[32 * k] = 32 * k == last ? own : id[k];
+    }
+}
+
 __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs A) {
-    extern __shared__ uint32_t sm[];
-    const int words = 1 << (A.shift - 5);
-    uint32_t *keep = sm, *drop = sm + words;      // pages of rows with and without a child
-    int *first = reinterpret_cast<int *>(drop + words);      // each row's first child
-    int *fresh = first + kMaxBatch;     // each new row: a page of its own, -1: none, -2: refused
+    extern __shared__ __align__(16) uint32_t sm[];
     __shared__ int warp_sums[32], slots[kMaxCluster];
     cg::cluster_group cluster = cg::this_cluster();
     const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Marks marks = {cluster, A.shift};
+    const int held = A.near ? C * A.words : A.words;
+    const Marks marks = {cluster, sm, A.words, A.shift, A.near};
+    int *first = reinterpret_cast<int *>(sm + held);         // each row's first child
+    int *pages = first + A.batch;       // each row's pages; then, of each new row:
+    int *fresh = pages;                 // a page of its own, -1: none, -2: refused
     const int64_t ps = A.page_size, room = min(A.max_pages * ps, int64_t(0x7fffffff));
     int status = 0;
     int64_t count = *A.free_count;
@@ -117,8 +240,13 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs A) 
     auto pages_of = [&](int len) {      // of a row that is in order
         return len < 0 || len > room ? int64_t(0) : (len + ps - 1) / ps;
     };
-    for (int i = tid; i < 2 * words; i += kThreads) sm[i] = 0;
-    for (int i = tid; i < A.batch; i += kThreads) first[i] = INT32_MAX;
+    for (int i = tid; i < held; i += kThreads) sm[i] = 0;
+    for (int i = tid; i < A.batch; i += kThreads) {
+        const int len = A.lens[i];
+        if (len < 0 || len > room) status |= 1;
+        first[i] = INT32_MAX;
+        pages[i] = int(pages_of(len));
+    }
     __syncthreads();
     for (int r = tid; r < A.batch_out; r += kThreads) {
         const int p = A.parents[r];
@@ -127,36 +255,43 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs A) 
     }
     __syncthreads();
     int orphan = 0;
-    for (int i = tid; i < A.batch; i += kThreads) {
-        const int len = A.lens[i];
-        if (len < 0 || len > room) status |= 1;
-        orphan |= first[i] == INT32_MAX && pages_of(len) > 0;
-    }
+    for (int i = tid; i < A.batch; i += kThreads) orphan |= first[i] == INT32_MAX && pages[i] > 0;
     orphan = __syncthreads_or(orphan);
-    cluster.sync();                     // every CTA's marks are clear
-    // 1. the pages of rows that have no child and those of rows that have one
-    const int64_t segs = (A.max_pages + kSegment - 1) / kSegment;
-    for (int64_t i = int64_t(rank) * kWarps + warp; i < A.batch * segs; i += C * kWarps) {
-        const int b = int(i / segs);
-        const int64_t n = pages_of(A.lens[b]), j0 = (i - b * segs) * kSegment;
-        if (j0 >= n) continue;
-        const bool has = first[b] != INT32_MAX;
-        const int64_t above =
-            b > 0 && (first[b - 1] != INT32_MAX) == has ? pages_of(A.lens[b - 1]) : 0;
-        const int32_t *row = A.table + b * A.ldt;
-        for (int64_t j = j0 + lane; j < min(n, j0 + kSegment); j += 32) {
-            const int id = row[j];
-            if (id < 0 || id >= A.num_pages) status |= 4;
-            else if (orphan && !(j < above && row[j - A.ldt] == id)) marks.set(has ? keep : drop, id);
+    if (!A.near) cluster.sync();        // every CTA's bits are clear
+    // 1. the pages of rows that have no child, then without those of rows that have one;
+    // an entry that is the one above it is that row's to mark, or kept by it
+    auto look = [&](auto orphans) {
+        constexpr bool SET = decltype(orphans)::value;
+        for (Segments at(A.batch, A.max_pages, rank * kWarps + warp, C * kWarps); at.more(); at.next()) {
+            const int b = at.row, n = at.left(pages[b]);
+            if ((first[b] == INT32_MAX) != SET || n <= 0) continue;
+            const bool over = orphan && b > 0 && (SET || first[b - 1] != INT32_MAX);
+            const int32_t *p = A.table + b * A.ldt + at.first();
+            int id[kDeep], up[kDeep];
+            load_entries(p, n, p - A.ldt, over ? min(n, at.left(pages[b - 1])) : 0, id, up);
+#pragma unroll
+            for (int k = 0; k < kDeep; ++k) {
+                if (32 * k >= n) break;
+                if (unsigned(id[k]) >= unsigned(A.num_pages)) status |= 4;
+                else if (orphan && up[k] != id[k]) marks.mark<SET>(id[k]);
+            }
         }
+    };
+    look(std::true_type());
+    if (orphan) {
+        marks.join<true>();
+        marks.spread();
     }
-    cluster.sync();
+    look(std::false_type());
     // 2. the pages that nobody holds any more, ascending, to the end of the free list
     int freed = 0, before;
     if (orphan) {
-        const int run = max(1, words / kThreads), w0 = tid * run;
+        marks.join<false>();
+        const uint32_t *drop = marks.mine();
+        const int run = (A.words + kThreads - 1) / kThreads, w0 = tid * run;
+        const int w1 = min(A.words, w0 + run);
         int mine = 0;
-        for (int w = w0; w < min(words, w0 + run); ++w) mine += __popc(drop[w] & ~keep[w]);
+        for (int w = w0; w < w1; ++w) mine += __popc(drop[w]);
         int cta, total;
         int at = block_scan(mine, warp_sums, &cta);
         exchange(cluster, slots, cta, &before, &total);
@@ -166,37 +301,63 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs A) 
             status |= 1;
         } else {
             int64_t to = count + before + at;
-            for (int w = w0; w < min(words, w0 + run); ++w)
-                for (uint32_t bits = drop[w] & ~keep[w]; bits; bits &= bits - 1)
-                    A.free_pages[to++] = (rank << A.shift) + w * 32 + __ffs(int(bits)) - 1;
+            for (int w = w0; w < w1; ++w)
+                for (uint32_t bits = drop[w]; bits; bits &= bits - 1)
+                    A.free_pages[to++] = (rank * A.words + w) * 32 + __ffs(int(bits)) - 1;
         }
     }
     // 3. a page for every child that shares a partly filled one with an earlier child
+    allow_dependents();
     const int per = (A.batch_out + kThreads - 1) / kThreads, r0 = tid * per;
     int need = 0;
     unsigned wants = 0;
-    for (int k = 0; k < per && r0 + k < A.batch_out; ++k) {
-        const int r = r0 + k, p = A.parents[r];
-        if (p < 0 || p >= A.batch || first[p] == r) continue;
-        const int len = A.lens[p];
-        const int64_t n = pages_of(len);
-        if (n == 0 || len % ps == 0) continue;
-        const int id = A.table[p * A.ldt + n - 1];
-        if (id < 0 || id >= A.num_pages) continue;
-        wants |= 1u << k;
-        ++need;
+    int last[kPerThread];               // the parent, its last page, the page of its own
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k)
+        last[k] = k < per && r0 + k < A.batch_out ? A.parents[r0 + k] : -1;
+    int len_of[kPerThread];
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        const int p = last[k];
+        const bool shares = p >= 0 && p < A.batch && first[p] != r0 + k;
+        len_of[k] = shares ? A.lens[p] : 0;
     }
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        const int64_t n = pages_of(len_of[k]);
+        last[k] = n > 0 && len_of[k] % ps != 0 ? A.table[last[k] * A.ldt + n - 1] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k)
+        if (last[k] >= 0 && last[k] < A.num_pages) {
+            wants |= 1u << k;
+            ++need;
+        }
     int wanted;
     int nth = block_scan(need, warp_sums, &wanted);
     cluster.sync();                     // the free list is whole
     const int64_t have = count + freed;
-    for (int k = 0; k < per && r0 + k < A.batch_out; ++k) {
-        int page = -1;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        last[k] = -1;
         if (wants >> k & 1) {
             const int64_t at = have - 1 - nth++;
-            page = at >= 0 ? __ldcg(A.free_pages + at) : -2;
-            if (at < 0) status |= 2;
-            else if (page < 0 || page >= A.num_pages) status |= 4, page = -2;
+            if (at >= 0) {
+                last[k] = __ldcg(A.free_pages + at);
+            } else {
+                status |= 2;
+                wants &= ~(1u << k);
+                last[k] = -2;
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        if (k >= per || r0 + k >= A.batch_out) break;
+        int page = last[k];
+        if (wants >> k & 1 && (page < 0 || page >= A.num_pages)) {
+            status |= 4;
+            page = -2;
         }
         fresh[r0 + k] = page;
     }
@@ -213,14 +374,9 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs A) 
         A.tokens[r] = own ? int(len % ps) : 0;
     }
     // 4. the new table
-    for (int64_t i = int64_t(rank) * kWarps + warp; i < A.batch_out * segs; i += C * kWarps) {
-        const int r = int(i / segs), p = A.parents[r];
-        if (p < 0 || p >= A.batch || fresh[r] == -2) continue;
-        const int64_t n = pages_of(A.lens[p]), j0 = (i - r * segs) * kSegment;
-        const int32_t *from = A.table + p * A.ldt;
-        int32_t *to = A.table_out + r * A.ldto;
-        for (int64_t j = j0 + lane; j < min(n, j0 + kSegment); j += 32)
-            to[j] = j == n - 1 && fresh[r] >= 0 ? fresh[r] : from[j];
+    if (!A.apart) {
+        cluster.sync();                 // the rows' lengths and pages are there
+        fork_rows(A, rank * kWarps + warp, C * kWarps);
     }
     if (rank == 0 && tid == 0)
         *A.free_count_out = int(have - min(int64_t(wanted), have));
@@ -228,6 +384,14 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs A) 
         status = __reduce_or_sync(0xffffffffu, unsigned(status));
         if (lane == 0 && status) atomicOr(reinterpret_cast<int *>(A.dev_status), status);
     }
+}
+
+constexpr int kRowThreads = 256;
+constexpr int kRowWarps = kRowThreads / 32;
+
+__global__ void __launch_bounds__(kRowThreads) pages_fork_rows_kernel(const ForkArgs A) {
+    grid_dependency_wait();
+    fork_rows(A, blockIdx.x * kRowWarps + (threadIdx.x >> 5), gridDim.x * kRowWarps);
 }
 
 struct CompactArgs {
@@ -238,47 +402,88 @@ struct CompactArgs {
     int32_t *table_out;
     int64_t ldto;
     int32_t *free_pages, *free_count_out, *src, *dst, *moves, *dev_status;
-    int shift;
+    int words, shift;         // of the pages' bits
+    bool near;
+    bool apart;               // the rows and the free list by launches of their own
 };
 
+// The new rows: warp w of `all`. Until the free list is written its place holds the
+// new ids of the pages past the first `used` ids: exactly as many entries.
+__device__ __forceinline__ void compact_rows(const CompactArgs &A, int used, int w, int all) {
+    const int64_t ps = A.page_size, room = min(A.max_pages * ps, int64_t(0x7fffffff));
+    for (Segments at(A.batch, A.max_pages, w, all); at.more(); at.next()) {
+        const int b = at.row, len = A.lens[b];
+        const int n = at.left(len < 0 || len > room ? 0 : (len + ps - 1) / ps);
+        if (n <= 0) continue;
+        const int32_t *from = A.table + b * A.ldt + at.first();
+        int32_t *to = A.table_out + b * A.ldto + at.first();
+        int id[kDeep];
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) id[k] = 32 * k < n ? from[32 * k] : -1;
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k)
+            if (id[k] >= used && id[k] < A.num_pages) id[k] = __ldcg(A.free_pages + (id[k] - used));
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k)
+            if (32 * k < n) to[32 * k] = id[k];
+    }
+}
+__device__ __forceinline__ void compact_free(const CompactArgs &A, int used, int64_t t, int64_t all) {
+    for (int64_t i = t; i < A.num_pages - used; i += all)
+        A.free_pages[i] = int(A.num_pages - 1 - i);
+}
+
+__global__ void __launch_bounds__(kRowThreads) pages_compact_rows_kernel(const CompactArgs A) {
+    grid_dependency_wait();
+    allow_dependents();
+    compact_rows(A, int(A.num_pages - __ldcg(A.free_count_out)),
+                 blockIdx.x * kRowWarps + (threadIdx.x >> 5), gridDim.x * kRowWarps);
+}
+__global__ void __launch_bounds__(kRowThreads) pages_compact_free_kernel(const CompactArgs A) {
+    grid_dependency_wait();
+    compact_free(A, int(A.num_pages - __ldcg(A.free_count_out)),
+                 int64_t(blockIdx.x) * kRowThreads + threadIdx.x, int64_t(gridDim.x) * kRowThreads);
+}
+
 __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const CompactArgs A) {
-    extern __shared__ uint32_t sm[];
-    const int words = 1 << (A.shift - 5);
-    uint32_t *held = sm;
+    extern __shared__ __align__(16) uint32_t sm[];
     __shared__ int warp_sums[32], slots[3][kMaxCluster];
     cg::cluster_group cluster = cg::this_cluster();
     const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Marks marks = {cluster, A.shift};
+    const int words = A.words;
+    const Marks marks = {cluster, sm, words, A.shift, A.near};
     const int64_t ps = A.page_size, room = min(A.max_pages * ps, int64_t(0x7fffffff));
     int status = 0;
     auto pages_of = [&](int len) {
         return len < 0 || len > room ? int64_t(0) : (len + ps - 1) / ps;
     };
-    for (int i = tid; i < words; i += kThreads) held[i] = 0;
-    cluster.sync();
-    const int64_t segs = (A.max_pages + kSegment - 1) / kSegment;
-    for (int64_t i = int64_t(rank) * kWarps + warp; i < A.batch * segs; i += C * kWarps) {
-        const int b = int(i / segs), len = A.lens[b];
+    for (int i = tid; i < (A.near ? C * words : words); i += kThreads) sm[i] = 0;
+    if (A.near) __syncthreads(); else cluster.sync();
+    for (Segments at(A.batch, A.max_pages, rank * kWarps + warp, C * kWarps); at.more(); at.next()) {
+        const int b = at.row, len = A.lens[b], over = b > 0 ? A.lens[b - 1] : 0;
         if (len < 0 || len > room) status |= 1;
-        const int64_t n = pages_of(len), j0 = (i - b * segs) * kSegment;
-        if (j0 >= n) continue;
-        const int64_t above = b > 0 ? pages_of(A.lens[b - 1]) : 0;
-        const int32_t *row = A.table + b * A.ldt;
-        for (int64_t j = j0 + lane; j < min(n, j0 + kSegment); j += 32) {
-            const int id = row[j];
-            if (id < 0 || id >= A.num_pages) status |= 4;
-            else if (!(j < above && row[j - A.ldt] == id)) marks.set(held, id);
+        const int n = at.left(pages_of(len));
+        if (n <= 0) continue;
+        const int32_t *p = A.table + b * A.ldt + at.first();
+        int id[kDeep], up[kDeep];
+        load_entries(p, n, p - A.ldt, min(n, at.left(pages_of(over))), id, up);
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            if (32 * k >= n) break;
+            if (unsigned(id[k]) >= unsigned(A.num_pages)) status |= 4;
+            else if (up[k] != id[k]) marks.mark<true>(id[k]);
         }
     }
-    cluster.sync();
+    marks.join<true>();
+    const uint32_t *held = marks.mine();
     // the pages in use, then those of them past the first `used` ids and the holes before
-    const int run = max(1, words / kThreads), w0 = tid * run, w1 = min(words, w0 + run);
+    const int run = (words + kThreads - 1) / kThreads, w0 = tid * run, w1 = min(words, w0 + run);
     int mine = 0, cta, before, used;
     for (int w = w0; w < w1; ++w) mine += __popc(held[w]);
     block_scan(mine, warp_sums, &cta);
     exchange(cluster, slots[0], cta, &before, &used);
-    const int base = rank << A.shift;
+    const int base = rank * words * 32;
     auto moving = [&](int w) {          // of word w: in use at or past `used`
         const int at = base + w * 32;
         const uint32_t past = at >= used ? ~0u : at + 32 <= used ? 0u : ~0u << (used - at);
@@ -304,25 +509,16 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const CompactAr
             A.dst[bh + ah++] = base + w * 32 + __ffs(int(bits)) - 1;
     }
     cluster.sync();                     // the lists are whole
-    for (int64_t i = int64_t(rank) * kWarps + warp; i < A.batch * segs; i += C * kWarps) {
-        const int b = int(i / segs);
-        const int64_t n = pages_of(A.lens[b]), j0 = (i - b * segs) * kSegment;
-        for (int64_t j = j0 + lane; j < min(n, j0 + kSegment); j += 32) {
-            int id = A.table[b * A.ldt + j];
-            if (id >= used && id < A.num_pages) {
-                int lo = 0, hi = total;         // src[lo] <= id < src[hi]
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (__ldcg(A.src + mid) <= id) lo = mid; else hi = mid;
-                }
-                id = __ldcg(A.dst + lo);
-            }
-            A.table_out[b * A.ldto + j] = id;
-        }
-    }
+    allow_dependents();
+    for (int i = rank * kThreads + tid; i < total; i += C * kThreads)
+        A.free_pages[__ldcg(A.src + i) - used] = __ldcg(A.dst + i);
     const int64_t spare = A.num_pages - used;
-    for (int64_t i = int64_t(rank) * kThreads + tid; i < spare; i += C * kThreads)
-        A.free_pages[i] = int(A.num_pages - 1 - i);
+    if (!A.apart) {
+        cluster.sync();                 // the moved pages' new ids are there
+        compact_rows(A, used, rank * kWarps + warp, C * kWarps);
+        cluster.sync();                 // and have been used
+        compact_free(A, used, rank * kThreads + tid, C * kThreads);
+    }
     if (rank == 0 && tid == 0) {
         *A.free_count_out = int(spare);
         *A.moves = total;
@@ -334,9 +530,10 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const CompactAr
 }
 
 // ---------------------------------------------------------------- copy
-constexpr int kCopyThreads = 256;
+constexpr int kCopyThreads = 512;
 constexpr int kFilterWords = 4096;                  // 2^17 pages, by the low bits
 constexpr int kUnroll = 8;
+constexpr int kCopyCtas = 2;                       // an SM's
 
 struct CopyArgs {
     float *k, *v;
@@ -351,7 +548,7 @@ struct CopyArgs {
 
 // WIDE: floats of a unit (4 or 1). Units of a piece: token, then head, then dim.
 template <int WIDE>
-__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const CopyArgs A) {
+__global__ void __launch_bounds__(kCopyThreads, kCopyCtas) kv_copy_kernel(const CopyArgs A) {
     // pages that are a source; a destination; a destination at least twice
     __shared__ uint32_t is_src[kFilterWords], is_dst[kFilterWords], twice[kFilterWords];
     const int tid = threadIdx.x;
@@ -376,6 +573,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const CopyArgs A)
         }
         return s != d && t > 0;
     };
+#pragma unroll 4
     for (int i = tid; i < n; i += kCopyThreads) {
         int s, d, t;
         if (!valid(i, s, d, t)) continue;
@@ -440,17 +638,27 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const CopyArgs A)
     }
 }
 
-// CTAs of the cluster and pages of a CTA's marks (a power of two of at least 32):
-// enough CTAs that a warp has few table segments and the marks fit.
+// CTAs of the cluster, so many that a warp has few table segments, and the words of a
+// slice of the pages' bits (a multiple of 4).
 struct ClusterPlan {
-    int ctas, shift;
+    int ctas, words, shift;
+    bool near;
+    size_t bytes;             // of the bits, of a CTA
 };
 ClusterPlan cluster_plan(int64_t rows, int64_t max_pages, int64_t num_pages) {
-    ClusterPlan p = {1, 5};
-    const int64_t work = rows * ((max_pages + 127) / 128) + num_pages / 4096;
+    ClusterPlan p = {1, 0, 0, true, 0};
+    const int64_t work = rows * ((max_pages + kSegment - 1) / kSegment) + num_pages / 4096;
     while (p.ctas < kMaxCluster && p.ctas * kWarps < work) p.ctas *= 2;
-    while ((int64_t(p.ctas) << kSliceShift) < num_pages) p.ctas *= 2;
-    while ((int64_t(p.ctas) << p.shift) < num_pages) ++p.shift;
+    int64_t slice = (num_pages + p.ctas * 128 - 1) / (p.ctas * 128) * 128;
+    p.near = slice * p.ctas / 8 <= kMaxBits;
+    if (!p.near) {
+        while ((int64_t(p.ctas) << kSliceShift) < num_pages) p.ctas *= 2;
+        p.shift = 7;
+        while ((int64_t(p.ctas) << p.shift) < num_pages) ++p.shift;
+        slice = int64_t(1) << p.shift;
+    }
+    p.words = int(slice / 32);
+    p.bytes = size_t(slice) / 8 * (p.near ? p.ctas : 1);
     return p;
 }
 
@@ -476,6 +684,14 @@ cudaError_t run_cluster(K kern, const Args &A, int ctas, size_t smem, cudaStream
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+// A warp a segment of a row, at most 8 CTAs an SM.
+dim3 rows_grid(int64_t rows, int64_t max_pages) {
+    const int64_t warps = rows * ((max_pages + kSegment - 1) / kSegment);
+    return dim3(unsigned(std::max<int64_t>(
+        1, std::min<int64_t>((warps + kRowWarps - 1) / kRowWarps,
+                             int64_t(sm_count_current_device()) * 8))));
+}
+
 }  // namespace
 
 cudaError_t launch_pages_fork(int64_t batch, int64_t batch_out, int64_t page_size,
@@ -488,9 +704,13 @@ cudaError_t launch_pages_fork(int64_t batch, int64_t batch_out, int64_t page_siz
     const ClusterPlan p = cluster_plan(std::max(batch, batch_out), max_pages, num_pages);
     const ForkArgs A = {int(batch), int(batch_out), page_size, num_pages, lens, parents, table,
                         max_pages, ldt, table_out, ldto, free_pages, capacity, free_count, lens_out,
-                        free_count_out, src, dst, tokens, dev_status, p.shift};
-    const size_t smem = (size_t(1) << p.shift) / 8 * 2 + 2 * kMaxBatch * 4;
-    return run_cluster(pages_fork_kernel, A, p.ctas, smem, s);
+                        free_count_out, src, dst, tokens, dev_status, p.words, p.shift, p.near,
+                        batch_out * max_pages >= kLarge};
+    const size_t smem = p.bytes + size_t(batch + std::max(batch, batch_out)) * 4;
+    const cudaError_t e = run_cluster(pages_fork_kernel, A, p.ctas, smem, s);
+    if (e != cudaSuccess || !A.apart) return e;
+    return launch_dependent(pages_fork_rows_kernel, rows_grid(batch_out, max_pages),
+                            dim3(kRowThreads), 0, s, A);
 }
 
 cudaError_t launch_pages_compact(int64_t batch, int64_t page_size, int64_t num_pages,
@@ -501,8 +721,17 @@ cudaError_t launch_pages_compact(int64_t batch, int64_t page_size, int64_t num_p
                                  cudaStream_t s) {
     const ClusterPlan p = cluster_plan(batch, max_pages, num_pages);
     const CompactArgs A = {int(batch), page_size, num_pages, lens, table, max_pages, ldt, table_out,
-                           ldto, free_pages, free_count_out, src, dst, moves, dev_status, p.shift};
-    return run_cluster(pages_compact_kernel, A, p.ctas, (size_t(1) << p.shift) / 8, s);
+                           ldto, free_pages, free_count_out, src, dst, moves, dev_status, p.words,
+                           p.shift, p.near, batch * max_pages + num_pages >= kLarge};
+    cudaError_t e = run_cluster(pages_compact_kernel, A, p.ctas, p.bytes, s);
+    if (e != cudaSuccess || !A.apart) return e;
+    e = launch_dependent(pages_compact_rows_kernel, rows_grid(batch, max_pages), dim3(kRowThreads), 0,
+                         s, A);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = std::min<int64_t>((num_pages + kRowThreads - 1) / kRowThreads,
+                                           int64_t(sm_count_current_device()) * 8);
+    return launch_dependent(pages_compact_free_kernel, dim3(unsigned(std::max<int64_t>(1, grid))),
+                            dim3(kRowThreads), 0, s, A);
 }
 
 cudaError_t launch_kv_copy(int64_t pairs, const int32_t *src, const int32_t *dst,
@@ -514,12 +743,14 @@ cudaError_t launch_kv_copy(int64_t pairs, const int32_t *src, const int32_t *dst
     CopyArgs A = {c.k, c.v, c.num_pages, int(c.page_size), int(c.kv_heads), int(c.head_dim),
                   c.page_stride, c.token_stride, c.head_stride, src, dst, tokens, count, int(pairs),
                   0, 0, dev_status};
-    // a piece: tokens whose units all have one round of the threads' loads, or one
+    // a piece: tokens whose units all have one round of the threads' loads, fewer where
+    // the pieces would be too few for the GPU, or one
     const int64_t units = c.kv_heads * c.head_dim / (vec ? 4 : 1);
-    const int64_t fit = std::max<int64_t>(1, kCopyThreads * kUnroll / units);
-    A.seg_tokens = int(std::min(fit, c.page_size));
+    const int64_t ctas = int64_t(sm_count_current_device()) * kCopyCtas;
+    const int64_t fit = std::min(kCopyThreads * kUnroll / units, pairs * c.page_size / ctas);
+    A.seg_tokens = int(std::max<int64_t>(1, std::min(fit, c.page_size)));
     A.segs = int((c.page_size + A.seg_tokens - 1) / A.seg_tokens);
-    const int64_t grid = std::min<int64_t>(pairs * A.segs, int64_t(sm_count_current_device()) * 4);
+    const int64_t grid = std::min<int64_t>(pairs * A.segs, ctas);
     if (vec) kv_copy_kernel<4><<<unsigned(grid), kCopyThreads, 0, s>>>(A);
     else kv_copy_kernel<1><<<unsigned(grid), kCopyThreads, 0, s>>>(A);
     return cudaGetLastError();

@@ -896,7 +896,8 @@ det_status detbeam_select_f32(const det_profile_v1 *prof, int64_t requests, cons
  * are not); 2 where the free list has run out, 4 for a page outside
  * 0..num_pages - 1 (left as it is in a table; in the free list as if it had run
  * out): a row that needs a page then is left empty.
- * The outputs must not overlap the inputs, but for free_pages. One launch.
+ * The outputs must not overlap the inputs, but for free_pages. One launch, for large
+ * tables two.
  * Errors: DET_ERR_INVALID_ARG as detpages_extend (batch and batch_out 0..8192),
  * num_pages outside 0..2^23, or lens_out, table_out or free_count_out equal to their
  * input. */
@@ -917,7 +918,8 @@ det_status detpages_fork(const det_profile_v1 *prof, int64_t batch, int64_t batc
  * down to U, so the lowest are taken first, and *free_count_out their number. Every
  * page in use must be in a row: others count as free.
  * *dev_status (may be NULL): 1 for a length outside the table's row (the row counts
- * as empty), 4 for a page outside 0..num_pages - 1 (left as it is). One launch.
+ * as empty), 4 for a page outside 0..num_pages - 1 (left as it is). One launch, for large
+ * tables or caches three.
  * Errors: DET_ERR_INVALID_ARG as detpages_extend, num_pages outside 0..2^23,
  * max_moves < num_pages / 2, or table_out == table with another stride. */
 det_status detpages_compact(const det_profile_v1 *prof, int64_t batch, int64_t page_size,
