@@ -1383,6 +1383,8 @@ DET_API det_status det_watchdog_status(int32_t *code, int clear) {
     if (e == cudaSuccess) e = logprob_watchdog(&c7, clear);
     unsigned int c8 = 0;
     if (e == cudaSuccess) e = shared_decode_watchdog(&c8, clear);
-    *code = int32_t(c | c2 | c3 | c5 | c6 | c7 | c8);
+    unsigned int c9 = 0;
+    if (e == cudaSuccess) e = few_decode_watchdog(&c9, clear);
+    *code = int32_t(c | c2 | c3 | c5 | c6 | c7 | c8 | c9);
     return from_cuda(e);
 }

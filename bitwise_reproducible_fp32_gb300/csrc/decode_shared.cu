@@ -17,10 +17,14 @@
 // the register tile: up to 16 rows x 8 tokens (or dimensions) a thread. Scores lie
 // in octets of 8 tokens, a group's rows side by side: [octet][row][8], so a warp's
 // stores of 4 rows x 8 tokens and its loads of exps are whole 128-byte lines.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <type_traits>
 
-#include "decode.cuh"
+#include "decode_shared.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace det {
 
@@ -29,115 +33,95 @@ __device__ unsigned int g_shared_watchdog;
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanRows = 1024;                    // requests looked through at once
-constexpr unsigned kWatchdogDecode = 32u;          // det_watchdog_status bit 5
+constexpr int kPlanCtas = 8;                       // of a cluster
 constexpr int kScoreStage = kKChunk * 128;         // a chunk's tokens x 32 dimensions
 constexpr int kScoreStages = 2;
 constexpr int kPvTokens = 16;                      // of a step of P V
 constexpr int kPvStages = 3;
-constexpr size_t kMaxSmem = 112 * 1024;            // of a CTA
-
-struct SharedArgs {
-    int batch, group, groups, heads, kv_heads, per_kv, d;
-    int64_t rows;             // of a whole group and a key-value head: group * per_kv
-    const float *q;
-    int64_t ldq;
-    const float *k, *v;
-    int64_t num_pages;
-    unsigned page_size;
-    int page_shift;           // log2(page_size), or -1
-    int64_t page_stride, token_stride, head_stride;
-    const int32_t *table;
-    int64_t ldt;
-    const int32_t *kv_lens;
-    int64_t max_len;
-    float scale;
-    int wide;                 // 16-byte loads of the cache where TMA cannot be used
-    int box;                  // tokens of a TMA box
-    int row_blocks, dim_tiles;
-    int *chunks, *lead;       // of each group: shared chunks, a request in order
-    int *own;                 // of each request: its own chunks, 0 if it is not in order
-    unsigned *top;            // of each row (b, h): the maximum of its scores, by max_key
-    float *inv;               // 1 / S
-    float *x;                 // ((group * kv_heads + head) * octets + octet) * rows + row) * 8
-    int64_t octets;
-    float *part;              // (row * ldpart + chunk) * d
-    int64_t ldpart;
-    float *out;
-    int64_t ldo;
-    int32_t *dev_status;
-};
-
-__device__ __forceinline__ unsigned page_of(const SharedArgs &A, int t) {
-    return A.page_shift >= 0 ? unsigned(t) >> A.page_shift : unsigned(t) / A.page_size;
-}
 
 // ---------------------------------------------------------------- plan
-// A CTA a group. Every request keeps a token of its own, so a chunk is shared where
-// it ends before the shortest's last token. A request whose own pages are not all in
-// order has no chunks and no part in the rest.
+// A cluster of up to 8 CTAs a group. Every request keeps a token of its own, so a
+// chunk is shared where it ends before the shortest's last token. A request whose own
+// pages are not all in order has no chunks and no part in the rest. What bounds it is
+// the latency of the lengths, then the shared pages, then the own ones: 32 columns of
+// the table are a warp's, and where there are few, the requests are dealt out too.
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedArgs A) {
-    __shared__ int s_least, s_lead, s_live, s_bad, who[kPlanRows];
-    const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ int s_least, s_lead, s_live, s_bad, who[kPlanRows], found[kPlanCtas];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+    const int g = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int w0 = rank * (kPlanThreads / 32) + warp, all = C * (kPlanThreads / 32);
     const int b0 = g * A.group, b1 = min(A.batch, b0 + A.group);
     auto in_order = [&](int n) { return n > 0 && n <= A.max_len; };
+    if (C > 1) cluster.barrier_arrive();    // waited for before the first remote access
+    grid_dependency_wait();
+    allow_dependents();
     if (tid == 0) {
         s_least = s_lead = s_bad = INT32_MAX;
         s_live = 0;
     }
     __syncthreads();
-    int live = 0, status = 0;
+    int live = 0, status = 0, least = INT32_MAX, first_live = INT32_MAX;
     for (int b = b0 + tid; b < b1; b += kPlanThreads) {
         const int n = A.kv_lens[b];
         if (!in_order(n)) {
             if (n != 0) status = 1;
             continue;
         }
-        atomicMin(&s_least, n);
-        atomicMin(&s_lead, b);
+        least = min(least, n);
+        first_live = min(first_live, b);
         ++live;
     }
-    if (live) atomicAdd(&s_live, live);
-    for (int64_t i = int64_t(b0) * A.heads + tid; i < int64_t(b1) * A.heads; i += kPlanThreads)
+    if (live) {
+        atomicMin(&s_least, least);
+        atomicMin(&s_lead, first_live);
+        atomicAdd(&s_live, live);
+    }
+    for (int64_t i = int64_t(b0) * A.heads + rank * kPlanThreads + tid; i < int64_t(b1) * A.heads;
+         i += C * kPlanThreads)
         A.top[i] = 0;
     __syncthreads();
+    if (C > 1) cluster.barrier_wait();
     int chunks = 0;
     if (s_live > 1) {
         chunks = (s_least - 1) / kKChunk;
         const int64_t ps = A.page_size;
         const int pages = int((int64_t(chunks) * kKChunk + ps - 1) / ps);
         const int32_t *first = A.table + s_lead * A.ldt;
-        // 256 pages at a time, the requests dealt out to four
-        const int col = tid & 255, part = tid >> 8;
+        const int cols = (pages + 31) / 32;
         for (int r0 = b0; r0 < b1; r0 += kPlanRows) {
             const int rows = min(kPlanRows, b1 - r0);
             __syncthreads();
             if (tid < rows) who[tid] = in_order(A.kv_lens[r0 + tid]) ? r0 + tid : s_lead;
             __syncthreads();
-            for (int j0 = 0; j0 < pages; j0 += 256) {
-                const int j = j0 + col;
-                bool bad = false;
-                if (j < pages) {
-                    const int id = first[j];
-                    bad = id < 0 || id >= A.num_pages;
+            const int parts = cols ? max(1, min(rows, all / cols)) : 0;
+            for (int i = w0; i < cols * parts; i += all) {
+                const int part = i / cols, j = (i - part * cols) * 32 + lane;
+                if (j >= pages) continue;
+                const int id = first[j];
+                bool bad = id < 0 || id >= A.num_pages;
 #pragma unroll 8
-                    for (int r = part; r < rows; r += 4) bad |= A.table[who[r] * A.ldt + j] != id;
-                }
+                for (int r = part; r < rows; r += parts) bad |= A.table[who[r] * A.ldt + j] != id;
                 if (bad) atomicMin(&s_bad, j);
-                if (__syncthreads_or(bad)) break;
             }
         }
-        if (s_bad != INT32_MAX) chunks = min(chunks, int(s_bad * ps / kKChunk));
+        __syncthreads();
+        int bad = s_bad;
+        if (C > 1) {
+            if (tid < C) *cluster.map_shared_rank(found + rank, tid) = bad;
+            cluster.sync();
+            for (int r = 0; r < C; ++r) bad = min(bad, found[r]);
+        }
+        if (bad != INT32_MAX) chunks = min(chunks, int(bad * ps / kKChunk));
     }
-    if (tid == 0) {
+    if (rank == 0 && tid == 0) {
         A.chunks[g] = chunks;
         A.lead[g] = s_live ? s_lead : b0;
     }
     // the requests' own pages
-    for (int b = b0 + warp; b < b1; b += kPlanThreads / 32) {
+    for (int b = b0 + w0; b < b1; b += all) {
         const int n = A.kv_lens[b];
         int own = 0;
         if (in_order(n)) {
@@ -160,126 +144,14 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
     }
 }
 
-// ---------------------------------------------------------------- work
-// The items of a kernel: for each unit (OWN: a request with its own chunks; else a
-// group with the shared ones) `mul` runs (of heads and blocks of rows or dimensions)
-// of its chunks, the chunk fastest.
-struct Item {
-    int u, run, c, n;         // n: the unit's chunks
-};
-template <bool OWN>
-__device__ __forceinline__ int units(const SharedArgs &A) { return OWN ? A.batch : A.groups; }
-template <bool OWN>
-__device__ __forceinline__ int chunks_of(const SharedArgs &A, int u) {
-    return OWN ? A.own[u] : A.chunks[u];
-}
-// The item's first token, how many it has, and the table row of its pages.
-template <bool OWN>
-__device__ __forceinline__ int first_token(const SharedArgs &A, const Item &it) {
-    return (it.c + (OWN ? A.chunks[it.u / A.group] : 0)) * kKChunk;
-}
-template <bool OWN>
-__device__ __forceinline__ int tokens_from(const SharedArgs &A, const Item &it, int t0) {
-    return OWN ? min(kKChunk, A.kv_lens[it.u] - t0) : kKChunk;
-}
-template <bool OWN>
-__device__ __forceinline__ const int32_t *pages_of(const SharedArgs &A, const Item &it) {
-    return A.table + (OWN ? it.u : A.lead[it.u]) * A.ldt;
-}
-// Row r of the unit's rows of a key-value head: its place among its group's; the row
-// (b, h) of a place, -1 where there is none or its request is not in order.
-template <bool OWN>
-__device__ __forceinline__ int place_of(const SharedArgs &A, int u, int r) {
-    return OWN ? u % A.group * A.per_kv + r : r;
-}
-template <bool OWN>
-__device__ __forceinline__ int group_of(const SharedArgs &A, int u) {
-    return OWN ? u / A.group : u;
-}
-template <bool OWN>
-__device__ __forceinline__ int rows_of(const SharedArgs &A) {
-    return OWN ? A.per_kv : int(A.rows);
-}
-__device__ __forceinline__ int row_at(const SharedArgs &A, int g, int kv, int place) {
-    const int m = place / A.per_kv, b = g * A.group + m;
-    if (m >= A.group || b >= A.batch || A.own[b] == 0) return -1;
-    return b * A.heads + kv * A.per_kv + (place - m * A.per_kv);
-}
-
-// A worker's share [lo, hi) of the items is a run of them, all as long but for one;
-// the longer ones go to the first workers. All threads of the CTA call; the CTA has
-// the workers first, first + step, ... of `all`.
-struct Share {
-    int64_t items;
-    Item at;
-};
-template <bool OWN, int WORKERS>
-__device__ __forceinline__ void shares(const SharedArgs &A, int mul, int first, int step, int all,
-                                       Share *out) {
-    __shared__ int64_t warp_sums[kWarps];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = units<OWN>(A);
-    const int per = (n + kThreads - 1) / kThreads;
-    const int u0 = min(n, tid * per), u1 = min(n, u0 + per);
-    int64_t sum = 0;
-    for (int u = u0; u < u1; ++u) sum += chunks_of<OWN>(A, u);
-    int64_t in = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off *= 2) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, in, off);
-        if (lane >= off) in += o;
-    }
-    if (lane == 31) warp_sums[warp] = in;
-    __syncthreads();
-    int64_t before = in - sum, total = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        before += w < warp ? warp_sums[w] : 0;
-        total += warp_sums[w];
-    }
-    total *= mul;
-    const int64_t base = total / all, rem = total % all;
-    for (int w = 0; w < WORKERS; ++w) {
-        const int64_t i = first + int64_t(w) * step, lo = i * base + min(i, rem);
-        if (tid == 0) out[w].items = base + (i < rem);
-        if (base + (i < rem) > 0 && before * mul <= lo && lo < (before + sum) * mul) {
-            int64_t at = before;
-            int u = u0;
-            while ((at + chunks_of<OWN>(A, u)) * mul <= lo) at += chunks_of<OWN>(A, u++);
-            const int c = chunks_of<OWN>(A, u);
-            const int64_t k = lo - at * mul;
-            out[w].at = {u, int(k / c), int(k % c), c};
-        }
-    }
-    __syncthreads();
-}
-template <bool OWN>
-__device__ __forceinline__ void advance(const SharedArgs &A, int mul, Item &it) {
-    if (++it.c < it.n) return;
-    it.c = 0;
-    if (++it.run < mul) return;
-    it.run = 0;
-    do {
-        ++it.u;
-    } while (it.u < units<OWN>(A) && (it.n = chunks_of<OWN>(A, it.u)) == 0);
-}
-
-// A token's offset in the cache (its page is in order: the plan has seen it).
-__device__ __forceinline__ int64_t offset_of(const SharedArgs &A, const int32_t *pages, int t) {
-    const unsigned p = page_of(A, t);
-    return pages[p] * A.page_stride + int64_t(unsigned(t) - p * A.page_size) * A.token_stride;
-}
-
 // RT consecutive floats of shared memory as pairs.
 template <int RT>
 __device__ __forceinline__ void load_pairs(const float *p, f32x2 (&v)[RT / 2]) {
-    if constexpr (RT == 2) {
-        v[0] = *reinterpret_cast<const f32x2 *>(p);
-    } else {
 #pragma unroll
-        for (int i = 0; i < RT / 4; ++i) {
-            const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(p + 4 * i);
-            v[2 * i] = w.x;
-            v[2 * i + 1] = w.y;
-        }
+    for (int i = 0; i < RT / 4; ++i) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(p + 4 * i);
+        v[2 * i] = w.x;
+        v[2 * i + 1] = w.y;
     }
 }
 __device__ __forceinline__ float part_of(const float4 &v, int i) {
@@ -306,6 +178,8 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
         for (int i = 0; i < kScoreStages; ++i) mbar_init(smem_u32(full + i), 1);
         fence_mbar_init();
     }
+    grid_dependency_wait();
+    allow_dependents();
     shares<OWN, 1>(A, mul, blockIdx.x, 1, gridDim.x, &share);
     const int64_t items = share.items;
     if (items <= 0) return;
@@ -388,13 +262,11 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
             const float *q = A.q + b * A.ldq + int64_t(row - b * A.heads) * d;
             for (int j = tid / R; j < d; j += kThreads / R) qs[j * R + p] = row >= 0 ? q[j] : 0.0f;
         }
-        f32x2 acc[RT >= 2 ? RT / 2 : 1][8];
-        float one[RT == 1 ? 8 : 1];
+        f32x2 acc[RT / 2][8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
 #pragma unroll
             for (int r = 0; r < RT / 2; ++r) acc[r][c] = 0;
-            if (RT == 1) one[c] = 0.0f;
         }
         for (int sl = 0; sl < nsl; ++sl) {
             if constexpr (TMA) {
@@ -416,20 +288,13 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
                 for (int kk = 0; kk < 4; ++kk) {
                     if (kk >= live4) break;
                     const float *p = qp + (4 * g4 + kk) * R;
-                    if constexpr (RT >= 2) {
-                        f32x2 a[RT / 2];
-                        load_pairs<RT>(p, a);
+                    f32x2 a[RT / 2];
+                    load_pairs<RT>(p, a);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const f32x2 kc = splat2(part_of(k[c], kk));
+                    for (int c = 0; c < 8; ++c) {
+                        const f32x2 kc = splat2(part_of(k[c], kk));
 #pragma unroll
-                            for (int r = 0; r < RT / 2; ++r) acc[r][c] = fma2(a[r], kc, acc[r][c]);
-                        }
-                    } else {
-                        const float a = *p;
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            one[c] = __fmaf_rn(a, part_of(k[c], kk), one[c]);
+                        for (int r = 0; r < RT / 2; ++r) acc[r][c] = fma2(a[r], kc, acc[r][c]);
                     }
                 }
             };
@@ -462,12 +327,8 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     float s, other;
-                    if constexpr (RT == 1) {
-                        s = one[c];
-                    } else {
-                        unpack2(acc[r / 2][c], s, other);
-                        if (r & 1) s = other;
-                    }
+                    unpack2(acc[r / 2][c], s, other);
+                    if (r & 1) s = other;
                     const float v = __fmul_rn(s, A.scale);
                     const bool here = !OWN || 64 * warp + 8 * c + tl < live;
                     if (row >= 0 && here) x[c * A.rows * 8 + r * 32] = v;
@@ -503,6 +364,8 @@ __global__ void __launch_bounds__(kSumThreads) shared_sums_kernel(const SharedAr
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 3, place = blockIdx.x * kSumRows + r;
     const int g = blockIdx.y / A.kv_heads, kv = blockIdx.y % A.kv_heads;
+    grid_dependency_wait();
+    allow_dependents();
     const int row = place < A.rows ? row_at(A, g, kv, place) : -1;
     const int n = row >= 0 ? A.kv_lens[row / A.heads] : 0;
     const float m = row >= 0 ? max_of_key(A.top[row]) : 0.0f;
@@ -576,6 +439,8 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
         for (int i = 0; i < kWarps * kPvStages; ++i) mbar_init(smem_u32(&full[0][i]), 1);
         fence_mbar_init();
     }
+    grid_dependency_wait();
+    allow_dependents();
     shares<OWN, kWarps>(A, mul, blockIdx.x, gridDim.x, gridDim.x * kWarps, share);
     const int64_t items = share[warp].items;
     if (items <= 0) return;
@@ -834,6 +699,8 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
 constexpr int kJoinDeep = 32;
 __global__ void __launch_bounds__(kThreads) shared_join_kernel(const SharedArgs A) {
     const int b = blockIdx.y, i = blockIdx.x * kThreads + threadIdx.x;
+    grid_dependency_wait();
+    allow_dependents();
     if (i >= A.heads * A.d) return;
     const int n = A.kv_lens[b], h = i / A.d;
     const int chunks = A.own[b] ? (n + kKChunk - 1) / kKChunk : 0;
@@ -854,9 +721,9 @@ __global__ void __launch_bounds__(kThreads) shared_join_kernel(const SharedArgs 
 // ---------------------------------------------------------------- host
 constexpr size_t kSliceBytes = size_t(1) << 30;     // scores and partials of a round of heads
 
-// Rows a thread takes of a unit's rows.
+// Rows a thread takes of a unit's rows, more than kFewRows.
 int rows_a_thread(int64_t rows, int64_t head_dim) {
-    return rows <= 4 ? 1 : rows <= 8 ? 2 : rows <= 16 ? 4 : rows <= 32 || head_dim > 192 ? 8 : 16;
+    return rows <= 16 ? 4 : rows <= 32 || head_dim > 192 ? 8 : 16;
 }
 
 struct SharedPlan {
@@ -899,8 +766,28 @@ cudaError_t run(K kern, int64_t grid, size_t smem, cudaStream_t s, const SharedA
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxSmem));
     if (e != cudaSuccess) return e;
-    kern<<<unsigned(std::max<int64_t>(1, grid)), kThreads, smem, s>>>(A, map);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(unsigned(std::max<int64_t>(1, grid))), dim3(kThreads), smem,
+                            s, A, map);
+}
+
+cudaError_t run_plan(const SharedArgs &A, int64_t max_pages, cudaStream_t s) {
+    // CTAs a group: while a thread looks at many entries and SMs are idle
+    int ctas = 1;
+    while (ctas < kPlanCtas && A.groups * 2 * ctas <= sm_count_current_device() &&
+           A.group * max_pages > int64_t(4) * kPlanThreads * ctas)
+        ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(A.groups * ctas));
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(ctas);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_plan_kernel, A);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 // most: the chunks of all units, at most.
@@ -919,8 +806,6 @@ template <bool OWN>
 cudaError_t scores(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
     const int64_t rows = OWN ? A.per_kv : A.rows;
     switch (rows_a_thread(rows, A.d)) {
-        case 1: return run_scores<1, OWN>(A, map, rows, most, s);
-        case 2: return run_scores<2, OWN>(A, map, rows, most, s);
         case 4: return run_scores<4, OWN>(A, map, rows, most, s);
         case 8: return run_scores<8, OWN>(A, map, rows, most, s);
         default: return run_scores<16, OWN>(A, map, rows, most, s);
@@ -945,8 +830,6 @@ template <int DH, bool OWN>
 cudaError_t partials(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
     const int64_t rows = OWN ? A.per_kv : A.rows;
     switch (rows_a_thread(rows, 0)) {
-        case 1: return run_partials<1, DH, OWN>(A, map, rows, most, s);
-        case 2: return run_partials<2, DH, OWN>(A, map, rows, most, s);
         case 4: return run_partials<4, DH, OWN>(A, map, rows, most, s);
         case 8: return run_partials<8, DH, OWN>(A, map, rows, most, s);
         default: return run_partials<16, DH, OWN>(A, map, rows, most, s);
@@ -1009,6 +892,7 @@ cudaError_t launch_shared_decode(int64_t batch, int64_t group, int heads, const 
     A.wide = vec && d % 4 == 0;
     const bool boxes = c.page_size == 8 || c.page_size == 16 || c.page_size == 32 ||
                        c.page_size % 64 == 0;
+    const bool few = A.rows <= kFewRows, few_own = A.per_kv <= kFewRows;
     const int64_t most = p.groups * p.ldpart, most_own = batch * p.ldpart;
     for (int64_t g0 = 0; g0 < c.kv_heads; g0 += p.kv) {
         A.kv_heads = int(std::min(p.kv, c.kv_heads - g0));
@@ -1017,7 +901,7 @@ cudaError_t launch_shared_decode(int64_t batch, int64_t group, int heads, const 
         A.v = c.v + g0 * c.head_stride;
         A.q = q + g0 * A.per_kv * d;
         A.out = out + g0 * A.per_kv * d;
-        CUtensorMap kmap = {}, vmap = {};
+        CUtensorMap kmap = {}, vmap = {}, vmap_few = {};
         const int kbox = int(std::min<int64_t>(c.page_size, 64));
         const int vbox = int(std::min<int64_t>(c.page_size, kPvTokens));
         bool tma = false;
@@ -1025,29 +909,43 @@ cudaError_t launch_shared_decode(int64_t batch, int64_t group, int heads, const 
             const int64_t extent[4] = {d, A.kv_heads, c.page_size, c.num_pages};
             const int64_t stride[3] = {c.head_stride, c.token_stride, c.page_stride};
             tma = make_tensor_map_4d(&kmap, A.k, extent, stride, {32, 1, uint32_t(kbox), 1}) &&
-                  make_tensor_map_4d(&vmap, A.v, extent, stride, {32, 1, uint32_t(vbox), 1});
+                  make_tensor_map_4d(&vmap, A.v, extent, stride, {32, 1, uint32_t(vbox), 1}) &&
+                  make_tensor_map_4d(&vmap_few, A.v, extent, stride, {32, 1, uint32_t(kbox), 1});
         }
-        shared_plan_kernel<<<unsigned(p.groups), kPlanThreads, 0, s>>>(A);
-        cudaError_t e = cudaGetLastError();
+        cudaError_t e = run_plan(A, max_pages, s);
         A.box = kbox;
-        if (e == cudaSuccess) e = scores<false>(A, tma ? &kmap : nullptr, most, s);
-        if (e == cudaSuccess) e = scores<true>(A, tma ? &kmap : nullptr, most_own, s);
-        if (e == cudaSuccess) {
-            shared_sums_kernel<<<dim3(unsigned((A.rows + kSumRows - 1) / kSumRows),
-                                      unsigned(p.groups * A.kv_heads)),
-                                 kSumThreads, 0, s>>>(A);
-            e = cudaGetLastError();
-        }
-        A.box = vbox;
-        const CUtensorMap *map = tma ? &vmap : nullptr;
+        const CUtensorMap *map = tma ? &kmap : nullptr;
         if (e == cudaSuccess)
-            e = d <= 32 ? partials<1, false>(A, map, most, s) : partials<2, false>(A, map, most, s);
-        if (e == cudaSuccess) e = partials<1, true>(A, map, most_own, s);
+            e = few ? launch_few_scores(false, A, map, most, s) : scores<false>(A, map, most, s);
+        if (e == cudaSuccess)
+            e = few_own ? launch_few_scores(true, A, map, most_own, s)
+                        : scores<true>(A, map, most_own, s);
         if (e == cudaSuccess) {
-            shared_join_kernel<<<dim3(unsigned((A.heads * d + kThreads - 1) / kThreads),
+            e = launch_dependent(shared_sums_kernel,
+                                 dim3(unsigned((A.rows + kSumRows - 1) / kSumRows),
+                                      unsigned(p.groups * A.kv_heads)),
+                                 dim3(kSumThreads), 0, s, A);
+        }
+        auto values = [&](bool of_few) {
+            A.box = of_few ? kbox : vbox;
+            return !tma ? nullptr : of_few ? &vmap_few : &vmap;
+        };
+        if (e == cudaSuccess) {
+            map = values(few);
+            e = few       ? launch_few_partials(false, A, map, most, s)
+                : d <= 32 ? partials<1, false>(A, map, most, s)
+                          : partials<2, false>(A, map, most, s);
+        }
+        if (e == cudaSuccess) {
+            map = values(few_own);
+            e = few_own ? launch_few_partials(true, A, map, most_own, s)
+                        : partials<1, true>(A, map, most_own, s);
+        }
+        if (e == cudaSuccess) {
+            e = launch_dependent(shared_join_kernel,
+                                 dim3(unsigned((A.heads * d + kThreads - 1) / kThreads),
                                       unsigned(batch)),
-                                 kThreads, 0, s>>>(A);
-            e = cudaGetLastError();
+                                 dim3(kThreads), 0, s, A);
         }
         if (e != cudaSuccess) return e;
     }

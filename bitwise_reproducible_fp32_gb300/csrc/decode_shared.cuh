@@ -1,0 +1,182 @@
+// decode_shared.cuh -- what the kernels of decode attention for requests that share a
+// prefix have in common (decode_shared.cu: the plan, and units of many rows;
+// decode_few.cu: units of up to 8 rows).
+#pragma once
+
+#include "decode.cuh"
+
+namespace det {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr unsigned kWatchdogDecode = 32u;          // det_watchdog_status bit 5
+constexpr size_t kMaxSmem = 112 * 1024;            // of a CTA
+
+struct SharedArgs {
+    int batch, group, groups, heads, kv_heads, per_kv, d;
+    int64_t rows;             // of a whole group and a key-value head: group * per_kv
+    const float *q;
+    int64_t ldq;
+    const float *k, *v;
+    int64_t num_pages;
+    unsigned page_size;
+    int page_shift;           // log2(page_size), or -1
+    int64_t page_stride, token_stride, head_stride;
+    const int32_t *table;
+    int64_t ldt;
+    const int32_t *kv_lens;
+    int64_t max_len;
+    float scale;
+    int wide;                 // 16-byte loads of the cache where TMA cannot be used
+    int box;                  // tokens of a TMA box
+    int row_blocks, dim_tiles;
+    int *chunks, *lead;       // of each group: shared chunks, a request in order
+    int *own;                 // of each request: its own chunks, 0 if it is not in order
+    unsigned *top;            // of each row (b, h): the maximum of its scores, by max_key
+    float *inv;               // 1 / S
+    float *x;                 // ((group * kv_heads + head) * octets + octet) * rows + row) * 8
+    int64_t octets;
+    float *part;              // (row * ldpart + chunk) * d
+    int64_t ldpart;
+    float *out;
+    int64_t ldo;
+    int32_t *dev_status;
+};
+
+namespace {
+
+__device__ __forceinline__ unsigned page_of(const SharedArgs &A, int t) {
+    return A.page_shift >= 0 ? unsigned(t) >> A.page_shift : unsigned(t) / A.page_size;
+}
+
+// ---------------------------------------------------------------- work
+// The items of a kernel: for each unit (a group with the shared chunks, or a request
+// with its own chunks; or either with tiles of kTile tokens of them) `mul` runs (of heads
+// and blocks of rows or dimensions) of its chunks or tiles, these fastest.
+enum Cut { kShared, kOwn, kSharedTiles, kOwnTiles };
+template <int CUT>
+constexpr bool kIsOwn = (CUT & 1) != 0;
+template <int CUT>
+constexpr bool kInTiles = (CUT & 2) != 0;
+constexpr int kTile = 64;
+struct Item {
+    int u, run, c, n;         // n: the unit's chunks or tiles
+};
+template <int CUT>
+__device__ __forceinline__ int units(const SharedArgs &A) { return kIsOwn<CUT> ? A.batch : A.groups; }
+template <int CUT>
+__device__ __forceinline__ int chunks_of(const SharedArgs &A, int u) {
+    const int n = kIsOwn<CUT> ? A.own[u] : A.chunks[u];
+    if (!kInTiles<CUT> || n == 0) return n;
+    if (!kIsOwn<CUT>) return n * (kKChunk / kTile);
+    return (A.kv_lens[u] - A.chunks[u / A.group] * kKChunk + kTile - 1) / kTile;
+}
+// The item's first token, how many it has, and the table row of its pages.
+template <int CUT>
+__device__ __forceinline__ int first_token(const SharedArgs &A, const Item &it) {
+    return it.c * (kInTiles<CUT> ? kTile : kKChunk) +
+           (kIsOwn<CUT> ? A.chunks[it.u / A.group] * kKChunk : 0);
+}
+template <int CUT>
+__device__ __forceinline__ int tokens_from(const SharedArgs &A, const Item &it, int t0) {
+    const int most = kInTiles<CUT> ? kTile : kKChunk;
+    return kIsOwn<CUT> ? min(most, A.kv_lens[it.u] - t0) : most;
+}
+template <int CUT>
+__device__ __forceinline__ const int32_t *pages_of(const SharedArgs &A, const Item &it) {
+    return A.table + (kIsOwn<CUT> ? it.u : A.lead[it.u]) * A.ldt;
+}
+// Row r of the unit's rows of a key-value head: its place among its group's; the row
+// (b, h) of a place, -1 where there is none or its request is not in order.
+template <int CUT>
+__device__ __forceinline__ int place_of(const SharedArgs &A, int u, int r) {
+    return kIsOwn<CUT> ? u % A.group * A.per_kv + r : r;
+}
+template <int CUT>
+__device__ __forceinline__ int group_of(const SharedArgs &A, int u) {
+    return kIsOwn<CUT> ? u / A.group : u;
+}
+template <int CUT>
+__device__ __forceinline__ int rows_of(const SharedArgs &A) {
+    return kIsOwn<CUT> ? A.per_kv : int(A.rows);
+}
+__device__ __forceinline__ int row_at(const SharedArgs &A, int g, int kv, int place) {
+    const int m = place / A.per_kv, b = g * A.group + m;
+    if (m >= A.group || b >= A.batch || A.own[b] == 0) return -1;
+    return b * A.heads + kv * A.per_kv + (place - m * A.per_kv);
+}
+
+// A worker's share [lo, hi) of the items is a run of them, all as long but for one;
+// the longer ones go to the first workers. All threads of the CTA call; the CTA has
+// the workers first, first + step, ... of `all`.
+struct Share {
+    int64_t items;
+    Item at;
+};
+template <int CUT, int WORKERS>
+__device__ __forceinline__ void shares(const SharedArgs &A, int mul, int first, int step, int all,
+                                       Share *out) {
+    __shared__ int64_t warp_sums[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = units<CUT>(A);
+    const int per = (n + kThreads - 1) / kThreads;
+    const int u0 = min(n, tid * per), u1 = min(n, u0 + per);
+    int64_t sum = 0;
+    for (int u = u0; u < u1; ++u) sum += chunks_of<CUT>(A, u);
+    int64_t in = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off *= 2) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, in, off);
+        if (lane >= off) in += o;
+    }
+    if (lane == 31) warp_sums[warp] = in;
+    __syncthreads();
+    int64_t before = in - sum, total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        before += w < warp ? warp_sums[w] : 0;
+        total += warp_sums[w];
+    }
+    total *= mul;
+    const int64_t base = total / all, rem = total % all;
+    for (int w = 0; w < WORKERS; ++w) {
+        const int64_t i = first + int64_t(w) * step, lo = i * base + min(i, rem);
+        if (tid == 0) out[w].items = base + (i < rem);
+        if (base + (i < rem) > 0 && before * mul <= lo && lo < (before + sum) * mul) {
+            int64_t at = before;
+            int u = u0;
+            while ((at + chunks_of<CUT>(A, u)) * mul <= lo) at += chunks_of<CUT>(A, u++);
+            const int c = chunks_of<CUT>(A, u);
+            const int64_t k = lo - at * mul;
+            out[w].at = {u, int(k / c), int(k % c), c};
+        }
+    }
+    __syncthreads();
+}
+template <int CUT>
+__device__ __forceinline__ void advance(const SharedArgs &A, int mul, Item &it) {
+    if (++it.c < it.n) return;
+    it.c = 0;
+    if (++it.run < mul) return;
+    it.run = 0;
+    do {
+        ++it.u;
+    } while (it.u < units<CUT>(A) && (it.n = chunks_of<CUT>(A, it.u)) == 0);
+}
+
+// A token's offset in the cache (its page is in order: the plan has seen it).
+__device__ __forceinline__ int64_t offset_of(const SharedArgs &A, const int32_t *pages, int t) {
+    const unsigned p = page_of(A, t);
+    return pages[p] * A.page_stride + int64_t(unsigned(t) - p * A.page_size) * A.token_stride;
+}
+
+}  // namespace
+
+// Units of at most kFewRows rows a key-value head: scores and their maxima; partials of
+// the chunks. map: keys or values with boxes of A.box tokens (nullptr: TMA cannot be
+// used); most: the chunks of all units, at most.
+constexpr int kFewRows = 8;
+cudaError_t launch_few_scores(bool own, const SharedArgs &A, const CUtensorMap *map, int64_t most,
+                              cudaStream_t s);
+cudaError_t launch_few_partials(bool own, const SharedArgs &A, const CUtensorMap *map, int64_t most,
+                                cudaStream_t s);
+
+}  // namespace det
