@@ -39,7 +39,6 @@ constexpr int kPlanCtas = 8;                       // of a cluster
 constexpr int kScoreStage = kKChunk * 128;         // a chunk's tokens x 32 dimensions
 constexpr int kScoreStages = 2;
 constexpr int kPvTokens = 16;                      // of a step of P V
-constexpr int kPvStages = 3;
 
 // ---------------------------------------------------------------- plan
 // A cluster of up to 8 CTAs a group. Every request keeps a token of its own, so a
@@ -409,34 +408,34 @@ __global__ void __launch_bounds__(kSumThreads) shared_sums_kernel(const SharedAr
 }
 
 // ---------------------------------------------------------------- partials
-// An item: 4 RT rows, 32 DH dimensions, a chunk; it is a warp's alone (4 lanes x RT
-// rows, 8 lanes x 4 DH dimensions), which walks the chunk's tokens 16 at a time:
-// values by its own ring, exps loaded a step ahead, multiplied by 1 / S and laid
-// down transposed (rows 16 apart swapped for every other four tokens, so that the two
-// halves of an octet go to different banks).
-template <int RT, int DH>
+// An item: 4 TR rows, 32 DH dimensions, a chunk; it is a warp's alone (4 lanes x TR
+// rows, 4 apart; 8 lanes x 4 DH dimensions), which walks the chunk's tokens 16 at a time
+// with a ring of its own: values, and exps as they lie (two octets of a block of rows are
+// two bulk copies). Accumulators pair dimensions, which come in pairs; an exp is
+// multiplied by 1 / S where it is used, once for 4 DH multiply-adds a lane.
+template <int TR, int DH>
 struct PvWarp {
-    static constexpr int kR = 4 * RT;
-    static constexpr int kStage = kPvTokens * 128 * DH;
-    static constexpr int kBytes = (kPvStages * kStage + kPvTokens * kR * 4 + 1023) / 1024 * 1024;
+    static constexpr int kR = 4 * TR;
+    static constexpr int kValues = kPvTokens * 128 * DH;
+    static constexpr int kStage = kValues + kPvTokens * kR * 4;
+    static constexpr int kStages = DH == 4 ? 2 : 3;
+    static constexpr int kCtas = DH == 4 ? 2 : 3;        // an SM's
+    static constexpr size_t kBytes = size_t(kWarps) * kStages * kStage;
+    static_assert(kStage % 1024 == 0 && kCtas * (kBytes + 2048) <= 228 * 1024, "shared memory");
 };
 
-template <int RT, int DH, bool OWN, bool TMA>
-__global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
+template <int TR, int DH, bool OWN, bool TMA>
+__global__ void __launch_bounds__(kThreads, (PvWarp<TR, DH>::kCtas))
     shared_partials_kernel(const SharedArgs A, const __grid_constant__ CUtensorMap vmap) {
-    using W = PvWarp<RT, DH>;
-    constexpr int R = W::kR;
-    constexpr int LOADS = R / 8 > 1 ? R / 8 : 1;      // 16-byte loads of exps a lane and step
-    constexpr int OWNED = R / 16 > 1 ? R / 16 : 1;    // rows whose exps a lane loads
-    constexpr int SWAP = R >= 32 ? 16 : 0;
+    using W = PvWarp<TR, DH>;
+    constexpr int R = W::kR, STAGES = W::kStages;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ Share share[kWarps];
-    __shared__ uint64_t full[kWarps][kPvStages];
-    __shared__ int rows[kWarps][R];
+    __shared__ uint64_t full[kWarps][STAGES];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, dl = lane & 7, rl = lane >> 3;
     const int d = A.d, mul = A.kv_heads * A.row_blocks * A.dim_tiles;
     if (TMA && tid == 0) {
-        for (int i = 0; i < kWarps * kPvStages; ++i) mbar_init(smem_u32(&full[0][i]), 1);
+        for (int i = 0; i < kWarps * STAGES; ++i) mbar_init(smem_u32(&full[0][i]), 1);
         fence_mbar_init();
     }
     grid_dependency_wait();
@@ -444,13 +443,21 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
     shares<OWN, kWarps>(A, mul, blockIdx.x, gridDim.x, gridDim.x * kWarps, share);
     const int64_t items = share[warp].items;
     if (items <= 0) return;
-    const uint32_t ring = smem_u32(smem_raw) + warp * W::kBytes;
-    float *ps = reinterpret_cast<float *>(smem_raw + warp * W::kBytes + kPvStages * W::kStage);
+    const uint32_t ring = smem_u32(smem_raw) + warp * STAGES * W::kStage;
+    // an item's key-value head, first row, and where its first octet's exps are
+    auto head_of = [&](const Item &i) { return i.run / (A.row_blocks * A.dim_tiles); };
+    auto row_of = [&](const Item &i) { return i.run / A.dim_tiles % A.row_blocks * R; };
+    auto exps_of = [&](const Item &i, int t0) {
+        const int64_t octet =
+            (int64_t(group_of<OWN>(A, i.u)) * A.kv_heads + head_of(i)) * A.octets + t0 / 8;
+        return A.x + (octet * A.rows + place_of<OWN>(A, i.u, row_of(i))) * 8;
+    };
 
-    // ---- values
+    // ---- values and exps
     Item in = share[warp].at;
     int64_t in_items = items;
     int in_t = 0, in_live = 0, in_slot = 0, in_id = 0;      // next token of the item, tokens left
+    const float *in_x = nullptr;
     const int per_half = TMA ? kPvTokens / A.box : 1;       // boxes of 32 dimensions
     auto look_up = [&]() {            // the page of the lane's box of the next step
         if (TMA && in_items > 0 && lane < DH * per_half && lane % per_half * A.box < in_live)
@@ -460,17 +467,20 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
         if (in_items <= 0) return;
         in_t = first_token<OWN>(A, in);
         in_live = tokens_from<OWN>(A, in, in_t);
+        in_x = exps_of(in, in_t);
     };
     start();
     look_up();
     auto issue = [&]() {
         if (in_items > 0) {
-            const int kv = in.run / (A.row_blocks * A.dim_tiles), dim0 = in.run % A.dim_tiles * 32 * DH;
+            const int kv = head_of(in), dim0 = in.run % A.dim_tiles * 32 * DH;
             const uint32_t dst = ring + in_slot * W::kStage, bar = smem_u32(&full[warp][in_slot]);
-            const int live = min(kPvTokens, in_live);
+            const int live = min(kPvTokens, in_live), octets = (live + 7) / 8;
+            const int alive = min(R, rows_of<OWN>(A) - row_of(in));
             if constexpr (TMA) {
                 const int boxes = (live + A.box - 1) / A.box;
-                if (lane == 0) mbar_arrive_expect_tx(bar, boxes * A.box * 128 * DH);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar, boxes * A.box * 128 * DH + octets * alive * 32);
                 __syncwarp();
                 const int half = lane / per_half, box = lane % per_half;
                 if (half < DH && box < boxes) {
@@ -478,8 +488,16 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
                     tma_load_4d(dst + half * kPvTokens * 128 + box * A.box * 128, &vmap,
                                 dim0 + 32 * half, kv,
                                 int(unsigned(t) - page_of(A, t) * A.page_size), in_id, bar);
+                } else if (lane >= 30 && lane - 30 < octets) {
+                    const int o = lane - 30;
+                    bulk_load(dst + W::kValues + o * R * 32, in_x + o * A.rows * 8, alive * 32, bar);
                 }
             } else {
+                for (int i = lane; i < octets * alive * 2; i += 32) {
+                    const int o = i / (alive * 2), unit = i - o * alive * 2;
+                    cp_async<16>(dst + W::kValues + o * R * 32 + unit * 16,
+                                 in_x + o * A.rows * 8 + unit * 4);
+                }
                 const int32_t *pages = pages_of<OWN>(A, in);
                 const float *src = A.v + kv * A.head_stride + dim0;
                 if (A.wide) {
@@ -504,9 +522,10 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
                     }
                 }
             }
-            in_slot = in_slot + 1 == kPvStages ? 0 : in_slot + 1;
+            in_slot = in_slot + 1 == STAGES ? 0 : in_slot + 1;
             in_t += kPvTokens;
             in_live -= kPvTokens;
+            in_x += 2 * A.rows * 8;
             if (in_live <= 0) {
                 advance<OWN>(A, mul, in);
                 --in_items;
@@ -516,112 +535,54 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
         }
         if (!TMA) cp_commit();
     };
-    for (int i = 0; i < kPvStages - 1; ++i) issue();
+    for (int i = 0; i < STAGES - 1; ++i) issue();
 
-    // ---- exps: load k of a lane is number i = lane + 32 k of the step's 4 R: octet i /
-    // (2 R), row i mod 2 R / 2, half i mod 2
-    float4 e[LOADS];
-    float inv[OWNED];
-    const float *from = nullptr;      // of the item's first octet and the block's first row
-    int alive = 0;                    // the block's rows
-    auto ask = [&](int t) {
-#pragma unroll
-        for (int k = 0; k < LOADS; ++k) {
-            const int i = lane + 32 * k, row = i % (2 * R) / 2;
-            e[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (i < 4 * R && row < alive)
-                e[k] = *reinterpret_cast<const float4 *>(
-                    from + (int64_t(t / 8 + i / (2 * R)) * A.rows + row) * 8 + 4 * (i & 1));
-        }
-    };
     Item it = share[warp].at;
-    int held_u = -1, held_run = -1, slot = 0;
+    int held_u = -1, held_block = -1, slot = 0;
     uint32_t phase = 0;
     bool stuck = false;
-    auto hold = [&]() {               // the item's rows
-        const int block = it.run / A.dim_tiles, kv = block / A.row_blocks;
-        const int r0 = (block - kv * A.row_blocks) * R, g = group_of<OWN>(A, it.u);
-        from = A.x + (((int64_t(g) * A.kv_heads + kv) * A.octets + first_token<OWN>(A, it) / 8) *
-                          A.rows + place_of<OWN>(A, it.u, r0)) * 8;
-        if (it.u == held_u && it.run == held_run) return;
-        held_u = it.u;
-        held_run = it.run;
-        alive = min(R, rows_of<OWN>(A) - r0);
-        __syncwarp();
-        for (int r = lane; r < R; r += 32)
-            rows[warp][r] = r < alive ? row_at(A, g, kv, place_of<OWN>(A, it.u, r0 + r)) : -1;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < OWNED; ++i) {
-            const int row = rows[warp][(lane + 32 * i) % (2 * R) / 2];
-            inv[i] = row >= 0 ? A.inv[row] : 0.0f;
-        }
-    };
-    hold();
-    ask(0);
-    constexpr bool kRowPairs = RT >= 8;
+    int mine[TR];                     // the lane's rows (b, h), -1 where there is none
+    float inv[TR];
     for (int64_t i = 0; i < items; ++i) {
-        constexpr int N0 = kRowPairs ? RT / 2 : RT, N1 = kRowPairs ? 4 * DH : 2 * DH;
-        f32x2 acc[N0][N1];
+        if (it.u != held_u || it.run / A.dim_tiles != held_block) {
+            held_u = it.u;
+            held_block = it.run / A.dim_tiles;
+            const int g = group_of<OWN>(A, it.u), kv = head_of(it), r0 = row_of(it);
 #pragma unroll
-        for (int a = 0; a < N0; ++a)
+            for (int r = 0; r < TR; ++r) {
+                const int at = r0 + 4 * r + rl;
+                mine[r] = at < rows_of<OWN>(A) ? row_at(A, g, kv, place_of<OWN>(A, it.u, at)) : -1;
+                inv[r] = mine[r] >= 0 ? A.inv[mine[r]] : 0.0f;
+            }
+        }
+        f32x2 acc[TR][2 * DH];
 #pragma unroll
-            for (int b = 0; b < N1; ++b) acc[a][b] = 0;
+        for (int r = 0; r < TR; ++r)
+#pragma unroll
+            for (int k = 0; k < 2 * DH; ++k) acc[r][k] = 0;
         const int t0 = first_token<OWN>(A, it), tokens = tokens_from<OWN>(A, it, t0);
-        const int dim0 = it.run % A.dim_tiles * 32 * DH + 4 * dl;
-        int mine[RT];                 // the rows whose partials the lane has
-#pragma unroll
-        for (int r = 0; r < RT; ++r) mine[r] = rows[warp][rl * RT + r];
         for (int t1 = 0; t1 < tokens; t1 += kPvTokens) {
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < LOADS; ++k) {
-                const int j = lane + 32 * k, half = j & 1;
-                if (j < 4 * R) {
-                    float *to = ps + (8 * (j / (2 * R)) + 4 * half) * R +
-                                (j % (2 * R) / 2 ^ SWAP * half);
-                    const float w = inv[k % OWNED];
-                    to[0] = __fmul_rn(e[k].x, w);
-                    to[R] = __fmul_rn(e[k].y, w);
-                    to[2 * R] = __fmul_rn(e[k].z, w);
-                    to[3 * R] = __fmul_rn(e[k].w, w);
-                }
-            }
-            if (t1 + kPvTokens < tokens) {
-                ask(t1 + kPvTokens);
-            } else if (i + 1 < items) {
-                advance<OWN>(A, mul, it);
-                hold();
-                ask(0);
-            }
             if constexpr (TMA) {
                 if (!stuck)
                     stuck = __any_sync(0xffffffffu,
                                        !mbar_wait_bounded(smem_u32(&full[warp][slot]), phase));
             } else {
-                cp_wait<kPvStages - 2>();
+                cp_wait<STAGES - 2>();
             }
             __syncwarp();
             if (!stuck) issue();      // into the slot consumed before this one
             const uint32_t vals = ring + slot * W::kStage;
-            auto token = [&](int t) {
-                const float *p = ps + t * R + (rl * RT ^ SWAP * (t >> 2 & 1));
-                const uint32_t at = vals + t * 128 + ((dl ^ (t & 7)) << 4);
-                if constexpr (kRowPairs) {
-                    f32x2 w[RT / 2];
-                    load_pairs<RT>(p, w);
+            const uint32_t exps = vals + W::kValues + rl * 32;
+            auto four = [&](int t4, int live) {
+                float4 e[TR];
 #pragma unroll
-                    for (int half = 0; half < DH; ++half) {
-                        const float4 v = lds4(at + half * kPvTokens * 128);
+                for (int r = 0; r < TR; ++r)
+                    e[r] = lds4(exps + (t4 >> 3) * R * 32 + r * 128 + (t4 & 4) * 4);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const f32x2 vk = splat2(part_of(v, k));
-#pragma unroll
-                            for (int r = 0; r < RT / 2; ++r)
-                                acc[r][4 * half + k] = fma2(w[r], vk, acc[r][4 * half + k]);
-                        }
-                    }
-                } else {
+                for (int k = 0; k < 4; ++k) {
+                    if (k >= live) break;
+                    const int t = t4 + k;
+                    const uint32_t at = vals + t * 128 + ((dl ^ (t & 7)) << 4);
                     f32x2 v[2 * DH];
 #pragma unroll
                     for (int half = 0; half < DH; ++half) {
@@ -630,45 +591,35 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
                         v[2 * half + 1] = pack2(u.z, u.w);
                     }
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        const f32x2 w = splat2(p[r]);
+                    for (int r = 0; r < TR; ++r) {
+                        const f32x2 w = splat2(__fmul_rn(part_of(e[r], k), inv[r]));
 #pragma unroll
-                        for (int k = 0; k < 2 * DH; ++k) acc[r][k] = fma2(w, v[k], acc[r][k]);
+                        for (int c = 0; c < 2 * DH; ++c) acc[r][c] = fma2(w, v[c], acc[r][c]);
                     }
                 }
             };
             if (!OWN || t1 + kPvTokens <= tokens) {
 #pragma unroll
-                for (int t = 0; t < kPvTokens; ++t) token(t);
+                for (int t = 0; t < kPvTokens; t += 4) four(t, 4);
             } else {
-                for (int t = 0; t < tokens - t1; ++t) token(t);
+                for (int t = 0; t1 + t < tokens; t += 4) four(t, tokens - t1 - t);
             }
-            if (++slot == kPvStages) {
+            if (++slot == STAGES) {
                 slot = 0;
                 phase ^= 1;
             }
         }
         // ---- the partials of the lane's rows and dimensions
+        const int dim0 = it.run % A.dim_tiles * 32 * DH + 4 * dl;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
+        for (int r = 0; r < TR; ++r) {
             if (mine[r] < 0) continue;
             float *to = A.part + (mine[r] * A.ldpart + t0 / kKChunk) * d;
 #pragma unroll
             for (int half = 0; half < DH; ++half) {
                 float4 o;
-                float other;
-                if constexpr (kRowPairs) {
-                    float o4[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        unpack2(acc[r / 2][4 * half + k], o4[k], other);
-                        if (r & 1) o4[k] = other;
-                    }
-                    o = make_float4(o4[0], o4[1], o4[2], o4[3]);
-                } else {
-                    unpack2(acc[r][2 * half], o.x, o.y);
-                    unpack2(acc[r][2 * half + 1], o.z, o.w);
-                }
+                unpack2(acc[r][2 * half], o.x, o.y);
+                unpack2(acc[r][2 * half + 1], o.z, o.w);
                 if (stuck) o.x = o.y = o.z = o.w = __uint_as_float(0x7fc00000u);
                 const int at = dim0 + 32 * half;
                 if (d % 4 == 0) {
@@ -680,12 +631,13 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
                 }
             }
         }
+        advance<OWN>(A, mul, it);
     }
     if (!TMA) cp_wait<0>();
     if (TMA && stuck) {                   // let the copies in flight land
-        for (int i = 0; i < kPvStages; ++i) {
+        for (int i = 0; i < STAGES; ++i) {
             (void)mbar_wait_bounded(smem_u32(&full[warp][slot]), phase);
-            if (++slot == kPvStages) {
+            if (++slot == STAGES) {
                 slot = 0;
                 phase ^= 1;
             }
@@ -721,9 +673,24 @@ __global__ void __launch_bounds__(kThreads) shared_join_kernel(const SharedArgs 
 // ---------------------------------------------------------------- host
 constexpr size_t kSliceBytes = size_t(1) << 30;     // scores and partials of a round of heads
 
-// Rows a thread takes of a unit's rows, more than kFewRows.
-int rows_a_thread(int64_t rows, int64_t head_dim) {
-    return rows <= 16 ? 4 : rows <= 32 || head_dim > 192 ? 8 : 16;
+// Rows a thread takes of a unit's rows (more than kFewRows), a power of two from 4 to
+// `widest`: those whose items, `tiles` a block of 4 RT rows, take the fewest waves over
+// the workers of an SM, an item counted as its rows and two (what does not depend on
+// them), as many workers at a time as share the SM.
+template <class Workers>
+int rows_a_thread(int64_t rows, int64_t tiles, int widest, Workers workers) {
+    int best = 4;
+    double least = 1e300;
+    for (int rt = 4; rt <= widest; rt *= 2) {
+        const int64_t items = tiles * ((rows + 4 * rt - 1) / (4 * rt));
+        const int64_t slots = int64_t(sm_count_current_device()) * workers(rt);
+        const double cost = double((items + slots - 1) / slots) * (rt + 2) * workers(rt);
+        if (cost <= least) {
+            least = cost;
+            best = rt;
+        }
+    }
+    return best;
 }
 
 struct SharedPlan {
@@ -805,35 +772,40 @@ cudaError_t run_scores(SharedArgs A, const CUtensorMap *map, int64_t rows, int64
 template <bool OWN>
 cudaError_t scores(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
     const int64_t rows = OWN ? A.per_kv : A.rows;
-    switch (rows_a_thread(rows, A.d)) {
+    switch (rows_a_thread(rows, most * A.kv_heads, A.d <= 192 ? 16 : 8,
+                          [](int rt) { return rt >= 8 ? 2 : 3; })) {
         case 4: return run_scores<4, OWN>(A, map, rows, most, s);
         case 8: return run_scores<8, OWN>(A, map, rows, most, s);
         default: return run_scores<16, OWN>(A, map, rows, most, s);
     }
 }
 
-template <int RT, int DH, bool OWN>
+template <int TR, int DH, bool OWN>
 cudaError_t run_partials(SharedArgs A, const CUtensorMap *map, int64_t rows, int64_t most,
                          cudaStream_t s) {
-    A.row_blocks = int((rows + 4 * RT - 1) / (4 * RT));
+    using W = PvWarp<TR, DH>;
+    A.row_blocks = int((rows + W::kR - 1) / W::kR);
     A.dim_tiles = (A.d + 32 * DH - 1) / (32 * DH);
     const int64_t items = most * A.kv_heads * A.row_blocks * A.dim_tiles;
-    const int64_t grid =
-        std::min<int64_t>((items + kWarps - 1) / kWarps,
-                          int64_t(sm_count_current_device()) * (RT >= 8 ? 2 : 3));
-    const size_t smem = size_t(kWarps) * PvWarp<RT, DH>::kBytes;
+    const int64_t grid = std::min<int64_t>((items + kWarps - 1) / kWarps,
+                                           int64_t(sm_count_current_device()) * W::kCtas);
     const CUtensorMap none = {};
-    return map ? run(shared_partials_kernel<RT, DH, OWN, true>, grid, smem, s, A, *map)
-               : run(shared_partials_kernel<RT, DH, OWN, false>, grid, smem, s, A, none);
+    return map ? run(shared_partials_kernel<TR, DH, OWN, true>, grid, W::kBytes, s, A, *map)
+               : run(shared_partials_kernel<TR, DH, OWN, false>, grid, W::kBytes, s, A, none);
 }
 template <int DH, bool OWN>
-cudaError_t partials(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
+cudaError_t partials_of(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
     const int64_t rows = OWN ? A.per_kv : A.rows;
-    switch (rows_a_thread(rows, 0)) {
-        case 4: return run_partials<4, DH, OWN>(A, map, rows, most, s);
-        case 8: return run_partials<8, DH, OWN>(A, map, rows, most, s);
-        default: return run_partials<16, DH, OWN>(A, map, rows, most, s);
-    }
+    const int64_t tiles = most * A.kv_heads * ((A.d + 32 * DH - 1) / (32 * DH));
+    return rows_a_thread(rows, tiles, 8, [](int) { return kWarps * PvWarp<8, DH>::kCtas; }) == 8
+               ? run_partials<8, DH, OWN>(A, map, rows, most, s)
+               : run_partials<4, DH, OWN>(A, map, rows, most, s);
+}
+template <bool OWN>
+cudaError_t partials(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
+    return A.d <= 32   ? partials_of<1, OWN>(A, map, most, s)
+           : A.d <= 64 ? partials_of<2, OWN>(A, map, most, s)
+                       : partials_of<4, OWN>(A, map, most, s);
 }
 
 }  // namespace
@@ -932,14 +904,12 @@ cudaError_t launch_shared_decode(int64_t batch, int64_t group, int heads, const 
         };
         if (e == cudaSuccess) {
             map = values(few);
-            e = few       ? launch_few_partials(false, A, map, most, s)
-                : d <= 32 ? partials<1, false>(A, map, most, s)
-                          : partials<2, false>(A, map, most, s);
+            e = few ? launch_few_partials(false, A, map, most, s) : partials<false>(A, map, most, s);
         }
         if (e == cudaSuccess) {
             map = values(few_own);
             e = few_own ? launch_few_partials(true, A, map, most_own, s)
-                        : partials<1, true>(A, map, most_own, s);
+                        : partials<true>(A, map, most_own, s);
         }
         if (e == cudaSuccess) {
             e = launch_dependent(shared_join_kernel,
