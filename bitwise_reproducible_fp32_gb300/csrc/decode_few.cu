@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
     int64_t left = items * nsl;
     int in_sl = 0, in_t0 = 0, in_live = 0;
     auto start = [&]() {
-        in_t0 = first_token<CUT>(A, in);
-        in_live = tokens_from<CUT>(A, in, in_t0);
+        in_t0 = first_token<CUT>(in);
+        in_live = tokens_from<CUT>(in, in_t0);
         ring.look_up(pages_of<CUT>(A, in), in_t0, in_live);
     };
     start();
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
             }
             __syncwarp();
         }
-        const int t0 = first_token<CUT>(A, it), live = tokens_from<CUT>(A, it, t0);
+        const int t0 = first_token<CUT>(it), live = tokens_from<CUT>(it, t0);
         float acc[2][NH];         // of tokens lane and lane + 32
 #pragma unroll
         for (int h = 0; h < NH; ++h) acc[0][h] = acc[1][h] = 0.0f;
@@ -303,18 +303,21 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
     Item in = share[warp].at;
     int64_t in_items = items;
     int in_t = 0, in_left = 0;            // next token of the item, tokens left
+    int in_kv = 0, in_sl = 0;
     auto look_up = [&]() {
         if (in_items > 0) ring.look_up(pages_of<CUT>(A, in), in_t, min(kTile, in_left));
     };
     auto start = [&]() {
-        in_t = first_token<CUT>(A, in);
-        in_left = tokens_from<CUT>(A, in, in_t);
+        in_t = first_token<CUT>(in);
+        in_left = tokens_from<CUT>(in, in_t);
+        in_kv = in.run / nsl;
+        in_sl = in.run - in_kv * nsl;
     };
     start();
     look_up();
     auto issue = [&]() {
         if (in_items > 0) {
-            ring.fetch(in.run / nsl, in.run % nsl, in_t, min(kTile, in_left));
+            ring.fetch(in_kv, in_sl, in_t, min(kTile, in_left));
             in_t += kTile;
             in_left -= kTile;
             if (in_left <= 0) {
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
     int held_u = -1, held_kv = -1;
     auto hold = [&]() {
         const int kv = it.run / nsl, g = group_of<CUT>(A, it.u), place = place_of<CUT>(A, it.u, 0);
-        const int64_t octet = (int64_t(g) * A.kv_heads + kv) * A.octets + first_token<CUT>(A, it) / 8;
+        const int64_t octet = (int64_t(g) * A.kv_heads + kv) * A.octets + first_token<CUT>(it) / 8;
         from = A.x + ((octet + lane / 8) * A.rows + place) * 8 + (lane & 7);
         if (it.u == held_u && kv == held_kv) return;
         held_u = it.u;
@@ -360,12 +363,12 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
                                       : 0.0f;
             }
     };
-    auto tokens_of = [&]() { return tokens_from<CUT>(A, it, first_token<CUT>(A, it)); };
+    auto tokens_of = [&]() { return tokens_from<CUT>(it, first_token<CUT>(it)); };
     hold();
     ask(0, tokens_of());
     for (int64_t i = 0; i < items; ++i) {
         const int sl = it.run % nsl;
-        const int t0 = first_token<CUT>(A, it), tokens = tokens_of();
+        const int t0 = first_token<CUT>(it), tokens = tokens_of();
         float *out = A.part + int64_t(t0 / kKChunk) * d + 32 * sl + lane;
         float acc[NH];
         int mine[NH];             // the rows, before the next item's

@@ -186,12 +186,13 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
 
     // ---- keys
     Item in = share.at;
-    int in_sl = 0, in_slot = 0, in_t0 = 0, in_live = 0, in_boxes = 0, in_id = 0;
+    int in_sl = 0, in_slot = 0, in_t0 = 0, in_live = 0, in_boxes = 0, in_id = 0, in_kv = 0;
     int64_t left = items * nsl;
     auto look_up = [&]() {            // the item's tokens and, warp 0, the lane's box's page
         if (in.u >= units<OWN>(A)) return;
-        in_t0 = first_token<OWN>(A, in);
-        in_live = tokens_from<OWN>(A, in, in_t0);
+        in_t0 = first_token<OWN>(in);
+        in_live = tokens_from<OWN>(in, in_t0);
+        in_kv = in.run / A.row_blocks;
         if (TMA) {
             in_boxes = (in_live + A.box - 1) / A.box;             // at most 32
             if (warp == 0 && lane < in_boxes)
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
     auto issue = [&]() {
         if (left > 0) {
             --left;
-            const int kv = in.run / A.row_blocks;
+            const int kv = in_kv;
             const uint32_t dst = ring + in_slot * kScoreStage, bar = smem_u32(full + in_slot);
             if constexpr (TMA) {
                 if (warp == 0) {
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
     for (int64_t i = 0; i < items; ++i) {
         const int kv = it.run / A.row_blocks, r0 = (it.run - kv * A.row_blocks) * R;
         const int g = group_of<OWN>(A, it.u);
-        const int t0 = first_token<OWN>(A, it), live = tokens_from<OWN>(A, it, t0);
+        const int t0 = first_token<OWN>(it), live = tokens_from<OWN>(it, t0);
         if (it.u != held_u || it.run != held_run) {         // other rows
             held_u = it.u;
             held_run = it.run;
@@ -362,14 +363,15 @@ __global__ void __launch_bounds__(kSumThreads) shared_sums_kernel(const SharedAr
     __shared__ float chains[kSumRows][256], red[kSumRows][8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 3, place = blockIdx.x * kSumRows + r;
-    const int g = blockIdx.y / A.kv_heads, kv = blockIdx.y % A.kv_heads;
+    // the scores written last are still in L2, and are read first
+    const int gkv = gridDim.y - 1 - blockIdx.y, g = gkv / A.kv_heads, kv = gkv % A.kv_heads;
     grid_dependency_wait();
     allow_dependents();
     const int row = place < A.rows ? row_at(A, g, kv, place) : -1;
     const int n = row >= 0 ? A.kv_lens[row / A.heads] : 0;
     const float m = row >= 0 ? max_of_key(A.top[row]) : 0.0f;
     const bool finite = fabsf(m) <= 0x1.fffffep127f;
-    float *x = A.x + (int64_t(blockIdx.y) * A.octets * A.rows + place) * 8;
+    float *x = A.x + (int64_t(gkv) * A.octets * A.rows + place) * 8;
     for (int l = 8 * warp + (lane & 7); l < 256; l += 8 * (kSumThreads / 32)) {
         float sum = 0.0f;
         for (int t = 4 * l; t < n; t += 1024 * kSumDeep) {
@@ -457,26 +459,31 @@ __global__ void __launch_bounds__(kThreads, (PvWarp<TR, DH>::kCtas))
     Item in = share[warp].at;
     int64_t in_items = items;
     int in_t = 0, in_live = 0, in_slot = 0, in_id = 0;      // next token of the item, tokens left
+    int in_kv = 0, in_dim0 = 0, in_alive = 0;
     const float *in_x = nullptr;
+    const int32_t *in_pages = nullptr;
     const int per_half = TMA ? kPvTokens / A.box : 1;       // boxes of 32 dimensions
     auto look_up = [&]() {            // the page of the lane's box of the next step
         if (TMA && in_items > 0 && lane < DH * per_half && lane % per_half * A.box < in_live)
-            in_id = pages_of<OWN>(A, in)[page_of(A, in_t + lane % per_half * A.box)];
+            in_id = in_pages[page_of(A, in_t + lane % per_half * A.box)];
     };
     auto start = [&]() {
         if (in_items <= 0) return;
-        in_t = first_token<OWN>(A, in);
-        in_live = tokens_from<OWN>(A, in, in_t);
+        in_t = first_token<OWN>(in);
+        in_live = tokens_from<OWN>(in, in_t);
+        in_kv = head_of(in);
+        in_dim0 = in.run % A.dim_tiles * 32 * DH;
+        in_alive = min(R, rows_of<OWN>(A) - row_of(in));
         in_x = exps_of(in, in_t);
+        in_pages = pages_of<OWN>(A, in);
     };
     start();
     look_up();
     auto issue = [&]() {
         if (in_items > 0) {
-            const int kv = head_of(in), dim0 = in.run % A.dim_tiles * 32 * DH;
+            const int kv = in_kv, dim0 = in_dim0, alive = in_alive;
             const uint32_t dst = ring + in_slot * W::kStage, bar = smem_u32(&full[warp][in_slot]);
             const int live = min(kPvTokens, in_live), octets = (live + 7) / 8;
-            const int alive = min(R, rows_of<OWN>(A) - row_of(in));
             if constexpr (TMA) {
                 const int boxes = (live + A.box - 1) / A.box;
                 if (lane == 0)
@@ -498,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, (PvWarp<TR, DH>::kCtas))
                     cp_async<16>(dst + W::kValues + o * R * 32 + unit * 16,
                                  in_x + o * A.rows * 8 + unit * 4);
                 }
-                const int32_t *pages = pages_of<OWN>(A, in);
+                const int32_t *pages = in_pages;
                 const float *src = A.v + kv * A.head_stride + dim0;
                 if (A.wide) {
                     for (int r = lane >> 3; r < live; r += 4) {
@@ -560,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, (PvWarp<TR, DH>::kCtas))
         for (int r = 0; r < TR; ++r)
 #pragma unroll
             for (int k = 0; k < 2 * DH; ++k) acc[r][k] = 0;
-        const int t0 = first_token<OWN>(A, it), tokens = tokens_from<OWN>(A, it, t0);
+        const int t0 = first_token<OWN>(it), tokens = tokens_from<OWN>(it, t0);
         for (int t1 = 0; t1 < tokens; t1 += kPvTokens) {
             if constexpr (TMA) {
                 if (!stuck)

@@ -60,7 +60,8 @@ template <int CUT>
 constexpr bool kInTiles = (CUT & 2) != 0;
 constexpr int kTile = 64;
 struct Item {
-    int u, run, c, n;         // n: the unit's chunks or tiles
+    int u, run, c;
+    int n, base, end;         // the unit's chunks or tiles, its first token and its end
 };
 template <int CUT>
 __device__ __forceinline__ int units(const SharedArgs &A) { return kIsOwn<CUT> ? A.batch : A.groups; }
@@ -71,16 +72,20 @@ __device__ __forceinline__ int chunks_of(const SharedArgs &A, int u) {
     if (!kIsOwn<CUT>) return n * (kKChunk / kTile);
     return (A.kv_lens[u] - A.chunks[u / A.group] * kKChunk + kTile - 1) / kTile;
 }
+template <int CUT>
+__device__ __forceinline__ void enter(const SharedArgs &A, Item &it) {      // its unit
+    it.n = chunks_of<CUT>(A, it.u);
+    it.base = kIsOwn<CUT> ? A.chunks[it.u / A.group] * kKChunk : 0;
+    it.end = kIsOwn<CUT> ? A.kv_lens[it.u] : A.chunks[it.u] * kKChunk;
+}
 // The item's first token, how many it has, and the table row of its pages.
 template <int CUT>
-__device__ __forceinline__ int first_token(const SharedArgs &A, const Item &it) {
-    return it.c * (kInTiles<CUT> ? kTile : kKChunk) +
-           (kIsOwn<CUT> ? A.chunks[it.u / A.group] * kKChunk : 0);
+__device__ __forceinline__ int first_token(const Item &it) {
+    return it.base + it.c * (kInTiles<CUT> ? kTile : kKChunk);
 }
 template <int CUT>
-__device__ __forceinline__ int tokens_from(const SharedArgs &A, const Item &it, int t0) {
-    const int most = kInTiles<CUT> ? kTile : kKChunk;
-    return kIsOwn<CUT> ? min(most, A.kv_lens[it.u] - t0) : most;
+__device__ __forceinline__ int tokens_from(const Item &it, int t0) {
+    return min(kInTiles<CUT> ? kTile : kKChunk, it.end - t0);
 }
 template <int CUT>
 __device__ __forceinline__ const int32_t *pages_of(const SharedArgs &A, const Item &it) {
@@ -146,7 +151,8 @@ __device__ __forceinline__ void shares(const SharedArgs &A, int mul, int first, 
             while ((at + chunks_of<CUT>(A, u)) * mul <= lo) at += chunks_of<CUT>(A, u++);
             const int c = chunks_of<CUT>(A, u);
             const int64_t k = lo - at * mul;
-            out[w].at = {u, int(k / c), int(k % c), c};
+            out[w].at = {u, int(k / c), int(k % c)};
+            enter<CUT>(A, out[w].at);
         }
     }
     __syncthreads();
@@ -159,7 +165,8 @@ __device__ __forceinline__ void advance(const SharedArgs &A, int mul, Item &it) 
     it.run = 0;
     do {
         ++it.u;
-    } while (it.u < units<CUT>(A) && (it.n = chunks_of<CUT>(A, it.u)) == 0);
+    } while (it.u < units<CUT>(A) && chunks_of<CUT>(A, it.u) == 0);
+    if (it.u < units<CUT>(A)) enter<CUT>(A, it);
 }
 
 // A token's offset in the cache (its page is in order: the plan has seen it).
