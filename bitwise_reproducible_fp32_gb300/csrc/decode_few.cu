@@ -138,8 +138,7 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int d = A.d, nsl = (d + 31) / 32, live_rows = rows_of<CUT>(A), ldq = nsl * 32;
     init_bars<LOAD>(&full[0][0]);
-    grid_dependency_wait();
-    allow_dependents();
+    Beside<OWN> beside;
     shares<CUT, kWarps>(A, A.kv_heads, blockIdx.x, gridDim.x, gridDim.x * kWarps, share);
     const int64_t items = share[warp].items;
     if (items <= 0) return;
@@ -290,8 +289,7 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int d = A.d, nsl = (d + 31) / 32, live_rows = rows_of<CUT>(A), mul = A.kv_heads * nsl;
     init_bars<LOAD>(&full[0][0]);
-    grid_dependency_wait();
-    allow_dependents();
+    Beside<OWN> beside;
     shares<CUT, kWarps>(A, mul, blockIdx.x, gridDim.x, gridDim.x * kWarps, share);
     const int64_t items = share[warp].items;
     if (items <= 0) return;
@@ -470,19 +468,23 @@ cudaError_t partials_of(const SharedArgs &A, const CUtensorMap *map, int64_t mos
 template <bool OWN>
 cudaError_t scores_by_rows(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
     const int64_t rows = OWN ? A.per_kv : A.rows;
-    return rows == 1   ? scores_of<1, OWN>(A, map, most, s)
-           : rows == 2 ? scores_of<2, OWN>(A, map, most, s)
-           : rows <= 4 ? scores_of<4, OWN>(A, map, most, s)
-                       : scores_of<kFewRows, OWN>(A, map, most, s);
+    if constexpr (OWN) {       // two rows are not worth reading together
+        if (rows == 1) return scores_of<1, OWN>(A, map, most, s);
+        if (rows == 2) return scores_of<2, OWN>(A, map, most, s);
+    }
+    return rows <= 4 ? scores_of<4, OWN>(A, map, most, s)
+                     : scores_of<kFewRows, OWN>(A, map, most, s);
 }
 template <bool OWN>
 cudaError_t partials_by_rows(const SharedArgs &A, const CUtensorMap *map, int64_t most,
                              cudaStream_t s) {
     const int64_t rows = OWN ? A.per_kv : A.rows;
-    return rows == 1   ? partials_of<1, OWN>(A, map, most, s)
-           : rows == 2 ? partials_of<2, OWN>(A, map, most, s)
-           : rows <= 4 ? partials_of<4, OWN>(A, map, most, s)
-                       : partials_of<kFewRows, OWN>(A, map, most, s);
+    if constexpr (OWN) {       // two rows are not worth reading together
+        if (rows == 1) return partials_of<1, OWN>(A, map, most, s);
+        if (rows == 2) return partials_of<2, OWN>(A, map, most, s);
+    }
+    return rows <= 4 ? partials_of<4, OWN>(A, map, most, s)
+                     : partials_of<kFewRows, OWN>(A, map, most, s);
 }
 
 }  // namespace

@@ -38,7 +38,10 @@ constexpr int kPlanRows = 1024;                    // requests looked through at
 constexpr int kPlanCtas = 8;                       // of a cluster
 constexpr int kScoreStage = kKChunk * 128;         // a chunk's tokens x 32 dimensions
 constexpr int kScoreStages = 2;
+constexpr int kScoreRows = 4;                      // of a thread
+constexpr int kScoreCtas = 3;                      // an SM's
 constexpr int kPvTokens = 16;                      // of a step of P V
+constexpr int kPvCtas = 2;                         // an SM's
 
 // ---------------------------------------------------------------- plan
 // A cluster of up to 8 CTAs a group. Every request keeps a token of its own, so a
@@ -162,10 +165,10 @@ __device__ __forceinline__ float part_of(const float4 &v, int i) {
 // apart, so that 16-byte reads along the dimensions of 8 keys meet no bank
 // conflict), 4 lanes x RT rows (4 apart). Keys come 32 dimensions at a time, a stage
 // ahead; the query rows stay in shared memory, transposed, while they do not change.
-template <int RT, bool OWN, bool TMA>
-__global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
+template <bool OWN, bool TMA>
+__global__ void __launch_bounds__(kThreads, kScoreCtas)
     shared_scores_kernel(const SharedArgs A, const __grid_constant__ CUtensorMap kmap) {
-    constexpr int R = 4 * RT;
+    constexpr int RT = kScoreRows, R = 4 * RT;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     float *qs = reinterpret_cast<float *>(smem_raw + kScoreStages * kScoreStage);
     __shared__ Share share;
@@ -177,8 +180,7 @@ __global__ void __launch_bounds__(kThreads, RT >= 8 ? 2 : 3)
         for (int i = 0; i < kScoreStages; ++i) mbar_init(smem_u32(full + i), 1);
         fence_mbar_init();
     }
-    grid_dependency_wait();
-    allow_dependents();
+    Beside<OWN> beside;
     shares<OWN, 1>(A, mul, blockIdx.x, 1, gridDim.x, &share);
     const int64_t items = share.items;
     if (items <= 0) return;
@@ -420,14 +422,14 @@ struct PvWarp {
     static constexpr int kR = 4 * TR;
     static constexpr int kValues = kPvTokens * 128 * DH;
     static constexpr int kStage = kValues + kPvTokens * kR * 4;
-    static constexpr int kStages = DH == 4 ? 2 : 3;
-    static constexpr int kCtas = DH == 4 ? 2 : 3;        // an SM's
+    static constexpr int kFit = int(kMaxSmem / kWarps) / kStage;
+    static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr size_t kBytes = size_t(kWarps) * kStages * kStage;
-    static_assert(kStage % 1024 == 0 && kCtas * (kBytes + 2048) <= 228 * 1024, "shared memory");
+    static_assert(kStage % 1024 == 0 && kStages >= 2, "shared memory");
 };
 
 template <int TR, int DH, bool OWN, bool TMA>
-__global__ void __launch_bounds__(kThreads, (PvWarp<TR, DH>::kCtas))
+__global__ void __launch_bounds__(kThreads, kPvCtas)
     shared_partials_kernel(const SharedArgs A, const __grid_constant__ CUtensorMap vmap) {
     using W = PvWarp<TR, DH>;
     constexpr int R = W::kR, STAGES = W::kStages;
@@ -440,8 +442,7 @@ __global__ void __launch_bounds__(kThreads, (PvWarp<TR, DH>::kCtas))
         for (int i = 0; i < kWarps * STAGES; ++i) mbar_init(smem_u32(&full[0][i]), 1);
         fence_mbar_init();
     }
-    grid_dependency_wait();
-    allow_dependents();
+    Beside<OWN> beside;
     shares<OWN, kWarps>(A, mul, blockIdx.x, gridDim.x, gridDim.x * kWarps, share);
     const int64_t items = share[warp].items;
     if (items <= 0) return;
@@ -680,24 +681,24 @@ __global__ void __launch_bounds__(kThreads) shared_join_kernel(const SharedArgs 
 // ---------------------------------------------------------------- host
 constexpr size_t kSliceBytes = size_t(1) << 30;     // scores and partials of a round of heads
 
-// Rows a thread takes of a unit's rows (more than kFewRows), a power of two from 4 to
-// `widest`: those whose items, `tiles` a block of 4 RT rows, take the fewest waves over
-// the workers of an SM, an item counted as its rows and two (what does not depend on
-// them), as many workers at a time as share the SM.
-template <class Workers>
-int rows_a_thread(int64_t rows, int64_t tiles, int widest, Workers workers) {
-    int best = 4;
-    double least = 1e300;
-    for (int rt = 4; rt <= widest; rt *= 2) {
-        const int64_t items = tiles * ((rows + 4 * rt - 1) / (4 * rt));
-        const int64_t slots = int64_t(sm_count_current_device()) * workers(rt);
-        const double cost = double((items + slots - 1) / slots) * (rt + 2) * workers(rt);
-        if (cost <= least) {
-            least = cost;
-            best = rt;
-        }
-    }
-    return best;
+// Whether the requests are read together, or each for itself by decode.cu: one launch of
+// 18 us and more, its keys and values from L2 at 9 TB/s (with 4 and 8 heads of a key-value
+// head 1.5 and 3 times as long for their multiply-adds), against seven launches of 45 us and
+// more, each key and value once at 4.2 TB/s or the multiply-adds at 20 TFLOP/s. Rows are
+// taken as long as the table is wide, so only a gain of a quarter counts. Measured, for
+// itself / together, us: 12 heads of 64, 16 groups of 4 of 700..1900 tokens 74 / 79, of 8
+// of 1100..1500 139 / 115, of 4500..6000 437 / 212; one group of 32 of 1500 50 / 65, of
+// 6000 150 / 75; 16 groups of 2 of 6000 163 / 153; 4 groups of 4 with 4 query heads a
+// key-value head of 1500 46 / 68, of 6000 128 / 90.
+bool read_together(int64_t batch, int64_t group, int64_t heads, int64_t kv_heads, int64_t d,
+                   int64_t max_len) {
+    if (group < 2 || max_len <= 2 * kKChunk) return false;
+    const double token = 8.0 * double(kv_heads * d) * double(max_len);      // of one request
+    const double per_kv = double(heads / kv_heads), groups = double((batch + group - 1) / group);
+    const double alone = 18.0 + double(batch) * token / 9.0e6 * std::max(1.0, 0.37 * per_kv);
+    const double shared =
+        45.0 + std::max(groups * token / 4.2e6, double(batch) * per_kv * token / 2.0 / 20.0e6);
+    return alone > 1.25 * shared;
 }
 
 struct SharedPlan {
@@ -712,7 +713,8 @@ SharedPlan shared_plan(int64_t batch, int64_t group, int64_t heads, int64_t kv_h
     group = std::min(group, batch);
     const int64_t per_kv = heads / kv_heads;
     p.groups = group > 0 ? (batch + group - 1) / group : 0;
-    p.together = group > 1 && max_len > 2 * kKChunk && p.groups * group * heads < 0x7fffffff / 8;
+    p.together = read_together(batch, group, heads, kv_heads, head_dim, max_len) &&
+                 p.groups * group * heads < 0x7fffffff / 8;
     if (!p.together) {
         p.bytes = decode_workspace_bytes(batch, heads, kv_heads, head_dim, max_len);
         return p;
@@ -765,26 +767,17 @@ cudaError_t run_plan(const SharedArgs &A, int64_t max_pages, cudaStream_t s) {
 }
 
 // most: the chunks of all units, at most.
-template <int RT, bool OWN>
-cudaError_t run_scores(SharedArgs A, const CUtensorMap *map, int64_t rows, int64_t most,
-                       cudaStream_t s) {
-    A.row_blocks = int((rows + 4 * RT - 1) / (4 * RT));
-    const int64_t grid = std::min<int64_t>(
-        most * A.kv_heads * A.row_blocks, int64_t(sm_count_current_device()) * (RT >= 8 ? 2 : 3));
-    const size_t smem = kScoreStages * kScoreStage + size_t(A.d) * 4 * RT * 4;
-    const CUtensorMap none = {};
-    return map ? run(shared_scores_kernel<RT, OWN, true>, grid, smem, s, A, *map)
-               : run(shared_scores_kernel<RT, OWN, false>, grid, smem, s, A, none);
-}
 template <bool OWN>
-cudaError_t scores(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
+cudaError_t scores(SharedArgs A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
+    constexpr int R = 4 * kScoreRows;
     const int64_t rows = OWN ? A.per_kv : A.rows;
-    switch (rows_a_thread(rows, most * A.kv_heads, A.d <= 192 ? 16 : 8,
-                          [](int rt) { return rt >= 8 ? 2 : 3; })) {
-        case 4: return run_scores<4, OWN>(A, map, rows, most, s);
-        case 8: return run_scores<8, OWN>(A, map, rows, most, s);
-        default: return run_scores<16, OWN>(A, map, rows, most, s);
-    }
+    A.row_blocks = int((rows + R - 1) / R);
+    const int64_t grid = std::min<int64_t>(most * A.kv_heads * A.row_blocks,
+                                           int64_t(sm_count_current_device()) * kScoreCtas);
+    const size_t smem = kScoreStages * kScoreStage + size_t(A.d) * R * 4;
+    const CUtensorMap none = {};
+    return map ? run(shared_scores_kernel<OWN, true>, grid, smem, s, A, *map)
+               : run(shared_scores_kernel<OWN, false>, grid, smem, s, A, none);
 }
 
 template <int TR, int DH, bool OWN>
@@ -795,24 +788,39 @@ cudaError_t run_partials(SharedArgs A, const CUtensorMap *map, int64_t rows, int
     A.dim_tiles = (A.d + 32 * DH - 1) / (32 * DH);
     const int64_t items = most * A.kv_heads * A.row_blocks * A.dim_tiles;
     const int64_t grid = std::min<int64_t>((items + kWarps - 1) / kWarps,
-                                           int64_t(sm_count_current_device()) * W::kCtas);
+                                           int64_t(sm_count_current_device()) * kPvCtas);
     const CUtensorMap none = {};
     return map ? run(shared_partials_kernel<TR, DH, OWN, true>, grid, W::kBytes, s, A, *map)
                : run(shared_partials_kernel<TR, DH, OWN, false>, grid, W::kBytes, s, A, none);
 }
-template <int DH, bool OWN>
-cudaError_t partials_of(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
-    const int64_t rows = OWN ? A.per_kv : A.rows;
-    const int64_t tiles = most * A.kv_heads * ((A.d + 32 * DH - 1) / (32 * DH));
-    return rows_a_thread(rows, tiles, 8, [](int) { return kWarps * PvWarp<8, DH>::kCtas; }) == 8
-               ? run_partials<8, DH, OWN>(A, map, rows, most, s)
-               : run_partials<4, DH, OWN>(A, map, rows, most, s);
-}
+// The rows and slices a lane takes: an item's time is as 6 + TR DH (measured: 53 cycles a
+// token for 4 x 1, 65 for 4 x 2, 100 for 4 x 4, 104 for 8 x 2, 179 for 8 x 4), and a
+// scheduler's items come one after the other.
 template <bool OWN>
 cudaError_t partials(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
-    return A.d <= 32   ? partials_of<1, OWN>(A, map, most, s)
-           : A.d <= 64 ? partials_of<2, OWN>(A, map, most, s)
-                       : partials_of<4, OWN>(A, map, most, s);
+    const int64_t rows = OWN ? A.per_kv : A.rows;
+    const int64_t tiles = most * A.kv_heads, workers = int64_t(sm_count_current_device()) * kWarps;
+    int best = 0;
+    int64_t least = INT64_MAX;
+    for (int tr = 4; tr <= 8; tr *= 2)
+        for (int dh = 1; dh <= 4; dh *= 2) {
+            if (dh > 1 && 16 * dh >= A.d) break;      // a half of the slices would be empty
+            const int64_t items =
+                tiles * ((rows + 4 * tr - 1) / (4 * tr)) * ((A.d + 32 * dh - 1) / (32 * dh));
+            const int64_t cost = (items + workers - 1) / workers * (6 + tr * dh);
+            if (cost < least) {
+                least = cost;
+                best = tr * 10 + dh;
+            }
+        }
+    switch (best) {
+        case 41: return run_partials<4, 1, OWN>(A, map, rows, most, s);
+        case 42: return run_partials<4, 2, OWN>(A, map, rows, most, s);
+        case 44: return run_partials<4, 4, OWN>(A, map, rows, most, s);
+        case 81: return run_partials<8, 1, OWN>(A, map, rows, most, s);
+        case 82: return run_partials<8, 2, OWN>(A, map, rows, most, s);
+        default: return run_partials<8, 4, OWN>(A, map, rows, most, s);
+    }
 }
 
 }  // namespace

@@ -169,6 +169,22 @@ __device__ __forceinline__ void advance(const SharedArgs &A, int mul, Item &it) 
     if (it.u < units<CUT>(A)) enter<CUT>(A, it);
 }
 
+// Scores (and partials) of the shared chunks and of the own ones do not depend on each
+// other. So the kernel of the own ones (OWN), launched behind the other one, starts as
+// soon as that one's CTAs have all begun (which they do once everything before them is
+// complete) and there is room, and waits for it at its end, so that its own end is
+// both's.
+template <bool OWN>
+struct Beside {
+    __device__ __forceinline__ Beside() {
+        if (!OWN) grid_dependency_wait();
+        allow_dependents();
+    }
+    __device__ __forceinline__ ~Beside() {
+        if (OWN) grid_dependency_wait();
+    }
+};
+
 // A token's offset in the cache (its page is in order: the plan has seen it).
 __device__ __forceinline__ int64_t offset_of(const SharedArgs &A, const int32_t *pages, int t) {
     const unsigned p = page_of(A, t);

@@ -17,6 +17,9 @@ from gpu_util import host, need_gpu, to_dev, torch
 pytestmark = pytest.mark.gpu
 
 
+WIDE = 1 << 20                  # tokens
+
+
 @pytest.fixture(scope="module")
 def dev():
     return need_gpu()
@@ -69,7 +72,8 @@ def shared_cache(prefixes, own, ps, G, d, layout, rng, edit=None):
 
 def both(q, kc, vc, table, lens, H, group, layout="dense", **kw):
     """The shared attention's output, after its bits and status have been compared with
-    decode attention's."""
+    decode attention's; also over the same table with room for much longer requests (short
+    ones are not worth reading together)."""
     qd, ld = to_dev(q, layout), on_gpu(np.asarray(lens, np.int32))
     s1, s2 = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
     want = host(detlib.detdecode_attention_f32(qd, kc, vc, table, ld, H, dev_status=s1, **kw))
@@ -79,6 +83,17 @@ def both(q, kc, vc, table, lens, H, group, layout="dense", **kw):
     assert_bitwise(got, want, f"group {group}")
     assert int(s1) == int(s2)
     assert bool((out[:, -3:] == 5.0).all())
+    cols = WIDE // kc.shape[1]
+    if table.shape[1] < cols:
+        wide = torch.full((table.shape[0], cols), -7, dtype=torch.int32, device="cuda")
+        wide[:, :table.shape[1]] = table
+        s2.zero_()
+        got = host(detlib.detdecode_attention_shared_f32(qd, kc, vc, wide, ld, H, group,
+                                                         out=out[:, :-3], dev_status=s2, **kw))
+        assert_bitwise(got, want, f"group {group} of a wide table")
+        if not (np.asarray(lens) > table.shape[1] * kc.shape[1]).any():
+            assert int(s1) == int(s2)
+        assert bool((out[:, -3:] == 5.0).all())
     return got
 
 
