@@ -11,12 +11,17 @@ whatever the batch, the page size and the order in which pages were taken.
 A step is library calls and copies on device buffers made once; nothing in it
 waits for the host, so it can be captured in a CUDA graph and replayed. Each
 layer is one page-table-sharing [pages, page_size, heads, head_dim] pair.
+
+Requests can go on from one another's tokens (fork) and then share the pages that
+are full; a step reads what neighbours share once. beam_search is made of that and
+the selection of the next beams.
 """
 from __future__ import annotations
 
 from typing import NamedTuple
 
 APPEND_ROWS = 1 << 20           # detkv_append_f32 takes so many rows in a call
+FORK_PAGES = 1 << 23            # detpages_fork knows so many pages
 
 
 class Next(NamedTuple):
@@ -31,16 +36,26 @@ class Next(NamedTuple):
     logp: object
 
 
+class Answers(NamedTuple):
+    """The answers that beam search found: of each prompt `beams` rows, the best first,
+    with their tokens (-1 past their length), lengths and scores (the sum of the tokens'
+    log probabilities; -inf, and length 0, where there are fewer)."""
+    ids: object
+    lens: object
+    scores: object
+
+
 class Decoder:
     """The cache, its page tables and a step's buffers for up to max_batch requests
     of up to max_len tokens (prompt and answer; whole pages, so up to the next
     multiple of page_size). model: the tensors of
     inputs.byte_lm_cfg2 or decoder_162m on the device. pages: the pages of
     page_size tokens that all requests share (default: enough for every request
-    to reach max_len)."""
+    to reach max_len). group: a step's attention reads what `group` consecutive requests
+    share once (1: each request for itself); the bits do not depend on it."""
 
     def __init__(self, model, max_batch, max_len, device, page_size=64, pages=None, top_k=1,
-                 eps=1e-6, theta=10000.0):
+                 eps=1e-6, theta=10000.0, group=1):
         import torch
 
         from bitwise_reproducible_fp32_gb300 import detlib as L
@@ -52,14 +67,17 @@ class Decoder:
             raise ValueError("max_len must be in 1..2^20")
         if page_size < 1 or (pages is not None and pages < 1):
             raise ValueError("page_size and pages must be at least 1")
+        if group < 1:
+            raise ValueError("group must be at least 1")
         if not 0 <= top_k <= min(32, model["vocab"]):
             raise ValueError(f"top_k must be in 0..{min(32, model['vocab'])}")
         self.model, self.B, self.max_len, self.device = model, max_batch, max_len, device
         self.page_size, self.top_k, self.eps, self.theta = page_size, top_k, eps, theta
+        self.group = min(group, max_batch)
         self.H, D, Fd, V = model["heads"], model["d"], model["dff"], model["vocab"]
         self.hd, B = D // model["heads"], max_batch
         width = -(-max_len // page_size)
-        pages = max_batch * width if pages is None else pages
+        self.pages = pages = max_batch * width if pages is None else pages
         f = lambda *s: torch.empty(s, dtype=torch.float32, device=device)  # noqa: E731
         i = lambda *s: torch.zeros(s, dtype=torch.int32, device=device)    # noqa: E731
         self.cache = [(f(pages, page_size, self.H, self.hd), f(pages, page_size, self.H, self.hd))
@@ -91,8 +109,16 @@ class Decoder:
         self.ws["gate_up"] = L.gemm_group_workspace(
             [dict(A=self.buf["h2"], B=wg["W_gate"], C=self.buf["gate"]),
              dict(A=self.buf["h2"], B=wg["W_up"], C=self.buf["up"])])
-        n = L.detdecode_attention_workspace_bytes(B, self.H, self.H, self.hd, width * page_size)
+        sizes = self.H, self.H, self.hd, width * page_size
+        n = (L.detdecode_attention_workspace_bytes(B, *sizes) if self.group == 1 else
+             L.detdecode_attention_shared_workspace_bytes(B, self.group, *sizes))
         self.ws["att"] = f((n + 3) // 4) if n else None
+        # what fork and compact write: the next table, and the pages to copy
+        self.next_table = i(max_batch, width)
+        self.src, self.dst, self.tokens = i(B), i(B), i(B)
+        self.itself = torch.arange(B, dtype=torch.int32, device=device)
+        self.forked = False             # whether requests may share pages
+        self.moved, self.moves = i(2, pages // 2), i(1)
 
     def _extend(self, new_tokens, rows, row_start, positions, slots):
         from bitwise_reproducible_fp32_gb300 import detlib as L
@@ -189,8 +215,12 @@ class Decoder:
             L.detgemm_f32(b["h"], w["W_qkv"], b["qkv"], workspace=self.ws["qkv"])
             q = L.detkv_append_f32(b["qkv"], slots, kc, vc, self.H, positions=pos,
                                    theta=self.theta, dev_status=self.status)
-            L.detdecode_attention_f32(q, kc, vc, self.table, self.lens, self.H, out=b["att"],
-                                      workspace=self.ws["att"], dev_status=self.status)
+            kw = dict(out=b["att"], workspace=self.ws["att"], dev_status=self.status)
+            if self.group == 1:
+                L.detdecode_attention_f32(q, kc, vc, self.table, self.lens, self.H, **kw)
+            else:
+                L.detdecode_attention_shared_f32(q, kc, vc, self.table, self.lens, self.H,
+                                                 self.group, **kw)
             L.detgemm_f32(b["att"], w["W_o"], b["o"], workspace=self.ws["o"])
             L.detadd_rmsnorm_f32(x, b["o"], w["g2"], self.eps, x=b["x1"], y=b["h2"],
                                  inv_rms=self.inv)
@@ -210,12 +240,57 @@ class Decoder:
     def release(self, done):
         """Gives back the pages of the requests with done[b] != 0 (max_batch int32 on
         the device); they are empty then."""
+        import torch
+
         from bitwise_reproducible_fp32_gb300 import detlib as L
         B = self.B
+        # pages may be shared (a captured call may be replayed after a later fork):
+        # everybody else goes on from itself, and a page that one of them holds stays
+        if self.forked or (torch.cuda.is_current_stream_capturing() and self.pages <= FORK_PAGES):
+            self._fork(torch.where(done != 0, self.none, self.itself))
+            return
         L.detpages_release(self.lens, done, self.table, self.free, self.count, self.page_size,
                            lens_out=self.after[:B], free_count_out=self.after[B:],
                            dev_status=self.status)
         self.state.copy_(self.after)
+
+    def _fork(self, parents):
+        from bitwise_reproducible_fp32_gb300 import detlib as L
+        B = self.B
+        L.detpages_fork(self.lens, parents, self.table, self.free, self.count, self.page_size,
+                        self.pages, table_out=self.next_table, lens_out=self.after[:B],
+                        free_count_out=self.after[B:], src=self.src, dst=self.dst,
+                        tokens=self.tokens, dev_status=self.status)
+        self.state.copy_(self.after)
+
+    def fork(self, parents):
+        """Every request goes on from request parents[b] (max_batch int32 on the device),
+        with its tokens; -1 leaves it empty. Requests of one parent share its full
+        pages and get copies of a partly filled one; the pages of requests that are
+        nobody's parent are given back. Can be captured, as a step can. A request that
+        finds no free page is left empty, and check() raises. For caches of up to 2^23
+        pages."""
+        from bitwise_reproducible_fp32_gb300 import detlib as L
+        if self.pages > FORK_PAGES:
+            raise ValueError(f"fork takes caches of up to {FORK_PAGES} pages")
+        self.forked = True
+        self._fork(parents)
+        self.table.copy_(self.next_table)
+        for kc, vc in self.cache:
+            L.detkv_copy_f32(kc, vc, self.src, self.dst, tokens=self.tokens,
+                             dev_status=self.status)
+
+    def compact(self):
+        """Moves the pages that requests hold to the lowest ids, so that the rest of the
+        cache is one run of free pages. Can be captured, as a step can."""
+        from bitwise_reproducible_fp32_gb300 import detlib as L
+        src, dst = self.moved
+        L.detpages_compact(self.lens, self.table, self.free, self.page_size, table_out=self.table,
+                           free_count_out=self.count, src=src, dst=dst, moves=self.moves,
+                           dev_status=self.status)
+        if self.pages > 1:
+            for kc, vc in self.cache:
+                L.detkv_copy_f32(kc, vc, src, dst, count=self.moves, dev_status=self.status)
 
     def check(self):
         """Raises if a call since the last check met a token outside the vocabulary,
@@ -248,3 +323,50 @@ class Decoder:
         self.release(active)
         self.check()
         return ids[:k], logp[:k]
+
+    def beam_search(self, prompts, new_tokens, beams, eos=-1, weights=None):
+        """The `beams` (up to top_k) most probable answers of up to new_tokens tokens to each
+        of up to max_batch // beams prompts, from an empty decoder, by beam search: each
+        step keeps the best of all beams' top_k continuations (detbeam_select_f32). eos:
+        the id that ends an answer. weights: floats on the device; answers are then
+        ranked by score * weights[length]. Nothing waits for the host until the end. The
+        requests are released after. Decoder(group=beams) reads what a prompt's beams share
+        once. Returns Answers (prompts x beams)."""
+        import torch
+
+        from bitwise_reproducible_fp32_gb300 import detlib as L
+        k, B = len(prompts), self.B
+        n = k * beams
+        if not 1 <= beams <= self.top_k:
+            raise ValueError(f"beams must be in 1..{self.top_k}, the decoder's top_k")
+        if not 1 <= n <= B or new_tokens < 1:
+            raise ValueError(f"1..{B // beams} prompts and at least one new token")
+        if max(map(len, prompts)) + new_tokens - 1 > self.table.size(1) * self.page_size:
+            raise ValueError("the prompts leave no room for so many tokens")
+        i32 = dict(dtype=torch.int32, device=self.device)
+        hist = [torch.full((n, new_tokens), -1, **i32) for _ in range(2)]
+        parents, tok = torch.arange(B, **i32), torch.zeros(B, **i32)
+        active = torch.zeros(B, **i32)
+        nx = self.prefill([r * beams for r in range(k)], prompts)
+        # first each prompt is one beam
+        b = L.detbeam_select_f32(torch.zeros((k, 1), dtype=torch.float32, device=self.device),
+                                 nx.ids, nx.top_logp, beams, eos=eos, lens=torch.zeros(k, **i32),
+                                 weights=weights, hist=hist[1][:k], hist_out=hist[0],
+                                 dev_status=self.status)
+        for t in range(1, new_tokens):
+            # the prompts' requests are beams apart
+            parents[:n] = b.forks if t > 1 else torch.where(b.forks < 0, -1, b.forks * beams)
+            self.fork(parents)
+            torch.clamp(b.tokens, min=0, out=tok[:n])
+            active[:n] = 1 - b.finished
+            nx = self.step(tok, active)
+            b = L.detbeam_select_f32(b.scores, nx.ids[:n], nx.top_logp[:n], beams, eos=eos,
+                                     finished=b.finished, lens=b.lens, weights=weights,
+                                     hist=hist[(t - 1) % 2], hist_out=hist[t % 2],
+                                     dev_status=self.status)
+        active[:n] = 1
+        self.release(active)
+        self.check()
+        col = torch.arange(new_tokens, **i32)
+        ids = torch.where(col < b.lens[:, None], b.hist, -1)
+        return Answers(ids.view(k, beams, new_tokens), b.lens.view(k, beams), b.scores)

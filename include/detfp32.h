@@ -735,8 +735,10 @@ det_status detpages_extend(const det_profile_v1 *prof, int64_t batch, int64_t pa
  * count after. The table is not changed. A done request with a length outside
  * its table row ORs 1 into *dev_status; one whose pages, after those of the done
  * requests before it, do not fit the free list's capacity ORs 2; both keep their
- * length. A *free_count outside 0..capacity counts as 0 and ORs 1. Sizes and
- * errors as detpages_extend. */
+ * length. A *free_count outside 0..capacity counts as 0 and ORs 1. Requests that
+ * share pages (detpages_fork) are given back by that call, with parents of -1: this
+ * one would give a shared page back once for each. Sizes and errors as
+ * detpages_extend. */
 det_status detpages_release(const det_profile_v1 *prof, int64_t batch, int64_t page_size,
                             const int32_t *lens, const int32_t *done, const int32_t *table,
                             int64_t max_pages, int64_t ldt, int32_t *free_pages,
