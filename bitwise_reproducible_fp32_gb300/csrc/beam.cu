@@ -209,12 +209,13 @@ cudaError_t launch_beam_select(int64_t requests, const det_beams &in, const det_
         auto al16 = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
         A.vec = al16(A.hist) && al16(A.hist_out) && A.ldh % 4 == 0 && A.ldho % 4 == 0;
         warps = std::max(warps, A.wout);
-        A.part = 1024;
+        // 1024 columns and more a CTA, and no more CTAs than about one wave: each makes the
+        // selection again (512 requests of 16 beams and 2048 tokens: 30 us in two parts, XX
+        // in one)
+        const int64_t wave = int64_t(sm_count_current_device()) * 4;
+        parts = std::max<int64_t>(1, std::min((cols + 1023) / 1024, wave / requests));
+        A.part = ((cols + parts - 1) / parts + 127) / 128 * 128;
         parts = std::max<int64_t>(1, (cols + A.part - 1) / A.part);
-        if (parts > 65535) {
-            A.part = ((cols + 65534) / 65535 + 127) / 128 * 128;
-            parts = (cols + A.part - 1) / A.part;
-        }
     }
     beam_select_kernel<<<dim3(unsigned(requests), unsigned(parts)), unsigned(warps * 32), 0, s>>>(
         A);

@@ -910,9 +910,9 @@ def _gen_stream(stream, dev):
 def _gen_empty(shape, like, stream, dtype=None):
     """A tensor for this call's outputs, allocated for the stream it runs on."""
     if stream is None:
-        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+        return like.new_empty(*shape) if dtype is None else like.new_empty(*shape, dtype=dtype)
     with _N.stream_scope(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(*shape, dtype=dtype)
 
 
 def _at(t, name, dtype, dev):
@@ -938,16 +938,17 @@ def _mat(t, name, dtype, dev, rows=None, cols=None):
     """(pointer, row stride) as _at, for a 2-D tensor with contiguous rows, `rows`
     of them of at least `cols`."""
     p = _at(t, name, dtype, dev)
-    if t.dim() != 2:
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
-    n, m = t.size(0), t.size(1)
-    if m > 1 and n > 0 and t.stride(1) != 1:
+    n, m = shape
+    if m > 1 and n > 0 and strides[1] != 1:
         raise ValueError(f"{name} must have contiguous rows")
     if (rows is not None and n != rows) or (cols is not None and m < cols):
         raise ValueError(f"{name} must be {rows if rows is not None else n} rows of at least "
                          f"{cols} columns, got {n} x {m}")
     # a single row has no stride to speak of: its length
-    return p, (t.stride(0) if n > 1 else max(m, 1))
+    return p, (strides[0] if n > 1 else m or 1)
 
 
 def _word(t, dev):
@@ -1195,7 +1196,7 @@ def _decode(q, k_cache, v_cache, table, kv_lens, heads, group, scale, out, works
     d = c.head_dim
     width = heads * d
     qp, ldq = _mat(q, "q", _N.f32, dev, None, width)
-    batch = q.size(0)
+    batch = q.shape[0]
     tp, ldt = _mat(table, "table", _N.i32, dev, batch)
     lp = _vec(kv_lens, "kv_lens", _N.i32, dev, batch)
     if out is None:
@@ -1205,7 +1206,7 @@ def _decode(q, k_cache, v_cache, table, kv_lens, heads, group, scale, out, works
         op, ldo = _mat(out, "out", _N.f32, dev, batch, width)
     if scale is None:
         scale = 1.0 / float(d) ** 0.5
-    max_pages = table.size(1)
+    max_pages = table.shape[1]
     wp, wn = None, 0
     if workspace is not None:
         wp, wn = _vec(workspace, "workspace", _N.f32, dev), workspace.numel() * 4
@@ -1257,14 +1258,14 @@ def detbeam_select_f32(scores, top_ids, top_logp, beams, eos=-1, finished=None, 
     lib, prof, dev = _gen_begin(profile, scores, "scores")
     f32, i32 = _N.f32, _N.i32
     sp, lds = _mat(scores, "scores", f32, dev)
-    requests, old = scores.size(0), scores.size(1)
+    requests, old = scores.shape
     if requests > 1 and lds != old:
         raise ValueError("scores must be contiguous")
     rows, new = requests * old, requests * beams
     ip, ldi = _mat(top_ids, "top_ids", i32, dev, rows)
-    k = top_ids.size(1)
-    tp, ldt = _mat(top_logp, "top_logp", f32, dev, rows, k)
-    if top_logp.size(1) != k or (rows > 1 and (ldi != k or ldt != k)):
+    tp, ldt = _mat(top_logp, "top_logp", f32, dev, rows)
+    k = top_ids.shape[1]
+    if top_logp.shape[1] != k or (rows > 1 and (ldi != k or ldt != k)):
         raise ValueError("top_ids and top_logp must be contiguous rows of one length")
     fp = None if finished is None else _vec(finished, "finished", i32, dev, rows)
     lp = None if lens is None else _vec(lens, "lens", i32, dev, rows)
@@ -1278,26 +1279,28 @@ def detbeam_select_f32(scores, top_ids, top_logp, beams, eos=-1, finished=None, 
     hp, ldh, hop, ldho, cols = None, 0, None, 0, 0
     if hist is not None:
         hp, ldh = _mat(hist, "hist", i32, dev, rows)
-        cols = hist.size(1)
+        cols = hist.shape[1]
         if cols < 1:
             raise ValueError("hist must have at least one column")
         if hist_out is None:
             hist_out = _gen_empty((new, cols), scores, stream, i32)
         hop, ldho = _mat(hist_out, "hist_out", i32, dev, new, cols)
-        if hist_out.size(1) != cols:
+        if hist_out.shape[1] != cols:
             raise ValueError(f"hist_out must have {cols} columns")
     elif hist_out is not None:
         raise ValueError("hist_out needs hist")
     if scores_out is None:
         scores_out = _gen_empty((requests, beams), scores, stream)
-    sop, lds = _mat(scores_out, "scores_out", f32, dev, requests, beams)
-    if scores_out.size(1) != beams or (requests > 1 and lds != beams):
-        raise ValueError(f"scores_out must be contiguous rows of {beams}")
+        sop = scores_out.data_ptr()
+    else:
+        sop, lds = _mat(scores_out, "scores_out", f32, dev, requests, beams)
+        if scores_out.shape[1] != beams or (requests > 1 and lds != beams):
+            raise ValueError(f"scores_out must be contiguous rows of {beams}")
     parts = None
     if (tokens is None and parents is None and forks is None and finished_out is None
             and lens_out is None):
         # one allocation for the whole numbers, taken apart once the launch is on its way
-        parts = _gen_empty(((4 if lens is None else 5) * new,), scores, stream, i32)
+        parts = _gen_empty(((4 if lens is None else 5) * new,), top_ids, stream)
         p = parts.data_ptr()
         at = [p, p + 4 * new, p + 8 * new, p + 12 * new, None if lens is None else p + 16 * new]
     else:
@@ -1321,9 +1324,11 @@ def detbeam_select_f32(scores, top_ids, top_logp, beams, eos=-1, finished=None, 
     if st:
         _check("detbeam_select_f32", st)
     if parts is not None:
-        parts = parts.unsafe_split(new) if new else [parts] * 5
-        tokens, parents, forks, finished_out = parts[:4]
-        lens_out = None if lens is None else parts[4]
+        if lens is None:
+            tokens, parents, forks, finished_out = parts.unsafe_split_with_sizes((new,) * 4)
+        else:
+            tokens, parents, forks, finished_out, lens_out = parts.unsafe_split_with_sizes(
+                (new,) * 5)
     return Beams(scores_out, tokens, parents, forks, finished_out, lens_out, hist_out)
 
 
@@ -1346,7 +1351,7 @@ def detpages_fork(lens, parents, table, free_pages, free_count, page_size, num_p
     pp = _vec(parents, "parents", i32, dev)
     new = parents.numel()
     tp, ldt = _mat(table, "table", i32, dev, batch)
-    width = table.size(1)
+    width = table.shape[1]
     fp = _vec(free_pages, "free_pages", i32, dev)
     cp = _vec(free_count, "free_count", i32, dev, 1)
     if table_out is None:
@@ -1397,25 +1402,31 @@ def detpages_compact(lens, table, free_pages, page_size, table_out=None, free_co
     lp = _vec(lens, "lens", i32, dev)
     batch = lens.numel()
     tp, ldt = _mat(table, "table", i32, dev, batch)
-    width = table.size(1)
+    width = table.shape[1]
     fp = _vec(free_pages, "free_pages", i32, dev)
     pages = free_pages.numel()
     if table_out is None:
         table_out = _gen_empty((batch, width), lens, stream)
     op, ldo = _mat(table_out, "table_out", i32, dev, batch, width)
+    half = pages // 2
     if src is None:
-        src = _gen_empty((pages // 2,), lens, stream)
+        src = _gen_empty((half,), lens, stream)
     if dst is None:
-        dst = _gen_empty((pages // 2,), lens, stream)
+        dst = _gen_empty((half,), lens, stream)
+    sp, half = _vec(src, "src", i32, dev), src.numel()
+    dp = _vec(dst, "dst", i32, dev, half)
     if free_count_out is None:
         free_count_out = _gen_empty((1,), lens, stream)
+        cp = free_count_out.data_ptr()
+    else:
+        cp = _vec(free_count_out, "free_count_out", i32, dev, 1)
     if moves is None:
         moves = _gen_empty((1,), lens, stream)
-    st = lib.detpages_compact(prof, batch, page_size, pages, lp, tp, width, ldt, op, ldo, fp,
-                              _vec(free_count_out, "free_count_out", i32, dev, 1),
-                              _vec(src, "src", i32, dev), _vec(dst, "dst", i32, dev, src.numel()),
-                              src.numel(), _vec(moves, "moves", i32, dev, 1),
-                              _word(dev_status, dev), _gen_stream(stream, dev))
+        mp = moves.data_ptr()
+    else:
+        mp = _vec(moves, "moves", i32, dev, 1)
+    st = lib.detpages_compact(prof, batch, page_size, pages, lp, tp, width, ldt, op, ldo, fp, cp,
+                              sp, dp, half, mp, _word(dev_status, dev), _gen_stream(stream, dev))
     if st:
         _check("detpages_compact", st)
     return table_out, free_count_out, moves, src, dst
