@@ -210,7 +210,7 @@ cudaError_t launch_beam_select(int64_t requests, const det_beams &in, const det_
         A.vec = al16(A.hist) && al16(A.hist_out) && A.ldh % 4 == 0 && A.ldho % 4 == 0;
         warps = std::max(warps, A.wout);
         // 1024 columns and more a CTA, and no more CTAs than about one wave: each makes the
-        // selection again (512 requests of 16 beams and 2048 tokens: 30 us in two parts, XX
+        // selection again (512 requests of 16 beams and 2048 tokens: 30 us in two parts, 26
         // in one)
         const int64_t wave = int64_t(sm_count_current_device()) * 4;
         parts = std::max<int64_t>(1, std::min((cols + 1023) / 1024, wave / requests));

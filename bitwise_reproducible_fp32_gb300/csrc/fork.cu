@@ -167,13 +167,8 @@ __device__ __forceinline__ void load_entries(const int32_t *p, int n, const int3
     }
 }
 
-// Every CTA's value to every CTA: the sum before this one's, and of all. The
-// cluster meets once; `slots` is not reused before it meets again.
-__device__ __forceinline__ void exchange(cg::cluster_group &cluster, int *slots, int value,
-                                         int *before, int *total) {
-    const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
-    if (int(threadIdx.x) < C) *cluster.map_shared_rank(slots + rank, threadIdx.x) = value;
-    cluster.sync();
+// The sum of the CTAs' values before this one's, and of all.
+__device__ __forceinline__ void add_up(const int *slots, int C, int rank, int *before, int *total) {
     int b = 0, t = 0;
     for (int r = 0; r < C; ++r) {
         b += r < rank ? slots[r] : 0;
@@ -181,6 +176,15 @@ __device__ __forceinline__ void exchange(cg::cluster_group &cluster, int *slots,
     }
     *before = b;
     *total = t;
+}
+// Every CTA's value to every CTA, and add_up. The cluster meets once; `slots` is not
+// reused before it meets again.
+__device__ __forceinline__ void exchange(cg::cluster_group &cluster, int *slots, int value,
+                                         int *before, int *total) {
+    const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+    if (int(threadIdx.x) < C) *cluster.map_shared_rank(slots + rank, threadIdx.x) = value;
+    cluster.sync();
+    add_up(slots, C, rank, before, total);
 }
 
 struct ForkArgs {
@@ -199,11 +203,14 @@ struct ForkArgs {
     bool apart;               // the new table is written by a launch of its own
 };
 
-// The new table, from the rows' lengths and pages of their own: warp w of `all`.
-__device__ __forceinline__ void fork_rows(const ForkArgs &A, int w, int all) {
+// The new table: warp w of `all`. row(r, own): the new row's pages, and the page that it
+// has in the place of the last one (-1: none).
+template <class Row>
+__device__ __forceinline__ void fork_rows(const ForkArgs &A, int w, int all, Row row) {
     for (Segments at(A.batch_out, A.max_pages, w, all); at.more(); at.next()) {
-        const int r = at.row, own = __ldcg(A.dst + r);
-        const int64_t pages = (__ldcg(A.lens_out + r) + A.page_size - 1) / A.page_size;
+        const int r = at.row;
+        int own;
+        const int64_t pages = row(r, own);
         const int n = at.left(pages);
         if (n <= 0) continue;
         const int32_t *from = A.table + A.parents[r] * A.ldt + at.first();
@@ -248,6 +255,8 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs A) 
         pages[i] = int(pages_of(len));
     }
     __syncthreads();
+    // the thread's new rows
+    const int per = (A.batch_out + kThreads - 1) / kThreads, r0 = tid * per;
     for (int r = tid; r < A.batch_out; r += kThreads) {
         const int p = A.parents[r];
         if (p >= 0 && p < A.batch) atomicMin(first + p, r);
@@ -257,6 +266,28 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs A) 
     int orphan = 0;
     for (int i = tid; i < A.batch; i += kThreads) orphan |= first[i] == INT32_MAX && pages[i] > 0;
     orphan = __syncthreads_or(orphan);
+    // of new rows r0.. the partly filled page that each shares with an earlier one, or -1;
+    // where a thread has one row it is asked for here, and used in 3
+    auto shared_pages = [&](auto rows, int *page) {
+        constexpr int N = decltype(rows)::value;
+        int len[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            page[k] = k < per && r0 + k < A.batch_out ? A.parents[r0 + k] : -1;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int p = page[k];
+            const bool shares = p >= 0 && p < A.batch && first[p] != r0 + k;
+            len[k] = shares ? A.lens[p] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int64_t n = pages_of(len[k]);
+            page[k] = n > 0 && len[k] % ps != 0 ? A.table[page[k] * A.ldt + n - 1] : -1;
+        }
+    };
+    int early = -1;
+    if (per == 1) shared_pages(std::integral_constant<int, 1>(), &early);
     if (!A.near) cluster.sync();        // every CTA's bits are clear
     // 1. the pages of rows that have no child, then without those of rows that have one;
     // an entry that is the one above it is that row's to mark, or kept by it
@@ -308,24 +339,13 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs A) 
     }
     // 3. a page for every child that shares a partly filled one with an earlier child
     allow_dependents();
-    const int per = (A.batch_out + kThreads - 1) / kThreads, r0 = tid * per;
-    int need = 0;
+    int need = 0, last[kPerThread];     // that page, then the page of their own
     unsigned wants = 0;
-    int last[kPerThread];               // the parent, its last page, the page of its own
+    if (per == 1) {
 #pragma unroll
-    for (int k = 0; k < kPerThread; ++k)
-        last[k] = k < per && r0 + k < A.batch_out ? A.parents[r0 + k] : -1;
-    int len_of[kPerThread];
-#pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-        const int p = last[k];
-        const bool shares = p >= 0 && p < A.batch && first[p] != r0 + k;
-        len_of[k] = shares ? A.lens[p] : 0;
-    }
-#pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-        const int64_t n = pages_of(len_of[k]);
-        last[k] = n > 0 && len_of[k] % ps != 0 ? A.table[last[k] * A.ldt + n - 1] : -1;
+        for (int k = 0; k < kPerThread; ++k) last[k] = k == 0 ? early : -1;
+    } else {
+        shared_pages(std::integral_constant<int, kPerThread>(), last);
     }
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k)
@@ -374,10 +394,12 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const ForkArgs A) 
         A.tokens[r] = own ? int(len % ps) : 0;
     }
     // 4. the new table
-    if (!A.apart) {
-        cluster.sync();                 // the rows' lengths and pages are there
-        fork_rows(A, rank * kWarps + warp, C * kWarps);
-    }
+    if (!A.apart)
+        fork_rows(A, rank * kWarps + warp, C * kWarps, [&](int r, int &own) {
+            const int p = A.parents[r];
+            own = fresh[r];
+            return p >= 0 && p < A.batch && own != -2 ? pages_of(A.lens[p]) : int64_t(0);
+        });
     if (rank == 0 && tid == 0)
         *A.free_count_out = int(have - min(int64_t(wanted), have));
     if (A.dev_status) {
@@ -391,7 +413,11 @@ constexpr int kRowWarps = kRowThreads / 32;
 
 __global__ void __launch_bounds__(kRowThreads) pages_fork_rows_kernel(const ForkArgs A) {
     grid_dependency_wait();
-    fork_rows(A, blockIdx.x * kRowWarps + (threadIdx.x >> 5), gridDim.x * kRowWarps);
+    fork_rows(A, blockIdx.x * kRowWarps + (threadIdx.x >> 5), gridDim.x * kRowWarps,
+              [&](int r, int &own) {
+                  own = __ldcg(A.dst + r);
+                  return (__ldcg(A.lens_out + r) + A.page_size - 1) / A.page_size;
+              });
 }
 
 struct CompactArgs {
@@ -500,8 +526,13 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const CompactAr
         nh += __popc(holes(w));
     }
     int am = block_scan(nm, warp_sums, &cm), ah = block_scan(nh, warp_sums, &ch);
-    exchange(cluster, slots[1], cm, &bm, &total);
-    exchange(cluster, slots[2], ch, &bh, &same);
+    if (tid < C) {
+        *cluster.map_shared_rank(slots[1] + rank, tid) = cm;
+        *cluster.map_shared_rank(slots[2] + rank, tid) = ch;
+    }
+    cluster.sync();
+    add_up(slots[1], C, rank, &bm, &total);
+    add_up(slots[2], C, rank, &bh, &same);
     for (int w = w0; w < w1; ++w) {
         for (uint32_t bits = moving(w); bits; bits &= bits - 1)
             A.src[bm + am++] = base + w * 32 + __ffs(int(bits)) - 1;
