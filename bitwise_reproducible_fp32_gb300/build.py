@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libdetfp32.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["gemm.cu", "gemm_n64.cu", "gemm_m128.cu", "rowops.cu", "rmsbwd.cu", "shardsum.cu", "block.cu",
            "adamw.cu", "rotary.cu", "pages.cu", "decode.cu", "decode_shared.cu",
-           "decode_few.cu", "logprob.cu", "beam.cu", "fork.cu", "api.cu"]
+           "decode_few.cu", "decode_group.cu", "logprob.cu", "beam.cu", "fork.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NUMERICS = ["-fmad=false", "-ftz=false", "-prec-div=true", "-prec-sqrt=true"]
 

@@ -1385,6 +1385,8 @@ DET_API det_status det_watchdog_status(int32_t *code, int clear) {
     if (e == cudaSuccess) e = shared_decode_watchdog(&c8, clear);
     unsigned int c9 = 0;
     if (e == cudaSuccess) e = few_decode_watchdog(&c9, clear);
-    *code = int32_t(c | c2 | c3 | c5 | c6 | c7 | c8 | c9);
+    unsigned int c10 = 0;
+    if (e == cudaSuccess) e = group_decode_watchdog(&c10, clear);
+    *code = int32_t(c | c2 | c3 | c5 | c6 | c7 | c8 | c9 | c10);
     return from_cuda(e);
 }

@@ -1,5 +1,5 @@
-// decode_few.cu -- units of decode_shared.cu with at most 8 query rows a key-value head (a
-// request's own tokens, or a small group's shared ones), for sm_103a.
+// decode_few.cu -- the tokens that a request of decode_shared.cu has to itself, with at
+// most 8 query rows a key-value head, for sm_103a.
 //
 // The same formulas and bits; a key or value takes at most 16 multiply-adds, so HBM
 // bounds it. As in decode.cu a warp streams pieces of 64 tokens x 32 dimensions through
@@ -18,127 +18,20 @@ __device__ unsigned int g_few_watchdog;
 
 namespace {
 
-constexpr int kPieceBytes = kTile * 128;
-constexpr int kMostStages = 3;
 constexpr int kFewCtas = 2;               // an SM's
 
-// A warp's ring of pieces.
-template <Loader LOAD>
-struct Ring {
-    const SharedArgs &A;
-    const CUtensorMap *map;
-    const float *cache;
-    uint32_t slots, bars;
-    int stages, slot_in = 0, slot = 0;
-    uint32_t phase = 0;
-    bool stuck = false;
-    int id = 0;                           // of the lane's box
-    int64_t off[2];                       // of tokens lane, lane + 32
-
-    __device__ __forceinline__ Ring(const SharedArgs &a, const CUtensorMap *m, const float *c,
-                                    uint32_t s, uint32_t b, int n)
-        : A(a), map(m), cache(c), slots(s), bars(b), stages(n) {}
-    // where the piece of `live` tokens from t on is; ahead of fetch
-    __device__ __forceinline__ void look_up(const int32_t *pages, int t, int live) {
-        const int lane = threadIdx.x & 31;
-        if constexpr (LOAD == kTma) {
-            if (lane * A.box < live) id = pages[page_of(A, t + lane * A.box)];
-        } else {
-            if (lane < live) off[0] = offset_of(A, pages, t + lane);
-            if (lane + 32 < live) off[1] = offset_of(A, pages, t + lane + 32);
-        }
-    }
-    __device__ __forceinline__ void fetch(int kv, int sl, int t, int live) {
-        const int lane = threadIdx.x & 31;
-        const uint32_t dst = slots + slot_in * kPieceBytes;
-        if constexpr (LOAD == kTma) {
-            const uint32_t bar = bars + 8 * slot_in;
-            const int boxes = (live + A.box - 1) / A.box;
-            if (lane == 0) mbar_arrive_expect_tx(bar, boxes * A.box * 128);
-            __syncwarp();
-            if (lane < boxes) {
-                const int at = t + lane * A.box;
-                tma_load_4d(dst + lane * A.box * 128, map, 32 * sl, kv,
-                            int(unsigned(at) - page_of(A, at) * A.page_size), id, bar);
-            }
-        } else if constexpr (LOAD == kCopy16) {
-            const int col = lane & 7, r0 = lane >> 3;
-            const bool in = 4 * col < A.d - 32 * sl;
-            const float *src = cache + kv * A.head_stride + 32 * sl + 4 * col;
-#pragma unroll
-            for (int i = 0; i < kTile / 4; ++i) {
-                const int r = 4 * i + r0;
-                const int64_t at = __shfl_sync(0xffffffffu, off[i >> 3], r & 31);
-                if (in && r < live) cp_async<16>(dst + r * 128 + ((col ^ (r & 7)) << 4), src + at);
-            }
-        } else {
-            const bool in = lane < A.d - 32 * sl;
-            const float *src = cache + kv * A.head_stride + 32 * sl + lane;
-#pragma unroll 8
-            for (int r = 0; r < kTile; ++r) {
-                const int64_t at = __shfl_sync(0xffffffffu, r < 32 ? off[0] : off[1], r & 31);
-                if (in && r < live)
-                    cp_async<4>(dst + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | (lane & 3) << 2),
-                                src + at);
-            }
-        }
-        slot_in = slot_in + 1 == stages ? 0 : slot_in + 1;
-    }
-    __device__ __forceinline__ void wait() {
-        if constexpr (LOAD == kTma) {
-            if (!stuck)
-                stuck = __any_sync(0xffffffffu, !mbar_wait_bounded(bars + 8 * slot, phase));
-        } else {
-            if (stages == 3) cp_wait<1>(); else cp_wait<0>();
-        }
-        __syncwarp();
-    }
-    // the piece that was waited for
-    __device__ __forceinline__ uint32_t piece() {
-        const uint32_t p = slots + slot * kPieceBytes;
-        if (++slot == stages) {
-            slot = 0;
-            phase ^= 1;
-        }
-        return p;
-    }
-    // at the end: the copies in flight land
-    __device__ __forceinline__ void drain() {
-        if constexpr (LOAD != kTma) {
-            cp_wait<0>();
-        } else if (stuck) {
-            for (int i = 0; i < stages; ++i) {
-                (void)mbar_wait_bounded(bars + 8 * slot, phase);
-                if (++slot == stages) {
-                    slot = 0;
-                    phase ^= 1;
-                }
-            }
-            if ((threadIdx.x & 31) == 0) atomicOr(&g_few_watchdog, kWatchdogDecode);
-        }
-    }
-};
-
-template <Loader LOAD>
-__device__ __forceinline__ void init_bars(uint64_t *bars) {
-    if (LOAD == kTma && threadIdx.x == 0) {
-        for (int i = 0; i < kWarps * kMostStages; ++i) mbar_init(smem_u32(bars + i), 1);
-        fence_mbar_init();
-    }
-}
-
 // NH: the rows the registers hold, of which the unit has at most NH.
-template <int NH, Loader LOAD, bool OWN>
+template <int NH, Loader LOAD>
 __global__ void __launch_bounds__(kThreads, kFewCtas)
     few_scores_kernel(const SharedArgs A, const __grid_constant__ CUtensorMap kmap, int stages) {
-    constexpr int CUT = OWN ? kOwnTiles : kSharedTiles;
+    constexpr int CUT = kOwnTiles;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ Share share[kWarps];
     __shared__ uint64_t full[kWarps][kMostStages];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int d = A.d, nsl = (d + 31) / 32, live_rows = rows_of<CUT>(A), ldq = nsl * 32;
     init_bars<LOAD>(&full[0][0]);
-    Beside<OWN> beside;
+    Beside<true> beside;
     shares<CUT, kWarps>(A, A.kv_heads, blockIdx.x, gridDim.x, gridDim.x * kWarps, share);
     const int64_t items = share[warp].items;
     if (items <= 0) return;
@@ -276,20 +169,20 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
         advance<CUT>(A, A.kv_heads, it);
     }
     flush();
-    ring.drain();
+    ring.drain(&g_few_watchdog);
 }
 
-template <int NH, Loader LOAD, bool OWN>
+template <int NH, Loader LOAD>
 __global__ void __launch_bounds__(kThreads, kFewCtas)
     few_partials_kernel(const SharedArgs A, const __grid_constant__ CUtensorMap vmap, int stages) {
-    constexpr int CUT = OWN ? kOwn : kShared;
+    constexpr int CUT = kOwn;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ Share share[kWarps];
     __shared__ uint64_t full[kWarps][kMostStages];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int d = A.d, nsl = (d + 31) / 32, live_rows = rows_of<CUT>(A), mul = A.kv_heads * nsl;
     init_bars<LOAD>(&full[0][0]);
-    Beside<OWN> beside;
+    Beside<true> beside;
     shares<CUT, kWarps>(A, mul, blockIdx.x, gridDim.x, gridDim.x * kWarps, share);
     const int64_t items = share[warp].items;
     if (items <= 0) return;
@@ -428,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
                 if (mine[h] >= 0)
                     out[mine[h] * A.ldpart * d] = ring.stuck ? __uint_as_float(0x7fc00000u) : acc[h];
     }
-    ring.drain();
+    ring.drain(&g_few_watchdog);
 }
 
 template <class K>
@@ -449,53 +342,38 @@ cudaError_t run_few(K kern, int64_t items, size_t row_bytes, const SharedArgs &A
                             stages);
 }
 
-template <int NH, bool OWN>
+template <int NH>
 cudaError_t scores_of(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
     const size_t rows = size_t(NH) * ((A.d + 31) / 32 * 32) * 4;
     const int64_t items = most * (kKChunk / kTile) * A.kv_heads;
-    return map      ? run_few(few_scores_kernel<NH, kTma, OWN>, items, rows, A, map, s)
-           : A.wide ? run_few(few_scores_kernel<NH, kCopy16, OWN>, items, rows, A, map, s)
-                    : run_few(few_scores_kernel<NH, kCopy4, OWN>, items, rows, A, map, s);
+    return map      ? run_few(few_scores_kernel<NH, kTma>, items, rows, A, map, s)
+           : A.wide ? run_few(few_scores_kernel<NH, kCopy16>, items, rows, A, map, s)
+                    : run_few(few_scores_kernel<NH, kCopy4>, items, rows, A, map, s);
 }
-template <int NH, bool OWN>
+template <int NH>
 cudaError_t partials_of(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
     const size_t rows = size_t(NH) * kTile * 4;
     const int64_t items = most * A.kv_heads * ((A.d + 31) / 32);
-    return map      ? run_few(few_partials_kernel<NH, kTma, OWN>, items, rows, A, map, s)
-           : A.wide ? run_few(few_partials_kernel<NH, kCopy16, OWN>, items, rows, A, map, s)
-                    : run_few(few_partials_kernel<NH, kCopy4, OWN>, items, rows, A, map, s);
-}
-template <bool OWN>
-cudaError_t scores_by_rows(const SharedArgs &A, const CUtensorMap *map, int64_t most, cudaStream_t s) {
-    const int64_t rows = OWN ? A.per_kv : A.rows;
-    if constexpr (OWN) {       // two rows are not worth reading together
-        if (rows == 1) return scores_of<1, OWN>(A, map, most, s);
-        if (rows == 2) return scores_of<2, OWN>(A, map, most, s);
-    }
-    return rows <= 4 ? scores_of<4, OWN>(A, map, most, s)
-                     : scores_of<kFewRows, OWN>(A, map, most, s);
-}
-template <bool OWN>
-cudaError_t partials_by_rows(const SharedArgs &A, const CUtensorMap *map, int64_t most,
-                             cudaStream_t s) {
-    const int64_t rows = OWN ? A.per_kv : A.rows;
-    if constexpr (OWN) {       // two rows are not worth reading together
-        if (rows == 1) return partials_of<1, OWN>(A, map, most, s);
-        if (rows == 2) return partials_of<2, OWN>(A, map, most, s);
-    }
-    return rows <= 4 ? partials_of<4, OWN>(A, map, most, s)
-                     : partials_of<kFewRows, OWN>(A, map, most, s);
+    return map      ? run_few(few_partials_kernel<NH, kTma>, items, rows, A, map, s)
+           : A.wide ? run_few(few_partials_kernel<NH, kCopy16>, items, rows, A, map, s)
+                    : run_few(few_partials_kernel<NH, kCopy4>, items, rows, A, map, s);
 }
 
 }  // namespace
 
-cudaError_t launch_few_scores(bool own, const SharedArgs &A, const CUtensorMap *map, int64_t most,
+cudaError_t launch_few_scores(const SharedArgs &A, const CUtensorMap *map, int64_t most,
                               cudaStream_t s) {
-    return own ? scores_by_rows<true>(A, map, most, s) : scores_by_rows<false>(A, map, most, s);
+    return A.per_kv == 1   ? scores_of<1>(A, map, most, s)
+           : A.per_kv == 2 ? scores_of<2>(A, map, most, s)
+           : A.per_kv <= 4 ? scores_of<4>(A, map, most, s)
+                           : scores_of<kFewRows>(A, map, most, s);
 }
-cudaError_t launch_few_partials(bool own, const SharedArgs &A, const CUtensorMap *map, int64_t most,
+cudaError_t launch_few_partials(const SharedArgs &A, const CUtensorMap *map, int64_t most,
                                 cudaStream_t s) {
-    return own ? partials_by_rows<true>(A, map, most, s) : partials_by_rows<false>(A, map, most, s);
+    return A.per_kv == 1   ? partials_of<1>(A, map, most, s)
+           : A.per_kv == 2 ? partials_of<2>(A, map, most, s)
+           : A.per_kv <= 4 ? partials_of<4>(A, map, most, s)
+                           : partials_of<kFewRows>(A, map, most, s);
 }
 
 cudaError_t few_decode_watchdog(unsigned int *code, int clear) {

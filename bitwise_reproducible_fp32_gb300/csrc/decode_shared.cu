@@ -681,28 +681,42 @@ __global__ void __launch_bounds__(kThreads) shared_join_kernel(const SharedArgs 
 // ---------------------------------------------------------------- host
 constexpr size_t kSliceBytes = size_t(1) << 30;     // scores and partials of a round of heads
 
-// Whether the requests are read together, or each for itself by decode.cu: one launch of
-// 18 us and more, its keys and values from L2 at 9 TB/s (with 4 and 8 heads of a key-value
-// head 1.5 and 3 times as long for their multiply-adds), against seven launches of 45 us and
-// more, each key and value once at 4.2 TB/s or the multiply-adds at 20 TFLOP/s. Rows are
-// taken as long as the table is wide, so only a gain of a quarter counts. Measured, for
-// itself / together, us: 12 heads of 64, 16 groups of 4 of 700..1900 tokens 74 / 79, of 8
-// of 1100..1500 139 / 115, of 4500..6000 437 / 212; one group of 32 of 1500 50 / 65, of
-// 6000 150 / 75; 16 groups of 2 of 6000 163 / 153; 4 groups of 4 with 4 query heads a
-// key-value head of 1500 46 / 68, of 6000 128 / 90.
-bool read_together(int64_t batch, int64_t group, int64_t heads, int64_t kv_heads, int64_t d,
-                   int64_t max_len) {
-    if (group < 2 || max_len <= 2 * kKChunk) return false;
-    const double token = 8.0 * double(kv_heads * d) * double(max_len);      // of one request
+// How requests are read: each for itself (decode.cu), in small groups (decode_group.cu) or
+// many together (this file), by an estimate of the three with rows as long as the table
+// is wide; as they are shorter, only a gain of a tenth, or a quarter for this file's
+// longer chain of launches, counts.
+//  - each for itself: 18 us and the keys and values of all from L2 at 9 TB/s (with 4 and 8
+//    heads of a key-value head 1.5 and 3 times as long for their multiply-adds);
+//  - in groups: 34 us and each key and value once, with 200 tokens of its own a request, at
+//    5.8 TB/s or 18 GB/s a CTA;
+//  - together: 45 us and each once at 4.2 TB/s, or the multiply-adds at 20 TFLOP/s.
+// Measured, us, each for itself / in groups: 12 heads of 64, 16 groups of 4 of 700..1900
+// tokens 73 / 63, of 4500..6000 228 / 129, of 8 of 1100..1500 138 / 96; 4 groups of 4 of
+// 1500 29 / 36; 16 groups of 2 with 4 query heads a key-value head of 6000 240 / 168. Each
+// for itself / together: one group of 32 of 1500 50 / 65, of 6000 150 / 75; 4 groups of 4
+// with 4 query heads a key-value head of 1500 46 / 68, of 6000 128 / 90.
+enum How { kAlone, kInGroups, kTogether };
+How how_to_read(int64_t batch, int64_t group, int64_t heads, int64_t kv_heads, int64_t d,
+                int64_t max_len) {
+    if (group < 2 || max_len <= 2 * kKChunk) return kAlone;
+    const double token = 8.0 * double(kv_heads * d), len = double(max_len);
     const double per_kv = double(heads / kv_heads), groups = double((batch + group - 1) / group);
-    const double alone = 18.0 + double(batch) * token / 9.0e6 * std::max(1.0, 0.37 * per_kv);
-    const double shared =
-        45.0 + std::max(groups * token / 4.2e6, double(batch) * per_kv * token / 2.0 / 20.0e6);
-    return alone > 1.25 * shared;
+    const double alone = 18.0 + double(batch) * token * len / 9.0e6 * std::max(1.0, 0.37 * per_kv);
+    if (double(group) * per_kv <= kFewRows) {
+        const GroupPlan p = group_plan(int64_t(groups), 1, kv_heads, d, max_len);
+        const double rate = std::min(5.8e6, 18.0e3 * double(p.units * p.cluster));
+        return alone > 1.1 * (34.0 + groups * (len + 200.0 * double(group)) * token / rate)
+                   ? kInGroups
+                   : kAlone;
+    }
+    const double shared = 45.0 + std::max(groups * token * len / 4.2e6,
+                                          double(batch) * per_kv * token * len / 2.0 / 20.0e6);
+    return alone > 1.25 * shared ? kTogether : kAlone;
 }
 
 struct SharedPlan {
-    bool together;            // false: decode.cu
+    How how;
+    GroupPlan group;          // in groups; the rest is of this file
     int64_t groups, kv, heads, ldx, ldpart;      // kv, heads: of a round
     size_t top, inv, x, part, bytes;             // offsets in the workspace
 };
@@ -713,9 +727,14 @@ SharedPlan shared_plan(int64_t batch, int64_t group, int64_t heads, int64_t kv_h
     group = std::min(group, batch);
     const int64_t per_kv = heads / kv_heads;
     p.groups = group > 0 ? (batch + group - 1) / group : 0;
-    p.together = read_together(batch, group, heads, kv_heads, head_dim, max_len) &&
-                 p.groups * group * heads < 0x7fffffff / 8;
-    if (!p.together) {
+    p.how = how_to_read(batch, group, heads, kv_heads, head_dim, max_len);
+    if (p.groups * group * heads >= 0x7fffffff / 8) p.how = kAlone;
+    if (p.how == kInGroups) {
+        p.group = group_plan(p.groups, group * per_kv, kv_heads, head_dim, max_len);
+        p.bytes = p.group.bytes;
+        return p;
+    }
+    if (p.how == kAlone) {
         p.bytes = decode_workspace_bytes(batch, heads, kv_heads, head_dim, max_len);
         return p;
     }
@@ -837,7 +856,7 @@ cudaError_t launch_shared_decode(int64_t batch, int64_t group, int heads, const 
                                  int32_t *dev_status, cudaStream_t s) {
     const int64_t max_len = max_pages * c.page_size, d = c.head_dim;
     const SharedPlan p = shared_plan(batch, group, heads, c.kv_heads, d, max_len);
-    if (!p.together)
+    if (p.how == kAlone)
         return launch_decode_attention(batch, heads, q, ldq, c, table, max_pages, ldt, kv_lens,
                                        scale, out, ldo, workspace, dev_status, s);
     char *ws = reinterpret_cast<char *>(workspace);
@@ -879,7 +898,27 @@ cudaError_t launch_shared_decode(int64_t batch, int64_t group, int heads, const 
     A.wide = vec && d % 4 == 0;
     const bool boxes = c.page_size == 8 || c.page_size == 16 || c.page_size == 32 ||
                        c.page_size % 64 == 0;
-    const bool few = A.rows <= kFewRows, few_own = A.per_kv <= kFewRows;
+    const int kbox = int(std::min<int64_t>(c.page_size, 64));
+    const int vbox = int(std::min<int64_t>(c.page_size, kPvTokens));
+    if (p.how == kInGroups) {
+        A.kv_heads = int(c.kv_heads);
+        A.heads = heads;
+        A.k = c.k;
+        A.v = c.v;
+        A.q = q;
+        A.out = out;
+        A.x = reinterpret_cast<float *>(ws);
+        A.part = reinterpret_cast<float *>(ws + p.group.part);
+        A.box = kbox;
+        CUtensorMap maps[2] = {};
+        const int64_t extent[4] = {d, c.kv_heads, c.page_size, c.num_pages};
+        const int64_t stride[3] = {c.head_stride, c.token_stride, c.page_stride};
+        const uint32_t box[4] = {32, 1, uint32_t(kbox), 1};
+        const bool tma = vec && boxes && make_tensor_map_4d(&maps[0], c.k, extent, stride, box) &&
+                         make_tensor_map_4d(&maps[1], c.v, extent, stride, box);
+        return launch_group_decode(A, p.group, tma ? maps : nullptr, s);
+    }
+    const bool few = A.per_kv <= kFewRows;        // rows of a request
     const int64_t most = p.groups * p.ldpart, most_own = batch * p.ldpart;
     for (int64_t g0 = 0; g0 < c.kv_heads; g0 += p.kv) {
         A.kv_heads = int(std::min(p.kv, c.kv_heads - g0));
@@ -889,8 +928,6 @@ cudaError_t launch_shared_decode(int64_t batch, int64_t group, int heads, const 
         A.q = q + g0 * A.per_kv * d;
         A.out = out + g0 * A.per_kv * d;
         CUtensorMap kmap = {}, vmap = {}, vmap_few = {};
-        const int kbox = int(std::min<int64_t>(c.page_size, 64));
-        const int vbox = int(std::min<int64_t>(c.page_size, kPvTokens));
         bool tma = false;
         if (vec && boxes) {
             const int64_t extent[4] = {d, A.kv_heads, c.page_size, c.num_pages};
@@ -902,29 +939,23 @@ cudaError_t launch_shared_decode(int64_t batch, int64_t group, int heads, const 
         cudaError_t e = run_plan(A, max_pages, s);
         A.box = kbox;
         const CUtensorMap *map = tma ? &kmap : nullptr;
+        if (e == cudaSuccess) e = scores<false>(A, map, most, s);
         if (e == cudaSuccess)
-            e = few ? launch_few_scores(false, A, map, most, s) : scores<false>(A, map, most, s);
-        if (e == cudaSuccess)
-            e = few_own ? launch_few_scores(true, A, map, most_own, s)
-                        : scores<true>(A, map, most_own, s);
+            e = few ? launch_few_scores(A, map, most_own, s) : scores<true>(A, map, most_own, s);
         if (e == cudaSuccess) {
             e = launch_dependent(shared_sums_kernel,
                                  dim3(unsigned((A.rows + kSumRows - 1) / kSumRows),
                                       unsigned(p.groups * A.kv_heads)),
                                  dim3(kSumThreads), 0, s, A);
         }
-        auto values = [&](bool of_few) {
-            A.box = of_few ? kbox : vbox;
-            return !tma ? nullptr : of_few ? &vmap_few : &vmap;
-        };
-        if (e == cudaSuccess) {
-            map = values(few);
-            e = few ? launch_few_partials(false, A, map, most, s) : partials<false>(A, map, most, s);
-        }
-        if (e == cudaSuccess) {
-            map = values(few_own);
-            e = few_own ? launch_few_partials(true, A, map, most_own, s)
-                        : partials<true>(A, map, most_own, s);
+        A.box = vbox;
+        map = tma ? &vmap : nullptr;
+        if (e == cudaSuccess) e = partials<false>(A, map, most, s);
+        if (e == cudaSuccess && few) {
+            A.box = kbox;
+            e = launch_few_partials(A, tma ? &vmap_few : nullptr, most_own, s);
+        } else if (e == cudaSuccess) {
+            e = partials<true>(A, map, most_own, s);
         }
         if (e == cudaSuccess) {
             e = launch_dependent(shared_join_kernel,

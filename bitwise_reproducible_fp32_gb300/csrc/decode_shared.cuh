@@ -1,6 +1,7 @@
 // decode_shared.cuh -- what the kernels of decode attention for requests that share a
 // prefix have in common (decode_shared.cu: the plan, and units of many rows;
-// decode_few.cu: units of up to 8 rows).
+// decode_few.cu: requests' own tokens with up to 8 rows; decode_group.cu: groups of up to
+// 8 rows).
 #pragma once
 
 #include "decode.cuh"
@@ -191,15 +192,154 @@ __device__ __forceinline__ int64_t offset_of(const SharedArgs &A, const int32_t 
     return pages[p] * A.page_stride + int64_t(unsigned(t) - p * A.page_size) * A.token_stride;
 }
 
+// ---------------------------------------------------------------- pieces
+// kTile tokens x 32 dimensions in shared memory: rows of 128 bytes, their 16-byte units
+// swapped by row mod 8.
+constexpr int kPieceBytes = kTile * 128;
+constexpr int kMostStages = 3;
+
+// A warp's ring of pieces.
+template <Loader LOAD>
+struct Ring {
+    const SharedArgs &A;
+    const CUtensorMap *map;              // of the keys or values that are fetched
+    const float *cache;
+    uint32_t slots, bars;
+    int stages, slot_in = 0, slot = 0;
+    uint32_t phase = 0;
+    bool stuck = false;
+    int id = 0;                           // of the lane's box
+    int64_t off[2];                       // of tokens lane, lane + 32
+
+    __device__ __forceinline__ Ring(const SharedArgs &a, const CUtensorMap *m, const float *c,
+                                    uint32_t s, uint32_t b, int n)
+        : A(a), map(m), cache(c), slots(s), bars(b), stages(n) {}
+    // where the piece of `live` tokens from t on is; ahead of fetch. CHECK: whether one
+    // of the lane's pages is out of range (page 0 stands for it).
+    template <bool CHECK = false>
+    __device__ __forceinline__ bool look_up(const int32_t *pages, int t, int live) {
+        const int lane = threadIdx.x & 31;
+        bool bad = false;
+        auto page = [&](unsigned p) {
+            const int at = pages[p];
+            if (!CHECK || unsigned(at) < unsigned(A.num_pages)) return at;
+            bad = true;
+            return 0;
+        };
+        if constexpr (LOAD == kTma) {
+            if (lane * A.box < live) id = page(page_of(A, t + lane * A.box));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int at = t + lane + 32 * k;
+                if (lane + 32 * k >= live) continue;
+                const unsigned p = page_of(A, at);
+                off[k] = page(p) * A.page_stride + int64_t(unsigned(at) - p * A.page_size) * A.token_stride;
+            }
+        }
+        return bad;
+    }
+    __device__ __forceinline__ void fetch(int kv, int sl, int t, int live) {
+        const int lane = threadIdx.x & 31;
+        const uint32_t dst = slots + slot_in * kPieceBytes;
+        if constexpr (LOAD == kTma) {
+            const uint32_t bar = bars + 8 * slot_in;
+            const int boxes = (live + A.box - 1) / A.box;
+            if (lane == 0) mbar_arrive_expect_tx(bar, boxes * A.box * 128);
+            __syncwarp();
+            if (lane < boxes) {
+                const int at = t + lane * A.box;
+                tma_load_4d(dst + lane * A.box * 128, map, 32 * sl, kv,
+                            int(unsigned(at) - page_of(A, at) * A.page_size), id, bar);
+            }
+        } else if constexpr (LOAD == kCopy16) {
+            const int col = lane & 7, r0 = lane >> 3;
+            const bool in = 4 * col < A.d - 32 * sl;
+            const float *src = cache + kv * A.head_stride + 32 * sl + 4 * col;
+#pragma unroll
+            for (int i = 0; i < kTile / 4; ++i) {
+                const int r = 4 * i + r0;
+                const int64_t at = __shfl_sync(0xffffffffu, off[i >> 3], r & 31);
+                if (in && r < live) cp_async<16>(dst + r * 128 + ((col ^ (r & 7)) << 4), src + at);
+            }
+        } else {
+            const bool in = lane < A.d - 32 * sl;
+            const float *src = cache + kv * A.head_stride + 32 * sl + lane;
+#pragma unroll 8
+            for (int r = 0; r < kTile; ++r) {
+                const int64_t at = __shfl_sync(0xffffffffu, r < 32 ? off[0] : off[1], r & 31);
+                if (in && r < live)
+                    cp_async<4>(dst + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | (lane & 3) << 2),
+                                src + at);
+            }
+        }
+        slot_in = slot_in + 1 == stages ? 0 : slot_in + 1;
+    }
+    __device__ __forceinline__ void wait() {
+        if constexpr (LOAD == kTma) {
+            if (!stuck)
+                stuck = __any_sync(0xffffffffu, !mbar_wait_bounded(bars + 8 * slot, phase));
+        } else {
+            if (stages == 3) cp_wait<1>(); else cp_wait<0>();
+        }
+        __syncwarp();
+    }
+    // the piece that was waited for
+    __device__ __forceinline__ uint32_t piece() {
+        const uint32_t p = slots + slot * kPieceBytes;
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
+        }
+        return p;
+    }
+    // at the end: the copies in flight land
+    __device__ __forceinline__ void drain(unsigned *watchdog) {
+        if constexpr (LOAD != kTma) {
+            cp_wait<0>();
+        } else if (stuck) {
+            for (int i = 0; i < stages; ++i) {
+                (void)mbar_wait_bounded(bars + 8 * slot, phase);
+                if (++slot == stages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+            if ((threadIdx.x & 31) == 0) atomicOr(watchdog, kWatchdogDecode);
+        }
+    }
+};
+
+template <Loader LOAD>
+__device__ __forceinline__ void init_bars(uint64_t *bars) {
+    if (LOAD == kTma && threadIdx.x == 0) {
+        for (int i = 0; i < kWarps * kMostStages; ++i) mbar_init(smem_u32(bars + i), 1);
+        fence_mbar_init();
+    }
+}
+
 }  // namespace
 
-// Units of at most kFewRows rows a key-value head: scores and their maxima; partials of
-// the chunks. map: keys or values with boxes of A.box tokens (nullptr: TMA cannot be
-// used); most: the chunks of all units, at most.
 constexpr int kFewRows = 8;
-cudaError_t launch_few_scores(bool own, const SharedArgs &A, const CUtensorMap *map, int64_t most,
+
+// The requests' own tokens, at most kFewRows rows a key-value head: scores and their
+// maxima; partials of the chunks. map: keys or values with boxes of A.box tokens
+// (nullptr: TMA cannot be used); most: the chunks of all requests, at most.
+cudaError_t launch_few_scores(const SharedArgs &A, const CUtensorMap *map, int64_t most,
                               cudaStream_t s);
-cudaError_t launch_few_partials(bool own, const SharedArgs &A, const CUtensorMap *map, int64_t most,
+cudaError_t launch_few_partials(const SharedArgs &A, const CUtensorMap *map, int64_t most,
+                                cudaStream_t s);
+
+// Groups of at most kFewRows rows a key-value head, in one launch. maps: keys and values
+// with boxes of A.box tokens.
+struct GroupPlan {
+    int cluster;
+    int64_t units, chunks;        // chunks: of a request, at most
+    size_t part, bytes;           // the partials' place in the workspace, and its size
+};
+GroupPlan group_plan(int64_t groups, int64_t rows, int64_t kv_heads, int64_t head_dim,
+                     int64_t max_len);
+cudaError_t launch_group_decode(const SharedArgs &A, const GroupPlan &p, const CUtensorMap *maps,
                                 cudaStream_t s);
 
 }  // namespace det

@@ -132,6 +132,7 @@ cudaError_t block_watchdog(unsigned int *code, int clear);
 cudaError_t decode_watchdog(unsigned int *code, int clear);
 cudaError_t shared_decode_watchdog(unsigned int *code, int clear);
 cudaError_t few_decode_watchdog(unsigned int *code, int clear);
+cudaError_t group_decode_watchdog(unsigned int *code, int clear);
 cudaError_t logprob_watchdog(unsigned int *code, int clear);
 
 // 2-D fp32 TMA descriptor over a row-major matrix: inner = contiguous extent,
