@@ -13,10 +13,17 @@
 //   5. join: each row's chunk partials, left to right.
 // The profile's chains are of fmaf, so the products run on the CUDA cores: with R
 // rows, a key and value (2 x 4 bytes a dimension) take 2 R multiply-adds, and from R of
-// about 24 on they, not HBM, bound a unit. As in the GEMM, shared memory's rate sets
-// the register tile: up to 16 rows x 8 tokens (or dimensions) a thread. Scores lie
-// in octets of 8 tokens, a group's rows side by side: [octet][row][8], so a warp's
-// stores of 4 rows x 8 tokens and its loads of exps are whole 128-byte lines.
+// about 24 on they, not HBM, bound a unit. Scores lie in octets of 8 tokens, a group's
+// rows side by side: [octet][row][8], so a warp's stores of 4 rows x 8 tokens and its
+// loads of exps are whole 128-byte lines, and a block of rows is one bulk copy an octet.
+// Own tokens with few rows (decode_few.cu) are bound by HBM; their kernels run behind
+// those of the shared ones and beside their last waves. Every launch overlaps the end
+// of the one before (programmatic dependent launches).
+// Measured: 48 requests on a document of 20001..24000 tokens, 32 heads of 128 over 8, 565
+// us (32 TFLOP/s; scores 180 us and P V 168, the FMA pipe about 65% busy, sums 51, own
+// tokens 50 of which some is hidden, the join 15); 64 requests on 8100..8192 tokens and up
+// to 1000 of their own, 12 heads of 64, 155 us (1.6 TB/s, 11 TFLOP/s: seven dependent
+// launches of 5 to 35 us).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -161,9 +168,10 @@ __device__ __forceinline__ float part_of(const float4 &v, int i) {
 }
 
 // ---------------------------------------------------------------- scores
-// An item: 4 RT rows, a chunk's 256 tokens; a warp 64 tokens (8 lanes x 8, tokens 8
+// An item: 16 rows, a chunk's 256 tokens; a warp 64 tokens (8 lanes x 8, tokens 8
 // apart, so that 16-byte reads along the dimensions of 8 keys meet no bank
-// conflict), 4 lanes x RT rows (4 apart). Keys come 32 dimensions at a time, a stage
+// conflict), 4 lanes x RT = 4 rows (4 apart; 8 and 16 rows a lane took as long on large
+// cases, 176..185 us for scores of 180, and longer on small ones). Keys come 32 dimensions at a time, a stage
 // ahead; the query rows stay in shared memory, transposed, while they do not change.
 template <bool OWN, bool TMA>
 __global__ void __launch_bounds__(kThreads, kScoreCtas)

@@ -953,7 +953,8 @@ det_status detkv_copy_f32(const det_profile_v1 *prof, int64_t pairs, const int32
  * (those of length 0 or out of range left out; every request keeps one token of its
  * own at least) are found from the table; their keys and values are read once for
  * the group instead of once a request. Pages need not be shared: group only says
- * where to look.
+ * where to look. For few requests or a narrow table, where reading each for itself is
+ * faster, that is done (the choice goes by the arguments' sizes, not by lengths).
  * Arguments, status bits and errors as detdecode_attention_f32, and
  * DET_ERR_INVALID_ARG for group < 1. workspace: at least
  * detdecode_attention_shared_workspace_bytes (16-byte aligned, no contents
