@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(1024) beam_select_kernel(const SelectArgs A) {
                 status |= 2;
             }
         }
-        const bool dead = parent < 0, ended = dead || done || token == A.eos;
+        const bool dead = parent < 0;
+        const bool ended = dead || done || (A.eos >= 0 && token == A.eos);
         s_parent[lane] = parent;
         s_len[lane] = len;
         s_col[lane] = dead || done || len < 0 ? -1 : len;
@@ -215,7 +216,7 @@ cudaError_t launch_beam_select(int64_t requests, const det_beams &in, const det_
         // in one)
         const int64_t wave = int64_t(sm_count_current_device()) * 4;
         parts = std::max<int64_t>(1, std::min((cols + 1023) / 1024, wave / requests));
-        A.part = ((cols + parts - 1) / parts + 127) / 128 * 128;
+        A.part = std::max<int64_t>(128, ((cols + parts - 1) / parts + 127) / 128 * 128);
         parts = std::max<int64_t>(1, (cols + A.part - 1) / A.part);
     }
     beam_select_kernel<<<dim3(unsigned(requests), unsigned(parts)), unsigned(warps * 32), 0, s>>>(

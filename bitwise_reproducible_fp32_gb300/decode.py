@@ -343,6 +343,8 @@ class Decoder:
             raise ValueError(f"1..{B // beams} prompts and at least one new token")
         if max(map(len, prompts)) + new_tokens - 1 > self.table.size(1) * self.page_size:
             raise ValueError("the prompts leave no room for so many tokens")
+        if self.lens[:n].any():
+            raise ValueError("a request that the beams need still holds tokens; release it first")
         i32 = dict(dtype=torch.int32, device=self.device)
         hist = [torch.full((n, new_tokens), -1, **i32) for _ in range(2)]
         parents, tok = torch.arange(B, **i32), torch.zeros(B, **i32)

@@ -170,6 +170,34 @@ def test_no_requests(dev):
     assert got.scores.shape == (0, 4) and got.tokens.numel() == 0 and got.lens.numel() == 0
 
 
+def test_a_negative_ending_ends_nothing(dev):
+    # an id of -1 with a score is a token like others where eos says that there is no ending
+    s, lp = torch.zeros((1, 1), device="cuda"), torch.tensor([[-1.0, -2.0]], device="cuda")
+    ids = torch.tensor([[-1, 5]], dtype=torch.int32, device="cuda")
+    got = detlib.detbeam_select_f32(s, ids, lp, 2)
+    assert host(got.tokens).tolist() == [-1, 5] and host(got.finished).tolist() == [0, 0]
+    assert host(got.forks).tolist() == [0, 0]
+
+
+def test_histories_without_columns(dev):
+    # the C entry takes histories of no columns: nothing is written, and every one is cut
+    lib, prof = detlib.load(), detlib.det_profile_default()
+    rng = np.random.default_rng(12)
+    s, i, lp = (on_gpu(a) for a in draw(3, 2, 4, rng))
+    n = torch.zeros(6, dtype=torch.int32, device="cuda")
+    h, ho = (torch.full((6,), v, dtype=torch.int32, device="cuda") for v in (3, 4))
+    so = torch.empty(6, device="cuda")
+    tok, par, st = (torch.zeros(6, dtype=torch.int32, device="cuda") for _ in range(3))
+    args = [detlib.BeamsArg(2, s.data_ptr(), None, n.data_ptr(), h.data_ptr(), 1),
+            detlib.BeamsArg(2, so.data_ptr(), None, None, ho.data_ptr(), 1)]
+    rc = lib.detbeam_select_f32(prof, 3, *args, 4, i.data_ptr(), lp.data_ptr(), -1, None, 0, 0,
+                                tok.data_ptr(), par.data_ptr(), None, st.data_ptr(),
+                                torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and int(st[0]) == 2 and bool((ho == 4).all())
+    want = select_plain(*map(host, (s, i, lp)), 2)
+    assert np.array_equal(host(so).reshape(3, 2), want[0]) and np.array_equal(host(tok), want[1])
+
+
 def test_binding_refusals(dev):
     rng = np.random.default_rng(8)
     s, i, lp = (on_gpu(a) for a in draw(2, 4, 8, rng))

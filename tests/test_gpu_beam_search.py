@@ -215,6 +215,12 @@ def test_out_of_pages_and_refusals(dev):
     assert host(dec.lens).tolist() == [0] * 4 and int(dec.count) == 3
     with pytest.raises(ValueError):
         Decoder(cd, 4, 32, device, group=0)
+    # a request of the beams' that holds tokens is not overwritten
+    dec.prefill([1], [p[:3]])
+    with pytest.raises(ValueError):
+        dec.beam_search([p], 2, 2)
+    assert host(dec.lens).tolist() == [0, 3, 0, 0]
+    dec.release(i32([0, 1, 0, 0]))
     # two of three copies of the partly filled page find no page and stay empty
     dec.prefill([0], [p])
     dec.fork(i32([0, 0, 0, 0]))
