@@ -43,8 +43,8 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanRows = 1024;                    // requests looked through at once
 constexpr int kPlanCtas = 8;                       // of a cluster
-constexpr int kScoreStage = kKChunk * 128;         // a chunk's tokens x 32 dimensions
-constexpr int kScoreStages = 2;
+constexpr int kScoreStages = 2;                    // of a warp's ring
+constexpr size_t kScoreRing = size_t(kWarps) * kScoreStages * kPieceBytes;
 constexpr int kScoreRows = 4;                      // of a thread
 constexpr int kScoreCtas = 3;                      // an SM's
 constexpr int kPvTokens = 16;                      // of a step of P V
@@ -171,90 +171,62 @@ __device__ __forceinline__ float part_of(const float4 &v, int i) {
 // An item: 16 rows, a chunk's 256 tokens; a warp 64 tokens (8 lanes x 8, tokens 8
 // apart, so that 16-byte reads along the dimensions of 8 keys meet no bank
 // conflict), 4 lanes x RT = 4 rows (4 apart; 8 and 16 rows a lane took as long on large
-// cases, 176..185 us for scores of 180, and longer on small ones). Keys come 32 dimensions at a time, a stage
-// ahead; the query rows stay in shared memory, transposed, while they do not change.
-template <bool OWN, bool TMA>
+// cases, 176..185 us for scores of 180, and longer on small ones). A warp's keys come
+// through a ring of its own, so warps meet only where the rows change; the query rows
+// stay in shared memory, transposed, while they do not.
+template <bool OWN, Loader LOAD>
 __global__ void __launch_bounds__(kThreads, kScoreCtas)
     shared_scores_kernel(const SharedArgs A, const __grid_constant__ CUtensorMap kmap) {
     constexpr int RT = kScoreRows, R = 4 * RT;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    float *qs = reinterpret_cast<float *>(smem_raw + kScoreStages * kScoreStage);
+    float *qs = reinterpret_cast<float *>(smem_raw + kScoreRing);
     __shared__ Share share;
     __shared__ int rows[R];           // (b, h) of the row at qs's place
-    __shared__ uint64_t full[kScoreStages];
+    __shared__ uint64_t full[kWarps][kMostStages];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tl = lane & 7, rl = lane >> 3;
     const int d = A.d, nsl = (d + 31) / 32, mul = A.kv_heads * A.row_blocks;
-    if (TMA && tid == 0) {
-        for (int i = 0; i < kScoreStages; ++i) mbar_init(smem_u32(full + i), 1);
-        fence_mbar_init();
-    }
+    init_bars<LOAD>(&full[0][0]);
     Beside<OWN> beside;
     shares<OWN, 1>(A, mul, blockIdx.x, 1, gridDim.x, &share);
     const int64_t items = share.items;
     if (items <= 0) return;
-    const uint32_t ring = smem_u32(smem_raw);
+    Ring<LOAD> ring(A, &kmap, A.k, smem_u32(smem_raw) + warp * kScoreStages * kPieceBytes,
+                    smem_u32(&full[warp][0]), kScoreStages);
 
     // ---- keys
     Item in = share.at;
-    int in_sl = 0, in_slot = 0, in_t0 = 0, in_live = 0, in_boxes = 0, in_id = 0, in_kv = 0;
-    int64_t left = items * nsl;
-    auto look_up = [&]() {            // the item's tokens and, warp 0, the lane's box's page
-        if (in.u >= units<OWN>(A)) return;
-        in_t0 = first_token<OWN>(in);
-        in_live = tokens_from<OWN>(in, in_t0);
-        in_kv = in.run / A.row_blocks;
-        if (TMA) {
-            in_boxes = (in_live + A.box - 1) / A.box;             // at most 32
-            if (warp == 0 && lane < in_boxes)
-                in_id = pages_of<OWN>(A, in)[page_of(A, in_t0 + lane * A.box)];
+    int64_t in_items = items;
+    int in_sl = 0, in_t0 = 0, in_live = 0, in_kv = 0;
+    auto seek = [&]() {               // the warp's tile of the item, or of the next that has one
+        while (in_items > 0) {
+            const int t0 = first_token<OWN>(in);
+            in_t0 = t0 + kTile * warp;
+            in_live = min(kTile, tokens_from<OWN>(in, t0) - kTile * warp);
+            if (in_live > 0) {
+                in_kv = in.run / A.row_blocks;
+                ring.look_up(pages_of<OWN>(A, in), in_t0, in_live);
+                return;
+            }
+            advance<OWN>(A, mul, in);
+            --in_items;
         }
     };
-    look_up();
+    seek();
     auto issue = [&]() {
-        if (left > 0) {
-            --left;
-            const int kv = in_kv;
-            const uint32_t dst = ring + in_slot * kScoreStage, bar = smem_u32(full + in_slot);
-            if constexpr (TMA) {
-                if (warp == 0) {
-                    if (lane == 0) mbar_arrive_expect_tx(bar, in_boxes * A.box * 128);
-                    __syncwarp();
-                    if (lane < in_boxes) {
-                        const int t = in_t0 + lane * A.box;
-                        tma_load_4d(dst + lane * A.box * 128, &kmap, 32 * in_sl, kv,
-                                    int(unsigned(t) - page_of(A, t) * A.page_size), in_id, bar);
-                    }
-                }
-            } else {
-                const int32_t *pages = pages_of<OWN>(A, in);
-                const float *src = A.k + kv * A.head_stride + 32 * in_sl;
-                if (A.wide) {
-                    const int col = tid & 7;
-                    if (4 * col < d - 32 * in_sl)
-                        for (int r = tid >> 3; r < in_live; r += kThreads / 8)
-                            cp_async<16>(dst + r * 128 + ((col ^ (r & 7)) << 4),
-                                         src + offset_of(A, pages, in_t0 + r) + 4 * col);
-                } else if (lane < d - 32 * in_sl) {
-                    for (int r = warp; r < in_live; r += kWarps)
-                        cp_async<4>(dst + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) |
-                                                     (lane & 3) << 2),
-                                    src + offset_of(A, pages, in_t0 + r) + lane);
-                }
-            }
-            in_slot ^= 1;
+        if (in_items > 0) {
+            ring.fetch(in_kv, in_sl, in_t0, in_live);
             if (++in_sl == nsl) {
                 in_sl = 0;
                 advance<OWN>(A, mul, in);
-                look_up();
+                --in_items;
+                seek();
             }
         }
-        if (!TMA) cp_commit();
+        if (LOAD != kTma) cp_commit();
     };
-    issue();
+    for (int i = 0; i < kScoreStages - 1; ++i) issue();
     Item it = share.at;
-    int held_u = -1, held_run = -1, slot = 0;
-    uint32_t phase = 0;
-    bool stuck = false;
+    int held_u = -1, held_run = -1;
     for (int64_t i = 0; i < items; ++i) {
         const int kv = it.run / A.row_blocks, r0 = (it.run - kv * A.row_blocks) * R;
         const int g = group_of<OWN>(A, it.u);
@@ -271,6 +243,11 @@ __global__ void __launch_bounds__(kThreads, kScoreCtas)
             const int b = row / A.heads;
             const float *q = A.q + b * A.ldq + int64_t(row - b * A.heads) * d;
             for (int j = tid / R; j < d; j += kThreads / R) qs[j * R + p] = row >= 0 ? q[j] : 0.0f;
+            __syncthreads();
+        }
+        if (OWN && kTile * warp >= live) {      // the request ends before this warp's tokens
+            advance<OWN>(A, mul, it);
+            continue;
         }
         f32x2 acc[RT / 2][8];
 #pragma unroll
@@ -279,16 +256,9 @@ __global__ void __launch_bounds__(kThreads, kScoreCtas)
             for (int r = 0; r < RT / 2; ++r) acc[r][c] = 0;
         }
         for (int sl = 0; sl < nsl; ++sl) {
-            if constexpr (TMA) {
-                if (!stuck) stuck = !mbar_wait_bounded(smem_u32(full + slot), phase);
-                stuck = __syncthreads_or(stuck);
-                if (stuck) break;
-            } else {
-                cp_wait<0>();
-                __syncthreads();
-            }
-            issue();              // into the slot consumed before this one
-            const uint32_t keys = ring + slot * kScoreStage + (64 * warp + tl) * 128;
+            ring.wait();
+            if (!ring.stuck) issue();           // into the slot consumed before this one
+            const uint32_t keys = ring.piece() + tl * 128;
             const float *qp = qs + 32 * sl * R + rl * RT;
             auto four = [&](int g4, int live4) {
                 float4 k[8];
@@ -309,24 +279,15 @@ __global__ void __launch_bounds__(kThreads, kScoreCtas)
                 }
             };
             const int width = min(32, d - 32 * sl);
-            if (OWN && 64 * warp >= live) {
-                // the request ends before this warp's tokens
-            } else if (width == 32) {
+            if (width == 32) {
 #pragma unroll
                 for (int g4 = 0; g4 < 8; ++g4) four(g4, 4);
             } else {
                 for (int g4 = 0; 4 * g4 < width; ++g4) four(g4, width - 4 * g4);
             }
-            slot ^= 1;
-            phase ^= slot == 0;
         }
-        if (stuck) {              // this and the other rows of the share are NaN
-            if (tid < R) {
-                const int r = r0 + tid;
-                const int row =
-                    r < rows_of<OWN>(A) ? row_at(A, g, kv, place_of<OWN>(A, it.u, r)) : -1;
-                if (row >= 0) atomicMax(A.top + row, 0xffffffffu);
-            }
+        if (ring.stuck) {             // this and the other rows of the share are NaN
+            if (lane < R && rows[lane] >= 0) atomicMax(A.top + rows[lane], 0xffffffffu);
         } else {
             const int64_t octet = (int64_t(g) * A.kv_heads + kv) * A.octets + t0 / 8 + 8 * warp;
             float *x = A.x + (octet * A.rows + place_of<OWN>(A, it.u, r0 + rl)) * 8 + tl;
@@ -352,14 +313,7 @@ __global__ void __launch_bounds__(kThreads, kScoreCtas)
         }
         advance<OWN>(A, mul, it);
     }
-    if (TMA && stuck) {                   // let the copies in flight land
-        for (int i = 0; i < kScoreStages; ++i) {
-            (void)mbar_wait_bounded(smem_u32(full + slot), phase);
-            slot ^= 1;
-            phase ^= slot == 0;
-        }
-        if (tid == 0) atomicOr(&g_shared_watchdog, kWatchdogDecode);
-    }
+    ring.drain(&g_shared_watchdog);
 }
 
 // ---------------------------------------------------------------- sums
@@ -801,10 +755,11 @@ cudaError_t scores(SharedArgs A, const CUtensorMap *map, int64_t most, cudaStrea
     A.row_blocks = int((rows + R - 1) / R);
     const int64_t grid = std::min<int64_t>(most * A.kv_heads * A.row_blocks,
                                            int64_t(sm_count_current_device()) * kScoreCtas);
-    const size_t smem = kScoreStages * kScoreStage + size_t(A.d) * R * 4;
+    const size_t smem = kScoreRing + size_t(A.d) * R * 4;
     const CUtensorMap none = {};
-    return map ? run(shared_scores_kernel<OWN, true>, grid, smem, s, A, *map)
-               : run(shared_scores_kernel<OWN, false>, grid, smem, s, A, none);
+    return map      ? run(shared_scores_kernel<OWN, kTma>, grid, smem, s, A, *map)
+           : A.wide ? run(shared_scores_kernel<OWN, kCopy16>, grid, smem, s, A, none)
+                    : run(shared_scores_kernel<OWN, kCopy4>, grid, smem, s, A, none);
 }
 
 template <int TR, int DH, bool OWN>

@@ -52,13 +52,13 @@ __device__ __forceinline__ unsigned page_of(const SharedArgs &A, int t) {
 
 // ---------------------------------------------------------------- work
 // The items of a kernel: for each unit (a group with the shared chunks, or a request
-// with its own chunks; or either with tiles of kTile tokens of them) `mul` runs (of heads
-// and blocks of rows or dimensions) of its chunks or tiles, these fastest.
-enum Cut { kShared, kOwn, kSharedTiles, kOwnTiles };
+// with its own chunks, or with tiles of kTile tokens of them) `mul` runs (of heads and
+// blocks of rows or dimensions) of its chunks or tiles, these fastest.
+enum Cut { kShared, kOwn, kOwnTiles };
 template <int CUT>
-constexpr bool kIsOwn = (CUT & 1) != 0;
+constexpr bool kIsOwn = CUT != kShared;
 template <int CUT>
-constexpr bool kInTiles = (CUT & 2) != 0;
+constexpr bool kInTiles = CUT == kOwnTiles;
 constexpr int kTile = 64;
 struct Item {
     int u, run, c;
@@ -70,7 +70,6 @@ template <int CUT>
 __device__ __forceinline__ int chunks_of(const SharedArgs &A, int u) {
     const int n = kIsOwn<CUT> ? A.own[u] : A.chunks[u];
     if (!kInTiles<CUT> || n == 0) return n;
-    if (!kIsOwn<CUT>) return n * (kKChunk / kTile);
     return (A.kv_lens[u] - A.chunks[u / A.group] * kKChunk + kTile - 1) / kTile;
 }
 template <int CUT>
