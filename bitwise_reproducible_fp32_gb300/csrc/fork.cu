@@ -583,9 +583,9 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const CompactAr
 
 // ---------------------------------------------------------------- copy
 constexpr int kCopyThreads = 512;
-constexpr int kFilterWords = 4096;                  // 2^17 pages, by the low bits
+constexpr int kMostFilter = 18;                     // filters of at most 2^18 bits
 constexpr int kUnroll = 8;
-constexpr int kCopyCtas = 2;                       // an SM's
+constexpr int kCopyCtas = 2;                        // an SM's
 
 struct CopyArgs {
     float *k, *v;
@@ -594,24 +594,47 @@ struct CopyArgs {
     int64_t page_stride, token_stride, head_stride;
     const int32_t *src, *dst, *tokens, *count;
     int pairs;
-    int seg_tokens, segs;             // tokens of a CTA's piece; pieces of a page
+    int seg_tokens, segs;             // tokens of a piece; pieces of a page
+    int filter;                       // bits of a filter, by the pages' low bits
     int32_t *dev_status;
 };
 
-// WIDE: floats of a unit (4 or 1). Units of a piece: token, then head, then dim.
-template <int WIDE>
+// Whether x holds for any thread of the CTA's team'th team of N threads (all of them
+// call).
+template <int N>
+__device__ __forceinline__ bool team_any(bool x, int team) {
+    if (N == 32) return __any_sync(0xffffffffu, x);
+    unsigned r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(unsigned(x)), "r"(team + 1), "r"(N)
+        : "memory");
+    return r != 0;
+}
+
+// WIDE: floats of a unit (4 or 1). Units of a piece: token, then head, then dim. A team of
+// TEAM threads takes a piece, so that small pages go by many at a time (4096 of 512 bytes
+// 26 -> 11 us).
+template <int WIDE, int TEAM>
 __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) kv_copy_kernel(const CopyArgs A) {
     // pages that are a source; a destination; a destination at least twice
-    __shared__ uint32_t is_src[kFilterWords], is_dst[kFilterWords], twice[kFilterWords];
-    const int tid = threadIdx.x;
+    extern __shared__ uint32_t is_src[];
+    const int words = A.filter / 32;
+    uint32_t *is_dst = is_src + words, *twice = is_dst + words;
+    const int tid = threadIdx.x, lane = tid & 31;
+    constexpr int teams = kCopyThreads / TEAM;
+    const int team = tid / TEAM, at_team = tid % TEAM;
     int n = A.pairs, status = 0;
     if (A.count) {
         const int c = *A.count;
         if (c < 0 || c > n) status |= 1;
         n = min(max(c, 0), n);
     }
-    if (int64_t(blockIdx.x) >= int64_t(n) * A.segs && blockIdx.x != 0) return;
-    for (int i = tid; i < kFilterWords; i += kCopyThreads) is_src[i] = is_dst[i] = twice[i] = 0;
+    const int64_t pieces = int64_t(n) * A.segs;
+    if (int64_t(blockIdx.x) * teams >= pieces && blockIdx.x != 0) return;
+    for (int i = tid; i < 3 * words; i += kCopyThreads) is_src[i] = 0;
     __syncthreads();
     // a pair that copies: both pages there, and as many tokens as a page holds
     auto valid = [&](int i, int &s, int &d, int &t) {
@@ -629,31 +652,31 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) kv_copy_kernel(const 
     for (int i = tid; i < n; i += kCopyThreads) {
         int s, d, t;
         if (!valid(i, s, d, t)) continue;
-        const unsigned a = unsigned(s) & (kFilterWords * 32 - 1);
-        const unsigned b = unsigned(d) & (kFilterWords * 32 - 1);
+        const unsigned a = unsigned(s) & unsigned(A.filter - 1);
+        const unsigned b = unsigned(d) & unsigned(A.filter - 1);
         atomicOr(is_src + (a >> 5), 1u << (a & 31));
         if (atomicOr(is_dst + (b >> 5), 1u << (b & 31)) >> (b & 31) & 1)
             atomicOr(twice + (b >> 5), 1u << (b & 31));
     }
     __syncthreads();
     const int units = A.head_dim / WIDE, row = A.kv_heads * units;
-    for (int64_t w = blockIdx.x; w < int64_t(n) * A.segs; w += gridDim.x) {
+    for (int64_t w = int64_t(blockIdx.x) * teams + team; w < pieces; w += int64_t(gridDim.x) * teams) {
         const int i = int(w / A.segs), seg = int(w - int64_t(i) * A.segs);
         int s, d, t;
-        if (!valid(i, s, d, t)) continue;           // the same for all threads
-        const unsigned b = unsigned(d) & (kFilterWords * 32 - 1);
+        if (!valid(i, s, d, t)) continue;           // the same for the whole team
+        const unsigned b = unsigned(d) & unsigned(A.filter - 1);
         const uint32_t bit = 1u << (b & 31);
         if ((is_src[b >> 5] | twice[b >> 5]) & bit) {
             // maybe: look through the pairs
-            int later = 0, read = 0;
-            for (int j = tid; j < n; j += kCopyThreads) {
+            bool later = false, read = false;
+            for (int j = at_team; j < n; j += TEAM) {
                 int s2, d2, t2;
                 if (!valid(j, s2, d2, t2)) continue;
                 read |= s2 == d;
                 later |= d2 == d && j > i;
             }
-            read = __syncthreads_or(read);
-            later = __syncthreads_or(later);
+            read = team_any<TEAM>(read, team);
+            later = team_any<TEAM>(later, team);
             if (read) status |= 2;
             if (read || later) continue;
         }
@@ -662,12 +685,12 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) kv_copy_kernel(const 
         const int total = max(0, t1 - t0) * row;
         for (int half = 0; half < 2; ++half) {
             float *base = half ? A.v : A.k;
-            for (int u0 = tid; u0 < total; u0 += kCopyThreads * kUnroll) {
+            for (int u0 = at_team; u0 < total; u0 += TEAM * kUnroll) {
                 float4 v4[kUnroll];
                 int64_t at[kUnroll];
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
-                    const int x = u0 + u * kCopyThreads;
+                    const int x = u0 + u * TEAM;
                     if (x >= total) break;
                     const int tok = x / row, rest = x - tok * row, g = rest / units;
                     at[u] = (t0 + tok) * A.token_stride + g * A.head_stride +
@@ -677,7 +700,7 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) kv_copy_kernel(const 
                 }
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
-                    if (u0 + u * kCopyThreads >= total) break;
+                    if (u0 + u * TEAM >= total) break;
                     if (WIDE == 4) *reinterpret_cast<float4 *>(base + to + at[u]) = v4[u];
                     else base[to + at[u]] = v4[u].x;
                 }
@@ -685,8 +708,9 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) kv_copy_kernel(const 
         }
     }
     if (A.dev_status) {
+        __syncwarp();
         status = __reduce_or_sync(0xffffffffu, unsigned(status));
-        if ((tid & 31) == 0 && status) atomicOr(reinterpret_cast<int *>(A.dev_status), status);
+        if (lane == 0 && status) atomicOr(reinterpret_cast<int *>(A.dev_status), status);
     }
 }
 
@@ -794,18 +818,37 @@ cudaError_t launch_kv_copy(int64_t pairs, const int32_t *src, const int32_t *dst
                      c.head_stride % 4 == 0 && c.head_dim % 4 == 0;
     CopyArgs A = {c.k, c.v, c.num_pages, int(c.page_size), int(c.kv_heads), int(c.head_dim),
                   c.page_stride, c.token_stride, c.head_stride, src, dst, tokens, count, int(pairs),
-                  0, 0, dev_status};
-    // a piece: tokens whose units all have one round of the threads' loads, fewer where
-    // the pieces would be too few for the GPU, or one
+                  0, 0, 0, dev_status};
+    // a piece: tokens whose units all have one round of a CTA's loads, fewer where the
+    // pieces would be too few for the GPU, or one; a thread takes up to eight units of it
     const int64_t units = c.kv_heads * c.head_dim / (vec ? 4 : 1);
     const int64_t ctas = int64_t(sm_count_current_device()) * kCopyCtas;
     const int64_t fit = std::min(kCopyThreads * kUnroll / units, pairs * c.page_size / ctas);
     A.seg_tokens = int(std::max<int64_t>(1, std::min(fit, c.page_size)));
     A.segs = int((c.page_size + A.seg_tokens - 1) / A.seg_tokens);
-    const int64_t grid = std::min<int64_t>(pairs * A.segs, ctas);
-    if (vec) kv_copy_kernel<4><<<unsigned(grid), kCopyThreads, 0, s>>>(A);
-    else kv_copy_kernel<1><<<unsigned(grid), kCopyThreads, 0, s>>>(A);
-    return cudaGetLastError();
+    const int64_t wants = A.seg_tokens * units / 8;
+    const int team = wants <= 32 ? 32 : wants <= 128 ? 128 : kCopyThreads;
+    const int64_t teams = kCopyThreads / team;
+    const int64_t grid = std::min<int64_t>((pairs * A.segs + teams - 1) / teams, ctas);
+    A.filter = 1024;
+    while (A.filter < (1 << kMostFilter) && A.filter < c.num_pages) A.filter *= 2;
+    const size_t smem = size_t(A.filter) / 8 * 3;
+    auto run = [&](auto kern) {
+        if (smem > 48 * 1024) {           // the most any call takes
+            const cudaError_t e = cudaFuncSetAttribute(
+                kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (1 << kMostFilter) / 8 * 3);
+            if (e != cudaSuccess) return e;
+        }
+        kern<<<unsigned(grid), kCopyThreads, smem, s>>>(A);
+        return cudaGetLastError();
+    };
+    if (vec)
+        return team == 32    ? run(kv_copy_kernel<4, 32>)
+               : team == 128 ? run(kv_copy_kernel<4, 128>)
+                             : run(kv_copy_kernel<4, kCopyThreads>);
+    return team == 32    ? run(kv_copy_kernel<1, 32>)
+           : team == 128 ? run(kv_copy_kernel<1, 128>)
+                         : run(kv_copy_kernel<1, kCopyThreads>);
 }
 
 }  // namespace det

@@ -272,7 +272,7 @@ def run_copy(kc, vc, src, dst, tokens=None, count=None):
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
-@pytest.mark.parametrize("ps,G,d", [(16, 12, 64), (1, 1, 1), (7, 3, 10), (64, 8, 128), (5, 2, 250),
+@pytest.mark.parametrize("ps,G,d", [(16, 12, 64), (1, 1, 1), (7, 3, 10), (64, 8, 128), (5, 2, 250), (120, 4, 64),
                                     (300, 2, 16)])
 def test_copy(dev, layout, ps, G, d):
     rng = np.random.default_rng(ps + d)
