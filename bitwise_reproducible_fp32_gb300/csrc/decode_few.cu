@@ -7,7 +7,9 @@
 // two tokens a lane for the scores and a dimension a lane for P V. A worker is a warp,
 // and its work a run of all units' tiles or chunks, so short requests leave no SM
 // idle. Measured: 64 requests with 157..1255 tokens of their own, 12 heads of 64, scores 25
-// us and P V 26 (123 MB each, 4.8 TB/s).
+// us and P V 26 (123 MB each, 4.8 TB/s). Neighbouring runs go to one CTA's warps (a call of
+// 64 requests on 8192 tokens 157 -> 146 us with the same in P V of the shared ones), and
+// rings of two pieces leave room for three CTAs an SM.
 #include <algorithm>
 
 #include "decode_shared.cuh"
@@ -19,12 +21,13 @@ __device__ unsigned int g_few_watchdog;
 
 namespace {
 
-constexpr int kFewCtas = 2;               // an SM's
+constexpr int kFewCtas = 3;               // an SM's, where registers allow
+constexpr int kFewStages = 2;             // pieces of a warp's ring
 
 // NH: the rows the registers hold, of which the unit has at most NH.
 template <int NH, Loader LOAD>
-__global__ void __launch_bounds__(kThreads, kFewCtas)
-    few_scores_kernel(const SharedArgs A, const __grid_constant__ CUtensorMap kmap, int stages) {
+__global__ void __launch_bounds__(kThreads, 2)
+    few_scores_kernel(const SharedArgs A, const __grid_constant__ CUtensorMap kmap) {
     constexpr int CUT = kOwnTiles;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ Share share[kWarps];
@@ -33,12 +36,12 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
     const int d = A.d, nsl = (d + 31) / 32, live_rows = rows_of<CUT>(A), ldq = nsl * 32;
     init_bars<LOAD>(&full[0][0]);
     Beside<true> beside;
-    shares<CUT, kWarps>(A, A.kv_heads, blockIdx.x, gridDim.x, gridDim.x * kWarps, share);
+    shares<CUT, kWarps>(A, A.kv_heads, blockIdx.x * kWarps, 1, gridDim.x * kWarps, share);
     const int64_t items = share[warp].items;
     if (items <= 0) return;
-    Ring<LOAD> ring(A, &kmap, A.k, smem_u32(smem_raw) + warp * stages * kPieceBytes,
-                    smem_u32(&full[warp][0]), stages);
-    float *qs = reinterpret_cast<float *>(smem_raw + kWarps * stages * kPieceBytes) +
+    Ring<LOAD> ring(A, &kmap, A.k, smem_u32(smem_raw) + warp * kFewStages * kPieceBytes,
+                    smem_u32(&full[warp][0]), kFewStages);
+    float *qs = reinterpret_cast<float *>(smem_raw + kWarps * kFewStages * kPieceBytes) +
                 warp * NH * ldq;
 
     Item in = share[warp].at;
@@ -62,7 +65,7 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
         }
         if (LOAD != kTma) cp_commit();
     };
-    for (int i = 0; i < stages - 1; ++i) issue();
+    for (int i = 0; i < kFewStages - 1; ++i) issue();
     uint32_t kat[8];              // 16-byte unit i of row `lane` of a piece
 #pragma unroll
     for (int i = 0; i < 8; ++i) kat[i] = lane * 128 + ((i ^ (lane & 7)) << 4);
@@ -174,8 +177,8 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
 }
 
 template <int NH, Loader LOAD>
-__global__ void __launch_bounds__(kThreads, kFewCtas)
-    few_partials_kernel(const SharedArgs A, const __grid_constant__ CUtensorMap vmap, int stages) {
+__global__ void __launch_bounds__(kThreads, 2)
+    few_partials_kernel(const SharedArgs A, const __grid_constant__ CUtensorMap vmap) {
     constexpr int CUT = kOwn;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ Share share[kWarps];
@@ -184,12 +187,12 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
     const int d = A.d, nsl = (d + 31) / 32, live_rows = rows_of<CUT>(A), mul = A.kv_heads * nsl;
     init_bars<LOAD>(&full[0][0]);
     Beside<true> beside;
-    shares<CUT, kWarps>(A, mul, blockIdx.x, gridDim.x, gridDim.x * kWarps, share);
+    shares<CUT, kWarps>(A, mul, blockIdx.x * kWarps, 1, gridDim.x * kWarps, share);
     const int64_t items = share[warp].items;
     if (items <= 0) return;
-    Ring<LOAD> ring(A, &vmap, A.v, smem_u32(smem_raw) + warp * stages * kPieceBytes,
-                    smem_u32(&full[warp][0]), stages);
-    const uint32_t copies = smem_u32(smem_raw) + kWarps * stages * kPieceBytes +
+    Ring<LOAD> ring(A, &vmap, A.v, smem_u32(smem_raw) + warp * kFewStages * kPieceBytes,
+                    smem_u32(&full[warp][0]), kFewStages);
+    const uint32_t copies = smem_u32(smem_raw) + kWarps * kFewStages * kPieceBytes +
                             warp * (NH * kTile * 4);
 
     Item in = share[warp].at;
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
         }
         if (LOAD != kTma) cp_commit();
     };
-    for (int i = 0; i < stages - 1; ++i) issue();
+    for (int i = 0; i < kFewStages - 1; ++i) issue();
     uint32_t vat[8];              // column `lane` of rows i mod 8 of a piece
 #pragma unroll
     for (int i = 0; i < 8; ++i) vat[i] = i * 128 + (((lane >> 2) ^ i) << 4) + ((lane & 3) << 2);
@@ -328,9 +331,6 @@ __global__ void __launch_bounds__(kThreads, kFewCtas)
 template <class K>
 cudaError_t run_few(K kern, int64_t items, size_t row_bytes, const SharedArgs &A,
                     const CUtensorMap *map, cudaStream_t s) {
-    // three stages where they and the rows fit
-    int stages = kMostStages;
-    if (kWarps * (stages * kPieceBytes + row_bytes) > kMaxSmem) stages = 2;
     // the most any call takes, as another thread's call may come before the launch
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxSmem));
@@ -339,8 +339,8 @@ cudaError_t run_few(K kern, int64_t items, size_t row_bytes, const SharedArgs &A
                                            int64_t(sm_count_current_device()) * kFewCtas);
     const CUtensorMap none = {};
     return launch_dependent(kern, dim3(unsigned(std::max<int64_t>(1, grid))), dim3(kThreads),
-                            kWarps * (stages * kPieceBytes + row_bytes), s, A, map ? *map : none,
-                            stages);
+                            kWarps * (kFewStages * kPieceBytes + row_bytes), s, A,
+                            map ? *map : none);
 }
 
 template <int NH>

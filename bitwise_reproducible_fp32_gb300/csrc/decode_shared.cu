@@ -19,10 +19,10 @@
 // Own tokens with few rows (decode_few.cu) are bound by HBM; their kernels run behind
 // those of the shared ones and beside their last waves. Every launch overlaps the end
 // of the one before (programmatic dependent launches).
-// Measured: 48 requests on a document of 20001..24000 tokens, 32 heads of 128 over 8, 565
+// Measured: 48 requests on a document of 20001..24000 tokens, 32 heads of 128 over 8, 550
 // us (32 TFLOP/s; scores 180 us and P V 168, the FMA pipe about 65% busy, sums 51, own
 // tokens 50 of which some is hidden, the join 15); 64 requests on 8100..8192 tokens and up
-// to 1000 of their own, 12 heads of 64, 155 us (1.6 TB/s, 11 TFLOP/s: seven dependent
+// to 1000 of their own, 12 heads of 64, 146 us (1.7 TB/s, 12 TFLOP/s: seven dependent
 // launches of 5 to 35 us).
 #include <cooperative_groups.h>
 
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, kPvCtas)
         fence_mbar_init();
     }
     Beside<OWN> beside;
-    shares<OWN, kWarps>(A, mul, blockIdx.x, gridDim.x, gridDim.x * kWarps, share);
+    shares<OWN, kWarps>(A, mul, blockIdx.x * kWarps, 1, gridDim.x * kWarps, share);
     const int64_t items = share[warp].items;
     if (items <= 0) return;
     const uint32_t ring = smem_u32(smem_raw) + warp * STAGES * W::kStage;
