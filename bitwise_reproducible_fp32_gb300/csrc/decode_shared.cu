@@ -19,10 +19,10 @@
 // Own tokens with few rows (decode_few.cu) are bound by HBM; their kernels run behind
 // those of the shared ones and beside their last waves. Every launch overlaps the end
 // of the one before (programmatic dependent launches).
-// Measured: 48 requests on a document of 20001..24000 tokens, 32 heads of 128 over 8, 550
-// us (32 TFLOP/s; scores 180 us and P V 168, the FMA pipe about 65% busy, sums 51, own
-// tokens 50 of which some is hidden, the join 15); 64 requests on 8100..8192 tokens and up
-// to 1000 of their own, 12 heads of 64, 146 us (1.7 TB/s, 12 TFLOP/s: seven dependent
+// Measured: 48 requests on a document of 20001..24000 tokens, 32 heads of 128 over 8, 543
+// us (32 TFLOP/s; scores 180 us and P V 168, the FMA pipe about 65% busy, sums 48, own
+// tokens 45 of which some is hidden, the join 15); 64 requests on 8100..8192 tokens and up
+// to 1000 of their own, 12 heads of 64, 140 us (1.8 TB/s, 12 TFLOP/s: seven dependent
 // launches of 5 to 35 us).
 #include <cooperative_groups.h>
 
@@ -48,7 +48,7 @@ constexpr size_t kScoreRing = size_t(kWarps) * kScoreStages * kPieceBytes;
 constexpr int kScoreRows = 4;                      // of a thread
 constexpr int kScoreCtas = 3;                      // an SM's
 constexpr int kPvTokens = 16;                      // of a step of P V
-constexpr int kPvCtas = 2;                         // an SM's
+constexpr int kPvGrid = 3;                         // CTAs an SM, where two run: finer shares
 
 // ---------------------------------------------------------------- plan
 // A cluster of up to 8 CTAs a group. Every request keeps a token of its own, so a
@@ -318,10 +318,10 @@ __global__ void __launch_bounds__(kThreads, kScoreCtas)
 
 // ---------------------------------------------------------------- sums
 // A CTA four rows of a group and head: 8 lanes have the two halves of 4 octets of a
-// row, so 8 of its 256 chains; a thread two chains, each in ascending order.
-constexpr int kSumThreads = 512;
+// row, so 8 of its 256 chains; a thread a chain, in ascending order.
+constexpr int kSumThreads = 1024;
 constexpr int kSumRows = 4;
-constexpr int kSumDeep = 8;                        // groups of a chain in flight
+constexpr int kSumDeep = 4;                        // groups of a chain in flight
 
 __global__ void __launch_bounds__(kSumThreads) shared_sums_kernel(const SharedArgs A) {
     __shared__ float chains[kSumRows][256], red[kSumRows][8];
@@ -384,14 +384,15 @@ struct PvWarp {
     static constexpr int kR = 4 * TR;
     static constexpr int kValues = kPvTokens * 128 * DH;
     static constexpr int kStage = kValues + kPvTokens * kR * 4;
-    static constexpr int kFit = int(kMaxSmem / kWarps) / kStage;
+    static constexpr int kCtas = TR * DH >= 16 ? 2 : 3;       // an SM's, by registers
+    static constexpr int kFit = int((kCtas == 2 ? kMaxSmem : 72 * 1024) / kWarps) / kStage;
     static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr size_t kBytes = size_t(kWarps) * kStages * kStage;
     static_assert(kStage % 1024 == 0 && kStages >= 2, "shared memory");
 };
 
 template <int TR, int DH, bool OWN, bool TMA>
-__global__ void __launch_bounds__(kThreads, kPvCtas)
+__global__ void __launch_bounds__(kThreads, (PvWarp<TR, DH>::kCtas))
     shared_partials_kernel(const SharedArgs A, const __grid_constant__ CUtensorMap vmap) {
     using W = PvWarp<TR, DH>;
     constexpr int R = W::kR, STAGES = W::kStages;
@@ -770,7 +771,7 @@ cudaError_t run_partials(SharedArgs A, const CUtensorMap *map, int64_t rows, int
     A.dim_tiles = (A.d + 32 * DH - 1) / (32 * DH);
     const int64_t items = most * A.kv_heads * A.row_blocks * A.dim_tiles;
     const int64_t grid = std::min<int64_t>((items + kWarps - 1) / kWarps,
-                                           int64_t(sm_count_current_device()) * kPvCtas);
+                                           int64_t(sm_count_current_device()) * kPvGrid);
     const CUtensorMap none = {};
     return map ? run(shared_partials_kernel<TR, DH, OWN, true>, grid, W::kBytes, s, A, *map)
                : run(shared_partials_kernel<TR, DH, OWN, false>, grid, W::kBytes, s, A, none);
