@@ -18,8 +18,9 @@
 // half a million pages compacted 37, of 3000 pages 16.
 //
 // The copy streams pages through registers, 16 bytes a thread where the layout
-// allows; HBM bounds it (each byte read and written once): 4096 pages of 131 KB in 192
-// us, 5.6 TB/s, 83% of the measured copy rate.
+// allows; HBM bounds it (each byte read and written once): 4096 pages of 131 KB in 175
+// us, 6.1 TB/s, 90% of the measured copy rate. Four loads a thread: with eight, which
+// spill, 195 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -584,8 +585,9 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const CompactAr
 // ---------------------------------------------------------------- copy
 constexpr int kCopyThreads = 512;
 constexpr int kMostFilter = 18;                     // filters of at most 2^18 bits
-constexpr int kUnroll = 8;
+constexpr int kUnroll = 4;
 constexpr int kCopyCtas = 2;                        // an SM's
+constexpr double kStreamBytes = 128.0 * (1 << 20);
 
 struct CopyArgs {
     float *k, *v;
@@ -616,8 +618,9 @@ __device__ __forceinline__ bool team_any(bool x, int team) {
 
 // WIDE: floats of a unit (4 or 1). Units of a piece: token, then head, then dim. A team of
 // TEAM threads takes a piece, so that small pages go by many at a time (4096 of 512 bytes
-// 26 -> 11 us).
-template <int WIDE, int TEAM>
+// 26 -> 11 us). STREAM: more than L2 holds, so nothing is kept there (4096 pages of 131 KB
+// 183 -> 175 us).
+template <int WIDE, int TEAM, bool STREAM = false>
 __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) kv_copy_kernel(const CopyArgs A) {
     // pages that are a source; a destination; a destination at least twice
     extern __shared__ uint32_t is_src[];
@@ -695,14 +698,18 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) kv_copy_kernel(const 
                     const int tok = x / row, rest = x - tok * row, g = rest / units;
                     at[u] = (t0 + tok) * A.token_stride + g * A.head_stride +
                             int64_t(rest - g * units) * WIDE;
-                    if (WIDE == 4) v4[u] = *reinterpret_cast<const float4 *>(base + from + at[u]);
-                    else v4[u].x = base[from + at[u]];
+                    const float *p = base + from + at[u];
+                    if (WIDE == 1) v4[u].x = *p;
+                    else if (STREAM) v4[u] = __ldcs(reinterpret_cast<const float4 *>(p));
+                    else v4[u] = *reinterpret_cast<const float4 *>(p);
                 }
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
                     if (u0 + u * TEAM >= total) break;
-                    if (WIDE == 4) *reinterpret_cast<float4 *>(base + to + at[u]) = v4[u];
-                    else base[to + at[u]] = v4[u].x;
+                    float *p = base + to + at[u];
+                    if (WIDE == 1) *p = v4[u].x;
+                    else if (STREAM) __stcs(reinterpret_cast<float4 *>(p), v4[u]);
+                    else *reinterpret_cast<float4 *>(p) = v4[u];
                 }
             }
         }
@@ -842,9 +849,12 @@ cudaError_t launch_kv_copy(int64_t pairs, const int32_t *src, const int32_t *dst
         kern<<<unsigned(grid), kCopyThreads, smem, s>>>(A);
         return cudaGetLastError();
     };
+    const bool stream =
+        16.0 * double(pairs) * double(c.page_size) * double(c.kv_heads * c.head_dim) > kStreamBytes;
     if (vec)
         return team == 32    ? run(kv_copy_kernel<4, 32>)
                : team == 128 ? run(kv_copy_kernel<4, 128>)
+               : stream      ? run(kv_copy_kernel<4, kCopyThreads, true>)
                              : run(kv_copy_kernel<4, kCopyThreads>);
     return team == 32    ? run(kv_copy_kernel<1, 32>)
            : team == 128 ? run(kv_copy_kernel<1, 128>)

@@ -307,6 +307,17 @@ def test_copy_of_many_pages_past_the_filter(dev):
     run_copy(kc, vc, ids[:5000], dst)
 
 
+def test_copy_of_more_than_l2_holds(dev):
+    rng = np.random.default_rng(6)
+    pages = 330
+    kc, vc = (on_gpu(rng.standard_normal((pages, 64, 8, 128)).astype(F)) for _ in range(2))
+    ids = rng.permutation(pages).astype(I)
+    run_copy(kc, vc, ids[:160], ids[160:320])
+    dst = ids[160:320].copy()
+    dst[::50], dst[1::70] = dst[7], ids[3]
+    run_copy(kc, vc, ids[:160], dst, rng.integers(0, 65, 160).astype(I))
+
+
 def test_copy_past_32_bit_offsets(dev):
     pages, ps, G, d = 35_000, 64, 8, 128          # 2.3e9 floats each
     kc, vc = (torch.full((pages, ps, G, d), float("nan"), device="cuda") for _ in range(2))
