@@ -356,3 +356,39 @@ def test_two_threads_at_once(dev):
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+@pytest.mark.parametrize("B,H,G,group", [(20, 4, 4, 20), (24, 4, 2, 3), (12, 9, 1, 12)])
+def test_read_together_captured_and_on_two_streams(dev, B, H, G, group):
+    # tables wide enough that requests are read together or in groups; two captured calls
+    # replayed on two streams at once, on other queries each time
+    rng = np.random.default_rng(B)
+    own = rng.integers(1, 600, B)
+    kc, vc, table, lens, _, _ = shared_cache([1500], own, 16, G, 64, "token", rng)
+    wide = torch.full((B, WIDE // 16), -7, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    ld = on_gpu(lens)
+    jobs = []
+    for _ in range(2):
+        q = torch.zeros((B, H * 64), device="cuda")
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            detlib.detdecode_attention_shared_f32(q, kc, vc, wide, ld, H, group)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            out = detlib.detdecode_attention_shared_f32(q, kc, vc, wide, ld, H, group)
+        jobs.append((q, s, g, out))
+    for step in range(5):
+        for q, _, _, _ in jobs:
+            q.copy_(on_gpu(rng.standard_normal((B, H * 64)).astype(F)))
+        torch.cuda.synchronize()
+        for q, s, g, out in jobs:
+            with torch.cuda.stream(s):
+                for _ in range(3):
+                    g.replay()
+        torch.cuda.synchronize()
+        for q, s, g, out in jobs:
+            want = detlib.detdecode_attention_f32(q, kc, vc, table, ld, H)
+            assert_bitwise(host(out), host(want), f"replay {step}")
