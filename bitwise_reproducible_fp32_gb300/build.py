@@ -47,17 +47,25 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build_variant(defines, out_path: str) -> str:
+def build_variant(defines, out_path: str, sources=None) -> str:
     """Compile a separate copy of the library with extra -D flags into out_path
-    (the test suite's copy with a shortened GEMM wait). Never the shipped
-    library: LIB is not touched."""
+    (the test suite's copies with shortened waits or a given way of reading). Never the
+    shipped library: LIB is not touched. sources: those that the flags are for (default:
+    all); the others are compiled without, or are the shipped library's objects where
+    those are there and no file is newer."""
     work = out_path + ".build"
     os.makedirs(work, exist_ok=True)
     dflags = [f"-D{d}" for d in defines]
+    kept = not _stale()
 
     def compile_one(src):
+        mine = sources is None or src in sources
+        shipped = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
+        if not mine and kept and os.path.exists(shipped):
+            return shipped
         obj = os.path.join(work, src.replace(".cu", ".o"))
-        cmd = [nvcc(), *common_flags(dflags), "-c", os.path.join(CSRC, src), "-o", obj]
+        cmd = [nvcc(), *common_flags(dflags if mine else ()), "-c", os.path.join(CSRC, src), "-o",
+               obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")

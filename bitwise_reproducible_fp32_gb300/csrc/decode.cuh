@@ -11,6 +11,17 @@ namespace {
 
 enum Loader { kTma, kCopy16, kCopy4 };
 
+// Waits for the piece in a slot of a warp's ring of `stages`; false when the wait gave up.
+// In the test suite's copy of the library (DET_TEST_DECODE_GIVE_UP) a warp gives up on
+// one of its first 2 * stages pieces, which one by its CTA's number, without a look at
+// it, so that it leaves healthy copies in flight.
+__device__ __forceinline__ bool wait_for_piece(uint32_t bars, int slot, uint32_t phase, int stages) {
+#ifdef DET_TEST_DECODE_GIVE_UP
+    if (slot + stages * int(phase) == int(blockIdx.x) % (2 * stages)) return false;
+#endif
+    return mbar_wait_bounded(bars + 8 * slot, phase);
+}
+
 __device__ __forceinline__ float4 lds4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"

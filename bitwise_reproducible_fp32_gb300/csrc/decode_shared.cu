@@ -33,6 +33,12 @@
 
 namespace cg = cooperative_groups;
 
+#ifdef DET_TEST_SHARED_HOW
+// Of the test suite's copies of the library: how groups are read whatever their size
+// (det::How), below 0 as the estimate says.
+extern "C" __attribute__((visibility("default"))) int det_test_shared_how = -1;
+#endif
+
 namespace det {
 
 // Set when a bounded wait for a piece gave up.
@@ -512,6 +518,12 @@ __global__ void __launch_bounds__(kThreads, (PvWarp<TR, DH>::kCtas))
     int held_u = -1, held_block = -1, slot = 0;
     uint32_t phase = 0;
     bool stuck = false;
+    auto step = [&]() {
+        if (++slot == STAGES) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
     int mine[TR];                     // the lane's rows (b, h), -1 where there is none
     float inv[TR];
     for (int64_t i = 0; i < items; ++i) {
@@ -536,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, (PvWarp<TR, DH>::kCtas))
             if constexpr (TMA) {
                 if (!stuck)
                     stuck = __any_sync(0xffffffffu,
-                                       !mbar_wait_bounded(smem_u32(&full[warp][slot]), phase));
+                                       !wait_for_piece(smem_u32(&full[warp][0]), slot, phase, STAGES));
             } else {
                 cp_wait<STAGES - 2>();
             }
@@ -575,10 +587,7 @@ __global__ void __launch_bounds__(kThreads, (PvWarp<TR, DH>::kCtas))
             } else {
                 for (int t = 0; t1 + t < tokens; t += 4) four(t, tokens - t1 - t);
             }
-            if (++slot == STAGES) {
-                slot = 0;
-                phase ^= 1;
-            }
+            if (!stuck) step();
         }
         // ---- the partials of the lane's rows and dimensions
         const int dim0 = it.run % A.dim_tiles * 32 * DH + 4 * dl;
@@ -605,14 +614,8 @@ __global__ void __launch_bounds__(kThreads, (PvWarp<TR, DH>::kCtas))
         advance<OWN>(A, mul, it);
     }
     if (!TMA) cp_wait<0>();
-    if (TMA && stuck) {                   // let the copies in flight land
-        for (int i = 0; i < STAGES; ++i) {
-            (void)mbar_wait_bounded(smem_u32(&full[warp][slot]), phase);
-            if (++slot == STAGES) {
-                slot = 0;
-                phase ^= 1;
-            }
-        }
+    if (TMA && stuck) {                   // let the copies in flight land (as Ring::drain)
+        for (; slot != in_slot; step()) (void)mbar_wait_bounded(smem_u32(&full[warp][slot]), phase);
         if (lane == 0) atomicOr(&g_shared_watchdog, kWatchdogDecode);
     }
 }
@@ -661,6 +664,12 @@ constexpr size_t kSliceBytes = size_t(1) << 30;     // scores and partials of a 
 enum How { kAlone, kInGroups, kTogether };
 How how_to_read(int64_t batch, int64_t group, int64_t heads, int64_t kv_heads, int64_t d,
                 int64_t max_len) {
+#ifdef DET_TEST_SHARED_HOW
+    if (det_test_shared_how >= 0 && group >= 2)
+        return det_test_shared_how == kInGroups && group * (heads / kv_heads) > kFewRows
+                   ? kTogether
+                   : How(det_test_shared_how);
+#endif
     if (group < 2 || max_len <= 2 * kKChunk) return kAlone;
     const double token = 8.0 * double(kv_heads * d), len = double(max_len);
     const double per_kv = double(heads / kv_heads), groups = double((batch + group - 1) / group);

@@ -277,33 +277,31 @@ struct Ring {
     __device__ __forceinline__ void wait() {
         if constexpr (LOAD == kTma) {
             if (!stuck)
-                stuck = __any_sync(0xffffffffu, !mbar_wait_bounded(bars + 8 * slot, phase));
+                stuck = __any_sync(0xffffffffu, !wait_for_piece(bars, slot, phase, stages));
         } else {
             if (stages == 3) cp_wait<1>(); else cp_wait<0>();
         }
         __syncwarp();
     }
-    // the piece that was waited for
-    __device__ __forceinline__ uint32_t piece() {
-        const uint32_t p = slots + slot * kPieceBytes;
+    __device__ __forceinline__ void step() {
         if (++slot == stages) {
             slot = 0;
             phase ^= 1;
         }
+    }
+    // the piece that was waited for; once a wait has given up, that one for good
+    __device__ __forceinline__ uint32_t piece() {
+        const uint32_t p = slots + slot * kPieceBytes;
+        if (!stuck) step();
         return p;
     }
-    // at the end: the copies in flight land
+    // at the end: the copies in flight land, which are those from the one that a wait
+    // gave up on to the last one asked for
     __device__ __forceinline__ void drain(unsigned *watchdog) {
         if constexpr (LOAD != kTma) {
             cp_wait<0>();
         } else if (stuck) {
-            for (int i = 0; i < stages; ++i) {
-                (void)mbar_wait_bounded(bars + 8 * slot, phase);
-                if (++slot == stages) {
-                    slot = 0;
-                    phase ^= 1;
-                }
-            }
+            for (; slot != slot_in; step()) (void)mbar_wait_bounded(bars + 8 * slot, phase);
             if ((threadIdx.x & 31) == 0) atomicOr(watchdog, kWatchdogDecode);
         }
     }
