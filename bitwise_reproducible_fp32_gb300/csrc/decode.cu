@@ -233,17 +233,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (t + lane + 32 < end) off[1] = offset_of(t + lane + 32);
     };
     auto issue = [&](const float *src, const CUtensorMap *map, int t, int sl, int end) {
-        const uint32_t dst = ring + slot_in * kPieceBytes;
+        const uint32_t dst = ring + slot_in * kPieceBytes, bar = bars + 8 * slot_in;
+        slot_in = slot_in + 1 == stages ? 0 : slot_in + 1;
         const int live = min(kTokens, end - t);
         if constexpr (LOAD == kTma) {
             const int boxes = (live + A.box - 1) / A.box;
-            if (lane == 0) mbar_arrive_expect_tx(bars + 8 * slot_in, boxes * A.box * 128);
+            if (lane == 0) mbar_arrive_expect_tx(bar, boxes * A.box * 128);
             __syncwarp();
             if (lane < boxes) {
                 const int at = t + lane * A.box;
                 const unsigned p = page_of(at);
                 tma_load_4d(dst + lane * A.box * 128, map, 32 * sl, g,
-                            int(unsigned(at) - p * A.page_size), id_of(p), bars + 8 * slot_in);
+                            int(unsigned(at) - p * A.page_size), id_of(p), bar);
             }
         } else if constexpr (LOAD == kCopy16) {
             const int col = lane & 7, r0 = lane >> 3;
@@ -289,25 +290,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             if (vt >= vend) vj += kWarps;
         }
         if (LOAD != kTma) cp_commit();
-        slot_in = slot_in + 1 == stages ? 0 : slot_in + 1;
     };
     for (int i = 0; i < stages - 1; ++i) issue_next();
     int slot = 0;
     uint32_t phase = 0;
-    bool stuck = false;           // a wait gave up: the rest wait no more
+    bool stuck = false;           // a wait gave up: the rest wait no more, the ring stops there
+    auto turn = [&]() {
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
     auto next_piece = [&]() {
         if constexpr (LOAD == kTma) {
-            if (!stuck) stuck = __any_sync(0xffffffffu, !mbar_wait_bounded(bars + 8 * slot, phase));
+            if (!stuck) stuck = __any_sync(0xffffffffu, !wait_for_piece(bars, slot, phase, stages));
         } else {
             if (stages == 3) cp_wait<1>(); else cp_wait<0>();
         }
         __syncwarp();
         if (!stuck) issue_next();   // into the slot consumed before this one
         const uint32_t p = ring + slot * kPieceBytes;
-        if (++slot == stages) {
-            slot = 0;
-            phase ^= 1;
-        }
+        if (!stuck) turn();
         return p;
     };
     // shared-memory offsets in a piece: 16-byte unit c of row `lane`, and column
@@ -561,13 +564,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     if (LOAD != kTma) cp_wait<0>();
     if (LOAD == kTma && stuck) {        // let the copies in flight land, tell the cluster
-        for (int i = 0; i < stages; ++i) {
-            (void)mbar_wait_bounded(bars + 8 * slot, phase);
-            if (++slot == stages) {
-                slot = 0;
-                phase ^= 1;
-            }
-        }
+        for (; slot != slot_in; turn()) (void)mbar_wait_bounded(bars + 8 * slot, phase);
         if (lane == 0) {
             atomicOr(&g_decode_watchdog, kWatchdogDecode);
             for (int r = 0; r < C; ++r) *cluster.map_shared_rank(&F.lost[rank], r) = 2;

@@ -11,7 +11,7 @@ import tempfile
 from bitwise_reproducible_fp32_gb300 import build, detlib
 
 ALONE, GROUPS, TOGETHER = 0, 1, 2
-RINGS = ["decode_shared.cu", "decode_few.cu", "decode_group.cu"]
+RINGS = ["decode.cu", "decode_shared.cu", "decode_few.cu", "decode_group.cu"]
 
 
 @functools.cache

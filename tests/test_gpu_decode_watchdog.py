@@ -7,7 +7,7 @@ import pytest
 
 from bitcmp import assert_bitwise
 from bitwise_reproducible_fp32_gb300 import detlib
-from decode_variants import GROUPS, TOGETHER, reading
+from decode_variants import ALONE, GROUPS, TOGETHER, reading
 from gen_util import F
 from gpu_util import host, need_gpu, to_dev, torch
 from test_gpu_shared_attention import on_gpu, shared_cache
@@ -21,15 +21,16 @@ def dev():
 
 
 # groups of 4 rows a head; groups of 12 with few own rows and with 10 a request (tiles of
-# their own); slices of 32 dimensions that are whole and not
-@pytest.mark.parametrize("how,H,G,d,group", [(GROUPS, 4, 4, 64, 4), (GROUPS, 8, 4, 40, 4),
-                                             (TOGETHER, 8, 4, 64, 6), (TOGETHER, 6, 1, 128, 2),
-                                             (TOGETHER, 20, 2, 72, 4)])
-def test_a_wait_that_runs_out_is_reported(dev, how, H, G, d, group):
+# their own); slices of 32 dimensions that are whole and not; rings of two and three pieces
+@pytest.mark.parametrize("how,H,G,d,group,prefix", [
+    (GROUPS, 4, 4, 64, 4, 1500), (GROUPS, 8, 4, 40, 4, 1500), (TOGETHER, 8, 4, 64, 6, 1500),
+    (TOGETHER, 6, 1, 128, 2, 1500), (TOGETHER, 20, 2, 72, 4, 1500), (ALONE, 4, 4, 64, 4, 200),
+    (ALONE, 16, 4, 64, 4, 1500), (ALONE, 1, 1, 100, 4, 9000)])
+def test_a_wait_that_runs_out_is_reported(dev, how, H, G, d, group, prefix):
     rng = np.random.default_rng(H + d)
     B = 12
     own = rng.integers(1, 700, B)
-    kc, vc, table, lens, _, _ = shared_cache([1500] * (B // group), own, 16, G, d, "token", rng)
+    kc, vc, table, lens, _, _ = shared_cache([prefix] * (B // group), own, 16, G, d, "token", rng)
     q, ld = to_dev(rng.standard_normal((B, H * d)).astype(F)), on_gpu(lens)
     want = host(detlib.detdecode_attention_f32(q, kc, vc, table, ld, H))
     assert detlib.det_watchdog_status(clear=True) == 0
