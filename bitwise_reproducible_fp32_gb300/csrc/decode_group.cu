@@ -449,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, kGroupCtas)
             for (int k = 0; k < 16; ++k)
                 if (c + k < chunks) t = c + k == 0 ? v[k] : __fadd_rn(t, v[k]);
         }
-        if (stuck || gone >> w & 1 || (raw[w] != 0 && len[w] == 0)) t = __uint_as_float(0x7fc00000u);
+        // a request without tokens is 0 whatever happened to the others
+        if (raw[w] != 0 && (stuck || gone >> w & 1 || len[w] == 0)) t = __uint_as_float(0x7fc00000u);
         A.out[(b0 + w) * A.ldo + int64_t(kv * per + h - w * per) * d + j] = t;
     }
     if (A.dev_status && rank == 0) {
