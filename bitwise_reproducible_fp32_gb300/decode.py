@@ -244,6 +244,7 @@ class Decoder:
 
         from bitwise_reproducible_fp32_gb300 import detlib as L
         B = self.B
+        L.check_values(done, "done", torch.int32, B)
         # pages may be shared (a captured call may be replayed after a later fork):
         # everybody else goes on from itself, and a page that one of them holds stays
         if self.forked or (torch.cuda.is_current_stream_capturing() and self.pages <= FORK_PAGES):

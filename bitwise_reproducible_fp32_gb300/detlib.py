@@ -934,6 +934,15 @@ def _vec(t, name, dtype, dev, n=None):
     return p
 
 
+def check_values(t, name, dtype, n=None):
+    """Raises, as the generation calls do, unless t is a contiguous 1-D CUDA tensor of dtype
+    on the current device (of n values)."""
+    import torch
+    if not getattr(t, "is_cuda", False):
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+    _vec(t, name, dtype, torch.cuda.current_device(), n)
+
+
 def _mat(t, name, dtype, dev, rows=None, cols=None):
     """(pointer, row stride) as _at, for a 2-D tensor with contiguous rows, `rows`
     of them of at least `cols`."""

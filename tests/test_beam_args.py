@@ -123,3 +123,25 @@ def test_the_binding_refuses_cpu_tensors_and_shapes(lib):
                  lambda: detlib.detdecode_attention_shared_f32(x, c, c, t[:2], i[:2], 2, 2)):
         with pytest.raises(TypeError):
             call()
+
+
+def decoder(**kw):
+    """A decoder's state on the CPU, as far as refusals look at it."""
+    import torch
+
+    from bitwise_reproducible_fp32_gb300.decode import Decoder
+    dec = Decoder.__new__(Decoder)
+    at = dict(B=4, pages=16, page_size=4, top_k=4, device="cpu", forked=False,
+              lens=torch.zeros(4, dtype=torch.int32), table=torch.zeros(4, 4, dtype=torch.int32))
+    dec.__dict__.update({**at, **kw})
+    return dec
+
+
+@pytest.mark.parametrize("forked", [False, True])
+def test_release_refuses_other_flags(lib, forked):
+    import torch
+    dec = decoder(forked=forked)
+    for done in ([1, 0, 0, 0], True, torch.ones(4), torch.ones(4, dtype=torch.bool),
+                 torch.ones(4, dtype=torch.int32)):
+        with pytest.raises(TypeError, match="done must be a CUDA tensor"):
+            dec.release(done)

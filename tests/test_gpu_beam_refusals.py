@@ -1,0 +1,51 @@
+"""What a decoder refuses for several answers of a prompt leaves it as it was: no request is
+released and no page taken by a call that raises."""
+import numpy as np
+import pytest
+
+from bitwise_reproducible_fp32_gb300 import inputs
+from bitwise_reproducible_fp32_gb300.decode import Decoder
+from gpu_util import host, need_gpu, torch
+from test_gpu_beam_search import i32, upload
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    return need_gpu()
+
+
+@pytest.fixture(scope="module")
+def model(dev):
+    c = inputs.byte_lm_cfg2(batch=2, seq=32)
+    return upload(c), c["tokens"].reshape(2, 32)
+
+
+def state(dec):
+    return [host(t).tolist() for t in (dec.lens, dec.count, dec.free, dec.table)]
+
+
+def test_release_takes_one_int32_flag_a_request(dev, model):
+    cd, toks = model
+    dec = Decoder(cd, 4, 32, torch.device("cuda"), page_size=4)
+    dec.prefill([0], [toks[0, :13]])
+    wrong = [i32([1]), i32([1] * 5), i32([1, 0, 0]), i32([[1, 0, 0, 0]]), i32([1, 0] * 4)[::2],
+             i32(1), torch.ones(4, device="cuda"), torch.ones(4, dtype=torch.bool, device="cuda"),
+             torch.ones(4, dtype=torch.int64, device="cuda"), torch.ones(4, dtype=torch.int32)]
+    for forked in (False, True):
+        if forked:
+            dec.fork(i32([0, 0, 0, -1]))
+        before = state(dec)
+        for done in wrong:
+            with pytest.raises((TypeError, ValueError)):
+                dec.release(done)
+            with pytest.raises((TypeError, ValueError)):
+                with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                    dec.release(done)
+        assert state(dec) == before
+    dec.release(i32([1, 0, 1, 0]))
+    assert host(dec.lens).tolist() == [0, 13, 0, 0] and int(dec.count) == dec.pages - 4
+    dec.release(i32([0, 1, 0, 0]))
+    assert sorted(host(dec.free).tolist()) == list(range(dec.pages)) and int(dec.count) == dec.pages
+    dec.check()
