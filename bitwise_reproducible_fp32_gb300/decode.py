@@ -21,7 +21,7 @@ from __future__ import annotations
 from typing import NamedTuple
 
 APPEND_ROWS = 1 << 20           # detkv_append_f32 takes so many rows in a call
-FORK_PAGES = 1 << 23            # detpages_fork knows so many pages
+FORK_PAGES = 1 << 23            # detpages_fork and detpages_compact know so many pages
 
 
 class Next(NamedTuple):
@@ -264,6 +264,10 @@ class Decoder:
                         tokens=self.tokens, dev_status=self.status)
         self.state.copy_(self.after)
 
+    def _knows_pages(self, what):
+        if self.pages > FORK_PAGES:
+            raise ValueError(f"{what} takes caches of up to {FORK_PAGES} pages")
+
     def fork(self, parents):
         """Every request goes on from request parents[b] (max_batch int32 on the device),
         with its tokens; -1 leaves it empty. Requests of one parent share its full
@@ -272,8 +276,7 @@ class Decoder:
         finds no free page is left empty, and check() raises. For caches of up to 2^23
         pages."""
         from bitwise_reproducible_fp32_gb300 import detlib as L
-        if self.pages > FORK_PAGES:
-            raise ValueError(f"fork takes caches of up to {FORK_PAGES} pages")
+        self._knows_pages("fork")
         self.forked = True
         self._fork(parents)
         self.table.copy_(self.next_table)
@@ -283,8 +286,10 @@ class Decoder:
 
     def compact(self):
         """Moves the pages that requests hold to the lowest ids, so that the rest of the
-        cache is one run of free pages. Can be captured, as a step can."""
+        cache is one run of free pages. Can be captured, as a step can. For caches of up to
+        2^23 pages."""
         from bitwise_reproducible_fp32_gb300 import detlib as L
+        self._knows_pages("compact")
         src, dst = self.moved
         L.detpages_compact(self.lens, self.table, self.free, self.page_size, table_out=self.table,
                            free_count_out=self.count, src=src, dst=dst, moves=self.moves,
@@ -330,7 +335,7 @@ class Decoder:
         of up to max_batch // beams prompts, from an empty decoder, by beam search: each
         step keeps the best of all beams' top_k continuations (detbeam_select_f32). eos:
         the id that ends an answer. weights: floats on the device; answers are then
-        ranked by score * weights[length]. Nothing waits for the host until the end. The
+        ranked by score * weights[length]. For caches of up to 2^23 pages. Nothing waits for the host until the end. The
         requests are released after. Decoder(group=beams) reads what a prompt's beams share
         once. Returns Answers (prompts x beams)."""
         import torch
@@ -344,6 +349,15 @@ class Decoder:
             raise ValueError(f"1..{B // beams} prompts and at least one new token")
         if max(map(len, prompts)) + new_tokens - 1 > self.table.size(1) * self.page_size:
             raise ValueError("the prompts leave no room for so many tokens")
+        # what a later call would refuse, while no pages are taken
+        if new_tokens > 1:
+            self._knows_pages("beam search")
+        if not -1 << 31 <= eos < 1 << 31:
+            raise ValueError("eos must be an int32")
+        if weights is not None:
+            L.check_values(weights, "weights", torch.float32)
+            if not weights.numel():
+                raise ValueError("weights must hold at least one value")
         if self.lens[:n].any():
             raise ValueError("a request that the beams need still holds tokens; release it first")
         i32 = dict(dtype=torch.int32, device=self.device)

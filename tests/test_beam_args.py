@@ -145,3 +145,19 @@ def test_release_refuses_other_flags(lib, forked):
                  torch.ones(4, dtype=torch.int32)):
         with pytest.raises(TypeError, match="done must be a CUDA tensor"):
             dec.release(done)
+
+
+def test_beam_search_refuses_before_it_takes_pages(lib):
+    import torch
+    dec = decoder()
+    dec.prefill = lambda *a: pytest.fail("pages were taken")
+    for error, kw in ((TypeError, dict(weights=torch.ones(4))), (TypeError, dict(weights=[1.0])),
+                      (ValueError, dict(eos=1 << 31)), (ValueError, dict(eos=(-1 << 31) - 1)),
+                      (TypeError, dict(eos="end"))):
+        with pytest.raises(error):
+            dec.beam_search([[1, 2]], 3, 2, **kw)
+    dec.pages = (1 << 23) + 1
+    for call in (lambda: dec.beam_search([[1, 2]], 2, 2), lambda: dec.fork(dec.lens), dec.compact):
+        with pytest.raises(ValueError, match="caches of up to 8388608 pages"):
+            call()
+    assert not dec.forked

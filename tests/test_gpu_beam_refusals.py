@@ -49,3 +49,29 @@ def test_release_takes_one_int32_flag_a_request(dev, model):
     dec.release(i32([0, 1, 0, 0]))
     assert sorted(host(dec.free).tolist()) == list(range(dec.pages)) and int(dec.count) == dec.pages
     dec.check()
+
+
+def test_beam_search_refuses_before_it_takes_pages(dev, model):
+    cd, toks = model
+    dec = Decoder(cd, 4, 32, torch.device("cuda"), page_size=4, top_k=4)
+    before = state(dec)
+    for kw in (dict(weights=torch.ones(6)), dict(weights=torch.ones(6, device="cuda").double()),
+               dict(weights=torch.ones((2, 3), device="cuda")),
+               dict(weights=torch.ones(6, device="cuda")[::2]),
+               dict(weights=torch.ones(0, device="cuda")), dict(weights=[1.0] * 6),
+               dict(eos=1 << 32), dict(eos=1.5j)):
+        with pytest.raises((TypeError, ValueError)):
+            dec.beam_search([toks[0, :9]], 5, 4, **kw)
+        assert state(dec) == before
+    # a cache that a fork does not know: one token needs none
+    dec.pages, pages = (1 << 23) + 1, dec.pages
+    for call in (lambda: dec.beam_search([toks[0, :9]], 5, 4), dec.compact,
+                 lambda: dec.fork(i32([0] * 4))):
+        with pytest.raises(ValueError):
+            call()
+        assert state(dec) == before
+    dec.beam_search([toks[0, :9]], 1, 4)
+    dec.pages = pages
+    dec.beam_search([toks[0, :9]], 5, 4, eos=np.int32(3))
+    assert host(dec.lens).tolist() == [0] * 4 and int(dec.count) == dec.pages
+    dec.check()
