@@ -1285,6 +1285,8 @@ def detbeam_select_f32(scores, top_ids, top_logp, beams, eos=-1, finished=None, 
         raise ValueError("weights, hist and lens_out need lens")
     if not 1 <= beams <= 32:
         raise ValueError("beams must be in 1..32")
+    if not -1 << 31 <= eos < 1 << 31:
+        raise ValueError("eos must be an int32")
     hp, ldh, hop, ldho, cols = None, 0, None, 0, 0
     if hist is not None:
         hp, ldh = _mat(hist, "hist", i32, dev, rows)

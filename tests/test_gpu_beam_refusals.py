@@ -3,7 +3,7 @@ released and no page taken by a call that raises."""
 import numpy as np
 import pytest
 
-from bitwise_reproducible_fp32_gb300 import inputs
+from bitwise_reproducible_fp32_gb300 import detlib, inputs
 from bitwise_reproducible_fp32_gb300.decode import Decoder
 from gpu_util import host, need_gpu, torch
 from test_gpu_beam_search import i32, upload
@@ -75,3 +75,10 @@ def test_beam_search_refuses_before_it_takes_pages(dev, model):
     dec.beam_search([toks[0, :9]], 5, 4, eos=np.int32(3))
     assert host(dec.lens).tolist() == [0] * 4 and int(dec.count) == dec.pages
     dec.check()
+
+
+def test_selection_refuses_an_ending_that_is_no_int32(dev):
+    x, ids = torch.zeros((1, 2), device="cuda"), torch.zeros((2, 3), dtype=torch.int32, device="cuda")
+    for eos in (1 << 31, (1 << 32) + 5, (-1 << 31) - 1):
+        with pytest.raises(ValueError):
+            detlib.detbeam_select_f32(x, ids, ids.float(), 2, eos=eos)
