@@ -35,12 +35,14 @@ def reading(how, giving_up=False):
     so (in groups: those of at most 8 query rows a key-value head, others together)."""
     lib = library(giving_up)
     shipped, sizes = detlib.load(), dict(detlib._decode_workspaces)
-    ctypes.c_int.in_dll(lib, "det_test_shared_how").value = how
+    word = ctypes.c_int.in_dll(lib, "det_test_shared_how")
+    before, word.value = word.value, how
     detlib._lib = lib
     detlib._decode_workspaces.clear()
     try:
         yield lib
     finally:
+        word.value = before
         detlib._lib = shipped
         detlib._decode_workspaces.clear()
         detlib._decode_workspaces.update(sizes)
