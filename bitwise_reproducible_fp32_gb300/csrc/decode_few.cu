@@ -22,7 +22,6 @@ __device__ unsigned int g_few_watchdog;
 namespace {
 
 constexpr int kFewCtas = 3;               // an SM's, where registers allow
-constexpr int kFewStages = 2;             // pieces of a warp's ring
 
 // NH: the rows the registers hold, of which the unit has at most NH.
 template <int NH, Loader LOAD>
@@ -31,7 +30,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr int CUT = kOwnTiles;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ Share share[kWarps];
-    __shared__ uint64_t full[kWarps][kMostStages];
+    __shared__ uint64_t full[kWarps][kRingPieces];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int d = A.d, nsl = (d + 31) / 32, live_rows = rows_of<CUT>(A), ldq = nsl * 32;
     init_bars<LOAD>(&full[0][0]);
@@ -39,9 +38,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     shares<CUT, kWarps>(A, A.kv_heads, blockIdx.x * kWarps, 1, gridDim.x * kWarps, share);
     const int64_t items = share[warp].items;
     if (items <= 0) return;
-    Ring<LOAD> ring(A, &kmap, A.k, smem_u32(smem_raw) + warp * kFewStages * kPieceBytes,
-                    smem_u32(&full[warp][0]), kFewStages);
-    float *qs = reinterpret_cast<float *>(smem_raw + kWarps * kFewStages * kPieceBytes) +
+    Ring<LOAD> ring(A, &kmap, A.k, smem_u32(smem_raw) + warp * kRingBytes, smem_u32(&full[warp][0]));
+    float *qs = reinterpret_cast<float *>(smem_raw + kWarps * kRingBytes) +
                 warp * NH * ldq;
 
     Item in = share[warp].at;
@@ -65,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (LOAD != kTma) cp_commit();
     };
-    for (int i = 0; i < kFewStages - 1; ++i) issue();
+    for (int i = 0; i < kRingPieces - 1; ++i) issue();
     uint32_t kat[8];              // 16-byte unit i of row `lane` of a piece
 #pragma unroll
     for (int i = 0; i < 8; ++i) kat[i] = lane * 128 + ((i ^ (lane & 7)) << 4);
@@ -182,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr int CUT = kOwn;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ Share share[kWarps];
-    __shared__ uint64_t full[kWarps][kMostStages];
+    __shared__ uint64_t full[kWarps][kRingPieces];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int d = A.d, nsl = (d + 31) / 32, live_rows = rows_of<CUT>(A), mul = A.kv_heads * nsl;
     init_bars<LOAD>(&full[0][0]);
@@ -190,10 +188,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     shares<CUT, kWarps>(A, mul, blockIdx.x * kWarps, 1, gridDim.x * kWarps, share);
     const int64_t items = share[warp].items;
     if (items <= 0) return;
-    Ring<LOAD> ring(A, &vmap, A.v, smem_u32(smem_raw) + warp * kFewStages * kPieceBytes,
-                    smem_u32(&full[warp][0]), kFewStages);
-    const uint32_t copies = smem_u32(smem_raw) + kWarps * kFewStages * kPieceBytes +
-                            warp * (NH * kTile * 4);
+    Ring<LOAD> ring(A, &vmap, A.v, smem_u32(smem_raw) + warp * kRingBytes, smem_u32(&full[warp][0]));
+    const uint32_t copies = smem_u32(smem_raw) + kWarps * kRingBytes + warp * (NH * kTile * 4);
 
     Item in = share[warp].at;
     int64_t in_items = items;
@@ -223,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (LOAD != kTma) cp_commit();
     };
-    for (int i = 0; i < kFewStages - 1; ++i) issue();
+    for (int i = 0; i < kRingPieces - 1; ++i) issue();
     uint32_t vat[8];              // column `lane` of rows i mod 8 of a piece
 #pragma unroll
     for (int i = 0; i < 8; ++i) vat[i] = i * 128 + (((lane >> 2) ^ i) << 4) + ((lane & 3) << 2);
@@ -339,7 +335,7 @@ cudaError_t run_few(K kern, int64_t items, size_t row_bytes, const SharedArgs &A
                                            int64_t(sm_count_current_device()) * kFewCtas);
     const CUtensorMap none = {};
     return launch_dependent(kern, dim3(unsigned(std::max<int64_t>(1, grid))), dim3(kThreads),
-                            kWarps * (kFewStages * kPieceBytes + row_bytes), s, A,
+                            kWarps * (kRingBytes + row_bytes), s, A,
                             map ? *map : none);
 }
 

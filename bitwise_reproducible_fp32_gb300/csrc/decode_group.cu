@@ -30,7 +30,6 @@ namespace {
 
 constexpr int kMaxCluster = 16;
 constexpr int kGroupCtas = 3;             // an SM's
-constexpr int kStages = 2;                // pieces of a warp's ring
 constexpr int kDeep = 8;                  // groups of a chain of S in flight
 
 // A chunk of the unit: `vc` of it, shared ones first, then request after request.
@@ -46,7 +45,7 @@ __global__ void __launch_bounds__(kThreads, kGroupCtas)
     group_kernel(const SharedArgs A, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, int64_t unit_x, int64_t unit_part) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ uint64_t full[kWarps][kMostStages];
+    __shared__ uint64_t full[kWarps][kRingPieces];
     __shared__ __align__(16) float rows[NH][256];     // q, the chains of S, then each warp's
                                                       // probabilities of a piece
     __shared__ float red[NH][8], top[kMaxCluster][NH], most_of[kWarps][NH], inv[NH];
@@ -149,9 +148,8 @@ __global__ void __launch_bounds__(kThreads, kGroupCtas)
     // ---- the warp's pieces: of each chunk of the CTA one tile of 64 tokens (a quarter,
     // another one from chunk to chunk), all slices of keys; then of every fourth
     // (chunk, slice) the values, 64 tokens at a time
-    const int stages = kStages, jobs = my * nsl;
-    Ring<LOAD> ring(A, &kmap, A.k, smem_u32(smem_raw) + warp * stages * kPieceBytes,
-                    smem_u32(&full[warp][0]), stages);
+    const int jobs = my * nsl;
+    Ring<LOAD> ring(A, &kmap, A.k, smem_u32(smem_raw) + warp * kRingBytes, smem_u32(&full[warp][0]));
     auto quarter = [&](int place) { return (warp + place) & 3; };
     int kp = -1, ksl = 0, vj = warp, vt = 0, in_t = 0, in_live = 0;
     Chunk in;
@@ -202,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, kGroupCtas)
         }
         if (LOAD != kTma) cp_commit();
     };
-    for (int i = 0; i < stages - 1; ++i) issue();
+    for (int i = 0; i < kRingPieces - 1; ++i) issue();
     uint32_t kat[8], vat[8];      // 16-byte unit i of row `lane` of a piece; column `lane` of row i
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -463,7 +461,7 @@ template <int NH, int PER, Loader LOAD>
 cudaError_t run_group(const SharedArgs &A, const GroupPlan &p, const CUtensorMap *maps,
                       cudaStream_t s) {
     auto kern = group_kernel<NH, PER, LOAD>;
-    const size_t smem = size_t(kWarps) * kStages * kPieceBytes;
+    const size_t smem = size_t(kWarps) * kRingBytes;
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e == cudaSuccess && p.cluster > 8)

@@ -49,8 +49,7 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanRows = 1024;                    // requests looked through at once
 constexpr int kPlanCtas = 8;                       // of a cluster
-constexpr int kScoreStages = 2;                    // of a warp's ring
-constexpr size_t kScoreRing = size_t(kWarps) * kScoreStages * kPieceBytes;
+constexpr size_t kScoreRing = size_t(kWarps) * kRingBytes;
 constexpr int kScoreRows = 4;                      // of a thread
 constexpr int kScoreCtas = 3;                      // an SM's
 constexpr int kPvTokens = 16;                      // of a step of P V
@@ -188,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, kScoreCtas)
     float *qs = reinterpret_cast<float *>(smem_raw + kScoreRing);
     __shared__ Share share;
     __shared__ int rows[R];           // (b, h) of the row at qs's place
-    __shared__ uint64_t full[kWarps][kMostStages];
+    __shared__ uint64_t full[kWarps][kRingPieces];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tl = lane & 7, rl = lane >> 3;
     const int d = A.d, nsl = (d + 31) / 32, mul = A.kv_heads * A.row_blocks;
     init_bars<LOAD>(&full[0][0]);
@@ -196,8 +195,7 @@ __global__ void __launch_bounds__(kThreads, kScoreCtas)
     shares<OWN, 1>(A, mul, blockIdx.x, 1, gridDim.x, &share);
     const int64_t items = share.items;
     if (items <= 0) return;
-    Ring<LOAD> ring(A, &kmap, A.k, smem_u32(smem_raw) + warp * kScoreStages * kPieceBytes,
-                    smem_u32(&full[warp][0]), kScoreStages);
+    Ring<LOAD> ring(A, &kmap, A.k, smem_u32(smem_raw) + warp * kRingBytes, smem_u32(&full[warp][0]));
 
     // ---- keys
     Item in = share.at;
@@ -230,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, kScoreCtas)
         }
         if (LOAD != kTma) cp_commit();
     };
-    for (int i = 0; i < kScoreStages - 1; ++i) issue();
+    for (int i = 0; i < kRingPieces - 1; ++i) issue();
     Item it = share.at;
     int held_u = -1, held_run = -1;
     for (int64_t i = 0; i < items; ++i) {

@@ -195,7 +195,8 @@ __device__ __forceinline__ int64_t offset_of(const SharedArgs &A, const int32_t 
 // kTile tokens x 32 dimensions in shared memory: rows of 128 bytes, their 16-byte units
 // swapped by row mod 8.
 constexpr int kPieceBytes = kTile * 128;
-constexpr int kMostStages = 3;
+constexpr int kRingPieces = 2;            // three leave room for two CTAs an SM, not three
+constexpr int kRingBytes = kRingPieces * kPieceBytes;
 
 // A warp's ring of pieces.
 template <Loader LOAD>
@@ -204,15 +205,15 @@ struct Ring {
     const CUtensorMap *map;              // of the keys or values that are fetched
     const float *cache;
     uint32_t slots, bars;
-    int stages, slot_in = 0, slot = 0;
+    int slot_in = 0, slot = 0;
     uint32_t phase = 0;
     bool stuck = false;
     int id = 0;                           // of the lane's box
     int64_t off[2];                       // of tokens lane, lane + 32
 
     __device__ __forceinline__ Ring(const SharedArgs &a, const CUtensorMap *m, const float *c,
-                                    uint32_t s, uint32_t b, int n)
-        : A(a), map(m), cache(c), slots(s), bars(b), stages(n) {}
+                                    uint32_t s, uint32_t b)
+        : A(a), map(m), cache(c), slots(s), bars(b) {}
     // where the piece of `live` tokens from t on is; ahead of fetch. CHECK: whether one
     // of the lane's pages is out of range (page 0 stands for it).
     template <bool CHECK = false>
@@ -272,19 +273,19 @@ struct Ring {
                                 src + at);
             }
         }
-        slot_in = slot_in + 1 == stages ? 0 : slot_in + 1;
+        slot_in = slot_in + 1 == kRingPieces ? 0 : slot_in + 1;
     }
     __device__ __forceinline__ void wait() {
         if constexpr (LOAD == kTma) {
             if (!stuck)
-                stuck = __any_sync(0xffffffffu, !wait_for_piece(bars, slot, phase, stages));
+                stuck = __any_sync(0xffffffffu, !wait_for_piece(bars, slot, phase, kRingPieces));
         } else {
-            if (stages == 3) cp_wait<1>(); else cp_wait<0>();
+            cp_wait<kRingPieces - 2>();
         }
         __syncwarp();
     }
     __device__ __forceinline__ void step() {
-        if (++slot == stages) {
+        if (++slot == kRingPieces) {
             slot = 0;
             phase ^= 1;
         }
@@ -310,7 +311,7 @@ struct Ring {
 template <Loader LOAD>
 __device__ __forceinline__ void init_bars(uint64_t *bars) {
     if (LOAD == kTma && threadIdx.x == 0) {
-        for (int i = 0; i < kWarps * kMostStages; ++i) mbar_init(smem_u32(bars + i), 1);
+        for (int i = 0; i < kWarps * kRingPieces; ++i) mbar_init(smem_u32(bars + i), 1);
         fence_mbar_init();
     }
 }
