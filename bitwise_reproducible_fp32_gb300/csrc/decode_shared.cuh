@@ -172,8 +172,8 @@ __device__ __forceinline__ void advance(const SharedArgs &A, int mul, Item &it) 
 // Scores (and partials) of the shared chunks and of the own ones do not depend on each
 // other. So the kernel of the own ones (OWN), launched behind the other one, starts as
 // soon as that one's CTAs have all begun (which they do once everything before them is
-// complete) and there is room, and waits for it at its end, so that its own end is
-// both's.
+// complete, so the plan's lists, the exps and 1 / S may be read before the wait) and
+// there is room, and waits for it at its end, so that its own end is both's.
 template <bool OWN>
 struct Beside {
     __device__ __forceinline__ Beside() {

@@ -267,9 +267,15 @@ void adamw_bias_correction(int64_t step, float beta1, float beta2, float *bc1, f
 
 int sm_count_current_device();
 
-// Launches kern as a programmatic dependent of the work before it on stream s:
-// its launch overlaps the tail of the previous kernel, and the kernel must
-// call grid_dependency_wait() before it touches global memory.
+// Launches kern as a programmatic dependent of the work before it on stream s: its
+// launch overlaps the tail of the previous kernel. The kernel must call
+// grid_dependency_wait() before it touches what that kernel writes, or writes what that
+// one touches. What older kernels wrote it may read before its wait where the previous
+// kernel lets its dependents start after a wait of its own (allow_dependents): those
+// kernels were complete then. The RMSNorm backward's dx kernel and the kernels of
+// requests' own tokens (decode_shared.cuh, Beside) do. Every kernel so launched waits, at
+// its end at the latest and on early returns too, so that the next one's wait covers all
+// before it.
 template <class... KParams, class... Args>
 cudaError_t launch_dependent(void (*kern)(KParams...), dim3 grid, dim3 block, size_t smem,
                              cudaStream_t s, Args... args) {
