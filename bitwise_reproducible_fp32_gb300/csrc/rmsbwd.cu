@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rmsbwd_rows_bulk_kernel(const 
             }
             const float q = __fdiv_rn(butterfly32(s), float(a.D));
             float4 *o = reinterpret_cast<float4 *>(a.dx + row * a.lddx);
+            if (a.dx == a.dy) grid_dependency_wait();   // the column kernel still reads dy
             for (int g = lane; g < ng; g += 32) {
                 const float4 xv = xr[g], dv = dr[g], gv = gs[g];
                 o[g] = make_float4(
