@@ -180,10 +180,11 @@ __device__ __forceinline__ float butterfly32(float s) {
 
 // dgain_j = P_0 + P_1 + ... left to right, for the columns of this CTA.
 __device__ __forceinline__ void fold_partials(const RowArgs &a) {
-    if (a.nchunks <= 1) return;
     if (int64_t(blockIdx.x) * (kRowWarps * 32) >= a.D) return;
-    // the partials are complete and visible once the column grid has finished
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the partials are complete and visible once the column grid has finished; without
+    // partials too, so that this grid's end is both's for the next dependent one
+    grid_dependency_wait();
+    if (a.nchunks <= 1) return;
     const int64_t j = int64_t(blockIdx.x) * (kRowWarps * 32) + threadIdx.x;
     if (j >= a.D) return;
     float t = a.partials[j];
@@ -228,6 +229,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rmsbwd_rows_bulk_kernel(const 
             if (threadIdx.x == 0) {
                 atomicOr(&g_rmsbwd_watchdog, kWatchdogRmsBwd);
                 (void)mbar_wait_bounded(smem_u32(bar), 0);
+                grid_dependency_wait();
             }
             return;
         }
