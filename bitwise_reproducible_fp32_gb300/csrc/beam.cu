@@ -12,8 +12,10 @@
 // by a bitonic network of shuffles, and the warps' lists are joined pairwise: the 32
 // largest of two sorted lists are max(a_i, b_31-i), five exchanges from sorted. The
 // histories of a request are copied by several CTAs, each of which makes the same
-// selection again, so nothing waits. Measured: 16 requests of 4 beams 8 us on the GPU; 512
-// of 16 beams of 32 alternatives with histories of 2048 tokens 31 us (4.2 TB/s).
+// selection again, so nothing waits. Measured on the GPU: 16 requests of 4 beams 8 us; 512
+// of 16 beams of 32 alternatives with histories of 2048 tokens 31 us, with one parent a
+// request and with four (67 MB are written, much of which stays in L2, and 4 to 16 MB
+// read: the selection, before the first of these bytes, is a good part of it).
 #include <algorithm>
 
 #include "det_internal.cuh"
@@ -212,7 +214,7 @@ cudaError_t launch_beam_select(int64_t requests, const det_beams &in, const det_
         A.vec = al16(A.hist) && al16(A.hist_out) && A.ldh % 4 == 0 && A.ldho % 4 == 0;
         warps = std::max(warps, A.wout);
         // 1024 columns and more a CTA, and no more CTAs than about one wave: each makes the
-        // selection again (512 requests of 16 beams and 2048 tokens: 30 us in two parts, 26
+        // selection again (512 requests of 16 beams and 2048 tokens: 33 us in two parts, 31
         // in one)
         const int64_t wave = int64_t(sm_count_current_device()) * 4;
         parts = std::max<int64_t>(1, std::min((cols + 1023) / 1024, wave / requests));

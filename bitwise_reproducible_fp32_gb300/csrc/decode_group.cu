@@ -9,8 +9,9 @@
 // reads its prompts' keys and values once, in one launch: HBM bounds it, and the latency
 // of its phases (the shared pages, K, the maxima, S, V, the chunks left to right).
 // Measured, 12 heads of 64: 16 groups of 4 requests of 700..1900 tokens and up to 148 of
-// their own 59 us (157 MB; K and V go by at 4.9 TB/s, the other phases take about 16 us;
-// each request for itself 73 us), of 4500..6000 tokens 129 us (4.3 TB/s; 228). Three CTAs
+// their own 60..63 us (157 MB; K and V go by at 4.9 TB/s, 32 us, the phases between take
+// about 16, and the units, all on the GPU at once, end with the longest: 1.2 to 1.45 times
+// the mean; each request for itself 73 us), of 4500..6000 tokens 129 us (4.3 TB/s; 228). Three CTAs
 // an SM with rings of two pieces: two CTAs with three took 72 us and 162; clusters of
 // twice the CTAs 77 and 149.
 #include <cooperative_groups.h>

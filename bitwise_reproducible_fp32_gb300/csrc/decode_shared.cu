@@ -19,7 +19,7 @@
 // Own tokens with few rows (decode_few.cu) are bound by HBM; their kernels run behind
 // those of the shared ones and beside their last waves. Every launch overlaps the end
 // of the one before (programmatic dependent launches).
-// Measured: 48 requests on a document of 20001..24000 tokens, 32 heads of 128 over 8, 543
+// Measured: 48 requests on a document of 20001..24000 tokens, 32 heads of 128 over 8, 541
 // us (32 TFLOP/s; scores 180 us and P V 168, the FMA pipe about 65% busy, sums 48, own
 // tokens 45 of which some is hidden, the join 15); 64 requests on 8100..8192 tokens and up
 // to 1000 of their own, 12 heads of 64, 140 us (1.8 TB/s, 12 TFLOP/s: seven dependent
@@ -659,6 +659,13 @@ constexpr size_t kSliceBytes = size_t(1) << 30;     // scores and partials of a 
 // 1500 29 / 36; 16 groups of 2 with 4 query heads a key-value head of 6000 240 / 168. Each
 // for itself / together: one group of 32 of 1500 50 / 65, of 6000 150 / 75; 4 groups of 4
 // with 4 query heads a key-value head of 1500 46 / 68, of 6000 128 / 90.
+// Where it is wrong: reading each for itself has at most 16 CTAs a unit too, which the first
+// line leaves out (two requests of 32768 tokens with 8 query heads over one head of 128
+// take 115 us so, 69 together); together is not weighed for 8 rows and fewer (one group of
+// 8, a head of 128, 24000 tokens: 53 / 106 in groups / 58 together); and rows may be much
+// shorter than the table is wide (two groups of 8 of 400 tokens, 12 heads of 64, in a table
+// of 2^17: 12.5 us each for itself, 51 in groups; 48 of 1200, 32 heads of 128 over 8: 114
+// and 170 together).
 enum How { kAlone, kInGroups, kTogether };
 How how_to_read(int64_t batch, int64_t group, int64_t heads, int64_t kv_heads, int64_t d,
                 int64_t max_len) {

@@ -27,8 +27,8 @@ constexpr unsigned int kWatchdogGemm = 1u;   // GEMM operand staging
 // bit 1 (2u): cross-entropy row staging, defined in rowops.cu; bit 2 (4u):
 // RMSNorm-backward staging (rmsbwd.cu); bit 3 (8u): RMSNorm row staging
 // (rowops.cu); bit 4 (16u): causal-softmax row staging (block.cu); bit 5 (32u):
-// decode attention's pieces (decode.cu, decode_shared.cu); bit 6 (64u): log-probability row
-// staging (logprob.cu)
+// decode attention's pieces (decode.cu, decode_shared.cu, decode_few.cu, decode_group.cu);
+// bit 6 (64u): log-probability row staging (logprob.cu)
 
 // ---------------------------------------------------------------- launchers
 // Each returns cudaSuccess or the launch error; arguments are validated by

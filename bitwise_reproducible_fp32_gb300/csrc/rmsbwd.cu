@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(kCols)
     uint64_t *bar = reinterpret_cast<uint64_t *>(rs + kKChunk);
     // this grid is itself a programmatic dependent: once the previous grid
     // (the producer of x, dy or inv_rms) is complete, the dx kernel may start
-    // (it reads x and dy at once, and waits for this grid only where it folds
-    // the partials)
+    // (it reads x and dy at once, and waits for this grid before it writes dx
+    // over dy, where it folds the partials, and before it ends)
     grid_dependency_wait();
     allow_dependents();
     const int t = threadIdx.x;

@@ -940,6 +940,8 @@ det_status detpages_compact(const det_profile_v1 *prof, int64_t batch, int64_t p
  * call. A page past num_pages or a number of tokens outside 0..page_size ORs 1,
  * and the pair copies nothing; a *count outside 0..pairs ORs 1 and counts as the
  * nearest of them.
+ * Past some ten thousand pairs in a cache of more than 2^18 pages the search for such
+ * destinations grows with the square of the pairs (262,000 of a million pages: 0.1 s).
  * pairs 0..2^23. Errors: DET_ERR_INVALID_ARG for that, the cache's rules
  * (detkv_append_f32) or null pointers. */
 det_status detkv_copy_f32(const det_profile_v1 *prof, int64_t pairs, const int32_t *src,
@@ -953,8 +955,10 @@ det_status detkv_copy_f32(const det_profile_v1 *prof, int64_t pairs, const int32
  * (those of length 0 or out of range left out; every request keeps one token of its
  * own at least) are found from the table; their keys and values are read once for
  * the group instead of once a request. Pages need not be shared: group only says
- * where to look. For few requests or a narrow table, where reading each for itself is
- * faster, that is done (the choice goes by the arguments' sizes, not by lengths).
+ * where to look. For few requests or a narrow table each is read for itself, where an
+ * estimate has that faster (the choice goes by the arguments' sizes, the table's width
+ * among them, not by lengths: requests much shorter than their table is wide may take
+ * longer than by detdecode_attention_f32).
  * Arguments, status bits and errors as detdecode_attention_f32, and
  * DET_ERR_INVALID_ARG for group < 1. workspace: at least
  * detdecode_attention_shared_workspace_bytes (16-byte aligned, no contents
